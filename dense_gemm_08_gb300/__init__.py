@@ -10,13 +10,19 @@ Same names as the C ABI:
     gemm_f32, gemm_bf16_f32acc, gemm_f16_f32acc, gemm_bf16_f32acc_ex,
     gemm_f32_noalloc, gemm_status_string, gemm_last_device_status, gemm_last_kernel,
     gemm_memory_info, gemm_release_memory,
+    gemm_group_rows,
+    gemm_grouped_f32, gemm_grouped_bf16_f32acc, gemm_grouped_f16_f32acc,
+    gemm_grouped_wgrad_f32, gemm_grouped_wgrad_bf16_f32acc, gemm_grouped_wgrad_f16_f32acc,
+    gemm_lora_bf16_f32acc, gemm_lora_f16_f32acc,
     gemm_probe_tc_bf16, gemm_probe_fma_f32, gemm_probe_wait_timeout
 Pointer arguments take an integer device address or a torch CUDA tensor;
 ``stream`` takes an integer ``cudaStream_t``, a ``torch.cuda.Stream`` or None
 (torch's current stream).  A non-zero status raises ``GemmError``.
 
 ``gemm(...)`` is a convenience wrapper for torch tensors that reads each
-operand's storage order and leading dimension from its strides.
+operand's storage order and leading dimension from its strides; so are
+``group_rows(...)``, ``gemm_grouped(...)``, ``gemm_grouped_wgrad(...)`` and
+``gemm_lora(...)`` for the grouped operators.
 """
 from __future__ import annotations
 
@@ -41,6 +47,10 @@ LIB_PATH = os.environ.get("DENSE_GEMM_08_GB300_LIB") or os.path.join(
 EXPORTED = ("gemm_f32", "gemm_bf16_f32acc", "gemm_f16_f32acc", "gemm_bf16_f32acc_ex",
             "gemm_f32_noalloc", "gemm_status_string", "gemm_last_device_status",
             "gemm_last_kernel", "gemm_memory_info", "gemm_release_memory",
+            "gemm_group_rows", "gemm_grouped_f32", "gemm_grouped_bf16_f32acc",
+            "gemm_grouped_f16_f32acc", "gemm_grouped_wgrad_f32",
+            "gemm_grouped_wgrad_bf16_f32acc", "gemm_grouped_wgrad_f16_f32acc",
+            "gemm_lora_bf16_f32acc", "gemm_lora_f16_f32acc",
             "gemm_probe_tc_bf16", "gemm_probe_fma_f32", "gemm_probe_wait_timeout")
 
 GEMM_ACT_NONE = 0
@@ -48,6 +58,7 @@ GEMM_ACT_RELU = 1
 GEMM_ACT_GELU = 2
 GEMM_D_F32 = 0
 GEMM_D_BF16 = 1
+GEMM_D_F16 = 2  # the grouped operators with FP16 inputs only
 
 
 class MemoryInfo(ctypes.Structure):
@@ -102,6 +113,23 @@ def library() -> ctypes.CDLL:
             lib.gemm_memory_info.restype = ip
             lib.gemm_release_memory.argtypes = []
             lib.gemm_release_memory.restype = ip
+            ep = ctypes.POINTER(Epilogue)
+            lib.gemm_group_rows.argtypes = [i64, i64, vp, vp, vp, vp, vp]
+            lib.gemm_group_rows.restype = ip
+            for t in ("f32", "bf16_f32acc", "f16_f32acc"):
+                fn = getattr(lib, "gemm_grouped_" + t)
+                fn.argtypes = [i64, i64, i64, i64, f32, vp, i64, i64, vp, vp, vp, i64, i64, ip,
+                               vp, i64, ep, vp]
+                fn.restype = ip
+                fn = getattr(lib, "gemm_grouped_wgrad_" + t)
+                fn.argtypes = [i64, i64, i64, i64, f32, vp, i64, i64, vp, vp, vp, i64, f32, vp,
+                               i64, i64, vp, i64, i64, ip, vp]
+                fn.restype = ip
+            for t in ("bf16_f32acc", "f16_f32acc"):
+                fn = getattr(lib, "gemm_lora_" + t)
+                fn.argtypes = [i64, i64, i64, vp, i64, vp, i64, ip, i64, i64, vp, vp, vp, i64,
+                               i64, ip, vp, i64, i64, ip, vp, i64, ep, vp]
+                fn.restype = ip
             dp = ctypes.POINTER(ctypes.c_double)
             lib.gemm_probe_tc_bf16.argtypes = [ip, i64, dp, vp]
             lib.gemm_probe_tc_bf16.restype = ip
@@ -214,6 +242,128 @@ def gemm_release_memory(check=True) -> int:
     return st
 
 
+def gemm_group_rows(rows, groups, group_of_row, offsets, order, position=None, stream=None,
+                    check=True) -> int:
+    """Rows grouped by a number: offsets, order and (optional) positions (see include/gemm.h)."""
+    st = library().gemm_group_rows(int(rows), int(groups), _addr(group_of_row), _addr(offsets),
+                                   _addr(order), _addr(position), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_group_rows")
+    return st
+
+
+def _call_grouped(fn_name, groups, rows, N, K, alpha, A, lda, rows_a, row_index, offsets, B, ldb,
+                  stride_b, order_b, D, ldd, bias, activation, d_type, stream, check):
+    ep = Epilogue(_addr(bias), int(activation), int(d_type))
+    st = getattr(library(), fn_name)(
+        int(groups), int(rows), int(N), int(K), float(alpha), _addr(A), int(lda), int(rows_a),
+        _addr(row_index), _addr(offsets), _addr(B), int(ldb), int(stride_b), int(order_b),
+        _addr(D), int(ldd), ctypes.byref(ep), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, fn_name)
+    return st
+
+
+def gemm_grouped_f32(groups, rows, N, K, alpha, A, lda, rows_a, row_index, offsets, B, ldb,
+                     stride_b, order_b, D, ldd, bias=None, activation=GEMM_ACT_NONE,
+                     d_type=GEMM_D_F32, stream=None, check=True) -> int:
+    """D(r, :) = act(alpha * A(idx(r), :) B_g + bias_g), FP32 on the CUDA cores."""
+    return _call_grouped("gemm_grouped_f32", groups, rows, N, K, alpha, A, lda, rows_a, row_index,
+                         offsets, B, ldb, stride_b, order_b, D, ldd, bias, activation, d_type,
+                         stream, check)
+
+
+def gemm_grouped_bf16_f32acc(groups, rows, N, K, alpha, A, lda, rows_a, row_index, offsets, B,
+                             ldb, stride_b, order_b, D, ldd, bias=None,
+                             activation=GEMM_ACT_NONE, d_type=GEMM_D_F32, stream=None,
+                             check=True) -> int:
+    """D(r, :) = act(alpha * A(idx(r), :) B_g + bias_g), BF16 inputs, FP32 or BF16 D."""
+    return _call_grouped("gemm_grouped_bf16_f32acc", groups, rows, N, K, alpha, A, lda, rows_a,
+                         row_index, offsets, B, ldb, stride_b, order_b, D, ldd, bias, activation,
+                         d_type, stream, check)
+
+
+def gemm_grouped_f16_f32acc(groups, rows, N, K, alpha, A, lda, rows_a, row_index, offsets, B, ldb,
+                            stride_b, order_b, D, ldd, bias=None, activation=GEMM_ACT_NONE,
+                            d_type=GEMM_D_F32, stream=None, check=True) -> int:
+    """D(r, :) = act(alpha * A(idx(r), :) B_g + bias_g), FP16 inputs, FP32 or FP16 D."""
+    return _call_grouped("gemm_grouped_f16_f32acc", groups, rows, N, K, alpha, A, lda, rows_a,
+                         row_index, offsets, B, ldb, stride_b, order_b, D, ldd, bias, activation,
+                         d_type, stream, check)
+
+
+def _call_wgrad(fn_name, groups, rows, M, N, alpha, A, lda, rows_a, row_index, offsets, B, ldb,
+                beta, C, ldc, stride_c, D, ldd, stride_d, d_type, stream, check):
+    st = getattr(library(), fn_name)(
+        int(groups), int(rows), int(M), int(N), float(alpha), _addr(A), int(lda), int(rows_a),
+        _addr(row_index), _addr(offsets), _addr(B), int(ldb), float(beta), _addr(C), int(ldc),
+        int(stride_c), _addr(D), int(ldd), int(stride_d), int(d_type), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, fn_name)
+    return st
+
+
+def gemm_grouped_wgrad_f32(groups, rows, M, N, alpha, A, lda, rows_a, row_index, offsets, B, ldb,
+                           beta, C, ldc, stride_c, D, ldd, stride_d, d_type=GEMM_D_F32,
+                           stream=None, check=True) -> int:
+    """D_g = alpha * A_g^T B_g + beta * C_g over each group's rows, FP32 on the CUDA cores."""
+    return _call_wgrad("gemm_grouped_wgrad_f32", groups, rows, M, N, alpha, A, lda, rows_a,
+                       row_index, offsets, B, ldb, beta, C, ldc, stride_c, D, ldd, stride_d,
+                       d_type, stream, check)
+
+
+def gemm_grouped_wgrad_bf16_f32acc(groups, rows, M, N, alpha, A, lda, rows_a, row_index, offsets,
+                                   B, ldb, beta, C, ldc, stride_c, D, ldd, stride_d,
+                                   d_type=GEMM_D_F32, stream=None, check=True) -> int:
+    """D_g = alpha * A_g^T B_g + beta * C_g over each group's rows, BF16 inputs."""
+    return _call_wgrad("gemm_grouped_wgrad_bf16_f32acc", groups, rows, M, N, alpha, A, lda, rows_a,
+                       row_index, offsets, B, ldb, beta, C, ldc, stride_c, D, ldd, stride_d,
+                       d_type, stream, check)
+
+
+def gemm_grouped_wgrad_f16_f32acc(groups, rows, M, N, alpha, A, lda, rows_a, row_index, offsets, B,
+                                  ldb, beta, C, ldc, stride_c, D, ldd, stride_d,
+                                  d_type=GEMM_D_F32, stream=None, check=True) -> int:
+    """D_g = alpha * A_g^T B_g + beta * C_g over each group's rows, FP16 inputs."""
+    return _call_wgrad("gemm_grouped_wgrad_f16_f32acc", groups, rows, M, N, alpha, A, lda, rows_a,
+                       row_index, offsets, B, ldb, beta, C, ldc, stride_c, D, ldd, stride_d,
+                       d_type, stream, check)
+
+
+def _call_lora(fn_name, M, N, K, X, ldx, W, ldw, order_w, adapters, rank, adapter_of_row, scale,
+               LA, ld_a, stride_a, order_a, LB, ld_b, stride_b, order_b, D, ldd, bias, activation,
+               d_type, stream, check):
+    ep = Epilogue(_addr(bias), int(activation), int(d_type))
+    st = getattr(library(), fn_name)(
+        int(M), int(N), int(K), _addr(X), int(ldx), _addr(W), int(ldw), int(order_w),
+        int(adapters), int(rank), _addr(adapter_of_row), _addr(scale), _addr(LA), int(ld_a),
+        int(stride_a), int(order_a), _addr(LB), int(ld_b), int(stride_b), int(order_b), _addr(D),
+        int(ldd), ctypes.byref(ep), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, fn_name)
+    return st
+
+
+def gemm_lora_bf16_f32acc(M, N, K, X, ldx, W, ldw, order_w, adapters, rank, adapter_of_row, scale,
+                          LA, ld_a, stride_a, order_a, LB, ld_b, stride_b, order_b, D, ldd,
+                          bias=None, activation=GEMM_ACT_NONE, d_type=GEMM_D_F32, stream=None,
+                          check=True) -> int:
+    """A shared projection with each row's own low-rank adapter, BF16 (see include/gemm.h)."""
+    return _call_lora("gemm_lora_bf16_f32acc", M, N, K, X, ldx, W, ldw, order_w, adapters, rank,
+                      adapter_of_row, scale, LA, ld_a, stride_a, order_a, LB, ld_b, stride_b,
+                      order_b, D, ldd, bias, activation, d_type, stream, check)
+
+
+def gemm_lora_f16_f32acc(M, N, K, X, ldx, W, ldw, order_w, adapters, rank, adapter_of_row, scale,
+                         LA, ld_a, stride_a, order_a, LB, ld_b, stride_b, order_b, D, ldd,
+                         bias=None, activation=GEMM_ACT_NONE, d_type=GEMM_D_F32, stream=None,
+                         check=True) -> int:
+    """A shared projection with each row's own low-rank adapter, FP16 (see include/gemm.h)."""
+    return _call_lora("gemm_lora_f16_f32acc", M, N, K, X, ldx, W, ldw, order_w, adapters, rank,
+                      adapter_of_row, scale, LA, ld_a, stride_a, order_a, LB, ld_b, stride_b,
+                      order_b, D, ldd, bias, activation, d_type, stream, check)
+
+
 def gemm_probe_tc_bf16(cta_group, n_mma, stream=None, check=True):
     """Enqueue the tensor-pipe probe; returns (status, FLOPs of the launch)."""
     flops = ctypes.c_double(0.0)
@@ -296,4 +446,206 @@ def gemm(A, B, C=None, alpha=1.0, beta=0.0, out=None, stream=None):
     fn = fns[A.dtype]
     fn(M, N, K, alpha, A, lda, oa, B, ldb, ob, beta, C if beta != 0.0 else None, ldc, out, ldd,
        ocd, stream)
+    return out
+
+
+# ------------------------------------------------- torch helpers, grouped
+def stack_order(t):
+    """(order, ld, stride) of a stack of matrices (3-D tensor), from its strides."""
+    if t.dim() != 3:
+        raise ValueError("expected a 3-D tensor (a stack of matrices)")
+    if t.shape[0] > 1 and t.stride(0) < 0:
+        raise ValueError("negative strides are not supported")
+    if t.shape[0] == 0:
+        return ROW_MAJOR, max(t.shape[2], 1), 0
+    order, ld = storage_order(t[0])
+    return order, ld, t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _row_major(t, what):
+    order, ld = storage_order(t)
+    if order != ROW_MAJOR and t.shape[0] > 1:
+        raise ValueError(f"{what} must be row-major")
+    return max(ld, t.shape[1], 1)
+
+
+def _int_vector(t, n, what, device):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous vector of {n}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+
+
+def _f32_dense(t, shape, what, device):
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with shape {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+
+
+_SUFFIX = {"torch.float32": "f32", "torch.bfloat16": "bf16_f32acc", "torch.float16": "f16_f32acc"}
+_D_TYPE = {"torch.float32": GEMM_D_F32, "torch.bfloat16": GEMM_D_BF16, "torch.float16": GEMM_D_F16}
+
+
+def _types(A, B, out, out_dtype, default):
+    """(entry point suffix, output dtype, d_type); A and B share a dtype, D is FP32 or that dtype."""
+    if A.dtype != B.dtype:
+        raise TypeError("the operands must share a dtype")
+    if A.device != B.device:
+        raise ValueError("the operands must share a device")
+    suffix = _SUFFIX.get(str(A.dtype))
+    if suffix is None:
+        raise TypeError("the operands must be float32, bfloat16 or float16")
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out must have out_dtype")
+        if out.device != A.device:
+            raise ValueError("out must be on the operands' device")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = default
+    d_type = _D_TYPE.get(str(out_dtype))
+    if d_type is None or (d_type != GEMM_D_F32 and out_dtype != A.dtype):
+        raise TypeError("the output must be float32 or the operands' dtype")
+    return suffix, out_dtype, d_type
+
+
+def group_rows(ids, groups, stream=None):
+    """(offsets, order, position) of rows grouped by the int32 numbers `ids` (gemm_group_rows)."""
+    import torch
+    _int_vector(ids, ids.numel(), "ids", ids.device)
+    n = ids.numel()
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
+    order = torch.empty(n, dtype=torch.int32, device=ids.device)
+    position = torch.empty(n, dtype=torch.int32, device=ids.device)
+    gemm_group_rows(n, groups, ids, offsets, order, position, stream)
+    return offsets, order, position
+
+
+def gemm_grouped(A, B, offsets, row_index=None, bias=None, activation=GEMM_ACT_NONE,
+                 out_dtype=None, out=None, alpha=1.0, stream=None):
+    """D[r] = act(alpha * A[idx(r)] @ B[g] + bias[g]) for the rows r of each group g.
+
+    A is (rows_a x K) row-major, B a stack (groups x K x N) of row- or
+    column-major matrices (e.g. ``W.transpose(1, 2)`` of groups x N x K
+    weights), offsets int32 (groups + 1) on the device; row_index int32 gathers
+    the rows of A (one per row of D).  D is float32 or the operands' dtype
+    (the default).  Rows of D outside every group are left as they are.
+    """
+    import torch
+    suffix, out_dtype, d_type = _types(A, B, out, out_dtype, A.dtype)
+    groups, K, N = B.shape
+    if A.dim() != 2 or A.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    rows = A.shape[0] if row_index is None else row_index.shape[0]
+    lda = _row_major(A, "A")
+    order_b, ldb, stride_b = stack_order(B)
+    _int_vector(offsets, groups + 1, "offsets", A.device)
+    if row_index is not None:
+        _int_vector(row_index, rows, "row_index", A.device)
+    if bias is not None:
+        _f32_dense(bias, (groups, N), "bias", A.device)
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=A.device)
+    elif tuple(out.shape) != (rows, N):
+        raise ValueError(f"out must be {rows} x {N}")
+    _call_grouped("gemm_grouped_" + suffix, groups, rows, N, K, alpha, A, lda, A.shape[0],
+                  row_index, offsets, B, ldb, stride_b, order_b, out, _row_major(out, "out"), bias,
+                  activation, d_type, stream, True)
+    return out
+
+
+def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.0, out_dtype=None,
+                       out=None, stream=None):
+    """D[g] = alpha * A[idx(rows of g)].T @ B[rows of g] + beta * C[g], a stack (groups x M x N).
+
+    A is (rows_a x M), B (rows x N), both row-major; offsets and row_index as
+    for ``gemm_grouped``.  D is float32 (the default) or the operands' dtype, C
+    float32.  Groups without rows give beta * C[g].
+    """
+    import torch
+    suffix, out_dtype, d_type = _types(A, B, out, out_dtype, torch.float32)
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be matrices")
+    M, (rows, N), groups = A.shape[1], B.shape, offsets.shape[0] - 1
+    lda, ldb = _row_major(A, "A"), _row_major(B, "B")
+    _int_vector(offsets, groups + 1, "offsets", A.device)
+    if row_index is not None:
+        _int_vector(row_index, rows, "row_index", A.device)
+    elif A.shape[0] != rows:
+        raise ValueError("A and B must have as many rows")
+
+    def stack(t, what):
+        if tuple(t.shape) != (groups, M, N):
+            raise ValueError(f"{what} must be {groups} x {M} x {N}")
+        order, ld, stride = stack_order(t)
+        if order != ROW_MAJOR and M > 1:
+            raise ValueError(f"{what} must be a stack of row-major matrices")
+        return max(ld, N, 1), stride
+
+    if out is None:
+        out = torch.empty((groups, M, N), dtype=out_dtype, device=A.device)
+    ldd, stride_d = stack(out, "out")
+    ldc = stride_c = 0
+    if beta != 0.0:
+        if C is None:
+            raise ValueError("beta != 0 needs C")
+        if C.dtype != torch.float32:
+            raise TypeError("C must be float32")
+        if C.device != A.device:
+            raise ValueError("C must be on the operands' device")
+        ldc, stride_c = stack(C, "C")
+    _call_wgrad("gemm_grouped_wgrad_" + suffix, groups, rows, M, N, alpha, A, lda, A.shape[0],
+                row_index, offsets, B, ldb, beta, C if beta != 0.0 else None, ldc, stride_c, out,
+                ldd, stride_d, d_type, stream, True)
+    return out
+
+
+def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GEMM_ACT_NONE,
+              out_dtype=None, out=None, stream=None):
+    """D[i] = act(X[i] @ W + scale[a] * (X[i] @ LA[a]) @ LB[a] + bias), a = adapter_of_row[i].
+
+    X is (M x K) row-major, W (K x N), LA a stack (adapters x K x rank), LB a
+    stack (adapters x rank x N), each row- or column-major, all bfloat16 or
+    all float16; adapter_of_row int32 (a number outside [0, adapters): no
+    adapter), scale float32 per adapter.  D is float32 or the operands' dtype
+    (the default).
+    """
+    import torch
+    suffix, out_dtype, d_type = _types(X, W, out, out_dtype, X.dtype)
+    if suffix == "f32":
+        raise TypeError("gemm_lora takes bfloat16 or float16")
+    for t in (LA, LB):
+        if t.dtype != X.dtype:
+            raise TypeError("the operands must share a dtype")
+        if t.device != X.device:
+            raise ValueError("the operands must share a device")
+    (M, K), N = X.shape, W.shape[1]
+    adapters, rank = LA.shape[0], LA.shape[2]
+    if W.shape[0] != K or LA.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    if tuple(LB.shape) != (adapters, rank, N):
+        raise ValueError(f"LB must be {adapters} x {rank} x {N}")
+    ldx = _row_major(X, "X")
+    order_w, ldw = storage_order(W)
+    order_a, ld_a, stride_a = stack_order(LA)
+    order_b, ld_b, stride_b = stack_order(LB)
+    _int_vector(adapter_of_row, M, "adapter_of_row", X.device)
+    if scale is not None:
+        _f32_dense(scale, (adapters,), "scale", X.device)
+    if bias is not None:
+        _f32_dense(bias, (N,), "bias", X.device)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=X.device)
+    elif tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be {M} x {N}")
+    _call_lora("gemm_lora_" + suffix, M, N, K, X, ldx, W, ldw, order_w, adapters, rank,
+               adapter_of_row, scale, LA, ld_a, stride_a, order_a, LB, ld_b, stride_b, order_b,
+               out, _row_major(out, "out"), bias, activation, d_type, stream, True)
     return out

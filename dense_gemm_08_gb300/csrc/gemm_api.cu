@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "call.h"
 #include "gemm.h"
 #include "gemm_probe.h"
 #include "internal.h"
@@ -114,6 +115,13 @@ gemm_status_t finish(cudaError_t e, const char *name) {
 }
 
 }  // namespace
+
+// for the entry points in other files (call.h)
+namespace gemm {
+void set_last_kernel(const char *name) { t_last_kernel = name; }
+gemm_status_t check_device_status() { return check_device(); }
+gemm_status_t finish_call(cudaError_t e, const char *name) { return finish(e, name); }
+}  // namespace gemm
 
 GEMM_API gemm_status_t gemm_f32(int64_t M, int64_t N, int64_t K, float alpha, const float *A,
                                 int64_t lda, gemm_order_t order_a, const float *B, int64_t ldb,

@@ -235,7 +235,11 @@ gemm_status_t gemm_f32_noalloc(int64_t M, int64_t N, int64_t K, float alpha,
  * bits).
  */
 typedef enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2 } gemm_activation_t;
-typedef enum { GEMM_D_F32 = 0, GEMM_D_BF16 = 1 } gemm_d_type_t;
+typedef enum {
+    GEMM_D_F32 = 0,
+    GEMM_D_BF16 = 1,
+    GEMM_D_F16 = 2 /* the grouped operators with FP16 inputs only */
+} gemm_d_type_t;
 typedef struct {
     const float *bias;
     gemm_activation_t activation;
@@ -248,6 +252,165 @@ gemm_status_t gemm_bf16_f32acc_ex(int64_t M, int64_t N, int64_t K, float alpha,
                                   float beta, const float *C, int64_t ldc,
                                   void *D, int64_t ldd, gemm_order_t order_cd,
                                   const gemm_epilogue_t *epilogue, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Grouped operators: products whose weight matrix depends on the row (the
+ * experts of a mixture, the low-rank adapters of many requests).  The GEMM
+ * pages have no counterpart to them.
+ *
+ * Common contract.  Ownership, workspace, graph capture, threads,
+ * asynchrony and errors are those of gemm_f32 above; in addition:
+ * Rows of a group: product row r belongs to the group g with
+ *   offsets[g] <= r < offsets[g + 1].  `offsets` holds groups + 1
+ *   non-decreasing int32 values on the device (what gemm_group_rows writes);
+ *   the host does not read it, so a call never waits for the sizes and can be
+ *   captured in a graph.  The kernels clamp each value to [0, rows] and take
+ *   a falling pair as an empty group.  Rows past offsets[groups] (and before
+ *   offsets[0]) belong to no group: no value computed from them is stored.
+ * row_index (or NULL): product row r reads row row_index[r] of A, so rows
+ *   need not be copied into group order first; an index outside [0, rows_a)
+ *   reads a row of zeros.  Without it row r of A is read and rows_a >= rows.
+ * Matrices: A and D are row-major (a group is a run of rows).  Matrix g of a
+ *   stack starts stride elements after matrix g - 1 (stride_b = 0: one B for
+ *   all groups).  Every matrix and group stride is in elements.
+ * Types: FP32 accumulation.  d_type is GEMM_D_F32, or the inputs' 16-bit
+ *   type (GEMM_D_BF16, GEMM_D_F16): rounded once, to nearest even, after the
+ *   whole epilogue.
+ * Kernels: tensor cores (tcgen05) for 16-bit inputs that TMA can describe
+ *   (16-byte aligned pointers, leading dimensions and strides multiples of 8
+ *   elements), CUDA cores otherwise and for FP32 (no TF32).  D may have any
+ *   alignment.
+ * Special values: a row's infinities and NaNs reach that row's results only
+ *   (for the weight gradient: that group's).
+ * Sizes: each of rows, M, N, K, groups is at most 2^31 - 1; no rows or no
+ *   columns is a no-op (the weight gradient's groups without rows still give
+ *   beta * C).  K == 0 or alpha == 0: A and B are not read.
+ */
+
+/*
+ * gemm_group_rows -- rows grouped by a number, in one kernel.
+ *
+ *   group_of_row  rows int32 numbers (device); numbers outside [0, groups)
+ *                 drop their row
+ *   offsets       groups + 1 int32: rows whose number is below g (dropped
+ *                 rows do not count); offsets[groups] = rows kept
+ *   order         rows int32: the row at each place, by number and then by
+ *                 row (stable); -1 past offsets[groups].  As row_index (or
+ *                 divided by the number of experts per token) it gathers the
+ *                 rows of A for the grouped products.
+ *   position      rows int32 or NULL: the place of each row, -1 if dropped
+ * groups >= 1; rows == 0 writes zeros to offsets.
+ */
+gemm_status_t gemm_group_rows(int64_t rows, int64_t groups, const int32_t *group_of_row,
+                              int32_t *offsets, int32_t *order, int32_t *position,
+                              cudaStream_t stream);
+
+/*
+ * gemm_grouped_* -- one product per group of rows:
+ *
+ *     D(r, :) = act(alpha * A(idx(r), :) * op(B_g) + bias_g),  r in group g
+ *
+ * op(B_g) is K x N, stored in order_b.  epilogue->bias points to groups x N
+ * FP32 values (row g for group g) or is NULL; epilogue may be NULL (no bias,
+ * no activation, FP32 D).  The input gradient of a grouped product is the
+ * same call with the other order_b (K and N exchanged).
+ * Accuracy: |D - D_ref| <= rel * sum_k |alpha A B| + 1e-6 before the
+ * activation, rel = 1e-5 (FP32) or 4e-3 (16-bit inputs), plus D's rounding.
+ */
+gemm_status_t gemm_grouped_f32(int64_t groups, int64_t rows, int64_t N, int64_t K, float alpha,
+                               const float *A, int64_t lda, int64_t rows_a,
+                               const int32_t *row_index, const int32_t *offsets, const float *B,
+                               int64_t ldb, int64_t stride_b, gemm_order_t order_b, void *D,
+                               int64_t ldd, const gemm_epilogue_t *epilogue, cudaStream_t stream);
+gemm_status_t gemm_grouped_bf16_f32acc(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                       float alpha, const gemm_bf16_t *A, int64_t lda,
+                                       int64_t rows_a, const int32_t *row_index,
+                                       const int32_t *offsets, const gemm_bf16_t *B, int64_t ldb,
+                                       int64_t stride_b, gemm_order_t order_b, void *D,
+                                       int64_t ldd, const gemm_epilogue_t *epilogue,
+                                       cudaStream_t stream);
+gemm_status_t gemm_grouped_f16_f32acc(int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                      float alpha, const gemm_f16_t *A, int64_t lda,
+                                      int64_t rows_a, const int32_t *row_index,
+                                      const int32_t *offsets, const gemm_f16_t *B, int64_t ldb,
+                                      int64_t stride_b, gemm_order_t order_b, void *D,
+                                      int64_t ldd, const gemm_epilogue_t *epilogue,
+                                      cudaStream_t stream);
+
+/*
+ * gemm_grouped_wgrad_* -- the weight gradients of the grouped products:
+ *
+ *     D_g = alpha * sum over the rows r of group g of A(idx(r), :)^T B(r, :)
+ *           + beta * C_g
+ *
+ * A has M columns (the product's inputs), B has N columns (the gradient of
+ * its outputs, row-major, one row per product row), D_g and C_g are M x N
+ * row-major with group strides stride_d and stride_c.  C is FP32 and not read
+ * when beta == 0; C == D with equal strides is allowed when D is FP32
+ * (accumulation in place); the matrices of D must not overlap.
+ * Accuracy as gemm_grouped_*, plus 1e-6 |beta C|.
+ */
+gemm_status_t gemm_grouped_wgrad_f32(int64_t groups, int64_t rows, int64_t M, int64_t N,
+                                     float alpha, const float *A, int64_t lda, int64_t rows_a,
+                                     const int32_t *row_index, const int32_t *offsets,
+                                     const float *B, int64_t ldb, float beta, const float *C,
+                                     int64_t ldc, int64_t stride_c, void *D, int64_t ldd,
+                                     int64_t stride_d, gemm_d_type_t d_type, cudaStream_t stream);
+gemm_status_t gemm_grouped_wgrad_bf16_f32acc(int64_t groups, int64_t rows, int64_t M, int64_t N,
+                                             float alpha, const gemm_bf16_t *A, int64_t lda,
+                                             int64_t rows_a, const int32_t *row_index,
+                                             const int32_t *offsets, const gemm_bf16_t *B,
+                                             int64_t ldb, float beta, const float *C, int64_t ldc,
+                                             int64_t stride_c, void *D, int64_t ldd,
+                                             int64_t stride_d, gemm_d_type_t d_type,
+                                             cudaStream_t stream);
+gemm_status_t gemm_grouped_wgrad_f16_f32acc(int64_t groups, int64_t rows, int64_t M, int64_t N,
+                                            float alpha, const gemm_f16_t *A, int64_t lda,
+                                            int64_t rows_a, const int32_t *row_index,
+                                            const int32_t *offsets, const gemm_f16_t *B,
+                                            int64_t ldb, float beta, const float *C, int64_t ldc,
+                                            int64_t stride_c, void *D, int64_t ldd,
+                                            int64_t stride_d, gemm_d_type_t d_type,
+                                            cudaStream_t stream);
+
+/*
+ * gemm_lora_* -- a shared projection with each row's own low-rank adapter:
+ *
+ *     D(i, :) = act(X(i, :) op(W) + scale[a] (X(i, :) op(LA_a)) op(LB_a) + bias),
+ *     a = adapter_of_row[i]
+ *
+ * X is M x K row-major, op(W) K x N; every op(LA_a) is K x rank and op(LB_a)
+ * rank x N, in stacks of `adapters` matrices.  A row whose number lies outside
+ * [0, adapters) has no adapter.  Rows come in any order: nothing is sorted
+ * and the host does not read the numbers.  scale is `adapters` FP32 values or
+ * NULL (all 1); epilogue as for gemm_grouped_* with one bias of N values.
+ * The input gradient is the same call with W, LA and LB exchanged:
+ * dX = dD op(W)^T + scale (dD LB^T) LA^T; the adapters' own gradients are
+ * gemm_grouped_wgrad_* over rows grouped by adapter.
+ * An adapter's values reach the rows that use it only (also infinities and
+ * NaNs).  Rounding: the first product scale * X LA is summed in FP32 and
+ * enters the second one rounded to the inputs' type when D has that type, and
+ * as the sum of two such values (about 16 bits for BF16, 22 for FP16) when D
+ * is FP32; with FP16 it must stay inside FP16's range.
+ * Accuracy: the bound of gemm_grouped_* on X W, plus 2^-8 (2^-15 with an FP32
+ * D) of sum |scale (X LA)| |LB|.
+ */
+gemm_status_t gemm_lora_bf16_f32acc(int64_t M, int64_t N, int64_t K, const gemm_bf16_t *X,
+                                    int64_t ldx, const gemm_bf16_t *W, int64_t ldw,
+                                    gemm_order_t order_w, int64_t adapters, int64_t rank,
+                                    const int32_t *adapter_of_row, const float *scale,
+                                    const gemm_bf16_t *LA, int64_t ld_a, int64_t stride_a,
+                                    gemm_order_t order_a, const gemm_bf16_t *LB, int64_t ld_b,
+                                    int64_t stride_b, gemm_order_t order_b, void *D, int64_t ldd,
+                                    const gemm_epilogue_t *epilogue, cudaStream_t stream);
+gemm_status_t gemm_lora_f16_f32acc(int64_t M, int64_t N, int64_t K, const gemm_f16_t *X,
+                                   int64_t ldx, const gemm_f16_t *W, int64_t ldw,
+                                   gemm_order_t order_w, int64_t adapters, int64_t rank,
+                                   const int32_t *adapter_of_row, const float *scale,
+                                   const gemm_f16_t *LA, int64_t ld_a, int64_t stride_a,
+                                   gemm_order_t order_a, const gemm_f16_t *LB, int64_t ld_b,
+                                   int64_t stride_b, gemm_order_t order_b, void *D, int64_t ldd,
+                                   const gemm_epilogue_t *epilogue, cudaStream_t stream);
 
 /* Static English description of a status code; never NULL. */
 const char *gemm_status_string(gemm_status_t status);
