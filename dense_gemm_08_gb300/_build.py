@@ -20,10 +20,12 @@ LIB_NAME = "libdense_gemm_08_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["gemm_api.cu", "sgemm_simt.cu", "sgemm_cluster.cu", "gemm_tc.cu", "workspace.cu",
-           "probe.cu", "skinny.cu", "grouped_api.cu", "grouped_simt.cu", "group_rows.cu"]
+           "probe.cu", "skinny.cu", "grouped_api.cu", "grouped_simt.cu",
+           "grouped_tc.cu", "group_rows.cu"]
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "epilogue.cuh"),
            os.path.join(CSRC, "call.h"), os.path.join(CSRC, "grouped.h"),
-           os.path.join(CSRC, "grouped.cuh"),
+           os.path.join(CSRC, "grouped.cuh"), os.path.join(CSRC, "tcgen05.cuh"),
+           os.path.join(CSRC, "tc_epilogue.cuh"), os.path.join(CSRC, "tma_maps.h"),
            os.path.join(INCLUDE, "gemm.h"), os.path.join(INCLUDE, "gemm_probe.h")]
 
 NVCC_FLAGS = [

@@ -13,6 +13,7 @@
 #include "call.h"
 #include "gemm.h"
 #include "gemm_probe.h"
+#include "grouped.h"
 #include "internal.h"
 
 #define GEMM_API extern "C" __attribute__((visibility("default")))
@@ -280,7 +281,10 @@ GEMM_API const char *gemm_status_string(gemm_status_t status) {
 GEMM_API gemm_status_t gemm_last_device_status(cudaStream_t stream) {
     int status = 0;
     if (gemm::tc_read_and_clear_status(stream, &status) != cudaSuccess) return GEMM_ERR_INTERNAL;
-    if (status) {
+    int grouped = 0;
+    if (gemm::grouped_tc_read_and_clear_status(stream, &grouped) != cudaSuccess)
+        return GEMM_ERR_INTERNAL;
+    if (status || grouped) {
         // a kernel that gave up may have left split counters mid-count
         if (gemm::split_sync_release_device() != cudaSuccess) return GEMM_ERR_INTERNAL;
         return GEMM_ERR_TIMEOUT;

@@ -15,7 +15,8 @@ namespace gemm {
 // ceil(m / tile_rows) * per_row tiles.  The 32 lanes of a warp hold 32 groups
 // at a time (one load and one warp scan per 32 groups), so a tile's group is
 // found without a table in shared memory and without the host knowing the
-// sizes.  locate() must be called by the whole warp, with tile numbers that
+// sizes.  Offsets count as the largest clamped value so far, so groups never
+// share a row, whatever the values.  locate() must be called by the whole warp, with tile numbers that
 // never fall.
 struct GroupWalk {
     const int32_t *offsets;
@@ -28,6 +29,7 @@ struct GroupWalk {
     uint32_t chunk_tiles = 0;
     uint32_t incl = 0;       // this lane's group and the ones before it in the chunk
     int32_t lo = 0, hi = 0;  // this lane's group's rows
+    int32_t reached = 0;     // largest offset of the chunks before
 
     __device__ __forceinline__ GroupWalk(const int32_t *offsets, int64_t groups, int64_t rows,
                                          int tile_rows, uint32_t per_row)
@@ -54,8 +56,15 @@ struct GroupWalk {
             if (mine < groups) {
                 lo = bounded(__ldg(offsets + mine));
                 hi = bounded(__ldg(offsets + mine + 1));
-                if (hi < lo) hi = lo;
             }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t below = __shfl_up_sync(0xffffffffu, lo, d);
+                if (lane >= d && below > lo) lo = below;
+            }
+            if (lo < reached) lo = reached;
+            if (hi < lo) hi = lo;
+            reached = __shfl_sync(0xffffffffu, hi, 31);
             incl = static_cast<uint32_t>((static_cast<int64_t>(hi) - lo + tile_rows - 1) / tile_rows) * per_row;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {

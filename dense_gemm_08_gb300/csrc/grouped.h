@@ -83,6 +83,16 @@ cudaError_t launch_wgrad_simt(const WgradProblem &p, InType in, cudaStream_t str
 cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t stream,
                              const char **name);
 
+// Tensor-core kernels (grouped_tc.cu): BF16 or FP16 operands that TMA can describe.
+bool grouped_tc_eligible(const GroupedProblem &p);
+cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t stream,
+                              const char **name);
+bool wgrad_tc_eligible(const WgradProblem &p);
+cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t stream,
+                            const char **name);
+// Reads and clears those kernels' device status word (after a sync).
+cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status);
+
 // Rows grouped by a number (group_rows.cu).
 cudaError_t launch_group_rows(int64_t rows, int64_t groups, const int32_t *group_of_row,
                               int32_t *offsets, int32_t *order, int32_t *position,

@@ -98,7 +98,10 @@ gemm_status_t grouped(InType in, int64_t groups, int64_t rows, int64_t N, int64_
     p.act = static_cast<int>(ep.activation);
     p.out = static_cast<int>(ep.d_type);
     const char *name = "";
-    return gemm::finish_call(gemm::launch_grouped_simt(p, in, stream, &name), name);
+    const bool tc = in != InType::F32 && gemm::grouped_tc_eligible(p);
+    return gemm::finish_call(tc ? gemm::launch_grouped_tc(p, in, stream, &name)
+                                : gemm::launch_grouped_simt(p, in, stream, &name),
+                             name);
 }
 
 gemm_status_t wgrad(InType in, int64_t groups, int64_t rows, int64_t M, int64_t N, float alpha,
@@ -144,7 +147,10 @@ gemm_status_t wgrad(InType in, int64_t groups, int64_t rows, int64_t M, int64_t 
     p.stride_d = stride_d;
     p.out = static_cast<int>(d_type);
     const char *name = "";
-    return gemm::finish_call(gemm::launch_wgrad_simt(p, in, stream, &name), name);
+    const bool tc = in != InType::F32 && gemm::wgrad_tc_eligible(p);
+    return gemm::finish_call(tc ? gemm::launch_wgrad_tc(p, in, stream, &name)
+                                : gemm::launch_wgrad_simt(p, in, stream, &name),
+                             name);
 }
 
 gemm_status_t lora(InType in, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,

@@ -1,0 +1,747 @@
+// grouped_tc.cu -- the grouped products and their weight gradients on the
+// sm_103a tensor cores (BF16 or FP16 inputs, FP32 accumulation).
+//
+//   rows:   D(r, :) = act(alpha * A(idx(r), :) op(B_g) + bias_g), r in group g
+//   wgrad:  D_g = alpha * sum_{r in g} A(idx(r), :)^T B(r, :) + beta * C_g
+//
+// Persistent CTAs (or CTA pairs) walk the tiles of all groups; a tile belongs
+// to one group.  The sizes of the groups are on the device only: each warp
+// finds a tile's group with a warp scan over the offsets (GroupWalk).  Warp 0
+// fills a ring of 128-byte-swizzled stages by TMA, warp 1 issues tcgen05.mma
+// into one of two TMEM accumulators, warps 2-5 write the other to D.
+//
+//   rows: a row tile may end inside the next group's rows.  They are loaded
+//     or not, but only reach accumulator rows that are not stored (each row
+//     of D depends on its own row of A), so no zero fill is needed.  A row
+//     tile with few rows loads 16-row boxes; gathered rows come four at a time
+//     by TMA gather, with each lane's row numbers in registers.
+//   wgrad: both operands have their rows along K and are MN-major.  A group's
+//     last K block must not read the next group's rows (not even times zero:
+//     they may be infinite), so that block is fetched by TMA gather with row
+//     numbers outside the tensor (zeros) past the group's end, and only its
+//     16-row slices that hold rows are multiplied.
+#include <mutex>
+
+#include "grouped.cuh"
+#include "internal.h"
+#include "tc_epilogue.cuh"
+#include "tcgen05.cuh"
+#include "tma_maps.h"
+
+namespace gemm {
+namespace {
+
+using namespace tc;
+
+enum : int { kRows = 0, kWgrad = 1 };
+
+constexpr int kGroupM = 16;  // row tiles per band of the raster inside a group
+constexpr int kMaxStages = 16;
+constexpr int kThreads = 192;
+constexpr int kEpiWarps = 4;
+constexpr int kRingBytes = 7 * 32768;  // both variants
+constexpr int kSmemBytes = kRingBytes + 1024 + 512;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+
+struct Args {
+    int64_t groups, rows, M, N;  // M: wgrad only
+    const int32_t *offsets, *row_index;
+    OutArgs out;
+    int64_t stride_d, stride_c;
+    uint32_t tiles_m, tiles_n;  // tiles_m: wgrad only
+    int num_kb;                 // rows: K blocks
+    int b_kmajor;               // rows
+    int bn;                     // columns per tile (of the CTA or the pair)
+    int stages;
+    uint32_t stage_bytes;
+    int ab_format;
+    int z_step;  // rows: 0 when all groups share one B
+    uint64_t timeout_ns;
+};
+
+struct Tile {
+    int g;
+    int32_t first, last;  // the group's rows
+    int64_t m0, n0;       // first row (rows: of all product rows; wgrad: of D_g) and column
+    int m_valid;          // rows of D in the tile, 1 .. 128 CG
+    int nkb;              // K blocks
+};
+
+template <int CG, int MODE>
+struct TileWalk {
+    const Args &a;
+    GroupWalk walk;
+    __device__ __forceinline__ explicit TileWalk(const Args &a)
+        : a(a), walk(a.offsets, a.groups, a.rows, BM * CG, a.tiles_n) {}
+
+    // Tile w; the whole warp calls.  False past the last tile.
+    __device__ __forceinline__ bool get(uint32_t w, Tile &t) {
+        uint32_t in_group, tiles_m;
+        if constexpr (MODE == kRows) {
+            if (!walk.locate(w, t.g, t.first, t.last, in_group)) return false;
+            tiles_m = (static_cast<uint32_t>(t.last - t.first) + BM * CG - 1) / (BM * CG);
+        } else {
+            const uint32_t per = a.tiles_m * a.tiles_n;
+            const uint32_t g = w / per;
+            if (g >= a.groups) return false;
+            in_group = w - g * per;
+            t.g = static_cast<int>(g);
+            t.first = walk.bounded(__ldg(a.offsets + g));
+            t.last = walk.bounded(__ldg(a.offsets + g + 1));
+            if (t.last < t.first) t.last = t.first;
+            tiles_m = a.tiles_m;
+        }
+        const uint32_t width = kGroupM * a.tiles_n;
+        const uint32_t band = in_group / width, in_band = in_group - band * width;
+        const uint32_t rest = tiles_m - band * kGroupM;
+        const uint32_t high = rest < kGroupM ? rest : kGroupM;
+        const uint32_t q = in_band / high;
+        const int64_t tm = band * kGroupM + (in_band - q * high);
+        t.n0 = static_cast<int64_t>(q) * a.bn;
+        const int64_t m_first = MODE == kRows ? t.first : 0;
+        const int64_t m_last = MODE == kRows ? t.last : a.M;
+        t.m0 = m_first + tm * (BM * CG);
+        t.m_valid = m_last - t.m0 < BM * CG ? static_cast<int>(m_last - t.m0) : BM * CG;
+        t.nkb = MODE == kRows ? a.num_kb
+                              : static_cast<int>((static_cast<int64_t>(t.last) - t.first + BK - 1) / BK);
+        return true;
+    }
+};
+
+// Rows of the tile in CTA `rank` of the group (0 to 128).
+__device__ __forceinline__ int cta_rows(const Tile &t, int rank) {
+    const int r = t.m_valid - rank * BM;
+    return r < 0 ? 0 : (r > BM ? BM : r);
+}
+
+// rows: A bytes a CTA loads per stage for n of its 128 rows -- all 128 in one
+// box when more than 64 hold data, else boxes of 16 rows; gathered: quads.
+__device__ __forceinline__ uint32_t a_bytes(int n, bool gather) {
+    if (gather) return static_cast<uint32_t>((n + 3) / 4) * 512u;
+    return n > 64 ? BM * 128u : static_cast<uint32_t>((n + 15) / 16) * 2048u;
+}
+
+template <int CG, int MODE, bool GATHER>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_a_part,
+                      const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_b_part, const Args args) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + kRingBytes);
+    uint64_t *full = bars;                // [kMaxStages] TMA -> MMA (the leader counts both CTAs)
+    uint64_t *empty = bars + kMaxStages;  // [kMaxStages] MMA -> TMA
+    uint64_t *tfull = empty + kMaxStages;  // [2] MMA -> epilogue
+    uint64_t *tempty = tfull + 2;          // [2] epilogue -> MMA (the leader counts both CTAs)
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 1 ? 0u : cluster_rank();
+    const bool leader = rank == 0;
+    const uint32_t first_tile = blockIdx.x / CG, tile_step = gridDim.x / CG;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_addr(&full[s]), 1);
+            mbar_init(smem_addr(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&tfull[b]), 1);
+            mbar_init(smem_addr(&tempty[b]), kEpiWarps * CG);
+        }
+        mbar_init(smem_addr(drain), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a_part))
+                     : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
+        if (MODE == kWgrad)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b_part))
+                         : "memory");
+    }
+    if (warp == 1) tmem_alloc<CG>(smem_addr(tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const uint32_t ring_base = smem_addr(ring);
+    const int stages = args.stages;
+    const uint32_t stage_bytes = args.stage_bytes;
+    constexpr uint32_t kABytes = BM * BK * 2;
+    const int b_rows = args.bn / CG;  // columns of B this CTA loads
+    TileWalk<CG, MODE> tiles(args);
+    Tile t;
+    bool aborted = false;
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        int ok = 1;
+        bool reverse = false;
+        for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
+            const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+            if constexpr (MODE == kRows) {
+                const int mine = cta_rows(t, rank);
+                const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
+                const uint32_t tx = a_bytes(cta_rows(t, 0), GATHER) +
+                                    (CG == 2 ? a_bytes(cta_rows(t, 1), GATHER) : 0u) +
+                                    CG * b_rows * 128u;
+                const int32_t z = t.g * args.z_step;
+                int32_t rows4[4];
+                if constexpr (GATHER) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        rows4[i] = lane * 4 + i < mine ? __ldg(args.row_index + m0 + lane * 4 + i) : -1;
+                }
+                for (int i = 0; i < t.nkb; ++i) {
+                    // every other tile walks K backwards: it starts on the
+                    // blocks of B the tile before it read last
+                    const int32_t k0 = (reverse ? t.nkb - 1 - i : i) * BK;
+                    if (lane == 0)
+                        ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
+                                          args.timeout_ns);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        if (lane == 0) raise_abort(abort_flag);
+                        break;
+                    }
+                    const uint32_t fb_local = smem_addr(&full[stage]);
+                    const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
+                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + kABytes;
+                    if (lane == 0) {
+                        if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                        if (args.b_kmajor) {
+                            tma_load_3d<CG>(sb, &map_b, k0, b0, z, fb);
+                        } else {
+                            for (int j = 0; j < b_rows; j += 64)
+                                tma_load_3d<CG>(sb + j * 128, &map_b, b0 + j, k0, z, fb);
+                        }
+                        if constexpr (!GATHER) {
+                            if (mine > 64) {
+                                tma_load_2d<CG>(sa, &map_a, k0, m0, fb);
+                            } else {
+                                for (int j = 0; j < mine; j += 16)
+                                    tma_load_2d<CG>(sa + j * 128, &map_a_part, k0, m0 + j, fb);
+                            }
+                        }
+                    }
+                    if constexpr (GATHER) {
+                        if (lane * 4 < mine)
+                            tma_gather4<CG>(sa + lane * 512, &map_a_part, k0, rows4[0], rows4[1],
+                                            rows4[2], rows4[3], fb);
+                    }
+                    ++issued;
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            } else {
+                const int32_t a0 = static_cast<int32_t>(t.m0 + rank * BM);
+                const int b_blocks = b_rows / 64;
+                // gathered blocks: lane -> quad of rows (lane % 16) of 64-column
+                // blocks lane / 16, lane / 16 + 2, ...
+                const int quad = lane % 16;
+                int32_t next[4] = {-1, -1, -1, -1};
+                auto fetch = [&](int kb) {  // numbers of this lane's rows of A in block kb
+                    const int64_t r0 = static_cast<int64_t>(t.first) + kb * BK + quad * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        next[i] = -1;
+                        if (r0 + i < t.last)
+                            next[i] = GATHER ? __ldg(args.row_index + r0 + i)
+                                             : static_cast<int32_t>(r0 + i);
+                    }
+                };
+                if (t.nkb > 0) fetch(0);
+                for (int i = 0; i < t.nkb; ++i) {
+                    const int32_t r0 = t.first + i * BK;
+                    const int rem = t.last - r0 < BK ? t.last - r0 : BK;
+                    const int quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
+                    const bool part = rem < BK;
+                    int32_t mine[4] = {next[0], next[1], next[2], next[3]};
+                    if (i + 1 < t.nkb) fetch(i + 1);
+                    if (lane == 0)
+                        ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
+                                          args.timeout_ns);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        if (lane == 0) raise_abort(abort_flag);
+                        break;
+                    }
+                    const uint32_t fb_local = smem_addr(&full[stage]);
+                    const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
+                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + kABytes;
+                    if (lane == 0) {
+                        if (leader)
+                            mbar_arrive_expect_tx(
+                                fb_local, CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
+                        if (!part) {
+                            if constexpr (!GATHER) {
+                                tma_load_2d<CG>(sa, &map_a, a0, r0, fb);
+                                tma_load_2d<CG>(sa + 8192, &map_a, a0 + 64, r0, fb);
+                            }
+                            for (int j = 0; j < b_blocks; ++j)
+                                tma_load_2d<CG>(sb + j * 8192, &map_b, b0 + 64 * j, r0, fb);
+                        }
+                    }
+                    if (quad < quads) {
+                        if (GATHER || part)
+                            tma_gather4<CG>(sa + (lane / 16) * 8192 + quad * 512, &map_a_part,
+                                            a0 + (lane / 16) * 64, mine[0], mine[1], mine[2],
+                                            mine[3], fb);
+                        if (part) {
+                            const int32_t q0 = r0 + quad * 4;
+                            for (int j = lane / 16; j < b_blocks; j += 2)
+                                tma_gather4<CG>(sb + j * 8192 + quad * 512, &map_b_part, b0 + 64 * j,
+                                                q0 < t.last ? q0 : -1, q0 + 1 < t.last ? q0 + 1 : -1,
+                                                q0 + 2 < t.last ? q0 + 2 : -1,
+                                                q0 + 3 < t.last ? q0 + 3 : -1, fb);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        // the copies in flight land before the CTA exits (the leader's
+        // barriers count both CTAs' bytes)
+        if (lane == 0 && leader) {
+            const int64_t outstanding = issued < stages ? issued : stages;
+            for (int64_t i = 0; i < outstanding; ++i) {
+                if (--stage < 0) {
+                    stage = stages - 1;
+                    phase ^= 1;
+                }
+                const volatile int never = 0;
+                if (!wait_bounded(smem_addr(&full[stage]), phase, &never, args.timeout_ns))
+                    raise_abort(abort_flag);
+            }
+        }
+        aborted = !ok;
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer
+        if (leader) {
+            const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
+            const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
+            const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring_base, 0) : desc_kmajor(ring_base, 0);
+            const uint64_t b_desc0 = b_mn ? desc_mnmajor(ring_base + kABytes, 0)
+                                          : desc_kmajor(ring_base + kABytes, 0);
+            const uint64_t a_step = a_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+            const uint64_t b_step = b_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+            const uint32_t full0 = smem_addr(&full[0]), empty0 = smem_addr(&empty[0]);
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t acc = 0;  // accumulators filled so far
+            int ok = 1;
+            for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step) {
+                if (MODE == kWgrad && t.nkb == 0) continue;  // no rows: nothing to add
+                if (lane == 0) {
+                    const int buf = static_cast<int>(acc & 1);
+                    ok = wait_bounded(smem_addr(&tempty[buf]), ((acc >> 1) & 1) ^ 1, abort_flag,
+                                      args.timeout_ns);
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
+                    // 16-row slices of the last block that hold rows
+                    const int last_slices =
+                        MODE == kWgrad ? (t.last - t.first - (t.nkb - 1) * BK + 15) / 16 : 4;
+                    auto wait_full = [&](int s, uint32_t p) {
+                        const uint32_t fb = full0 + 8u * static_cast<uint32_t>(s);
+                        return mbar_try_wait(fb, p) ||
+                               wait_bounded(fb, p, abort_flag, args.timeout_ns);
+                    };
+                    auto multiply = [&](int s, int slices, uint32_t add) {
+                        const uint64_t ad = a_desc0 + static_cast<uint64_t>(s) * (stage_bytes >> 4);
+                        const uint64_t bd = b_desc0 + static_cast<uint64_t>(s) * (stage_bytes >> 4);
+                        tc_mma<CG>(d_tmem, ad, bd, idesc, add);
+                        if (MODE == kRows || slices > 1)
+                            tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
+                        if (MODE == kRows || slices > 2)
+                            tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
+                        if (MODE == kRows || slices > 3)
+                            tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
+                    };
+                    for (int i = 0; ok && i < t.nkb; i += 2) {
+                        // two stages per round: their MMAs issue back to back
+                        const bool two = i + 1 < t.nkb;
+                        const int s0 = stage, s1 = s0 + 1 == stages ? 0 : s0 + 1;
+                        const uint32_t p0 = phase, p1 = s1 == 0 ? p0 ^ 1u : p0;
+                        if (!wait_full(s0, p0) || (two && !wait_full(s1, p1))) {
+                            ok = 0;
+                            break;
+                        }
+                        tc_fence_after();
+                        multiply(s0, i + 1 == t.nkb ? last_slices : 4, i > 0 ? 1u : 0u);
+                        if (two) multiply(s1, i + 2 == t.nkb ? last_slices : 4, 1u);
+                        tc_commit<CG>(empty0 + 8u * static_cast<uint32_t>(s0));
+                        if (two) {
+                            tc_commit<CG>(empty0 + 8u * static_cast<uint32_t>(s1));
+                            stage = s1 + 1 == stages ? 0 : s1 + 1;
+                            phase = stage == 0 ? p1 ^ 1u : p1;
+                        } else {
+                            stage = s1;
+                            phase = p1;
+                        }
+                    }
+                    if (ok)
+                        tc_commit<CG>(smem_addr(&tfull[buf]));
+                    else
+                        raise_abort(abort_flag);
+                }
+                ++acc;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            }
+            if (lane == 0) {
+                tc_commit_local<CG>(smem_addr(drain));
+                const volatile int never = 0;
+                if (!wait_bounded(smem_addr(drain), 0, &never, args.timeout_ns))
+                    raise_abort(abort_flag);
+            }
+            aborted = !ok;
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------- epilogue warps 2-5
+        const int quarter = warp % 4;  // TMEM lanes this warp may access
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t acc = 0;
+        for (uint32_t w = first_tile; tiles.get(w, t); w += tile_step) {
+            const bool empty_sum = MODE == kWgrad && t.nkb == 0;
+            const int buf = static_cast<int>(acc & 1);
+            if (!empty_sum) {
+                int ok = 1;
+                if (lane == 0)
+                    ok = wait_bounded(smem_addr(&tfull[buf]), (acc >> 1) & 1, abort_flag,
+                                      args.timeout_ns);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) {
+                    if (lane == 0) raise_abort(abort_flag);
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                ++acc;
+            }
+            auto release_acc = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t te = smem_addr(&tempty[buf]);
+                    if constexpr (CG == 1)
+                        mbar_arrive(te);
+                    else
+                        mbar_arrive_cluster(map_to_rank(te, 0));
+                }
+            };
+            int nrows = t.m_valid - static_cast<int>(rank) * BM - quarter * 32;
+            nrows = nrows < 0 ? 0 : (nrows > 32 ? 32 : nrows);
+            const int64_t row0 = t.m0 + rank * BM + quarter * 32;
+            const int64_t rest = args.N - t.n0;
+            const int ncols = rest < args.bn ? static_cast<int>(rest) : args.bn;
+            const int n_chunks = nrows > 0 ? (ncols + 31) / 32 : 0;
+            OutArgs o = args.out;
+            if constexpr (MODE == kRows) {
+                if (o.bias != nullptr) o.bias += t.g * args.N;
+            } else {
+                o.D = static_cast<uint8_t *>(o.D) + t.g * args.stride_d * (o.out == kOutF32 ? 4 : 2);
+                if (o.beta != 0.f) o.C += t.g * args.stride_c;
+            }
+            const uint32_t t_acc = tmem_base + lane_off + static_cast<uint32_t>(buf * 256);
+            const bool use_c = MODE == kWgrad && o.beta != 0.f;
+            float c_next[32];
+            auto next_c = [&](int chunk) {  // this lane's C of the chunk, one chunk ahead
+                if (use_c && lane < nrows && direct_block(o, ncols - chunk * 32 < 32 ? 0 : 32))
+                    load_c_row(o, row0 + lane, t.n0 + chunk * 32, c_next);
+            };
+            if (n_chunks > 0) next_c(0);
+#pragma unroll 1
+            for (int chunk = 0; chunk < n_chunks; ++chunk) {
+                float c[32], v[32];
+                if (use_c) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) c[j] = c_next[j];
+                    if (chunk + 1 < n_chunks) next_c(chunk + 1);
+                }
+                if (empty_sum) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                } else {
+                    uint32_t raw[32];
+                    __syncwarp();
+                    tmem_load_32cols(t_acc + chunk * 32, raw);
+                    if (chunk == n_chunks - 1) release_acc();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                }
+                const int left = ncols - chunk * 32;
+                emit_block(v, c, o, row0, nrows, t.n0 + chunk * 32, left < 32 ? left : 32);
+                __syncwarp();
+            }
+            if (n_chunks == 0 && !empty_sum) release_acc();
+        }
+        __syncwarp();
+    }
+
+    if (aborted) {
+        // give copies issued by a peer that gave up a short time to land
+        const uint64_t t0 = global_timer();
+        while (global_timer() - t0 < 2000000ull) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc<CG>(tmem_base);
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kMaxDevices = 64;
+
+struct DeviceInfo {
+    std::once_flag once;
+    cudaError_t err = cudaSuccess;
+    int sms = 1;
+    int pairs = 0;  // CTA pairs resident at once
+};
+DeviceInfo g_dev[kMaxDevices];
+
+template <int CG, int MODE, bool GATHER>
+cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    set_pdl_attribute(&attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
+    return cfg;
+}
+
+template <int CG, int MODE, bool GATHER>
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(grouped_tc_kernel<CG, MODE, GATHER>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+}
+
+DeviceInfo *device_info() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    DeviceInfo *d = &g_dev[dev];
+    std::call_once(d->once, [d, dev] {
+        int n = 0;
+        d->err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (d->err != cudaSuccess) return;
+        d->sms = n > 0 ? n : 1;
+        for (cudaError_t e : {allow_smem<1, kRows, false>(), allow_smem<1, kRows, true>(),
+                              allow_smem<2, kRows, false>(), allow_smem<2, kRows, true>(),
+                              allow_smem<1, kWgrad, false>(), allow_smem<1, kWgrad, true>(),
+                              allow_smem<2, kWgrad, false>(), allow_smem<2, kWgrad, true>()})
+            if (d->err == cudaSuccess) d->err = e;
+        if (d->err != cudaSuccess) return;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = config<2, kRows, false>(2 * (d->sms / 2), 0, attr);
+        cfg.attrs = attr + 1;  // the occupancy query takes the cluster shape only
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&d->pairs, grouped_tc_kernel<2, kRows, false>, &cfg) !=
+            cudaSuccess) {
+            d->pairs = 0;
+            (void)cudaGetLastError();  // the pair variants are then not used
+        }
+    });
+    return d;
+}
+
+template <int CG, int MODE>
+cudaError_t launch(const CUtensorMap (&maps)[4], const Args &a, bool gather, int64_t max_tiles,
+                   const DeviceInfo *d, cudaStream_t stream) {
+    const int64_t resident = CG == 2 ? d->pairs : d->sms;
+    const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
+    cudaLaunchAttribute attr[2];
+    if (gather) {
+        cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
+        return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
+                                  maps[2], maps[3], a);
+    }
+    cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, stream, attr);
+    return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, false>, maps[0], maps[1], maps[2],
+                              maps[3], a);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile width of the single-CTA variant and the ring to match.
+void set_width(Args &a, int cg, int bn) {
+    a.bn = bn;
+    a.stage_bytes = BM * BK * 2 + static_cast<uint32_t>(bn / cg) * BK * 2;
+    const int fit = static_cast<int>(kRingBytes / a.stage_bytes);
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+}
+
+constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bit
+
+}  // namespace
+
+bool grouped_tc_eligible(const GroupedProblem &p) {
+    return p.K > 0 && p.rows_a > 0 && tma_rows(p.A, p.lda) &&
+           tma_rows(p.B, p.ldb, p.groups > 1 ? p.stride_b : 0) &&
+           (ceil_div(p.rows, BM) + (p.groups < p.rows ? p.groups : p.rows)) * ceil_div(p.N, 64) <
+               kMaxTiles;
+}
+
+cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t stream,
+                              const char **name) {
+    const bool bf16 = in == InType::BF16;
+    DeviceInfo *d = device_info();
+    if (d == nullptr) return cudaErrorInvalidDevice;
+    if (d->err != cudaSuccess) return d->err;
+    Args a = {};
+    a.groups = p.groups;
+    a.rows = p.rows;
+    a.N = p.N;
+    a.offsets = p.offsets;
+    a.row_index = p.row_index;
+    a.out.D = p.D;
+    a.out.ldd = p.ldd;
+    a.out.bias = p.bias;
+    a.out.alpha = p.alpha;
+    a.out.act = p.act;
+    a.out.out = p.out;
+    a.out.row_vec = row_alignment(p.D, p.ldd, 0, p.out == kOutF32 ? 4 : 2);
+    a.num_kb = static_cast<int>(ceil_div(p.K, BK));
+    a.b_kmajor = p.b_kmajor ? 1 : 0;
+    a.ab_format = bf16 ? 1 : 0;
+    a.timeout_ns = 1000ull * 1000ull * 1000ull;
+    const bool one_b = p.groups == 1 || p.stride_b == 0;
+    a.z_step = one_b ? 0 : 1;
+    // Groups that may hold rows, and row tiles if the rows spread evenly.
+    const int64_t live = p.groups < p.rows ? p.groups : p.rows;
+    const int64_t pair_tiles = live * ceil_div(ceil_div(p.rows, live), 2 * BM) * ceil_div(p.N, 256);
+    const bool pair = d->pairs > 0 && p.rows / live > BM && pair_tiles >= d->pairs;
+    if (pair) {
+        set_width(a, 2, 256);
+    } else {
+        const int64_t row_tiles = live * ceil_div(ceil_div(p.rows, live), BM);
+        int bn = 256;
+        while (bn > 64 && row_tiles * ceil_div(p.N, bn) < 4 * d->sms) bn /= 2;
+        set_width(a, 1, bn);
+    }
+    a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
+    const int cg = pair ? 2 : 1;
+    const bool gather = p.row_index != nullptr;
+    CUtensorMap maps[4];
+    bool ok = encode_stack(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, BM, 2) &&
+              encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, gather ? 1 : 16, 2);
+    const int64_t count = one_b ? 1 : p.groups, stride = one_b ? p.ldb : p.stride_b;
+    if (p.b_kmajor)
+        ok = ok && encode_stack(&maps[2], bf16, p.B, p.K, p.N, p.ldb, count, stride, BK,
+                                static_cast<uint32_t>(a.bn / cg), 3);
+    else
+        ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64, BK, 3);
+    if (!ok) return cudaErrorInvalidValue;
+    maps[3] = maps[2];
+    const int64_t max_tiles = (p.rows / (BM * cg) + live) * a.tiles_n;
+    static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
+                                             {"grouped_tc<bf16>", "grouped_tc<bf16,pair>"}};
+    *name = kNames[bf16][pair];
+    return pair ? launch<2, kRows>(maps, a, gather, max_tiles, d, stream)
+                : launch<1, kRows>(maps, a, gather, max_tiles, d, stream);
+}
+
+bool wgrad_tc_eligible(const WgradProblem &p) {
+    return p.rows > 0 && p.rows_a > 0 && tma_rows(p.A, p.lda) && tma_rows(p.B, p.ldb) &&
+           ceil_div(p.M, BM) * ceil_div(p.N, 64) < kMaxTiles / p.groups;
+}
+
+cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t stream,
+                            const char **name) {
+    const bool bf16 = in == InType::BF16;
+    DeviceInfo *d = device_info();
+    if (d == nullptr) return cudaErrorInvalidDevice;
+    if (d->err != cudaSuccess) return d->err;
+    Args a = {};
+    a.groups = p.groups;
+    a.rows = p.rows;
+    a.M = p.M;
+    a.N = p.N;
+    a.offsets = p.offsets;
+    a.row_index = p.row_index;
+    const int64_t elt = p.out == kOutF32 ? 4 : 2;
+    a.out.D = p.D;
+    a.out.ldd = p.ldd;
+    a.out.C = p.C;
+    a.out.ldc = p.ldc;
+    a.out.alpha = p.alpha;
+    a.out.beta = p.beta;
+    a.out.out = p.out;
+    a.out.row_vec = row_alignment(p.D, p.ldd, p.groups > 1 ? p.stride_d : 0, elt);
+    if (p.beta != 0.f) {
+        const int c = row_alignment(p.C, p.ldc, p.groups > 1 ? p.stride_c : 0, 4);
+        if (c < a.out.row_vec) a.out.row_vec = c;
+    }
+    a.stride_d = p.stride_d;
+    a.stride_c = p.stride_c;
+    a.ab_format = bf16 ? 1 : 0;
+    a.timeout_ns = 1000ull * 1000ull * 1000ull;
+    const int64_t pair_tiles = p.groups * ceil_div(p.M, 2 * BM) * ceil_div(p.N, 256);
+    const bool pair = d->pairs > 0 && p.M > BM && pair_tiles >= d->pairs;
+    const int cg = pair ? 2 : 1;
+    if (pair) {
+        set_width(a, 2, 256);
+    } else {
+        int bn = 256;
+        while (bn > 64 && p.groups * ceil_div(p.M, BM) * ceil_div(p.N, bn) < 2 * d->sms) bn /= 2;
+        set_width(a, 1, bn);
+    }
+    a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, BM * cg));
+    a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
+    CUtensorMap maps[4];
+    const bool gather = p.row_index != nullptr;
+    const bool ok =
+        encode_stack(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2) &&
+        encode_stack(&maps[1], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, 1, 2) &&
+        encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2) &&
+        encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
+    if (!ok) return cudaErrorInvalidValue;
+    const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
+    static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
+                                             {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
+    *name = kNames[bf16][pair];
+    return pair ? launch<2, kWgrad>(maps, a, gather, max_tiles, d, stream)
+                : launch<1, kWgrad>(maps, a, gather, max_tiles, d, stream);
+}
+
+cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status) {
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_status, sizeof(int), 0,
+                                              cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && *status != 0) {
+        e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    return e;
+}
+
+}  // namespace gemm

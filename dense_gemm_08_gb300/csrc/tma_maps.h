@@ -1,0 +1,55 @@
+// tma_maps.h -- tensor maps of the grouped kernels' 16-bit operands.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+namespace gemm {
+namespace tc {
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// A stack of `count` matrices of `outer` rows of `inner` 16-bit values: row
+// pitch ld, matrix pitch stride (elements), boxes of box_inner x box_outer
+// values of one matrix; values outside read as zero.  count = 1: 2-D maps.
+inline bool encode_stack(CUtensorMap *map, bool bf16, const void *base, int64_t inner,
+                         int64_t outer, int64_t ld, int64_t count, int64_t stride,
+                         uint32_t box_inner, uint32_t box_outer, int rank,
+                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+    const auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                          static_cast<cuuint64_t>(count)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {box_inner, box_outer, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What TMA asks of a matrix: 16-byte aligned base, row pitch (and matrix
+// pitch) of whole 16 bytes and below 2^40 bytes.
+inline bool tma_rows(const void *p, int64_t ld, int64_t stride = 0) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && stride % 8 == 0 &&
+           ld < (int64_t(1) << 39) && stride < (int64_t(1) << 39);
+}
+
+}  // namespace tc
+}  // namespace gemm

@@ -265,7 +265,8 @@ gemm_status_t gemm_bf16_f32acc_ex(int64_t M, int64_t N, int64_t K, float alpha,
  *   non-decreasing int32 values on the device (what gemm_group_rows writes);
  *   the host does not read it, so a call never waits for the sizes and can be
  *   captured in a graph.  The kernels clamp each value to [0, rows] and take
- *   a falling pair as an empty group.  Rows past offsets[groups] (and before
+ *   a falling pair as an empty group: other values than the above give
+ *   unspecified results, but no access outside the operands.  Rows past offsets[groups] (and before
  *   offsets[0]) belong to no group: no value computed from them is stored.
  * row_index (or NULL): product row r reads row row_index[r] of A, so rows
  *   need not be copied into group order first; an index outside [0, rows_a)
