@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["gemm_api.cu", "sgemm_simt.cu", "sgemm_cluster.cu", "gemm_tc.cu", "workspace.cu",
            "probe.cu", "skinny.cu", "grouped_api.cu", "grouped_simt.cu",
-           "grouped_tc.cu", "group_rows.cu"]
+           "grouped_tc.cu", "lora_shrink.cu", "group_rows.cu"]
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "epilogue.cuh"),
            os.path.join(CSRC, "call.h"), os.path.join(CSRC, "grouped.h"),
            os.path.join(CSRC, "grouped.cuh"), os.path.join(CSRC, "tcgen05.cuh"),

@@ -281,10 +281,11 @@ GEMM_API const char *gemm_status_string(gemm_status_t status) {
 GEMM_API gemm_status_t gemm_last_device_status(cudaStream_t stream) {
     int status = 0;
     if (gemm::tc_read_and_clear_status(stream, &status) != cudaSuccess) return GEMM_ERR_INTERNAL;
-    int grouped = 0;
-    if (gemm::grouped_tc_read_and_clear_status(stream, &grouped) != cudaSuccess)
+    int grouped = 0, shrink = 0;
+    if (gemm::grouped_tc_read_and_clear_status(stream, &grouped) != cudaSuccess ||
+        gemm::lora_shrink_read_and_clear_status(stream, &shrink) != cudaSuccess)
         return GEMM_ERR_INTERNAL;
-    if (status || grouped) {
+    if (status || grouped || shrink) {
         // a kernel that gave up may have left split counters mid-count
         if (gemm::split_sync_release_device() != cudaSuccess) return GEMM_ERR_INTERNAL;
         return GEMM_ERR_TIMEOUT;

@@ -90,6 +90,28 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
 bool wgrad_tc_eligible(const WgradProblem &p);
 cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t stream,
                             const char **name);
+bool lora_tc_eligible(const LoraProblem &p);
+cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream, const char **name);
+
+// What the first product of gemm_lora leaves for the second (lora_shrink.cu).
+// Rows are taken in tiles of tile_rows (at most 256); a tile's distinct
+// adapters have slots 0 .. count - 1.  V is a matrix of one row per row of X
+// with rc columns per slot: row i holds s_a X(i) LA_a rounded to the inputs'
+// type in its own adapter's slot (r_pad columns, and, when rc = 2 r_pad, the
+// rounding's remainder in r_pad more) and zeros in the tile's other slots.
+struct LoraPlan {
+    int tile_rows, r_pad, rc;
+    uint16_t *V;
+    int64_t ldv;
+    int *count;  // [tiles] slots in use
+    int *list;   // [tiles][tile_rows] the slots' adapters
+    int *slot;   // [rows] each row's slot, -1: no adapter
+};
+cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InType in,
+                               cudaStream_t stream);
+bool lora_shrink_eligible(const LoraProblem &p);
+cudaError_t lora_shrink_read_and_clear_status(cudaStream_t stream, int *status);
+
 // Reads and clears those kernels' device status word (after a sync).
 cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status);
 

@@ -207,7 +207,9 @@ gemm_status_t lora(InType in, int64_t M, int64_t N, int64_t K, const void *X, in
     p.act = static_cast<int>(ep.activation);
     p.out = static_cast<int>(ep.d_type);
     const char *name = "";
-    return gemm::finish_call(gemm::launch_lora_simt(p, in, stream, &name), name);
+    return gemm::finish_call(gemm::lora_tc_eligible(p) ? gemm::launch_lora_tc(p, in, stream, &name)
+                                                       : gemm::launch_lora_simt(p, in, stream, &name),
+                             name);
 }
 
 }  // namespace

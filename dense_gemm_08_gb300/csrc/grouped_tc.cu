@@ -33,14 +33,14 @@ namespace {
 
 using namespace tc;
 
-enum : int { kRows = 0, kWgrad = 1 };
+enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
 
 constexpr int kGroupM = 16;  // row tiles per band of the raster inside a group
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 32;
 constexpr int kThreads = 192;
 constexpr int kEpiWarps = 4;
-constexpr int kRingBytes = 7 * 32768;  // both variants
-constexpr int kSmemBytes = kRingBytes + 1024 + 512;
+constexpr int kRingBytes = 7 * 32768;  // all variants
+constexpr int kSmemBytes = kRingBytes + 1024 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
 struct Args {
@@ -52,10 +52,15 @@ struct Args {
     int num_kb;                 // rows: K blocks
     int b_kmajor;               // rows
     int bn;                     // columns per tile (of the CTA or the pair)
+    int am;                     // rows of D per CTA: 128, or 16 / 32 / 64 (single CTAs)
     int stages;
-    uint32_t stage_bytes;
+    uint32_t stage_bytes, a_region;  // B starts a_region bytes into a stage
     int ab_format;
     int z_step;  // rows: 0 when all groups share one B
+    int lb_z_step;  // lora: likewise for LB
+    int late_wait;  // lora: the kernel before this one wrote nothing but the plan
+    LoraPlan plan;  // lora (count null: no adapters)
+    LoraProblem l;  // lora: operands of the exact recomputation
     uint64_t timeout_ns;
 };
 
@@ -65,6 +70,7 @@ struct Tile {
     int64_t m0, n0;       // first row (rows: of all product rows; wgrad: of D_g) and column
     int m_valid;          // rows of D in the tile, 1 .. 128 CG
     int nkb;              // K blocks
+    int tile_m;           // its row of tiles
 };
 
 template <int CG, int MODE>
@@ -72,14 +78,22 @@ struct TileWalk {
     const Args &a;
     GroupWalk walk;
     __device__ __forceinline__ explicit TileWalk(const Args &a)
-        : a(a), walk(a.offsets, a.groups, a.rows, BM * CG, a.tiles_n) {}
+        : a(a), walk(a.offsets, a.groups, a.rows, a.am * CG, a.tiles_n) {}
 
     // Tile w; the whole warp calls.  False past the last tile.
     __device__ __forceinline__ bool get(uint32_t w, Tile &t) {
         uint32_t in_group, tiles_m;
+        const int tile_rows = MODE == kWgrad ? BM * CG : a.am * CG;
         if constexpr (MODE == kRows) {
             if (!walk.locate(w, t.g, t.first, t.last, in_group)) return false;
-            tiles_m = (static_cast<uint32_t>(t.last - t.first) + BM * CG - 1) / (BM * CG);
+            tiles_m = static_cast<uint32_t>((static_cast<int64_t>(t.last) - t.first + tile_rows - 1) / tile_rows);
+        } else if constexpr (MODE == kLora) {
+            if (w >= a.tiles_m * a.tiles_n) return false;
+            in_group = w;
+            t.g = 0;
+            t.first = 0;
+            t.last = static_cast<int32_t>(a.rows);
+            tiles_m = a.tiles_m;
         } else {
             const uint32_t per = a.tiles_m * a.tiles_n;
             const uint32_t g = w / per;
@@ -98,12 +112,13 @@ struct TileWalk {
         const uint32_t q = in_band / high;
         const int64_t tm = band * kGroupM + (in_band - q * high);
         t.n0 = static_cast<int64_t>(q) * a.bn;
-        const int64_t m_first = MODE == kRows ? t.first : 0;
-        const int64_t m_last = MODE == kRows ? t.last : a.M;
-        t.m0 = m_first + tm * (BM * CG);
-        t.m_valid = m_last - t.m0 < BM * CG ? static_cast<int>(m_last - t.m0) : BM * CG;
-        t.nkb = MODE == kRows ? a.num_kb
-                              : static_cast<int>((static_cast<int64_t>(t.last) - t.first + BK - 1) / BK);
+        const int64_t m_first = MODE == kWgrad ? 0 : t.first;
+        const int64_t m_last = MODE == kWgrad ? a.M : t.last;
+        t.m0 = m_first + tm * tile_rows;
+        t.m_valid = m_last - t.m0 < tile_rows ? static_cast<int>(m_last - t.m0) : tile_rows;
+        t.nkb = MODE == kWgrad ? static_cast<int>((static_cast<int64_t>(t.last) - t.first + BK - 1) / BK)
+                               : a.num_kb;
+        t.tile_m = static_cast<int>(tm);
         return true;
     }
 };
@@ -121,12 +136,42 @@ __device__ __forceinline__ uint32_t a_bytes(int n, bool gather) {
     return n > 64 ? BM * 128u : static_cast<uint32_t>((n + 15) / 16) * 2048u;
 }
 
+__device__ __forceinline__ float value_16(const void *p, int64_t at, int ab_format) {
+    const uint16_t b = static_cast<const uint16_t *>(p)[at];
+    return ab_format == 1 ? __uint_as_float(static_cast<uint32_t>(b) << 16)
+                          : __half2float(__ushort_as_half(b));
+}
+
+// lora: the sum of D(i, n) by its definition in FP32, from row i's own adapter
+// only (one column per lane; 0 past N).
+__device__ __noinline__ float lora_exact(const Args &a, int64_t i, int64_t n) {
+    const LoraProblem &l = a.l;
+    if (n >= l.N) return 0.f;
+    float s = 0.f;
+    for (int64_t k = 0; k < l.K; ++k)
+        s = fmaf(value_16(l.X, i * l.ldx + k, a.ab_format),
+                 value_16(l.W, l.w_kmajor ? n * l.ldw + k : k * l.ldw + n, a.ab_format), s);
+    const int slot = a.plan.slot[i];
+    if (slot < 0) return s;
+    const int64_t ad = l.adapter[i];
+    const uint16_t *v = a.plan.V + i * a.plan.ldv + static_cast<int64_t>(slot) * a.plan.rc;
+    float u = 0.f;
+    for (int64_t j = 0; j < l.rank; ++j) {
+        float x = value_16(v, j, a.ab_format);
+        if (a.plan.rc > a.plan.r_pad) x += value_16(v, a.plan.r_pad + j, a.ab_format);
+        u = fmaf(x, value_16(l.LB, ad * l.stride_b + (l.b_kmajor ? n * l.ld_b + j : j * l.ld_b + n),
+                             a.ab_format), u);
+    }
+    return s + u;
+}
+
 template <int CG, int MODE, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_a_part,
                       const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_b_part, const Args args) {
+                      const __grid_constant__ CUtensorMap map_b_part,
+                      const __grid_constant__ CUtensorMap map_v, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -161,8 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a_part))
                      : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
-        if (MODE == kWgrad)
+        if (MODE != kRows)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b_part))
+                         : "memory");
+        if (MODE == kLora)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v))
                          : "memory");
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(tmem_slot));
@@ -171,13 +219,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    pdl_wait();
+    // lora: the kernel before this one only makes the plan and V, and lets this
+    // one start once everything before it is complete; X and W are read at
+    // once, and each role waits for that kernel when it needs the plan
+    const bool late = MODE == kLora && args.late_wait;
+    if (!late) pdl_wait();
     pdl_launch_dependents();
 
     const uint32_t ring_base = smem_addr(ring);
     const int stages = args.stages;
     const uint32_t stage_bytes = args.stage_bytes;
-    constexpr uint32_t kABytes = BM * BK * 2;
+    const uint32_t a_region = args.a_region;
     const int b_rows = args.bn / CG;  // columns of B this CTA loads
     TileWalk<CG, MODE> tiles(args);
     Tile t;
@@ -192,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool reverse = false;
         for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
             const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
-            if constexpr (MODE == kRows) {
+            if constexpr (MODE != kWgrad) {
                 const int mine = cta_rows(t, rank);
                 const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
                 const uint32_t tx = a_bytes(cta_rows(t, 0), GATHER) +
@@ -219,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t fb_local = smem_addr(&full[stage]);
                     const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
-                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + kABytes;
+                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
                     if (lane == 0) {
                         if (leader) mbar_arrive_expect_tx(fb_local, tx);
                         if (args.b_kmajor) {
@@ -246,6 +298,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
+                    }
+                }
+                if (MODE == kLora && ok && args.plan.count != nullptr) {
+                    // the second product: V (128-byte rows of 64 columns) times
+                    // the slots' LB, fetched in 16-row slices of one adapter each
+                    if (late) pdl_wait();
+                    const LoraPlan &pl = args.plan;
+                    const int cols = pl.count[t.tile_m] * pl.rc;
+                    const int *list = pl.list + static_cast<int64_t>(t.tile_m) * pl.tile_rows;
+                    const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
+                    const uint32_t a0_bytes = static_cast<uint32_t>((cta_rows(t, 0) + 15) / 16) * 2048u;
+                    const uint32_t a1_bytes =
+                        CG == 2 ? static_cast<uint32_t>((cta_rows(t, 1) + 15) / 16) * 2048u : 0u;
+                    for (int c0 = 0; c0 < cols; c0 += BK) {
+                        if (lane == 0)
+                            ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
+                                              args.timeout_ns);
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) {
+                            if (lane == 0) raise_abort(abort_flag);
+                            break;
+                        }
+                        const uint32_t fb_local = smem_addr(&full[stage]);
+                        const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
+                        const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
+                        const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                        if (lane == 0) {
+                            if (leader)
+                                mbar_arrive_expect_tx(fb_local, a0_bytes + a1_bytes + CG * slices * slice_bytes);
+                            for (int j = 0; j < mine; j += 16)
+                                tma_load_2d<CG>(sa + j * 128, &map_v, c0, m0 + j, fb);
+                            for (int q = 0; q < slices; ++q) {
+                                const int c = c0 + q * 16, s = c / pl.rc;
+                                const int32_t ad = list[s] * args.lb_z_step;
+                                const int32_t j0 = (c - s * pl.rc) % pl.r_pad;
+                                const uint32_t dst = sb + q * slice_bytes;
+                                if (args.l.b_kmajor) {
+                                    tma_load_3d<CG>(dst, &map_b_part, j0, b0, ad, fb);
+                                } else {
+                                    for (int j = 0; j < b_rows; j += 64)
+                                        tma_load_3d<CG>(dst + j * 32, &map_b_part, b0 + j, j0, ad, fb);
+                                }
+                            }
+                        }
+                        ++issued;
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
             } else {
@@ -283,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t fb_local = smem_addr(&full[stage]);
                     const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
-                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + kABytes;
+                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
                     if (lane == 0) {
                         if (leader)
                             mbar_arrive_expect_tx(
@@ -342,10 +443,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
             const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
             const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring_base, 0) : desc_kmajor(ring_base, 0);
-            const uint64_t b_desc0 = b_mn ? desc_mnmajor(ring_base + kABytes, 0)
-                                          : desc_kmajor(ring_base + kABytes, 0);
+            const uint64_t b_desc0 = b_mn ? desc_mnmajor(ring_base + a_region, 0)
+                                          : desc_kmajor(ring_base + a_region, 0);
             const uint64_t a_step = a_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
             const uint64_t b_step = b_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+            // lora: slices of LB -- K-major: 32-byte rows (32-byte swizzle);
+            // N-major: 16 rows per 64-column block (128-byte swizzle)
+            const bool lb_mn = MODE == kLora && !args.l.b_kmajor;
+            const uint32_t lb_idesc = make_idesc(BM * CG, args.bn, 0, lb_mn, args.ab_format);
+            const uint64_t lb_desc0 = lb_mn ? smem_desc(ring_base + a_region, 16 * 128, 1024)
+                                            : smem_desc(ring_base + a_region, 16, 256, kSwizzle32);
             const uint32_t full0 = smem_addr(&full[0]), empty0 = smem_addr(&empty[0]);
             int stage = 0;
             uint32_t phase = 0;
@@ -371,11 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t ad = a_desc0 + static_cast<uint64_t>(s) * (stage_bytes >> 4);
                         const uint64_t bd = b_desc0 + static_cast<uint64_t>(s) * (stage_bytes >> 4);
                         tc_mma<CG>(d_tmem, ad, bd, idesc, add);
-                        if (MODE == kRows || slices > 1)
+                        if (MODE != kWgrad || slices > 1)
                             tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
-                        if (MODE == kRows || slices > 2)
+                        if (MODE != kWgrad || slices > 2)
                             tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
-                        if (MODE == kRows || slices > 3)
+                        if (MODE != kWgrad || slices > 3)
                             tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
                     };
                     for (int i = 0; ok && i < t.nkb; i += 2) {
@@ -400,6 +507,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                             phase = p1;
                         }
                     }
+                    if (MODE == kLora && ok && args.plan.count != nullptr) {
+                        if (late) pdl_wait();
+                        const int cols = args.plan.count[t.tile_m] * args.plan.rc;
+                        const uint32_t slice_step = static_cast<uint32_t>(b_rows) * 32u >> 4;
+                        for (int c0 = 0; c0 < cols; c0 += BK) {
+                            if (!wait_full(stage, phase)) {
+                                ok = 0;
+                                break;
+                            }
+                            tc_fence_after();
+                            const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                            const uint64_t at = static_cast<uint64_t>(stage) * (stage_bytes >> 4);
+                            for (int q = 0; q < slices; ++q)
+                                tc_mma<CG>(d_tmem, a_desc0 + at + q * a_step,
+                                           lb_desc0 + at + q * slice_step, lb_idesc, 1u);
+                            tc_commit<CG>(empty0 + 8u * static_cast<uint32_t>(stage));
+                            if (++stage == stages) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                    }
                     if (ok)
                         tc_commit<CG>(smem_addr(&tfull[buf]));
                     else
@@ -422,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp % 4;  // TMEM lanes this warp may access
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t acc = 0;
+        if (late) pdl_wait();
         for (uint32_t w = first_tile; tiles.get(w, t); w += tile_step) {
             const bool empty_sum = MODE == kWgrad && t.nkb == 0;
             const int buf = static_cast<int>(acc & 1);
@@ -457,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ncols = rest < args.bn ? static_cast<int>(rest) : args.bn;
             const int n_chunks = nrows > 0 ? (ncols + 31) / 32 : 0;
             OutArgs o = args.out;
-            if constexpr (MODE == kRows) {
+            if constexpr (MODE != kWgrad) {
                 if (o.bias != nullptr) o.bias += t.g * args.N;
             } else {
                 o.D = static_cast<uint8_t *>(o.D) + t.g * args.stride_d * (o.out == kOutF32 ? 4 : 2);
@@ -487,6 +617,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     tmem_load_32cols(t_acc + chunk * 32, raw);
                     if (chunk == n_chunks - 1) release_acc();
+                    if constexpr (MODE == kLora) {
+                        // A slot's LB meets zeros of V in the rows of other
+                        // adapters; where it holds infinities or NaNs those
+                        // products are NaN.  Sums that are not finite are
+                        // computed again from the row's own adapter alone.
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const uint32_t b = raw[j] & 0x7fffffffu;
+                            top = b > top ? b : top;
+                        }
+                        const bool redo = args.plan.count != nullptr && lane < nrows && top >= 0x7f800000u;
+                        if (__any_sync(0xffffffffu, redo)) {
+#pragma unroll 1
+                            for (int l = 0; l < nrows; ++l) {
+                                if (!__shfl_sync(0xffffffffu, redo ? 1 : 0, l)) continue;
+                                const float mine = lora_exact(args, row0 + l, t.n0 + chunk * 32 + lane);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const float x = __shfl_sync(0xffffffffu, mine, j);
+                                    if (lane == l && (raw[j] & 0x7fffffffu) >= 0x7f800000u)
+                                        raw[j] = __float_as_uint(x);
+                                }
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
                 }
@@ -557,7 +713,8 @@ DeviceInfo *device_info() {
         for (cudaError_t e : {allow_smem<1, kRows, false>(), allow_smem<1, kRows, true>(),
                               allow_smem<2, kRows, false>(), allow_smem<2, kRows, true>(),
                               allow_smem<1, kWgrad, false>(), allow_smem<1, kWgrad, true>(),
-                              allow_smem<2, kWgrad, false>(), allow_smem<2, kWgrad, true>()})
+                              allow_smem<2, kWgrad, false>(), allow_smem<2, kWgrad, true>(),
+                              allow_smem<1, kLora, false>(), allow_smem<2, kLora, false>()})
             if (d->err == cudaSuccess) d->err = e;
         if (d->err != cudaSuccess) return;
         cudaLaunchAttribute attr[2];
@@ -574,28 +731,37 @@ DeviceInfo *device_info() {
 }
 
 template <int CG, int MODE>
-cudaError_t launch(const CUtensorMap (&maps)[4], const Args &a, bool gather, int64_t max_tiles,
+cudaError_t launch(const CUtensorMap (&maps)[5], const Args &a, bool gather, int64_t max_tiles,
                    const DeviceInfo *d, cudaStream_t stream) {
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
     cudaLaunchAttribute attr[2];
-    if (gather) {
-        cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
-        return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
-                                  maps[2], maps[3], a);
+    if constexpr (MODE != kLora) {
+        if (gather) {
+            cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
+            return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
+                                      maps[2], maps[3], maps[4], a);
+        }
     }
     cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, stream, attr);
     return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, false>, maps[0], maps[1], maps[2],
-                              maps[3], a);
+                              maps[3], maps[4], a);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile width of the single-CTA variant and the ring to match.
-void set_width(Args &a, int cg, int bn) {
+// Tile of am rows per CTA and bn columns, and the ring to match: stages of am
+// rows of A and the CTA's rows of B, as many as fit.  With am < 128 the MMA's
+// 128-row A operand runs on into B and the next stages: stale rows, which
+// reach only accumulator rows that are not stored.  The last stage keeps 128
+// rows inside the ring.
+void set_tile(Args &a, int cg, int am, int bn) {
+    a.am = am;
     a.bn = bn;
-    a.stage_bytes = BM * BK * 2 + static_cast<uint32_t>(bn / cg) * BK * 2;
-    const int fit = static_cast<int>(kRingBytes / a.stage_bytes);
+    a.a_region = static_cast<uint32_t>(am) * BK * 2;
+    a.stage_bytes = a.a_region + static_cast<uint32_t>(bn / cg) * BK * 2;
+    const int over = BM * BK * 2 - static_cast<int>(a.stage_bytes);
+    const int fit = (kRingBytes - (over > 0 ? over : 0)) / static_cast<int>(a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 }
 
@@ -606,7 +772,7 @@ constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bi
 bool grouped_tc_eligible(const GroupedProblem &p) {
     return p.K > 0 && p.rows_a > 0 && tma_rows(p.A, p.lda) &&
            tma_rows(p.B, p.ldb, p.groups > 1 ? p.stride_b : 0) &&
-           (ceil_div(p.rows, BM) + (p.groups < p.rows ? p.groups : p.rows)) * ceil_div(p.N, 64) <
+           (ceil_div(p.rows, 16) + (p.groups < p.rows ? p.groups : p.rows)) * ceil_div(p.N, 64) <
                kMaxTiles;
 }
 
@@ -640,17 +806,19 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
     const int64_t pair_tiles = live * ceil_div(ceil_div(p.rows, live), 2 * BM) * ceil_div(p.N, 256);
     const bool pair = d->pairs > 0 && p.rows / live > BM && pair_tiles >= d->pairs;
     if (pair) {
-        set_width(a, 2, 256);
+        set_tile(a, 2, BM, 256);
     } else {
-        const int64_t row_tiles = live * ceil_div(ceil_div(p.rows, live), BM);
+        const int64_t mean = ceil_div(p.rows, live);
+        const int am = mean <= 8 ? 32 : (mean <= 24 ? 64 : BM);
+        const int64_t row_tiles = live * ceil_div(mean, am);
         int bn = 256;
         while (bn > 64 && row_tiles * ceil_div(p.N, bn) < 4 * d->sms) bn /= 2;
-        set_width(a, 1, bn);
+        set_tile(a, 1, am, bn);
     }
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
     const int cg = pair ? 2 : 1;
     const bool gather = p.row_index != nullptr;
-    CUtensorMap maps[4];
+    CUtensorMap maps[5];
     bool ok = encode_stack(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, BM, 2) &&
               encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, gather ? 1 : 16, 2);
     const int64_t count = one_b ? 1 : p.groups, stride = one_b ? p.ldb : p.stride_b;
@@ -660,8 +828,8 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
     else
         ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64, BK, 3);
     if (!ok) return cudaErrorInvalidValue;
-    maps[3] = maps[2];
-    const int64_t max_tiles = (p.rows / (BM * cg) + live) * a.tiles_n;
+    maps[3] = maps[4] = maps[2];
+    const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
     static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
                                              {"grouped_tc<bf16>", "grouped_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];
@@ -708,15 +876,15 @@ cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t strea
     const bool pair = d->pairs > 0 && p.M > BM && pair_tiles >= d->pairs;
     const int cg = pair ? 2 : 1;
     if (pair) {
-        set_width(a, 2, 256);
+        set_tile(a, 2, BM, 256);
     } else {
         int bn = 256;
         while (bn > 64 && p.groups * ceil_div(p.M, BM) * ceil_div(p.N, bn) < 2 * d->sms) bn /= 2;
-        set_width(a, 1, bn);
+        set_tile(a, 1, BM, bn);
     }
     a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, BM * cg));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
-    CUtensorMap maps[4];
+    CUtensorMap maps[5];
     const bool gather = p.row_index != nullptr;
     const bool ok =
         encode_stack(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2) &&
@@ -724,12 +892,149 @@ cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t strea
         encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2) &&
         encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
     if (!ok) return cudaErrorInvalidValue;
+    maps[4] = maps[3];
     const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
     static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
                                              {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];
     return pair ? launch<2, kWgrad>(maps, a, gather, max_tiles, d, stream)
                 : launch<1, kWgrad>(maps, a, gather, max_tiles, d, stream);
+}
+
+bool lora_tc_eligible(const LoraProblem &p) {
+    if (p.K == 0 || !tma_rows(p.X, p.ldx) || !tma_rows(p.W, p.ldw) ||
+        ceil_div(p.M, 16) * ceil_div(p.N, 32) >= kMaxTiles)
+        return false;
+    return p.adapters == 0 ||
+           (lora_shrink_eligible(p) && tma_rows(p.LB, p.ld_b, p.adapters > 1 ? p.stride_b : 0));
+}
+
+cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
+                           const char **name) {
+    const bool bf16 = in == InType::BF16;
+    DeviceInfo *d = device_info();
+    if (d == nullptr) return cudaErrorInvalidDevice;
+    if (d->err != cudaSuccess) return d->err;
+    Args a = {};
+    a.groups = 1;
+    a.N = p.N;
+    a.out.ldd = p.ldd;
+    a.out.bias = p.bias;
+    a.out.alpha = 1.f;
+    a.out.act = p.act;
+    a.out.out = p.out;
+    const int64_t elt = p.out == kOutF32 ? 4 : 2;
+    a.out.row_vec = row_alignment(p.D, p.ldd, 0, elt);
+    a.num_kb = static_cast<int>(ceil_div(p.K, BK));
+    a.b_kmajor = p.w_kmajor ? 1 : 0;
+    a.ab_format = bf16 ? 1 : 0;
+    // 1 s per wait, longer where recomputing a tile's sums one by one could
+    // take as long
+    a.timeout_ns = 1000ull * 1000ull * 1000ull * static_cast<uint64_t>(1 + p.K / 65536);
+    const int64_t pair_tiles = ceil_div(p.M, 2 * BM) * ceil_div(p.N, 256);
+    const bool pair = d->pairs > 0 && p.M > BM && pair_tiles >= d->pairs;
+    const int cg = pair ? 2 : 1;
+    if (pair) {
+        set_tile(a, 2, BM, 256);
+    } else {
+        const int am = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : (p.M <= 64 ? 64 : BM));
+        // the narrowest tiles that still fill the SMs once (all K-major: in
+        // steps of 32 columns; an N-major operand comes in blocks of 64)
+        const int step = p.w_kmajor && (p.adapters == 0 || p.b_kmajor) ? 32 : 64;
+        const int64_t per_row = d->sms / ceil_div(p.M, am) > 0 ? d->sms / ceil_div(p.M, am) : 1;
+        int64_t bn = ceil_div(ceil_div(p.N, per_row), step) * step;
+        if (bn > 256) bn = 256;
+        set_tile(a, 1, am, static_cast<int>(bn));
+    }
+    a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
+    static const char *const kNames[2][2] = {{"lora_tc<f16>", "lora_tc<f16,pair>"},
+                                             {"lora_tc<bf16>", "lora_tc<bf16,pair>"}};
+    *name = kNames[bf16][pair];
+
+    LoraPlan plan = {};
+    plan.tile_rows = a.am * cg;
+    int64_t chunk = p.M;  // rows per launch
+    void *ws = nullptr;
+    size_t v_bytes = 0, count_bytes = 0, list_bytes = 0;
+    if (p.adapters > 0) {
+        plan.r_pad = 16;
+        while (plan.r_pad < p.rank) plan.r_pad *= 2;
+        // a 16-bit D is rounded to the inputs' type itself: one rounding of
+        // the first product is of the same size; an FP32 D takes two parts
+        plan.rc = p.out == kOutF32 ? 2 * plan.r_pad : plan.r_pad;
+        const int64_t slots = p.adapters < plan.tile_rows ? p.adapters : plan.tile_rows;
+        plan.ldv = ceil_div(slots * plan.rc, BK) * BK;
+        // V is at most 128 MiB: more rows go in several launches
+        const int64_t fit = (int64_t(128) << 20) / (plan.ldv * 2) / plan.tile_rows * plan.tile_rows;
+        const int64_t most = fit > plan.tile_rows ? fit : plan.tile_rows;
+        if (chunk > most) chunk = most;
+        const int64_t tiles = ceil_div(chunk, plan.tile_rows);
+        v_bytes = static_cast<size_t>(tiles * plan.tile_rows * plan.ldv * 2);
+        count_bytes = static_cast<size_t>(ceil_div(tiles * 4, 256) * 256);
+        list_bytes = static_cast<size_t>(tiles * plan.tile_rows * 4);
+        cudaError_t e = workspace_alloc(v_bytes + count_bytes + 2 * list_bytes, stream, &ws);
+        if (e != cudaSuccess) return e;
+        uint8_t *at = static_cast<uint8_t *>(ws);
+        plan.V = reinterpret_cast<uint16_t *>(at);
+        plan.count = reinterpret_cast<int *>(at + v_bytes);
+        plan.list = reinterpret_cast<int *>(at + v_bytes + count_bytes);
+        plan.slot = reinterpret_cast<int *>(at + v_bytes + count_bytes + list_bytes);
+    }
+    cudaError_t e = cudaSuccess;
+    for (int64_t row = 0; row < p.M && e == cudaSuccess; row += chunk) {
+        const int64_t rows = p.M - row < chunk ? p.M - row : chunk;
+        LoraProblem l = p;
+        l.M = rows;
+        l.X = static_cast<const uint16_t *>(p.X) + row * p.ldx;
+        l.adapter = p.adapters > 0 ? p.adapter + row : nullptr;
+        a.rows = rows;
+        a.tiles_m = static_cast<uint32_t>(ceil_div(rows, plan.tile_rows));
+        a.out.D = static_cast<uint8_t *>(p.D) + row * p.ldd * elt;
+        a.l = l;
+        a.plan = plan;
+        if (p.adapters > 0) {
+            e = launch_lora_shrink(l, plan, in, stream);
+            if (e != cudaSuccess) break;
+            a.late_wait = 1;
+        }
+        CUtensorMap maps[5];
+        bool ok = encode_stack(&maps[0], bf16, l.X, p.K, rows, p.ldx, 1, 0, BK, BM, 2) &&
+                  encode_stack(&maps[1], bf16, l.X, p.K, rows, p.ldx, 1, 0, BK, 16, 2);
+        if (p.w_kmajor)
+            ok = ok && encode_stack(&maps[2], bf16, p.W, p.K, p.N, p.ldw, 1, p.ldw, BK,
+                                    static_cast<uint32_t>(a.bn / cg), 3);
+        else
+            ok = ok && encode_stack(&maps[2], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw, 64, BK, 3);
+        maps[3] = maps[4] = maps[2];
+        if (p.adapters > 0) {
+            const bool one_lb = p.adapters == 1 || p.stride_b == 0;
+            const int64_t stride = one_lb ? p.ld_b : p.stride_b;
+            const int64_t count = one_lb ? 1 : p.adapters;
+            a.lb_z_step = one_lb ? 0 : 1;
+            if (p.b_kmajor)
+                ok = ok && encode_stack(&maps[3], bf16, p.LB, p.rank, p.N, p.ld_b, count, stride,
+                                        16, static_cast<uint32_t>(a.bn / cg), 3,
+                                        CU_TENSOR_MAP_SWIZZLE_32B);
+            else
+                ok = ok && encode_stack(&maps[3], bf16, p.LB, p.N, p.rank, p.ld_b, count, stride,
+                                        64, 16, 3);
+            ok = ok && encode_stack(&maps[4], bf16, plan.V, plan.ldv,
+                                    static_cast<int64_t>(a.tiles_m) * plan.tile_rows, plan.ldv, 1,
+                                    0, BK, 16, 2);
+        }
+        if (!ok) {
+            e = cudaErrorInvalidValue;
+            break;
+        }
+        const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+        e = pair ? launch<2, kLora>(maps, a, false, tiles, d, stream)
+                 : launch<1, kLora>(maps, a, false, tiles, d, stream);
+    }
+    if (ws != nullptr) {
+        const cudaError_t ef = workspace_free(ws, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e;
 }
 
 cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status) {

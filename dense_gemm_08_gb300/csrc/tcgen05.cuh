@@ -273,13 +273,16 @@ __device__ __forceinline__ void tmem_load_32cols(uint32_t taddr, uint32_t (&v)[3
 //   [32,46) stride-dimension byte offset >> 4
 //   [46,48) version = 1               [49,52) base offset (0: atoms 1024-aligned)
 //   [52]    LBO mode = 0              [61,64) swizzle: 2 = 128-byte swizzle
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+//   (4 = 64-byte, 6 = 32-byte; atoms then 512- / 256-aligned)
+enum : uint32_t { kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6 };
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo,
+                                              uint32_t swizzle = kSwizzle128) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
     d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16;
     d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32;
     d |= 1ull << 46;
-    d |= 2ull << 61;
+    d |= static_cast<uint64_t>(swizzle) << 61;
     return d;
 }
 
