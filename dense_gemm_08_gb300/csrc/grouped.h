@@ -106,10 +106,12 @@ struct LoraPlan {
     int *count;  // [tiles] slots in use
     int *list;   // [tiles][tile_rows] the slots' adapters
     int *slot;   // [rows] each row's slot, -1: no adapter
+    float *part;  // lora_shrink_part_bytes of scratch
 };
 cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InType in,
                                cudaStream_t stream);
 bool lora_shrink_eligible(const LoraProblem &p);
+size_t lora_shrink_part_bytes(int64_t rows, int r_pad);
 cudaError_t lora_shrink_read_and_clear_status(cudaStream_t stream, int *status);
 
 // Reads and clears those kernels' device status word (after a sync).

@@ -36,12 +36,23 @@ using namespace tc;
 enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
 
 constexpr int kGroupM = 16;  // row tiles per band of the raster inside a group
-constexpr int kMaxStages = 32;
-constexpr int kThreads = 192;
+constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 4;
+constexpr int kGatherWarps = 2;
 constexpr int kRingBytes = 7 * 32768;  // all variants
-constexpr int kSmemBytes = kRingBytes + 1024 + 1024;
+constexpr int kMaxSlots = 256;         // lora: adapters of a tile
+// ring + alignment + barriers + row numbers (gathers) or adapters (lora)
+constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kMaxSlots * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+
+// Gathers are issued by warps of their own: a TMA gather takes its row numbers
+// from uniform registers, and one thread needs about 40 ns to issue it, so the
+// 32 gathers of a 16 KiB stage would keep a single warp busy for four times as
+// long as the MMAs of the stage (4096 x 14336, 16384 rows: 4.2 ms).
+template <int MODE, bool GATHER>
+constexpr int threads() {
+    return 64 + 32 * kEpiWarps + (GATHER || MODE == kWgrad ? 32 * kGatherWarps : 0);
+}
 
 struct Args {
     int64_t groups, rows, M, N;  // M: wgrad only
@@ -166,7 +177,7 @@ __device__ __noinline__ float lora_exact(const Args &a, int64_t i, int64_t n) {
 }
 
 template <int CG, int MODE, bool GATHER>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_a_part,
                       const __grid_constant__ CUtensorMap map_b,
@@ -180,9 +191,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *empty = bars + kMaxStages;  // [kMaxStages] MMA -> TMA
     uint64_t *tfull = empty + kMaxStages;  // [2] MMA -> epilogue
     uint64_t *tempty = tfull + 2;          // [2] epilogue -> MMA (the leader counts both CTAs)
-    uint64_t *drain = tempty + 2;
+    uint64_t *go = tempty + 2;  // [kGatherWarps][kMaxStages] producer -> gather warp: stage is free
+    uint64_t *drain = go + kGatherWarps * kMaxStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *numbers = reinterpret_cast<int *>(ring + kRingBytes + 1024);  // [kMaxSlots]
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
@@ -194,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&full[s]), 1);
             mbar_init(smem_addr(&empty[s]), 1);
         }
+        for (int s = 0; s < kGatherWarps * kMaxStages; ++s) mbar_init(smem_addr(&go[s]), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&tfull[b]), 1);
             mbar_init(smem_addr(&tempty[b]), kEpiWarps * CG);
@@ -251,16 +265,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     (CG == 2 ? a_bytes(cta_rows(t, 1), GATHER) : 0u) +
                                     CG * b_rows * 128u;
                 const int32_t z = t.g * args.z_step;
-                int32_t rows4[4];
-                if constexpr (GATHER) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        rows4[i] = lane * 4 + i < mine ? __ldg(args.row_index + m0 + lane * 4 + i) : -1;
-                }
+                // every other tile walks K backwards: it starts on the blocks
+                // of B the tile before it read last.  Single CTAs also start
+                // at different blocks: columns of B are a power of two apart
+                // as a rule, and CTAs in step would read the same few DRAM
+                // channels, and the same lines of A, at once.
+                int kb = CG == 1 ? static_cast<int>((w * 5u) % static_cast<uint32_t>(t.nkb))
+                                 : (reverse ? t.nkb - 1 : 0);
                 for (int i = 0; i < t.nkb; ++i) {
-                    // every other tile walks K backwards: it starts on the
-                    // blocks of B the tile before it read last
-                    const int32_t k0 = (reverse ? t.nkb - 1 - i : i) * BK;
+                    const int32_t k0 = kb * BK;
+                    kb = CG == 2 && reverse ? kb - 1 : (kb + 1 == t.nkb ? 0 : kb + 1);
                     if (lane == 0)
                         ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
                                           args.timeout_ns);
@@ -274,6 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
                     if (lane == 0) {
                         if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                        if constexpr (GATHER) {
+                            for (int h = 0; h < kGatherWarps; ++h)
+                                if (mine > h * 64) mbar_arrive(smem_addr(&go[h * kMaxStages + stage]));
+                        }
                         if (args.b_kmajor) {
                             tma_load_3d<CG>(sb, &map_b, k0, b0, z, fb);
                         } else {
@@ -289,11 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    if constexpr (GATHER) {
-                        if (lane * 4 < mine)
-                            tma_gather4<CG>(sa + lane * 512, &map_a_part, k0, rows4[0], rows4[1],
-                                            rows4[2], rows4[3], fb);
-                    }
                     ++issued;
                     if (++stage == stages) {
                         stage = 0;
@@ -307,6 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const LoraPlan &pl = args.plan;
                     const int cols = pl.count[t.tile_m] * pl.rc;
                     const int *list = pl.list + static_cast<int64_t>(t.tile_m) * pl.tile_rows;
+                    __syncwarp();
+                    for (int i = lane; i < cols / pl.rc; i += 32) numbers[i] = list[i] * args.lb_z_step;
+                    __syncwarp();
                     const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
                     const uint32_t a0_bytes = static_cast<uint32_t>((cta_rows(t, 0) + 15) / 16) * 2048u;
                     const uint32_t a1_bytes =
@@ -331,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tma_load_2d<CG>(sa + j * 128, &map_v, c0, m0 + j, fb);
                             for (int q = 0; q < slices; ++q) {
                                 const int c = c0 + q * 16, s = c / pl.rc;
-                                const int32_t ad = list[s] * args.lb_z_step;
+                                const int32_t ad = numbers[s];
                                 const int32_t j0 = (c - s * pl.rc) % pl.r_pad;
                                 const uint32_t dst = sb + q * slice_bytes;
                                 if (args.l.b_kmajor) {
@@ -352,28 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const int32_t a0 = static_cast<int32_t>(t.m0 + rank * BM);
                 const int b_blocks = b_rows / 64;
-                // gathered blocks: lane -> quad of rows (lane % 16) of 64-column
-                // blocks lane / 16, lane / 16 + 2, ...
-                const int quad = lane % 16;
-                int32_t next[4] = {-1, -1, -1, -1};
-                auto fetch = [&](int kb) {  // numbers of this lane's rows of A in block kb
-                    const int64_t r0 = static_cast<int64_t>(t.first) + kb * BK + quad * 4;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        next[i] = -1;
-                        if (r0 + i < t.last)
-                            next[i] = GATHER ? __ldg(args.row_index + r0 + i)
-                                             : static_cast<int32_t>(r0 + i);
-                    }
-                };
-                if (t.nkb > 0) fetch(0);
                 for (int i = 0; i < t.nkb; ++i) {
                     const int32_t r0 = t.first + i * BK;
                     const int rem = t.last - r0 < BK ? t.last - r0 : BK;
                     const int quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
                     const bool part = rem < BK;
-                    int32_t mine[4] = {next[0], next[1], next[2], next[3]};
-                    if (i + 1 < t.nkb) fetch(i + 1);
                     if (lane == 0)
                         ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
                                           args.timeout_ns);
@@ -389,6 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (leader)
                             mbar_arrive_expect_tx(
                                 fb_local, CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
+                        if (GATHER || part) {
+                            for (int h = 0; h < kGatherWarps; ++h)
+                                mbar_arrive(smem_addr(&go[h * kMaxStages + stage]));
+                        }
                         if (!part) {
                             if constexpr (!GATHER) {
                                 tma_load_2d<CG>(sa, &map_a, a0, r0, fb);
@@ -396,20 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             for (int j = 0; j < b_blocks; ++j)
                                 tma_load_2d<CG>(sb + j * 8192, &map_b, b0 + 64 * j, r0, fb);
-                        }
-                    }
-                    if (quad < quads) {
-                        if (GATHER || part)
-                            tma_gather4<CG>(sa + (lane / 16) * 8192 + quad * 512, &map_a_part,
-                                            a0 + (lane / 16) * 64, mine[0], mine[1], mine[2],
-                                            mine[3], fb);
-                        if (part) {
-                            const int32_t q0 = r0 + quad * 4;
-                            for (int j = lane / 16; j < b_blocks; j += 2)
-                                tma_gather4<CG>(sb + j * 8192 + quad * 512, &map_b_part, b0 + 64 * j,
-                                                q0 < t.last ? q0 : -1, q0 + 1 < t.last ? q0 + 1 : -1,
-                                                q0 + 2 < t.last ? q0 + 2 : -1,
-                                                q0 + 3 < t.last ? q0 + 3 : -1, fb);
                         }
                     }
                     ++issued;
@@ -544,6 +533,102 @@ __global__ void __launch_bounds__(kThreads, 1)
                     raise_abort(abort_flag);
             }
             aborted = !ok;
+        }
+        __syncwarp();
+    } else if (warp >= 2 + kEpiWarps) {
+        // ------------------------------------------------- gather warps 6-7
+        // They follow the producer's stages and issue the parts of a stage
+        // that come by row number: one thread each, the numbers in shared
+        // memory.  The producer, which has waited for the stage and counted
+        // their bytes in its expect_tx, tells each warp through its own
+        // barrier of that stage; it cannot tell it again before the bytes have
+        // arrived, so one parity bit per stage is enough.
+        const int half = warp - (2 + kEpiWarps);
+        int *const mine = numbers + half * 64;  // 64 row numbers of this warp
+        int stage = 0;
+        uint32_t told = 0;  // parity of the next word on each stage
+        int ok = 1;
+        // rows quads * 4 of `mine`, 64 columns from c0 on, to dst
+        auto gather = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, int quads, uint32_t fb) {
+#pragma unroll 4
+            for (int q = 0; q < quads; ++q) {
+                const int4 r = *reinterpret_cast<const int4 *>(mine + q * 4);
+                tma_gather4<CG>(dst + q * 512, map, c0, r.x, r.y, r.z, r.w, fb);
+            }
+        };
+        bool reverse = false;
+        for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
+            const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+            const int b_blocks = b_rows / 64;
+            const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
+            int quads = 0;  // rows mode: this warp's quads of the tile
+            int kb = 0;
+            if constexpr (MODE != kWgrad) {
+                const int rows = cta_rows(t, rank) - half * 64;
+                quads = rows <= 0 ? 0 : (rows >= 64 ? 16 : (rows + 3) / 4);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = lane + i * 32;
+                    mine[r] = r < rows ? __ldg(args.row_index + m0 + half * 64 + r) : -1;
+                }
+                __syncwarp();
+                kb = CG == 1 ? static_cast<int>((w * 5u) % static_cast<uint32_t>(t.nkb))
+                             : (reverse ? t.nkb - 1 : 0);
+            }
+            for (int i = 0; i < t.nkb; ++i) {
+                const uint32_t fb_local = smem_addr(&full[stage]);
+                const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
+                const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
+                bool work = true, part = false;
+                if constexpr (MODE == kWgrad) {
+                    const int32_t r0 = t.first + i * BK;
+                    const int rem = t.last - r0 < BK ? t.last - r0 : BK;
+                    part = rem < BK;
+                    quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
+                    work = GATHER || part;
+                    if (work) {
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = lane + j * 32;
+                            mine[r] = r >= rem ? -1
+                                      : GATHER ? __ldg(args.row_index + r0 + r)
+                                               : static_cast<int>(r0 + r);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (work && quads > 0 && lane == 0) {
+                    ok = wait_bounded(smem_addr(&go[half * kMaxStages + stage]), (told >> stage) & 1u,
+                                      abort_flag, args.timeout_ns);
+                    told ^= 1u << stage;
+                    if (ok) {
+                        if constexpr (MODE == kWgrad) {
+                            gather(sa + half * 8192, &map_a_part, m0 + half * 64, quads, fb);
+                            if (part) {
+                                // B's rows go by their own numbers
+                                if constexpr (GATHER) {
+                                    const int32_t r0 = t.first + i * BK;
+                                    for (int r = 0; r < quads * 4; ++r)
+                                        mine[r] = r0 + r < t.last ? r0 + r : -1;
+                                }
+                                for (int j = half; j < b_blocks; j += kGatherWarps)
+                                    gather(sb + j * 8192, &map_b_part, b0 + 64 * j, quads, fb);
+                            }
+                        } else {
+                            gather(sa + half * 64 * 128, &map_a_part, kb * BK, quads, fb);
+                        }
+                    } else {
+                        raise_abort(abort_flag);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if constexpr (MODE != kWgrad)
+                    kb = CG == 2 && reverse ? kb - 1 : (kb + 1 == t.nkb ? 0 : kb + 1);
+                if (++stage == stages) stage = 0;
+            }
         }
         __syncwarp();
     } else {
@@ -682,7 +767,7 @@ template <int CG, int MODE, bool GATHER>
 cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(threads<MODE, GATHER>(), 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -972,13 +1057,17 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         v_bytes = static_cast<size_t>(tiles * plan.tile_rows * plan.ldv * 2);
         count_bytes = static_cast<size_t>(ceil_div(tiles * 4, 256) * 256);
         list_bytes = static_cast<size_t>(tiles * plan.tile_rows * 4);
-        cudaError_t e = workspace_alloc(v_bytes + count_bytes + 2 * list_bytes, stream, &ws);
+        list_bytes = static_cast<size_t>(ceil_div(static_cast<int64_t>(list_bytes), 256) * 256);
+        const size_t part_bytes = lora_shrink_part_bytes(chunk, plan.r_pad);
+        cudaError_t e =
+            workspace_alloc(v_bytes + count_bytes + 2 * list_bytes + part_bytes, stream, &ws);
         if (e != cudaSuccess) return e;
         uint8_t *at = static_cast<uint8_t *>(ws);
         plan.V = reinterpret_cast<uint16_t *>(at);
         plan.count = reinterpret_cast<int *>(at + v_bytes);
         plan.list = reinterpret_cast<int *>(at + v_bytes + count_bytes);
         plan.slot = reinterpret_cast<int *>(at + v_bytes + count_bytes + list_bytes);
+        plan.part = reinterpret_cast<float *>(at + v_bytes + count_bytes + 2 * list_bytes);
     }
     cudaError_t e = cudaSuccess;
     for (int64_t row = 0; row < p.M && e == cudaSuccess; row += chunk) {

@@ -6,13 +6,17 @@
 // tile's distinct adapters itself (tile_rows comparisons per row, in shared
 // memory), in order of first appearance, so nothing is sorted and one launch
 // makes both the plan and V.
-//   few rows:  one CTA per row on the CUDA cores; its warps share the columns
-//              (K-major LA) or K (rank-major LA).  Each adapter's LA is read
-//              once per row that uses it, which for a decode step is about
-//              once at all.
-//   more rows: one CTA per 128 rows on the tensor cores; X times the adapters
+//   few rows:  a cluster of up to 8 CTAs per row on the CUDA cores, K split
+//              over them; a CTA's warps share the columns (K-major LA) or K
+//              (rank-major LA), and the CTAs' sums meet in distributed shared
+//              memory.  Each adapter's LA is read once per row that uses it,
+//              which for a decode step is about once at all.
+//   more rows: 128 rows at a time on the tensor cores; X times the adapters
 //              of those rows, side by side in TMEM, up to 256 columns at a
-//              time; each row keeps its own adapter's columns.
+//              time (a pass); each row keeps its own adapter's columns.  A
+//              cluster of up to 8 CTAs splits K, as many passes run beside
+//              each other as the SMs have room for, and the parts of a sum
+//              are added in cluster order.
 #include <mutex>
 
 #include "grouped.cuh"
@@ -26,6 +30,8 @@ namespace {
 using namespace tc;
 
 constexpr int kMaxTileRows = 256;
+constexpr int kMaxCluster = 8;     // the largest portable cluster
+constexpr int64_t kRowsMax = 128;  // rows the CUDA-core kernel takes
 constexpr int kThreads = 256;
 
 struct ShrinkArgs {
@@ -33,6 +39,8 @@ struct ShrinkArgs {
     LoraPlan plan;
     int ab_format;
     int la_z_step;  // 0 when all adapters share one LA
+    int ks;         // CTAs of a cluster, each with a part of K
+    float *part;    // tensor cores: [ks][M][r_pad] parts of the sums
     uint64_t timeout_ns;
 };
 
@@ -138,45 +146,53 @@ __device__ __forceinline__ void write_v_row(const ShrinkArgs &a, int64_t row, in
 }
 
 // -------------------------------------------------------- few rows: CUDA cores
+__device__ __forceinline__ float load_from_rank(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(v)
+                 : "r"(map_to_rank(smem_addr(p), rank))
+                 : "memory");
+    return v;
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) lora_shrink_rows_kernel(const ShrinkArgs a) {
     __shared__ alignas(16) TilePlan t;
-    __shared__ float u[256];
+    __shared__ float u[256];                     // this CTA's part of the row's sums
     __shared__ float part[kThreads / 32][256];
     pdl_wait();
     pdl_launch_dependents();
     const LoraProblem &p = a.p;
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x / a.ks;
+    const uint32_t rank = cluster_rank();
     const int64_t tile = row / a.plan.tile_rows, row0 = tile * a.plan.tile_rows;
     const int n = static_cast<int>(p.M - row0 < a.plan.tile_rows ? p.M - row0 : a.plan.tile_rows);
-    make_plan(p, row0, n, t);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int slot = t.slot_of[row - row0], count = t.count;
-    if (tid == 0) a.plan.slot[row] = slot;
-    if (row == row0) {
-        if (tid == 0) a.plan.count[tile] = count;
-        if (tid < count) a.plan.list[row0 + tid] = t.list[tid];
-    }
-    if (slot >= 0) {
-        const int64_t ad = t.list[slot];
-        const float scale = p.scale != nullptr ? p.scale[ad] : 1.f;
+    const int64_t id = p.adapter[row];
+    const bool has = id >= 0 && id < p.adapters;
+    const int r_cols = static_cast<int>(p.rank);
+    if (has) {
         const uint16_t *x = static_cast<const uint16_t *>(p.X) + row * p.ldx;
-        const uint16_t *la = static_cast<const uint16_t *>(p.LA) + ad * p.stride_a;
-        const int64_t k8 = p.K / 8 * 8;
-        const int rank = static_cast<int>(p.rank);
+        const uint16_t *la = static_cast<const uint16_t *>(p.LA) + id * p.stride_a;
+        // this CTA's K, in steps of 256
+        const int64_t steps = (p.K + 255) / 256;
+        const int64_t k_begin = steps * rank / a.ks * 256;
+        const int64_t k_stop = steps * (rank + 1) / a.ks * 256;
+        const int64_t k_end = k_stop < p.K ? k_stop : p.K;
+        const int64_t k8 = k_end / 8 * 8;
         if (p.a_kmajor) {
             // two columns per warp at a time, lanes over K
-            for (int c = warp * 2; c < rank; c += kThreads / 32 * 2) {
+            for (int c = warp * 2; c < r_cols; c += kThreads / 32 * 2) {
                 const uint16_t *l0 = la + c * p.ld_a;
-                const uint16_t *l1 = c + 1 < rank ? l0 + p.ld_a : l0;
+                const uint16_t *l1 = c + 1 < r_cols ? l0 + p.ld_a : l0;
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
-                for (int64_t k = lane * 8; k < k8; k += 256) {
+                for (int64_t k = k_begin + lane * 8; k < k8; k += 256) {
                     const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + k));
                     s0 = dot8<FMT>(xv, __ldg(reinterpret_cast<const uint4 *>(l0 + k)), s0);
                     s1 = dot8<FMT>(xv, __ldg(reinterpret_cast<const uint4 *>(l1 + k)), s1);
                 }
-                if (k8 + lane < p.K) {
+                if (k8 >= k_begin && k8 + lane < k_end) {
                     const float xk = widen_16(x[k8 + lane], FMT);
                     s0 = fmaf(xk, widen_16(l0[k8 + lane], FMT), s0);
                     s1 = fmaf(xk, widen_16(l1[k8 + lane], FMT), s1);
@@ -187,61 +203,78 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_rows_kernel(const Shrink
                     s1 += __shfl_xor_sync(0xffffffffu, s1, d);
                 }
                 if (lane == 0) {
-                    u[c] = s0 * scale;
-                    if (c + 1 < rank) u[c + 1] = s1 * scale;
+                    u[c] = s0;
+                    if (c + 1 < r_cols) u[c + 1] = s1;
                 }
             }
         } else {
             // eight columns (16 bytes of a row of LA) per lane; the lanes of
             // one 8-column group and the warps share K; sums added in a fixed
             // order
-            const int groups = (rank + 7) / 8;
-            for (int g0 = 0; g0 < groups; g0 += 32) {
-                const int live = groups - g0 < 32 ? groups - g0 : 32;
-                int wide = 1;
-                while (wide < live) wide *= 2;  // lanes per k
-                const int g = lane % wide, per = 32 / wide;
-                float s[8] = {};
-                if (g < live) {
+            const int live = (r_cols + 7) / 8;  // groups of eight, at most 32
+            int wide = 1;
+            while (wide < live) wide *= 2;  // lanes per k
+            const int g = lane % wide, per = 32 / wide;
+            float s[8] = {};
+            if (g < live) {
 #pragma unroll 4
-                    for (int64_t k = warp * per + lane / wide; k < p.K; k += kThreads / 32 * per) {
-                        const float xk = widen_16(x[k], FMT);
-                        const uint16_t *lk = la + k * p.ld_a + (g0 + g) * 8;
-                        uint32_t w[4] = {};
-                        if ((g0 + g) * 8 + 8 <= rank) {
-                            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(lk));
-                            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-                        } else {  // the last columns of a rank that is no multiple of 8
-                            for (int i = 0; i < rank - (g0 + g) * 8; ++i)
-                                w[i / 2] |= static_cast<uint32_t>(lk[i]) << (i % 2 * 16);
-                        }
+                for (int64_t k = k_begin + warp * per + lane / wide; k < k_end;
+                     k += kThreads / 32 * per) {
+                    const float xk = widen_16(x[k], FMT);
+                    const uint16_t *lk = la + k * p.ld_a + g * 8;
+                    uint32_t w[4] = {};
+                    if (g * 8 + 8 <= r_cols) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(lk));
+                        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+                    } else {  // the last columns of a rank that is no multiple of 8
+                        for (int i = 0; i < r_cols - g * 8; ++i)
+                            w[i / 2] |= static_cast<uint32_t>(lk[i]) << (i % 2 * 16);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            s[2 * i] = fmaf(xk, widen_16(w[i] & 0xffffu, FMT), s[2 * i]);
-                            s[2 * i + 1] = fmaf(xk, widen_16(w[i] >> 16, FMT), s[2 * i + 1]);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        s[2 * i] = fmaf(xk, widen_16(w[i] & 0xffffu, FMT), s[2 * i]);
+                        s[2 * i + 1] = fmaf(xk, widen_16(w[i] >> 16, FMT), s[2 * i + 1]);
                     }
                 }
-                for (int d = 16; d >= wide; d >>= 1) {
+            }
+            for (int d = 16; d >= wide; d >>= 1) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-                }
-                if (lane < wide && g < live) {
+                for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+            }
+            if (lane < wide && g < live) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) part[warp][(g0 + g) * 8 + i] = s[i];
-                }
+                for (int i = 0; i < 8; ++i) part[warp][g * 8 + i] = s[i];
             }
             __syncthreads();
-            if (tid < rank) {
-                float s = 0.f;
+            if (tid < r_cols) {
+                float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) s += part[w][tid];
-                u[tid] = s * scale;
+                for (int w = 0; w < kThreads / 32; ++w) sum += part[w][tid];
+                u[tid] = sum;
             }
         }
     }
-    __syncthreads();
-    write_v_row(a, row, slot, count, u);
+    // only the first CTA of the cluster goes on with the row
+    if (rank == 0) make_plan(p, row0, n, t);
+    __syncwarp();
+    cluster_sync();  // every part is written
+    if (rank == 0) {
+        const int slot = t.slot_of[row - row0], count = t.count;
+        if (tid == 0) a.plan.slot[row] = slot;
+        if (row == row0) {
+            if (tid == 0) a.plan.count[tile] = count;
+            if (tid < count) a.plan.list[row0 + tid] = t.list[tid];
+        }
+        if (has && tid < r_cols) {
+            float sum = u[tid];
+            for (uint32_t c = 1; c < static_cast<uint32_t>(a.ks); ++c)
+                sum += load_from_rank(&u[tid], c);
+            part[0][tid] = sum * (p.scale != nullptr ? p.scale[id] : 1.f);
+        }
+        __syncthreads();
+        write_v_row(a, row, slot, count, part[0]);
+    }
+    cluster_sync();  // the parts have been read
 }
 
 // ------------------------------------------------------ more rows: tensor cores
@@ -268,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) TilePlan t;
     __shared__ int used[kMaxTileRows];  // slots of this CTA's rows
-    __shared__ int n_used;
+    __shared__ int pass_of[kMaxTileRows];  // a slot's pass
     __shared__ uint64_t full[kStages], empty[kStages], done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
@@ -296,18 +329,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const LoraProblem &p = a.p;
     const LoraPlan &pl = a.plan;
-    const int64_t row_first = static_cast<int64_t>(blockIdx.x) * BM;  // this CTA's rows
+    // cluster x: parts of K; y: 128 rows each; z: every gridDim.z-th pass
+    const uint32_t rank = cluster_rank();
+    const int64_t row_first = static_cast<int64_t>(blockIdx.y) * BM;
+    const bool first_z = blockIdx.z == 0;
     const int64_t tile = row_first / pl.tile_rows, row0 = tile * pl.tile_rows;
     const int n = static_cast<int>(p.M - row0 < pl.tile_rows ? p.M - row0 : pl.tile_rows);
     const int n_mine = static_cast<int>(p.M - row_first < BM ? p.M - row_first : BM);
     make_plan(p, row0, n, t);
     const int off = static_cast<int>(row_first - row0);  // 0 or 128
     const int count = t.count;
-    if (row_first == row0) {
-        if (tid == 0) pl.count[tile] = count;
-        if (tid < count) pl.list[row0 + tid] = t.list[tid];
+    if (first_z && rank == 0) {
+        if (row_first == row0) {
+            if (tid == 0) pl.count[tile] = count;
+            if (tid < count) pl.list[row0 + tid] = t.list[tid];
+        }
+        if (tid < n_mine) pl.slot[row_first + tid] = t.slot_of[off + tid];
     }
-    if (tid < n_mine) pl.slot[row_first + tid] = t.slot_of[off + tid];
     // the slots that occur among this CTA's rows, in slot order
     int occurs = 0;
     if (tid < count)
@@ -321,13 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w < warp) at += t.warp_first[w];
         all += t.warp_first[w];
     }
-    if (occurs) used[at] = tid;
-    if (tid == 0) n_used = all;
-    __syncthreads();
-    const int total = n_used;
-
     const int per_pass = 256 / pl.r_pad;  // slots whose columns fit the stage and TMEM
-    const int num_kb = static_cast<int>((p.K + BK - 1) / BK);
+    if (occurs) {
+        used[at] = tid;
+        pass_of[tid] = at / per_pass;
+    }
+    __syncthreads();
+    const int passes = (all + per_pass - 1) / per_pass;
+
+    const int64_t blocks = (p.K + BK - 1) / BK;
+    const int kb_begin = static_cast<int>(blocks * rank / a.ks);
+    const int kb_end = static_cast<int>(blocks * (rank + 1) / a.ks);
     const uint32_t ring_base = smem_addr(ring);
     const uint32_t slot_bytes = static_cast<uint32_t>(pl.r_pad) * BK * 2;
     const int mn_block = pl.r_pad < 64 ? pl.r_pad : 64;  // rank-major LA: columns per TMA box
@@ -335,12 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int pass = 0; pass < total && ok; pass += per_pass) {
-        const int ns = total - pass < per_pass ? total - pass : per_pass;
+    uint32_t parity = 0;
+    for (int pass = blockIdx.z; pass < passes && ok; pass += gridDim.z) {
+        const int first_used = pass * per_pass;
+        const int ns = all - first_used < per_pass ? all - first_used : per_pass;
         if (warp == 0) {
             if (lane == 0) {
                 const uint32_t tx = static_cast<uint32_t>(a_rows) * 128u + ns * slot_bytes;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
                     if (!wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag, a.timeout_ns)) {
                         raise_abort(abort_flag);
                         ok = false;
@@ -353,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_2d<1>(sa + j * 128, &map_x, kb * BK,
                                        static_cast<int32_t>(row_first) + j, fb);
                     for (int s = 0; s < ns; ++s) {
-                        const int32_t ad = t.list[used[pass + s]] * a.la_z_step;
+                        const int32_t ad = t.list[used[first_used + s]] * a.la_z_step;
                         const uint32_t dst = sb + s * slot_bytes;
                         if (p.a_kmajor) {
                             tma_load_3d<1>(dst, &map_la, kb * BK, 0, ad, fb);
@@ -384,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n_mma = p.a_kmajor ? 1 : ns;
                 const uint32_t idesc = make_idesc(BM, p.a_kmajor ? ns * pl.r_pad : pl.r_pad, 0,
                                                   !p.a_kmajor, a.ab_format);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
                     if (!wait_bounded(smem_addr(&full[stage]), phase, abort_flag, a.timeout_ns)) {
                         raise_abort(abort_flag);
                         ok = false;
@@ -398,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_mma<1>(tmem_base + static_cast<uint32_t>(s * pl.r_pad),
                                       a_desc0 + st + kk * a_step,
                                       b_desc0 + st + s * (slot_bytes >> 4) + kk * b_step, idesc,
-                                      kb > 0 || kk > 0 ? 1u : 0u);
+                                      kb > kb_begin || kk > 0 ? 1u : 0u);
                     tc_commit<1>(smem_addr(&empty[stage]));
                     if (++stage == kStages) {
                         stage = 0;
@@ -410,11 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         // the sums are complete (every thread waits: TMEM is reused next pass)
-        const uint32_t parity = static_cast<uint32_t>(pass / per_pass) & 1u;
         if (!wait_bounded(smem_addr(&done), parity, abort_flag, a.timeout_ns)) {
             raise_abort(abort_flag);
             ok = false;
         }
+        parity ^= 1u;
         ok = __syncthreads_and(ok ? 1 : 0) != 0;
         if (!ok) break;
         tc_fence_after();
@@ -424,32 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;
         const int my_slot = r < n_mine ? t.slot_of[off + r] : -1;
         const int64_t row = row_first + r;
+        float *const mine = a.part + (static_cast<int64_t>(rank) * p.M + row) * pl.r_pad;
         for (int s = warp / 4; s < ns; s += 2) {
-            const int slot = used[pass + s];
-            const float scale = p.scale != nullptr ? p.scale[t.list[slot]] : 1.f;
+            const int slot = used[first_used + s];
             for (int j = 0; j < pl.r_pad; j += 16) {
                 uint32_t v[16];
                 __syncwarp();
                 tmem_load_16cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                      static_cast<uint32_t>(s * pl.r_pad + j), v);
                 if (my_slot == slot) {
-                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint16_t h0, l0, h1, l1;
-                        split_16(__uint_as_float(v[2 * i]) * scale, a.ab_format, h0, l0);
-                        split_16(__uint_as_float(v[2 * i + 1]) * scale, a.ab_format, h1, l1);
-                        hi[i] = h0 | (static_cast<uint32_t>(h1) << 16);
-                        lo[i] = l0 | (static_cast<uint32_t>(l1) << 16);
-                    }
-                    uint4 *d = reinterpret_cast<uint4 *>(pl.V + row * pl.ldv + slot * pl.rc + j);
-                    d[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    d[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                    if (pl.rc > pl.r_pad) {
-                        d = reinterpret_cast<uint4 *>(pl.V + row * pl.ldv + slot * pl.rc + pl.r_pad + j);
-                        d[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        d[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4 *>(mine + j)[i] =
+                            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
         }
@@ -457,13 +488,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         tc_fence_after();
     }
-    // zeros in the rows' other slots, 16 bytes at a time
-    const int quads = pl.rc / 8;
-    for (int r = warp; r < n_mine; r += kThreads / 32) {
+    // Each CTA of the cluster finishes a share of the rows: the parts of a sum
+    // in cluster order, the scale, the rounding; zeros in the row's other
+    // slots.  A row belongs to the z whose passes hold its slot (rows without
+    // an adapter: the first).
+    __threadfence();
+    __syncwarp();
+    cluster_sync();
+    const int groups = pl.rc / 8;  // 16 bytes of V
+    const int n_hi = pl.r_pad / 8;
+    const int share = (n_mine + a.ks - 1) / a.ks;
+    const int r_end = share * (static_cast<int>(rank) + 1) < n_mine ? share * (static_cast<int>(rank) + 1) : n_mine;
+    for (int r = share * static_cast<int>(rank) + warp; ok && r < r_end; r += kThreads / 32) {
         const int own = t.slot_of[off + r];
+        const bool mine = own >= 0 ? pass_of[own] % gridDim.z == blockIdx.z : first_z;
+        if (!mine) continue;
+        const float scale = own >= 0 && p.scale != nullptr ? p.scale[t.list[own]] : 1.f;
+        const float *part = a.part + (row_first + r) * pl.r_pad;
         uint4 *d = reinterpret_cast<uint4 *>(pl.V + (row_first + r) * pl.ldv);
-        for (int c = lane; c < count * quads; c += 32)
-            if (c / quads != own) d[c] = make_uint4(0, 0, 0, 0);
+        for (int c = lane; c < count * groups; c += 32) {
+            uint32_t w[4] = {};
+            const int slot = c / groups, in = c - slot * groups;
+            if (slot == own) {
+                const int j = (in < n_hi ? in : in - n_hi) * 8;
+                float u[8] = {};
+                for (int k = 0; k < a.ks; ++k) {
+                    const float4 *q = reinterpret_cast<const float4 *>(
+                        part + static_cast<int64_t>(k) * p.M * pl.r_pad + j);
+                    const float4 x = __ldcg(q), y = __ldcg(q + 1);
+                    u[0] += x.x, u[1] += x.y, u[2] += x.z, u[3] += x.w;
+                    u[4] += y.x, u[5] += y.y, u[6] += y.z, u[7] += y.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint16_t h0, l0, h1, l1;
+                    split_16(u[2 * i] * scale, a.ab_format, h0, l0);
+                    split_16(u[2 * i + 1] * scale, a.ab_format, h1, l1);
+                    w[i] = in < n_hi ? (h0 | (static_cast<uint32_t>(h1) << 16))
+                                     : (l0 | (static_cast<uint32_t>(l1) << 16));
+                }
+            }
+            d[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
     if (!ok) {
         // copies in flight land before the CTA exits
@@ -479,8 +545,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMaxDevices = 64;
 std::once_flag g_once[kMaxDevices];
 cudaError_t g_err[kMaxDevices];
+int g_sms[kMaxDevices];
 
 }  // namespace
+
+// Tensor cores: CTAs that share K, so that few rows still fill the SMs (at
+// least four K blocks each).
+static int shrink_parts(const LoraProblem &p, int sms) {
+    const int64_t tiles = (p.M + BM - 1) / BM, blocks = (p.K + BK - 1) / BK;
+    int64_t ks = sms / tiles;
+    if (ks > blocks / 4) ks = blocks / 4;
+    if (ks > kMaxCluster) ks = kMaxCluster;
+    return static_cast<int>(ks < 1 ? 1 : ks);
+}
+
+size_t lora_shrink_part_bytes(int64_t rows, int r_pad) {
+    if (rows <= kRowsMax) return 0;
+    // parts x rows: at most SMs x 128 while there are several parts (256 SMs allowed for)
+    const int64_t most = rows > 256 * BM ? rows : 256 * BM;
+    const int64_t n = kMaxCluster * rows < most ? kMaxCluster * rows : most;
+    return static_cast<size_t>(n) * r_pad * sizeof(float);
+}
 
 bool lora_shrink_eligible(const LoraProblem &p) {
     return p.rank <= 256 && tma_rows(p.X, p.ldx) &&
@@ -494,15 +579,23 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     a.plan = plan;
     a.ab_format = in == InType::BF16 ? 1 : 0;
     a.timeout_ns = 1000ull * 1000ull * 1000ull;
-    cudaLaunchAttribute attr;
-    set_pdl_attribute(&attr);
+    cudaLaunchAttribute attr[2];
+    set_pdl_attribute(&attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (p.M <= 128) {
-        cfg.gridDim = dim3(static_cast<unsigned>(p.M), 1, 1);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (p.M <= kRowsMax) {
+        // at least 512 of K per CTA
+        const int64_t ks = p.K / 512;
+        a.ks = static_cast<int>(ks < 1 ? 1 : (ks > kMaxCluster ? kMaxCluster : ks));
+        attr[1].val.clusterDim.x = static_cast<unsigned>(a.ks);
+        cfg.gridDim = dim3(static_cast<unsigned>(p.M * a.ks), 1, 1);
         return in == InType::BF16 ? cudaLaunchKernelEx(&cfg, lora_shrink_rows_kernel<1>, a)
                                   : cudaLaunchKernelEx(&cfg, lora_shrink_rows_kernel<0>, a);
     }
@@ -513,6 +606,8 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     std::call_once(g_once[dev], [dev] {
         g_err[dev] = cudaFuncSetAttribute(lora_shrink_tc_kernel,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        if (g_err[dev] == cudaSuccess)
+            g_err[dev] = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
     });
     if (g_err[dev] != cudaSuccess) return g_err[dev];
     const bool bf16 = in == InType::BF16;
@@ -531,7 +626,16 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
                                 : plan.r_pad == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                    : CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(static_cast<unsigned>((p.M + BM - 1) / BM), 1, 1);
+    const int64_t tiles = (p.M + BM - 1) / BM;
+    a.ks = shrink_parts(p, g_sms[dev]);
+    a.part = plan.part;
+    const int64_t slots = p.adapters < BM ? p.adapters : BM;
+    const int64_t passes = (slots * plan.r_pad + 255) / 256;
+    int64_t z = g_sms[dev] / (tiles * a.ks);
+    z = z < 1 ? 1 : (z > passes ? passes : z);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.ks);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ks), static_cast<unsigned>(tiles),
+                       static_cast<unsigned>(z));
     cfg.dynamicSmemBytes = kTcSmem;
     return cudaLaunchKernelEx(&cfg, lora_shrink_tc_kernel, map_x, map_la, a);
 }
