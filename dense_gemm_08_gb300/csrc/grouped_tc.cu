@@ -8,18 +8,19 @@
 // to one group.  The sizes of the groups are on the device only: each warp
 // finds a tile's group with a warp scan over the offsets (GroupWalk).  Warp 0
 // fills a ring of 128-byte-swizzled stages by TMA, warp 1 issues tcgen05.mma
-// into one of two TMEM accumulators, warps 2-5 write the other to D.
+// into one of two TMEM accumulators, warps 2-9 write the other to D.
 //
-//   rows: a row tile may end inside the next group's rows.  They are loaded
-//     or not, but only reach accumulator rows that are not stored (each row
-//     of D depends on its own row of A), so no zero fill is needed.  A row
-//     tile with few rows loads 16-row boxes; gathered rows come four at a time
-//     by TMA gather, with each lane's row numbers in registers.
+//   rows: a row tile may end inside the next group's rows.  They only reach
+//     accumulator rows that are not stored (each row of D depends on its own
+//     row of A), so no zero fill is needed.  Gathered rows come four at a time
+//     by TMA gather (warps 10 and 11).
 //   wgrad: both operands have their rows along K and are MN-major.  A group's
 //     last K block must not read the next group's rows (not even times zero:
 //     they may be infinite), so that block is fetched by TMA gather with row
 //     numbers outside the tensor (zeros) past the group's end, and only its
 //     16-row slices that hold rows are multiplied.
+//   lora:   D(i, :) = act(X(i, :) op(W) + V(i, :) op(LB) + bias): the projection
+//     of all rows, its K loop continued over the slots of the tile's adapters.
 #include <mutex>
 
 #include "grouped.cuh"
@@ -37,7 +38,7 @@ enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
 
 constexpr int kGroupM = 16;  // row tiles per band of the raster inside a group
 constexpr int kMaxStages = 24;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 2;
 constexpr int kRingBytes = 7 * 32768;  // all variants
 constexpr int kMaxSlots = 256;         // lora: adapters of a tile
@@ -60,7 +61,9 @@ struct Args {
     OutArgs out;
     int64_t stride_d, stride_c;
     uint32_t tiles_m, tiles_n;  // tiles_m: wgrad only
-    int num_kb;                 // rows: K blocks
+    int num_kb;                 // rows, lora: K steps of a stage each
+    int ksub;                   // rows, lora: blocks of 64 of K per stage
+    int a_wide, b_wide;         // wgrad: whole 64-column blocks, several per copy
     int b_kmajor;               // rows
     int bn;                     // columns per tile (of the CTA or the pair)
     int am;                     // rows of D per CTA: 128, or 16 / 32 / 64 (single CTAs)
@@ -80,7 +83,7 @@ struct Tile {
     int32_t first, last;  // the group's rows
     int64_t m0, n0;       // first row (rows: of all product rows; wgrad: of D_g) and column
     int m_valid;          // rows of D in the tile, 1 .. 128 CG
-    int nkb;              // K blocks
+    int nkb;              // K steps (stages)
     int tile_m;           // its row of tiles
 };
 
@@ -140,11 +143,31 @@ __device__ __forceinline__ int cta_rows(const Tile &t, int rank) {
     return r < 0 ? 0 : (r > BM ? BM : r);
 }
 
-// rows: A bytes a CTA loads per stage for n of its 128 rows -- all 128 in one
-// box when more than 64 hold data, else boxes of 16 rows; gathered: quads.
-__device__ __forceinline__ uint32_t a_bytes(int n, bool gather) {
-    if (gather) return static_cast<uint32_t>((n + 3) / 4) * 512u;
-    return n > 64 ? BM * 128u : static_cast<uint32_t>((n + 15) / 16) * 2048u;
+// Bytes of A a CTA loads per stage when n of its rows hold data: one box of am
+// rows (rows past the group's end come along), or whole quads of gathered rows.
+template <bool GATHER>
+__device__ __forceinline__ uint32_t a_bytes(const Args &a, int n) {
+    if (n == 0) return 0;
+    const int rows = GATHER ? (n + 3) / 4 * 4 : a.am;
+    return static_cast<uint32_t>(rows * a.ksub) * 128u;
+}
+
+// The order of a tile's K blocks.  CTA pairs: every other tile walks K
+// backwards, so that it starts on the blocks of B the tile before it read last.
+// Single CTAs start at different blocks: columns of B are a power of two apart
+// as a rule, and CTAs in step would read the same few DRAM channels, and the
+// same lines of A, at once.
+template <int CG>
+__device__ __forceinline__ int first_block(uint32_t w, int nkb, bool reverse) {
+    return CG == 1 ? static_cast<int>((w * 5u) % static_cast<uint32_t>(nkb)) : (reverse ? nkb - 1 : 0);
+}
+template <int CG>
+__device__ __forceinline__ int next_block(int kb, int nkb, bool reverse) {
+    return CG == 2 && reverse ? kb - 1 : (kb + 1 == nkb ? 0 : kb + 1);
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 __device__ __forceinline__ float value_16(const void *p, int64_t at, int ab_format) {
@@ -179,21 +202,22 @@ __device__ __noinline__ float lora_exact(const Args &a, int64_t i, int64_t n) {
 template <int CG, int MODE, bool GATHER>
 __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a,
-                      const __grid_constant__ CUtensorMap map_a_part,
+                      const __grid_constant__ CUtensorMap map_a_rows,
                       const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_b_part,
+                      const __grid_constant__ CUtensorMap map_b_rows,
                       const __grid_constant__ CUtensorMap map_v, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + kRingBytes);
-    uint64_t *full = bars;                // [kMaxStages] TMA -> MMA (the leader counts both CTAs)
-    uint64_t *empty = bars + kMaxStages;  // [kMaxStages] MMA -> TMA
-    uint64_t *tfull = empty + kMaxStages;  // [2] MMA -> epilogue
-    uint64_t *tempty = tfull + 2;          // [2] epilogue -> MMA (the leader counts both CTAs)
-    uint64_t *go = tempty + 2;  // [kGatherWarps][kMaxStages] producer -> gather warp: stage is free
-    uint64_t *drain = go + kGatherWarps * kMaxStages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    // barriers (8 bytes each): full[kMaxStages] TMA -> MMA (the leader's count
+    // both CTAs), empty[kMaxStages] MMA -> TMA, tfull[2] MMA -> epilogue,
+    // tempty[2] epilogue -> MMA (the leader's count both CTAs),
+    // go[kGatherWarps][kMaxStages] producer -> gather warp, drain
+    const uint32_t ring0 = smem_addr(ring);
+    const uint32_t full0 = ring0 + kRingBytes, empty0 = full0 + 8 * kMaxStages;
+    const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16;
+    const uint32_t go0 = tempty0 + 16, drain = go0 + 8 * kGatherWarps * kMaxStages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + (drain + 8 - ring0));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *numbers = reinterpret_cast<int *>(ring + kRingBytes + 1024);  // [kMaxSlots]
 
@@ -203,29 +227,21 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
     const uint32_t first_tile = blockIdx.x / CG, tile_step = gridDim.x / CG;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(smem_addr(&full[s]), 1);
-            mbar_init(smem_addr(&empty[s]), 1);
-        }
-        for (int s = 0; s < kGatherWarps * kMaxStages; ++s) mbar_init(smem_addr(&go[s]), 1);
+        for (int s = 0; s < 2 * kMaxStages; ++s) mbar_init(full0 + 8 * s, 1);
+        for (int s = 0; s < kGatherWarps * kMaxStages; ++s) mbar_init(go0 + 8 * s, 1);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_addr(&tfull[b]), 1);
-            mbar_init(smem_addr(&tempty[b]), kEpiWarps * CG);
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, kEpiWarps * CG);
         }
-        mbar_init(smem_addr(drain), 1);
+        mbar_init(drain, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a_part))
-                     : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
-        if (MODE != kRows)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b_part))
-                         : "memory");
-        if (MODE == kLora)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v))
-                         : "memory");
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+        if (GATHER || MODE == kWgrad) prefetch_map(&map_a_rows);
+        if (MODE != kRows) prefetch_map(&map_b_rows);
+        if (MODE == kLora) prefetch_map(&map_v);
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(tmem_slot));
     tc_fence_before();
@@ -240,78 +256,73 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
     if (!late) pdl_wait();
     pdl_launch_dependents();
 
-    const uint32_t ring_base = smem_addr(ring);
     const int stages = args.stages;
-    const uint32_t stage_bytes = args.stage_bytes;
-    const uint32_t a_region = args.a_region;
+    const uint32_t stage_bytes = args.stage_bytes, a_region = args.a_region;
     const int b_rows = args.bn / CG;  // columns of B this CTA loads
+    const int ksub = MODE == kWgrad ? 1 : args.ksub;
+    // where the copies of a stage are counted
+    const uint32_t count0 = CG == 1 ? full0 : map_to_rank(full0, 0);
     TileWalk<CG, MODE> tiles(args);
     Tile t;
     bool aborted = false;
+    // every lane waits (the warp stays converged); false: gave up
+    auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+        const bool done = __all_sync(
+            0xffffffffu, wait_bounded(bar, parity, abort_flag, args.timeout_ns));
+        if (!done && lane == 0) raise_abort(abort_flag);
+        return done;
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         int stage = 0;
         uint32_t phase = 0;
-        int64_t issued = 0;
-        int ok = 1;
+        uint32_t issued = 0;
+        bool ok = true;
+        auto advance = [&]() {
+            issued += issued < static_cast<uint32_t>(stages) ? 1u : 0u;
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
         bool reverse = false;
         for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
             const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+            const int mine = cta_rows(t, rank);
+            const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
             if constexpr (MODE != kWgrad) {
-                const int mine = cta_rows(t, rank);
-                const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
-                const uint32_t tx = a_bytes(cta_rows(t, 0), GATHER) +
-                                    (CG == 2 ? a_bytes(cta_rows(t, 1), GATHER) : 0u) +
-                                    CG * b_rows * 128u;
+                const uint32_t tx = a_bytes<GATHER>(args, cta_rows(t, 0)) +
+                                    (CG == 2 ? a_bytes<GATHER>(args, cta_rows(t, 1)) : 0u) +
+                                    static_cast<uint32_t>(CG * b_rows * ksub) * 128u;
                 const int32_t z = t.g * args.z_step;
-                // every other tile walks K backwards: it starts on the blocks
-                // of B the tile before it read last.  Single CTAs also start
-                // at different blocks: columns of B are a power of two apart
-                // as a rule, and CTAs in step would read the same few DRAM
-                // channels, and the same lines of A, at once.
-                int kb = CG == 1 ? static_cast<int>((w * 5u) % static_cast<uint32_t>(t.nkb))
-                                 : (reverse ? t.nkb - 1 : 0);
+                int kb = first_block<CG>(w, t.nkb, reverse);
                 for (int i = 0; i < t.nkb; ++i) {
-                    const int32_t k0 = kb * BK;
-                    kb = CG == 2 && reverse ? kb - 1 : (kb + 1 == t.nkb ? 0 : kb + 1);
-                    if (lane == 0)
-                        ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
-                                          args.timeout_ns);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) {
-                        if (lane == 0) raise_abort(abort_flag);
-                        break;
-                    }
-                    const uint32_t fb_local = smem_addr(&full[stage]);
-                    const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
-                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
-                    if (lane == 0) {
-                        if (leader) mbar_arrive_expect_tx(fb_local, tx);
+                    ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+                    if (!ok) break;
+                    const uint32_t fb = count0 + 8 * stage;
+                    const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
                         if constexpr (GATHER) {
-                            for (int h = 0; h < kGatherWarps; ++h)
-                                if (mine > h * 64) mbar_arrive(smem_addr(&go[h * kMaxStages + stage]));
+                            if (mine > 0) mbar_arrive(go0 + 8 * stage);
+                            if (mine > 64) mbar_arrive(go0 + 8 * (kMaxStages + stage));
                         }
+                        // several blocks of 64 at once: the maps count K in blocks
+                        const int32_t block = kb * ksub;
+                        const int32_t k_in = ksub > 1 ? 0 : block * BK, k_block = ksub > 1 ? block : 0;
                         if (args.b_kmajor) {
-                            tma_load_3d<CG>(sb, &map_b, k0, b0, z, fb);
+                            tma_load_4d<CG>(sb, &map_b, k_in, b0, k_block, z, fb);
                         } else {
                             for (int j = 0; j < b_rows; j += 64)
-                                tma_load_3d<CG>(sb + j * 128, &map_b, b0 + j, k0, z, fb);
+                                tma_load_3d<CG>(sb + j * 128 * ksub, &map_b, b0 + j, block * BK, z, fb);
                         }
                         if constexpr (!GATHER) {
-                            if (mine > 64) {
-                                tma_load_2d<CG>(sa, &map_a, k0, m0, fb);
-                            } else {
-                                for (int j = 0; j < mine; j += 16)
-                                    tma_load_2d<CG>(sa + j * 128, &map_a_part, k0, m0 + j, fb);
-                            }
+                            if (mine > 0) tma_load_3d<CG>(sa, &map_a, k_in, m0, k_block, fb);
                         }
                     }
-                    ++issued;
-                    if (++stage == stages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    kb = next_block<CG>(kb, t.nkb, reverse);
+                    advance();
                 }
                 if (MODE == kLora && ok && args.plan.count != nullptr) {
                     // the second product: V (128-byte rows of 64 columns) times
@@ -324,88 +335,80 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     for (int i = lane; i < cols / pl.rc; i += 32) numbers[i] = list[i] * args.lb_z_step;
                     __syncwarp();
                     const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
-                    const uint32_t a0_bytes = static_cast<uint32_t>((cta_rows(t, 0) + 15) / 16) * 2048u;
-                    const uint32_t a1_bytes =
-                        CG == 2 ? static_cast<uint32_t>((cta_rows(t, 1) + 15) / 16) * 2048u : 0u;
+                    const uint32_t v_bytes = static_cast<uint32_t>(args.am) * 128u;
+                    const uint32_t v_tx = v_bytes + (CG == 2 && cta_rows(t, 1) > 0 ? v_bytes : 0u);
+                    int slot = 0, in_slot = 0, j0 = 0;  // of the next slice
                     for (int c0 = 0; c0 < cols; c0 += BK) {
-                        if (lane == 0)
-                            ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
-                                              args.timeout_ns);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (!ok) {
-                            if (lane == 0) raise_abort(abort_flag);
-                            break;
-                        }
-                        const uint32_t fb_local = smem_addr(&full[stage]);
-                        const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
-                        const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
+                        ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+                        if (!ok) break;
+                        const uint32_t fb = count0 + 8 * stage;
+                        const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
                         const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
-                        if (lane == 0) {
+                        if (elect_one()) {
                             if (leader)
-                                mbar_arrive_expect_tx(fb_local, a0_bytes + a1_bytes + CG * slices * slice_bytes);
-                            for (int j = 0; j < mine; j += 16)
-                                tma_load_2d<CG>(sa + j * 128, &map_v, c0, m0 + j, fb);
-                            for (int q = 0; q < slices; ++q) {
-                                const int c = c0 + q * 16, s = c / pl.rc;
-                                const int32_t ad = numbers[s];
-                                const int32_t j0 = (c - s * pl.rc) % pl.r_pad;
-                                const uint32_t dst = sb + q * slice_bytes;
+                                mbar_arrive_expect_tx(full0 + 8 * stage, v_tx + CG * slices * slice_bytes);
+                            if (mine > 0) tma_load_2d<CG>(sa, &map_v, c0, m0, fb);
+                        }
+                        for (int q = 0; q < slices; ++q) {
+                            const int32_t ad = numbers[slot];
+                            const uint32_t dst = sb + q * slice_bytes;
+                            if (elect_one()) {
                                 if (args.l.b_kmajor) {
-                                    tma_load_3d<CG>(dst, &map_b_part, j0, b0, ad, fb);
+                                    tma_load_3d<CG>(dst, &map_b_rows, j0, b0, ad, fb);
                                 } else {
                                     for (int j = 0; j < b_rows; j += 64)
-                                        tma_load_3d<CG>(dst + j * 32, &map_b_part, b0 + j, j0, ad, fb);
+                                        tma_load_3d<CG>(dst + j * 32, &map_b_rows, b0 + j, j0, ad, fb);
                                 }
                             }
+                            // (the rounding's remainders meet the same rows of LB again)
+                            in_slot += 16;
+                            j0 = j0 + 16 == pl.r_pad ? 0 : j0 + 16;
+                            if (in_slot == pl.rc) {
+                                in_slot = 0;
+                                ++slot;
+                            }
                         }
-                        ++issued;
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                        advance();
                     }
                 }
             } else {
-                const int32_t a0 = static_cast<int32_t>(t.m0 + rank * BM);
                 const int b_blocks = b_rows / 64;
                 for (int i = 0; i < t.nkb; ++i) {
                     const int32_t r0 = t.first + i * BK;
                     const int rem = t.last - r0 < BK ? t.last - r0 : BK;
                     const int quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
                     const bool part = rem < BK;
-                    if (lane == 0)
-                        ok = wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag,
-                                          args.timeout_ns);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) {
-                        if (lane == 0) raise_abort(abort_flag);
-                        break;
-                    }
-                    const uint32_t fb_local = smem_addr(&full[stage]);
-                    const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
-                    const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
-                    if (lane == 0) {
+                    ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+                    if (!ok) break;
+                    const uint32_t fb = count0 + 8 * stage;
+                    const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                    if (elect_one()) {
                         if (leader)
                             mbar_arrive_expect_tx(
-                                fb_local, CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
+                                full0 + 8 * stage,
+                                CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
                         if (GATHER || part) {
                             for (int h = 0; h < kGatherWarps; ++h)
-                                mbar_arrive(smem_addr(&go[h * kMaxStages + stage]));
+                                mbar_arrive(go0 + 8 * (h * kMaxStages + stage));
                         }
                         if (!part) {
                             if constexpr (!GATHER) {
-                                tma_load_2d<CG>(sa, &map_a, a0, r0, fb);
-                                tma_load_2d<CG>(sa + 8192, &map_a, a0 + 64, r0, fb);
+                                if (args.a_wide) {
+                                    tma_load_3d<CG>(sa, &map_a, 0, r0, m0 / 64, fb);
+                                } else {
+                                    tma_load_2d<CG>(sa, &map_a, m0, r0, fb);
+                                    tma_load_2d<CG>(sa + 8192, &map_a, m0 + 64, r0, fb);
+                                }
                             }
-                            for (int j = 0; j < b_blocks; ++j)
-                                tma_load_2d<CG>(sb + j * 8192, &map_b, b0 + 64 * j, r0, fb);
+                            if (args.b_wide) {
+                                tma_load_3d<CG>(sb, &map_b, 0, r0, b0 / 64, fb);
+                            } else {
+                                for (int j = 0; j < b_blocks; ++j)
+                                    tma_load_2d<CG>(sb + j * 8192, &map_b, b0 + 64 * j, r0, fb);
+                            }
                         }
                     }
-                    ++issued;
-                    if (++stage == stages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    advance();
                 }
             }
         }
@@ -413,14 +416,13 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         // the copies in flight land before the CTA exits (the leader's
         // barriers count both CTAs' bytes)
         if (lane == 0 && leader) {
-            const int64_t outstanding = issued < stages ? issued : stages;
-            for (int64_t i = 0; i < outstanding; ++i) {
+            for (uint32_t i = 0; i < issued; ++i) {
                 if (--stage < 0) {
                     stage = stages - 1;
                     phase ^= 1;
                 }
                 const volatile int never = 0;
-                if (!wait_bounded(smem_addr(&full[stage]), phase, &never, args.timeout_ns))
+                if (!wait_bounded(full0 + 8 * stage, phase, &never, args.timeout_ns))
                     raise_abort(abort_flag);
             }
         }
@@ -431,112 +433,105 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         if (leader) {
             const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
             const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
-            const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring_base, 0) : desc_kmajor(ring_base, 0);
-            const uint64_t b_desc0 = b_mn ? desc_mnmajor(ring_base + a_region, 0)
-                                          : desc_kmajor(ring_base + a_region, 0);
+            const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring0, 0) : desc_kmajor(ring0, 0);
+            const uint64_t b_desc0 =
+                b_mn ? smem_desc(ring0 + a_region, static_cast<uint32_t>(ksub) * 8192u, 1024)
+                     : desc_kmajor(ring0 + a_region, 0);
             const uint64_t a_step = a_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
             const uint64_t b_step = b_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+            // a stage's blocks of 64: rows x 128 bytes apart (N-major: 64 rows of K)
+            const uint64_t a_sub = static_cast<uint64_t>(args.am) * 128u >> 4;
+            const uint64_t b_sub = b_mn ? 8192u >> 4 : static_cast<uint64_t>(b_rows) * 128u >> 4;
             // lora: slices of LB -- K-major: 32-byte rows (32-byte swizzle);
             // N-major: 16 rows per 64-column block (128-byte swizzle)
             const bool lb_mn = MODE == kLora && !args.l.b_kmajor;
             const uint32_t lb_idesc = make_idesc(BM * CG, args.bn, 0, lb_mn, args.ab_format);
-            const uint64_t lb_desc0 = lb_mn ? smem_desc(ring_base + a_region, 16 * 128, 1024)
-                                            : smem_desc(ring_base + a_region, 16, 256, kSwizzle32);
-            const uint32_t full0 = smem_addr(&full[0]), empty0 = smem_addr(&empty[0]);
+            const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
+                                            : smem_desc(ring0 + a_region, 16, 256, kSwizzle32);
+            const uint64_t stage_step = stage_bytes >> 4;
             int stage = 0;
             uint32_t phase = 0;
             uint32_t acc = 0;  // accumulators filled so far
-            int ok = 1;
+            bool ok = true;
             for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step) {
                 if (MODE == kWgrad && t.nkb == 0) continue;  // no rows: nothing to add
-                if (lane == 0) {
-                    const int buf = static_cast<int>(acc & 1);
-                    ok = wait_bounded(smem_addr(&tempty[buf]), ((acc >> 1) & 1) ^ 1, abort_flag,
-                                      args.timeout_ns);
+                const uint32_t buf = acc & 1;
+                ok = wait_all(tempty0 + 8 * buf, ((acc >> 1) & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * 256;
+                // 16-row slices of the last block that hold rows
+                const int last_slices =
+                    MODE == kWgrad ? (t.last - t.first - (t.nkb - 1) * BK + 15) / 16 : 4;
+                for (int i = 0; i < t.nkb; ++i) {
+                    ok = wait_all(full0 + 8 * stage, phase);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
-                    // 16-row slices of the last block that hold rows
-                    const int last_slices =
-                        MODE == kWgrad ? (t.last - t.first - (t.nkb - 1) * BK + 15) / 16 : 4;
-                    auto wait_full = [&](int s, uint32_t p) {
-                        const uint32_t fb = full0 + 8u * static_cast<uint32_t>(s);
-                        return mbar_try_wait(fb, p) ||
-                               wait_bounded(fb, p, abort_flag, args.timeout_ns);
-                    };
-                    auto multiply = [&](int s, int slices, uint32_t add) {
-                        const uint64_t ad = a_desc0 + static_cast<uint64_t>(s) * (stage_bytes >> 4);
-                        const uint64_t bd = b_desc0 + static_cast<uint64_t>(s) * (stage_bytes >> 4);
-                        tc_mma<CG>(d_tmem, ad, bd, idesc, add);
+                    const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage) * stage_step;
+                    const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage) * stage_step;
+                    const int slices = MODE == kWgrad && i + 1 == t.nkb ? last_slices : 4;
+                    if (elect_one()) {
+                        tc_mma<CG>(d_tmem, ad, bd, idesc, i > 0 ? 1u : 0u);
                         if (MODE != kWgrad || slices > 1)
                             tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
                         if (MODE != kWgrad || slices > 2)
                             tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
                         if (MODE != kWgrad || slices > 3)
                             tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
-                    };
-                    for (int i = 0; ok && i < t.nkb; i += 2) {
-                        // two stages per round: their MMAs issue back to back
-                        const bool two = i + 1 < t.nkb;
-                        const int s0 = stage, s1 = s0 + 1 == stages ? 0 : s0 + 1;
-                        const uint32_t p0 = phase, p1 = s1 == 0 ? p0 ^ 1u : p0;
-                        if (!wait_full(s0, p0) || (two && !wait_full(s1, p1))) {
-                            ok = 0;
-                            break;
-                        }
-                        tc_fence_after();
-                        multiply(s0, i + 1 == t.nkb ? last_slices : 4, i > 0 ? 1u : 0u);
-                        if (two) multiply(s1, i + 2 == t.nkb ? last_slices : 4, 1u);
-                        tc_commit<CG>(empty0 + 8u * static_cast<uint32_t>(s0));
-                        if (two) {
-                            tc_commit<CG>(empty0 + 8u * static_cast<uint32_t>(s1));
-                            stage = s1 + 1 == stages ? 0 : s1 + 1;
-                            phase = stage == 0 ? p1 ^ 1u : p1;
-                        } else {
-                            stage = s1;
-                            phase = p1;
-                        }
-                    }
-                    if (MODE == kLora && ok && args.plan.count != nullptr) {
-                        if (late) pdl_wait();
-                        const int cols = args.plan.count[t.tile_m] * args.plan.rc;
-                        const uint32_t slice_step = static_cast<uint32_t>(b_rows) * 32u >> 4;
-                        for (int c0 = 0; c0 < cols; c0 += BK) {
-                            if (!wait_full(stage, phase)) {
-                                ok = 0;
-                                break;
+                        if constexpr (MODE != kWgrad) {
+                            for (int u = 1; u < ksub; ++u) {
+                                const uint64_t au = ad + u * a_sub, bu = bd + u * b_sub;
+                                tc_mma<CG>(d_tmem, au, bu, idesc, 1u);
+                                tc_mma<CG>(d_tmem, au + a_step, bu + b_step, idesc, 1u);
+                                tc_mma<CG>(d_tmem, au + 2 * a_step, bu + 2 * b_step, idesc, 1u);
+                                tc_mma<CG>(d_tmem, au + 3 * a_step, bu + 3 * b_step, idesc, 1u);
                             }
-                            tc_fence_after();
-                            const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
-                            const uint64_t at = static_cast<uint64_t>(stage) * (stage_bytes >> 4);
+                        }
+                        tc_commit<CG>(empty0 + 8 * stage);  // frees the stage (both CTAs)
+                    }
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (MODE == kLora && ok && args.plan.count != nullptr) {
+                    if (late) pdl_wait();
+                    const int cols = args.plan.count[t.tile_m] * args.plan.rc;
+                    const uint64_t slice_step = static_cast<uint64_t>(b_rows) * 32u >> 4;
+                    for (int c0 = 0; c0 < cols; c0 += BK) {
+                        ok = wait_all(full0 + 8 * stage, phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                        const uint64_t at = static_cast<uint64_t>(stage) * stage_step;
+                        if (elect_one()) {
                             for (int q = 0; q < slices; ++q)
                                 tc_mma<CG>(d_tmem, a_desc0 + at + q * a_step,
                                            lb_desc0 + at + q * slice_step, lb_idesc, 1u);
-                            tc_commit<CG>(empty0 + 8u * static_cast<uint32_t>(stage));
-                            if (++stage == stages) {
-                                stage = 0;
-                                phase ^= 1u;
-                            }
+                            tc_commit<CG>(empty0 + 8 * stage);
+                        }
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1u;
                         }
                     }
-                    if (ok)
-                        tc_commit<CG>(smem_addr(&tfull[buf]));
-                    else
-                        raise_abort(abort_flag);
                 }
+                if (!ok) break;
+                if (elect_one()) tc_commit<CG>(tfull0 + 8 * buf);
                 ++acc;
-                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            if (lane == 0) {
-                tc_commit_local<CG>(smem_addr(drain));
+            __syncwarp();
+            // all MMAs issued here have finished once `drain` completes
+            if (elect_one()) {
+                tc_commit_local<CG>(drain);
                 const volatile int never = 0;
-                if (!wait_bounded(smem_addr(drain), 0, &never, args.timeout_ns))
-                    raise_abort(abort_flag);
+                if (!wait_bounded(drain, 0, &never, args.timeout_ns)) raise_abort(abort_flag);
             }
             aborted = !ok;
         }
         __syncwarp();
     } else if (warp >= 2 + kEpiWarps) {
-        // ------------------------------------------------- gather warps 6-7
+        // ---------------------------------------- gather warps (the last two)
         // They follow the producer's stages and issue the parts of a stage
         // that come by row number: one thread each, the numbers in shared
         // memory.  The producer, which has waited for the stage and counted
@@ -544,22 +539,22 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         // barrier of that stage; it cannot tell it again before the bytes have
         // arrived, so one parity bit per stage is enough.
         const int half = warp - (2 + kEpiWarps);
-        int *const mine = numbers + half * 64;  // 64 row numbers of this warp
+        int *const mine = numbers + half * 128;  // 64 row numbers of A, then 64 of B
+        const uint32_t go = go0 + 8 * half * kMaxStages;
         int stage = 0;
         uint32_t told = 0;  // parity of the next word on each stage
-        int ok = 1;
-        // rows quads * 4 of `mine`, 64 columns from c0 on, to dst
-        auto gather = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, int quads, uint32_t fb) {
-#pragma unroll 4
+        bool ok = true;
+        // 4 * quads rows (numbers from `from` on), 64 columns from c0 on, to dst
+        auto gather = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, const int *from,
+                          int quads, uint32_t fb) {
             for (int q = 0; q < quads; ++q) {
-                const int4 r = *reinterpret_cast<const int4 *>(mine + q * 4);
-                tma_gather4<CG>(dst + q * 512, map, c0, r.x, r.y, r.z, r.w, fb);
+                const int4 r = *reinterpret_cast<const int4 *>(from + q * 4);
+                if (elect_one()) tma_gather4<CG>(dst + q * 512, map, c0, r.x, r.y, r.z, r.w, fb);
             }
         };
         bool reverse = false;
         for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
             const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
-            const int b_blocks = b_rows / 64;
             const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
             int quads = 0;  // rows mode: this warp's quads of the tile
             int kb = 0;
@@ -573,14 +568,12 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     mine[r] = r < rows ? __ldg(args.row_index + m0 + half * 64 + r) : -1;
                 }
                 __syncwarp();
-                kb = CG == 1 ? static_cast<int>((w * 5u) % static_cast<uint32_t>(t.nkb))
-                             : (reverse ? t.nkb - 1 : 0);
+                kb = first_block<CG>(w, t.nkb, reverse);
             }
             for (int i = 0; i < t.nkb; ++i) {
-                const uint32_t fb_local = smem_addr(&full[stage]);
-                const uint32_t fb = CG == 1 ? fb_local : map_to_rank(fb_local, 0);
-                const uint32_t sa = ring_base + stage * stage_bytes, sb = sa + a_region;
-                bool work = true, part = false;
+                const uint32_t fb = count0 + 8 * stage;
+                const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                bool work = quads > 0, part = false;
                 if constexpr (MODE == kWgrad) {
                     const int32_t r0 = t.first + i * BK;
                     const int rem = t.last - r0 < BK ? t.last - r0 : BK;
@@ -592,62 +585,69 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const int r = lane + j * 32;
-                            mine[r] = r >= rem ? -1
-                                      : GATHER ? __ldg(args.row_index + r0 + r)
-                                               : static_cast<int>(r0 + r);
+                            const int own = r >= rem ? -1 : static_cast<int>(r0 + r);
+                            mine[64 + r] = own;
+                            mine[r] = GATHER && own >= 0 ? __ldg(args.row_index + own) : own;
                         }
                         __syncwarp();
                     }
                 }
-                if (work && quads > 0 && lane == 0) {
-                    ok = wait_bounded(smem_addr(&go[half * kMaxStages + stage]), (told >> stage) & 1u,
-                                      abort_flag, args.timeout_ns);
+                if (work) {
+                    ok = wait_all(go + 8 * stage, (told >> stage) & 1u);
+                    if (!ok) break;
                     told ^= 1u << stage;
-                    if (ok) {
-                        if constexpr (MODE == kWgrad) {
-                            gather(sa + half * 8192, &map_a_part, m0 + half * 64, quads, fb);
-                            if (part) {
-                                // B's rows go by their own numbers
-                                if constexpr (GATHER) {
-                                    const int32_t r0 = t.first + i * BK;
-                                    for (int r = 0; r < quads * 4; ++r)
-                                        mine[r] = r0 + r < t.last ? r0 + r : -1;
-                                }
-                                for (int j = half; j < b_blocks; j += kGatherWarps)
-                                    gather(sb + j * 8192, &map_b_part, b0 + 64 * j, quads, fb);
-                            }
-                        } else {
-                            gather(sa + half * 64 * 128, &map_a_part, kb * BK, quads, fb);
-                        }
+                    if constexpr (MODE == kWgrad) {
+                        gather(sa + half * 8192, &map_a_rows, m0 + half * 64, mine, quads, fb);
+                        if (part)
+                            for (int j = half; j < b_rows / 64; j += kGatherWarps)
+                                gather(sb + j * 8192, &map_b_rows, b0 + 64 * j, mine + 64, quads, fb);
                     } else {
-                        raise_abort(abort_flag);
+                        for (int u = 0; u < ksub; ++u)
+                            gather(sa + (u * args.am + half * 64) * 128, &map_a_rows,
+                                   (kb * ksub + u) * BK, mine, quads, fb);
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                if constexpr (MODE != kWgrad)
-                    kb = CG == 2 && reverse ? kb - 1 : (kb + 1 == t.nkb ? 0 : kb + 1);
+                if constexpr (MODE != kWgrad) kb = next_block<CG>(kb, t.nkb, reverse);
                 if (++stage == stages) stage = 0;
             }
         }
         __syncwarp();
     } else {
-        // ---------------------------------------------- epilogue warps 2-5
-        const int quarter = warp % 4;  // TMEM lanes this warp may access
+        // -------------------------------------------------- epilogue warps
+        // Two per quarter of the TMEM lanes; each takes every other block of
+        // 32 columns.  C of a block is loaded while the one before it is
+        // stored (the first while the tile is still summed).
+        const int e = warp - 2, quarter = warp % 4, half = e / 4;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t acc = 0;
         if (late) pdl_wait();
         for (uint32_t w = first_tile; tiles.get(w, t); w += tile_step) {
             const bool empty_sum = MODE == kWgrad && t.nkb == 0;
-            const int buf = static_cast<int>(acc & 1);
+            const uint32_t buf = acc & 1;
+            int nrows = t.m_valid - static_cast<int>(rank) * BM - quarter * 32;
+            nrows = nrows < 0 ? 0 : (nrows > 32 ? 32 : nrows);
+            const int64_t row0 = t.m0 + rank * BM + quarter * 32;
+            const int64_t rest = args.N - t.n0;
+            const int ncols = rest < args.bn ? static_cast<int>(rest) : args.bn;
+            const int n_chunks = nrows > 0 ? (ncols + 31) / 32 : 0;
+            // this warp's last block (-1: it has none)
+            const int last = n_chunks > half ? half + ((n_chunks - 1 - half) / 2) * 2 : -1;
+            OutArgs o = args.out;
+            if constexpr (MODE != kWgrad) {
+                if (o.bias != nullptr) o.bias += t.g * args.N;
+            } else {
+                o.D = static_cast<uint8_t *>(o.D) + t.g * args.stride_d * (o.out == kOutF32 ? 4 : 2);
+                if (o.beta != 0.f) o.C += t.g * args.stride_c;
+            }
+            const bool use_c = MODE == kWgrad && o.beta != 0.f;
+            float c[32];
+            auto load_c = [&](int chunk) {
+                if (use_c && lane < nrows && direct_block(o, ncols - chunk * 32 < 32 ? 0 : 32))
+                    load_c_row(o, row0 + lane, t.n0 + chunk * 32, c);
+            };
+            if (last >= 0) load_c(half);
             if (!empty_sum) {
-                int ok = 1;
-                if (lane == 0)
-                    ok = wait_bounded(smem_addr(&tfull[buf]), (acc >> 1) & 1, abort_flag,
-                                      args.timeout_ns);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) {
-                    if (lane == 0) raise_abort(abort_flag);
+                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
                     aborted = true;
                     break;
                 }
@@ -658,42 +658,16 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t te = smem_addr(&tempty[buf]);
                     if constexpr (CG == 1)
-                        mbar_arrive(te);
+                        mbar_arrive(tempty0 + 8 * buf);
                     else
-                        mbar_arrive_cluster(map_to_rank(te, 0));
+                        mbar_arrive_cluster(map_to_rank(tempty0 + 8 * buf, 0));
                 }
             };
-            int nrows = t.m_valid - static_cast<int>(rank) * BM - quarter * 32;
-            nrows = nrows < 0 ? 0 : (nrows > 32 ? 32 : nrows);
-            const int64_t row0 = t.m0 + rank * BM + quarter * 32;
-            const int64_t rest = args.N - t.n0;
-            const int ncols = rest < args.bn ? static_cast<int>(rest) : args.bn;
-            const int n_chunks = nrows > 0 ? (ncols + 31) / 32 : 0;
-            OutArgs o = args.out;
-            if constexpr (MODE != kWgrad) {
-                if (o.bias != nullptr) o.bias += t.g * args.N;
-            } else {
-                o.D = static_cast<uint8_t *>(o.D) + t.g * args.stride_d * (o.out == kOutF32 ? 4 : 2);
-                if (o.beta != 0.f) o.C += t.g * args.stride_c;
-            }
-            const uint32_t t_acc = tmem_base + lane_off + static_cast<uint32_t>(buf * 256);
-            const bool use_c = MODE == kWgrad && o.beta != 0.f;
-            float c_next[32];
-            auto next_c = [&](int chunk) {  // this lane's C of the chunk, one chunk ahead
-                if (use_c && lane < nrows && direct_block(o, ncols - chunk * 32 < 32 ? 0 : 32))
-                    load_c_row(o, row0 + lane, t.n0 + chunk * 32, c_next);
-            };
-            if (n_chunks > 0) next_c(0);
+            const uint32_t t_acc = tmem_base + lane_off + buf * 256;
 #pragma unroll 1
-            for (int chunk = 0; chunk < n_chunks; ++chunk) {
-                float c[32], v[32];
-                if (use_c) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) c[j] = c_next[j];
-                    if (chunk + 1 < n_chunks) next_c(chunk + 1);
-                }
+            for (int chunk = half; chunk < n_chunks; chunk += 2) {
+                float v[32];
                 if (empty_sum) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -701,7 +675,7 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     uint32_t raw[32];
                     __syncwarp();
                     tmem_load_32cols(t_acc + chunk * 32, raw);
-                    if (chunk == n_chunks - 1) release_acc();
+                    if (chunk == last) release_acc();
                     if constexpr (MODE == kLora) {
                         // A slot's LB meets zeros of V in the rows of other
                         // adapters; where it holds infinities or NaNs those
@@ -732,10 +706,18 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
                 }
                 const int left = ncols - chunk * 32;
-                emit_block(v, c, o, row0, nrows, t.n0 + chunk * 32, left < 32 ? left : 32);
+                const int width = left < 32 ? left : 32;
+                const int64_t c0 = t.n0 + chunk * 32;
+                if (direct_block(o, width)) {
+                    finish_direct<MODE == kWgrad>(v, c, o, c0);
+                    if (chunk + 2 < n_chunks) load_c(chunk + 2);
+                    store_direct(v, o, row0, nrows, c0);
+                } else {
+                    store_transposed(v, o, row0, nrows, c0, width);
+                }
                 __syncwarp();
             }
-            if (n_chunks == 0 && !empty_sum) release_acc();
+            if (last < 0 && !empty_sum) release_acc();
         }
         __syncwarp();
     }
@@ -839,15 +821,26 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // rows of A and the CTA's rows of B, as many as fit.  With am < 128 the MMA's
 // 128-row A operand runs on into B and the next stages: stale rows, which
 // reach only accumulator rows that are not stored.  The last stage keeps 128
-// rows inside the ring.
-void set_tile(Args &a, int cg, int am, int bn) {
+// rows inside the ring.  ksub blocks of 64 of K share a stage (see sub_blocks).
+void set_tile(Args &a, int cg, int am, int bn, int ksub = 1) {
     a.am = am;
     a.bn = bn;
-    a.a_region = static_cast<uint32_t>(am) * BK * 2;
-    a.stage_bytes = a.a_region + static_cast<uint32_t>(bn / cg) * BK * 2;
+    a.ksub = ksub;
+    a.a_region = static_cast<uint32_t>(am * ksub) * BK * 2;
+    a.stage_bytes = a.a_region + static_cast<uint32_t>(bn / cg * ksub) * BK * 2;
     const int over = BM * BK * 2 - static_cast<int>(a.stage_bytes);
     const int fit = (kRingBytes - (over > 0 ? over : 0)) / static_cast<int>(a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
+}
+
+// Blocks of 64 of K per stage: a copy takes the producer about 100 ns to issue
+// whatever its size, so narrow tiles put up to four blocks into one stage (at
+// least 16 KiB of B).  The copies of K-major operands then count K in blocks
+// of 64, which needs K to be a multiple of 64.
+int sub_blocks(int64_t K, int bn) {
+    int ksub = 1;
+    while (ksub < 4 && bn * 128 * ksub < 16384) ksub *= 2;
+    return K % BK == 0 ? ksub : 1;
 }
 
 constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bit
@@ -880,7 +873,6 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
     a.out.act = p.act;
     a.out.out = p.out;
     a.out.row_vec = row_alignment(p.D, p.ldd, 0, p.out == kOutF32 ? 4 : 2);
-    a.num_kb = static_cast<int>(ceil_div(p.K, BK));
     a.b_kmajor = p.b_kmajor ? 1 : 0;
     a.ab_format = bf16 ? 1 : 0;
     a.timeout_ns = 1000ull * 1000ull * 1000ull;
@@ -898,20 +890,22 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
         const int64_t row_tiles = live * ceil_div(mean, am);
         int bn = 256;
         while (bn > 64 && row_tiles * ceil_div(p.N, bn) < 4 * d->sms) bn /= 2;
-        set_tile(a, 1, am, bn);
+        set_tile(a, 1, am, bn, sub_blocks(p.K, bn));
     }
+    a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
     const int cg = pair ? 2 : 1;
     const bool gather = p.row_index != nullptr;
     CUtensorMap maps[5];
-    bool ok = encode_stack(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, BM, 2) &&
-              encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, gather ? 1 : 16, 2);
+    bool ok = encode_kmajor(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, p.lda, a.am, a.ksub, 3) &&
+              encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, 1, 2);
     const int64_t count = one_b ? 1 : p.groups, stride = one_b ? p.ldb : p.stride_b;
     if (p.b_kmajor)
-        ok = ok && encode_stack(&maps[2], bf16, p.B, p.K, p.N, p.ldb, count, stride, BK,
-                                static_cast<uint32_t>(a.bn / cg), 3);
+        ok = ok && encode_kmajor(&maps[2], bf16, p.B, p.K, p.N, p.ldb, count, stride, a.bn / cg,
+                                 a.ksub, 4);
     else
-        ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64, BK, 3);
+        ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64,
+                                static_cast<uint32_t>(BK * a.ksub), 3);
     if (!ok) return cudaErrorInvalidValue;
     maps[3] = maps[4] = maps[2];
     const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
@@ -971,10 +965,17 @@ cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t strea
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
     CUtensorMap maps[5];
     const bool gather = p.row_index != nullptr;
+    // rows of whole 64-column blocks: one copy for all of a stage's blocks
+    const int b_blocks = a.bn / cg / 64;
+    a.a_wide = p.M % 64 == 0;
+    a.b_wide = p.N % 64 == 0;
     const bool ok =
-        encode_stack(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2) &&
+        (a.a_wide ? encode_blocks(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, p.lda, BK, 2, 3)
+                  : encode_stack(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2)) &&
         encode_stack(&maps[1], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, 1, 2) &&
-        encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2) &&
+        (a.b_wide ? encode_blocks(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, p.ldb, BK,
+                                  static_cast<uint32_t>(b_blocks), 3)
+                  : encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2)) &&
         encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
     if (!ok) return cudaErrorInvalidValue;
     maps[4] = maps[3];
@@ -1010,7 +1011,6 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
     a.out.out = p.out;
     const int64_t elt = p.out == kOutF32 ? 4 : 2;
     a.out.row_vec = row_alignment(p.D, p.ldd, 0, elt);
-    a.num_kb = static_cast<int>(ceil_div(p.K, BK));
     a.b_kmajor = p.w_kmajor ? 1 : 0;
     a.ab_format = bf16 ? 1 : 0;
     // 1 s per wait, longer where recomputing a tile's sums one by one could
@@ -1029,8 +1029,9 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         const int64_t per_row = d->sms / ceil_div(p.M, am) > 0 ? d->sms / ceil_div(p.M, am) : 1;
         int64_t bn = ceil_div(ceil_div(p.N, per_row), step) * step;
         if (bn > 256) bn = 256;
-        set_tile(a, 1, am, static_cast<int>(bn));
+        set_tile(a, 1, am, static_cast<int>(bn), sub_blocks(p.K, static_cast<int>(bn)));
     }
+    a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
     static const char *const kNames[2][2] = {{"lora_tc<f16>", "lora_tc<f16,pair>"},
                                              {"lora_tc<bf16>", "lora_tc<bf16,pair>"}};
@@ -1087,14 +1088,14 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
             a.late_wait = 1;
         }
         CUtensorMap maps[5];
-        bool ok = encode_stack(&maps[0], bf16, l.X, p.K, rows, p.ldx, 1, 0, BK, BM, 2) &&
-                  encode_stack(&maps[1], bf16, l.X, p.K, rows, p.ldx, 1, 0, BK, 16, 2);
+        bool ok = encode_kmajor(&maps[0], bf16, l.X, p.K, rows, p.ldx, 1, p.ldx, a.am, a.ksub, 3);
         if (p.w_kmajor)
-            ok = ok && encode_stack(&maps[2], bf16, p.W, p.K, p.N, p.ldw, 1, p.ldw, BK,
-                                    static_cast<uint32_t>(a.bn / cg), 3);
+            ok = ok && encode_kmajor(&maps[2], bf16, p.W, p.K, p.N, p.ldw, 1, p.ldw, a.bn / cg,
+                                     a.ksub, 4);
         else
-            ok = ok && encode_stack(&maps[2], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw, 64, BK, 3);
-        maps[3] = maps[4] = maps[2];
+            ok = ok && encode_stack(&maps[2], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw, 64,
+                                    static_cast<uint32_t>(BK * a.ksub), 3);
+        maps[1] = maps[3] = maps[4] = maps[2];
         if (p.adapters > 0) {
             const bool one_lb = p.adapters == 1 || p.stride_b == 0;
             const int64_t stride = one_lb ? p.ld_b : p.stride_b;
@@ -1109,7 +1110,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
                                         64, 16, 3);
             ok = ok && encode_stack(&maps[4], bf16, plan.V, plan.ldv,
                                     static_cast<int64_t>(a.tiles_m) * plan.tile_rows, plan.ldv, 1,
-                                    0, BK, 16, 2);
+                                    0, BK, static_cast<uint32_t>(a.am), 2);
         }
         if (!ok) {
             e = cudaErrorInvalidValue;

@@ -65,54 +65,52 @@ __device__ __forceinline__ void load_c_row(const OutArgs &a, int64_t row, int64_
     }
 }
 
-// The warp's block of D: rows row0 .. row0 + nrows - 1 (nrows <= 32), columns
-// c0 .. c0 + width - 1 (width <= 32); o holds lane l's row row0 + l of the
-// accumulator, c (used when beta != 0 and the block is `direct`) its row of C.
+// GELU in its tanh form, x / (1 + exp(-2 u)) with u = sqrt(2/pi) (x + 0.044715 x^3):
+// 0.5 (1 + tanh u) is the logistic function of 2 u.  The fast exponential and
+// division are off by a few units of 2^-22, a quarter of a BF16 ulp's 2^-13.
+__device__ __forceinline__ float activate(float x, int act) {
+    if (act == kActGelu) {
+        const float u = 0.7978845608028654f * fmaf(0.044715f * x, x * x, x);
+        return __fdividef(x, 1.f + __expf(-2.f * u));
+    }
+    return apply_activation(x, act);
+}
+
+// A block is 32 rows of D from row0 on (nrows of them inside) and 32 columns
+// from c0 on (width inside); v holds lane l's accumulators of row row0 + l.
 // Whole blocks with aligned rows go straight from registers, each lane its own
-// row (whole 32-byte sectors); others are transposed first, so that each store
+// row (whole 32-byte sectors); others are transposed first, so that a store
 // instruction writes consecutive columns of one row.
 __device__ __forceinline__ bool direct_block(const OutArgs &a, int width) {
     return width == 32 && a.row_vec >= 16;
 }
 
-__device__ __forceinline__ void emit_block(float (&o)[32], const float (&c)[32], const OutArgs &a,
-                                           int64_t row0, int nrows, int64_t c0, int width) {
-    const int lane = threadIdx.x % 32;
-    if (!direct_block(a, width)) {
-        transpose_32x32(o);  // o[i] = row row0 + i, this lane's column
-        if (lane >= width) return;
-        const float b = a.bias != nullptr ? a.bias[c0 + lane] : 0.f;
-        int64_t at = row0 * a.ldd + c0 + lane;
-        const float *cp = a.beta != 0.f ? a.C + row0 * a.ldc + c0 + lane : nullptr;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i < nrows) {
-                float v = o[i] * a.alpha + b;
-                if (a.beta != 0.f) v = fmaf(a.beta, *cp, v);
-                store_out(a.D, at, apply_activation(v, a.act), a.out);
-            }
-            at += a.ldd;
-            if (a.beta != 0.f) cp += a.ldc;
-        }
-        return;
-    }
-    if (a.bias != nullptr) {
-        const float mine = a.bias[c0 + lane];
+// v = act(alpha v + bias + beta c); c is this lane's row of C.
+template <bool WITH_C>
+__device__ __forceinline__ void finish_direct(float (&v)[32], const float (&c)[32],
+                                              const OutArgs &a, int64_t c0) {
+    if (!WITH_C && a.bias != nullptr) {
+        const float mine = a.bias[c0 + threadIdx.x % 32];
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            o[j] = fmaf(o[j], a.alpha, __shfl_sync(0xffffffffu, mine, j));
+            v[j] = fmaf(v[j], a.alpha, __shfl_sync(0xffffffffu, mine, j));
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] *= a.alpha;
+        for (int j = 0; j < 32; ++j) v[j] *= a.alpha;
     }
-    if (a.beta != 0.f) {
+    if (WITH_C && a.beta != 0.f) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = fmaf(a.beta, c[j], o[j]);
+        for (int j = 0; j < 32; ++j) v[j] = fmaf(a.beta, c[j], v[j]);
     }
-    if (a.act != kActNone) {
+    if (!WITH_C && a.act != kActNone) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = apply_activation(o[j], a.act);
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], a.act);
     }
+}
+
+__device__ __forceinline__ void store_direct(const float (&v)[32], const OutArgs &a, int64_t row0,
+                                             int nrows, int64_t c0) {
+    const int lane = threadIdx.x % 32;
     if (lane >= nrows) return;
     const int64_t at = (row0 + lane) * a.ldd + c0;
     if (a.out == kOutF32) {
@@ -120,21 +118,21 @@ __device__ __forceinline__ void emit_block(float (&o)[32], const float (&c)[32],
         if (a.row_vec >= 32) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                st_global_v8(d + q * 8, __float_as_uint(o[q * 8 + 0]), __float_as_uint(o[q * 8 + 1]),
-                             __float_as_uint(o[q * 8 + 2]), __float_as_uint(o[q * 8 + 3]),
-                             __float_as_uint(o[q * 8 + 4]), __float_as_uint(o[q * 8 + 5]),
-                             __float_as_uint(o[q * 8 + 6]), __float_as_uint(o[q * 8 + 7]));
+                st_global_v8(d + q * 8, __float_as_uint(v[q * 8 + 0]), __float_as_uint(v[q * 8 + 1]),
+                             __float_as_uint(v[q * 8 + 2]), __float_as_uint(v[q * 8 + 3]),
+                             __float_as_uint(v[q * 8 + 4]), __float_as_uint(v[q * 8 + 5]),
+                             __float_as_uint(v[q * 8 + 6]), __float_as_uint(v[q * 8 + 7]));
         } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                st_global_v4(d + q * 4, __float_as_uint(o[q * 4 + 0]), __float_as_uint(o[q * 4 + 1]),
-                             __float_as_uint(o[q * 4 + 2]), __float_as_uint(o[q * 4 + 3]));
+                st_global_v4(d + q * 4, __float_as_uint(v[q * 4 + 0]), __float_as_uint(v[q * 4 + 1]),
+                             __float_as_uint(v[q * 4 + 2]), __float_as_uint(v[q * 4 + 3]));
         }
     } else {
         uint16_t *d = static_cast<uint16_t *>(a.D) + at;
         uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack_16(o[2 * j], o[2 * j + 1], a.out);
+        for (int j = 0; j < 16; ++j) w[j] = pack_16(v[2 * j], v[2 * j + 1], a.out);
         if (a.row_vec >= 32) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -145,6 +143,37 @@ __device__ __forceinline__ void emit_block(float (&o)[32], const float (&c)[32],
             for (int q = 0; q < 4; ++q)
                 st_global_v4(d + q * 8, w[q * 4 + 0], w[q * 4 + 1], w[q * 4 + 2], w[q * 4 + 3]);
         }
+    }
+}
+
+__device__ __forceinline__ void store_transposed(float (&v)[32], const OutArgs &a, int64_t row0,
+                                                 int nrows, int64_t c0, int width) {
+    const int lane = threadIdx.x % 32;
+    transpose_32x32(v);  // v[i] = row row0 + i, this lane's column
+    if (lane >= width) return;
+    const float b = a.bias != nullptr ? a.bias[c0 + lane] : 0.f;
+    const bool use_c = a.beta != 0.f;
+    const float *cp = use_c ? a.C + row0 * a.ldc + c0 + lane : nullptr;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] = fmaf(v[i], a.alpha, b);
+        if (use_c) {
+            if (i < nrows) v[i] = fmaf(a.beta, *cp, v[i]);
+            cp += a.ldc;
+        }
+        v[i] = activate(v[i], a.act);
+    }
+    const int64_t at = row0 * a.ldd + c0 + lane;
+    if (a.out == kOutF32) {
+        float *d = static_cast<float *>(a.D) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, d += a.ldd)
+            if (i < nrows) *d = v[i];
+    } else {
+        uint16_t *d = static_cast<uint16_t *>(a.D) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, d += a.ldd)
+            if (i < nrows) *d = static_cast<uint16_t>(pack_16(v[i], 0.f, a.out));
     }
 }
 

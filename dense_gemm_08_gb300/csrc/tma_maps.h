@@ -44,6 +44,48 @@ inline bool encode_stack(CUtensorMap *map, bool bf16, const void *base, int64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same stack seen as blocks of 64 values of a row: a box is box_outer rows
+// of box_blocks consecutive blocks, block after block.  Coordinates: 0, row,
+// block, matrix (rank 3: without the matrix).  `inner` must be a multiple of 64.
+inline bool encode_blocks(CUtensorMap *map, bool bf16, const void *base, int64_t inner,
+                          int64_t outer, int64_t ld, int64_t count, int64_t stride,
+                          uint32_t box_outer, uint32_t box_blocks, int rank) {
+    const auto fn = tensor_map_encoder();
+    if (fn == nullptr || inner % 64 != 0) return false;
+    cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(outer), static_cast<cuuint64_t>(inner / 64),
+                          static_cast<cuuint64_t>(count)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128,
+                             static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[4] = {64, box_outer, box_blocks, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A stack of K-major operands (rows of K values).  blocks = 1: boxes of box_rows
+// rows of one block of 64, coordinates k, row, 0, matrix; more: encode_blocks.
+inline bool encode_kmajor(CUtensorMap *map, bool bf16, const void *base, int64_t K, int64_t rows,
+                          int64_t ld, int64_t count, int64_t stride, int box_rows, int blocks,
+                          int rank) {
+    if (blocks > 1)
+        return encode_blocks(map, bf16, base, K, rows, ld, count, stride,
+                             static_cast<uint32_t>(box_rows), static_cast<uint32_t>(blocks), rank);
+    const auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows), 1,
+                          static_cast<cuuint64_t>(count)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2,
+                             static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // What TMA asks of a matrix: 16-byte aligned base, row pitch (and matrix
 // pitch) of whole 16 bytes and below 2^40 bytes.
 inline bool tma_rows(const void *p, int64_t ld, int64_t stride = 0) {
