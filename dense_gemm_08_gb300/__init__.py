@@ -84,6 +84,8 @@ class GemmError(RuntimeError):
 def library() -> ctypes.CDLL:
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -450,81 +452,117 @@ def gemm(A, B, C=None, alpha=1.0, beta=0.0, out=None, stream=None):
 
 
 # ------------------------------------------------- torch helpers, grouped
+# These run once per layer and token, beside kernels of a few microseconds, so
+# they read each tensor attribute once and go straight to the C entry point.
 def stack_order(t):
     """(order, ld, stride) of a stack of matrices (3-D tensor), from its strides."""
     if t.dim() != 3:
         raise ValueError("expected a 3-D tensor (a stack of matrices)")
-    if t.shape[0] > 1 and t.stride(0) < 0:
-        raise ValueError("negative strides are not supported")
-    if t.shape[0] == 0:
-        return ROW_MAJOR, max(t.shape[2], 1), 0
-    order, ld = storage_order(t[0])
-    return order, ld, t.stride(0) if t.shape[0] > 1 else 0
+    n, r, q = t.shape
+    s0, s1, s2 = t.stride()
+    stride = s0 if n > 1 else 0
+    if s2 == 1 and (s1 >= q or r <= 1):
+        return ROW_MAJOR, max(s1, q, 1), stride
+    if s1 == 1 and (s2 >= r or q <= 1):
+        return COL_MAJOR, max(s2, r, 1), stride
+    raise ValueError(f"tensor with strides {t.stride()} is neither row- nor column-major")
 
 
 def _row_major(t, what):
-    order, ld = storage_order(t)
-    if order != ROW_MAJOR and t.shape[0] > 1:
-        raise ValueError(f"{what} must be row-major")
-    return max(ld, t.shape[1], 1)
+    """Leading dimension of a row-major matrix."""
+    r, q = t.shape
+    s0, s1 = t.stride()
+    if (s1 == 1 or q <= 1) and (s0 >= q or r <= 1):
+        return max(s0, q, 1)
+    raise ValueError(f"{what} must be row-major")
 
 
 def _int_vector(t, n, what, device):
-    import torch
-    if t.dtype != torch.int32:
+    """Address of a contiguous int32 vector of n."""
+    if t.dtype is not _torch().int32:
         raise TypeError(f"{what} must be int32")
     if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous vector of {n}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}")
+    return t.data_ptr()
 
 
 def _f32_dense(t, shape, what, device):
-    import torch
-    if t.dtype != torch.float32:
+    """Address of a contiguous float32 tensor of this shape (None: None)."""
+    if t is None:
+        return None
+    if t.dtype is not _torch().float32:
         raise TypeError(f"{what} must be float32")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with shape {tuple(shape)}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with shape {shape}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}")
+    return t.data_ptr()
 
 
-_SUFFIX = {"torch.float32": "f32", "torch.bfloat16": "bf16_f32acc", "torch.float16": "f16_f32acc"}
-_D_TYPE = {"torch.float32": GEMM_D_F32, "torch.bfloat16": GEMM_D_BF16, "torch.float16": GEMM_D_F16}
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _stream_of(stream):
+    if stream is not None:
+        return _stream(stream)
+    c = _torch()._C  # torch.cuda.current_stream().cuda_stream without its Python objects
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _types(A, B, out, out_dtype, default):
-    """(entry point suffix, output dtype, d_type); A and B share a dtype, D is FP32 or that dtype."""
-    if A.dtype != B.dtype:
+    """(entry point suffix, output dtype, d_type, device); A and B share a dtype, D is FP32 or that."""
+    torch = _torch()
+    dtype = A.dtype
+    if B.dtype is not dtype:
         raise TypeError("the operands must share a dtype")
-    if A.device != B.device:
+    device = A.device
+    if B.device != device:
         raise ValueError("the operands must share a device")
-    suffix = _SUFFIX.get(str(A.dtype))
-    if suffix is None:
+    if dtype is torch.bfloat16:
+        suffix, same = "bf16_f32acc", GEMM_D_BF16
+    elif dtype is torch.float16:
+        suffix, same = "f16_f32acc", GEMM_D_F16
+    elif dtype is torch.float32:
+        suffix, same = "f32", GEMM_D_F32
+    else:
         raise TypeError("the operands must be float32, bfloat16 or float16")
     if out is not None:
-        if out_dtype is not None and out.dtype != out_dtype:
+        if out_dtype is not None and out.dtype is not out_dtype:
             raise TypeError("out must have out_dtype")
-        if out.device != A.device:
+        if out.device != device:
             raise ValueError("out must be on the operands' device")
         out_dtype = out.dtype
     elif out_dtype is None:
-        out_dtype = default
-    d_type = _D_TYPE.get(str(out_dtype))
-    if d_type is None or (d_type != GEMM_D_F32 and out_dtype != A.dtype):
-        raise TypeError("the output must be float32 or the operands' dtype")
-    return suffix, out_dtype, d_type
+        out_dtype = default or dtype
+    if out_dtype is dtype:
+        return suffix, out_dtype, same, device
+    if out_dtype is torch.float32:
+        return suffix, out_dtype, GEMM_D_F32, device
+    raise TypeError("the output must be float32 or the operands' dtype")
 
 
 def group_rows(ids, groups, stream=None):
     """(offsets, order, position) of rows grouped by the int32 numbers `ids` (gemm_group_rows)."""
-    import torch
-    _int_vector(ids, ids.numel(), "ids", ids.device)
-    n = ids.numel()
-    offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
-    order = torch.empty(n, dtype=torch.int32, device=ids.device)
-    position = torch.empty(n, dtype=torch.int32, device=ids.device)
-    gemm_group_rows(n, groups, ids, offsets, order, position, stream)
+    torch = _torch()
+    device, n = ids.device, ids.numel()
+    at = _int_vector(ids, n, "ids", device)
+    # one allocation: order, position, offsets
+    buf = torch.empty(2 * n + groups + 1, dtype=torch.int32, device=device)
+    order, position, offsets = buf.split((n, n, groups + 1))
+    p = buf.data_ptr()
+    st = library().gemm_group_rows(n, groups, at, p + 8 * n, p, p + 4 * n, _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_group_rows")
     return offsets, order, position
 
 
@@ -538,26 +576,32 @@ def gemm_grouped(A, B, offsets, row_index=None, bias=None, activation=GEMM_ACT_N
     the rows of A (one per row of D).  D is float32 or the operands' dtype
     (the default).  Rows of D outside every group are left as they are.
     """
-    import torch
-    suffix, out_dtype, d_type = _types(A, B, out, out_dtype, A.dtype)
+    suffix, out_dtype, d_type, device = _types(A, B, out, out_dtype, None)
+    order_b, ldb, stride_b = stack_order(B)
     groups, K, N = B.shape
     if A.dim() != 2 or A.shape[1] != K:
         raise ValueError("inner dimensions differ")
-    rows = A.shape[0] if row_index is None else row_index.shape[0]
+    rows_a = rows = A.shape[0]
     lda = _row_major(A, "A")
-    order_b, ldb, stride_b = stack_order(B)
-    _int_vector(offsets, groups + 1, "offsets", A.device)
+    index = None
     if row_index is not None:
-        _int_vector(row_index, rows, "row_index", A.device)
-    if bias is not None:
-        _f32_dense(bias, (groups, N), "bias", A.device)
+        rows = row_index.shape[0]
+        index = _int_vector(row_index, rows, "row_index", device)
+    at = _int_vector(offsets, groups + 1, "offsets", device)
+    ep = Epilogue(_f32_dense(bias, (groups, N), "bias", device), activation, d_type)
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype, device=A.device)
-    elif tuple(out.shape) != (rows, N):
-        raise ValueError(f"out must be {rows} x {N}")
-    _call_grouped("gemm_grouped_" + suffix, groups, rows, N, K, alpha, A, lda, A.shape[0],
-                  row_index, offsets, B, ldb, stride_b, order_b, out, _row_major(out, "out"), bias,
-                  activation, d_type, stream, True)
+        out = _torch().empty((rows, N), dtype=out_dtype, device=device)
+        ldd = N
+    else:
+        if tuple(out.shape) != (rows, N):
+            raise ValueError(f"out must be {rows} x {N}")
+        ldd = _row_major(out, "out")
+    fn = "gemm_grouped_" + suffix
+    st = getattr(library(), fn)(groups, rows, N, K, alpha, A.data_ptr(), lda, rows_a, index, at,
+                                B.data_ptr(), ldb, stride_b, order_b, out.data_ptr(), ldd, ep,
+                                _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, fn)
     return out
 
 
@@ -569,16 +613,17 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
     for ``gemm_grouped``.  D is float32 (the default) or the operands' dtype, C
     float32.  Groups without rows give beta * C[g].
     """
-    import torch
-    suffix, out_dtype, d_type = _types(A, B, out, out_dtype, torch.float32)
+    torch = _torch()
+    suffix, out_dtype, d_type, device = _types(A, B, out, out_dtype, torch.float32)
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be matrices")
-    M, (rows, N), groups = A.shape[1], B.shape, offsets.shape[0] - 1
+    (rows_a, M), (rows, N), groups = A.shape, B.shape, offsets.shape[0] - 1
     lda, ldb = _row_major(A, "A"), _row_major(B, "B")
-    _int_vector(offsets, groups + 1, "offsets", A.device)
+    at = _int_vector(offsets, groups + 1, "offsets", device)
+    index = None
     if row_index is not None:
-        _int_vector(row_index, rows, "row_index", A.device)
-    elif A.shape[0] != rows:
+        index = _int_vector(row_index, rows, "row_index", device)
+    elif rows_a != rows:
         raise ValueError("A and B must have as many rows")
 
     def stack(t, what):
@@ -590,20 +635,26 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
         return max(ld, N, 1), stride
 
     if out is None:
-        out = torch.empty((groups, M, N), dtype=out_dtype, device=A.device)
-    ldd, stride_d = stack(out, "out")
-    ldc = stride_c = 0
+        out = torch.empty((groups, M, N), dtype=out_dtype, device=device)
+        ldd, stride_d = max(N, 1), M * N
+    else:
+        ldd, stride_d = stack(out, "out")
+    c, ldc, stride_c = None, 0, 0
     if beta != 0.0:
         if C is None:
             raise ValueError("beta != 0 needs C")
-        if C.dtype != torch.float32:
+        if C.dtype is not torch.float32:
             raise TypeError("C must be float32")
-        if C.device != A.device:
+        if C.device != device:
             raise ValueError("C must be on the operands' device")
         ldc, stride_c = stack(C, "C")
-    _call_wgrad("gemm_grouped_wgrad_" + suffix, groups, rows, M, N, alpha, A, lda, A.shape[0],
-                row_index, offsets, B, ldb, beta, C if beta != 0.0 else None, ldc, stride_c, out,
-                ldd, stride_d, d_type, stream, True)
+        c = C.data_ptr()
+    fn = "gemm_grouped_wgrad_" + suffix
+    st = getattr(library(), fn)(groups, rows, M, N, alpha, A.data_ptr(), lda, rows_a, index, at,
+                                B.data_ptr(), ldb, beta, c, ldc, stride_c, out.data_ptr(), ldd,
+                                stride_d, d_type, _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, fn)
     return out
 
 
@@ -617,35 +668,37 @@ def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GE
     adapter), scale float32 per adapter.  D is float32 or the operands' dtype
     (the default).
     """
-    import torch
-    suffix, out_dtype, d_type = _types(X, W, out, out_dtype, X.dtype)
+    suffix, out_dtype, d_type, device = _types(X, W, out, out_dtype, None)
     if suffix == "f32":
         raise TypeError("gemm_lora takes bfloat16 or float16")
-    for t in (LA, LB):
-        if t.dtype != X.dtype:
-            raise TypeError("the operands must share a dtype")
-        if t.device != X.device:
-            raise ValueError("the operands must share a device")
-    (M, K), N = X.shape, W.shape[1]
-    adapters, rank = LA.shape[0], LA.shape[2]
-    if W.shape[0] != K or LA.shape[1] != K:
+    if LA.dtype is not X.dtype or LB.dtype is not X.dtype:
+        raise TypeError("the operands must share a dtype")
+    if LA.device != device or LB.device != device:
+        raise ValueError("the operands must share a device")
+    order_a, ld_a, stride_a = stack_order(LA)
+    order_b, ld_b, stride_b = stack_order(LB)
+    (M, K), (kw, N), (adapters, ka, rank) = X.shape, W.shape, LA.shape
+    if kw != K or ka != K:
         raise ValueError("inner dimensions differ")
     if tuple(LB.shape) != (adapters, rank, N):
         raise ValueError(f"LB must be {adapters} x {rank} x {N}")
     ldx = _row_major(X, "X")
     order_w, ldw = storage_order(W)
-    order_a, ld_a, stride_a = stack_order(LA)
-    order_b, ld_b, stride_b = stack_order(LB)
-    _int_vector(adapter_of_row, M, "adapter_of_row", X.device)
-    if scale is not None:
-        _f32_dense(scale, (adapters,), "scale", X.device)
-    if bias is not None:
-        _f32_dense(bias, (N,), "bias", X.device)
+    ids = _int_vector(adapter_of_row, M, "adapter_of_row", device)
+    scales = _f32_dense(scale, (adapters,), "scale", device)
+    ep = Epilogue(_f32_dense(bias, (N,), "bias", device), activation, d_type)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-    elif tuple(out.shape) != (M, N):
-        raise ValueError(f"out must be {M} x {N}")
-    _call_lora("gemm_lora_" + suffix, M, N, K, X, ldx, W, ldw, order_w, adapters, rank,
-               adapter_of_row, scale, LA, ld_a, stride_a, order_a, LB, ld_b, stride_b, order_b,
-               out, _row_major(out, "out"), bias, activation, d_type, stream, True)
+        out = _torch().empty((M, N), dtype=out_dtype, device=device)
+        ldd = N
+    else:
+        if tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be {M} x {N}")
+        ldd = _row_major(out, "out")
+    fn = "gemm_lora_" + suffix
+    st = getattr(library(), fn)(M, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, order_w, adapters,
+                                rank, ids, scales, LA.data_ptr(), ld_a, stride_a, order_a,
+                                LB.data_ptr(), ld_b, stride_b, order_b, out.data_ptr(), ldd, ep,
+                                _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, fn)
     return out

@@ -46,10 +46,8 @@ constexpr int kMaxSlots = 256;         // lora: adapters of a tile
 constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kMaxSlots * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
-// Gathers are issued by warps of their own: a TMA gather takes its row numbers
-// from uniform registers, and one thread needs about 40 ns to issue it, so the
-// 32 gathers of a 16 KiB stage would keep a single warp busy for four times as
-// long as the MMAs of the stage (4096 x 14336, 16384 rows: 4.2 ms).
+// Gathers are issued by warps of their own, so that the producer goes on with
+// the copies of whole boxes.
 template <int MODE, bool GATHER>
 constexpr int threads() {
     return 64 + 32 * kEpiWarps + (GATHER || MODE == kWgrad ? 32 * kGatherWarps : 0);
@@ -734,6 +732,34 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
     if (warp == 1) tmem_dealloc<CG>(tmem_base);
 }
 
+// Rows of A in product order: out(r, :) = A(index[r], :), zeros for an index
+// outside A.  TMA fetches gathered rows one 128-byte line per 8 ns and SM, a
+// third of what the MMAs of a CTA pair take (8 experts, 16384 rows, 4096 ->
+// 14336: 3.1 ms gathered by TMA, 1.06 ms with the rows in order), so large
+// problems put the rows in order first: 200 MB of traffic, 30 us.
+__global__ void __launch_bounds__(256) order_rows_kernel(const uint16_t *A, int64_t lda,
+                                                         int64_t rows_a, const int32_t *index,
+                                                         int64_t rows, int64_t cols, uint16_t *out,
+                                                         int64_t ldo) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t quads = cols / 8;  // whole 16-byte pieces of a row
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int64_t from = index[r];
+        const bool inside = from >= 0 && from < rows_a;
+        const uint16_t *src = A + (inside ? from : 0) * lda;
+        uint16_t *dst = out + r * ldo;
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < quads; c += 256) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (inside) v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+            reinterpret_cast<uint4 *>(dst)[c] = v;
+        }
+        const int64_t c = quads * 8 + threadIdx.x;
+        if (c < cols) dst[c] = inside ? src[c] : static_cast<uint16_t>(0);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 constexpr int kMaxDevices = 64;
 
@@ -778,9 +804,8 @@ DeviceInfo *device_info() {
         if (d->err != cudaSuccess) return;
         d->sms = n > 0 ? n : 1;
         for (cudaError_t e : {allow_smem<1, kRows, false>(), allow_smem<1, kRows, true>(),
-                              allow_smem<2, kRows, false>(), allow_smem<2, kRows, true>(),
-                              allow_smem<1, kWgrad, false>(), allow_smem<1, kWgrad, true>(),
-                              allow_smem<2, kWgrad, false>(), allow_smem<2, kWgrad, true>(),
+                              allow_smem<2, kRows, false>(), allow_smem<1, kWgrad, false>(),
+                              allow_smem<1, kWgrad, true>(), allow_smem<2, kWgrad, false>(),
                               allow_smem<1, kLora, false>(), allow_smem<2, kLora, false>()})
             if (d->err == cudaSuccess) d->err = e;
         if (d->err != cudaSuccess) return;
@@ -803,7 +828,7 @@ cudaError_t launch(const CUtensorMap (&maps)[5], const Args &a, bool gather, int
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
     cudaLaunchAttribute attr[2];
-    if constexpr (MODE != kLora) {
+    if constexpr (MODE != kLora && CG == 1) {
         if (gather) {
             cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
             return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
@@ -847,6 +872,33 @@ constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bi
 
 }  // namespace
 
+// A launch's error, after the workspace (or null) is given back in stream order.
+static cudaError_t free_after(void *ws, cudaStream_t stream, cudaError_t e) {
+    if (ws == nullptr) return e;
+    const cudaError_t ef = workspace_free(ws, stream);
+    return e != cudaSuccess ? e : ef;
+}
+
+// Rows in product order in a workspace (order_rows_kernel); *ws to be freed.
+static cudaError_t order_rows(const void *A, int64_t lda, int64_t rows_a, const int32_t *index,
+                              int64_t rows, int64_t cols, int sms, cudaStream_t stream, void **ws,
+                              int64_t *ldo) {
+    *ldo = ceil_div(cols, 8) * 8;
+    cudaError_t e = workspace_alloc(static_cast<size_t>(rows * *ldo) * 2, stream, ws);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    set_pdl_attribute(&attr);
+    cudaLaunchConfig_t cfg = {};
+    const int64_t grid = rows < 8 * sms ? rows : 8 * sms;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, order_rows_kernel, static_cast<const uint16_t *>(A), lda, rows_a,
+                              index, rows, cols, static_cast<uint16_t *>(*ws), *ldo);
+}
+
 bool grouped_tc_eligible(const GroupedProblem &p) {
     return p.K > 0 && p.rows_a > 0 && tma_rows(p.A, p.lda) &&
            tma_rows(p.B, p.ldb, p.groups > 1 ? p.stride_b : 0) &&
@@ -854,8 +906,9 @@ bool grouped_tc_eligible(const GroupedProblem &p) {
                kMaxTiles;
 }
 
-cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t stream,
+cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream_t stream,
                               const char **name) {
+    GroupedProblem p = whole;
     const bool bf16 = in == InType::BF16;
     DeviceInfo *d = device_info();
     if (d == nullptr) return cudaErrorInvalidDevice;
@@ -895,9 +948,19 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
     const int cg = pair ? 2 : 1;
+    void *ws = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (pair && p.row_index != nullptr) {
+        int64_t ldo = 0;
+        e = order_rows(p.A, p.lda, p.rows_a, p.row_index, p.rows, p.K, d->sms, stream, &ws, &ldo);
+        p.A = ws;
+        p.lda = ldo;
+        p.rows_a = p.rows;
+        p.row_index = nullptr;
+    }
     const bool gather = p.row_index != nullptr;
     CUtensorMap maps[5];
-    bool ok = encode_kmajor(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, p.lda, a.am, a.ksub, 3) &&
+    bool ok = e == cudaSuccess && encode_kmajor(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, p.lda, a.am, a.ksub, 3) &&
               encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, 1, 2);
     const int64_t count = one_b ? 1 : p.groups, stride = one_b ? p.ldb : p.stride_b;
     if (p.b_kmajor)
@@ -906,14 +969,16 @@ cudaError_t launch_grouped_tc(const GroupedProblem &p, InType in, cudaStream_t s
     else
         ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64,
                                 static_cast<uint32_t>(BK * a.ksub), 3);
-    if (!ok) return cudaErrorInvalidValue;
     maps[3] = maps[4] = maps[2];
     const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
     static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
                                              {"grouped_tc<bf16>", "grouped_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];
-    return pair ? launch<2, kRows>(maps, a, gather, max_tiles, d, stream)
-                : launch<1, kRows>(maps, a, gather, max_tiles, d, stream);
+    if (e == cudaSuccess && !ok) e = cudaErrorInvalidValue;
+    if (e == cudaSuccess)
+        e = pair ? launch<2, kRows>(maps, a, gather, max_tiles, d, stream)
+                 : launch<1, kRows>(maps, a, gather, max_tiles, d, stream);
+    return free_after(ws, stream, e);
 }
 
 bool wgrad_tc_eligible(const WgradProblem &p) {
@@ -921,8 +986,9 @@ bool wgrad_tc_eligible(const WgradProblem &p) {
            ceil_div(p.M, BM) * ceil_div(p.N, 64) < kMaxTiles / p.groups;
 }
 
-cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t stream,
+cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t stream,
                             const char **name) {
+    WgradProblem p = whole;
     const bool bf16 = in == InType::BF16;
     DeviceInfo *d = device_info();
     if (d == nullptr) return cudaErrorInvalidDevice;
@@ -964,12 +1030,24 @@ cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t strea
     a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, BM * cg));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
     CUtensorMap maps[5];
+    void *ws = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (pair && p.row_index != nullptr) {
+        int64_t ldo = 0;
+        e = order_rows(p.A, p.lda, p.rows_a, p.row_index, p.rows, p.M, d->sms, stream, &ws, &ldo);
+        p.A = ws;
+        p.lda = ldo;
+        p.rows_a = p.rows;
+        p.row_index = nullptr;
+    }
+    a.row_index = p.row_index;
     const bool gather = p.row_index != nullptr;
     // rows of whole 64-column blocks: one copy for all of a stage's blocks
     const int b_blocks = a.bn / cg / 64;
     a.a_wide = p.M % 64 == 0;
     a.b_wide = p.N % 64 == 0;
     const bool ok =
+        e == cudaSuccess &&
         (a.a_wide ? encode_blocks(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, p.lda, BK, 2, 3)
                   : encode_stack(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2)) &&
         encode_stack(&maps[1], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, 1, 2) &&
@@ -977,14 +1055,16 @@ cudaError_t launch_wgrad_tc(const WgradProblem &p, InType in, cudaStream_t strea
                                   static_cast<uint32_t>(b_blocks), 3)
                   : encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2)) &&
         encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
-    if (!ok) return cudaErrorInvalidValue;
     maps[4] = maps[3];
     const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
     static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
                                              {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];
-    return pair ? launch<2, kWgrad>(maps, a, gather, max_tiles, d, stream)
-                : launch<1, kWgrad>(maps, a, gather, max_tiles, d, stream);
+    if (e == cudaSuccess && !ok) e = cudaErrorInvalidValue;
+    if (e == cudaSuccess)
+        e = pair ? launch<2, kWgrad>(maps, a, gather, max_tiles, d, stream)
+                 : launch<1, kWgrad>(maps, a, gather, max_tiles, d, stream);
+    return free_after(ws, stream, e);
 }
 
 bool lora_tc_eligible(const LoraProblem &p) {
@@ -1120,11 +1200,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         e = pair ? launch<2, kLora>(maps, a, false, tiles, d, stream)
                  : launch<1, kLora>(maps, a, false, tiles, d, stream);
     }
-    if (ws != nullptr) {
-        const cudaError_t ef = workspace_free(ws, stream);
-        if (e == cudaSuccess) e = ef;
-    }
-    return e;
+    return free_after(ws, stream, e);
 }
 
 cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status) {
