@@ -556,11 +556,12 @@ def group_rows(ids, groups, stream=None):
     torch = _torch()
     device, n = ids.device, ids.numel()
     at = _int_vector(ids, n, "ids", device)
-    # one allocation: order, position, offsets
-    buf = torch.empty(2 * n + groups + 1, dtype=torch.int32, device=device)
-    order, position, offsets = buf.split((n, n, groups + 1))
-    p = buf.data_ptr()
-    st = library().gemm_group_rows(n, groups, at, p + 8 * n, p, p + 4 * n, _stream_of(stream))
+    # (views of one allocation would cost the host more than three allocations)
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
+    order = torch.empty(n, dtype=torch.int32, device=device)
+    position = torch.empty(n, dtype=torch.int32, device=device)
+    st = library().gemm_group_rows(n, groups, at, offsets.data_ptr(), order.data_ptr(),
+                                   position.data_ptr(), _stream_of(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_group_rows")
     return offsets, order, position

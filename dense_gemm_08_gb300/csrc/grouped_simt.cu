@@ -1,9 +1,8 @@
 // grouped_simt.cu -- the grouped operators on the CUDA cores: FP32 inputs, and
 // 16-bit inputs whose rows TMA cannot describe.
 //
-// One kernel body for the three products; a CTA of 256 threads makes one 64 x
-// 64 tile of D from 16-deep slices staged in shared memory as FP32, each
-// thread a 4 x 4 block with FP32 FMAs (products of 16-bit values are exact):
+// One kernel body for the three products; a CTA of 128 threads makes one 64 x
+// 128 tile of D, each thread an 8 x 8 block:
 //   rows:   D(r, j) = act(alpha * sum_k A(idx(r), k) B_g(k, j) + bias_g(j)),
 //           r in group g; a tile never holds rows of two groups;
 //   wgrad:  D_g(i, j) = alpha * sum_{r in g} A(idx(r), i) B(r, j) + beta C_g(i, j);
@@ -11,12 +10,19 @@
 //   lora:   one group of M rows; the epilogue adds s_a * sum_c U(r, c) LB_a(c, j),
 //           with U = X LA (FP32, from lora_shrink_simt) and each row's own
 //           adapter, so no row ever reads another row's adapter.
+// Slices 16 deep in K go through shared memory as FP32, the next one loaded
+// into registers while the current one is multiplied.  The arithmetic is FP32
+// FMAs two rows at a time (fma.rn.f32x2, each half rounded as fmaf; products
+// of 16-bit values are exact): 32 of them per thread and step of K against 4
+// shared-memory loads, so the FMA pipe is the bound (80.5 TFLOP/s).  64 rows
+// per tile rather than 128: groups are small where FP32 is used, and a tile's
+// rows past the group's end are lost work.
 #include "grouped.cuh"
 
 namespace gemm {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16, THREADS = 256;
+constexpr int TM = 64, TN = 128, TK = 16, THREADS = 128;
 
 template <typename T>
 __device__ __forceinline__ float widened(const T *p);
@@ -33,6 +39,44 @@ __device__ __forceinline__ float widened<__half>(const __half *p) {
     return __half2float(*p);
 }
 
+__device__ __forceinline__ float to_float(uint16_t b) {
+    return __uint_as_float(static_cast<uint32_t>(b) << 16);
+}
+__device__ __forceinline__ float to_float(__half h) { return __half2float(h); }
+
+// Four consecutive values, of which the first `n` (<= 4) are read; zeros for
+// the rest.  `vec`: the address is aligned to all four.
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p, int64_t n, bool vec) {
+    if (n >= 4 && vec) {
+        if constexpr (sizeof(T) == 4) {
+            return __ldg(reinterpret_cast<const float4 *>(p));
+        } else {
+            alignas(8) T v[4];
+            *reinterpret_cast<uint2 *>(v) = __ldg(reinterpret_cast<const uint2 *>(p));
+            return make_float4(to_float(v[0]), to_float(v[1]), to_float(v[2]), to_float(v[3]));
+        }
+    }
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n > 0) f.x = widened<T>(p);
+    if (n > 1) f.y = widened<T>(p + 1);
+    if (n > 2) f.z = widened<T>(p + 2);
+    if (n > 3) f.w = widened<T>(p + 3);
+    return f;
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
 enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
 
 struct SimtGroupedArgs {
@@ -41,11 +85,13 @@ struct SimtGroupedArgs {
     LoraProblem l;     // kLora
     const float *U;    // kLora: M x rank
     uint32_t tiles_n, tiles_m;
+    bool vec_a, vec_b;  // rows of A and B start on four values
+    bool vec_d;         // rows of an FP32 D (and C) start on 16 bytes
 };
 
 template <typename T, int MODE>
 __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGroupedArgs a) {
-    __shared__ float As[TK][TM + 4], Bs[TK][TN + 4];
+    __shared__ alignas(16) float As[2][TK][TM + 4], Bs[2][TK][TN + 4];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -81,108 +127,197 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
     const int64_t ldb = MODE == kWgrad ? a.w.ldb : a.g.ldb;
     const int32_t *row_index = MODE == kWgrad ? a.w.row_index : a.g.row_index;
     const int64_t rows_a = MODE == kWgrad ? a.w.rows_a : a.g.rows_a;
+    const bool b_kmajor = MODE != kWgrad && a.g.b_kmajor;
 
-    // rows / lora: this thread stages A(row0 + tid / 4, 4 (tid % 4) ..)
-    int64_t my_row = -1;
+    // Quads of four values: A 2 and B 4 per thread and slice.
+    //   K-contiguous: quad i is row i / 4, values 4 (i % 4) of the slice's 16
+    //   else:         quad i is step i / (width / 4) of K, columns 4 (i % ..)
+    int64_t a_row[2];
     if constexpr (MODE != kWgrad) {
-        const int64_t r = m0 + tid / 4;
-        if (r < m_end) {
-            my_row = row_index != nullptr ? row_index[r] : r;
-            if (my_row < 0 || my_row >= rows_a) my_row = -1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t r = m0 + (tid + q * THREADS) / 4;
+            a_row[q] = -1;
+            if (r < m_end) {
+                a_row[q] = row_index != nullptr ? row_index[r] : r;
+                if (a_row[q] < 0 || a_row[q] >= rows_a) a_row[q] = -1;
+            }
         }
     }
-    float acc[4][4] = {};
-    const int tx = tid % 16, ty = tid / 16;
-    for (int64_t k0 = k_begin; k0 < k_end; k0 += TK) {
+    float4 a_next[2], b_next[4];
+    auto fetch = [&](int64_t k0) {
         if constexpr (MODE == kWgrad) {
-            const int64_t r = k0 + tid / 16;
-            int64_t ar = -1;
-            if (r < k_end) {
-                ar = row_index != nullptr ? row_index[r] : r;
-                if (ar < 0 || ar >= rows_a) ar = -1;
-            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t m = m0 + (tid % 16) * 4 + i, n = n0 + (tid % 16) * 4 + i;
-                As[tid / 16][(tid % 16) * 4 + i] =
-                    ar >= 0 && m < m_end ? widened<T>(A + ar * lda + m) : 0.f;
-                Bs[tid / 16][(tid % 16) * 4 + i] =
-                    r < k_end && n < n_end ? widened<T>(B + r * ldb + n) : 0.f;
+            for (int q = 0; q < 2; ++q) {
+                const int i = tid + q * THREADS;
+                const int64_t r = k0 + i / 16, m = m0 + (i % 16) * 4;
+                int64_t from = -1;
+                if (r < k_end) {
+                    from = row_index != nullptr ? row_index[r] : r;
+                    if (from < 0 || from >= rows_a) from = -1;
+                }
+                a_next[q] = load4(A + (from >= 0 ? from * lda + m : 0), from >= 0 ? m_end - m : 0, a.vec_a);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t k = k0 + (tid % 4) * 4 + i;
-                As[(tid % 4) * 4 + i][tid / 4] =
-                    my_row >= 0 && k < k_end ? widened<T>(A + my_row * lda + k) : 0.f;
-            }
-            if (a.g.b_kmajor) {
-                const int64_t n = n0 + tid / 4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t k = k0 + (tid % 4) * 4 + i;
-                    Bs[(tid % 4) * 4 + i][tid / 4] =
-                        n < n_end && k < k_end ? widened<T>(B + n * ldb + k) : 0.f;
-                }
-            } else {
-                const int64_t k = k0 + tid / 16;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t n = n0 + (tid % 16) * 4 + i;
-                    Bs[tid / 16][(tid % 16) * 4 + i] =
-                        n < n_end && k < k_end ? widened<T>(B + k * ldb + n) : 0.f;
-                }
+            for (int q = 0; q < 2; ++q) {
+                const int64_t k = k0 + (tid % 4) * 4;
+                a_next[q] = load4(A + (a_row[q] >= 0 ? a_row[q] * lda + k : 0),
+                                  a_row[q] >= 0 ? k_end - k : 0, a.vec_a);
             }
         }
-        __syncthreads();
+        if (b_kmajor) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t n = n0 + (tid + q * THREADS) / 4, k = k0 + (tid % 4) * 4;
+                b_next[q] = load4(B + (n < n_end ? n * ldb + k : 0), n < n_end ? k_end - k : 0, a.vec_b);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = tid + q * THREADS;
+                const int64_t k = k0 + i / 32, n = n0 + (i % 32) * 4;
+                b_next[q] = load4(B + (k < k_end ? k * ldb + n : 0), k < k_end ? n_end - n : 0, a.vec_b);
+            }
+        }
+    };
+    auto put = [&](int s) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int i = tid + q * THREADS;
+            if constexpr (MODE == kWgrad) {
+                *reinterpret_cast<float4 *>(&As[s][i / 16][(i % 16) * 4]) = a_next[q];
+            } else {
+                const int r = i / 4, k = (i % 4) * 4;
+                As[s][k + 0][r] = a_next[q].x;
+                As[s][k + 1][r] = a_next[q].y;
+                As[s][k + 2][r] = a_next[q].z;
+                As[s][k + 3][r] = a_next[q].w;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = tid + q * THREADS;
+            if (b_kmajor) {
+                const int n = i / 4, k = (i % 4) * 4;
+                Bs[s][k + 0][n] = b_next[q].x;
+                Bs[s][k + 1][n] = b_next[q].y;
+                Bs[s][k + 2][n] = b_next[q].z;
+                Bs[s][k + 3][n] = b_next[q].w;
+            } else {
+                *reinterpret_cast<float4 *>(&Bs[s][i / 32][(i % 32) * 4]) = b_next[q];
+            }
+        }
+    };
+
+    // rows ty * 8 .. + 7 in pairs; columns tx * 4 .. + 3 and 64 + tx * 4 .. + 3
+    const int tx = tid % 16, ty = tid / 16;
+    uint64_t acc[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0;
+    if (k_begin < k_end) {
+        fetch(k_begin);
+        put(0);
+    }
+    __syncthreads();
+    int s = 0;
+    for (int64_t k0 = k_begin; k0 < k_end; k0 += TK) {
+        const bool more = k0 + TK < k_end;
+        if (more) fetch(k0 + TK);
 #pragma unroll
         for (int k = 0; k < TK; ++k) {
-            float av[4], bv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) av[i] = As[k][ty * 4 + i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bv[j] = Bs[k][tx * 4 + j];
+            uint64_t av[4], bv[8];
+            const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][ty * 8]);
+            const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][ty * 8 + 4]);
+            av[0] = a0.x, av[1] = a0.y, av[2] = a1.x, av[3] = a1.y;
+            const float4 b0 = *reinterpret_cast<const float4 *>(&Bs[s][k][tx * 4]);
+            const float4 b1 = *reinterpret_cast<const float4 *>(&Bs[s][k][64 + tx * 4]);
+            bv[0] = pair(b0.x, b0.x), bv[1] = pair(b0.y, b0.y);
+            bv[2] = pair(b0.z, b0.z), bv[3] = pair(b0.w, b0.w);
+            bv[4] = pair(b1.x, b1.x), bv[5] = pair(b1.y, b1.y);
+            bv[6] = pair(b1.z, b1.z), bv[7] = pair(b1.w, b1.w);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+                for (int j = 0; j < 8; ++j) fma2(acc[i][j], av[i], bv[j]);
         }
+        if (more) put(s ^ 1);  // the other buffer was last read before the previous barrier
         __syncthreads();
+        s ^= 1;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = m0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = m0 + ty * 8 + i;
         if (r >= m_end) continue;
         int64_t adapter = -1;
         if constexpr (MODE == kLora) {
-            adapter = a.l.adapter[r];
+            if (a.l.adapters > 0) adapter = a.l.adapter[r];
             if (adapter >= a.l.adapters) adapter = -1;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx * 4 + j;
-            if (n >= n_end) continue;
-            float v = acc[i][j];
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n4 = n0 + h * 64 + tx * 4;
+            float o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                unpair(acc[i / 2][h * 4 + j], lo, hi);
+                o[j] = i % 2 ? hi : lo;
+            }
+            const bool whole = a.vec_d && n4 + 4 <= n_end;
             if constexpr (MODE == kWgrad) {
-                v *= a.w.alpha;
-                if (a.w.beta != 0.f)
-                    v = fmaf(a.w.beta, a.w.C[g * a.w.stride_c + r * a.w.ldc + n], v);
-                store_out(a.w.D, g * a.w.stride_d + r * a.w.ldd + n, v, a.w.out);
-            } else {
-                if constexpr (MODE == kLora) {
-                    if (adapter >= 0) {
-                        const T *lb = static_cast<const T *>(a.l.LB) + adapter * a.l.stride_b;
-                        const float *u = a.U + r * a.l.rank;
-                        float s = 0.f;
-                        for (int64_t c = 0; c < a.l.rank; ++c)
-                            s = fmaf(u[c], widened<T>(lb + (a.l.b_kmajor ? c + n * a.l.ld_b
-                                                                         : c * a.l.ld_b + n)), s);
-                        v += s;
+                const int64_t at = g * a.w.stride_d + r * a.w.ldd + n4;
+                const float *c = a.w.beta != 0.f ? a.w.C + g * a.w.stride_c + r * a.w.ldc + n4 : nullptr;
+                if (whole) {
+                    float4 v = make_float4(o[0] * a.w.alpha, o[1] * a.w.alpha, o[2] * a.w.alpha,
+                                           o[3] * a.w.alpha);
+                    if (c != nullptr) {
+                        const float4 cv = *reinterpret_cast<const float4 *>(c);
+                        v.x = fmaf(a.w.beta, cv.x, v.x), v.y = fmaf(a.w.beta, cv.y, v.y);
+                        v.z = fmaf(a.w.beta, cv.z, v.z), v.w = fmaf(a.w.beta, cv.w, v.w);
+                    }
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.w.D) + at) = v;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (n4 + j >= n_end) continue;
+                        float v = o[j] * a.w.alpha;
+                        if (c != nullptr) v = fmaf(a.w.beta, c[j], v);
+                        store_out(a.w.D, at + j, v, a.w.out);
                     }
                 }
-                v *= a.g.alpha;
-                if (a.g.bias != nullptr) v += a.g.bias[g * a.g.N + n];
-                store_out(a.g.D, r * a.g.ldd + n, apply_activation(v, a.g.act), a.g.out);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t n = n4 + j;
+                    if (n >= n_end) continue;
+                    float v = o[j];
+                    if constexpr (MODE == kLora) {
+                        if (adapter >= 0) {
+                            const T *lb = static_cast<const T *>(a.l.LB) + adapter * a.l.stride_b;
+                            const float *u = a.U + r * a.l.rank;
+                            float s2 = 0.f;
+                            for (int64_t c = 0; c < a.l.rank; ++c)
+                                s2 = fmaf(u[c], widened<T>(lb + (a.l.b_kmajor ? c + n * a.l.ld_b
+                                                                              : c * a.l.ld_b + n)), s2);
+                            v += s2;
+                        }
+                    }
+                    v *= a.g.alpha;
+                    if (a.g.bias != nullptr) v += a.g.bias[g * a.g.N + n];
+                    o[j] = apply_activation(v, a.g.act);
+                }
+                const int64_t at = r * a.g.ldd + n4;
+                if (whole) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.g.D) + at) =
+                        make_float4(o[0], o[1], o[2], o[3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n4 + j < n_end) store_out(a.g.D, at + j, o[j], a.g.out);
+                }
             }
         }
     }
@@ -190,8 +325,9 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
 
 // U(i, c) = s_a * sum_k X(i, k) LA_a(k, c), a = adapter[i]: one CTA per row,
 // one warp per column c, the lanes over k and a fixed shuffle tree.
+constexpr int kShrinkThreads = 256;
 template <typename T>
-__global__ void __launch_bounds__(THREADS) lora_shrink_simt_kernel(const LoraProblem p, float *U) {
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_simt_kernel(const LoraProblem p, float *U) {
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -201,7 +337,7 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_simt_kernel(const LoraPro
         const T *x = static_cast<const T *>(p.X) + i * p.ldx;
         const T *la = static_cast<const T *>(p.LA) + ad * p.stride_a;
         const float scale = p.scale != nullptr ? p.scale[ad] : 1.f;
-        for (int64_t c = warp; c < p.rank; c += THREADS / 32) {
+        for (int64_t c = warp; c < p.rank; c += kShrinkThreads / 32) {
             float s = 0.f;
             for (int64_t k = lane; k < p.K; k += 32)
                 s = fmaf(widened<T>(x + k),
@@ -238,6 +374,12 @@ cudaError_t launch_typed(const SimtGroupedArgs &a, InType in, int64_t grid, cuda
     return cudaErrorInvalidValue;
 }
 
+// Rows of a matrix (and the matrices of a stack) start on `bytes`.
+bool rows_on(const void *p, int64_t ld, int64_t stride, int64_t elt, int64_t bytes) {
+    return (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) % 16) | (ld * elt) | (stride * elt)) %
+               bytes == 0;
+}
+
 uint32_t tiles(int64_t n, int t) { return static_cast<uint32_t>((n + t - 1) / t); }
 
 const char *kNames[3][3] = {
@@ -253,6 +395,10 @@ cudaError_t launch_grouped_simt(const GroupedProblem &p, InType in, cudaStream_t
     SimtGroupedArgs a = {};
     a.g = p;
     a.tiles_n = tiles(p.N, TN);
+    const int64_t elt = in == InType::F32 ? 4 : 2;
+    a.vec_a = rows_on(p.A, p.lda, 0, elt, 4 * elt);
+    a.vec_b = rows_on(p.B, p.ldb, p.groups > 1 ? p.stride_b : 0, elt, 4 * elt);
+    a.vec_d = p.out == kOutF32 && rows_on(p.D, p.ldd, 0, 4, 16);
     // at most one partly filled row tile per group
     const int64_t row_tiles = p.rows / TM + (p.groups < p.rows ? p.groups : p.rows);
     return launch_typed<kRows>(a, in, row_tiles * a.tiles_n, stream);
@@ -265,6 +411,11 @@ cudaError_t launch_wgrad_simt(const WgradProblem &p, InType in, cudaStream_t str
     a.w = p;
     a.tiles_m = tiles(p.M, TM);
     a.tiles_n = tiles(p.N, TN);
+    const int64_t elt = in == InType::F32 ? 4 : 2;
+    a.vec_a = rows_on(p.A, p.lda, 0, elt, 4 * elt);
+    a.vec_b = rows_on(p.B, p.ldb, 0, elt, 4 * elt);
+    a.vec_d = p.out == kOutF32 && rows_on(p.D, p.ldd, p.groups > 1 ? p.stride_d : 0, 4, 16) &&
+              (p.beta == 0.f || rows_on(p.C, p.ldc, p.groups > 1 ? p.stride_c : 0, 4, 16));
     return launch_typed<kWgrad>(a, in, p.groups * a.tiles_m * a.tiles_n, stream);
 }
 
@@ -291,6 +442,9 @@ cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t strea
     g.act = p.act;
     g.out = p.out;
     a.tiles_n = tiles(p.N, TN);
+    a.vec_a = rows_on(p.X, p.ldx, 0, 2, 8);
+    a.vec_b = rows_on(p.W, p.ldw, 0, 2, 8);
+    a.vec_d = p.out == kOutF32 && rows_on(p.D, p.ldd, 0, 4, 16);
     void *u = nullptr;
     const bool any = p.adapters > 0 && p.rank > 0 && p.K > 0;
     cudaError_t e;
@@ -300,9 +454,9 @@ cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t strea
         a.U = static_cast<float *>(u);
         const unsigned grid = static_cast<unsigned>(p.M < 65536 ? p.M : 65536);
         if (in == InType::BF16)
-            lora_shrink_simt_kernel<uint16_t><<<grid, THREADS, 0, stream>>>(p, static_cast<float *>(u));
+            lora_shrink_simt_kernel<uint16_t><<<grid, kShrinkThreads, 0, stream>>>(p, static_cast<float *>(u));
         else
-            lora_shrink_simt_kernel<__half><<<grid, THREADS, 0, stream>>>(p, static_cast<float *>(u));
+            lora_shrink_simt_kernel<__half><<<grid, kShrinkThreads, 0, stream>>>(p, static_cast<float *>(u));
         e = cudaGetLastError();
     } else {
         a.l.adapters = 0;
