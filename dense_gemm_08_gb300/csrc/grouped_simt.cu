@@ -1,8 +1,8 @@
 // grouped_simt.cu -- the grouped operators on the CUDA cores: FP32 inputs, and
 // 16-bit inputs whose rows TMA cannot describe.
 //
-// One kernel body for the three products; a CTA of 128 threads makes one 64 x
-// 128 tile of D, each thread an 8 x 8 block:
+// One kernel body for the three products; a CTA of 256 threads makes one 64 x
+// 128 tile of D, each thread an 8 x 4 block:
 //   rows:   D(r, j) = act(alpha * sum_k A(idx(r), k) B_g(k, j) + bias_g(j)),
 //           r in group g; a tile never holds rows of two groups;
 //   wgrad:  D_g(i, j) = alpha * sum_{r in g} A(idx(r), i) B(r, j) + beta C_g(i, j);
@@ -13,16 +13,20 @@
 // Slices 16 deep in K go through shared memory as FP32, the next one loaded
 // into registers while the current one is multiplied.  The arithmetic is FP32
 // FMAs two rows at a time (fma.rn.f32x2, each half rounded as fmaf; products
-// of 16-bit values are exact): 32 of them per thread and step of K against 4
+// of 16-bit values are exact): 16 of them per thread and step of K against 3
 // shared-memory loads, so the FMA pipe is the bound (80.5 TFLOP/s).  64 rows
 // per tile rather than 128: groups are small where FP32 is used, and a tile's
-// rows past the group's end are lost work.
+// rows past the group's end are lost work.  8 x 4 per thread rather than 8 x 8:
+// with few tiles per SM the second set of warps hides more latency than the
+// larger block saves loads.
 #include "grouped.cuh"
 
 namespace gemm {
 namespace {
 
-constexpr int TM = 64, TN = 128, TK = 16, THREADS = 128;
+constexpr int TM = 64, TN = 128, TK = 32, THREADS = 256;
+constexpr int LA = TM + 4, LB = TN + 4;  // rows of a slice in shared memory
+constexpr int kSmemBytes = 2 * TK * (LA + LB) * 4;
 
 template <typename T>
 __device__ __forceinline__ float widened(const T *p);
@@ -87,38 +91,133 @@ struct SimtGroupedArgs {
     uint32_t tiles_n, tiles_m;
     bool vec_a, vec_b;  // rows of A and B start on four values
     bool vec_d;         // rows of an FP32 D (and C) start on 16 bytes
+    int ks;             // CTAs of a cluster, which share a tile's K
 };
+
+// 16 bytes of the same shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 load_from_rank(const float *p, uint32_t rank) {
+    uint32_t at;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sync_cluster() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Four columns of row r of D from n4 on: the sums o, then the epilogue.
+template <typename T, int MODE>
+__device__ __forceinline__ void finish_quad(const SimtGroupedArgs &a, int g, int64_t r, int64_t n4,
+                                            int64_t n_end, float4 sum) {
+    float o[4] = {sum.x, sum.y, sum.z, sum.w};
+    const bool whole = a.vec_d && n4 + 4 <= n_end;
+    if constexpr (MODE == kWgrad) {
+        const int64_t at = g * a.w.stride_d + r * a.w.ldd + n4;
+        const float *c = a.w.beta != 0.f ? a.w.C + g * a.w.stride_c + r * a.w.ldc + n4 : nullptr;
+        if (whole) {
+            float4 v = make_float4(o[0] * a.w.alpha, o[1] * a.w.alpha, o[2] * a.w.alpha,
+                                   o[3] * a.w.alpha);
+            if (c != nullptr) {
+                const float4 cv = *reinterpret_cast<const float4 *>(c);
+                v.x = fmaf(a.w.beta, cv.x, v.x), v.y = fmaf(a.w.beta, cv.y, v.y);
+                v.z = fmaf(a.w.beta, cv.z, v.z), v.w = fmaf(a.w.beta, cv.w, v.w);
+            }
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.w.D) + at) = v;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n4 + j >= n_end) continue;
+            float v = o[j] * a.w.alpha;
+            if (c != nullptr) v = fmaf(a.w.beta, c[j], v);
+            store_out(a.w.D, at + j, v, a.w.out);
+        }
+    } else {
+        int64_t adapter = -1;
+        if constexpr (MODE == kLora) {
+            if (a.l.adapters > 0) adapter = a.l.adapter[r];
+            if (adapter >= a.l.adapters) adapter = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t n = n4 + j;
+            if (n >= n_end) continue;
+            float v = o[j];
+            if constexpr (MODE == kLora) {
+                if (adapter >= 0) {
+                    const T *lb = static_cast<const T *>(a.l.LB) + adapter * a.l.stride_b;
+                    const float *u = a.U + r * a.l.rank;
+                    float s = 0.f;
+                    for (int64_t c = 0; c < a.l.rank; ++c)
+                        s = fmaf(u[c],
+                                 widened<T>(lb + (a.l.b_kmajor ? c + n * a.l.ld_b : c * a.l.ld_b + n)),
+                                 s);
+                    v += s;
+                }
+            }
+            v *= a.g.alpha;
+            if (a.g.bias != nullptr) v += a.g.bias[g * a.g.N + n];
+            o[j] = apply_activation(v, a.g.act);
+        }
+        const int64_t at = r * a.g.ldd + n4;
+        if (whole) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.g.D) + at) =
+                make_float4(o[0], o[1], o[2], o[3]);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n4 + j < n_end) store_out(a.g.D, at + j, o[j], a.g.out);
+    }
+}
 
 template <typename T, int MODE>
 __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGroupedArgs a) {
-    __shared__ alignas(16) float As[2][TK][TM + 4], Bs[2][TK][TN + 4];
+    extern __shared__ float4 smem4[];
+    float(*As)[TK][LA] = reinterpret_cast<float(*)[TK][LA]>(smem4);
+    float(*Bs)[TK][LB] = reinterpret_cast<float(*)[TK][LB]>(reinterpret_cast<float *>(smem4) + 2 * TK * LA);
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
+    // the CTAs of a cluster share a tile
+    const uint32_t tile = blockIdx.x / static_cast<uint32_t>(a.ks);
+    const uint32_t rank = blockIdx.x % static_cast<uint32_t>(a.ks);
     int g = 0;
     int32_t first = 0, last = 0;  // the group's rows
     uint32_t in_group = 0;
     if constexpr (MODE == kWgrad) {
         const uint32_t per = a.tiles_m * a.tiles_n;
-        g = static_cast<int>(blockIdx.x / per);
-        in_group = blockIdx.x % per;
+        g = static_cast<int>(tile / per);
+        in_group = tile % per;
         const int32_t lo = __ldg(a.w.offsets + g), hi = __ldg(a.w.offsets + g + 1);
         const int32_t rows = static_cast<int32_t>(a.w.rows);
         first = lo < 0 ? 0 : (lo > rows ? rows : lo);
         last = hi < first ? first : (hi > rows ? rows : hi);
     } else if constexpr (MODE == kRows) {
         GroupWalk walk(a.g.offsets, a.g.groups, a.g.rows, TM, a.tiles_n);
-        if (!walk.locate(blockIdx.x, g, first, last, in_group)) return;
+        if (!walk.locate(tile, g, first, last, in_group)) return;
     } else {
         last = static_cast<int32_t>(a.l.M);
-        in_group = blockIdx.x;
+        in_group = tile;
     }
     const int64_t tm = in_group / a.tiles_n, tn = in_group % a.tiles_n;
     const int64_t m0 = (MODE == kWgrad ? 0 : first) + tm * TM;  // first row of D in the tile
     const int64_t m_end = MODE == kWgrad ? a.w.M : last;
     const int64_t n0 = tn * TN, n_end = MODE == kWgrad ? a.w.N : a.g.N;
-    const int64_t k_begin = MODE == kWgrad ? first : 0;
-    const int64_t k_end = MODE == kWgrad ? last : a.g.K;
+    const int64_t k_first = MODE == kWgrad ? first : 0;
+    const int64_t k_last = MODE == kWgrad ? last : a.g.K;
+    const int64_t slices = (k_last - k_first + TK - 1) / TK;
+    const int64_t k_begin = k_first + slices * rank / a.ks * TK;
+    const int64_t k_stop = k_first + slices * (rank + 1) / a.ks * TK;
+    const int64_t k_end = k_stop < k_last ? k_stop : k_last;
 
     const T *A = static_cast<const T *>(MODE == kWgrad ? a.w.A : a.g.A);
     const T *B = static_cast<const T *>(MODE == kWgrad ? a.w.B : a.g.B) +
@@ -130,13 +229,13 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
     const bool b_kmajor = MODE != kWgrad && a.g.b_kmajor;
 
     // Quads of four values: A 2 and B 4 per thread and slice.
-    //   K-contiguous: quad i is row i / 4, values 4 (i % 4) of the slice's 16
+    //   K-contiguous: quad i is row i / 8, values 4 (i % 8) of the slice's 32
     //   else:         quad i is step i / (width / 4) of K, columns 4 (i % ..)
     int64_t a_row[2];
     if constexpr (MODE != kWgrad) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int64_t r = m0 + (tid + q * THREADS) / 4;
+            const int64_t r = m0 + (tid + q * THREADS) / 8;
             a_row[q] = -1;
             if (r < m_end) {
                 a_row[q] = row_index != nullptr ? row_index[r] : r;
@@ -161,7 +260,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t k = k0 + (tid % 4) * 4;
+                const int64_t k = k0 + (tid % 8) * 4;
                 a_next[q] = load4(A + (a_row[q] >= 0 ? a_row[q] * lda + k : 0),
                                   a_row[q] >= 0 ? k_end - k : 0, a.vec_a);
             }
@@ -169,7 +268,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         if (b_kmajor) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t n = n0 + (tid + q * THREADS) / 4, k = k0 + (tid % 4) * 4;
+                const int64_t n = n0 + (tid + q * THREADS) / 8, k = k0 + (tid % 8) * 4;
                 b_next[q] = load4(B + (n < n_end ? n * ldb + k : 0), n < n_end ? k_end - k : 0, a.vec_b);
             }
         } else {
@@ -188,7 +287,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
             if constexpr (MODE == kWgrad) {
                 *reinterpret_cast<float4 *>(&As[s][i / 16][(i % 16) * 4]) = a_next[q];
             } else {
-                const int r = i / 4, k = (i % 4) * 4;
+                const int r = i / 8, k = (i % 8) * 4;
                 As[s][k + 0][r] = a_next[q].x;
                 As[s][k + 1][r] = a_next[q].y;
                 As[s][k + 2][r] = a_next[q].z;
@@ -199,7 +298,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         for (int q = 0; q < 4; ++q) {
             const int i = tid + q * THREADS;
             if (b_kmajor) {
-                const int n = i / 4, k = (i % 4) * 4;
+                const int n = i / 8, k = (i % 8) * 4;
                 Bs[s][k + 0][n] = b_next[q].x;
                 Bs[s][k + 1][n] = b_next[q].y;
                 Bs[s][k + 2][n] = b_next[q].z;
@@ -210,13 +309,13 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         }
     };
 
-    // rows ty * 8 .. + 7 in pairs; columns tx * 4 .. + 3 and 64 + tx * 4 .. + 3
-    const int tx = tid % 16, ty = tid / 16;
-    uint64_t acc[4][8];
+    // rows ty * 8 .. + 7 in pairs; columns tx * 4 .. + 3
+    const int tx = tid % 32, ty = tid / 32;
+    uint64_t acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0;
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
     if (k_begin < k_end) {
         fetch(k_begin);
         put(0);
@@ -228,99 +327,59 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         if (more) fetch(k0 + TK);
 #pragma unroll
         for (int k = 0; k < TK; ++k) {
-            uint64_t av[4], bv[8];
+            uint64_t av[4], bv[4];
             const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][ty * 8]);
             const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][ty * 8 + 4]);
             av[0] = a0.x, av[1] = a0.y, av[2] = a1.x, av[3] = a1.y;
-            const float4 b0 = *reinterpret_cast<const float4 *>(&Bs[s][k][tx * 4]);
-            const float4 b1 = *reinterpret_cast<const float4 *>(&Bs[s][k][64 + tx * 4]);
-            bv[0] = pair(b0.x, b0.x), bv[1] = pair(b0.y, b0.y);
-            bv[2] = pair(b0.z, b0.z), bv[3] = pair(b0.w, b0.w);
-            bv[4] = pair(b1.x, b1.x), bv[5] = pair(b1.y, b1.y);
-            bv[6] = pair(b1.z, b1.z), bv[7] = pair(b1.w, b1.w);
+            const float4 b = *reinterpret_cast<const float4 *>(&Bs[s][k][tx * 4]);
+            bv[0] = pair(b.x, b.x), bv[1] = pair(b.y, b.y);
+            bv[2] = pair(b.z, b.z), bv[3] = pair(b.w, b.w);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) fma2(acc[i][j], av[i], bv[j]);
+                for (int j = 0; j < 4; ++j) fma2(acc[i][j], av[i], bv[j]);
         }
         if (more) put(s ^ 1);  // the other buffer was last read before the previous barrier
         __syncthreads();
         s ^= 1;
     }
+    auto sums = [&](int i) {  // row ty * 8 + i of the tile, this thread's columns
+        float o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = m0 + ty * 8 + i;
-        if (r >= m_end) continue;
-        int64_t adapter = -1;
-        if constexpr (MODE == kLora) {
-            if (a.l.adapters > 0) adapter = a.l.adapter[r];
-            if (adapter >= a.l.adapters) adapter = -1;
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            unpair(acc[i / 2][j], lo, hi);
+            o[j] = i % 2 ? hi : lo;
         }
+        return make_float4(o[0], o[1], o[2], o[3]);
+    };
+    const int64_t n4 = n0 + tx * 4;
+    if (a.ks == 1) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n4 = n0 + h * 64 + tx * 4;
-            float o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float lo, hi;
-                unpair(acc[i / 2][h * 4 + j], lo, hi);
-                o[j] = i % 2 ? hi : lo;
-            }
-            const bool whole = a.vec_d && n4 + 4 <= n_end;
-            if constexpr (MODE == kWgrad) {
-                const int64_t at = g * a.w.stride_d + r * a.w.ldd + n4;
-                const float *c = a.w.beta != 0.f ? a.w.C + g * a.w.stride_c + r * a.w.ldc + n4 : nullptr;
-                if (whole) {
-                    float4 v = make_float4(o[0] * a.w.alpha, o[1] * a.w.alpha, o[2] * a.w.alpha,
-                                           o[3] * a.w.alpha);
-                    if (c != nullptr) {
-                        const float4 cv = *reinterpret_cast<const float4 *>(c);
-                        v.x = fmaf(a.w.beta, cv.x, v.x), v.y = fmaf(a.w.beta, cv.y, v.y);
-                        v.z = fmaf(a.w.beta, cv.z, v.z), v.w = fmaf(a.w.beta, cv.w, v.w);
-                    }
-                    *reinterpret_cast<float4 *>(static_cast<float *>(a.w.D) + at) = v;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (n4 + j >= n_end) continue;
-                        float v = o[j] * a.w.alpha;
-                        if (c != nullptr) v = fmaf(a.w.beta, c[j], v);
-                        store_out(a.w.D, at + j, v, a.w.out);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t n = n4 + j;
-                    if (n >= n_end) continue;
-                    float v = o[j];
-                    if constexpr (MODE == kLora) {
-                        if (adapter >= 0) {
-                            const T *lb = static_cast<const T *>(a.l.LB) + adapter * a.l.stride_b;
-                            const float *u = a.U + r * a.l.rank;
-                            float s2 = 0.f;
-                            for (int64_t c = 0; c < a.l.rank; ++c)
-                                s2 = fmaf(u[c], widened<T>(lb + (a.l.b_kmajor ? c + n * a.l.ld_b
-                                                                              : c * a.l.ld_b + n)), s2);
-                            v += s2;
-                        }
-                    }
-                    v *= a.g.alpha;
-                    if (a.g.bias != nullptr) v += a.g.bias[g * a.g.N + n];
-                    o[j] = apply_activation(v, a.g.act);
-                }
-                const int64_t at = r * a.g.ldd + n4;
-                if (whole) {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(a.g.D) + at) =
-                        make_float4(o[0], o[1], o[2], o[3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (n4 + j < n_end) store_out(a.g.D, at + j, o[j], a.g.out);
-                }
-            }
-        }
+        for (int i = 0; i < 8; ++i)
+            if (m0 + ty * 8 + i < m_end)
+                finish_quad<T, MODE>(a, g, m0 + ty * 8 + i, n4, n_end, sums(i));
+        return;
     }
+    // the parts meet in the cluster's shared memory, each CTA adding a share of
+    // the rows in rank order (the slices are no longer needed)
+    float(*part)[LB] = reinterpret_cast<float(*)[LB]>(smem4);
+    static_assert(TM * LB * 4 <= kSmemBytes, "a tile of sums replaces the slices");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4 *>(&part[ty * 8 + i][tx * 4]) = sums(i);
+    sync_cluster();
+    for (int i = static_cast<int>(rank) * (TM / a.ks) + ty; i < (static_cast<int>(rank) + 1) * (TM / a.ks);
+         i += THREADS / 32) {
+        if (m0 + i >= m_end) break;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t c = 0; c < static_cast<uint32_t>(a.ks); ++c) {
+            const float4 v = load_from_rank(&part[i][tx * 4], c);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        finish_quad<T, MODE>(a, g, m0 + i, n4, n_end, sum);
+    }
+    sync_cluster();  // no CTA leaves while another reads its sums
 }
 
 // U(i, c) = s_a * sum_k X(i, k) LA_a(k, c), a = adapter[i]: one CTA per row,
@@ -353,14 +412,22 @@ template <int MODE, typename T>
 cudaError_t launch_as(const SimtGroupedArgs &a, int64_t grid, cudaStream_t stream) {
     if (grid <= 0) return cudaSuccess;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaLaunchAttribute attr;
-    set_pdl_attribute(&attr);
+    cudaLaunchAttribute attr[2];
+    set_pdl_attribute(&attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.ks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.ks > 1 ? 2 : 1;
+    const cudaError_t e = cudaFuncSetAttribute(grouped_simt_kernel<T, MODE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, grouped_simt_kernel<T, MODE>, a);
 }
 
@@ -378,6 +445,20 @@ cudaError_t launch_typed(const SimtGroupedArgs &a, InType in, int64_t grid, cuda
 bool rows_on(const void *p, int64_t ld, int64_t stride, int64_t elt, int64_t bytes) {
     return (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) % 16) | (ld * elt) | (stride * elt)) %
                bytes == 0;
+}
+
+// CTAs that share a tile's K: two CTAs are resident per SM, so a few tiles
+// more than 2 x SMs would take twice as long; up to 8 parts (each at least 128
+// of K) while there are fewer than 12 per SM.  (16 groups, 2000 rows, 1000 x
+// 1024, 320 tiles: 164 us in one part, see the launcher for the split.)
+int k_parts(int64_t tiles, int64_t k) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 1;
+    int ks = 1;
+    while (ks < 8 && tiles * ks < 6 * static_cast<int64_t>(sms) && k / (2 * ks) >= 128) ks *= 2;
+    return ks;
 }
 
 uint32_t tiles(int64_t n, int t) { return static_cast<uint32_t>((n + t - 1) / t); }
@@ -400,8 +481,11 @@ cudaError_t launch_grouped_simt(const GroupedProblem &p, InType in, cudaStream_t
     a.vec_b = rows_on(p.B, p.ldb, p.groups > 1 ? p.stride_b : 0, elt, 4 * elt);
     a.vec_d = p.out == kOutF32 && rows_on(p.D, p.ldd, 0, 4, 16);
     // at most one partly filled row tile per group
-    const int64_t row_tiles = p.rows / TM + (p.groups < p.rows ? p.groups : p.rows);
-    return launch_typed<kRows>(a, in, row_tiles * a.tiles_n, stream);
+    const int64_t live = p.groups < p.rows ? p.groups : p.rows;
+    const int64_t row_tiles = p.rows / TM + live;
+    // (the last tile of a group is half full on average)
+    a.ks = k_parts((p.rows / TM + live / 2) * a.tiles_n, p.K);
+    return launch_typed<kRows>(a, in, row_tiles * a.tiles_n * a.ks, stream);
 }
 
 cudaError_t launch_wgrad_simt(const WgradProblem &p, InType in, cudaStream_t stream,
@@ -416,7 +500,9 @@ cudaError_t launch_wgrad_simt(const WgradProblem &p, InType in, cudaStream_t str
     a.vec_b = rows_on(p.B, p.ldb, 0, elt, 4 * elt);
     a.vec_d = p.out == kOutF32 && rows_on(p.D, p.ldd, p.groups > 1 ? p.stride_d : 0, 4, 16) &&
               (p.beta == 0.f || rows_on(p.C, p.ldc, p.groups > 1 ? p.stride_c : 0, 4, 16));
-    return launch_typed<kWgrad>(a, in, p.groups * a.tiles_m * a.tiles_n, stream);
+    const int64_t all = p.groups * a.tiles_m * a.tiles_n;
+    a.ks = k_parts(all, p.rows / p.groups);
+    return launch_typed<kWgrad>(a, in, all * a.ks, stream);
 }
 
 cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t stream,
@@ -463,7 +549,11 @@ cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t strea
         e = cudaSuccess;
     }
     if (e == cudaSuccess)
-        e = launch_typed<kLora>(a, in, static_cast<int64_t>(tiles(p.M, TM)) * a.tiles_n, stream);
+        {
+        const int64_t all = static_cast<int64_t>(tiles(p.M, TM)) * a.tiles_n;
+        a.ks = k_parts(all, p.K);
+        e = launch_typed<kLora>(a, in, all * a.ks, stream);
+    }
     if (u != nullptr) {
         const cudaError_t ef = workspace_free(u, stream);
         if (e == cudaSuccess) e = ef;
