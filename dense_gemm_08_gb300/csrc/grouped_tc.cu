@@ -40,7 +40,7 @@ constexpr int kGroupM = 16;  // row tiles per band of the raster inside a group
 constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 2;
-constexpr int kRingBytes = 7 * 32768;  // all variants
+constexpr int kRingBytes = 7 * 32768;
 constexpr int kMaxSlots = 256;         // lora: adapters of a tile
 // ring + alignment + barriers + row numbers (gathers) or adapters (lora)
 constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kMaxSlots * 4;
@@ -335,35 +335,40 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
                     const uint32_t v_bytes = static_cast<uint32_t>(args.am) * 128u;
                     const uint32_t v_tx = v_bytes + (CG == 2 && cta_rows(t, 1) > 0 ? v_bytes : 0u);
-                    int slot = 0, in_slot = 0, j0 = 0;  // of the next slice
                     for (int c0 = 0; c0 < cols; c0 += BK) {
+                        const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                        // lane q: the adapter and first column of LA of slice q (the
+                        // rounding's remainders meet the same rows of LB again)
+                        int ad = 0, j0 = 0;
+                        if (lane < slices) {
+                            const int c = c0 + lane * 16, slot = c / pl.rc;
+                            ad = numbers[slot];
+                            j0 = (c - slot * pl.rc) & (pl.r_pad - 1);
+                        }
+                        int ads[4], j0s[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            ads[q] = __shfl_sync(0xffffffffu, ad, q);
+                            j0s[q] = __shfl_sync(0xffffffffu, j0, q);
+                        }
                         ok = wait_all(empty0 + 8 * stage, phase ^ 1);
                         if (!ok) break;
                         const uint32_t fb = count0 + 8 * stage;
                         const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
-                        const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
                         if (elect_one()) {
                             if (leader)
                                 mbar_arrive_expect_tx(full0 + 8 * stage, v_tx + CG * slices * slice_bytes);
                             if (mine > 0) tma_load_2d<CG>(sa, &map_v, c0, m0, fb);
-                        }
-                        for (int q = 0; q < slices; ++q) {
-                            const int32_t ad = numbers[slot];
-                            const uint32_t dst = sb + q * slice_bytes;
-                            if (elect_one()) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if (q >= slices) break;
+                                const uint32_t dst = sb + q * slice_bytes;
                                 if (args.l.b_kmajor) {
-                                    tma_load_3d<CG>(dst, &map_b_rows, j0, b0, ad, fb);
+                                    tma_load_3d<CG>(dst, &map_b_rows, j0s[q], b0, ads[q], fb);
                                 } else {
                                     for (int j = 0; j < b_rows; j += 64)
-                                        tma_load_3d<CG>(dst + j * 32, &map_b_rows, b0 + j, j0, ad, fb);
+                                        tma_load_3d<CG>(dst + j * 32, &map_b_rows, b0 + j, j0s[q], ads[q], fb);
                                 }
-                            }
-                            // (the rounding's remainders meet the same rows of LB again)
-                            in_slot += 16;
-                            j0 = j0 + 16 == pl.r_pad ? 0 : j0 + 16;
-                            if (in_slot == pl.rc) {
-                                in_slot = 0;
-                                ++slot;
                             }
                         }
                         advance();
@@ -743,20 +748,33 @@ __global__ void __launch_bounds__(256) order_rows_kernel(const uint16_t *A, int6
                                                          int64_t ldo) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t quads = cols / 8;  // whole 16-byte pieces of a row
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const int64_t from = index[r];
-        const bool inside = from >= 0 && from < rows_a;
-        const uint16_t *src = A + (inside ? from : 0) * lda;
-        uint16_t *dst = out + r * ldo;
-#pragma unroll 4
-        for (int64_t c = threadIdx.x; c < quads; c += 256) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (inside) v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-            reinterpret_cast<uint4 *>(dst)[c] = v;
+    // 16-byte pieces of all rows in order, four per thread and step
+    const int64_t per_row = (cols + 7) / 8, all = rows * per_row;
+    for (int64_t q0 = blockIdx.x * 1024ll + threadIdx.x; q0 < all; q0 += gridDim.x * 1024ll) {
+        uint4 v[4];
+        int64_t r[4], c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t q = q0 + i * 256;
+            r[i] = q < all ? q / per_row : -1;
+            c[i] = q - r[i] * per_row;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (r[i] < 0) continue;
+            const int64_t from = index[r[i]];
+            if (from < 0 || from >= rows_a) continue;
+            const uint16_t *src = A + from * lda + c[i] * 8;
+            if (c[i] * 8 + 8 <= cols) {
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            } else {  // the end of a row
+                uint32_t w[4] = {};
+                for (int k = 0; k < cols - c[i] * 8; ++k)
+                    w[k / 2] |= static_cast<uint32_t>(src[k]) << (k % 2 * 16);
+                v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
-        const int64_t c = quads * 8 + threadIdx.x;
-        if (c < cols) dst[c] = inside ? src[c] : static_cast<uint16_t>(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r[i] >= 0) *reinterpret_cast<uint4 *>(out + r[i] * ldo + c[i] * 8) = v[i];
     }
 }
 
@@ -889,7 +907,8 @@ static cudaError_t order_rows(const void *A, int64_t lda, int64_t rows_a, const 
     cudaLaunchAttribute attr;
     set_pdl_attribute(&attr);
     cudaLaunchConfig_t cfg = {};
-    const int64_t grid = rows < 8 * sms ? rows : 8 * sms;
+    const int64_t steps = ceil_div(rows * (*ldo / 8), 1024);
+    const int64_t grid = steps < 8 * sms ? steps : 8 * sms;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;

@@ -45,7 +45,8 @@ struct ShrinkArgs {
 };
 
 // The tile's distinct adapters: slot_of[i] for its n rows, list[s], and their
-// number.  All kThreads (>= the tile's rows) call; shared arrays.
+// number.  All kThreads (>= the tile's rows) call, with tile_id's result (the
+// adapter of row threadIdx.x, -1: none).
 struct TilePlan {
     int ids[kMaxTileRows];
     int slot_of[kMaxTileRows];
@@ -54,13 +55,17 @@ struct TilePlan {
     int count;
 };
 
-__device__ __forceinline__ void make_plan(const LoraProblem &p, int64_t row0, int n, TilePlan &t) {
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+__device__ __forceinline__ int tile_id(const LoraProblem &p, int64_t row0, int n) {
     int id = -1;
-    if (tid < n) {
-        id = p.adapter[row0 + tid];
+    if (static_cast<int>(threadIdx.x) < n) {
+        id = p.adapter[row0 + threadIdx.x];
         if (id < 0 || id >= p.adapters) id = -1;
     }
+    return id;
+}
+
+__device__ __forceinline__ void make_plan(int id, int n, TilePlan &t) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     t.ids[tid] = id;
     __syncthreads();
     int first = tid;  // the first row with this row's adapter
@@ -170,6 +175,9 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_rows_kernel(const Shrink
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int64_t id = p.adapter[row];
     const bool has = id >= 0 && id < p.adapters;
+    // (loaded here, used after the sums)
+    const int mine = rank == 0 ? tile_id(p, row0, n) : -1;
+    const float scale = has && p.scale != nullptr ? p.scale[id] : 1.f;
     const int r_cols = static_cast<int>(p.rank);
     if (has) {
         const uint16_t *x = static_cast<const uint16_t *>(p.X) + row * p.ldx;
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_rows_kernel(const Shrink
         }
     }
     // only the first CTA of the cluster goes on with the row
-    if (rank == 0) make_plan(p, row0, n, t);
+    if (rank == 0) make_plan(mine, n, t);
     __syncwarp();
     cluster_sync();  // every part is written
     if (rank == 0) {
@@ -266,10 +274,14 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_rows_kernel(const Shrink
             if (tid < count) a.plan.list[row0 + tid] = t.list[tid];
         }
         if (has && tid < r_cols) {
-            float sum = u[tid];
-            for (uint32_t c = 1; c < static_cast<uint32_t>(a.ks); ++c)
-                sum += load_from_rank(&u[tid], c);
-            part[0][tid] = sum * (p.scale != nullptr ? p.scale[id] : 1.f);
+            float v[kMaxCluster];
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)  // all in flight, then added in order
+                v[c] = c < a.ks ? load_from_rank(&u[tid], c) : 0.f;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) sum += v[c];
+            part[0][tid] = sum * scale;
         }
         __syncthreads();
         write_v_row(a, row, slot, count, part[0]);
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t tile = row_first / pl.tile_rows, row0 = tile * pl.tile_rows;
     const int n = static_cast<int>(p.M - row0 < pl.tile_rows ? p.M - row0 : pl.tile_rows);
     const int n_mine = static_cast<int>(p.M - row_first < BM ? p.M - row_first : BM);
-    make_plan(p, row0, n, t);
+    make_plan(tile_id(p, row0, n), n, t);
     const int off = static_cast<int>(row_first - row0);  // 0 or 128
     const int count = t.count;
     if (first_z && rank == 0) {
@@ -373,7 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring_base = smem_addr(ring);
     const uint32_t slot_bytes = static_cast<uint32_t>(pl.r_pad) * BK * 2;
     const int mn_block = pl.r_pad < 64 ? pl.r_pad : 64;  // rank-major LA: columns per TMA box
-    const int a_rows = n_mine > 64 ? BM : (n_mine + 15) / 16 * 16;  // a whole box, or parts of 16 rows
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -382,23 +393,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first_used = pass * per_pass;
         const int ns = all - first_used < per_pass ? all - first_used : per_pass;
         if (warp == 0) {
-            if (lane == 0) {
-                const uint32_t tx = static_cast<uint32_t>(a_rows) * 128u + ns * slot_bytes;
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    if (!wait_bounded(smem_addr(&empty[stage]), phase ^ 1, abort_flag, a.timeout_ns)) {
-                        raise_abort(abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_addr(&full[stage]);
-                    const uint32_t sa = ring_base + stage * kStageBytes, sb = sa + kStageA;
+            const uint32_t tx = kStageA + ns * slot_bytes;
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
+                ok = __all_sync(0xffffffffu, wait_bounded(smem_addr(&empty[stage]), phase ^ 1,
+                                                          abort_flag, a.timeout_ns));
+                if (!ok) break;
+                const uint32_t fb = smem_addr(&full[stage]);
+                const uint32_t sa = ring_base + stage * kStageBytes, sb = sa + kStageA;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(fb, tx);
-                    for (int j = 0; j < a_rows; j += 16)
-                        tma_load_2d<1>(sa + j * 128, &map_x, kb * BK,
-                                       static_cast<int32_t>(row_first) + j, fb);
-                    for (int s = 0; s < ns; ++s) {
-                        const int32_t ad = t.list[used[first_used + s]] * a.la_z_step;
-                        const uint32_t dst = sb + s * slot_bytes;
+                    tma_load_2d<1>(sa, &map_x, kb * BK, static_cast<int32_t>(row_first), fb);
+                }
+                for (int s = 0; s < ns; ++s) {
+                    const int32_t ad = t.list[used[first_used + s]] * a.la_z_step;
+                    const uint32_t dst = sb + s * slot_bytes;
+                    if (elect_one()) {
                         if (p.a_kmajor) {
                             tma_load_3d<1>(dst, &map_la, kb * BK, 0, ad, fb);
                         } else {
@@ -406,36 +415,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tma_load_3d<1>(dst + j * BK * 2, &map_la, j, kb * BK, ad, fb);
                         }
                     }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
+            if (!ok && lane == 0) raise_abort(abort_flag);
         } else if (warp == 1) {
-            if (lane == 0) {
-                const uint64_t a_desc0 = desc_kmajor(ring_base, 0);
-                const uint64_t a_step = (UMMA_K * 2) >> 4;
-                // K-major LA: the slots' rows follow one another, one MMA for
-                // all; rank-major: one MMA per slot, with the swizzle of its
-                // row length
-                const uint32_t sw = mn_block == 64 ? kSwizzle128 : (mn_block == 32 ? kSwizzle64 : kSwizzle32);
-                const uint32_t row_bytes = static_cast<uint32_t>(mn_block) * 2;
-                const uint64_t b_desc0 =
-                    p.a_kmajor ? desc_kmajor(ring_base + kStageA, 0)
-                               : smem_desc(ring_base + kStageA, BK * row_bytes, 8 * row_bytes, sw);
-                const uint64_t b_step = p.a_kmajor ? (UMMA_K * 2) >> 4 : (UMMA_K * row_bytes) >> 4;
-                const int n_mma = p.a_kmajor ? 1 : ns;
-                const uint32_t idesc = make_idesc(BM, p.a_kmajor ? ns * pl.r_pad : pl.r_pad, 0,
-                                                  !p.a_kmajor, a.ab_format);
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    if (!wait_bounded(smem_addr(&full[stage]), phase, abort_flag, a.timeout_ns)) {
-                        raise_abort(abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t st = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
+            const uint64_t a_desc0 = desc_kmajor(ring_base, 0);
+            const uint64_t a_step = (UMMA_K * 2) >> 4;
+            // K-major LA: the slots' rows follow one another, one MMA for all;
+            // rank-major: one MMA per slot, with the swizzle of its row length
+            const uint32_t sw = mn_block == 64 ? kSwizzle128 : (mn_block == 32 ? kSwizzle64 : kSwizzle32);
+            const uint32_t row_bytes = static_cast<uint32_t>(mn_block) * 2;
+            const uint64_t b_desc0 =
+                p.a_kmajor ? desc_kmajor(ring_base + kStageA, 0)
+                           : smem_desc(ring_base + kStageA, BK * row_bytes, 8 * row_bytes, sw);
+            const uint64_t b_step = p.a_kmajor ? (UMMA_K * 2) >> 4 : (UMMA_K * row_bytes) >> 4;
+            const int n_mma = p.a_kmajor ? 1 : ns;
+            const uint32_t idesc = make_idesc(BM, p.a_kmajor ? ns * pl.r_pad : pl.r_pad, 0,
+                                              !p.a_kmajor, a.ab_format);
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
+                ok = __all_sync(0xffffffffu, wait_bounded(smem_addr(&full[stage]), phase, abort_flag,
+                                                          a.timeout_ns));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t st = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
+                if (elect_one()) {
                     for (int s = 0; s < n_mma; ++s)
 #pragma unroll
                         for (int kk = 0; kk < BK / UMMA_K; ++kk)
@@ -444,13 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       b_desc0 + st + s * (slot_bytes >> 4) + kk * b_step, idesc,
                                       kb > kb_begin || kk > 0 ? 1u : 0u);
                     tc_commit<1>(smem_addr(&empty[stage]));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    if (kb + 1 == kb_end) tc_commit<1>(smem_addr(&done));
                 }
-                tc_commit<1>(smem_addr(&done));
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
+            if (!ok && lane == 0) raise_abort(abort_flag);
         }
         __syncwarp();
         // the sums are complete (every thread waits: TMEM is reused next pass)
@@ -590,15 +598,6 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (p.M <= kRowsMax) {
-        // at least 512 of K per CTA
-        const int64_t ks = p.K / 512;
-        a.ks = static_cast<int>(ks < 1 ? 1 : (ks > kMaxCluster ? kMaxCluster : ks));
-        attr[1].val.clusterDim.x = static_cast<unsigned>(a.ks);
-        cfg.gridDim = dim3(static_cast<unsigned>(p.M * a.ks), 1, 1);
-        return in == InType::BF16 ? cudaLaunchKernelEx(&cfg, lora_shrink_rows_kernel<1>, a)
-                                  : cudaLaunchKernelEx(&cfg, lora_shrink_rows_kernel<0>, a);
-    }
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -610,12 +609,22 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
             g_err[dev] = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
     });
     if (g_err[dev] != cudaSuccess) return g_err[dev];
+    if (p.M <= kRowsMax) {
+        // at least 512 of K per CTA (two loads of latency); the second product's
+        // CTAs start on each SM as these leave it
+        const int64_t ks = p.K / 512;
+        a.ks = static_cast<int>(ks < 1 ? 1 : (ks > kMaxCluster ? kMaxCluster : ks));
+        attr[1].val.clusterDim.x = static_cast<unsigned>(a.ks);
+        cfg.gridDim = dim3(static_cast<unsigned>(p.M * a.ks), 1, 1);
+        return in == InType::BF16 ? cudaLaunchKernelEx(&cfg, lora_shrink_rows_kernel<1>, a)
+                                  : cudaLaunchKernelEx(&cfg, lora_shrink_rows_kernel<0>, a);
+    }
     const bool bf16 = in == InType::BF16;
     const bool one = p.adapters == 1 || p.stride_a == 0;
     a.la_z_step = one ? 0 : 1;
     const int64_t count = one ? 1 : p.adapters, stride = one ? p.ld_a : p.stride_a;
     CUtensorMap map_x, map_la;
-    bool ok = encode_stack(&map_x, bf16, p.X, p.K, p.M, p.ldx, 1, 0, BK, 16, 2);
+    bool ok = encode_stack(&map_x, bf16, p.X, p.K, p.M, p.ldx, 1, 0, BK, BM, 2);
     if (p.a_kmajor)
         ok = ok && encode_stack(&map_la, bf16, p.LA, p.K, p.rank, p.ld_a, count, stride, BK,
                                 static_cast<uint32_t>(plan.r_pad), 3);
