@@ -46,6 +46,14 @@ constexpr int kMaxSlots = 256;         // lora: adapters of a tile
 constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kMaxSlots * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
+// wgrad, few rows per group: the tile's epilogue, not its K loop, is the time.
+// Each epilogue warp then has two boxes for C and one for D (32 x 32 FP32) at
+// the end of the ring's memory, filled and emptied by TMA: a block costs some
+// 60 instructions instead of about 500.  The ring keeps four stages.
+constexpr int kBoxBytes = kEpiWarps * 3 * 4096;
+constexpr int kStagedRing = 4 * 32768;
+static_assert(kStagedRing + kBoxBytes <= kRingBytes, "ring and boxes");
+
 // Gathers are issued by warps of their own, so that the producer goes on with
 // the copies of whole boxes.
 template <int MODE, bool GATHER>
@@ -62,6 +70,7 @@ struct Args {
     int num_kb;                 // rows, lora: K steps of a stage each
     int ksub;                   // rows, lora: blocks of 64 of K per stage
     int a_wide, b_wide;         // wgrad: whole 64-column blocks, several per copy
+    int staged;                 // wgrad: D and C move as TMA boxes (see kBoxBytes)
     int b_kmajor;               // rows
     int bn;                     // columns per tile (of the CTA or the pair)
     int am;                     // rows of D per CTA: 128, or 16 / 32 / 64 (single CTAs)
@@ -203,19 +212,23 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                       const __grid_constant__ CUtensorMap map_a_rows,
                       const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_b_rows,
-                      const __grid_constant__ CUtensorMap map_v, const Args args) {
+                      const __grid_constant__ CUtensorMap map_v,
+                      const __grid_constant__ CUtensorMap map_c,
+                      const __grid_constant__ CUtensorMap map_d, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     // barriers (8 bytes each): full[kMaxStages] TMA -> MMA (the leader's count
     // both CTAs), empty[kMaxStages] MMA -> TMA, tfull[2] MMA -> epilogue,
     // tempty[2] epilogue -> MMA (the leader's count both CTAs),
-    // go[kGatherWarps][kMaxStages] producer -> gather warp, drain
+    // go[kGatherWarps][kMaxStages] producer -> gather warp, drain,
+    // cbar[kEpiWarps][2] boxes of C loaded
     const uint32_t ring0 = smem_addr(ring);
     const uint32_t full0 = ring0 + kRingBytes, empty0 = full0 + 8 * kMaxStages;
     const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16;
     const uint32_t go0 = tempty0 + 16, drain = go0 + 8 * kGatherWarps * kMaxStages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + (drain + 8 - ring0));
+    const uint32_t cbar0 = drain + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + (cbar0 + 16 * kEpiWarps - ring0));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *numbers = reinterpret_cast<int *>(ring + kRingBytes + 1024);  // [kMaxSlots]
 
@@ -232,6 +245,7 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
             mbar_init(tempty0 + 8 * b, kEpiWarps * CG);
         }
         mbar_init(drain, 1);
+        for (int s = 0; s < 2 * kEpiWarps; ++s) mbar_init(cbar0 + 8 * s, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -240,6 +254,8 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         if (GATHER || MODE == kWgrad) prefetch_map(&map_a_rows);
         if (MODE != kRows) prefetch_map(&map_b_rows);
         if (MODE == kLora) prefetch_map(&map_v);
+        if (MODE == kWgrad && args.staged) prefetch_map(&map_d);
+        if (MODE == kWgrad && args.staged && args.out.beta != 0.f) prefetch_map(&map_c);
     }
     if (warp == 1) tmem_alloc<CG>(smem_addr(tmem_slot));
     tc_fence_before();
@@ -623,6 +639,7 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         const int e = warp - 2, quarter = warp % 4, half = e / 4;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t acc = 0;
+        uint32_t n_c = 0;  // staged: blocks of C fetched so far
         if (late) pdl_wait();
         for (uint32_t w = first_tile; tiles.get(w, t); w += tile_step) {
             const bool empty_sum = MODE == kWgrad && t.nkb == 0;
@@ -643,20 +660,7 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                 if (o.beta != 0.f) o.C += t.g * args.stride_c;
             }
             const bool use_c = MODE == kWgrad && o.beta != 0.f;
-            float c[32];
-            auto load_c = [&](int chunk) {
-                if (use_c && lane < nrows && direct_block(o, ncols - chunk * 32 < 32 ? 0 : 32))
-                    load_c_row(o, row0 + lane, t.n0 + chunk * 32, c);
-            };
-            if (last >= 0) load_c(half);
-            if (!empty_sum) {
-                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
-                    aborted = true;
-                    break;
-                }
-                tc_fence_after();
-                ++acc;
-            }
+            const uint32_t t_acc = tmem_base + lane_off + buf * 256;
             auto release_acc = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -667,7 +671,110 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                         mbar_arrive_cluster(map_to_rank(tempty0 + 8 * buf, 0));
                 }
             };
-            const uint32_t t_acc = tmem_base + lane_off + buf * 256;
+            if constexpr (MODE == kWgrad) {
+                if (args.staged) {
+                    const uint32_t d_box = ring0 + kStagedRing + e * 3 * 4096, c_boxes = d_box + 4096;
+                    const uint32_t cbar = cbar0 + 16 * e;
+                    // C of a block into box n_c % 2 (the block that used it last has been read)
+                    auto fetch_c = [&](int chunk) {
+                        if (use_c && elect_one()) {
+                            const uint32_t bar = cbar + 8 * (n_c & 1);
+                            mbar_arrive_expect_tx(bar, 4096);
+                            tma_load_3d<CG>(c_boxes + (n_c & 1) * 4096, &map_c,
+                                            static_cast<int32_t>(t.n0) + chunk * 32,
+                                            static_cast<int32_t>(row0), t.g,
+                                            CG == 1 ? bar : map_to_rank(bar, rank));
+                        }
+                        ++n_c;
+                    };
+                    if (last >= 0) fetch_c(half);
+                    if (!empty_sum) {
+                        if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
+                            aborted = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        ++acc;
+                    }
+                    bool stop = false;
+#pragma unroll 1
+                    for (int chunk = half; chunk < n_chunks; chunk += 2) {
+                        const uint32_t box = c_boxes + (n_c + 1) % 2 * 4096, bar = cbar + 8 * ((n_c + 1) % 2);
+                        const uint32_t parity = ((n_c - 1) >> 1) & 1;
+                        if (chunk + 2 < n_chunks) fetch_c(chunk + 2);
+                        uint32_t raw[32];
+                        if (empty_sum) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) raw[j] = 0;
+                        } else {
+                            __syncwarp();
+                            tmem_load_32cols(t_acc + chunk * 32, raw);
+                            if (chunk == last) release_acc();
+                        }
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = o.alpha * __uint_as_float(raw[j]);
+                        if (use_c) {
+                            if (!wait_all(bar, parity)) {
+                                stop = true;
+                                break;
+                            }
+                            const uint32_t row = box + lane * 128;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 cv = ld_shared_v4(row + ((q ^ (lane & 7)) << 4));
+                                v[q * 4 + 0] = fmaf(o.beta, cv.x, v[q * 4 + 0]);
+                                v[q * 4 + 1] = fmaf(o.beta, cv.y, v[q * 4 + 1]);
+                                v[q * 4 + 2] = fmaf(o.beta, cv.z, v[q * 4 + 2]);
+                                v[q * 4 + 3] = fmaf(o.beta, cv.w, v[q * 4 + 3]);
+                            }
+                        }
+                        if (elect_one()) bulk_wait_read();  // the last store has read its box
+                        __syncwarp();
+                        if (o.out == kOutF32) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                st_shared_v4(d_box + lane * 128 + ((q ^ (lane & 7)) << 4),
+                                             __float_as_uint(v[q * 4]), __float_as_uint(v[q * 4 + 1]),
+                                             __float_as_uint(v[q * 4 + 2]), __float_as_uint(v[q * 4 + 3]));
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                st_shared_v4(d_box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
+                                             pack_16(v[q * 8], v[q * 8 + 1], o.out),
+                                             pack_16(v[q * 8 + 2], v[q * 8 + 3], o.out),
+                                             pack_16(v[q * 8 + 4], v[q * 8 + 5], o.out),
+                                             pack_16(v[q * 8 + 6], v[q * 8 + 7], o.out));
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (elect_one())
+                            tma_store_3d(&map_d, static_cast<int32_t>(t.n0) + chunk * 32,
+                                         static_cast<int32_t>(row0), t.g, d_box);
+                    }
+                    if (stop) {
+                        aborted = true;
+                        break;
+                    }
+                    if (last < 0 && !empty_sum) release_acc();
+                    continue;
+                }
+            }
+            float c[32];
+            const bool quads = in_quads(o);
+            auto load_c = [&](int chunk) {
+                if (use_c && quads)
+                    load_c_quads(o, row0, nrows, t.n0 + chunk * 32, ncols - chunk * 32, c);
+            };
+            if (last >= 0) load_c(half);
+            if (!empty_sum) {
+                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                ++acc;
+            }
 #pragma unroll 1
             for (int chunk = half; chunk < n_chunks; chunk += 2) {
                 float v[32];
@@ -711,10 +818,11 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                 const int left = ncols - chunk * 32;
                 const int width = left < 32 ? left : 32;
                 const int64_t c0 = t.n0 + chunk * 32;
-                if (direct_block(o, width)) {
-                    finish_direct<MODE == kWgrad>(v, c, o, c0);
+                if (quads) {
+                    transpose_quads(v);
+                    finish_quads<MODE == kWgrad>(v, c, o, c0, width);
                     if (chunk + 2 < n_chunks) load_c(chunk + 2);
-                    store_direct(v, o, row0, nrows, c0);
+                    store_quads(v, o, row0, nrows, c0, width);
                 } else {
                     store_transposed(v, o, row0, nrows, c0, width);
                 }
@@ -722,6 +830,8 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
             }
             if (last < 0 && !empty_sum) release_acc();
         }
+        __syncwarp();
+        if (MODE == kWgrad && args.staged && elect_one()) bulk_wait_all();  // D is written
         __syncwarp();
     }
 
@@ -841,7 +951,7 @@ DeviceInfo *device_info() {
 }
 
 template <int CG, int MODE>
-cudaError_t launch(const CUtensorMap (&maps)[5], const Args &a, bool gather, int64_t max_tiles,
+cudaError_t launch(const CUtensorMap (&maps)[7], const Args &a, bool gather, int64_t max_tiles,
                    const DeviceInfo *d, cudaStream_t stream) {
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
@@ -850,12 +960,12 @@ cudaError_t launch(const CUtensorMap (&maps)[5], const Args &a, bool gather, int
         if (gather) {
             cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
             return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
-                                      maps[2], maps[3], maps[4], a);
+                                      maps[2], maps[3], maps[4], maps[5], maps[6], a);
         }
     }
     cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, stream, attr);
     return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, false>, maps[0], maps[1], maps[2],
-                              maps[3], maps[4], a);
+                              maps[3], maps[4], maps[5], maps[6], a);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -877,12 +987,12 @@ void set_tile(Args &a, int cg, int am, int bn, int ksub = 1) {
 }
 
 // Blocks of 64 of K per stage: a copy takes the producer about 100 ns to issue
-// whatever its size, so narrow tiles put up to four blocks into one stage (at
-// least 16 KiB of B).  The copies of K-major operands then count K in blocks
-// of 64, which needs K to be a multiple of 64.
-int sub_blocks(int64_t K, int bn) {
+// whatever its size, while 128 x 128 tiles multiply a block in 130 ns, so tiles
+// that small put two or four blocks into one stage.  The copies of K-major
+// operands then count K in blocks of 64, which needs K to be a multiple of 64.
+int sub_blocks(int64_t K, int am, int bn) {
     int ksub = 1;
-    while (ksub < 4 && bn * 128 * ksub < 16384) ksub *= 2;
+    while (ksub < 4 && bn * 2 * ksub <= 256 && (am + bn) * 128 * 2 * ksub <= 65536) ksub *= 2;
     return K % BK == 0 ? ksub : 1;
 }
 
@@ -962,7 +1072,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
         const int64_t row_tiles = live * ceil_div(mean, am);
         int bn = 256;
         while (bn > 64 && row_tiles * ceil_div(p.N, bn) < 4 * d->sms) bn /= 2;
-        set_tile(a, 1, am, bn, sub_blocks(p.K, bn));
+        set_tile(a, 1, am, bn, sub_blocks(p.K, am, bn));
     }
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
@@ -978,7 +1088,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
         p.row_index = nullptr;
     }
     const bool gather = p.row_index != nullptr;
-    CUtensorMap maps[5];
+    CUtensorMap maps[7];
     bool ok = e == cudaSuccess && encode_kmajor(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, p.lda, a.am, a.ksub, 3) &&
               encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, 1, 2);
     const int64_t count = one_b ? 1 : p.groups, stride = one_b ? p.ldb : p.stride_b;
@@ -988,7 +1098,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
     else
         ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64,
                                 static_cast<uint32_t>(BK * a.ksub), 3);
-    maps[3] = maps[4] = maps[2];
+    maps[3] = maps[4] = maps[5] = maps[6] = maps[2];
     const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
     static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
                                              {"grouped_tc<bf16>", "grouped_tc<bf16,pair>"}};
@@ -999,6 +1109,13 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
                  : launch<1, kRows>(maps, a, gather, max_tiles, d, stream);
     return free_after(ws, stream, e);
 }
+
+// Whether the weight gradient's epilogue goes through TMA boxes, by the mean
+// rows per group.  16 groups, 4096 x 4096 FP32 gradients, us for boxes / for
+// registers (whose ring is three stages deeper): beta = 0: 64 rows 197 / 256,
+// 512 rows 277 / 324, 1024 rows 410 / 373; beta = 1: 64 rows 391 / 993, 2048
+// rows 764 / 1053.
+constexpr int64_t kStagedRows = 640, kStagedRowsC = 4096;
 
 bool wgrad_tc_eligible(const WgradProblem &p) {
     return p.rows > 0 && p.rows_a > 0 && tma_rows(p.A, p.lda) && tma_rows(p.B, p.ldb) &&
@@ -1029,8 +1146,8 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     a.out.out = p.out;
     a.out.row_vec = row_alignment(p.D, p.ldd, p.groups > 1 ? p.stride_d : 0, elt);
     if (p.beta != 0.f) {
-        const int c = row_alignment(p.C, p.ldc, p.groups > 1 ? p.stride_c : 0, 4);
-        if (c < a.out.row_vec) a.out.row_vec = c;
+        // (quads of C are 16 bytes)
+        if (row_alignment(p.C, p.ldc, p.groups > 1 ? p.stride_c : 0, 4) < 16) a.out.row_vec = 0;
     }
     a.stride_d = p.stride_d;
     a.stride_c = p.stride_c;
@@ -1048,7 +1165,7 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     }
     a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, BM * cg));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
-    CUtensorMap maps[5];
+    CUtensorMap maps[7];
     void *ws = nullptr;
     cudaError_t e = cudaSuccess;
     if (pair && p.row_index != nullptr) {
@@ -1074,7 +1191,25 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
                                   static_cast<uint32_t>(b_blocks), 3)
                   : encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2)) &&
         encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
-    maps[4] = maps[3];
+    maps[4] = maps[5] = maps[6] = maps[3];
+    // D and C as TMA boxes: whole 16-byte pieces everywhere
+    const int64_t per_16 = 16 / elt;
+    auto boxes = [&](const void *q, int64_t ld, int64_t stride, int64_t per) {
+        return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % per == 0 && p.N % per == 0 &&
+               (p.groups == 1 || (stride % per == 0 && stride > 0)) && ld < (int64_t(1) << 37) &&
+               stride < (int64_t(1) << 37);
+    };
+    a.staged = ok && p.rows / p.groups <= (p.beta != 0.f ? kStagedRowsC : kStagedRows) && boxes(p.D, p.ldd, p.stride_d, per_16) &&
+               (p.beta == 0.f || boxes(p.C, p.ldc, p.stride_c, 4));
+    if (a.staged) {
+        const int64_t sd = p.groups > 1 ? p.stride_d : p.ldd, sc = p.groups > 1 ? p.stride_c : p.ldc;
+        if (!encode_box32(&maps[6], static_cast<int>(elt), bf16, p.D, p.N, p.M, p.ldd, p.groups, sd) ||
+            (p.beta != 0.f &&
+             !encode_box32(&maps[5], 4, false, p.C, p.N, p.M, p.ldc, p.groups, sc)))
+            a.staged = 0;
+    }
+    if (a.staged && a.stages > kStagedRing / static_cast<int>(a.stage_bytes))
+        a.stages = kStagedRing / static_cast<int>(a.stage_bytes);
     const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
     static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
                                              {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
@@ -1128,7 +1263,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         const int64_t per_row = d->sms / ceil_div(p.M, am) > 0 ? d->sms / ceil_div(p.M, am) : 1;
         int64_t bn = ceil_div(ceil_div(p.N, per_row), step) * step;
         if (bn > 256) bn = 256;
-        set_tile(a, 1, am, static_cast<int>(bn), sub_blocks(p.K, static_cast<int>(bn)));
+        set_tile(a, 1, am, static_cast<int>(bn), sub_blocks(p.K, am, static_cast<int>(bn)));
     }
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
@@ -1186,7 +1321,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
             if (e != cudaSuccess) break;
             a.late_wait = 1;
         }
-        CUtensorMap maps[5];
+        CUtensorMap maps[7];
         bool ok = encode_kmajor(&maps[0], bf16, l.X, p.K, rows, p.ldx, 1, p.ldx, a.am, a.ksub, 3);
         if (p.w_kmajor)
             ok = ok && encode_kmajor(&maps[2], bf16, p.W, p.K, p.N, p.ldw, 1, p.ldw, a.bn / cg,
@@ -1194,7 +1329,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         else
             ok = ok && encode_stack(&maps[2], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw, 64,
                                     static_cast<uint32_t>(BK * a.ksub), 3);
-        maps[1] = maps[3] = maps[4] = maps[2];
+        maps[1] = maps[3] = maps[4] = maps[5] = maps[6] = maps[2];
         if (p.adapters > 0) {
             const bool one_lb = p.adapters == 1 || p.stride_b == 0;
             const int64_t stride = one_lb ? p.ld_b : p.stride_b;

@@ -16,19 +16,13 @@ struct OutArgs {
     int64_t ldc;
     float alpha, beta;
     int act, out;
-    int row_vec;  // bytes every row of D (and C) is aligned to: 32, 16 or 0 (less)
+    int row_vec;  // bytes every row of D (and C) is aligned to: 16, 8 or 0 (less)
 };
 
 __device__ __forceinline__ uint32_t pack_16(float lo, float hi, int out) {
     if (out == kOutBf16) return pack_bf16x2(lo, hi);
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ void st_global_v4(void *p, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
 }
 
 // The warp's 32 x 32 block held one row per lane becomes one column per lane
@@ -51,17 +45,29 @@ __device__ __forceinline__ void transpose_32x32(float (&v)[32]) {
     }
 }
 
-// This lane's 32 values of C, row `row`, from column c0 on (rows aligned to 16 bytes).
-__device__ __forceinline__ void load_c_row(const OutArgs &a, int64_t row, int64_t c0,
-                                           float (&c)[32]) {
-    const float4 *p = reinterpret_cast<const float4 *>(a.C + row * a.ldc + c0);
+// The same block so that lane l holds quad l % 8 (columns 4 (l % 8) .. + 3) of
+// the rows 8 (l / 8) + i in v[4 i .. 4 i + 3]: eight lanes then cover a row's 32
+// columns, and a warp's 16-byte access four whole 128-byte lines.  (One row per
+// lane with 32-byte accesses costs a request per sector: a 256 x 256 FP32 tile
+// took 4.2 us to write, 9 us with C.)
+__device__ __forceinline__ void transpose_quads(float (&v)[32]) {
+    const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const float4 v = p[q];
-        c[q * 4 + 0] = v.x;
-        c[q * 4 + 1] = v.y;
-        c[q * 4 + 2] = v.z;
-        c[q * 4 + 3] = v.w;
+    for (int s = 4; s > 0; s >>= 1) {
+        const bool high = (lane & s) != 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k & s) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float give = high ? v[k * 4 + j] : v[(k + s) * 4 + j];
+                const float got = __shfl_xor_sync(0xffffffffu, give, s);
+                if (high)
+                    v[k * 4 + j] = got;
+                else
+                    v[(k + s) * 4 + j] = got;
+            }
+        }
     }
 }
 
@@ -78,70 +84,88 @@ __device__ __forceinline__ float activate(float x, int act) {
 
 // A block is 32 rows of D from row0 on (nrows of them inside) and 32 columns
 // from c0 on (width inside); v holds lane l's accumulators of row row0 + l.
-// Whole blocks with aligned rows go straight from registers, each lane its own
-// row (whole 32-byte sectors); others are transposed first, so that a store
-// instruction writes consecutive columns of one row.
-__device__ __forceinline__ bool direct_block(const OutArgs &a, int width) {
-    return width == 32 && a.row_vec >= 16;
+// Where rows start on whole quads (16 bytes of FP32, 8 of 16-bit values) the
+// block is written in quads, otherwise one column per lane.
+__device__ __forceinline__ bool in_quads(const OutArgs &a) {
+    return a.row_vec >= (a.out == kOutF32 ? 16 : 8);
 }
 
-// v = act(alpha v + bias + beta c); c is this lane's row of C.
-template <bool WITH_C>
-__device__ __forceinline__ void finish_direct(float (&v)[32], const float (&c)[32],
-                                              const OutArgs &a, int64_t c0) {
-    if (!WITH_C && a.bias != nullptr) {
-        const float mine = a.bias[c0 + threadIdx.x % 32];
+// This lane's quads of C.
+__device__ __forceinline__ void load_c_quads(const OutArgs &a, int64_t row0, int nrows, int64_t c0,
+                                             int width, float (&c)[32]) {
+    const int lane = threadIdx.x % 32, col = (lane % 8) * 4, first = (lane / 8) * 8;
+    const float *p = a.C + (row0 + first) * a.ldc + c0 + col;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            v[j] = fmaf(v[j], a.alpha, __shfl_sync(0xffffffffu, mine, j));
-    } else {
+    for (int i = 0; i < 8; ++i, p += a.ldc) {
+        if (first + i >= nrows) continue;
+        if (col + 4 <= width) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            c[i * 4 + 0] = q.x, c[i * 4 + 1] = q.y, c[i * 4 + 2] = q.z, c[i * 4 + 3] = q.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= a.alpha;
+            for (int j = 0; j < 3; ++j)
+                if (col + j < width) c[i * 4 + j] = p[j];
+        }
     }
+}
+
+// v = act(alpha v + bias + beta c), in quads (after transpose_quads).
+template <bool WITH_C>
+__device__ __forceinline__ void finish_quads(float (&v)[32], const float (&c)[32],
+                                             const OutArgs &a, int64_t c0, int width) {
+    const int col = (threadIdx.x % 8) * 4;
+    float b[4] = {};
+    if (!WITH_C && a.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (col + j < width) b[j] = a.bias[c0 + col + j];
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], a.alpha, b[i % 4]);
     if (WITH_C && a.beta != 0.f) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = fmaf(a.beta, c[j], v[j]);
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(a.beta, c[i], v[i]);
     }
     if (!WITH_C && a.act != kActNone) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], a.act);
+        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], a.act);
     }
 }
 
-__device__ __forceinline__ void store_direct(const float (&v)[32], const OutArgs &a, int64_t row0,
-                                             int nrows, int64_t c0) {
-    const int lane = threadIdx.x % 32;
-    if (lane >= nrows) return;
-    const int64_t at = (row0 + lane) * a.ldd + c0;
+__device__ __forceinline__ void store_quads(const float (&v)[32], const OutArgs &a, int64_t row0,
+                                            int nrows, int64_t c0, int width) {
+    const int lane = threadIdx.x % 32, col = (lane % 8) * 4, first = (lane / 8) * 8;
+    if (col >= width) return;
+    const int64_t at = (row0 + first) * a.ldd + c0 + col;
+    const bool whole = col + 4 <= width;
     if (a.out == kOutF32) {
         float *d = static_cast<float *>(a.D) + at;
-        if (a.row_vec >= 32) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                st_global_v8(d + q * 8, __float_as_uint(v[q * 8 + 0]), __float_as_uint(v[q * 8 + 1]),
-                             __float_as_uint(v[q * 8 + 2]), __float_as_uint(v[q * 8 + 3]),
-                             __float_as_uint(v[q * 8 + 4]), __float_as_uint(v[q * 8 + 5]),
-                             __float_as_uint(v[q * 8 + 6]), __float_as_uint(v[q * 8 + 7]));
-        } else {
+        for (int i = 0; i < 8; ++i, d += a.ldd) {
+            if (first + i >= nrows) continue;
+            if (whole) {
+                *reinterpret_cast<float4 *>(d) =
+                    make_float4(v[i * 4], v[i * 4 + 1], v[i * 4 + 2], v[i * 4 + 3]);
+            } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                st_global_v4(d + q * 4, __float_as_uint(v[q * 4 + 0]), __float_as_uint(v[q * 4 + 1]),
-                             __float_as_uint(v[q * 4 + 2]), __float_as_uint(v[q * 4 + 3]));
+                for (int j = 0; j < 3; ++j)
+                    if (col + j < width) d[j] = v[i * 4 + j];
+            }
         }
     } else {
         uint16_t *d = static_cast<uint16_t *>(a.D) + at;
-        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] = pack_16(v[2 * j], v[2 * j + 1], a.out);
-        if (a.row_vec >= 32) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                st_global_v8(d + q * 16, w[q * 8 + 0], w[q * 8 + 1], w[q * 8 + 2], w[q * 8 + 3],
-                             w[q * 8 + 4], w[q * 8 + 5], w[q * 8 + 6], w[q * 8 + 7]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                st_global_v4(d + q * 8, w[q * 4 + 0], w[q * 4 + 1], w[q * 4 + 2], w[q * 4 + 3]);
+        for (int i = 0; i < 8; ++i, d += a.ldd) {
+            if (first + i >= nrows) continue;
+            const uint32_t lo = pack_16(v[i * 4], v[i * 4 + 1], a.out);
+            const uint32_t hi = pack_16(v[i * 4 + 2], v[i * 4 + 3], a.out);
+            if (whole) {
+                *reinterpret_cast<uint2 *>(d) = make_uint2(lo, hi);
+            } else {
+                d[0] = static_cast<uint16_t>(lo);
+                if (col + 1 < width) d[1] = static_cast<uint16_t>(lo >> 16);
+                if (col + 2 < width) d[2] = static_cast<uint16_t>(hi);
+            }
         }
     }
 }
@@ -177,12 +201,12 @@ __device__ __forceinline__ void store_transposed(float (&v)[32], const OutArgs &
     }
 }
 
-// Bytes (32, 16 or 0 for less) to which every row of a matrix of `elt`-byte
+// Bytes (16, 8 or 0 for less) to which every row of a matrix of `elt`-byte
 // values starting at p, with these pitches (elements), is aligned.
 inline int row_alignment(const void *p, int64_t ld, int64_t stride, int64_t elt) {
     const auto all = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)) |
                      static_cast<uint64_t>(ld * elt) | static_cast<uint64_t>(stride * elt);
-    return all % 32 == 0 ? 32 : (all % 16 == 0 ? 16 : 0);
+    return all % 16 == 0 ? 16 : (all % 8 == 0 ? 8 : 0);
 }
 
 }  // namespace tc

@@ -86,6 +86,25 @@ inline bool encode_kmajor(CUtensorMap *map, bool bf16, const void *base, int64_t
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A stack of matrices as 32 x 32 boxes for the epilogue, of FP32 (128-byte rows
+// and swizzle) or 16-bit values (64-byte).
+inline bool encode_box32(CUtensorMap *map, int elt, bool bf16, const void *base, int64_t N, int64_t M,
+                         int64_t ld, int64_t count, int64_t stride) {
+    const auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M),
+                          static_cast<cuuint64_t>(count)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * elt, static_cast<cuuint64_t>(stride) * elt};
+    cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type = elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : bf16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              elt == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // What TMA asks of a matrix: 16-byte aligned base, row pitch (and matrix
 // pitch) of whole 16 bytes and below 2^40 bytes.
 inline bool tma_rows(const void *p, int64_t ld, int64_t stride = 0) {
