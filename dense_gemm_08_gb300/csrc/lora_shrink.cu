@@ -507,37 +507,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_hi = pl.r_pad / 8;
     const int share = (n_mine + a.ks - 1) / a.ks;
     const int r_end = share * (static_cast<int>(rank) + 1) < n_mine ? share * (static_cast<int>(rank) + 1) : n_mine;
-    for (int r = share * static_cast<int>(rank) + warp; ok && r < r_end; r += kThreads / 32) {
+    const int r_begin = share * static_cast<int>(rank), n_share = r_end > r_begin ? r_end - r_begin : 0;
+    // the rows' own slots: 8 columns per thread and step
+    for (int i = tid; ok && i < n_share * n_hi; i += kThreads) {
+        const int r = r_begin + i / n_hi, j = i % n_hi * 8;
+        const int own = t.slot_of[off + r];
+        if (own < 0 || pass_of[own] % gridDim.z != blockIdx.z) continue;
+        const float *part = a.part + (row_first + r) * pl.r_pad + j;
+        float4 x[kMaxCluster], y[kMaxCluster];
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {  // all in flight, then added in order
+            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < a.ks) {
+                const float4 *q = reinterpret_cast<const float4 *>(
+                    part + static_cast<int64_t>(k) * p.M * pl.r_pad);
+                x[k] = __ldcg(q);
+                y[k] = __ldcg(q + 1);
+            }
+        }
+        float u[8] = {};
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+            u[0] += x[k].x, u[1] += x[k].y, u[2] += x[k].z, u[3] += x[k].w;
+            u[4] += y[k].x, u[5] += y[k].y, u[6] += y[k].z, u[7] += y[k].w;
+        }
+        const float scale = p.scale != nullptr ? p.scale[t.list[own]] : 1.f;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint16_t h0, l0, h1, l1;
+            split_16(u[2 * k] * scale, a.ab_format, h0, l0);
+            split_16(u[2 * k + 1] * scale, a.ab_format, h1, l1);
+            hi[k] = h0 | (static_cast<uint32_t>(h1) << 16);
+            lo[k] = l0 | (static_cast<uint32_t>(l1) << 16);
+        }
+        uint16_t *d = pl.V + (row_first + r) * pl.ldv + own * pl.rc + j;
+        *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (pl.rc > pl.r_pad)
+            *reinterpret_cast<uint4 *>(d + pl.r_pad) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    // zeros in their other slots
+    for (int r = r_begin + warp; ok && r < r_begin + n_share; r += kThreads / 32) {
         const int own = t.slot_of[off + r];
         const bool mine = own >= 0 ? pass_of[own] % gridDim.z == blockIdx.z : first_z;
         if (!mine) continue;
-        const float scale = own >= 0 && p.scale != nullptr ? p.scale[t.list[own]] : 1.f;
-        const float *part = a.part + (row_first + r) * pl.r_pad;
         uint4 *d = reinterpret_cast<uint4 *>(pl.V + (row_first + r) * pl.ldv);
-        for (int c = lane; c < count * groups; c += 32) {
-            uint32_t w[4] = {};
-            const int slot = c / groups, in = c - slot * groups;
-            if (slot == own) {
-                const int j = (in < n_hi ? in : in - n_hi) * 8;
-                float u[8] = {};
-                for (int k = 0; k < a.ks; ++k) {
-                    const float4 *q = reinterpret_cast<const float4 *>(
-                        part + static_cast<int64_t>(k) * p.M * pl.r_pad + j);
-                    const float4 x = __ldcg(q), y = __ldcg(q + 1);
-                    u[0] += x.x, u[1] += x.y, u[2] += x.z, u[3] += x.w;
-                    u[4] += y.x, u[5] += y.y, u[6] += y.z, u[7] += y.w;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint16_t h0, l0, h1, l1;
-                    split_16(u[2 * i] * scale, a.ab_format, h0, l0);
-                    split_16(u[2 * i + 1] * scale, a.ab_format, h1, l1);
-                    w[i] = in < n_hi ? (h0 | (static_cast<uint32_t>(h1) << 16))
-                                     : (l0 | (static_cast<uint32_t>(l1) << 16));
-                }
-            }
-            d[c] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int c = lane; c < count * groups; c += 32)
+            if (c / groups != own) d[c] = make_uint4(0, 0, 0, 0);
     }
     if (!ok) {
         // copies in flight land before the CTA exits
