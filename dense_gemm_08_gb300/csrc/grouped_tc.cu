@@ -406,18 +406,16 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                             mbar_arrive_expect_tx(
                                 full0 + 8 * stage,
                                 CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
-                        if (GATHER || part) {
+                        if (part) {
                             for (int h = 0; h < kGatherWarps; ++h)
                                 mbar_arrive(go0 + 8 * (h * kMaxStages + stage));
                         }
                         if (!part) {
-                            if constexpr (!GATHER) {
-                                if (args.a_wide) {
-                                    tma_load_3d<CG>(sa, &map_a, 0, r0, m0 / 64, fb);
-                                } else {
-                                    tma_load_2d<CG>(sa, &map_a, m0, r0, fb);
-                                    tma_load_2d<CG>(sa + 8192, &map_a, m0 + 64, r0, fb);
-                                }
+                            if (args.a_wide) {
+                                tma_load_3d<CG>(sa, &map_a, 0, r0, m0 / 64, fb);
+                            } else {
+                                tma_load_2d<CG>(sa, &map_a, m0, r0, fb);
+                                tma_load_2d<CG>(sa + 8192, &map_a, m0 + 64, r0, fb);
                             }
                             if (args.b_wide) {
                                 tma_load_3d<CG>(sb, &map_b, 0, r0, b0 / 64, fb);
@@ -558,7 +556,7 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         // barrier of that stage; it cannot tell it again before the bytes have
         // arrived, so one parity bit per stage is enough.
         const int half = warp - (2 + kEpiWarps);
-        int *const mine = numbers + half * 128;  // 64 row numbers of A, then 64 of B
+        int *const mine = numbers + half * 64;  // 64 row numbers
         const uint32_t go = go0 + 8 * half * kMaxStages;
         int stage = 0;
         uint32_t told = 0;  // parity of the next word on each stage
@@ -598,15 +596,13 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     const int rem = t.last - r0 < BK ? t.last - r0 : BK;
                     part = rem < BK;
                     quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
-                    work = GATHER || part;
+                    work = part;
                     if (work) {
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const int r = lane + j * 32;
-                            const int own = r >= rem ? -1 : static_cast<int>(r0 + r);
-                            mine[64 + r] = own;
-                            mine[r] = GATHER && own >= 0 ? __ldg(args.row_index + own) : own;
+                            mine[r] = r < rem ? static_cast<int>(r0 + r) : -1;
                         }
                         __syncwarp();
                     }
@@ -617,9 +613,8 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     told ^= 1u << stage;
                     if constexpr (MODE == kWgrad) {
                         gather(sa + half * 8192, &map_a_rows, m0 + half * 64, mine, quads, fb);
-                        if (part)
-                            for (int j = half; j < b_rows / 64; j += kGatherWarps)
-                                gather(sb + j * 8192, &map_b_rows, b0 + 64 * j, mine + 64, quads, fb);
+                        for (int j = half; j < b_rows / 64; j += kGatherWarps)
+                            gather(sb + j * 8192, &map_b_rows, b0 + 64 * j, mine, quads, fb);
                     } else {
                         for (int u = 0; u < ksub; ++u)
                             gather(sa + (u * args.am + half * 64) * 128, &map_a_rows,
@@ -763,8 +758,11 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
             float c[32];
             const bool quads = in_quads(o);
             auto load_c = [&](int chunk) {
-                if (use_c && quads)
+                if (!use_c) return;
+                if (quads)
                     load_c_quads(o, row0, nrows, t.n0 + chunk * 32, ncols - chunk * 32, c);
+                else
+                    load_c_columns(o, row0, nrows, t.n0 + chunk * 32, ncols - chunk * 32, c);
             };
             if (last >= 0) load_c(half);
             if (!empty_sum) {
@@ -824,7 +822,10 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                     if (chunk + 2 < n_chunks) load_c(chunk + 2);
                     store_quads(v, o, row0, nrows, c0, width);
                 } else {
-                    store_transposed(v, o, row0, nrows, c0, width);
+                    transpose_32x32(v);
+                    finish_columns<MODE == kWgrad>(v, c, o, c0, width);
+                    if (chunk + 2 < n_chunks) load_c(chunk + 2);
+                    store_columns(v, o, row0, nrows, c0, width);
                 }
                 __syncwarp();
             }
@@ -850,8 +851,11 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
 // Rows of A in product order: out(r, :) = A(index[r], :), zeros for an index
 // outside A.  TMA fetches gathered rows one 128-byte line per 8 ns and SM, a
 // third of what the MMAs of a CTA pair take (8 experts, 16384 rows, 4096 ->
-// 14336: 3.1 ms gathered by TMA, 1.06 ms with the rows in order), so large
-// problems put the rows in order first: 200 MB of traffic, 30 us.
+// 14336: 3.1 ms gathered by TMA, 1.06 ms with the rows in order).  So only
+// groups of a few rows (kGatherRows on average) are gathered by TMA, which
+// saves a launch; others, and the weight gradients' rows, are put in order
+// first (16384 rows of 4096: 41 us at 6.5 TB/s).
+constexpr int64_t kGatherRows = 16;
 __global__ void __launch_bounds__(256) order_rows_kernel(const uint16_t *A, int64_t lda,
                                                          int64_t rows_a, const int32_t *index,
                                                          int64_t rows, int64_t cols, uint16_t *out,
@@ -933,7 +937,7 @@ DeviceInfo *device_info() {
         d->sms = n > 0 ? n : 1;
         for (cudaError_t e : {allow_smem<1, kRows, false>(), allow_smem<1, kRows, true>(),
                               allow_smem<2, kRows, false>(), allow_smem<1, kWgrad, false>(),
-                              allow_smem<1, kWgrad, true>(), allow_smem<2, kWgrad, false>(),
+                              allow_smem<2, kWgrad, false>(),
                               allow_smem<1, kLora, false>(), allow_smem<2, kLora, false>()})
             if (d->err == cudaSuccess) d->err = e;
         if (d->err != cudaSuccess) return;
@@ -956,7 +960,7 @@ cudaError_t launch(const CUtensorMap (&maps)[7], const Args &a, bool gather, int
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
     cudaLaunchAttribute attr[2];
-    if constexpr (MODE != kLora && CG == 1) {
+    if constexpr (MODE == kRows && CG == 1) {
         if (gather) {
             cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
             return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
@@ -1079,7 +1083,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
     const int cg = pair ? 2 : 1;
     void *ws = nullptr;
     cudaError_t e = cudaSuccess;
-    if (pair && p.row_index != nullptr) {
+    if (p.row_index != nullptr && p.rows / live > kGatherRows) {
         int64_t ldo = 0;
         e = order_rows(p.A, p.lda, p.rows_a, p.row_index, p.rows, p.K, d->sms, stream, &ws, &ldo);
         p.A = ws;
@@ -1168,7 +1172,7 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     CUtensorMap maps[7];
     void *ws = nullptr;
     cudaError_t e = cudaSuccess;
-    if (pair && p.row_index != nullptr) {
+    if (p.row_index != nullptr) {
         int64_t ldo = 0;
         e = order_rows(p.A, p.lda, p.rows_a, p.row_index, p.rows, p.M, d->sms, stream, &ws, &ldo);
         p.A = ws;
@@ -1176,8 +1180,6 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
         p.rows_a = p.rows;
         p.row_index = nullptr;
     }
-    a.row_index = p.row_index;
-    const bool gather = p.row_index != nullptr;
     // rows of whole 64-column blocks: one copy for all of a stage's blocks
     const int b_blocks = a.bn / cg / 64;
     a.a_wide = p.M % 64 == 0;
@@ -1216,8 +1218,8 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     *name = kNames[bf16][pair];
     if (e == cudaSuccess && !ok) e = cudaErrorInvalidValue;
     if (e == cudaSuccess)
-        e = pair ? launch<2, kWgrad>(maps, a, gather, max_tiles, d, stream)
-                 : launch<1, kWgrad>(maps, a, gather, max_tiles, d, stream);
+        e = pair ? launch<2, kWgrad>(maps, a, false, max_tiles, d, stream)
+                 : launch<1, kWgrad>(maps, a, false, max_tiles, d, stream);
     return free_after(ws, stream, e);
 }
 

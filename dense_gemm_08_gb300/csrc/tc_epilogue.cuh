@@ -85,7 +85,7 @@ __device__ __forceinline__ float activate(float x, int act) {
 // A block is 32 rows of D from row0 on (nrows of them inside) and 32 columns
 // from c0 on (width inside); v holds lane l's accumulators of row row0 + l.
 // Where rows start on whole quads (16 bytes of FP32, 8 of 16-bit values) the
-// block is written in quads, otherwise one column per lane.
+// block is written in quads, otherwise one column per lane (transpose_32x32).
 __device__ __forceinline__ bool in_quads(const OutArgs &a) {
     return a.row_vec >= (a.out == kOutF32 ? 16 : 8);
 }
@@ -170,23 +170,39 @@ __device__ __forceinline__ void store_quads(const float (&v)[32], const OutArgs 
     }
 }
 
-__device__ __forceinline__ void store_transposed(float (&v)[32], const OutArgs &a, int64_t row0,
-                                                 int nrows, int64_t c0, int width) {
+// Rows that start anywhere: one column per lane (after transpose_32x32, v[i] is
+// row row0 + i).  C is loaded ahead as for the quads.
+__device__ __forceinline__ void load_c_columns(const OutArgs &a, int64_t row0, int nrows, int64_t c0,
+                                               int width, float (&c)[32]) {
     const int lane = threadIdx.x % 32;
-    transpose_32x32(v);  // v[i] = row row0 + i, this lane's column
     if (lane >= width) return;
-    const float b = a.bias != nullptr ? a.bias[c0 + lane] : 0.f;
-    const bool use_c = a.beta != 0.f;
-    const float *cp = use_c ? a.C + row0 * a.ldc + c0 + lane : nullptr;
+    const float *p = a.C + row0 * a.ldc + c0 + lane;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i] = fmaf(v[i], a.alpha, b);
-        if (use_c) {
-            if (i < nrows) v[i] = fmaf(a.beta, *cp, v[i]);
-            cp += a.ldc;
-        }
-        v[i] = activate(v[i], a.act);
+    for (int i = 0; i < 32; ++i, p += a.ldc)
+        if (i < nrows) c[i] = *p;
+}
+
+template <bool WITH_C>
+__device__ __forceinline__ void finish_columns(float (&v)[32], const float (&c)[32],
+                                               const OutArgs &a, int64_t c0, int width) {
+    const int lane = threadIdx.x % 32;
+    const float b = !WITH_C && a.bias != nullptr && lane < width ? a.bias[c0 + lane] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], a.alpha, b);
+    if (WITH_C && a.beta != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(a.beta, c[i], v[i]);
     }
+    if (!WITH_C && a.act != kActNone) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], a.act);
+    }
+}
+
+__device__ __forceinline__ void store_columns(const float (&v)[32], const OutArgs &a, int64_t row0,
+                                              int nrows, int64_t c0, int width) {
+    const int lane = threadIdx.x % 32;
+    if (lane >= width) return;
     const int64_t at = row0 * a.ldd + c0 + lane;
     if (a.out == kOutF32) {
         float *d = static_cast<float *>(a.D) + at;
@@ -194,10 +210,13 @@ __device__ __forceinline__ void store_transposed(float (&v)[32], const OutArgs &
         for (int i = 0; i < 32; ++i, d += a.ldd)
             if (i < nrows) *d = v[i];
     } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack_16(v[2 * i], v[2 * i + 1], a.out);
         uint16_t *d = static_cast<uint16_t *>(a.D) + at;
 #pragma unroll
         for (int i = 0; i < 32; ++i, d += a.ldd)
-            if (i < nrows) *d = static_cast<uint16_t>(pack_16(v[i], 0.f, a.out));
+            if (i < nrows) *d = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
     }
 }
 
