@@ -519,6 +519,14 @@ def _stream_of(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _on_device(device):
+    """Refuse operands that the kernels of the current device cannot read."""
+    if device.type != "cuda":
+        raise ValueError("the operands must be CUDA tensors")
+    if device.index != _torch()._C._cuda_getDevice():
+        raise ValueError(f"the operands are on {device}, which is not the current device")
+
+
 def _types(A, B, out, out_dtype, default):
     """(entry point suffix, output dtype, d_type, device); A and B share a dtype, D is FP32 or that."""
     torch = _torch()
@@ -556,6 +564,7 @@ def group_rows(ids, groups, stream=None):
     torch = _torch()
     device, n = ids.device, ids.numel()
     at = _int_vector(ids, n, "ids", device)
+    _on_device(device)
     # (views of one allocation would cost the host more than three allocations)
     offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
     order = torch.empty(n, dtype=torch.int32, device=device)
@@ -590,12 +599,13 @@ def gemm_grouped(A, B, offsets, row_index=None, bias=None, activation=GEMM_ACT_N
         index = _int_vector(row_index, rows, "row_index", device)
     at = _int_vector(offsets, groups + 1, "offsets", device)
     ep = Epilogue(_f32_dense(bias, (groups, N), "bias", device), activation, d_type)
+    if out is not None and tuple(out.shape) != (rows, N):
+        raise ValueError(f"out must be {rows} x {N}")
+    _on_device(device)
     if out is None:
         out = _torch().empty((rows, N), dtype=out_dtype, device=device)
         ldd = N
     else:
-        if tuple(out.shape) != (rows, N):
-            raise ValueError(f"out must be {rows} x {N}")
         ldd = _row_major(out, "out")
     fn = "gemm_grouped_" + suffix
     st = getattr(library(), fn)(groups, rows, N, K, alpha, A.data_ptr(), lda, rows_a, index, at,
@@ -635,10 +645,7 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
             raise ValueError(f"{what} must be a stack of row-major matrices")
         return max(ld, N, 1), stride
 
-    if out is None:
-        out = torch.empty((groups, M, N), dtype=out_dtype, device=device)
-        ldd, stride_d = max(N, 1), M * N
-    else:
+    if out is not None:
         ldd, stride_d = stack(out, "out")
     c, ldc, stride_c = None, 0, 0
     if beta != 0.0:
@@ -650,6 +657,10 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
             raise ValueError("C must be on the operands' device")
         ldc, stride_c = stack(C, "C")
         c = C.data_ptr()
+    _on_device(device)
+    if out is None:
+        out = torch.empty((groups, M, N), dtype=out_dtype, device=device)
+        ldd, stride_d = max(N, 1), M * N
     fn = "gemm_grouped_wgrad_" + suffix
     st = getattr(library(), fn)(groups, rows, M, N, alpha, A.data_ptr(), lda, rows_a, index, at,
                                 B.data_ptr(), ldb, beta, c, ldc, stride_c, out.data_ptr(), ldd,
@@ -688,12 +699,13 @@ def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GE
     ids = _int_vector(adapter_of_row, M, "adapter_of_row", device)
     scales = _f32_dense(scale, (adapters,), "scale", device)
     ep = Epilogue(_f32_dense(bias, (N,), "bias", device), activation, d_type)
+    if out is not None and tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be {M} x {N}")
+    _on_device(device)
     if out is None:
         out = _torch().empty((M, N), dtype=out_dtype, device=device)
         ldd = N
     else:
-        if tuple(out.shape) != (M, N):
-            raise ValueError(f"out must be {M} x {N}")
         ldd = _row_major(out, "out")
     fn = "gemm_lora_" + suffix
     st = getattr(library(), fn)(M, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, order_w, adapters,

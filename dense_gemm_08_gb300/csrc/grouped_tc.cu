@@ -69,7 +69,7 @@ struct Args {
     uint32_t tiles_m, tiles_n;  // tiles_m: wgrad only
     int num_kb;                 // rows, lora: K steps of a stage each
     int ksub;                   // rows, lora: blocks of 64 of K per stage
-    int a_wide, b_wide;         // wgrad: whole 64-column blocks, several per copy
+    int a_blocks, b_blocks;     // wgrad: whole 64-column blocks of A and B
     int staged;                 // wgrad: D and C move as TMA boxes (see kBoxBytes)
     int b_kmajor;               // rows
     int bn;                     // columns per tile (of the CTA or the pair)
@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                       const __grid_constant__ CUtensorMap map_b_rows,
                       const __grid_constant__ CUtensorMap map_v,
                       const __grid_constant__ CUtensorMap map_c,
-                      const __grid_constant__ CUtensorMap map_d, const Args args) {
+                      const __grid_constant__ CUtensorMap map_d,
+                      const __grid_constant__ CUtensorMap map_b_edge, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
         prefetch_map(&map_b);
         if (GATHER || MODE == kWgrad) prefetch_map(&map_a_rows);
         if (MODE != kRows) prefetch_map(&map_b_rows);
-        if (MODE == kLora) prefetch_map(&map_v);
+        if (MODE != kRows) prefetch_map(&map_v);
         if (MODE == kWgrad && args.staged) prefetch_map(&map_d);
         if (MODE == kWgrad && args.staged && args.out.beta != 0.f) prefetch_map(&map_c);
     }
@@ -411,17 +412,19 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
                                 mbar_arrive(go0 + 8 * (h * kMaxStages + stage));
                         }
                         if (!part) {
-                            if (args.a_wide) {
+                            // whole 64-column blocks in one copy; a tile that holds
+                            // the columns past the last whole one, block by block
+                            if (m0 / 64 + 2 <= args.a_blocks) {
                                 tma_load_3d<CG>(sa, &map_a, 0, r0, m0 / 64, fb);
                             } else {
-                                tma_load_2d<CG>(sa, &map_a, m0, r0, fb);
-                                tma_load_2d<CG>(sa + 8192, &map_a, m0 + 64, r0, fb);
+                                tma_load_2d<CG>(sa, &map_v, m0, r0, fb);
+                                tma_load_2d<CG>(sa + 8192, &map_v, m0 + 64, r0, fb);
                             }
-                            if (args.b_wide) {
+                            if (b0 / 64 + b_blocks <= args.b_blocks) {
                                 tma_load_3d<CG>(sb, &map_b, 0, r0, b0 / 64, fb);
                             } else {
                                 for (int j = 0; j < b_blocks; ++j)
-                                    tma_load_2d<CG>(sb + j * 8192, &map_b, b0 + 64 * j, r0, fb);
+                                    tma_load_2d<CG>(sb + j * 8192, &map_b_edge, b0 + 64 * j, r0, fb);
                             }
                         }
                     }
@@ -955,7 +958,7 @@ DeviceInfo *device_info() {
 }
 
 template <int CG, int MODE>
-cudaError_t launch(const CUtensorMap (&maps)[7], const Args &a, bool gather, int64_t max_tiles,
+cudaError_t launch(const CUtensorMap (&maps)[8], const Args &a, bool gather, int64_t max_tiles,
                    const DeviceInfo *d, cudaStream_t stream) {
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
@@ -964,12 +967,12 @@ cudaError_t launch(const CUtensorMap (&maps)[7], const Args &a, bool gather, int
         if (gather) {
             cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
             return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
-                                      maps[2], maps[3], maps[4], maps[5], maps[6], a);
+                                      maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], a);
         }
     }
     cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, stream, attr);
     return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, false>, maps[0], maps[1], maps[2],
-                              maps[3], maps[4], maps[5], maps[6], a);
+                              maps[3], maps[4], maps[5], maps[6], maps[7], a);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1071,11 +1074,25 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
     if (pair) {
         set_tile(a, 2, BM, 256);
     } else {
+        // Few rows per group: the weights are the time; narrow tiles and few
+        // rows per tile (64 groups, 128 rows, 4096 x 2048: 160 us with 16 rows,
+        // 168 with 64; 32 groups of 32 rows: 90 us with 32, 101 with 128).  A
+        // group's further rows read the weights again, from L2.
         const int64_t mean = ceil_div(p.rows, live);
-        const int am = mean <= 8 ? 32 : (mean <= 24 ? 64 : BM);
+        const int am = mean <= 4 ? 16 : (mean <= 12 ? 32 : (mean <= 32 ? 64 : BM));
         const int64_t row_tiles = live * ceil_div(mean, am);
         int bn = 256;
-        while (bn > 64 && row_tiles * ceil_div(p.N, bn) < 4 * d->sms) bn /= 2;
+        if (am < BM) {
+            while (bn > 64 && row_tiles * ceil_div(p.N, bn) < 4 * d->sms) bn /= 2;
+        } else {
+            // rounds of tiles, each as long as its columns and a fixed part (17
+            // groups, 672 rows, 173 x 10416: 37 us at 256 columns, 45 at 64)
+            int64_t best = INT64_MAX;
+            for (int w : {256, 128, 64}) {
+                const int64_t cost = ceil_div(row_tiles * ceil_div(p.N, w), d->sms) * (w + 64);
+                if (cost < best) best = cost, bn = w;
+            }
+        }
         set_tile(a, 1, am, bn, sub_blocks(p.K, am, bn));
     }
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
@@ -1092,7 +1109,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
         p.row_index = nullptr;
     }
     const bool gather = p.row_index != nullptr;
-    CUtensorMap maps[7];
+    CUtensorMap maps[8];
     bool ok = e == cudaSuccess && encode_kmajor(&maps[0], bf16, p.A, p.K, p.rows_a, p.lda, 1, p.lda, a.am, a.ksub, 3) &&
               encode_stack(&maps[1], bf16, p.A, p.K, p.rows_a, p.lda, 1, 0, BK, 1, 2);
     const int64_t count = one_b ? 1 : p.groups, stride = one_b ? p.ldb : p.stride_b;
@@ -1102,7 +1119,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
     else
         ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64,
                                 static_cast<uint32_t>(BK * a.ksub), 3);
-    maps[3] = maps[4] = maps[5] = maps[6] = maps[2];
+    maps[3] = maps[4] = maps[5] = maps[6] = maps[7] = maps[2];
     const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
     static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
                                              {"grouped_tc<bf16>", "grouped_tc<bf16,pair>"}};
@@ -1169,7 +1186,7 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     }
     a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, BM * cg));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
-    CUtensorMap maps[7];
+    CUtensorMap maps[8];
     void *ws = nullptr;
     cudaError_t e = cudaSuccess;
     if (p.row_index != nullptr) {
@@ -1180,20 +1197,22 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
         p.rows_a = p.rows;
         p.row_index = nullptr;
     }
-    // rows of whole 64-column blocks: one copy for all of a stage's blocks
-    const int b_blocks = a.bn / cg / 64;
-    a.a_wide = p.M % 64 == 0;
-    a.b_wide = p.N % 64 == 0;
-    const bool ok =
-        e == cudaSuccess &&
-        (a.a_wide ? encode_blocks(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, p.lda, BK, 2, 3)
-                  : encode_stack(&maps[0], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2)) &&
-        encode_stack(&maps[1], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, 1, 2) &&
-        (a.b_wide ? encode_blocks(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, p.ldb, BK,
-                                  static_cast<uint32_t>(b_blocks), 3)
-                  : encode_stack(&maps[2], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2)) &&
-        encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
-    maps[4] = maps[5] = maps[6] = maps[3];
+    const uint32_t boxes_b = static_cast<uint32_t>(a.bn / cg / 64);
+    a.a_blocks = static_cast<int>(p.M / 64);
+    a.b_blocks = static_cast<int>(p.N / 64);
+    bool ok = e == cudaSuccess &&
+              encode_stack(&maps[4], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, BK, 2) &&
+              encode_stack(&maps[1], bf16, p.A, p.M, p.rows_a, p.lda, 1, 0, 64, 1, 2) &&
+              encode_stack(&maps[7], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, BK, 2) &&
+              encode_stack(&maps[3], bf16, p.B, p.N, p.rows, p.ldb, 1, 0, 64, 1, 2);
+    maps[0] = maps[4];
+    maps[2] = maps[7];
+    if (a.a_blocks > 0)
+        ok = ok && encode_blocks(&maps[0], bf16, p.A, p.M / 64 * 64, p.rows_a, p.lda, 1, p.lda, BK, 2, 3);
+    if (a.b_blocks > 0)
+        ok = ok && encode_blocks(&maps[2], bf16, p.B, p.N / 64 * 64, p.rows, p.ldb, 1, p.ldb, BK,
+                                 boxes_b, 3);
+    maps[5] = maps[6] = maps[3];
     // D and C as TMA boxes: whole 16-byte pieces everywhere
     const int64_t per_16 = 16 / elt;
     auto boxes = [&](const void *q, int64_t ld, int64_t stride, int64_t per) {
@@ -1323,7 +1342,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
             if (e != cudaSuccess) break;
             a.late_wait = 1;
         }
-        CUtensorMap maps[7];
+        CUtensorMap maps[8];
         bool ok = encode_kmajor(&maps[0], bf16, l.X, p.K, rows, p.ldx, 1, p.ldx, a.am, a.ksub, 3);
         if (p.w_kmajor)
             ok = ok && encode_kmajor(&maps[2], bf16, p.W, p.K, p.N, p.ldw, 1, p.ldw, a.bn / cg,
@@ -1331,7 +1350,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         else
             ok = ok && encode_stack(&maps[2], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw, 64,
                                     static_cast<uint32_t>(BK * a.ksub), 3);
-        maps[1] = maps[3] = maps[4] = maps[5] = maps[6] = maps[2];
+        maps[1] = maps[3] = maps[4] = maps[5] = maps[6] = maps[7] = maps[2];
         if (p.adapters > 0) {
             const bool one_lb = p.adapters == 1 || p.stride_b == 0;
             const int64_t stride = one_lb ? p.ld_b : p.stride_b;

@@ -385,3 +385,38 @@ def test_grouped_one_matrix_for_all_groups():
         done()
         ref, tol, _ = grouped_ref(A, B.expand(3, 64, 72), offsets.cpu().numpy(), None, None, 0, 1.0)
         assert_close(D, ref, tol, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_grouped_stacks_interleaved_and_broadcast(dtype):
+    # matrices of a stack that share rows of one buffer (pitch groups * N, matrix pitch N),
+    # and a C that is the same for all groups
+    rng = np.random.default_rng(23)
+    sizes, K, N = [70, 0, 33], 64, 72
+    offsets = offsets_of(sizes)
+    at = torch.from_numpy(offsets).cuda()
+    A = draw(rng, (103, K), dtype).cuda()
+    B = draw(rng, (K, 3, N), dtype, sigma=0.1).cuda().permute(1, 0, 2)
+    got = lib.gemm_grouped(A, B, at, out_dtype=torch.float32)
+    done()
+    ref, tol, _ = grouped_ref(A, B, offsets, None, None, 0, 1.0)
+    assert_close(got, ref, tol, "f32")
+    G = draw(rng, (103, N), dtype).cuda()
+    C = torch.from_numpy(rng.standard_normal((1, K, N)).astype(np.float32)).cuda().expand(3, K, N)
+    buf = torch.full((K + 1, 3, N), SENTINEL, dtype=torch.float32, device="cuda")
+    lib.gemm_grouped_wgrad(A, G, at, C=C, beta=2.0, out=buf[:K].permute(1, 0, 2))
+    done()
+    ref, tol = wgrad_ref(A, G, offsets, None, C, 1.0, 2.0)
+    assert_close(buf[:K].permute(1, 0, 2), ref, tol, "f32")
+    assert bool((buf[K] == SENTINEL).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("N", [248, 250, 251])
+@pytest.mark.parametrize("M", [200, 256])
+def test_wgrad_rows_of_any_alignment(dtype, N, M):
+    # rows of D and C on 16, 8 and 2 bytes; few and many rows per group (boxes, registers)
+    for sizes in ([40, 0, 90], [1500, 700]):
+        rng = np.random.default_rng(24 + N)
+        run_wgrad(rng, sizes, 3, M, N, dtype, dtype, beta=1.0)
+        run_wgrad(rng, sizes, 3, M, N, dtype, "f32")

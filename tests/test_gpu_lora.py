@@ -192,3 +192,23 @@ def test_lora_streams_graphs_and_repeats():
     done()
     ref, tol = lora_ref(X, W, LA, LB, ids, None, None, 0, "bf16", "bf16")
     assert_close(out, ref, tol, "bf16")
+
+
+def test_lora_many_slots_in_several_launches():
+    # 128 slots of 2 x 256 columns per tile: V of 1100 rows passes its 128 MiB
+    rng = np.random.default_rng(37)
+    run(rng, 1100, 72, 136, 256, 300, "bf16", "f32")
+    run(rng, 9, 72, 136, 300, 4, "f16", "f16")  # a rank past the tensor-core path's
+
+
+def test_lora_one_adapter_for_all_numbers():
+    # stacks of stride 0: every number names the same matrices
+    rng = np.random.default_rng(38)
+    for M in (20, 300):
+        X, W, LA, LB = operands(rng, M, 136, 264, 16, 1, "bf16", (1, 1, 1))
+        LA, LB = LA.expand(5, 136, 16), LB.expand(5, 16, 264)
+        ids = torch.from_numpy(rng.integers(-1, 5, M).astype(np.int32)).cuda()
+        got = lib.gemm_lora(X, W, LA, LB, ids, out_dtype=torch.float32)
+        done()
+        ref, tol = lora_ref(X, W, LA, LB, ids, None, None, 0, "bf16", "f32")
+        assert_close(got, ref, tol, "f32")

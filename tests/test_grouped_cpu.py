@@ -118,3 +118,8 @@ def test_helpers_check_before_calling_the_library():
             lib.gemm_lora(**dict(dict(X=X, W=W, LA=LA, LB=LB, adapter_of_row=ids), **bad))
     with pytest.raises(TypeError):
         lib.group_rows(ids.long(), 3)
+    # all well but for the device: nothing reaches the library
+    for call in (lambda: lib.gemm_grouped(A, B, off), lambda: lib.gemm_grouped_wgrad(A, dY, off),
+                 lambda: lib.gemm_lora(X, W, LA, LB, ids), lambda: lib.group_rows(ids, 3)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
