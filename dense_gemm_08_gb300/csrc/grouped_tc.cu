@@ -41,10 +41,15 @@ constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 8;
 constexpr int kGatherWarps = 2;
 constexpr int kRingBytes = 7 * 32768;
+// lora, up to 128 rows (single CTAs): a shorter ring, and 128 registers (launch
+// bounds of 512 threads), leave room on each SM for a CTA of the kernel that
+// makes V, so that W streams from the start (64 rows, 4096 -> 14336: the CTAs
+// otherwise start 5 us later).
+constexpr int kShortRing = 5 * 32768;
 constexpr int kMaxSlots = 256;         // lora: adapters of a tile
 // ring + alignment + barriers + row numbers (gathers) or adapters (lora)
-constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kMaxSlots * 4;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+constexpr int smem_bytes(int ring) { return ring + 1024 + 1024 + kMaxSlots * 4; }
+static_assert(smem_bytes(kRingBytes) <= 227 * 1024, "shared memory of one CTA");
 
 // wgrad, few rows per group: the tile's epilogue, not its K loop, is the time.
 // Each epilogue warp then has two boxes for C and one for D (32 x 32 FP32) at
@@ -74,7 +79,7 @@ struct Args {
     int b_kmajor;               // rows
     int bn;                     // columns per tile (of the CTA or the pair)
     int am;                     // rows of D per CTA: 128, or 16 / 32 / 64 (single CTAs)
-    int stages;
+    int stages, ring_bytes;
     uint32_t stage_bytes, a_region;  // B starts a_region bytes into a stage
     int ab_format;
     int z_step;  // rows: 0 when all groups share one B
@@ -207,7 +212,7 @@ __device__ __noinline__ float lora_exact(const Args &a, int64_t i, int64_t n) {
 }
 
 template <int CG, int MODE, bool GATHER>
-__global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
+__global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE, GATHER>(), 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_a_rows,
                       const __grid_constant__ CUtensorMap map_b,
@@ -225,13 +230,13 @@ __global__ void __launch_bounds__(threads<MODE, GATHER>(), 1)
     // go[kGatherWarps][kMaxStages] producer -> gather warp, drain,
     // cbar[kEpiWarps][2] boxes of C loaded
     const uint32_t ring0 = smem_addr(ring);
-    const uint32_t full0 = ring0 + kRingBytes, empty0 = full0 + 8 * kMaxStages;
+    const uint32_t full0 = ring0 + args.ring_bytes, empty0 = full0 + 8 * kMaxStages;
     const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16;
     const uint32_t go0 = tempty0 + 16, drain = go0 + 8 * kGatherWarps * kMaxStages;
     const uint32_t cbar0 = drain + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + (cbar0 + 16 * kEpiWarps - ring0));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *numbers = reinterpret_cast<int *>(ring + kRingBytes + 1024);  // [kMaxSlots]
+    int *numbers = reinterpret_cast<int *>(ring + args.ring_bytes + 1024);  // [kMaxSlots]
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
@@ -907,11 +912,11 @@ struct DeviceInfo {
 DeviceInfo g_dev[kMaxDevices];
 
 template <int CG, int MODE, bool GATHER>
-cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t config(int grid, int ring, cudaStream_t stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(threads<MODE, GATHER>(), 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(ring));
     cfg.stream = stream;
     cfg.attrs = attr;
     set_pdl_attribute(&attr[0]);
@@ -926,7 +931,8 @@ cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute *at
 template <int CG, int MODE, bool GATHER>
 cudaError_t allow_smem() {
     return cudaFuncSetAttribute(grouped_tc_kernel<CG, MODE, GATHER>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem_bytes(kRingBytes));
 }
 
 DeviceInfo *device_info() {
@@ -945,7 +951,7 @@ DeviceInfo *device_info() {
             if (d->err == cudaSuccess) d->err = e;
         if (d->err != cudaSuccess) return;
         cudaLaunchAttribute attr[2];
-        cudaLaunchConfig_t cfg = config<2, kRows, false>(2 * (d->sms / 2), 0, attr);
+        cudaLaunchConfig_t cfg = config<2, kRows, false>(2 * (d->sms / 2), kRingBytes, 0, attr);
         cfg.attrs = attr + 1;  // the occupancy query takes the cluster shape only
         cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&d->pairs, grouped_tc_kernel<2, kRows, false>, &cfg) !=
@@ -965,12 +971,12 @@ cudaError_t launch(const CUtensorMap (&maps)[8], const Args &a, bool gather, int
     cudaLaunchAttribute attr[2];
     if constexpr (MODE == kRows && CG == 1) {
         if (gather) {
-            cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, stream, attr);
+            cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, a.ring_bytes, stream, attr);
             return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
                                       maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], a);
         }
     }
-    cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, stream, attr);
+    cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, a.ring_bytes, stream, attr);
     return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, false>, maps[0], maps[1], maps[2],
                               maps[3], maps[4], maps[5], maps[6], maps[7], a);
 }
@@ -982,14 +988,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 128-row A operand runs on into B and the next stages: stale rows, which
 // reach only accumulator rows that are not stored.  The last stage keeps 128
 // rows inside the ring.  ksub blocks of 64 of K share a stage (see sub_blocks).
-void set_tile(Args &a, int cg, int am, int bn, int ksub = 1) {
+void set_tile(Args &a, int cg, int am, int bn, int ksub = 1, int ring = kRingBytes) {
+    a.ring_bytes = ring;
     a.am = am;
     a.bn = bn;
     a.ksub = ksub;
     a.a_region = static_cast<uint32_t>(am * ksub) * BK * 2;
     a.stage_bytes = a.a_region + static_cast<uint32_t>(bn / cg * ksub) * BK * 2;
     const int over = BM * BK * 2 - static_cast<int>(a.stage_bytes);
-    const int fit = (kRingBytes - (over > 0 ? over : 0)) / static_cast<int>(a.stage_bytes);
+    const int fit = (ring - (over > 0 ? over : 0)) / static_cast<int>(a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 }
 
@@ -1284,7 +1291,8 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         const int64_t per_row = d->sms / ceil_div(p.M, am) > 0 ? d->sms / ceil_div(p.M, am) : 1;
         int64_t bn = ceil_div(ceil_div(p.N, per_row), step) * step;
         if (bn > 256) bn = 256;
-        set_tile(a, 1, am, static_cast<int>(bn), sub_blocks(p.K, am, static_cast<int>(bn)));
+        set_tile(a, 1, am, static_cast<int>(bn), sub_blocks(p.K, am, static_cast<int>(bn)),
+                 p.M <= BM ? kShortRing : kRingBytes);
     }
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));

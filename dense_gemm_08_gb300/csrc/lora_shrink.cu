@@ -621,14 +621,25 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     std::call_once(g_once[dev], [dev] {
         g_err[dev] = cudaFuncSetAttribute(lora_shrink_tc_kernel,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        // the split of the SM's memory that the second product's kernel needs: an
+        // SM changes it only when it is empty, and both are to run on it at once
+        if (g_err[dev] == cudaSuccess)
+            g_err[dev] = cudaFuncSetAttribute(lora_shrink_rows_kernel<0>,
+                                              cudaFuncAttributePreferredSharedMemoryCarveout,
+                                              cudaSharedmemCarveoutMaxShared);
+        if (g_err[dev] == cudaSuccess)
+            g_err[dev] = cudaFuncSetAttribute(lora_shrink_rows_kernel<1>,
+                                              cudaFuncAttributePreferredSharedMemoryCarveout,
+                                              cudaSharedmemCarveoutMaxShared);
         if (g_err[dev] == cudaSuccess)
             g_err[dev] = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
     });
     if (g_err[dev] != cudaSuccess) return g_err[dev];
     if (p.M <= kRowsMax) {
-        // at least 512 of K per CTA (two loads of latency); the second product's
-        // CTAs start on each SM as these leave it
-        const int64_t ks = p.K / 512;
+        // at least 512 of K per CTA, and no more CTAs than SMs: one leaves room
+        // on its SM for a CTA of the second product's kernel, which streams W
+        // meanwhile
+        const int64_t ks = p.K / 512 < g_sms[dev] / p.M ? p.K / 512 : g_sms[dev] / p.M;
         a.ks = static_cast<int>(ks < 1 ? 1 : (ks > kMaxCluster ? kMaxCluster : ks));
         attr[1].val.clusterDim.x = static_cast<unsigned>(a.ks);
         cfg.gridDim = dim3(static_cast<unsigned>(p.M * a.ks), 1, 1);
