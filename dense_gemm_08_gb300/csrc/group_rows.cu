@@ -30,7 +30,7 @@ namespace {
 constexpr int THREADS = 1024, WARPS = 32;
 constexpr int kGroupsPass = 1024;  // 32 rows of counters: 128 KiB of shared memory at most
 constexpr int kUnroll = 4;         // row numbers loaded ahead per lane
-constexpr int64_t kOneCta = 4096;  // rows one CTA takes alone
+constexpr int64_t kOneCta = 2048;  // rows one CTA takes alone
 constexpr int kMaxCtas = 128;
 
 struct GroupRowsArgs {
@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(THREADS) group_place_kernel(const GroupRowsArg
     extern __shared__ int smem[];
     int *const counts = smem;                         // [WARPS][pass_groups]
     int *const base = smem + WARPS * a.pass_groups;   // [pass_groups] first place of this CTA
+    int *const parts = base + a.pass_groups;          // [2][THREADS] (several CTAs)
     __shared__ int warp_sum[WARPS];
     pdl_wait();
     pdl_launch_dependents();
@@ -83,41 +84,71 @@ __global__ void __launch_bounds__(THREADS) group_place_kernel(const GroupRowsArg
         const int gc = static_cast<int>(a.groups - gb < a.pass_groups ? a.groups - gb : a.pass_groups);
         for (int g = lane; g < gc; g += 32) mine[g] = 0;
         __syncwarp();
-        for (int64_t i0 = first; i0 < end; i0 += 32 * kUnroll) {
-            int key[kUnroll];
+        // a step: kUnroll times 32 rows, their numbers in this pass and the
+        // lanes with the same number
+        int key[kUnroll];
+        uint32_t same[kUnroll], dropped = 0;
+        auto load = [&](int64_t i0) {
+            dropped = 0;
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int64_t i = i0 + u * 32 + lane;
-                const int64_t id = i < end ? static_cast<int64_t>(a.ids[i]) - gb : -1;
-                key[u] = id >= 0 && id < gc ? static_cast<int>(id) : -1;
+                const int64_t id = i < end ? static_cast<int64_t>(a.ids[i]) : -1;
+                key[u] = id >= gb && id < gb + gc ? static_cast<int>(id - gb) : -1;
+                if (id < 0 || id >= a.groups) dropped |= 1u << u;
             }
 #pragma unroll
+            for (int u = 0; u < kUnroll; ++u) same[u] = __match_any_sync(0xffffffffu, key[u]);
+        };
+        const bool one_step = a.run <= 32 * kUnroll;  // kept for the second walk
+        for (int64_t i0 = first; i0 < end; i0 += 32 * kUnroll) {
+            load(i0);
+#pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const uint32_t same = __match_any_sync(0xffffffffu, key[u]);
-                if (key[u] >= 0 && (same & below_me) == 0) mine[key[u]] += __popc(same);
+                if (key[u] >= 0 && (same[u] & below_me) == 0) mine[key[u]] += __popc(same[u]);
                 __syncwarp();
             }
         }
         // rows of group gb + tid (pass_groups <= THREADS) in all CTAs and in
-        // the ones before this; independent of the counters
+        // the ones before this.  The threads split the CTAs: segment tid / wide
+        // takes every (THREADS / wide)-th, all its loads in flight.
         int all = 0, before = 0;
-        if (!ONE && tid < gc) {
-            const int32_t *c = a.counts + gb + tid;
+        if constexpr (!ONE) {
+            int wide = 32;
+            while (wide < gc) wide *= 2;
+            const int g = tid % wide, segs = THREADS / wide;
+            int part_all = 0, part_before = 0;
+            if (g < gc) {
+                const int32_t *c = a.counts + gb + g;
 #pragma unroll 8
-            for (int k = 0; k < static_cast<int>(gridDim.x); ++k) {
-                const int v = c[k * a.groups];
-                all += v;
-                if (k < cta) before += v;
+                for (int k = tid / wide; k < static_cast<int>(gridDim.x); k += segs) {
+                    const int v = c[k * a.groups];
+                    part_all += v;
+                    if (k < cta) part_before += v;
+                }
             }
+            parts[tid] = part_all;
+            parts[THREADS + tid] = part_before;
+            __syncthreads();
+            if (tid < gc)
+                for (int k = 0; k < segs; ++k) {
+                    all += parts[k * wide + tid];
+                    before += parts[THREADS + k * wide + tid];
+                }
         }
         __syncthreads();
         for (int g = tid; g < gc; g += THREADS) {
             int run = 0;
+#pragma unroll 1
+            for (int w0 = 0; w0 < WARPS; w0 += 8) {  // eight loads before the first store
+                int c[8];
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const int c = counts[w * a.pass_groups + g];
-                counts[w * a.pass_groups + g] = run;
-                run += c;
+                for (int w = 0; w < 8; ++w) c[w] = counts[(w0 + w) * a.pass_groups + g];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    counts[(w0 + w) * a.pass_groups + g] = run;
+                    run += c[w];
+                }
             }
             if (ONE) all = run;
         }
@@ -147,29 +178,20 @@ __global__ void __launch_bounds__(THREADS) group_place_kernel(const GroupRowsArg
         done += warp_sum[WARPS - 1];
         __syncthreads();
         for (int64_t i0 = first; i0 < end; i0 += 32 * kUnroll) {
-            int key[kUnroll];
-            uint32_t dropped = 0;
+            if (!one_step) load(i0);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int64_t i = i0 + u * 32 + lane;
-                const int64_t id = i < end ? static_cast<int64_t>(a.ids[i]) : -1;
-                key[u] = id >= gb && id < gb + gc ? static_cast<int>(id - gb) : -1;
-                if (id < 0 || id >= a.groups) dropped |= 1u << u;
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t i = i0 + u * 32 + lane;
-                const uint32_t same = __match_any_sync(0xffffffffu, key[u]);
                 int place = -1;
                 if (key[u] >= 0) {
-                    place = base[key[u]] + mine[key[u]] + __popc(same & below_me);
+                    place = base[key[u]] + mine[key[u]] + __popc(same[u] & below_me);
                     a.order[place] = static_cast<int32_t>(i);
                 }
                 if (a.position != nullptr && i < end &&
                     (key[u] >= 0 || (gb == 0 && ((dropped >> u) & 1u))))
                     a.position[i] = place;
                 __syncwarp();
-                if (key[u] >= 0 && (same & below_me) == 0) mine[key[u]] += __popc(same);
+                if (key[u] >= 0 && (same[u] & below_me) == 0) mine[key[u]] += __popc(same[u]);
                 __syncwarp();
             }
         }
@@ -209,10 +231,10 @@ cudaError_t launch_group_rows(int64_t rows, int64_t groups, const int32_t *group
     a.order = order;
     a.position = position;
     a.pass_groups = static_cast<int>(groups < kGroupsPass ? groups : kGroupsPass);
-    const size_t smem = static_cast<size_t>(WARPS + 1) * a.pass_groups * sizeof(int);
     const bool one = rows <= kOneCta;
+    const size_t smem = (static_cast<size_t>(WARPS + 1) * a.pass_groups + (one ? 0 : 2 * THREADS)) * sizeof(int);
     if (smem > 48 * 1024) {
-        const int most = static_cast<int>((WARPS + 1) * kGroupsPass * sizeof(int));
+        const int most = static_cast<int>(((WARPS + 1) * kGroupsPass + 2 * THREADS) * sizeof(int));
         const cudaError_t e =
             one ? cudaFuncSetAttribute(group_place_kernel<true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, most)

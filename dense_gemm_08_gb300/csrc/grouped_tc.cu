@@ -63,7 +63,7 @@ static_assert(kStagedRing + kBoxBytes <= kRingBytes, "ring and boxes");
 // the copies of whole boxes.
 template <int MODE, bool GATHER>
 constexpr int threads() {
-    return 64 + 32 * kEpiWarps + (GATHER || MODE == kWgrad ? 32 * kGatherWarps : 0);
+    return 64 + 32 * kEpiWarps + (GATHER || MODE == kWgrad ? 32 * kGatherWarps : MODE == kLora ? 32 : 0);
 }
 
 struct Args {
@@ -84,6 +84,7 @@ struct Args {
     int ab_format;
     int z_step;  // rows: 0 when all groups share one B
     int lb_z_step;  // lora: likewise for LB
+    int slice_warp;  // lora: at most one tile per CTA, see slice_copies
     int late_wait;  // lora: the kernel before this one wrote nothing but the plan
     LoraPlan plan;  // lora (count null: no adapters)
     LoraProblem l;  // lora: operands of the exact recomputation
@@ -176,6 +177,36 @@ __device__ __forceinline__ int first_block(uint32_t w, int nkb, bool reverse) {
 template <int CG>
 __device__ __forceinline__ int next_block(int kb, int nkb, bool reverse) {
     return CG == 2 && reverse ? kb - 1 : (kb + 1 == nkb ? 0 : kb + 1);
+}
+
+// lora, second product: the adapters and first columns of LA of the (up to four)
+// 16-row slices from column c0 of V on; all lanes get all of them.  (The
+// rounding's remainders meet the same rows of LB again.)
+__device__ __forceinline__ void slice_rows(const LoraPlan &pl, const int *numbers, int c0, int slices,
+                                           int (&ads)[4], int (&j0s)[4]) {
+    const int lane = threadIdx.x % 32;
+    int ad = 0, j0 = 0;
+    if (lane < slices) {
+        const int c = c0 + lane * 16, slot = c / pl.rc;
+        ad = numbers[slot];
+        j0 = (c - slot * pl.rc) & (pl.r_pad - 1);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        ads[q] = __shfl_sync(0xffffffffu, ad, q);
+        j0s[q] = __shfl_sync(0xffffffffu, j0, q);
+    }
+}
+
+// One slice of LB: 16 rows of adapter ad, the tile's columns.
+template <int CG>
+__device__ __forceinline__ void slice_copies(const Args &a, const CUtensorMap *map, uint32_t dst,
+                                             int b_rows, int32_t b0, int j0, int ad, uint32_t fb) {
+    if (a.l.b_kmajor) {
+        tma_load_3d<CG>(dst, map, j0, b0, ad, fb);
+    } else {
+        for (int j = 0; j < b_rows; j += 64) tma_load_3d<CG>(dst + j * 32, map, b0 + j, j0, ad, fb);
+    }
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
@@ -357,22 +388,11 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                     const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
                     const uint32_t v_bytes = static_cast<uint32_t>(args.am) * 128u;
                     const uint32_t v_tx = v_bytes + (CG == 2 && cta_rows(t, 1) > 0 ? v_bytes : 0u);
+                    if (args.slice_warp && elect_one()) mbar_arrive(go0);
                     for (int c0 = 0; c0 < cols; c0 += BK) {
                         const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
-                        // lane q: the adapter and first column of LA of slice q (the
-                        // rounding's remainders meet the same rows of LB again)
-                        int ad = 0, j0 = 0;
-                        if (lane < slices) {
-                            const int c = c0 + lane * 16, slot = c / pl.rc;
-                            ad = numbers[slot];
-                            j0 = (c - slot * pl.rc) & (pl.r_pad - 1);
-                        }
                         int ads[4], j0s[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            ads[q] = __shfl_sync(0xffffffffu, ad, q);
-                            j0s[q] = __shfl_sync(0xffffffffu, j0, q);
-                        }
+                        slice_rows(pl, numbers, c0, slices, ads, j0s);
                         ok = wait_all(empty0 + 8 * stage, phase ^ 1);
                         if (!ok) break;
                         const uint32_t fb = count0 + 8 * stage;
@@ -382,16 +402,10 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                                 mbar_arrive_expect_tx(full0 + 8 * stage, v_tx + CG * slices * slice_bytes);
                             if (mine > 0) tma_load_2d<CG>(sa, &map_v, c0, m0, fb);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if (q >= slices) break;
-                                const uint32_t dst = sb + q * slice_bytes;
-                                if (args.l.b_kmajor) {
-                                    tma_load_3d<CG>(dst, &map_b_rows, j0s[q], b0, ads[q], fb);
-                                } else {
-                                    for (int j = 0; j < b_rows; j += 64)
-                                        tma_load_3d<CG>(dst + j * 32, &map_b_rows, b0 + j, j0s[q], ads[q], fb);
-                                }
-                            }
+                            for (int q = 0; q < 4; ++q)
+                                if (q < slices && (q < 2 || !args.slice_warp))
+                                    slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0,
+                                                     j0s[q], ads[q], fb);
                         }
                         advance();
                     }
@@ -553,6 +567,42 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                 if (!wait_bounded(drain, 0, &never, args.timeout_ns)) raise_abort(abort_flag);
             }
             aborted = !ok;
+        }
+        __syncwarp();
+    } else if (MODE == kLora && warp >= 2 + kEpiWarps) {
+        // ------------------------------------------------- slice warp (the last)
+        // A decode step has many slices, 100 ns each to issue: this warp issues
+        // every second pair of them.  It joins the producer at the first block
+        // of V (go), waits for the same stages from there on and cannot run
+        // ahead of the ring: a CTA has one tile here.
+        if (args.slice_warp && tiles.get(first_tile, t) &&
+            __all_sync(0xffffffffu, wait_bounded(go0, 0, abort_flag, args.timeout_ns))) {
+            if (late) pdl_wait();
+            const LoraPlan &pl = args.plan;
+            const int cols = pl.count[t.tile_m] * pl.rc;
+            const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+            const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
+            // (numbers was written by the producer before it arrived on go)
+            int stage = t.nkb % stages;
+            uint32_t phase = static_cast<uint32_t>(t.nkb / stages) & 1u;
+            for (int c0 = 0; c0 < cols; c0 += BK) {
+                const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                int ads[4], j0s[4];
+                slice_rows(pl, numbers, c0, slices, ads, j0s);
+                if (!wait_all(empty0 + 8 * stage, phase ^ 1)) break;
+                const uint32_t sb = ring0 + stage * stage_bytes + a_region;
+                if (elect_one()) {
+#pragma unroll
+                    for (int q = 2; q < 4; ++q)
+                        if (q < slices)
+                            slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0, j0s[q],
+                                             ads[q], count0 + 8 * stage);
+                }
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
         }
         __syncwarp();
     } else if (warp >= 2 + kEpiWarps) {
@@ -1380,6 +1430,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
             break;
         }
         const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+        a.slice_warp = !pair && p.adapters > 0 && tiles <= d->sms;
         e = pair ? launch<2, kLora>(maps, a, false, tiles, d, stream)
                  : launch<1, kLora>(maps, a, false, tiles, d, stream);
     }
