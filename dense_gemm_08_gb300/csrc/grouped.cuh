@@ -16,8 +16,8 @@ namespace gemm {
 // at a time (one load and one warp scan per 32 groups), so a tile's group is
 // found without a table in shared memory and without the host knowing the
 // sizes.  Offsets count as the largest clamped value so far, so groups never
-// share a row, whatever the values.  locate() must be called by the whole warp, with tile numbers that
-// never fall.
+// share a row, whatever the values.  locate() must be called by the whole
+// warp, with tile numbers that never fall.
 struct GroupWalk {
     const int32_t *offsets;
     int groups;

@@ -10,7 +10,7 @@
 //   lora:   one group of M rows; the epilogue adds s_a * sum_c U(r, c) LB_a(c, j),
 //           with U = X LA (FP32, from lora_shrink_simt) and each row's own
 //           adapter, so no row ever reads another row's adapter.
-// Slices 16 deep in K go through shared memory as FP32, the next one loaded
+// Slices 32 deep in K go through shared memory as FP32, the next one loaded
 // into registers while the current one is multiplied.  The arithmetic is FP32
 // FMAs two rows at a time (fma.rn.f32x2, each half rounded as fmaf; products
 // of 16-bit values are exact): 16 of them per thread and step of K against 3
@@ -450,7 +450,7 @@ bool rows_on(const void *p, int64_t ld, int64_t stride, int64_t elt, int64_t byt
 // CTAs that share a tile's K: two CTAs are resident per SM, so a few tiles
 // more than 2 x SMs would take twice as long; up to 8 parts (each at least 128
 // of K) while there are fewer than 12 per SM.  (16 groups, 2000 rows, 1000 x
-// 1024, 320 tiles: 164 us in one part, see the launcher for the split.)
+// 1024, 320 tiles: 164 us in one part, 129 split.)
 int k_parts(int64_t tiles, int64_t k) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -1132,11 +1132,12 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
         set_tile(a, 2, BM, 256);
     } else {
         // Few rows per group: the weights are the time; narrow tiles and few
-        // rows per tile (64 groups, 128 rows, 4096 x 2048: 160 us with 16 rows,
-        // 168 with 64; 32 groups of 32 rows: 90 us with 32, 101 with 128).  A
-        // group's further rows read the weights again, from L2.
+        // rows per tile (32 groups of 32 rows, 4096 x 2048: 90 us with 32, 101
+        // with 128).  A group's further rows read the weights again, from L2:
+        // 16 rows gain 2 % for groups of two rows and lose 6 % when they are
+        // uneven (64 groups, 128 rows).
         const int64_t mean = ceil_div(p.rows, live);
-        const int am = mean <= 4 ? 16 : (mean <= 12 ? 32 : (mean <= 32 ? 64 : BM));
+        const int am = mean <= 12 ? 32 : (mean <= 32 ? 64 : BM);
         const int64_t row_tiles = live * ceil_div(mean, am);
         int bn = 256;
         if (am < BM) {
