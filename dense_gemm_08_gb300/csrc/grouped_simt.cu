@@ -25,8 +25,12 @@ namespace gemm {
 namespace {
 
 constexpr int TM = 64, TN = 128, TK = 32, THREADS = 256;
-constexpr int LA = TM + 4, LB = TN + 4;  // rows of a slice in shared memory
-constexpr int kSmemBytes = 2 * TK * (LA + LB) * 4;
+constexpr int kSmemBytes = 2 * TK * (TM + TN) * 4;
+
+// Where four values from column q (a multiple of 4) of step k of a slice are:
+// the quads of a row change places with k / 4, so that a warp that stores
+// quads along K as columns meets every bank once.
+__device__ __forceinline__ int spot(int k, int q) { return q ^ (k / 4 % 8 * 4); }
 
 template <typename T>
 __device__ __forceinline__ float widened(const T *p);
@@ -182,8 +186,8 @@ __device__ __forceinline__ void finish_quad(const SimtGroupedArgs &a, int g, int
 template <typename T, int MODE>
 __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGroupedArgs a) {
     extern __shared__ float4 smem4[];
-    float(*As)[TK][LA] = reinterpret_cast<float(*)[TK][LA]>(smem4);
-    float(*Bs)[TK][LB] = reinterpret_cast<float(*)[TK][LB]>(reinterpret_cast<float *>(smem4) + 2 * TK * LA);
+    float(*As)[TK][TM] = reinterpret_cast<float(*)[TK][TM]>(smem4);
+    float(*Bs)[TK][TN] = reinterpret_cast<float(*)[TK][TN]>(reinterpret_cast<float *>(smem4) + 2 * TK * TM);
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -285,9 +289,9 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         for (int q = 0; q < 2; ++q) {
             const int i = tid + q * THREADS;
             if constexpr (MODE == kWgrad) {
-                *reinterpret_cast<float4 *>(&As[s][i / 16][(i % 16) * 4]) = a_next[q];
+                *reinterpret_cast<float4 *>(&As[s][i / 16][spot(i / 16, (i % 16) * 4)]) = a_next[q];
             } else {
-                const int r = i / 8, k = (i % 8) * 4;
+                const int k = (i % 8) * 4, r = spot(k, i / 8);
                 As[s][k + 0][r] = a_next[q].x;
                 As[s][k + 1][r] = a_next[q].y;
                 As[s][k + 2][r] = a_next[q].z;
@@ -298,19 +302,20 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         for (int q = 0; q < 4; ++q) {
             const int i = tid + q * THREADS;
             if (b_kmajor) {
-                const int n = i / 8, k = (i % 8) * 4;
+                const int k = (i % 8) * 4, n = spot(k, i / 8);
                 Bs[s][k + 0][n] = b_next[q].x;
                 Bs[s][k + 1][n] = b_next[q].y;
                 Bs[s][k + 2][n] = b_next[q].z;
                 Bs[s][k + 3][n] = b_next[q].w;
             } else {
-                *reinterpret_cast<float4 *>(&Bs[s][i / 32][(i % 32) * 4]) = b_next[q];
+                *reinterpret_cast<float4 *>(&Bs[s][i / 32][spot(i / 32, (i % 32) * 4)]) = b_next[q];
             }
         }
     };
 
     // rows ty * 8 .. + 7 in pairs; columns tx * 4 .. + 3
-    const int tx = tid % 32, ty = tid / 32;
+    // (a warp's block is 16 x 64)
+    const int tx = tid / 32 % 2 * 16 + tid % 16, ty = tid / 64 * 2 + tid / 16 % 2;
     uint64_t acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -328,10 +333,10 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
 #pragma unroll
         for (int k = 0; k < TK; ++k) {
             uint64_t av[4], bv[4];
-            const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][ty * 8]);
-            const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][ty * 8 + 4]);
+            const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][spot(k, ty * 8)]);
+            const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][spot(k, ty * 8 + 4)]);
             av[0] = a0.x, av[1] = a0.y, av[2] = a1.x, av[3] = a1.y;
-            const float4 b = *reinterpret_cast<const float4 *>(&Bs[s][k][tx * 4]);
+            const float4 b = *reinterpret_cast<const float4 *>(&Bs[s][k][spot(k, tx * 4)]);
             bv[0] = pair(b.x, b.x), bv[1] = pair(b.y, b.y);
             bv[2] = pair(b.z, b.z), bv[3] = pair(b.w, b.w);
 #pragma unroll
@@ -363,8 +368,8 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
     }
     // the parts meet in the cluster's shared memory, each CTA adding a share of
     // the rows in rank order (the slices are no longer needed)
-    float(*part)[LB] = reinterpret_cast<float(*)[LB]>(smem4);
-    static_assert(TM * LB * 4 <= kSmemBytes, "a tile of sums replaces the slices");
+    float(*part)[TN] = reinterpret_cast<float(*)[TN]>(smem4);
+    static_assert(TM * TN * 4 <= kSmemBytes, "a tile of sums replaces the slices");
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         *reinterpret_cast<float4 *>(&part[ty * 8 + i][tx * 4]) = sums(i);
