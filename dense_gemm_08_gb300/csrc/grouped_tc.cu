@@ -6,14 +6,14 @@
 //
 // Persistent CTAs (or CTA pairs) walk the tiles of all groups; a tile belongs
 // to one group.  The sizes of the groups are on the device only: each warp
-// finds a tile's group with a warp scan over the offsets (GroupWalk).  Warp 0
-// fills a ring of 128-byte-swizzled stages by TMA, warp 1 issues tcgen05.mma
-// into one of two TMEM accumulators, warps 2-9 write the other to D.
+// finds a tile's group with a warp scan over the offsets (GroupWalk).  One warp
+// fills a ring of 128-byte-swizzled stages by TMA, one issues tcgen05.mma into
+// one of two TMEM accumulators, eight write the other to D.
 //
 //   rows: a row tile may end inside the next group's rows.  They only reach
 //     accumulator rows that are not stored (each row of D depends on its own
 //     row of A), so no zero fill is needed.  Gathered rows come four at a time
-//     by TMA gather (warps 10 and 11).
+//     by TMA gather, issued by two warps of their own.
 //   wgrad: both operands have their rows along K and are MN-major.  A group's
 //     last K block must not read the next group's rows (not even times zero:
 //     they may be infinite), so that block is fetched by TMA gather with row
@@ -52,18 +52,47 @@ constexpr int smem_bytes(int ring) { return ring + 1024 + 1024 + kMaxSlots * 4; 
 static_assert(smem_bytes(kRingBytes) <= 227 * 1024, "shared memory of one CTA");
 
 // wgrad, few rows per group: the tile's epilogue, not its K loop, is the time.
-// Each epilogue warp then has two boxes for C and one for D (32 x 32 FP32) at
-// the end of the ring's memory, filled and emptied by TMA: a block costs some
-// 60 instructions instead of about 500.  The ring keeps four stages.
-constexpr int kBoxBytes = kEpiWarps * 3 * 4096;
-constexpr int kStagedRing = 4 * 32768;
-static_assert(kStagedRing + kBoxBytes <= kRingBytes, "ring and boxes");
+// D then goes out through a box of 32 x 32 FP32 per epilogue warp in shared
+// memory, and C comes in through two more: a block costs some 60 instructions
+// instead of about 500.  The boxes take the end of the ring's memory, which
+// keeps six stages, four with C (16 groups of 1024 rows, 4096 x 4096: BF16
+// gradients 303 us, 363 from registers with seven stages; FP32 with C 455).
+constexpr int kBoxes = 1, kBoxesC = 3;
+__host__ __device__ constexpr int box_bytes(int boxes) { return kEpiWarps * boxes * 4096; }
 
-// Gathers are issued by warps of their own, so that the producer goes on with
-// the copies of whole boxes.
-template <int MODE, bool GATHER>
+// Sums in parts.  The tensor cores cut what an addition to the accumulator
+// cannot hold (they do not round it): a long sum comes out too small, by 1e-9 of
+// itself per step of K (2e-5 after 16384), which an FP32 D shows.  Such a D is
+// summed kPart steps at a time, each part in the other accumulator, and the
+// epilogue warps add the parts in registers, rounded to nearest: 7e-7 off for
+// BF16 and 9e-7 for FP16 at any length.  The 128 registers per thread that this
+// takes come from the other warps.  It costs 3 to 10 % (8 groups, 16384 rows,
+// 4096 x 14336: 1105 us without parts, 1142 in parts of 1024, 1181 of 768, 1234
+// of 640; the 16384 x 4096 x 4096 product 317 and 338), for each part is read
+// in 1.4 us beside the multiplication of the next (3.4 us at 768).
+constexpr int kPart = 768;
+// The weight gradients' groups have any length: parts are made where the mean
+// is kPartsRows, below which the write of D is the time and the other kernel,
+// with its free registers, is 7 % faster (16 groups of 64 rows, 4096 x 4096: 201
+// and 215 us).
+constexpr int kPartsRows = 192;
+constexpr int kEpiRegs = 216, kOtherRegs = 72, kPartsRegs = 168;
+static_assert(2 * kEpiRegs + kOtherRegs <= 3 * kPartsRegs,
+              "three warpgroups share the launch's registers");
+
+// Warps 0-7: epilogue, 8: TMA, 9: MMA; 10 and 11, where there are any: gathers
+// (issued by warps of their own, so that the producer goes on with the copies
+// of whole boxes), or slices of LB (lora).
+constexpr int kProducer = kEpiWarps, kIssuer = kEpiWarps + 1, kHelper = kEpiWarps + 2;
+template <int MODE, bool GATHER, bool PARTS>
 constexpr int threads() {
-    return 64 + 32 * kEpiWarps + (GATHER || MODE == kWgrad ? 32 * kGatherWarps : MODE == kLora ? 32 : 0);
+    return PARTS ? 384
+                 : 64 + 32 * kEpiWarps +
+                       (GATHER || MODE == kWgrad ? 32 * kGatherWarps : MODE == kLora ? 32 : 0);
+}
+template <int CG, int MODE, bool GATHER, bool PARTS>
+constexpr int max_threads() {
+    return MODE == kLora && CG == 1 && !PARTS ? 512 : threads<MODE, GATHER, PARTS>();
 }
 
 struct Args {
@@ -74,8 +103,10 @@ struct Args {
     uint32_t tiles_m, tiles_n;  // tiles_m: wgrad only
     int num_kb;                 // rows, lora: K steps of a stage each
     int ksub;                   // rows, lora: blocks of 64 of K per stage
+    int part;                   // K steps per part of a sum (see kPart)
     int a_blocks, b_blocks;     // wgrad: whole 64-column blocks of A and B
-    int staged;                 // wgrad: D and C move as TMA boxes (see kBoxBytes)
+    int staged;                 // wgrad: D and C move as TMA boxes
+    int boxes;                  // per epilogue warp, at the ring's end (see kBoxes)
     int b_kmajor;               // rows
     int bn;                     // columns per tile (of the CTA or the pair)
     int am;                     // rows of D per CTA: 128, or 16 / 32 / 64 (single CTAs)
@@ -242,8 +273,8 @@ __device__ __noinline__ float lora_exact(const Args &a, int64_t i, int64_t n) {
     return s + u;
 }
 
-template <int CG, int MODE, bool GATHER>
-__global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE, GATHER>(), 1)
+template <int CG, int MODE, bool GATHER, bool PARTS>
+__global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_a_rows,
                       const __grid_constant__ CUtensorMap map_b,
@@ -294,7 +325,7 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
         if (MODE == kWgrad && args.staged) prefetch_map(&map_d);
         if (MODE == kWgrad && args.staged && args.out.beta != 0.f) prefetch_map(&map_c);
     }
-    if (warp == 1) tmem_alloc<CG>(smem_addr(tmem_slot));
+    if (warp == kIssuer) tmem_alloc<CG>(smem_addr(tmem_slot));
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
@@ -324,379 +355,400 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
         return done;
     };
 
-    if (warp == 0) {
-        // ---------------------------------------------------- TMA producer
-        int stage = 0;
-        uint32_t phase = 0;
-        uint32_t issued = 0;
-        bool ok = true;
-        auto advance = [&]() {
-            issued += issued < static_cast<uint32_t>(stages) ? 1u : 0u;
-            if (++stage == stages) {
-                stage = 0;
-                phase ^= 1;
-            }
-        };
-        bool reverse = false;
-        for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
-            const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
-            const int mine = cta_rows(t, rank);
-            const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
-            if constexpr (MODE != kWgrad) {
-                const uint32_t tx = a_bytes<GATHER>(args, cta_rows(t, 0)) +
-                                    (CG == 2 ? a_bytes<GATHER>(args, cta_rows(t, 1)) : 0u) +
-                                    static_cast<uint32_t>(CG * b_rows * ksub) * 128u;
-                const int32_t z = t.g * args.z_step;
-                int kb = first_block<CG>(w, t.nkb, reverse);
-                for (int i = 0; i < t.nkb; ++i) {
-                    ok = wait_all(empty0 + 8 * stage, phase ^ 1);
-                    if (!ok) break;
-                    const uint32_t fb = count0 + 8 * stage;
-                    const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
-                    if (elect_one()) {
-                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
-                        if constexpr (GATHER) {
-                            if (mine > 0) mbar_arrive(go0 + 8 * stage);
-                            if (mine > 64) mbar_arrive(go0 + 8 * (kMaxStages + stage));
+    if (warp >= kEpiWarps) {
+        if constexpr (PARTS)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kProducer) {
+            // ---------------------------------------------------- TMA producer
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t issued = 0;
+            bool ok = true;
+            auto advance = [&]() {
+                issued += issued < static_cast<uint32_t>(stages) ? 1u : 0u;
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            bool reverse = false;
+            for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
+                const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+                const int mine = cta_rows(t, rank);
+                const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
+                if constexpr (MODE != kWgrad) {
+                    const uint32_t tx = a_bytes<GATHER>(args, cta_rows(t, 0)) +
+                                        (CG == 2 ? a_bytes<GATHER>(args, cta_rows(t, 1)) : 0u) +
+                                        static_cast<uint32_t>(CG * b_rows * ksub) * 128u;
+                    const int32_t z = t.g * args.z_step;
+                    int kb = first_block<CG>(w, t.nkb, reverse);
+                    for (int i = 0; i < t.nkb; ++i) {
+                        ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+                        if (!ok) break;
+                        const uint32_t fb = count0 + 8 * stage;
+                        const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                        if (elect_one()) {
+                            if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
+                            if constexpr (GATHER) {
+                                if (mine > 0) mbar_arrive(go0 + 8 * stage);
+                                if (mine > 64) mbar_arrive(go0 + 8 * (kMaxStages + stage));
+                            }
+                            // several blocks of 64 at once: the maps count K in blocks
+                            const int32_t block = kb * ksub;
+                            const int32_t k_in = ksub > 1 ? 0 : block * BK, k_block = ksub > 1 ? block : 0;
+                            if (args.b_kmajor) {
+                                tma_load_4d<CG>(sb, &map_b, k_in, b0, k_block, z, fb);
+                            } else {
+                                for (int j = 0; j < b_rows; j += 64)
+                                    tma_load_3d<CG>(sb + j * 128 * ksub, &map_b, b0 + j, block * BK, z, fb);
+                            }
+                            if constexpr (!GATHER) {
+                                if (mine > 0) tma_load_3d<CG>(sa, &map_a, k_in, m0, k_block, fb);
+                            }
                         }
-                        // several blocks of 64 at once: the maps count K in blocks
-                        const int32_t block = kb * ksub;
-                        const int32_t k_in = ksub > 1 ? 0 : block * BK, k_block = ksub > 1 ? block : 0;
-                        if (args.b_kmajor) {
-                            tma_load_4d<CG>(sb, &map_b, k_in, b0, k_block, z, fb);
-                        } else {
-                            for (int j = 0; j < b_rows; j += 64)
-                                tma_load_3d<CG>(sb + j * 128 * ksub, &map_b, b0 + j, block * BK, z, fb);
-                        }
-                        if constexpr (!GATHER) {
-                            if (mine > 0) tma_load_3d<CG>(sa, &map_a, k_in, m0, k_block, fb);
+                        kb = next_block<CG>(kb, t.nkb, reverse);
+                        advance();
+                    }
+                    if (MODE == kLora && ok && args.plan.count != nullptr) {
+                        // the second product: V (128-byte rows of 64 columns) times
+                        // the slots' LB, fetched in 16-row slices of one adapter each
+                        if (late) pdl_wait();
+                        const LoraPlan &pl = args.plan;
+                        const int cols = pl.count[t.tile_m] * pl.rc;
+                        const int *list = pl.list + static_cast<int64_t>(t.tile_m) * pl.tile_rows;
+                        __syncwarp();
+                        for (int i = lane; i < cols / pl.rc; i += 32) numbers[i] = list[i] * args.lb_z_step;
+                        __syncwarp();
+                        const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
+                        const uint32_t v_bytes = static_cast<uint32_t>(args.am) * 128u;
+                        const uint32_t v_tx = v_bytes + (CG == 2 && cta_rows(t, 1) > 0 ? v_bytes : 0u);
+                        if (args.slice_warp && elect_one()) mbar_arrive(go0);
+                        for (int c0 = 0; c0 < cols; c0 += BK) {
+                            const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                            int ads[4], j0s[4];
+                            slice_rows(pl, numbers, c0, slices, ads, j0s);
+                            ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+                            if (!ok) break;
+                            const uint32_t fb = count0 + 8 * stage;
+                            const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                            if (elect_one()) {
+                                if (leader)
+                                    mbar_arrive_expect_tx(full0 + 8 * stage, v_tx + CG * slices * slice_bytes);
+                                if (mine > 0) tma_load_2d<CG>(sa, &map_v, c0, m0, fb);
+    #pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (q < slices && (q < 2 || !args.slice_warp))
+                                        slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0,
+                                                         j0s[q], ads[q], fb);
+                            }
+                            advance();
                         }
                     }
-                    kb = next_block<CG>(kb, t.nkb, reverse);
-                    advance();
-                }
-                if (MODE == kLora && ok && args.plan.count != nullptr) {
-                    // the second product: V (128-byte rows of 64 columns) times
-                    // the slots' LB, fetched in 16-row slices of one adapter each
-                    if (late) pdl_wait();
-                    const LoraPlan &pl = args.plan;
-                    const int cols = pl.count[t.tile_m] * pl.rc;
-                    const int *list = pl.list + static_cast<int64_t>(t.tile_m) * pl.tile_rows;
-                    __syncwarp();
-                    for (int i = lane; i < cols / pl.rc; i += 32) numbers[i] = list[i] * args.lb_z_step;
-                    __syncwarp();
-                    const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
-                    const uint32_t v_bytes = static_cast<uint32_t>(args.am) * 128u;
-                    const uint32_t v_tx = v_bytes + (CG == 2 && cta_rows(t, 1) > 0 ? v_bytes : 0u);
-                    if (args.slice_warp && elect_one()) mbar_arrive(go0);
-                    for (int c0 = 0; c0 < cols; c0 += BK) {
-                        const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
-                        int ads[4], j0s[4];
-                        slice_rows(pl, numbers, c0, slices, ads, j0s);
+                } else {
+                    const int b_blocks = b_rows / 64;
+                    for (int i = 0; i < t.nkb; ++i) {
+                        const int32_t r0 = t.first + i * BK;
+                        const int rem = t.last - r0 < BK ? t.last - r0 : BK;
+                        const int quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
+                        const bool part = rem < BK;
                         ok = wait_all(empty0 + 8 * stage, phase ^ 1);
                         if (!ok) break;
                         const uint32_t fb = count0 + 8 * stage;
                         const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
                         if (elect_one()) {
                             if (leader)
-                                mbar_arrive_expect_tx(full0 + 8 * stage, v_tx + CG * slices * slice_bytes);
-                            if (mine > 0) tma_load_2d<CG>(sa, &map_v, c0, m0, fb);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (q < slices && (q < 2 || !args.slice_warp))
-                                    slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0,
-                                                     j0s[q], ads[q], fb);
+                                mbar_arrive_expect_tx(
+                                    full0 + 8 * stage,
+                                    CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
+                            if (part) {
+                                for (int h = 0; h < kGatherWarps; ++h)
+                                    mbar_arrive(go0 + 8 * (h * kMaxStages + stage));
+                            }
+                            if (!part) {
+                                // whole 64-column blocks in one copy; a tile that holds
+                                // the columns past the last whole one, block by block
+                                if (m0 / 64 + 2 <= args.a_blocks) {
+                                    tma_load_3d<CG>(sa, &map_a, 0, r0, m0 / 64, fb);
+                                } else {
+                                    tma_load_2d<CG>(sa, &map_v, m0, r0, fb);
+                                    tma_load_2d<CG>(sa + 8192, &map_v, m0 + 64, r0, fb);
+                                }
+                                if (b0 / 64 + b_blocks <= args.b_blocks) {
+                                    tma_load_3d<CG>(sb, &map_b, 0, r0, b0 / 64, fb);
+                                } else {
+                                    for (int j = 0; j < b_blocks; ++j)
+                                        tma_load_2d<CG>(sb + j * 8192, &map_b_edge, b0 + 64 * j, r0, fb);
+                                }
+                            }
                         }
                         advance();
                     }
                 }
-            } else {
-                const int b_blocks = b_rows / 64;
-                for (int i = 0; i < t.nkb; ++i) {
-                    const int32_t r0 = t.first + i * BK;
-                    const int rem = t.last - r0 < BK ? t.last - r0 : BK;
-                    const int quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
-                    const bool part = rem < BK;
-                    ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+            }
+            __syncwarp();
+            // the copies in flight land before the CTA exits (the leader's
+            // barriers count both CTAs' bytes)
+            if (lane == 0 && leader) {
+                for (uint32_t i = 0; i < issued; ++i) {
+                    if (--stage < 0) {
+                        stage = stages - 1;
+                        phase ^= 1;
+                    }
+                    const volatile int never = 0;
+                    if (!wait_bounded(full0 + 8 * stage, phase, &never, args.timeout_ns))
+                        raise_abort(abort_flag);
+                }
+            }
+            aborted = !ok;
+            __syncwarp();
+        } else if (warp == kIssuer) {
+            // ------------------------------------------------------ MMA issuer
+            if (leader) {
+                const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
+                const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
+                const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring0, 0) : desc_kmajor(ring0, 0);
+                const uint64_t b_desc0 =
+                    b_mn ? smem_desc(ring0 + a_region, static_cast<uint32_t>(ksub) * 8192u, 1024)
+                         : desc_kmajor(ring0 + a_region, 0);
+                const uint64_t a_step = a_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+                const uint64_t b_step = b_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+                // a stage's blocks of 64: rows x 128 bytes apart (N-major: 64 rows of K)
+                const uint64_t a_sub = static_cast<uint64_t>(args.am) * 128u >> 4;
+                const uint64_t b_sub = b_mn ? 8192u >> 4 : static_cast<uint64_t>(b_rows) * 128u >> 4;
+                // lora: slices of LB -- K-major: 32-byte rows (32-byte swizzle);
+                // N-major: 16 rows per 64-column block (128-byte swizzle)
+                const bool lb_mn = MODE == kLora && !args.l.b_kmajor;
+                const uint32_t lb_idesc = make_idesc(BM * CG, args.bn, 0, lb_mn, args.ab_format);
+                const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
+                                                : smem_desc(ring0 + a_region, 16, 256, kSwizzle32);
+                const uint64_t stage_step = stage_bytes >> 4;
+                int stage = 0;
+                uint32_t phase = 0;
+                uint32_t acc = 0;  // accumulators filled so far
+                bool ok = true;
+                for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step) {
+                    if (MODE == kWgrad && t.nkb == 0) continue;  // no rows: nothing to add
+                    uint32_t d_tmem = 0;
+                    auto take = [&]() {  // the accumulator not filled last, once it has been read
+                        ok = wait_all(tempty0 + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1);
+                        tc_fence_after();
+                        d_tmem = tmem_base + (acc & 1) * 256;
+                    };
+                    take();
                     if (!ok) break;
-                    const uint32_t fb = count0 + 8 * stage;
-                    const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
-                    if (elect_one()) {
-                        if (leader)
-                            mbar_arrive_expect_tx(
-                                full0 + 8 * stage,
-                                CG * (2 + b_blocks) * static_cast<uint32_t>(quads) * 512u);
-                        if (part) {
-                            for (int h = 0; h < kGatherWarps; ++h)
-                                mbar_arrive(go0 + 8 * (h * kMaxStages + stage));
+                    int in_part = 0;
+                    // 16-row slices of the last block that hold rows
+                    const int last_slices =
+                        MODE == kWgrad ? (t.last - t.first - (t.nkb - 1) * BK + 15) / 16 : 4;
+                    for (int i = 0; i < t.nkb; ++i, ++in_part) {
+                        if (PARTS && in_part == args.part) {
+                            if (elect_one()) tc_commit<CG>(tfull0 + 8 * (acc & 1));
+                            ++acc;
+                            take();
+                            if (!ok) break;
+                            in_part = 0;
                         }
-                        if (!part) {
-                            // whole 64-column blocks in one copy; a tile that holds
-                            // the columns past the last whole one, block by block
-                            if (m0 / 64 + 2 <= args.a_blocks) {
-                                tma_load_3d<CG>(sa, &map_a, 0, r0, m0 / 64, fb);
-                            } else {
-                                tma_load_2d<CG>(sa, &map_v, m0, r0, fb);
-                                tma_load_2d<CG>(sa + 8192, &map_v, m0 + 64, r0, fb);
+                        ok = wait_all(full0 + 8 * stage, phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage) * stage_step;
+                        const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage) * stage_step;
+                        const int slices = MODE == kWgrad && i + 1 == t.nkb ? last_slices : 4;
+                        if (elect_one()) {
+                            tc_mma<CG>(d_tmem, ad, bd, idesc, in_part > 0 ? 1u : 0u);
+                            if (MODE != kWgrad || slices > 1)
+                                tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
+                            if (MODE != kWgrad || slices > 2)
+                                tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
+                            if (MODE != kWgrad || slices > 3)
+                                tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
+                            if constexpr (MODE != kWgrad) {
+                                for (int u = 1; u < ksub; ++u) {
+                                    const uint64_t au = ad + u * a_sub, bu = bd + u * b_sub;
+                                    tc_mma<CG>(d_tmem, au, bu, idesc, 1u);
+                                    tc_mma<CG>(d_tmem, au + a_step, bu + b_step, idesc, 1u);
+                                    tc_mma<CG>(d_tmem, au + 2 * a_step, bu + 2 * b_step, idesc, 1u);
+                                    tc_mma<CG>(d_tmem, au + 3 * a_step, bu + 3 * b_step, idesc, 1u);
+                                }
                             }
-                            if (b0 / 64 + b_blocks <= args.b_blocks) {
-                                tma_load_3d<CG>(sb, &map_b, 0, r0, b0 / 64, fb);
-                            } else {
-                                for (int j = 0; j < b_blocks; ++j)
-                                    tma_load_2d<CG>(sb + j * 8192, &map_b_edge, b0 + 64 * j, r0, fb);
+                            tc_commit<CG>(empty0 + 8 * stage);  // frees the stage (both CTAs)
+                        }
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (MODE == kLora && ok && args.plan.count != nullptr) {
+                        if (late) pdl_wait();
+                        const int cols = args.plan.count[t.tile_m] * args.plan.rc;
+                        const uint64_t slice_step = static_cast<uint64_t>(b_rows) * 32u >> 4;
+                        for (int c0 = 0; c0 < cols; c0 += BK) {
+                            ok = wait_all(full0 + 8 * stage, phase);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                            const uint64_t at = static_cast<uint64_t>(stage) * stage_step;
+                            if (elect_one()) {
+                                for (int q = 0; q < slices; ++q)
+                                    tc_mma<CG>(d_tmem, a_desc0 + at + q * a_step,
+                                               lb_desc0 + at + q * slice_step, lb_idesc, 1u);
+                                tc_commit<CG>(empty0 + 8 * stage);
+                            }
+                            if (++stage == stages) {
+                                stage = 0;
+                                phase ^= 1u;
                             }
                         }
                     }
-                    advance();
-                }
-            }
-        }
-        __syncwarp();
-        // the copies in flight land before the CTA exits (the leader's
-        // barriers count both CTAs' bytes)
-        if (lane == 0 && leader) {
-            for (uint32_t i = 0; i < issued; ++i) {
-                if (--stage < 0) {
-                    stage = stages - 1;
-                    phase ^= 1;
-                }
-                const volatile int never = 0;
-                if (!wait_bounded(full0 + 8 * stage, phase, &never, args.timeout_ns))
-                    raise_abort(abort_flag);
-            }
-        }
-        aborted = !ok;
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer
-        if (leader) {
-            const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
-            const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
-            const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring0, 0) : desc_kmajor(ring0, 0);
-            const uint64_t b_desc0 =
-                b_mn ? smem_desc(ring0 + a_region, static_cast<uint32_t>(ksub) * 8192u, 1024)
-                     : desc_kmajor(ring0 + a_region, 0);
-            const uint64_t a_step = a_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
-            const uint64_t b_step = b_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
-            // a stage's blocks of 64: rows x 128 bytes apart (N-major: 64 rows of K)
-            const uint64_t a_sub = static_cast<uint64_t>(args.am) * 128u >> 4;
-            const uint64_t b_sub = b_mn ? 8192u >> 4 : static_cast<uint64_t>(b_rows) * 128u >> 4;
-            // lora: slices of LB -- K-major: 32-byte rows (32-byte swizzle);
-            // N-major: 16 rows per 64-column block (128-byte swizzle)
-            const bool lb_mn = MODE == kLora && !args.l.b_kmajor;
-            const uint32_t lb_idesc = make_idesc(BM * CG, args.bn, 0, lb_mn, args.ab_format);
-            const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
-                                            : smem_desc(ring0 + a_region, 16, 256, kSwizzle32);
-            const uint64_t stage_step = stage_bytes >> 4;
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t acc = 0;  // accumulators filled so far
-            bool ok = true;
-            for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step) {
-                if (MODE == kWgrad && t.nkb == 0) continue;  // no rows: nothing to add
-                const uint32_t buf = acc & 1;
-                ok = wait_all(tempty0 + 8 * buf, ((acc >> 1) & 1) ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + buf * 256;
-                // 16-row slices of the last block that hold rows
-                const int last_slices =
-                    MODE == kWgrad ? (t.last - t.first - (t.nkb - 1) * BK + 15) / 16 : 4;
-                for (int i = 0; i < t.nkb; ++i) {
-                    ok = wait_all(full0 + 8 * stage, phase);
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage) * stage_step;
-                    const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage) * stage_step;
-                    const int slices = MODE == kWgrad && i + 1 == t.nkb ? last_slices : 4;
+                    if (elect_one()) tc_commit<CG>(tfull0 + 8 * (acc & 1));
+                    ++acc;
+                }
+                __syncwarp();
+                // all MMAs issued here have finished once `drain` completes
+                if (elect_one()) {
+                    tc_commit_local<CG>(drain);
+                    const volatile int never = 0;
+                    if (!wait_bounded(drain, 0, &never, args.timeout_ns)) raise_abort(abort_flag);
+                }
+                aborted = !ok;
+            }
+            __syncwarp();
+        } else if (MODE == kLora && warp >= kHelper) {
+            // --------------------------------------------------------- slice warp
+            // A decode step has many slices, 100 ns each to issue: this warp issues
+            // every second pair of them.  It joins the producer at the first block
+            // of V (go), waits for the same stages from there on and cannot run
+            // ahead of the ring: a CTA has one tile here.
+            if (warp == kHelper && args.slice_warp && tiles.get(first_tile, t) &&
+                __all_sync(0xffffffffu, wait_bounded(go0, 0, abort_flag, args.timeout_ns))) {
+                if (late) pdl_wait();
+                const LoraPlan &pl = args.plan;
+                const int cols = pl.count[t.tile_m] * pl.rc;
+                const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+                const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
+                // (numbers was written by the producer before it arrived on go)
+                int stage = t.nkb % stages;
+                uint32_t phase = static_cast<uint32_t>(t.nkb / stages) & 1u;
+                for (int c0 = 0; c0 < cols; c0 += BK) {
+                    const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
+                    int ads[4], j0s[4];
+                    slice_rows(pl, numbers, c0, slices, ads, j0s);
+                    if (!wait_all(empty0 + 8 * stage, phase ^ 1)) break;
+                    const uint32_t sb = ring0 + stage * stage_bytes + a_region;
                     if (elect_one()) {
-                        tc_mma<CG>(d_tmem, ad, bd, idesc, i > 0 ? 1u : 0u);
-                        if (MODE != kWgrad || slices > 1)
-                            tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
-                        if (MODE != kWgrad || slices > 2)
-                            tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
-                        if (MODE != kWgrad || slices > 3)
-                            tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
-                        if constexpr (MODE != kWgrad) {
-                            for (int u = 1; u < ksub; ++u) {
-                                const uint64_t au = ad + u * a_sub, bu = bd + u * b_sub;
-                                tc_mma<CG>(d_tmem, au, bu, idesc, 1u);
-                                tc_mma<CG>(d_tmem, au + a_step, bu + b_step, idesc, 1u);
-                                tc_mma<CG>(d_tmem, au + 2 * a_step, bu + 2 * b_step, idesc, 1u);
-                                tc_mma<CG>(d_tmem, au + 3 * a_step, bu + 3 * b_step, idesc, 1u);
-                            }
-                        }
-                        tc_commit<CG>(empty0 + 8 * stage);  // frees the stage (both CTAs)
+    #pragma unroll
+                        for (int q = 2; q < 4; ++q)
+                            if (q < slices)
+                                slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0, j0s[q],
+                                                 ads[q], count0 + 8 * stage);
                     }
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                if (MODE == kLora && ok && args.plan.count != nullptr) {
-                    if (late) pdl_wait();
-                    const int cols = args.plan.count[t.tile_m] * args.plan.rc;
-                    const uint64_t slice_step = static_cast<uint64_t>(b_rows) * 32u >> 4;
-                    for (int c0 = 0; c0 < cols; c0 += BK) {
-                        ok = wait_all(full0 + 8 * stage, phase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
-                        const uint64_t at = static_cast<uint64_t>(stage) * stage_step;
-                        if (elect_one()) {
-                            for (int q = 0; q < slices; ++q)
-                                tc_mma<CG>(d_tmem, a_desc0 + at + q * a_step,
-                                           lb_desc0 + at + q * slice_step, lb_idesc, 1u);
-                            tc_commit<CG>(empty0 + 8 * stage);
-                        }
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                }
-                if (!ok) break;
-                if (elect_one()) tc_commit<CG>(tfull0 + 8 * buf);
-                ++acc;
             }
             __syncwarp();
-            // all MMAs issued here have finished once `drain` completes
-            if (elect_one()) {
-                tc_commit_local<CG>(drain);
-                const volatile int never = 0;
-                if (!wait_bounded(drain, 0, &never, args.timeout_ns)) raise_abort(abort_flag);
-            }
-            aborted = !ok;
-        }
-        __syncwarp();
-    } else if (MODE == kLora && warp >= 2 + kEpiWarps) {
-        // ------------------------------------------------- slice warp (the last)
-        // A decode step has many slices, 100 ns each to issue: this warp issues
-        // every second pair of them.  It joins the producer at the first block
-        // of V (go), waits for the same stages from there on and cannot run
-        // ahead of the ring: a CTA has one tile here.
-        if (args.slice_warp && tiles.get(first_tile, t) &&
-            __all_sync(0xffffffffu, wait_bounded(go0, 0, abort_flag, args.timeout_ns))) {
-            if (late) pdl_wait();
-            const LoraPlan &pl = args.plan;
-            const int cols = pl.count[t.tile_m] * pl.rc;
-            const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
-            const uint32_t slice_bytes = static_cast<uint32_t>(b_rows) * 32u;
-            // (numbers was written by the producer before it arrived on go)
-            int stage = t.nkb % stages;
-            uint32_t phase = static_cast<uint32_t>(t.nkb / stages) & 1u;
-            for (int c0 = 0; c0 < cols; c0 += BK) {
-                const int slices = cols - c0 < BK ? (cols - c0) / 16 : 4;
-                int ads[4], j0s[4];
-                slice_rows(pl, numbers, c0, slices, ads, j0s);
-                if (!wait_all(empty0 + 8 * stage, phase ^ 1)) break;
-                const uint32_t sb = ring0 + stage * stage_bytes + a_region;
-                if (elect_one()) {
-#pragma unroll
-                    for (int q = 2; q < 4; ++q)
-                        if (q < slices)
-                            slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0, j0s[q],
-                                             ads[q], count0 + 8 * stage);
+        } else if (MODE == kRows && !GATHER && warp >= kHelper) {
+            // (they only gave their registers)
+        } else if (warp >= kHelper) {
+            // -------------------------------------------------------- gather warps
+            // They follow the producer's stages and issue the parts of a stage
+            // that come by row number: one thread each, the numbers in shared
+            // memory.  The producer, which has waited for the stage and counted
+            // their bytes in its expect_tx, tells each warp through its own
+            // barrier of that stage; it cannot tell it again before the bytes have
+            // arrived, so one parity bit per stage is enough.
+            const int half = warp - kHelper;
+            int *const mine = numbers + half * 64;  // 64 row numbers
+            const uint32_t go = go0 + 8 * half * kMaxStages;
+            int stage = 0;
+            uint32_t told = 0;  // parity of the next word on each stage
+            bool ok = true;
+            // 4 * quads rows (numbers from `from` on), 64 columns from c0 on, to dst
+            auto gather = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, const int *from,
+                              int quads, uint32_t fb) {
+                for (int q = 0; q < quads; ++q) {
+                    const int4 r = *reinterpret_cast<const int4 *>(from + q * 4);
+                    if (elect_one()) tma_gather4<CG>(dst + q * 512, map, c0, r.x, r.y, r.z, r.w, fb);
                 }
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp >= 2 + kEpiWarps) {
-        // ---------------------------------------- gather warps (the last two)
-        // They follow the producer's stages and issue the parts of a stage
-        // that come by row number: one thread each, the numbers in shared
-        // memory.  The producer, which has waited for the stage and counted
-        // their bytes in its expect_tx, tells each warp through its own
-        // barrier of that stage; it cannot tell it again before the bytes have
-        // arrived, so one parity bit per stage is enough.
-        const int half = warp - (2 + kEpiWarps);
-        int *const mine = numbers + half * 64;  // 64 row numbers
-        const uint32_t go = go0 + 8 * half * kMaxStages;
-        int stage = 0;
-        uint32_t told = 0;  // parity of the next word on each stage
-        bool ok = true;
-        // 4 * quads rows (numbers from `from` on), 64 columns from c0 on, to dst
-        auto gather = [&](uint32_t dst, const CUtensorMap *map, int32_t c0, const int *from,
-                          int quads, uint32_t fb) {
-            for (int q = 0; q < quads; ++q) {
-                const int4 r = *reinterpret_cast<const int4 *>(from + q * 4);
-                if (elect_one()) tma_gather4<CG>(dst + q * 512, map, c0, r.x, r.y, r.z, r.w, fb);
-            }
-        };
-        bool reverse = false;
-        for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
-            const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
-            const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
-            int quads = 0;  // rows mode: this warp's quads of the tile
-            int kb = 0;
-            if constexpr (MODE != kWgrad) {
-                const int rows = cta_rows(t, rank) - half * 64;
-                quads = rows <= 0 ? 0 : (rows >= 64 ? 16 : (rows + 3) / 4);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = lane + i * 32;
-                    mine[r] = r < rows ? __ldg(args.row_index + m0 + half * 64 + r) : -1;
-                }
-                __syncwarp();
-                kb = first_block<CG>(w, t.nkb, reverse);
-            }
-            for (int i = 0; i < t.nkb; ++i) {
-                const uint32_t fb = count0 + 8 * stage;
-                const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
-                bool work = quads > 0, part = false;
-                if constexpr (MODE == kWgrad) {
-                    const int32_t r0 = t.first + i * BK;
-                    const int rem = t.last - r0 < BK ? t.last - r0 : BK;
-                    part = rem < BK;
-                    quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
-                    work = part;
-                    if (work) {
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int r = lane + j * 32;
-                            mine[r] = r < rem ? static_cast<int>(r0 + r) : -1;
-                        }
-                        __syncwarp();
+            };
+            bool reverse = false;
+            for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
+                const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
+                const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
+                int quads = 0;  // rows mode: this warp's quads of the tile
+                int kb = 0;
+                if constexpr (MODE != kWgrad) {
+                    const int rows = cta_rows(t, rank) - half * 64;
+                    quads = rows <= 0 ? 0 : (rows >= 64 ? 16 : (rows + 3) / 4);
+                    __syncwarp();
+    #pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = lane + i * 32;
+                        mine[r] = r < rows ? __ldg(args.row_index + m0 + half * 64 + r) : -1;
                     }
+                    __syncwarp();
+                    kb = first_block<CG>(w, t.nkb, reverse);
                 }
-                if (work) {
-                    ok = wait_all(go + 8 * stage, (told >> stage) & 1u);
-                    if (!ok) break;
-                    told ^= 1u << stage;
+                for (int i = 0; i < t.nkb; ++i) {
+                    const uint32_t fb = count0 + 8 * stage;
+                    const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                    bool work = quads > 0, part = false;
                     if constexpr (MODE == kWgrad) {
-                        gather(sa + half * 8192, &map_a_rows, m0 + half * 64, mine, quads, fb);
-                        for (int j = half; j < b_rows / 64; j += kGatherWarps)
-                            gather(sb + j * 8192, &map_b_rows, b0 + 64 * j, mine, quads, fb);
-                    } else {
-                        for (int u = 0; u < ksub; ++u)
-                            gather(sa + (u * args.am + half * 64) * 128, &map_a_rows,
-                                   (kb * ksub + u) * BK, mine, quads, fb);
+                        const int32_t r0 = t.first + i * BK;
+                        const int rem = t.last - r0 < BK ? t.last - r0 : BK;
+                        part = rem < BK;
+                        quads = (rem + 15) / 16 * 4;  // rows of whole 16-row slices
+                        work = part;
+                        if (work) {
+                            __syncwarp();
+    #pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int r = lane + j * 32;
+                                mine[r] = r < rem ? static_cast<int>(r0 + r) : -1;
+                            }
+                            __syncwarp();
+                        }
                     }
+                    if (work) {
+                        ok = wait_all(go + 8 * stage, (told >> stage) & 1u);
+                        if (!ok) break;
+                        told ^= 1u << stage;
+                        if constexpr (MODE == kWgrad) {
+                            gather(sa + half * 8192, &map_a_rows, m0 + half * 64, mine, quads, fb);
+                            for (int j = half; j < b_rows / 64; j += kGatherWarps)
+                                gather(sb + j * 8192, &map_b_rows, b0 + 64 * j, mine, quads, fb);
+                        } else {
+                            for (int u = 0; u < ksub; ++u)
+                                gather(sa + (u * args.am + half * 64) * 128, &map_a_rows,
+                                       (kb * ksub + u) * BK, mine, quads, fb);
+                        }
+                    }
+                    if constexpr (MODE != kWgrad) kb = next_block<CG>(kb, t.nkb, reverse);
+                    if (++stage == stages) stage = 0;
                 }
-                if constexpr (MODE != kWgrad) kb = next_block<CG>(kb, t.nkb, reverse);
-                if (++stage == stages) stage = 0;
             }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        if constexpr (PARTS)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // -------------------------------------------------- epilogue warps
         // Two per quarter of the TMEM lanes; each takes every other block of
         // 32 columns.  C of a block is loaded while the one before it is
         // stored (the first while the tile is still summed).
-        const int e = warp - 2, quarter = warp % 4, half = e / 4;
+        const int e = warp, quarter = warp % 4, half = e / 4;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t acc = 0;
-        uint32_t n_c = 0;  // staged: blocks of C fetched so far
+        // this warp's boxes; blocks that went through them so far
+        const uint32_t boxes0 = ring0 + args.ring_bytes - box_bytes(args.boxes) + e * args.boxes * 4096;
+        const uint32_t cbar = cbar0 + 16 * e;
+        uint32_t blocks = 0;
         if (late) pdl_wait();
         for (uint32_t w = first_tile; tiles.get(w, t); w += tile_step) {
             const bool empty_sum = MODE == kWgrad && t.nkb == 0;
-            const uint32_t buf = acc & 1;
             int nrows = t.m_valid - static_cast<int>(rank) * BM - quarter * 32;
             nrows = nrows < 0 ? 0 : (nrows > 32 ? 32 : nrows);
             const int64_t row0 = t.m0 + rank * BM + quarter * 32;
@@ -713,7 +765,8 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                 if (o.beta != 0.f) o.C += t.g * args.stride_c;
             }
             const bool use_c = MODE == kWgrad && o.beta != 0.f;
-            const uint32_t t_acc = tmem_base + lane_off + buf * 256;
+            const bool staged = MODE == kWgrad && args.staged;
+            uint32_t buf = 0, t_acc = 0;  // the accumulator being read
             auto release_acc = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -724,94 +777,205 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                         mbar_arrive_cluster(map_to_rank(tempty0 + 8 * buf, 0));
                 }
             };
-            if constexpr (MODE == kWgrad) {
-                if (args.staged) {
-                    const uint32_t d_box = ring0 + kStagedRing + e * 3 * 4096, c_boxes = d_box + 4096;
-                    const uint32_t cbar = cbar0 + 16 * e;
-                    // C of a block into box n_c % 2 (the block that used it last has been read)
-                    auto fetch_c = [&](int chunk) {
-                        if (use_c && elect_one()) {
-                            const uint32_t bar = cbar + 8 * (n_c & 1);
-                            mbar_arrive_expect_tx(bar, 4096);
-                            tma_load_3d<CG>(c_boxes + (n_c & 1) * 4096, &map_c,
-                                            static_cast<int32_t>(t.n0) + chunk * 32,
-                                            static_cast<int32_t>(row0), t.g,
-                                            CG == 1 ? bar : map_to_rank(bar, rank));
-                        }
-                        ++n_c;
-                    };
-                    if (last >= 0) fetch_c(half);
-                    if (!empty_sum) {
-                        if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
-                            aborted = true;
-                            break;
-                        }
-                        tc_fence_after();
-                        ++acc;
-                    }
-                    bool stop = false;
+            // staged: C of block number n into its box (the block that used it last
+            // has been read)
+            auto fetch_c = [&](int chunk, uint32_t n) {
+                if (use_c && elect_one()) {
+                    const uint32_t bar = cbar + 8 * (n & 1);
+                    mbar_arrive_expect_tx(bar, 4096);
+                    tma_load_3d<CG>(boxes0 + (1 + (n & 1)) * 4096, &map_c,
+                                    static_cast<int32_t>(t.n0) + chunk * 32,
+                                    static_cast<int32_t>(row0), t.g,
+                                    CG == 1 ? bar : map_to_rank(bar, rank));
+                }
+            };
+            // staged: C of the next block is on its way, and this block's is there
+            // (false: it did not come)
+            auto c_ready = [&](int chunk) -> bool {
+                if (chunk + 2 < n_chunks) fetch_c(chunk + 2, blocks + 1);
+                return !use_c || wait_all(cbar + 8 * (blocks & 1), (blocks >> 1) & 1);
+            };
+            // staged: quad q of this lane's row of the block
+            auto finished = [&](int q, float4 v) -> float4 {
+                v.x *= o.alpha, v.y *= o.alpha, v.z *= o.alpha, v.w *= o.alpha;
+                if (use_c) {
+                    const float4 c = ld_shared_v4(boxes0 + (1 + (blocks & 1)) * 4096 + box_quad(lane, q));
+                    v.x = fmaf(o.beta, c.x, v.x), v.y = fmaf(o.beta, c.y, v.y);
+                    v.z = fmaf(o.beta, c.z, v.z), v.w = fmaf(o.beta, c.w, v.w);
+                }
+                return v;
+            };
+            // staged: the last store has read the box / the box goes to D
+            auto open_box = [&]() {
+                if (elect_one()) bulk_wait_read();
+                __syncwarp();
+            };
+            auto close_box = [&](int chunk) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (elect_one())
+                    tma_store_3d(&map_d, static_cast<int32_t>(t.n0) + chunk * 32,
+                                 static_cast<int32_t>(row0), t.g, boxes0);
+                ++blocks;
+            };
+            auto put_quad = [&](int q, float4 v) {
+                st_shared_v4(boxes0 + box_quad(lane, q), __float_as_uint(v.x), __float_as_uint(v.y),
+                             __float_as_uint(v.z), __float_as_uint(v.w));
+            };
+            // The next accumulator, when it is complete.
+            auto next_acc = [&]() -> bool {
+                buf = acc & 1;
+                t_acc = tmem_base + lane_off + buf * 256;
+                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) return false;
+                tc_fence_after();
+                ++acc;
+                return true;
+            };
+            auto take_block = [&](int chunk, uint32_t (&raw)[32]) {
+                __syncwarp();
+                tmem_load_32cols(t_acc + chunk * 32, raw);
+                if (chunk == last) release_acc();
+            };
+            // lora: a slot's LB meets zeros of V in the rows of other adapters;
+            // where it holds infinities or NaNs those products are NaN.  Sums
+            // that are not finite are computed again from the row's own adapter
+            // alone.
+            auto redo_block = [&](int chunk, uint32_t (&raw)[32]) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const uint32_t b = raw[j] & 0x7fffffffu;
+                    top = b > top ? b : top;
+                }
+                const bool redo = args.plan.count != nullptr && lane < nrows && top >= 0x7f800000u;
+                if (!__any_sync(0xffffffffu, redo)) return;
 #pragma unroll 1
-                    for (int chunk = half; chunk < n_chunks; chunk += 2) {
-                        const uint32_t box = c_boxes + (n_c + 1) % 2 * 4096, bar = cbar + 8 * ((n_c + 1) % 2);
-                        const uint32_t parity = ((n_c - 1) >> 1) & 1;
-                        if (chunk + 2 < n_chunks) fetch_c(chunk + 2);
+                for (int l = 0; l < nrows; ++l) {
+                    if (!__shfl_sync(0xffffffffu, redo ? 1 : 0, l)) continue;
+                    const float mine = lora_exact(args, row0 + l, t.n0 + chunk * 32 + lane);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float x = __shfl_sync(0xffffffffu, mine, j);
+                        if (lane == l && (raw[j] & 0x7fffffffu) >= 0x7f800000u)
+                            raw[j] = __float_as_uint(x);
+                    }
+                }
+            };
+            if constexpr (PARTS) {
+                // run: the sums of this warp's blocks, where they have several parts
+                const bool parts = t.nkb > args.part;
+                uint32_t run[4][32] = {};  // (FP32)
+                if (staged && last >= 0) fetch_c(half, blocks);
+                for (int from = 0; from < t.nkb && !aborted; from += args.part) {
+                    if (!next_acc()) {
+                        aborted = true;
+                        break;
+                    }
+                    if (!parts) break;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (half + 2 * b > last) continue;
+                        uint32_t raw[32];
+                        __syncwarp();
+                        tmem_load_32cols(t_acc + (half + 2 * b) * 32, raw);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            run[b][j] =
+                                __float_as_uint(__uint_as_float(run[b][j]) + __uint_as_float(raw[j]));
+                    }
+                    release_acc();
+                }
+                if (aborted) break;
+#pragma unroll 1
+                for (int chunk = half; chunk < n_chunks; chunk += 2) {
+                    if (staged) open_box();
+                    auto put = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_v4(boxes0 + box_quad(lane, q), x[q * 4], x[q * 4 + 1],
+                                         x[q * 4 + 2], x[q * 4 + 3]);
+                    };
+                    if (parts) {
+                        // (indices into run are fixed at compile time)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (chunk == half + 2 * b) put(run[b]);
+                    } else {
                         uint32_t raw[32];
                         if (empty_sum) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) raw[j] = 0;
                         } else {
-                            __syncwarp();
-                            tmem_load_32cols(t_acc + chunk * 32, raw);
-                            if (chunk == last) release_acc();
+                            take_block(chunk, raw);
                         }
-                        float v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = o.alpha * __uint_as_float(raw[j]);
-                        if (use_c) {
-                            if (!wait_all(bar, parity)) {
-                                stop = true;
-                                break;
-                            }
-                            const uint32_t row = box + lane * 128;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const float4 cv = ld_shared_v4(row + ((q ^ (lane & 7)) << 4));
-                                v[q * 4 + 0] = fmaf(o.beta, cv.x, v[q * 4 + 0]);
-                                v[q * 4 + 1] = fmaf(o.beta, cv.y, v[q * 4 + 1]);
-                                v[q * 4 + 2] = fmaf(o.beta, cv.z, v[q * 4 + 2]);
-                                v[q * 4 + 3] = fmaf(o.beta, cv.w, v[q * 4 + 3]);
-                            }
-                        }
-                        if (elect_one()) bulk_wait_read();  // the last store has read its box
-                        __syncwarp();
-                        if (o.out == kOutF32) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                st_shared_v4(d_box + lane * 128 + ((q ^ (lane & 7)) << 4),
-                                             __float_as_uint(v[q * 4]), __float_as_uint(v[q * 4 + 1]),
-                                             __float_as_uint(v[q * 4 + 2]), __float_as_uint(v[q * 4 + 3]));
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                st_shared_v4(d_box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
-                                             pack_16(v[q * 8], v[q * 8 + 1], o.out),
-                                             pack_16(v[q * 8 + 2], v[q * 8 + 3], o.out),
-                                             pack_16(v[q * 8 + 4], v[q * 8 + 5], o.out),
-                                             pack_16(v[q * 8 + 6], v[q * 8 + 7], o.out));
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (elect_one())
-                            tma_store_3d(&map_d, static_cast<int32_t>(t.n0) + chunk * 32,
-                                         static_cast<int32_t>(row0), t.g, d_box);
+                        put(raw);
                     }
-                    if (stop) {
+                    if (!staged) {
+                        __syncwarp();
+                        store_from_box<MODE == kWgrad>(boxes0, o, row0, nrows, t.n0 + chunk * 32,
+                                                       ncols - chunk * 32);
+                        __syncwarp();
+                        continue;
+                    }
+                    if (!c_ready(chunk)) {
                         aborted = true;
                         break;
                     }
-                    if (last < 0 && !empty_sum) release_acc();
-                    continue;
+                    if (use_c || o.alpha != 1.f) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            put_quad(q, finished(q, ld_shared_v4(boxes0 + box_quad(lane, q))));
+                    }
+                    close_box(chunk);
                 }
+                if (aborted) break;
+                if (!parts && last < 0 && !empty_sum) release_acc();
+                continue;
+            }
+            if (staged) {
+                if (last >= 0) fetch_c(half, blocks);
+                if (!empty_sum && !next_acc()) {
+                    aborted = true;
+                    break;
+                }
+#pragma unroll 1
+                for (int chunk = half; chunk < n_chunks; chunk += 2) {
+                    uint32_t raw[32];
+                    if (empty_sum) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) raw[j] = 0;
+                    } else {
+                        take_block(chunk, raw);
+                    }
+                    if (!c_ready(chunk)) {
+                        aborted = true;
+                        break;
+                    }
+                    float4 v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        v[q] = finished(q, make_float4(__uint_as_float(raw[q * 4]),
+                                                       __uint_as_float(raw[q * 4 + 1]),
+                                                       __uint_as_float(raw[q * 4 + 2]),
+                                                       __uint_as_float(raw[q * 4 + 3])));
+                    open_box();
+                    if (o.out == kOutF32) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) put_quad(q, v[q]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)  // 64-byte rows
+                            st_shared_v4(boxes0 + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
+                                         pack_16(v[2 * q].x, v[2 * q].y, o.out),
+                                         pack_16(v[2 * q].z, v[2 * q].w, o.out),
+                                         pack_16(v[2 * q + 1].x, v[2 * q + 1].y, o.out),
+                                         pack_16(v[2 * q + 1].z, v[2 * q + 1].w, o.out));
+                    }
+                    close_box(chunk);
+                }
+                if (aborted) break;
+                if (last < 0 && !empty_sum) release_acc();
+                continue;
             }
             float c[32];
             const bool quads = in_quads(o);
@@ -823,13 +987,9 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                     load_c_columns(o, row0, nrows, t.n0 + chunk * 32, ncols - chunk * 32, c);
             };
             if (last >= 0) load_c(half);
-            if (!empty_sum) {
-                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
-                    aborted = true;
-                    break;
-                }
-                tc_fence_after();
-                ++acc;
+            if (!empty_sum && !next_acc()) {
+                aborted = true;
+                break;
             }
 #pragma unroll 1
             for (int chunk = half; chunk < n_chunks; chunk += 2) {
@@ -839,35 +999,8 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
                     for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 } else {
                     uint32_t raw[32];
-                    __syncwarp();
-                    tmem_load_32cols(t_acc + chunk * 32, raw);
-                    if (chunk == last) release_acc();
-                    if constexpr (MODE == kLora) {
-                        // A slot's LB meets zeros of V in the rows of other
-                        // adapters; where it holds infinities or NaNs those
-                        // products are NaN.  Sums that are not finite are
-                        // computed again from the row's own adapter alone.
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const uint32_t b = raw[j] & 0x7fffffffu;
-                            top = b > top ? b : top;
-                        }
-                        const bool redo = args.plan.count != nullptr && lane < nrows && top >= 0x7f800000u;
-                        if (__any_sync(0xffffffffu, redo)) {
-#pragma unroll 1
-                            for (int l = 0; l < nrows; ++l) {
-                                if (!__shfl_sync(0xffffffffu, redo ? 1 : 0, l)) continue;
-                                const float mine = lora_exact(args, row0 + l, t.n0 + chunk * 32 + lane);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    const float x = __shfl_sync(0xffffffffu, mine, j);
-                                    if (lane == l && (raw[j] & 0x7fffffffu) >= 0x7f800000u)
-                                        raw[j] = __float_as_uint(x);
-                                }
-                            }
-                        }
-                    }
+                    take_block(chunk, raw);
+                    if constexpr (MODE == kLora) redo_block(chunk, raw);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
                 }
@@ -903,7 +1036,7 @@ __global__ void __launch_bounds__(MODE == kLora && CG == 1 ? 512 : threads<MODE,
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc<CG>(tmem_base);
+    if (warp == kIssuer) tmem_dealloc<CG>(tmem_base);
 }
 
 // Rows of A in product order: out(r, :) = A(index[r], :), zeros for an index
@@ -961,11 +1094,11 @@ struct DeviceInfo {
 };
 DeviceInfo g_dev[kMaxDevices];
 
-template <int CG, int MODE, bool GATHER>
+template <int CG, int MODE, bool GATHER, bool PARTS>
 cudaLaunchConfig_t config(int grid, int ring, cudaStream_t stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(threads<MODE, GATHER>(), 1, 1);
+    cfg.blockDim = dim3(threads<MODE, GATHER, PARTS>(), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(ring));
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -978,10 +1111,17 @@ cudaLaunchConfig_t config(int grid, int ring, cudaStream_t stream, cudaLaunchAtt
     return cfg;
 }
 
-template <int CG, int MODE, bool GATHER>
+template <int CG, int MODE, bool GATHER, bool PARTS>
 cudaError_t allow_smem() {
-    return cudaFuncSetAttribute(grouped_tc_kernel<CG, MODE, GATHER>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const auto kernel = grouped_tc_kernel<CG, MODE, GATHER, PARTS>;
+    if (PARTS) {
+        // the warpgroups divide what the launch gives: without it they would wait
+        cudaFuncAttributes at;
+        const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != kPartsRegs) return cudaErrorInvalidKernelImage;
+    }
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 smem_bytes(kRingBytes));
 }
 
@@ -994,17 +1134,20 @@ DeviceInfo *device_info() {
         d->err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (d->err != cudaSuccess) return;
         d->sms = n > 0 ? n : 1;
-        for (cudaError_t e : {allow_smem<1, kRows, false>(), allow_smem<1, kRows, true>(),
-                              allow_smem<2, kRows, false>(), allow_smem<1, kWgrad, false>(),
-                              allow_smem<2, kWgrad, false>(),
-                              allow_smem<1, kLora, false>(), allow_smem<2, kLora, false>()})
+        for (cudaError_t e :
+             {allow_smem<1, kRows, false, false>(), allow_smem<1, kRows, false, true>(),
+              allow_smem<1, kRows, true, false>(), allow_smem<1, kRows, true, true>(),
+              allow_smem<2, kRows, false, false>(), allow_smem<2, kRows, false, true>(),
+              allow_smem<1, kWgrad, false, false>(), allow_smem<1, kWgrad, false, true>(),
+              allow_smem<2, kWgrad, false, false>(), allow_smem<2, kWgrad, false, true>(),
+              allow_smem<1, kLora, false, false>(), allow_smem<2, kLora, false, false>()})
             if (d->err == cudaSuccess) d->err = e;
         if (d->err != cudaSuccess) return;
         cudaLaunchAttribute attr[2];
-        cudaLaunchConfig_t cfg = config<2, kRows, false>(2 * (d->sms / 2), kRingBytes, 0, attr);
+        cudaLaunchConfig_t cfg = config<2, kRows, false, false>(2 * (d->sms / 2), kRingBytes, 0, attr);
         cfg.attrs = attr + 1;  // the occupancy query takes the cluster shape only
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&d->pairs, grouped_tc_kernel<2, kRows, false>, &cfg) !=
+        if (cudaOccupancyMaxActiveClusters(&d->pairs, grouped_tc_kernel<2, kRows, false, false>, &cfg) !=
             cudaSuccess) {
             d->pairs = 0;
             (void)cudaGetLastError();  // the pair variants are then not used
@@ -1013,22 +1156,42 @@ DeviceInfo *device_info() {
     return d;
 }
 
+template <int CG, int MODE, bool GATHER, bool PARTS>
+cudaError_t launch_as(const CUtensorMap (&maps)[8], const Args &a, int grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config<CG, MODE, GATHER, PARTS>(grid, a.ring_bytes, stream, attr);
+    return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, GATHER, PARTS>, maps[0], maps[1],
+                              maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], a);
+}
+
+// Boxes at the ring's end, for fewer stages.
+void take_boxes(Args &a, int boxes) {
+    a.boxes = boxes;
+    const int over = BM * BK * 2 - static_cast<int>(a.stage_bytes);
+    const int fit = (a.ring_bytes - box_bytes(boxes) - (over > 0 ? over : 0)) / static_cast<int>(a.stage_bytes);
+    if (a.stages > fit) a.stages = fit;
+}
+
+// `parts`: sums longer than kPart are made in parts.
 template <int CG, int MODE>
-cudaError_t launch(const CUtensorMap (&maps)[8], const Args &a, bool gather, int64_t max_tiles,
-                   const DeviceInfo *d, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap (&maps)[8], Args &a, bool gather, int64_t max_tiles,
+                   bool parts, const DeviceInfo *d, cudaStream_t stream) {
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
-    cudaLaunchAttribute attr[2];
-    if constexpr (MODE == kRows && CG == 1) {
-        if (gather) {
-            cudaLaunchConfig_t cfg = config<CG, MODE, true>(grid, a.ring_bytes, stream, attr);
-            return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, true>, maps[0], maps[1],
-                                      maps[2], maps[3], maps[4], maps[5], maps[6], maps[7], a);
+    a.part = kPart / (BK * a.ksub);
+    if constexpr (MODE != kLora) {
+        if (parts) {
+            if (a.boxes == 0) take_boxes(a, 1);
+            if constexpr (MODE == kRows && CG == 1) {
+                if (gather) return launch_as<CG, MODE, true, true>(maps, a, grid, stream);
+            }
+            return launch_as<CG, MODE, false, true>(maps, a, grid, stream);
         }
     }
-    cudaLaunchConfig_t cfg = config<CG, MODE, false>(grid, a.ring_bytes, stream, attr);
-    return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, false>, maps[0], maps[1], maps[2],
-                              maps[3], maps[4], maps[5], maps[6], maps[7], a);
+    if constexpr (MODE == kRows && CG == 1) {
+        if (gather) return launch_as<CG, MODE, true, false>(maps, a, grid, stream);
+    }
+    return launch_as<CG, MODE, false, false>(maps, a, grid, stream);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1179,22 +1342,16 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
                                 static_cast<uint32_t>(BK * a.ksub), 3);
     maps[3] = maps[4] = maps[5] = maps[6] = maps[7] = maps[2];
     const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
+    const bool parts = p.out == kOutF32 && p.K > kPart;
     static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
                                              {"grouped_tc<bf16>", "grouped_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];
     if (e == cudaSuccess && !ok) e = cudaErrorInvalidValue;
     if (e == cudaSuccess)
-        e = pair ? launch<2, kRows>(maps, a, gather, max_tiles, d, stream)
-                 : launch<1, kRows>(maps, a, gather, max_tiles, d, stream);
+        e = pair ? launch<2, kRows>(maps, a, gather, max_tiles, parts, d, stream)
+                 : launch<1, kRows>(maps, a, gather, max_tiles, parts, d, stream);
     return free_after(ws, stream, e);
 }
-
-// Whether the weight gradient's epilogue goes through TMA boxes, by the mean
-// rows per group.  16 groups, 4096 x 4096 FP32 gradients, us for boxes / for
-// registers (whose ring is three stages deeper): beta = 0: 64 rows 197 / 256,
-// 512 rows 277 / 324, 1024 rows 410 / 373; beta = 1: 64 rows 391 / 993, 2048
-// rows 764 / 1053.
-constexpr int64_t kStagedRows = 640, kStagedRowsC = 4096;
 
 bool wgrad_tc_eligible(const WgradProblem &p) {
     return p.rows > 0 && p.rows_a > 0 && tma_rows(p.A, p.lda) && tma_rows(p.B, p.ldb) &&
@@ -1278,7 +1435,7 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
                (p.groups == 1 || (stride % per == 0 && stride > 0)) && ld < (int64_t(1) << 37) &&
                stride < (int64_t(1) << 37);
     };
-    a.staged = ok && p.rows / p.groups <= (p.beta != 0.f ? kStagedRowsC : kStagedRows) && boxes(p.D, p.ldd, p.stride_d, per_16) &&
+    a.staged = ok && boxes(p.D, p.ldd, p.stride_d, per_16) &&
                (p.beta == 0.f || boxes(p.C, p.ldc, p.stride_c, 4));
     if (a.staged) {
         const int64_t sd = p.groups > 1 ? p.stride_d : p.ldd, sc = p.groups > 1 ? p.stride_c : p.ldc;
@@ -1287,16 +1444,16 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
              !encode_box32(&maps[5], 4, false, p.C, p.N, p.M, p.ldc, p.groups, sc)))
             a.staged = 0;
     }
-    if (a.staged && a.stages > kStagedRing / static_cast<int>(a.stage_bytes))
-        a.stages = kStagedRing / static_cast<int>(a.stage_bytes);
+    if (a.staged) take_boxes(a, p.beta != 0.f ? kBoxesC : kBoxes);
     const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
+    const bool parts = p.out == kOutF32 && p.rows / p.groups >= kPartsRows;
     static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
                                              {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];
     if (e == cudaSuccess && !ok) e = cudaErrorInvalidValue;
     if (e == cudaSuccess)
-        e = pair ? launch<2, kWgrad>(maps, a, false, max_tiles, d, stream)
-                 : launch<1, kWgrad>(maps, a, false, max_tiles, d, stream);
+        e = pair ? launch<2, kWgrad>(maps, a, false, max_tiles, parts, d, stream)
+                 : launch<1, kWgrad>(maps, a, false, max_tiles, parts, d, stream);
     return free_after(ws, stream, e);
 }
 
@@ -1432,8 +1589,8 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         }
         const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
         a.slice_warp = !pair && p.adapters > 0 && tiles <= d->sms;
-        e = pair ? launch<2, kLora>(maps, a, false, tiles, d, stream)
-                 : launch<1, kLora>(maps, a, false, tiles, d, stream);
+        e = pair ? launch<2, kLora>(maps, a, false, tiles, false, d, stream)
+                 : launch<1, kLora>(maps, a, false, tiles, false, d, stream);
     }
     return free_after(ws, stream, e);
 }

@@ -220,6 +220,80 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], const OutArg
     }
 }
 
+// An FP32 block by way of a box of shared memory: 4 KiB of the warp's own,
+// 1024-byte aligned, rows of 128 bytes whose 16-byte pieces change places with
+// the row.  Lane l puts its 32 sums into row l; the warp takes whole rows out,
+// four at a time in quads or one at a time.
+__device__ __forceinline__ uint32_t box_quad(int row, int q) {
+    return row * 128 + ((q ^ (row & 7)) << 4);
+}
+
+template <bool WITH_C>
+__device__ __forceinline__ void store_from_box(uint32_t box, const OutArgs &a, int64_t row0,
+                                               int nrows, int64_t c0, int width) {
+    const int lane = threadIdx.x % 32;
+    const bool with_c = WITH_C && a.beta != 0.f;
+    if (a.row_vec >= 16 && width >= 32) {
+        const int quad = lane % 8, first = lane / 8;
+        const int64_t col = c0 + quad * 4;
+        float b[4] = {};
+        if (!WITH_C && a.bias != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = a.bias[col + j];
+        }
+        float *d = static_cast<float *>(a.D) + (row0 + first) * a.ldd + col;
+        const float *c = with_c ? a.C + (row0 + first) * a.ldc + col : nullptr;
+        // (C may be D: a few rows of C are loaded before the first is stored)
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            float4 q[4], x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = ld_shared_v4(box + box_quad(first + 4 * (h + i), quad));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (with_c && first + 4 * (h + i) < nrows)
+                    q[i] = *reinterpret_cast<const float4 *>(c + 4 * (h + i) * a.ldc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i, d += 4 * a.ldd) {
+                const int row = first + 4 * (h + i);
+                if (row >= nrows) continue;
+                float v[4] = {fmaf(x[i].x, a.alpha, b[0]), fmaf(x[i].y, a.alpha, b[1]),
+                              fmaf(x[i].z, a.alpha, b[2]), fmaf(x[i].w, a.alpha, b[3])};
+                if (with_c) {
+                    v[0] = fmaf(a.beta, q[i].x, v[0]), v[1] = fmaf(a.beta, q[i].y, v[1]);
+                    v[2] = fmaf(a.beta, q[i].z, v[2]), v[3] = fmaf(a.beta, q[i].w, v[3]);
+                }
+                if (!WITH_C && a.act != kActNone) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = activate(v[j], a.act);
+                }
+                *reinterpret_cast<float4 *>(d) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    } else if (lane < width) {
+        const float b = !WITH_C && a.bias != nullptr ? a.bias[c0 + lane] : 0.f;
+        float *d = static_cast<float *>(a.D) + row0 * a.ldd + c0 + lane;
+        const float *c = with_c ? a.C + row0 * a.ldc + c0 + lane : nullptr;
+#pragma unroll 1
+        for (int h = 0; h < nrows; h += 8) {
+            float q[8], x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = ld_shared_f32(box + box_quad(h + i, lane / 4) + lane % 4 * 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (with_c && h + i < nrows) q[i] = c[(h + i) * a.ldc];
+#pragma unroll
+            for (int i = 0; i < 8; ++i, d += a.ldd) {
+                if (h + i >= nrows) continue;
+                float v = fmaf(x[i], a.alpha, b);
+                if (with_c) v = fmaf(a.beta, q[i], v);
+                if (!WITH_C) v = activate(v, a.act);
+                *d = v;
+            }
+        }
+    }
+}
+
 // Bytes (16, 8 or 0 for less) to which every row of a matrix of `elt`-byte
 // values starting at p, with these pitches (elements), is aligned.
 inline int row_alignment(const void *p, int64_t ld, int64_t stride, int64_t elt) {

@@ -197,6 +197,11 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
     }
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ float4 ld_shared_v4(uint32_t at) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
