@@ -1,8 +1,8 @@
 // grouped_simt.cu -- the grouped operators on the CUDA cores: FP32 inputs, and
 // 16-bit inputs whose rows TMA cannot describe.
 //
-// One kernel body for the three products; a CTA of 256 threads makes one 64 x
-// 128 tile of D, each thread an 8 x 4 block:
+// One kernel body for the three products; a CTA makes one 64 x 128 tile of D,
+// each thread an 8 x 8 or 8 x 4 block:
 //   rows:   D(r, j) = act(alpha * sum_k A(idx(r), k) B_g(k, j) + bias_g(j)),
 //           r in group g; a tile never holds rows of two groups;
 //   wgrad:  D_g(i, j) = alpha * sum_{r in g} A(idx(r), i) B(r, j) + beta C_g(i, j);
@@ -13,19 +13,34 @@
 // Slices 32 deep in K go through shared memory as FP32, the next one loaded
 // into registers while the current one is multiplied.  The arithmetic is FP32
 // FMAs two rows at a time (fma.rn.f32x2, each half rounded as fmaf; products
-// of 16-bit values are exact): 16 of them per thread and step of K against 3
-// shared-memory loads, so the FMA pipe is the bound (80.5 TFLOP/s).  64 rows
-// per tile rather than 128: groups are small where FP32 is used, and a tile's
-// rows past the group's end are lost work.  8 x 4 per thread rather than 8 x 8:
-// with few tiles per SM the second set of warps hides more latency than the
-// larger block saves loads.
+// of 16-bit values are exact), so the FMA pipe is the bound (80.5 TFLOP/s);
+// measured 46, the rest shared-memory reads and the waits at a slice's end.
+// 64 rows per tile rather than 128: groups are small where FP32 is used, and a
+// tile's rows past the group's end are lost work.
+//
+// 8 x 8 per thread (128 threads, three CTAs per SM) for the row products: four
+// 16-byte reads of shared memory per 32 FMAs (8 groups, 4096 rows, 2048 x 2048:
+// 741 us, 8 x 4 779).  8 x 4 (256 threads, two CTAs) for the weight gradients,
+// whose sums are often short: twice the warps hide more of a tile's start and
+// end (4 groups of 300 rows, 600 x 600: 39 us, 8 x 8 41; 16 groups, 2000 rows,
+// 1000 x 1024: 109 and 119).
 #include "grouped.cuh"
 
 namespace gemm {
 namespace {
 
-constexpr int TM = 64, TN = 128, TK = 32, THREADS = 256;
+constexpr int TM = 64, TN = 128, TK = 32;
 constexpr int kSmemBytes = 2 * TK * (TM + TN) * 4;
+
+enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
+
+template <int MODE>
+struct Shape {
+    static constexpr int RN = MODE == kWgrad ? 4 : 8;  // columns per thread, in quads TN / 2 apart
+    static constexpr int THREADS = TM / 8 * (TN / RN);
+    static constexpr int RESIDENT = MODE == kWgrad ? 2 : 3;
+    static constexpr int QA = TM * TK / 4 / THREADS, QB = TN * TK / 4 / THREADS;  // quads per slice
+};
 
 // Where four values from column q (a multiple of 4) of step k of a slice are:
 // the quads of a row change places with k / 4, so that a warp that stores
@@ -84,8 +99,6 @@ __device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
 __device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
-
-enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
 
 struct SimtGroupedArgs {
     GroupedProblem g;  // kRows; kLora (groups = 1, A = X, B = W)
@@ -184,7 +197,10 @@ __device__ __forceinline__ void finish_quad(const SimtGroupedArgs &a, int g, int
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGroupedArgs a) {
+__global__ void __launch_bounds__(Shape<MODE>::THREADS, Shape<MODE>::RESIDENT)
+    grouped_simt_kernel(const SimtGroupedArgs a) {
+    constexpr int THREADS = Shape<MODE>::THREADS, RN = Shape<MODE>::RN, QA = Shape<MODE>::QA,
+                  QB = Shape<MODE>::QB;
     extern __shared__ float4 smem4[];
     float(*As)[TK][TM] = reinterpret_cast<float(*)[TK][TM]>(smem4);
     float(*Bs)[TK][TN] = reinterpret_cast<float(*)[TK][TN]>(reinterpret_cast<float *>(smem4) + 2 * TK * TM);
@@ -232,13 +248,13 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
     const int64_t rows_a = MODE == kWgrad ? a.w.rows_a : a.g.rows_a;
     const bool b_kmajor = MODE != kWgrad && a.g.b_kmajor;
 
-    // Quads of four values: A 2 and B 4 per thread and slice.
+    // Quads of four values:
     //   K-contiguous: quad i is row i / 8, values 4 (i % 8) of the slice's 32
     //   else:         quad i is step i / (width / 4) of K, columns 4 (i % ..)
-    int64_t a_row[2];
+    int64_t a_row[QA];
     if constexpr (MODE != kWgrad) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < QA; ++q) {
             const int64_t r = m0 + (tid + q * THREADS) / 8;
             a_row[q] = -1;
             if (r < m_end) {
@@ -247,11 +263,11 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
             }
         }
     }
-    float4 a_next[2], b_next[4];
+    float4 a_next[QA], b_next[QB];
     auto fetch = [&](int64_t k0) {
         if constexpr (MODE == kWgrad) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < QA; ++q) {
                 const int i = tid + q * THREADS;
                 const int64_t r = k0 + i / 16, m = m0 + (i % 16) * 4;
                 int64_t from = -1;
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < QA; ++q) {
                 const int64_t k = k0 + (tid % 8) * 4;
                 a_next[q] = load4(A + (a_row[q] >= 0 ? a_row[q] * lda + k : 0),
                                   a_row[q] >= 0 ? k_end - k : 0, a.vec_a);
@@ -271,13 +287,13 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         }
         if (b_kmajor) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < QB; ++q) {
                 const int64_t n = n0 + (tid + q * THREADS) / 8, k = k0 + (tid % 8) * 4;
                 b_next[q] = load4(B + (n < n_end ? n * ldb + k : 0), n < n_end ? k_end - k : 0, a.vec_b);
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < QB; ++q) {
                 const int i = tid + q * THREADS;
                 const int64_t k = k0 + i / 32, n = n0 + (i % 32) * 4;
                 b_next[q] = load4(B + (k < k_end ? k * ldb + n : 0), k < k_end ? n_end - n : 0, a.vec_b);
@@ -286,7 +302,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
     };
     auto put = [&](int s) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < QA; ++q) {
             const int i = tid + q * THREADS;
             if constexpr (MODE == kWgrad) {
                 *reinterpret_cast<float4 *>(&As[s][i / 16][spot(i / 16, (i % 16) * 4)]) = a_next[q];
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
             }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < QB; ++q) {
             const int i = tid + q * THREADS;
             if (b_kmajor) {
                 const int k = (i % 8) * 4, n = spot(k, i / 8);
@@ -313,14 +329,15 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         }
     };
 
-    // rows ty * 8 .. + 7 in pairs; columns tx * 4 .. + 3
-    // (a warp's block is 16 x 64)
-    const int tx = tid / 32 % 2 * 16 + tid % 16, ty = tid / 64 * 2 + tid / 16 % 2;
-    uint64_t acc[4][4];
+    // rows ty * 8 .. + 7 in pairs; columns tx * 4 .. + 3, and as many TN / 2 on
+    // (RN = 8); a warp's block is 16 rows of 64 columns, or twice 64
+    const int tx = (RN == 8 ? 0 : tid / 32 % 2 * 16) + tid % 16;
+    const int ty = tid / (RN == 8 ? 32 : 64) * 2 + tid / 16 % 2;
+    uint64_t acc[4][RN];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+        for (int j = 0; j < RN; ++j) acc[i][j] = 0;
     if (k_begin < k_end) {
         fetch(k_begin);
         put(0);
@@ -332,38 +349,43 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
         if (more) fetch(k0 + TK);
 #pragma unroll
         for (int k = 0; k < TK; ++k) {
-            uint64_t av[4], bv[4];
+            uint64_t av[4];
             const ulonglong2 a0 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][spot(k, ty * 8)]);
             const ulonglong2 a1 = *reinterpret_cast<const ulonglong2 *>(&As[s][k][spot(k, ty * 8 + 4)]);
             av[0] = a0.x, av[1] = a0.y, av[2] = a1.x, av[3] = a1.y;
-            const float4 b = *reinterpret_cast<const float4 *>(&Bs[s][k][spot(k, tx * 4)]);
-            bv[0] = pair(b.x, b.x), bv[1] = pair(b.y, b.y);
-            bv[2] = pair(b.z, b.z), bv[3] = pair(b.w, b.w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int h = 0; h < RN / 4; ++h) {
+                const float4 b =
+                    *reinterpret_cast<const float4 *>(&Bs[s][k][spot(k, h * (TN / 2) + tx * 4)]);
+                const uint64_t bv[4] = {pair(b.x, b.x), pair(b.y, b.y), pair(b.z, b.z), pair(b.w, b.w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) fma2(acc[i][j], av[i], bv[j]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) fma2(acc[i][h * 4 + j], av[i], bv[j]);
+            }
         }
         if (more) put(s ^ 1);  // the other buffer was last read before the previous barrier
         __syncthreads();
         s ^= 1;
     }
-    auto sums = [&](int i) {  // row ty * 8 + i of the tile, this thread's columns
+    auto sums = [&](int i, int h) {  // row ty * 8 + i of the tile, columns from h TN / 2 + tx * 4 on
         float o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float lo, hi;
-            unpair(acc[i / 2][j], lo, hi);
+            unpair(acc[i / 2][h * 4 + j], lo, hi);
             o[j] = i % 2 ? hi : lo;
         }
         return make_float4(o[0], o[1], o[2], o[3]);
     };
-    const int64_t n4 = n0 + tx * 4;
     if (a.ks == 1) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (m0 + ty * 8 + i < m_end)
-                finish_quad<T, MODE>(a, g, m0 + ty * 8 + i, n4, n_end, sums(i));
+#pragma unroll
+            for (int h = 0; h < RN / 4; ++h)
+                if (m0 + ty * 8 + i < m_end)
+                    finish_quad<T, MODE>(a, g, m0 + ty * 8 + i, n0 + h * (TN / 2) + tx * 4, n_end,
+                                         sums(i, h));
         return;
     }
     // the parts meet in the cluster's shared memory, each CTA adding a share of
@@ -372,17 +394,20 @@ __global__ void __launch_bounds__(THREADS) grouped_simt_kernel(const SimtGrouped
     static_assert(TM * TN * 4 <= kSmemBytes, "a tile of sums replaces the slices");
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4 *>(&part[ty * 8 + i][tx * 4]) = sums(i);
+#pragma unroll
+        for (int h = 0; h < RN / 4; ++h)
+            *reinterpret_cast<float4 *>(&part[ty * 8 + i][h * (TN / 2) + tx * 4]) = sums(i, h);
     sync_cluster();
-    for (int i = static_cast<int>(rank) * (TM / a.ks) + ty; i < (static_cast<int>(rank) + 1) * (TM / a.ks);
-         i += THREADS / 32) {
+    const int col = tid % 32 * 4;
+    for (int i = static_cast<int>(rank) * (TM / a.ks) + tid / 32;
+         i < (static_cast<int>(rank) + 1) * (TM / a.ks); i += THREADS / 32) {
         if (m0 + i >= m_end) break;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t c = 0; c < static_cast<uint32_t>(a.ks); ++c) {
-            const float4 v = load_from_rank(&part[i][tx * 4], c);
+            const float4 v = load_from_rank(&part[i][col], c);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
-        finish_quad<T, MODE>(a, g, m0 + i, n4, n_end, sum);
+        finish_quad<T, MODE>(a, g, m0 + i, n0 + col, n_end, sum);
     }
     sync_cluster();  // no CTA leaves while another reads its sums
 }
@@ -425,7 +450,7 @@ cudaError_t launch_as(const SimtGroupedArgs &a, int64_t grid, cudaStream_t strea
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.blockDim = dim3(Shape<MODE>::THREADS, 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -452,10 +477,10 @@ bool rows_on(const void *p, int64_t ld, int64_t stride, int64_t elt, int64_t byt
                bytes == 0;
 }
 
-// CTAs that share a tile's K: two CTAs are resident per SM, so a few tiles
-// more than 2 x SMs would take twice as long; up to 8 parts (each at least 128
-// of K) while there are fewer than 12 per SM.  (16 groups, 2000 rows, 1000 x
-// 1024, 320 tiles: 164 us in one part, 129 split.)
+// CTAs that share a tile's K: few are resident per SM, so a few tiles more than
+// fit would take twice as long; up to 8 parts (each at least 128 of K) while
+// there are fewer than 12 per SM.  (16 groups, 2000 rows, 1000 x 1024, 320
+// tiles: 164 us in one part, 129 split, both with 8 x 4 per thread.)
 int k_parts(int64_t tiles, int64_t k) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
