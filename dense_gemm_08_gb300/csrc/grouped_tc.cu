@@ -104,7 +104,7 @@ struct Args {
     int num_kb;                 // rows, lora: K steps of a stage each
     int ksub;                   // rows, lora: blocks of 64 of K per stage
     int part;                   // K steps per part of a sum (see kPart)
-    int a_blocks, b_blocks;     // wgrad: whole 64-column blocks of A and B
+    int a_blocks, b_blocks;     // whole 64-column blocks of A (wgrad) and B (N-major)
     int staged;                 // wgrad: D and C move as TMA boxes
     int boxes;                  // per epilogue warp, at the ring's end (see kBoxes)
     int b_kmajor;               // rows
@@ -398,9 +398,12 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                             const int32_t k_in = ksub > 1 ? 0 : block * BK, k_block = ksub > 1 ? block : 0;
                             if (args.b_kmajor) {
                                 tma_load_4d<CG>(sb, &map_b, k_in, b0, k_block, z, fb);
+                            } else if ((b0 + b_rows) / 64 <= args.b_blocks) {
+                                tma_load_4d<CG>(sb, &map_b, 0, block * BK, b0 / 64, z, fb);
                             } else {
                                 for (int j = 0; j < b_rows; j += 64)
-                                    tma_load_3d<CG>(sb + j * 128 * ksub, &map_b, b0 + j, block * BK, z, fb);
+                                    tma_load_3d<CG>(sb + j * 128 * ksub, &map_b_edge, b0 + j, block * BK,
+                                                    z, fb);
                             }
                             if constexpr (!GATHER) {
                                 if (mine > 0) tma_load_3d<CG>(sa, &map_a, k_in, m0, k_block, fb);
@@ -505,7 +508,13 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
             // ------------------------------------------------------ MMA issuer
             if (leader) {
                 const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
-                const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
+                // N of an MMA: the tile's columns in whole blocks of the epilogue (a
+            // pair's B lies half in either CTA: always all of it)
+            auto idesc_of = [&](const Tile &tile, uint32_t b_mn_major) {
+                const int64_t rest = (args.N - tile.n0 + 31) / 32 * 32;
+                const int n = CG == 1 && rest < args.bn ? static_cast<int>(rest) : args.bn;
+                return make_idesc(BM * CG, n, MODE == kWgrad, b_mn_major, args.ab_format);
+            };
                 const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring0, 0) : desc_kmajor(ring0, 0);
                 const uint64_t b_desc0 =
                     b_mn ? smem_desc(ring0 + a_region, static_cast<uint32_t>(ksub) * 8192u, 1024)
@@ -518,8 +527,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                 // lora: slices of LB -- K-major: 32-byte rows (32-byte swizzle);
                 // N-major: 16 rows per 64-column block (128-byte swizzle)
                 const bool lb_mn = MODE == kLora && !args.l.b_kmajor;
-                const uint32_t lb_idesc = make_idesc(BM * CG, args.bn, 0, lb_mn, args.ab_format);
-                const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
+                    const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
                                                 : smem_desc(ring0 + a_region, 16, 256, kSwizzle32);
                 const uint64_t stage_step = stage_bytes >> 4;
                 int stage = 0;
@@ -528,6 +536,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                 bool ok = true;
                 for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step) {
                     if (MODE == kWgrad && t.nkb == 0) continue;  // no rows: nothing to add
+                    const uint32_t idesc = idesc_of(t, b_mn), lb_idesc = idesc_of(t, lb_mn);
                     uint32_t d_tmem = 0;
                     auto take = [&]() {  // the accumulator not filled last, once it has been read
                         ok = wait_all(tempty0 + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1);
@@ -1338,9 +1347,11 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
         ok = ok && encode_kmajor(&maps[2], bf16, p.B, p.K, p.N, p.ldb, count, stride, a.bn / cg,
                                  a.ksub, 4);
     else
-        ok = ok && encode_stack(&maps[2], bf16, p.B, p.N, p.K, p.ldb, count, stride, 64,
-                                static_cast<uint32_t>(BK * a.ksub), 3);
-    maps[3] = maps[4] = maps[5] = maps[6] = maps[7] = maps[2];
+        ok = ok && encode_nmajor(&maps[2], &maps[7], bf16, p.B, p.N, p.K, p.ldb, count, stride,
+                                 a.bn / cg, a.ksub);
+    a.b_blocks = static_cast<int>(p.N / 64);
+    if (p.b_kmajor) maps[7] = maps[2];
+    maps[3] = maps[4] = maps[5] = maps[6] = maps[2];
     const int64_t max_tiles = (p.rows / (a.am * cg) + live) * a.tiles_n;
     const bool parts = p.out == kOutF32 && p.K > kPart;
     static const char *const kNames[2][2] = {{"grouped_tc<f16>", "grouped_tc<f16,pair>"},
@@ -1564,9 +1575,11 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
             ok = ok && encode_kmajor(&maps[2], bf16, p.W, p.K, p.N, p.ldw, 1, p.ldw, a.bn / cg,
                                      a.ksub, 4);
         else
-            ok = ok && encode_stack(&maps[2], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw, 64,
-                                    static_cast<uint32_t>(BK * a.ksub), 3);
-        maps[1] = maps[3] = maps[4] = maps[5] = maps[6] = maps[7] = maps[2];
+            ok = ok && encode_nmajor(&maps[2], &maps[7], bf16, p.W, p.N, p.K, p.ldw, 1, p.ldw,
+                                     a.bn / cg, a.ksub);
+        a.b_blocks = static_cast<int>(p.N / 64);
+        if (p.w_kmajor) maps[7] = maps[2];
+        maps[1] = maps[3] = maps[4] = maps[5] = maps[6] = maps[2];
         if (p.adapters > 0) {
             const bool one_lb = p.adapters == 1 || p.stride_b == 0;
             const int64_t stride = one_lb ? p.ld_b : p.stride_b;

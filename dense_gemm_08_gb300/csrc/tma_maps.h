@@ -86,6 +86,19 @@ inline bool encode_kmajor(CUtensorMap *map, bool bf16, const void *base, int64_t
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A stack of N-major operands (rows of N values, one per K): `whole` copies
+// box_cols / 64 blocks of 64 columns of box_k * 64 steps of K at once, for tiles
+// inside the N / 64 whole blocks; `edge` one block (coordinates n, k, matrix).
+static bool encode_nmajor(CUtensorMap *whole, CUtensorMap *edge, bool bf16, const void *base,
+                          int64_t N, int64_t K, int64_t ld, int64_t count, int64_t stride,
+                          int box_cols, int box_k) {
+    const uint32_t steps = static_cast<uint32_t>(64 * box_k);
+    if (!encode_stack(edge, bf16, base, N, K, ld, count, stride, 64, steps, 3)) return false;
+    *whole = *edge;
+    return N < 64 || encode_blocks(whole, bf16, base, N / 64 * 64, K, ld, count, stride, steps,
+                                   static_cast<uint32_t>(box_cols / 64), 4);
+}
+
 // A stack of matrices as 32 x 32 boxes for the epilogue, of FP32 (128-byte rows
 // and swizzle) or 16-bit values (64-byte).
 inline bool encode_box32(CUtensorMap *map, int elt, bool bf16, const void *base, int64_t N, int64_t M,
