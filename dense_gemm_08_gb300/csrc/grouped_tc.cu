@@ -21,6 +21,7 @@
 //     16-row slices that hold rows are multiplied.
 //   lora:   D(i, :) = act(X(i, :) op(W) + V(i, :) op(LB) + bias): the projection
 //     of all rows, its K loop continued over the slots of the tile's adapters.
+#include <cfloat>
 #include <mutex>
 
 #include "grouped.cuh"
@@ -69,7 +70,9 @@ __host__ __device__ constexpr int box_bytes(int boxes) { return kEpiWarps * boxe
 // takes come from the other warps.  It costs 3 to 10 % (8 groups, 16384 rows,
 // 4096 x 14336: 1105 us without parts, 1142 in parts of 1024, 1181 of 768, 1234
 // of 640; the 16384 x 4096 x 4096 product 317 and 338), for each part is read
-// in 1.4 us beside the multiplication of the next (3.4 us at 768).
+// in 1.4 us beside the multiplication of the next (3.4 us at 768).  (lora, up to
+// 128 rows: 64 rows, 4096 -> 14336: 41 and 47 us, the SMs having no registers
+// left for the kernel that makes V.)
 constexpr int kPart = 768;
 // The weight gradients' groups have any length: parts are made where the mean
 // is kPartsRows, below which the write of D is the time and the other kernel,
@@ -870,6 +873,23 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     }
                 }
             };
+            auto redo_box = [&](int chunk) {  // the same, for the sums in the box
+                bool redo = false;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 x = ld_shared_v4(boxes0 + box_quad(lane, q));
+                    redo |= !(fabsf(x.x) <= FLT_MAX && fabsf(x.y) <= FLT_MAX &&
+                              fabsf(x.z) <= FLT_MAX && fabsf(x.w) <= FLT_MAX);
+                }
+                redo = redo && args.plan.count != nullptr && lane < nrows;
+                __syncwarp();
+                for (uint32_t left = __ballot_sync(0xffffffffu, redo); left != 0; left &= left - 1) {
+                    const int l = __ffs(left) - 1;
+                    const uint32_t at = boxes0 + box_quad(l, lane / 4) + lane % 4 * 4;
+                    const float mine = lora_exact(args, row0 + l, t.n0 + chunk * 32 + lane);
+                    if (!(fabsf(ld_shared_f32(at)) <= FLT_MAX)) st_shared_f32(at, mine);
+                }
+            };
             if constexpr (PARTS) {
                 // run: the sums of this warp's blocks, where they have several parts
                 const bool parts = t.nkb > args.part;
@@ -919,6 +939,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                         }
                         put(raw);
                     }
+                    if constexpr (MODE == kLora) redo_box(chunk);
                     if (!staged) {
                         __syncwarp();
                         store_from_box<MODE == kWgrad>(boxes0, o, row0, nrows, t.n0 + chunk * 32,
@@ -1149,7 +1170,8 @@ DeviceInfo *device_info() {
               allow_smem<2, kRows, false, false>(), allow_smem<2, kRows, false, true>(),
               allow_smem<1, kWgrad, false, false>(), allow_smem<1, kWgrad, false, true>(),
               allow_smem<2, kWgrad, false, false>(), allow_smem<2, kWgrad, false, true>(),
-              allow_smem<1, kLora, false, false>(), allow_smem<2, kLora, false, false>()})
+              allow_smem<1, kLora, false, false>(), allow_smem<1, kLora, false, true>(),
+              allow_smem<2, kLora, false, false>(), allow_smem<2, kLora, false, true>()})
             if (d->err == cudaSuccess) d->err = e;
         if (d->err != cudaSuccess) return;
         cudaLaunchAttribute attr[2];
@@ -1188,14 +1210,12 @@ cudaError_t launch(const CUtensorMap (&maps)[8], Args &a, bool gather, int64_t m
     const int64_t resident = CG == 2 ? d->pairs : d->sms;
     const int grid = static_cast<int>((max_tiles < resident ? max_tiles : resident) * CG);
     a.part = kPart / (BK * a.ksub);
-    if constexpr (MODE != kLora) {
-        if (parts) {
-            if (a.boxes == 0) take_boxes(a, 1);
-            if constexpr (MODE == kRows && CG == 1) {
-                if (gather) return launch_as<CG, MODE, true, true>(maps, a, grid, stream);
-            }
-            return launch_as<CG, MODE, false, true>(maps, a, grid, stream);
+    if (parts) {
+        if (a.boxes == 0) take_boxes(a, kBoxes);
+        if constexpr (MODE == kRows && CG == 1) {
+            if (gather) return launch_as<CG, MODE, true, true>(maps, a, grid, stream);
         }
+        return launch_as<CG, MODE, false, true>(maps, a, grid, stream);
     }
     if constexpr (MODE == kRows && CG == 1) {
         if (gather) return launch_as<CG, MODE, true, false>(maps, a, grid, stream);
@@ -1497,6 +1517,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
     // 1 s per wait, longer where recomputing a tile's sums one by one could
     // take as long
     a.timeout_ns = 1000ull * 1000ull * 1000ull * static_cast<uint64_t>(1 + p.K / 65536);
+    const bool parts = p.out == kOutF32 && p.K > kPart;
     const int64_t pair_tiles = ceil_div(p.M, 2 * BM) * ceil_div(p.N, 256);
     const bool pair = d->pairs > 0 && p.M > BM && pair_tiles >= d->pairs;
     const int cg = pair ? 2 : 1;
@@ -1511,7 +1532,7 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         int64_t bn = ceil_div(ceil_div(p.N, per_row), step) * step;
         if (bn > 256) bn = 256;
         set_tile(a, 1, am, static_cast<int>(bn), sub_blocks(p.K, am, static_cast<int>(bn)),
-                 p.M <= BM ? kShortRing : kRingBytes);
+                 p.M <= BM && !parts ? kShortRing : kRingBytes);
     }
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, a.bn));
@@ -1602,8 +1623,8 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
         }
         const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
         a.slice_warp = !pair && p.adapters > 0 && tiles <= d->sms;
-        e = pair ? launch<2, kLora>(maps, a, false, tiles, false, d, stream)
-                 : launch<1, kLora>(maps, a, false, tiles, false, d, stream);
+        e = pair ? launch<2, kLora>(maps, a, false, tiles, parts, d, stream)
+                 : launch<1, kLora>(maps, a, false, tiles, parts, d, stream);
     }
     return free_after(ws, stream, e);
 }

@@ -287,8 +287,7 @@ gemm_status_t gemm_bf16_f32acc_ex(int64_t M, int64_t N, int64_t K, float alpha,
  *   therefore summed 768 steps at a time and the parts added with rounding
  *   (relative error 7e-7 with BF16 inputs, 9e-7 with FP16, at any K or number
  *   of rows; measured on normally distributed values).  Not so the weight
- *   gradients of groups of fewer than 192 rows on average, and gemm_lora, whose
- *   first product is rounded further (below).
+ *   gradients of groups of fewer than 192 rows on average.
  * Workspace, from the library's pool as above: gathered rows are copied into
  *   group order where that is faster (16-bit inputs: rows x K values, or
  *   rows x M for the weight gradient); gemm_lora keeps X LA of up to 128 MiB at

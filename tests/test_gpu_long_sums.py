@@ -112,3 +112,51 @@ def test_special_values_in_long_sums(dtype):
     assert torch.equal(D[0], clean[0]) and torch.equal(D[2], clean[2])
     assert not bool(torch.isfinite(D[1, 3]).any())
     assert bool(torch.isnan(D[1, :, 5]).all())
+
+
+def adapters(seed, dtype, n, K, N, rank):
+    return (normal(seed, (n, rank, K), dtype).transpose(1, 2),
+            (normal(seed + 1, (n, N, rank), dtype) * 0.01).transpose(1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N", [(1, 512), (40, 200), (200, 999), (600, 26 * 256)])
+def test_lora(dtype, M, N):
+    """The adapters' part is a hundredth of the result, so its rounding (2^-15 at
+    most) is below the tolerance's last digit."""
+    K, n, rank = 16384, 5, 16
+    X, W = normal(10, (M, K), dtype), normal(11, (N, K), dtype).t()
+    LA, LB = adapters(12, dtype, n, K, N, rank)
+    ids = torch.from_numpy(np.random.default_rng(14).integers(-1, n, M).astype(np.int32)).cuda()
+    scale = torch.full((n,), 0.25, device="cuda")
+    D = lib.gemm_lora(X, W, LA, LB, ids, scale=scale, out_dtype=torch.float32)
+    name = lib.gemm_last_kernel()
+    done()
+    ref = X.double() @ W.double()
+    for a in range(n):
+        rows = ids == a
+        ref[rows] += 0.25 * (X[rows].double() @ LA[a].double()) @ LB[a].double()
+    assert name.startswith("lora_tc")
+    assert off_by(D, ref) <= long_tolerance(K), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N", [(1, 100), (33, 77), (300, 264), (2000, 2560)])
+def test_lora_values_of_other_adapters(dtype, M, N):
+    """Infinities and NaNs in one adapter's matrices leave the other rows alone."""
+    K, n = 1600, 4
+    X, W = normal(15, (M, K), dtype), normal(16, (N, K), dtype).t()
+    LA, LB = adapters(17, dtype, n, K, N, 16)
+    ids = torch.from_numpy((np.arange(M) % n).astype(np.int32)).cuda()
+    clean = lib.gemm_lora(X, W, LA, LB, ids, out_dtype=torch.float32)
+    LB[2, 3, 5], LB[2, 4, N - 1] = float("inf"), float("nan")
+    D = lib.gemm_lora(X, W, LA, LB, ids, out_dtype=torch.float32)
+    done()
+    others = ids != 2
+    d, c = D[others].double(), clean[others].double()
+    assert bool(torch.isfinite(d).all())
+    # recomputed sums are sequential: K roundings of 2^-24 of the absolute sum at most
+    S = X[others].double().abs() @ W.double().abs()
+    assert bool(((d - c).abs() <= (2 * K * 2.0 ** -24 + long_tolerance(K)) * (S + c.abs() + 1)).all())
+    if bool((~others).any()):
+        assert not bool(torch.isfinite(D[~others][:, 5]).any())
