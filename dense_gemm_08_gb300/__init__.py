@@ -469,9 +469,10 @@ def stack_order(t):
 
 
 def _row_major(t, what):
-    """Leading dimension of a row-major matrix."""
-    r, q = t.shape
-    s0, s1 = t.stride()
+    """Leading dimension of a row-major matrix, or of each matrix of a stack: the columns of a
+    row are adjacent (one row has no pitch, one column no distance)."""
+    r, q = t.shape[-2:]
+    s0, s1 = t.stride()[-2:]
     if (s1 == 1 or q <= 1) and (s0 >= q or r <= 1):
         return max(s0, q, 1)
     raise ValueError(f"{what} must be row-major")
@@ -640,10 +641,7 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
     def stack(t, what):
         if tuple(t.shape) != (groups, M, N):
             raise ValueError(f"{what} must be {groups} x {M} x {N}")
-        order, ld, stride = stack_order(t)
-        if order != ROW_MAJOR and M > 1:
-            raise ValueError(f"{what} must be a stack of row-major matrices")
-        return max(ld, N, 1), stride
+        return _row_major(t, what), t.stride(0) if groups > 1 else 0
 
     if out is not None:
         ldd, stride_d = stack(out, "out")
