@@ -233,7 +233,10 @@ cudaError_t launch_group_rows(int64_t rows, int64_t groups, const int32_t *group
     a.pass_groups = static_cast<int>(groups < kGroupsPass ? groups : kGroupsPass);
     const bool one = rows <= kOneCta;
     const size_t smem = (static_cast<size_t>(WARPS + 1) * a.pass_groups + (one ? 0 : 2 * THREADS)) * sizeof(int);
-    if (smem > 48 * 1024) {
+    // without the attribute a kernel has 48 KiB, its static arrays (warp_sum) included
+    constexpr size_t kStatic = 1024;
+    static_assert(WARPS * sizeof(int) <= kStatic, "group_place_kernel's static arrays");
+    if (smem > 48 * 1024 - kStatic) {
         const int most = static_cast<int>(((WARPS + 1) * kGroupsPass + 2 * THREADS) * sizeof(int));
         const cudaError_t e =
             one ? cudaFuncSetAttribute(group_place_kernel<true>,
