@@ -84,6 +84,13 @@ struct GroupWalk {
     }
 };
 
+// The activation of a grouped product.  ReLU passes a NaN on, as the sum it
+// comes from does (fmaxf(NaN, 0) would be 0).
+__device__ __forceinline__ float grouped_activation(float x, int act) {
+    if (act == kActRelu) return x <= 0.f ? 0.f : x;
+    return apply_activation(x, act);
+}
+
 // One value in the type of D.  16-bit results are rounded to nearest even,
 // once, from the FP32 accumulator after the whole epilogue.
 __device__ __forceinline__ void store_out(void *D, int64_t at, float v, int out) {

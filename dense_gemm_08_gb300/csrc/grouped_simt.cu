@@ -182,7 +182,7 @@ __device__ __forceinline__ void finish_quad(const SimtGroupedArgs &a, int g, int
             }
             v *= a.g.alpha;
             if (a.g.bias != nullptr) v += a.g.bias[g * a.g.N + n];
-            o[j] = apply_activation(v, a.g.act);
+            o[j] = grouped_activation(v, a.g.act);
         }
         const int64_t at = r * a.g.ldd + n4;
         if (whole) {

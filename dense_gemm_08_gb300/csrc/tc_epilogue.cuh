@@ -79,7 +79,7 @@ __device__ __forceinline__ float activate(float x, int act) {
         const float u = 0.7978845608028654f * fmaf(0.044715f * x, x * x, x);
         return __fdividef(x, 1.f + __expf(-2.f * u));
     }
-    return apply_activation(x, act);
+    return grouped_activation(x, act);
 }
 
 // A block is 32 rows of D from row0 on (nrows of them inside) and 32 columns
