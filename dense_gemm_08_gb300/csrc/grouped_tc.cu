@@ -74,11 +74,10 @@ __host__ __device__ constexpr int box_bytes(int boxes) { return kEpiWarps * boxe
 // 128 rows: 64 rows, 4096 -> 14336: 41 and 47 us, the SMs having no registers
 // left for the kernel that makes V.)
 constexpr int kPart = 768;
-// The weight gradients' groups have any length: parts are made where the mean
-// is kPartsRows, below which the write of D is the time and the other kernel,
-// with its free registers, is 7 % faster (16 groups of 64 rows, 4096 x 4096: 201
-// and 215 us).
-constexpr int kPartsRows = 192;
+// The weight gradients' groups have any length, which the host does not know:
+// the kernel with parts runs whenever one group could be longer than a part,
+// also where all are short and the other kernel, with its free registers, would
+// be 7 % faster (16 groups of 64 rows, 4096 x 4096: 215 and 201 us).
 constexpr int kEpiRegs = 216, kOtherRegs = 72, kPartsRegs = 168;
 static_assert(2 * kEpiRegs + kOtherRegs <= 3 * kPartsRegs,
               "three warpgroups share the launch's registers");
@@ -1477,7 +1476,7 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     }
     if (a.staged) take_boxes(a, p.beta != 0.f ? kBoxesC : kBoxes);
     const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
-    const bool parts = p.out == kOutF32 && p.rows / p.groups >= kPartsRows;
+    const bool parts = p.out == kOutF32 && p.rows > kPart;
     static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
                                              {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
     *name = kNames[bf16][pair];

@@ -286,8 +286,7 @@ gemm_status_t gemm_bf16_f32acc_ex(int64_t M, int64_t N, int64_t K, float alpha,
  *   instead of rounding it, by about 1e-9 of a sum per step of K; an FP32 D is
  *   therefore summed 768 steps at a time and the parts added with rounding
  *   (relative error 7e-7 with BF16 inputs, 9e-7 with FP16, at any K or number
- *   of rows; measured on normally distributed values).  Not so the weight
- *   gradients of groups of fewer than 192 rows on average.
+ *   of rows of a group; measured on normally distributed values).
  * Workspace, from the library's pool as above: gathered rows are copied into
  *   group order where that is faster (16-bit inputs: rows x K values, or
  *   rows x M for the weight gradient); gemm_lora keeps X LA of up to 128 MiB at
