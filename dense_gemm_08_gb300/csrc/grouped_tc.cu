@@ -246,33 +246,161 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
-__device__ __forceinline__ float value_16(const void *p, int64_t at, int ab_format) {
-    const uint16_t b = static_cast<const uint16_t *>(p)[at];
-    return ab_format == 1 ? __uint_as_float(static_cast<uint32_t>(b) << 16)
-                          : __half2float(__ushort_as_half(b));
+// 16-bit inputs: a value, and the bits of an infinity (more: a NaN).
+__device__ __forceinline__ float value_16(uint32_t bits, int ab_format) {
+    return ab_format == 1 ? __uint_as_float(bits << 16)
+                          : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+__device__ __forceinline__ uint32_t infinity_16(int ab_format) {
+    return ab_format == 1 ? 0x7f80u : 0x7c00u;
+}
+__device__ __forceinline__ void widen_8(uint4 q, int ab_format, float (&v)[8]) {
+    const uint32_t b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = value_16((b[i / 2] >> (i % 2 * 16)) & 0xffffu, ab_format);
+}
+// The largest magnitude among eight values, as bits.
+__device__ __forceinline__ uint32_t top_of_8(uint4 q) {
+    uint32_t top = 0;
+    for (uint32_t w : {q.x, q.y, q.z, q.w}) top = max(top, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+    return top;
 }
 
-// lora: the sum of D(i, n) by its definition in FP32, from row i's own adapter
-// only (one column per lane; 0 past N).
-__device__ __noinline__ float lora_exact(const Args &a, int64_t i, int64_t n) {
+// lora: a slot's LB meets zeros of V in the rows of other adapters; where it
+// holds infinities or NaNs those products are NaN, and the sum says nothing.
+// Such values of D are computed again by their definition in FP32, from the
+// row's own adapter alone -- but not the others whose sums are not finite, which
+// their own row of X or column of W made so: a request with a NaN costs its
+// batch nothing.
+//
+// A warp's 32 x 32 block of D from row0 and n0 on, already written; bit j of
+// `bad`: the sum of this lane's row and column n0 + j is not finite.  Left as
+// they are:
+//   - rows with a NaN in their V, or without an adapter in X: NaN in any case;
+//   - columns that are finite in the LB of all the tile's adapters, and those
+//     where the row's own adapter alone is not finite and holds a NaN.
+// The others take a column per lane, eight rows at a time to a value of W (64
+// rows, 48 adapters, 4096 -> 14336, 40 us when all is finite: a NaN in a row of X
+// 40, an infinity 71, one infinity in an adapter 1500, an adapter of NaNs 3300).
+__device__ __noinline__ void lora_redo(const Args &a, int64_t row0, int64_t n0, int tile_m,
+                                       uint32_t bad) {
     const LoraProblem &l = a.l;
-    if (n >= l.N) return 0.f;
-    float s = 0.f;
-    for (int64_t k = 0; k < l.K; ++k)
-        s = fmaf(value_16(l.X, i * l.ldx + k, a.ab_format),
-                 value_16(l.W, l.w_kmajor ? n * l.ldw + k : k * l.ldw + n, a.ab_format), s);
-    const int slot = a.plan.slot[i];
-    if (slot < 0) return s;
-    const int64_t ad = l.adapter[i];
-    const uint16_t *v = a.plan.V + i * a.plan.ldv + static_cast<int64_t>(slot) * a.plan.rc;
-    float u = 0.f;
-    for (int64_t j = 0; j < l.rank; ++j) {
-        float x = value_16(v, j, a.ab_format);
-        if (a.plan.rc > a.plan.r_pad) x += value_16(v, a.plan.r_pad + j, a.ab_format);
-        u = fmaf(x, value_16(l.LB, ad * l.stride_b + (l.b_kmajor ? n * l.ld_b + j : j * l.ld_b + n),
-                             a.ab_format), u);
+    const LoraPlan &pl = a.plan;
+    const int lane = threadIdx.x % 32;
+    const uint32_t inf = infinity_16(a.ab_format);
+    const uint16_t *const x0 = static_cast<const uint16_t *>(l.X) + row0 * l.ldx;
+    const uint16_t *const v0 = pl.V + row0 * pl.ldv;
+    const int slot = bad != 0 ? pl.slot[row0 + lane] : -1;
+    const int64_t k8 = l.K / 8 * 8;
+
+    if (bad != 0 && slot >= 0) {
+        const uint16_t *v = v0 + lane * pl.ldv + static_cast<int64_t>(slot) * pl.rc;
+        for (int j = 0; j < l.rank; ++j)
+            if ((v[j] & 0x7fffu) > inf) bad = 0;
     }
-    return s + u;
+    for (uint32_t left = __ballot_sync(0xffffffffu, bad != 0 && slot < 0); left != 0; left &= left - 1) {
+        const int r = __ffs(left) - 1;
+        const uint16_t *x = x0 + r * l.ldx;
+        uint32_t top = 0;
+        for (int64_t k = lane * 8; k < k8; k += 256)
+            top = max(top, top_of_8(__ldg(reinterpret_cast<const uint4 *>(x + k))));
+        if (k8 + lane < l.K) top = max(top, x[k8 + lane] & 0x7fffu);
+        if (__any_sync(0xffffffffu, top > inf) && lane == r) bad = 0;
+    }
+    if (!__any_sync(0xffffffffu, bad != 0)) return;
+
+    // this lane's column of the slots' LB: the first slot that is not finite
+    // there, whether it holds a NaN, whether there are more
+    const bool inside = n0 + lane < l.N;
+    const int64_t n = inside ? n0 + lane : l.N - 1;
+    const int count = pl.count[tile_m];
+    const int *const list = pl.list + static_cast<int64_t>(tile_m) * pl.tile_rows;
+    int first = -1;
+    bool has_nan = false, more = false;
+    for (int s = 0; s < count; ++s) {
+        const uint16_t *lb = static_cast<const uint16_t *>(l.LB) + list[s] * l.stride_b +
+                             (l.b_kmajor ? n * l.ld_b : n);
+        const int64_t step = l.b_kmajor ? 1 : l.ld_b;
+        const int64_t r8 = l.b_kmajor ? l.rank / 8 * 8 : 0;
+        uint32_t top = 0;
+        for (int64_t j = 0; j < r8; j += 8)
+            top = max(top, top_of_8(__ldg(reinterpret_cast<const uint4 *>(lb + j))));
+#pragma unroll 8
+        for (int64_t j = r8; j < l.rank; ++j) top = max(top, __ldg(lb + j * step) & 0x7fffu);
+        if (top < inf || !inside) continue;
+        more = first >= 0;
+        if (first < 0) first = s, has_nan = top > inf;
+    }
+    uint32_t redo = 0;
+#pragma unroll 1
+    for (int r = 0; r < 32; ++r) {
+        const int own = __shfl_sync(0xffffffffu, slot, r);
+        const uint32_t cols = __ballot_sync(
+            0xffffffffu, first >= 0 && (more || first != own || !has_nan));
+        if (lane == r) redo = cols & bad;
+    }
+    const uint32_t rows = __ballot_sync(0xffffffffu, redo != 0);
+
+    const uint16_t *w = static_cast<const uint16_t *>(l.W) + (l.w_kmajor ? n * l.ldw : n);
+    const int64_t w_step = l.w_kmajor ? 1 : l.ldw;
+    const float bias = a.out.bias != nullptr ? a.out.bias[n] : 0.f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+        const uint32_t some = (rows >> r0) & 0xffu;
+        if (some == 0) continue;
+        // (rows that are not to be replaced repeat one that is)
+        const uint16_t *x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = x0 + (r0 + ((some >> i) & 1u ? i : __ffs(some) - 1)) * l.ldx;
+        float sum[8] = {};
+#pragma unroll 1
+        for (int64_t k = 0; k < k8; k += 8) {
+            float wv[8];
+            if (l.w_kmajor) {
+                widen_8(__ldg(reinterpret_cast<const uint4 *>(w + k)), a.ab_format, wv);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wv[i] = value_16(__ldg(w + (k + i) * w_step), a.ab_format);
+            }
+            uint4 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __ldg(reinterpret_cast<const uint4 *>(x[i] + k));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float xv[8];
+                widen_8(q[i], a.ab_format, xv);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) sum[i] = fmaf(xv[c], wv[c], sum[i]);
+            }
+        }
+        for (int64_t k = k8; k < l.K; ++k) {
+            const float wk = value_16(w[k * w_step], a.ab_format);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(value_16(x[i][k], a.ab_format), wk, sum[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!((some >> i) & 1u)) continue;
+            const int r = r0 + i, own = __shfl_sync(0xffffffffu, slot, r);
+            if (own >= 0) {
+                const uint16_t *v = v0 + r * pl.ldv + static_cast<int64_t>(own) * pl.rc;
+                const uint16_t *lb = static_cast<const uint16_t *>(l.LB) + list[own] * l.stride_b +
+                                     (l.b_kmajor ? n * l.ld_b : n);
+                const int64_t step = l.b_kmajor ? 1 : l.ld_b;
+                float u = 0.f;
+                for (int64_t j = 0; j < l.rank; ++j) {
+                    float vj = value_16(v[j], a.ab_format);
+                    if (pl.rc > pl.r_pad) vj += value_16(v[pl.r_pad + j], a.ab_format);
+                    u = fmaf(vj, value_16(__ldg(lb + j * step), a.ab_format), u);
+                }
+                sum[i] += u;
+            }
+            if ((__shfl_sync(0xffffffffu, redo, r) >> lane) & 1u)
+                store_out(a.out.D, (row0 + r) * a.out.ldd + n, activate(sum[i] + bias, a.out.act),
+                          a.out.out);
+        }
+    }
 }
 
 template <int CG, int MODE, bool GATHER, bool PARTS>
@@ -847,47 +975,18 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                 tmem_load_32cols(t_acc + chunk * 32, raw);
                 if (chunk == last) release_acc();
             };
-            // lora: a slot's LB meets zeros of V in the rows of other adapters;
-            // where it holds infinities or NaNs those products are NaN.  Sums
-            // that are not finite are computed again from the row's own adapter
-            // alone.
-            auto redo_block = [&](int chunk, uint32_t (&raw)[32]) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t b = raw[j] & 0x7fffffffu;
-                    top = b > top ? b : top;
-                }
-                const bool redo = args.plan.count != nullptr && lane < nrows && top >= 0x7f800000u;
-                if (!__any_sync(0xffffffffu, redo)) return;
-#pragma unroll 1
-                for (int l = 0; l < nrows; ++l) {
-                    if (!__shfl_sync(0xffffffffu, redo ? 1 : 0, l)) continue;
-                    const float mine = lora_exact(args, row0 + l, t.n0 + chunk * 32 + lane);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float x = __shfl_sync(0xffffffffu, mine, j);
-                        if (lane == l && (raw[j] & 0x7fffffffu) >= 0x7f800000u)
-                            raw[j] = __float_as_uint(x);
-                    }
-                }
+            // lora: which of this lane's sums are not finite, and what to do about
+            // them once the block is written (lora_redo)
+            auto bad_sum = [](float x) -> uint32_t { return fabsf(x) <= FLT_MAX ? 0u : 1u; };
+            auto bad_quad = [&](float4 x) -> uint32_t {
+                return bad_sum(x.x) | bad_sum(x.y) << 1 | bad_sum(x.z) << 2 | bad_sum(x.w) << 3;
             };
-            auto redo_box = [&](int chunk) {  // the same, for the sums in the box
-                bool redo = false;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float4 x = ld_shared_v4(boxes0 + box_quad(lane, q));
-                    redo |= !(fabsf(x.x) <= FLT_MAX && fabsf(x.y) <= FLT_MAX &&
-                              fabsf(x.z) <= FLT_MAX && fabsf(x.w) <= FLT_MAX);
-                }
-                redo = redo && args.plan.count != nullptr && lane < nrows;
-                __syncwarp();
-                for (uint32_t left = __ballot_sync(0xffffffffu, redo); left != 0; left &= left - 1) {
-                    const int l = __ffs(left) - 1;
-                    const uint32_t at = boxes0 + box_quad(l, lane / 4) + lane % 4 * 4;
-                    const float mine = lora_exact(args, row0 + l, t.n0 + chunk * 32 + lane);
-                    if (!(fabsf(ld_shared_f32(at)) <= FLT_MAX)) st_shared_f32(at, mine);
-                }
+            auto in_rows = [&](uint32_t bad) -> uint32_t {
+                return args.plan.count != nullptr && lane < nrows ? bad : 0u;
+            };
+            auto redo_block = [&](int chunk, uint32_t bad) {
+                if (__any_sync(0xffffffffu, bad != 0))
+                    lora_redo(args, row0, t.n0 + chunk * 32, t.tile_m, bad);
             };
             if constexpr (PARTS) {
                 // run: the sums of this warp's blocks, where they have several parts
@@ -914,6 +1013,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     release_acc();
                 }
                 if (aborted) break;
+                uint32_t bad[4] = {};  // (lora, of this warp's blocks)
 #pragma unroll 1
                 for (int chunk = half; chunk < n_chunks; chunk += 2) {
                     if (staged) open_box();
@@ -938,8 +1038,16 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                         }
                         put(raw);
                     }
-                    if constexpr (MODE == kLora) redo_box(chunk);
                     if (!staged) {
+                        if constexpr (MODE == kLora) {
+                            uint32_t b = 0;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                b |= bad_quad(ld_shared_v4(boxes0 + box_quad(lane, q))) << (q * 4);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (chunk == half + 2 * i) bad[i] = in_rows(b);
+                        }
                         __syncwarp();
                         store_from_box<MODE == kWgrad>(boxes0, o, row0, nrows, t.n0 + chunk * 32,
                                                        ncols - chunk * 32);
@@ -958,6 +1066,11 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     close_box(chunk);
                 }
                 if (aborted) break;
+                if constexpr (MODE == kLora) {
+                    // (after the loop: the parts' sums need no registers any more)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) redo_block(half + 2 * i, bad[i]);
+                }
                 if (!parts && last < 0 && !empty_sum) release_acc();
                 continue;
             }
@@ -1016,6 +1129,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     load_c_columns(o, row0, nrows, t.n0 + chunk * 32, ncols - chunk * 32, c);
             };
             if (last >= 0) load_c(half);
+            uint32_t bads[4] = {};
             if (!empty_sum && !next_acc()) {
                 aborted = true;
                 break;
@@ -1023,15 +1137,20 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
 #pragma unroll 1
             for (int chunk = half; chunk < n_chunks; chunk += 2) {
                 float v[32];
+                uint32_t bad = 0;
                 if (empty_sum) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 } else {
                     uint32_t raw[32];
                     take_block(chunk, raw);
-                    if constexpr (MODE == kLora) redo_block(chunk, raw);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                    if constexpr (MODE == kLora) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) bad |= bad_sum(v[j]) << j;
+                        bad = in_rows(bad);
+                    }
                 }
                 const int left = ncols - chunk * 32;
                 const int width = left < 32 ? left : 32;
@@ -1048,6 +1167,15 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     store_columns(v, o, row0, nrows, c0, width);
                 }
                 __syncwarp();
+                if constexpr (MODE == kLora) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (chunk == half + 2 * i) bads[i] = bad;
+                }
+            }
+            if constexpr (MODE == kLora) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) redo_block(half + 2 * i, bads[i]);
             }
             if (last < 0 && !empty_sum) release_acc();
         }
@@ -1513,9 +1641,10 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
     a.out.row_vec = row_alignment(p.D, p.ldd, 0, elt);
     a.b_kmajor = p.w_kmajor ? 1 : 0;
     a.ab_format = bf16 ? 1 : 0;
-    // 1 s per wait, longer where recomputing a tile's sums one by one could
-    // take as long
-    a.timeout_ns = 1000ull * 1000ull * 1000ull * static_cast<uint64_t>(1 + p.K / 65536);
+    // 1 s per wait, and what lora_redo may take meanwhile: up to four blocks a
+    // warp, 1 us per step of K in all (16 are allowed)
+    a.timeout_ns = 1000ull * 1000ull * 1000ull;
+    if (p.adapters > 0) a.timeout_ns += static_cast<uint64_t>(p.K) * 16000ull;
     const bool parts = p.out == kOutF32 && p.K > kPart;
     const int64_t pair_tiles = ceil_div(p.M, 2 * BM) * ceil_div(p.N, 256);
     const bool pair = d->pairs > 0 && p.M > BM && pair_tiles >= d->pairs;
