@@ -106,7 +106,9 @@ struct LoraPlan {
     int *count;  // [tiles] slots in use
     int *list;   // [tiles][tile_rows] the slots' adapters
     int *slot;   // [rows] each row's slot, -1: no adapter
-    float *part;  // lora_shrink_part_bytes of scratch
+    // lora_shrink_part_bytes of scratch, [parts of K][rows][r_pad] sums; it
+    // leaves s_a X(i) LA_a, not rounded, in the first rows x r_pad of them
+    float *part;
 };
 cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InType in,
                                cudaStream_t stream);

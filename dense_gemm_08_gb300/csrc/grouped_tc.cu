@@ -271,12 +271,13 @@ __device__ __forceinline__ uint32_t top_of_8(uint4 q) {
 // Such values of D are computed again by their definition in FP32, from the
 // row's own adapter alone -- but not the others whose sums are not finite, which
 // their own row of X or column of W made so: a request with a NaN costs its
-// batch nothing.
+// batch nothing.  So are the rows whose first product passed the inputs' type
+// (65504 for FP16) and is infinite in V only.
 //
 // A warp's 32 x 32 block of D from row0 and n0 on, already written; bit j of
 // `bad`: the sum of this lane's row and column n0 + j is not finite.  Left as
 // they are:
-//   - rows with a NaN in their V, or without an adapter in X: NaN in any case;
+//   - rows with a NaN in X LA, or without an adapter in X: NaN in any case;
 //   - columns that are finite in the LB of all the tile's adapters, and those
 //     where the row's own adapter alone is not finite and holds a NaN.
 // The others take a column per lane, eight rows at a time to a value of W (64
@@ -289,14 +290,18 @@ __device__ __noinline__ void lora_redo(const Args &a, int64_t row0, int64_t n0, 
     const int lane = threadIdx.x % 32;
     const uint32_t inf = infinity_16(a.ab_format);
     const uint16_t *const x0 = static_cast<const uint16_t *>(l.X) + row0 * l.ldx;
-    const uint16_t *const v0 = pl.V + row0 * pl.ldv;
+    const float *const u0 = pl.part + row0 * pl.r_pad;
     const int slot = bad != 0 ? pl.slot[row0 + lane] : -1;
     const int64_t k8 = l.K / 8 * 8;
 
+    bool passed = false;  // X LA passed the inputs' type
     if (bad != 0 && slot >= 0) {
-        const uint16_t *v = v0 + lane * pl.ldv + static_cast<int64_t>(slot) * pl.rc;
-        for (int j = 0; j < l.rank; ++j)
-            if ((v[j] & 0x7fffu) > inf) bad = 0;
+        const uint16_t *v = pl.V + (row0 + lane) * pl.ldv + static_cast<int64_t>(slot) * pl.rc;
+        const float *u = u0 + lane * pl.r_pad;
+        for (int j = 0; j < l.rank; ++j) {
+            if (isnan(u[j])) bad = 0;
+            passed |= (v[j] & 0x7fffu) == inf && fabsf(u[j]) <= FLT_MAX;
+        }
     }
     for (uint32_t left = __ballot_sync(0xffffffffu, bad != 0 && slot < 0); left != 0; left &= left - 1) {
         const int r = __ffs(left) - 1;
@@ -335,8 +340,9 @@ __device__ __noinline__ void lora_redo(const Args &a, int64_t row0, int64_t n0, 
 #pragma unroll 1
     for (int r = 0; r < 32; ++r) {
         const int own = __shfl_sync(0xffffffffu, slot, r);
+        const bool all = __shfl_sync(0xffffffffu, passed, r);
         const uint32_t cols = __ballot_sync(
-            0xffffffffu, first >= 0 && (more || first != own || !has_nan));
+            0xffffffffu, inside && (all || (first >= 0 && (more || first != own || !has_nan))));
         if (lane == r) redo = cols & bad;
     }
     const uint32_t rows = __ballot_sync(0xffffffffu, redo != 0);
@@ -384,17 +390,14 @@ __device__ __noinline__ void lora_redo(const Args &a, int64_t row0, int64_t n0, 
             if (!((some >> i) & 1u)) continue;
             const int r = r0 + i, own = __shfl_sync(0xffffffffu, slot, r);
             if (own >= 0) {
-                const uint16_t *v = v0 + r * pl.ldv + static_cast<int64_t>(own) * pl.rc;
+                const float *u = u0 + r * pl.r_pad;
                 const uint16_t *lb = static_cast<const uint16_t *>(l.LB) + list[own] * l.stride_b +
                                      (l.b_kmajor ? n * l.ld_b : n);
                 const int64_t step = l.b_kmajor ? 1 : l.ld_b;
-                float u = 0.f;
-                for (int64_t j = 0; j < l.rank; ++j) {
-                    float vj = value_16(v[j], a.ab_format);
-                    if (pl.rc > pl.r_pad) vj += value_16(v[pl.r_pad + j], a.ab_format);
-                    u = fmaf(vj, value_16(__ldg(lb + j * step), a.ab_format), u);
-                }
-                sum[i] += u;
+                float own_sum = 0.f;
+                for (int64_t j = 0; j < l.rank; ++j)
+                    own_sum = fmaf(u[j], value_16(__ldg(lb + j * step), a.ab_format), own_sum);
+                sum[i] += own_sum;
             }
             if ((__shfl_sync(0xffffffffu, redo, r) >> lane) & 1u)
                 store_out(a.out.D, (row0 + r) * a.out.ldd + n, activate(sum[i] + bias, a.out.act),

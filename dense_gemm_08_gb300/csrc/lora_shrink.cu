@@ -40,7 +40,6 @@ struct ShrinkArgs {
     int ab_format;
     int la_z_step;  // 0 when all adapters share one LA
     int ks;         // CTAs of a cluster, each with a part of K
-    float *part;    // tensor cores: [ks][M][r_pad] parts of the sums
     uint64_t timeout_ns;
 };
 
@@ -282,6 +281,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_rows_kernel(const Shrink
 #pragma unroll
             for (int c = 0; c < kMaxCluster; ++c) sum += v[c];
             part[0][tid] = sum * scale;
+            a.plan.part[row * a.plan.r_pad + tid] = sum * scale;
         }
         __syncthreads();
         write_v_row(a, row, slot, count, part[0]);
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = quarter * 32 + lane;
         const int my_slot = r < n_mine ? t.slot_of[off + r] : -1;
         const int64_t row = row_first + r;
-        float *const mine = a.part + (static_cast<int64_t>(rank) * p.M + row) * pl.r_pad;
+        float *const mine = pl.part + (static_cast<int64_t>(rank) * p.M + row) * pl.r_pad;
         for (int s = warp / 4; s < ns; s += 2) {
             const int slot = used[first_used + s];
             for (int j = 0; j < pl.r_pad; j += 16) {
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = r_begin + i / n_hi, j = i % n_hi * 8;
         const int own = t.slot_of[off + r];
         if (own < 0 || pass_of[own] % gridDim.z != blockIdx.z) continue;
-        const float *part = a.part + (row_first + r) * pl.r_pad + j;
+        float *const part = pl.part + (row_first + r) * pl.r_pad + j;
         float4 x[kMaxCluster], y[kMaxCluster];
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {  // all in flight, then added in order
@@ -532,12 +532,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[4] += y[k].x, u[5] += y[k].y, u[6] += y[k].z, u[7] += y[k].w;
         }
         const float scale = p.scale != nullptr ? p.scale[t.list[own]] : 1.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] *= scale;
+        // (in the first part's place, which this thread alone has read)
+        *reinterpret_cast<float4 *>(part) = make_float4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<float4 *>(part + 4) = make_float4(u[4], u[5], u[6], u[7]);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint16_t h0, l0, h1, l1;
-            split_16(u[2 * k] * scale, a.ab_format, h0, l0);
-            split_16(u[2 * k + 1] * scale, a.ab_format, h1, l1);
+            split_16(u[2 * k], a.ab_format, h0, l0);
+            split_16(u[2 * k + 1], a.ab_format, h1, l1);
             hi[k] = h0 | (static_cast<uint32_t>(h1) << 16);
             lo[k] = l0 | (static_cast<uint32_t>(l1) << 16);
         }
@@ -584,7 +589,7 @@ static int shrink_parts(const LoraProblem &p, int sms) {
 }
 
 size_t lora_shrink_part_bytes(int64_t rows, int r_pad) {
-    if (rows <= kRowsMax) return 0;
+    if (rows <= kRowsMax) return static_cast<size_t>(rows) * r_pad * sizeof(float);
     // parts x rows: at most SMs x 128 while there are several parts (256 SMs allowed for)
     const int64_t most = rows > 256 * BM ? rows : 256 * BM;
     const int64_t n = kMaxCluster * rows < most ? kMaxCluster * rows : most;
@@ -664,7 +669,6 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     if (!ok) return cudaErrorInvalidValue;
     const int64_t tiles = (p.M + BM - 1) / BM;
     a.ks = shrink_parts(p, g_sms[dev]);
-    a.part = plan.part;
     const int64_t slots = p.adapters < BM ? p.adapters : BM;
     const int64_t passes = (slots * plan.r_pad + 255) / 256;
     int64_t z = g_sms[dev] / (tiles * a.ks);

@@ -404,7 +404,8 @@ gemm_status_t gemm_grouped_wgrad_f16_f32acc(int64_t groups, int64_t rows, int64_
  * NaNs).  Rounding: the first product scale * X LA is summed in FP32 and
  * enters the second one rounded to the inputs' type when D has that type, and
  * as the sum of two such values (about 16 bits for BF16, 22 for FP16) when D
- * is FP32; with FP16 it must stay inside FP16's range.
+ * is FP32.  Rows where it passes FP16's range are computed by their definition
+ * in FP32 instead, far more slowly.
  * Accuracy: the bound of gemm_grouped_* on X W, plus 2^-8 (2^-15 with an FP32
  * D) of sum |scale (X LA)| |LB|.
  */
