@@ -405,9 +405,10 @@ gemm_status_t gemm_grouped_wgrad_f16_f32acc(int64_t groups, int64_t rows, int64_
  * enters the second one rounded to the inputs' type when D has that type, and
  * as the sum of two such values (about 16 bits for BF16, 22 for FP16) when D
  * is FP32.  Rows where it passes FP16's range are computed by their definition
- * in FP32 instead, far more slowly.
+ * in FP32 instead, far more slowly; where it is small, FP16 holds it in steps
+ * of 2^-24, so a first product below 2^-25 (a tiny scale, X or LA) counts as 0.
  * Accuracy: the bound of gemm_grouped_* on X W, plus 2^-8 (2^-15 with an FP32
- * D) of sum |scale (X LA)| |LB|.
+ * D) of sum |scale (X LA)| |LB|; with FP16 inputs also 2^-25 sum |LB|.
  */
 gemm_status_t gemm_lora_bf16_f32acc(int64_t M, int64_t N, int64_t K, const gemm_bf16_t *X,
                                     int64_t ldx, const gemm_bf16_t *W, int64_t ldw,

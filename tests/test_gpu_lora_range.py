@@ -56,3 +56,35 @@ def test_past_it_beside_another_adapters_infinities():
     tol = tol + K * 2.0 ** -24 * (x @ w)
     keep = (ids.cpu().numpy() == 1) | (ids.cpu().numpy() == -1)
     assert_close(D[torch.from_numpy(keep).cuda()], ref[keep], tol[keep], "f32")
+
+
+@pytest.mark.parametrize("M", [3, 90, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("down", [0, 8, 14, 20, 30])
+def test_small_first_products(M, dtype, out, down):
+    """The documented bound: 2^-8 (an FP32 D 2^-15) of sum |u LB|, and with FP16 inputs
+    2^-25 sum |LB|; u = scale * X LA down to far below FP16's smallest step."""
+    out = dtype if out == "same" else out
+    rng = np.random.default_rng(M + down)
+    K, N, rank, n = 264, 200, 16, 3
+    X, W, LA, LB = operands(rng, M, K, N, rank, n, dtype, (1, 1, 1))
+    W *= 0  # (the second product alone)
+    LB *= 2.0 ** 12
+    ids = torch.from_numpy((np.arange(M) % (n + 1) - 1).astype(np.int32)).cuda()
+    s = torch.full((n,), 2.0 ** -down, device="cuda")
+    D = lib.gemm_lora(X, W, LA, LB, ids, scale=s, out_dtype=TORCH[out])
+    done()
+    ref, tol = np.zeros((M, N)), np.zeros((M, N))
+    x, la, lb = (t.double().cpu().numpy() for t in (X, LA, LB))
+    for i, a in enumerate(ids.tolist()):
+        if a < 0:
+            continue
+        u = 2.0 ** -down * (x[i] @ la[a])
+        summed = rel_sum(K) * 2.0 ** -down * (np.abs(x[i]) @ np.abs(la[a]))  # u's own sum
+        ref[i] = u @ lb[a]
+        part = 2.0 ** -15 if out == "f32" else 2.0 ** -8
+        tol[i] = (part * np.abs(u) + rel_sum(rank) * np.abs(u) + summed) @ np.abs(lb[a])
+        if dtype == "f16":
+            tol[i] += 2.0 ** -25 * np.abs(lb[a]).sum(0)
+    assert_close(D, ref, tol, out)
