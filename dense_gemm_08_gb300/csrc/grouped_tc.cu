@@ -12,8 +12,8 @@
 //
 //   rows: a row tile may end inside the next group's rows.  They only reach
 //     accumulator rows that are not stored (each row of D depends on its own
-//     row of A), so no zero fill is needed.  Gathered rows come four at a time
-//     by TMA gather, issued by two warps of their own.
+//     row of A), so no zero fill is needed.  Gathered rows of small
+//     groups come four at a time by TMA gather, issued by a warp of its own.
 //   wgrad: both operands have their rows along K and are MN-major.  A group's
 //     last K block must not read the next group's rows (not even times zero:
 //     they may be infinite), so that block is fetched by TMA gather with row
@@ -40,7 +40,7 @@ enum : int { kRows = 0, kWgrad = 1, kLora = 2 };
 constexpr int kGroupM = 16;  // row tiles per band of the raster inside a group
 constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 8;
-constexpr int kGatherWarps = 2;
+constexpr int kGatherWarps = 2;  // wgrad (rows: one, their tiles have 64 rows at most)
 constexpr int kRingBytes = 7 * 32768;
 // lora, up to 128 rows (single CTAs): a shorter ring, and 128 registers (launch
 // bounds of 512 threads), leave room on each SM for a CTA of the kernel that
@@ -82,15 +82,15 @@ constexpr int kEpiRegs = 216, kOtherRegs = 72, kPartsRegs = 168;
 static_assert(2 * kEpiRegs + kOtherRegs <= 3 * kPartsRegs,
               "three warpgroups share the launch's registers");
 
-// Warps 0-7: epilogue, 8: TMA, 9: MMA; 10 and 11, where there are any: gathers
-// (issued by warps of their own, so that the producer goes on with the copies
-// of whole boxes), or slices of LB (lora).
+// Warps 0-7: epilogue, 8: TMA, 9: MMA; 10 (and 11, for the weight gradients):
+// gathers, issued by warps of their own so that the producer goes on with the
+// copies of whole boxes, or slices of LB (lora).
 constexpr int kProducer = kEpiWarps, kIssuer = kEpiWarps + 1, kHelper = kEpiWarps + 2;
 template <int MODE, bool GATHER, bool PARTS>
 constexpr int threads() {
     return PARTS ? 384
                  : 64 + 32 * kEpiWarps +
-                       (GATHER || MODE == kWgrad ? 32 * kGatherWarps : MODE == kLora ? 32 : 0);
+                       (MODE == kWgrad ? 32 * kGatherWarps : GATHER || MODE == kLora ? 32 : 0);
 }
 template <int CG, int MODE, bool GATHER, bool PARTS>
 constexpr int max_threads() {
@@ -524,7 +524,6 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                             if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
                             if constexpr (GATHER) {
                                 if (mine > 0) mbar_arrive(go0 + 8 * stage);
-                                if (mine > 64) mbar_arrive(go0 + 8 * (kMaxStages + stage));
                             }
                             // several blocks of 64 at once: the maps count K in blocks
                             const int32_t block = kb * ksub;
@@ -792,7 +791,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                 }
             }
             __syncwarp();
-        } else if (MODE == kRows && !GATHER && warp >= kHelper) {
+        } else if (MODE == kRows && warp >= kHelper + (GATHER ? 1 : 0)) {
             // (they only gave their registers)
         } else if (warp >= kHelper) {
             // -------------------------------------------------------- gather warps
@@ -820,16 +819,16 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
             for (uint32_t w = first_tile; ok && tiles.get(w, t); w += tile_step, reverse = !reverse) {
                 const int32_t b0 = static_cast<int32_t>(t.n0 + rank * b_rows);
                 const int32_t m0 = static_cast<int32_t>(t.m0 + rank * BM);
-                int quads = 0;  // rows mode: this warp's quads of the tile
+                int quads = 0;  // rows mode: the tile's
                 int kb = 0;
                 if constexpr (MODE != kWgrad) {
-                    const int rows = cta_rows(t, rank) - half * 64;
-                    quads = rows <= 0 ? 0 : (rows >= 64 ? 16 : (rows + 3) / 4);
+                    const int rows = cta_rows(t, rank);  // (groups of few rows: at most 64)
+                    quads = (rows + 3) / 4;
                     __syncwarp();
     #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int r = lane + i * 32;
-                        mine[r] = r < rows ? __ldg(args.row_index + m0 + half * 64 + r) : -1;
+                        mine[r] = r < rows ? __ldg(args.row_index + m0 + r) : -1;
                     }
                     __syncwarp();
                     kb = first_block<CG>(w, t.nkb, reverse);
@@ -864,8 +863,8 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                                 gather(sb + j * 8192, &map_b_rows, b0 + 64 * j, mine, quads, fb);
                         } else {
                             for (int u = 0; u < ksub; ++u)
-                                gather(sa + (u * args.am + half * 64) * 128, &map_a_rows,
-                                       (kb * ksub + u) * BK, mine, quads, fb);
+                                gather(sa + u * args.am * 128, &map_a_rows, (kb * ksub + u) * BK, mine,
+                                       quads, fb);
                         }
                     }
                     if constexpr (MODE != kWgrad) kb = next_block<CG>(kb, t.nkb, reverse);
@@ -1206,6 +1205,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
 // groups of a few rows (kGatherRows on average) are gathered by TMA, which
 // saves a launch; others, and the weight gradients' rows, are put in order
 // first (16384 rows of 4096: 41 us at 6.5 TB/s).
+// (Tiles have 32 or 64 rows at such means.)
 constexpr int64_t kGatherRows = 16;
 __global__ void __launch_bounds__(256) order_rows_kernel(const uint16_t *A, int64_t lda,
                                                          int64_t rows_a, const int32_t *index,
