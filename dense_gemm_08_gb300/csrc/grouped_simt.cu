@@ -543,16 +543,13 @@ cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t strea
     a.l = p;
     GroupedProblem &g = a.g;
     g.groups = 1;
-    g.rows = g.rows_a = p.M;
     g.N = p.N;
     g.K = p.K;
     g.alpha = 1.f;
-    g.A = p.X;
     g.lda = p.ldx;
     g.B = p.W;
     g.ldb = p.ldw;
     g.b_kmajor = p.w_kmajor;
-    g.D = p.D;
     g.ldd = p.ldd;
     g.bias = p.bias;
     g.act = p.act;
@@ -561,26 +558,36 @@ cudaError_t launch_lora_simt(const LoraProblem &p, InType in, cudaStream_t strea
     a.vec_a = rows_on(p.X, p.ldx, 0, 2, 8);
     a.vec_b = rows_on(p.W, p.ldw, 0, 2, 8);
     a.vec_d = p.out == kOutF32 && rows_on(p.D, p.ldd, 0, 4, 16);
+    // U is at most 128 MiB (64 rows at least): more rows go in several launches
+    int64_t chunk = p.M;
     void *u = nullptr;
     const bool any = p.adapters > 0 && p.rank > 0 && p.K > 0;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
     if (any) {
-        e = workspace_alloc(static_cast<size_t>(p.M) * p.rank * sizeof(float), stream, &u);
+        const int64_t fit = (int64_t(128) << 20) / (p.rank * static_cast<int64_t>(sizeof(float))) / TM * TM;
+        const int64_t most = fit > TM ? fit : TM;
+        if (chunk > most) chunk = most;
+        e = workspace_alloc(static_cast<size_t>(chunk * p.rank) * sizeof(float), stream, &u);
         if (e != cudaSuccess) return e;
         a.U = static_cast<float *>(u);
-        const unsigned grid = static_cast<unsigned>(p.M < 65536 ? p.M : 65536);
-        if (in == InType::BF16)
-            lora_shrink_simt_kernel<uint16_t><<<grid, kShrinkThreads, 0, stream>>>(p, static_cast<float *>(u));
-        else
-            lora_shrink_simt_kernel<__half><<<grid, kShrinkThreads, 0, stream>>>(p, static_cast<float *>(u));
-        e = cudaGetLastError();
     } else {
         a.l.adapters = 0;
-        e = cudaSuccess;
     }
-    if (e == cudaSuccess)
-        {
-        const int64_t all = static_cast<int64_t>(tiles(p.M, TM)) * a.tiles_n;
+    for (int64_t row = 0; row < p.M && e == cudaSuccess; row += chunk) {
+        a.l.M = g.rows = g.rows_a = p.M - row < chunk ? p.M - row : chunk;
+        a.l.X = g.A = static_cast<const uint16_t *>(p.X) + row * p.ldx;
+        g.D = static_cast<uint8_t *>(p.D) + row * p.ldd * (p.out == kOutF32 ? 4 : 2);
+        if (any) {
+            a.l.adapter = p.adapter + row;
+            const unsigned grid = static_cast<unsigned>(a.l.M < 65536 ? a.l.M : 65536);
+            if (in == InType::BF16)
+                lora_shrink_simt_kernel<uint16_t><<<grid, kShrinkThreads, 0, stream>>>(a.l, static_cast<float *>(u));
+            else
+                lora_shrink_simt_kernel<__half><<<grid, kShrinkThreads, 0, stream>>>(a.l, static_cast<float *>(u));
+            e = cudaGetLastError();
+            if (e != cudaSuccess) break;
+        }
+        const int64_t all = static_cast<int64_t>(tiles(a.l.M, TM)) * a.tiles_n;
         a.ks = k_parts(all, p.K);
         e = launch_typed<kLora>(a, in, all * a.ks, stream);
     }
