@@ -454,6 +454,9 @@ def gemm(A, B, C=None, alpha=1.0, beta=0.0, out=None, stream=None):
 # ------------------------------------------------- torch helpers, grouped
 # These run once per layer and token, beside kernels of a few microseconds, so
 # they read each tensor attribute once and go straight to the C entry point.
+# With `stream` the work goes to that stream and new outputs belong to its memory
+# pool; as with torch's own operations, the caller orders the streams and calls
+# record_stream for tensors that another stream than their own uses.
 def stack_order(t):
     """(order, ld, stride) of a stack of matrices (3-D tensor), from its strides."""
     if t.dim() != 3:
@@ -520,6 +523,18 @@ def _stream_of(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _empty(shape, dtype, device, stream):
+    """An output that `stream` (None: torch's current stream) writes: memory of that stream's
+    pool, as work of another stream may still use what the current one's pool hands out."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _on_device(device):
     """Refuse operands that the kernels of the current device cannot read."""
     if device.type != "cuda":
@@ -567,9 +582,9 @@ def group_rows(ids, groups, stream=None):
     at = _int_vector(ids, n, "ids", device)
     _on_device(device)
     # (views of one allocation would cost the host more than three allocations)
-    offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
-    order = torch.empty(n, dtype=torch.int32, device=device)
-    position = torch.empty(n, dtype=torch.int32, device=device)
+    offsets = _empty(groups + 1, torch.int32, device, stream)
+    order = _empty(n, torch.int32, device, stream)
+    position = _empty(n, torch.int32, device, stream)
     st = library().gemm_group_rows(n, groups, at, offsets.data_ptr(), order.data_ptr(),
                                    position.data_ptr(), _stream_of(stream))
     if st != GEMM_OK:
@@ -604,7 +619,7 @@ def gemm_grouped(A, B, offsets, row_index=None, bias=None, activation=GEMM_ACT_N
         raise ValueError(f"out must be {rows} x {N}")
     _on_device(device)
     if out is None:
-        out = _torch().empty((rows, N), dtype=out_dtype, device=device)
+        out = _empty((rows, N), out_dtype, device, stream)
         ldd = N
     else:
         ldd = _row_major(out, "out")
@@ -657,7 +672,7 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
         c = C.data_ptr()
     _on_device(device)
     if out is None:
-        out = torch.empty((groups, M, N), dtype=out_dtype, device=device)
+        out = _empty((groups, M, N), out_dtype, device, stream)
         ldd, stride_d = max(N, 1), M * N
     fn = "gemm_grouped_wgrad_" + suffix
     st = getattr(library(), fn)(groups, rows, M, N, alpha, A.data_ptr(), lda, rows_a, index, at,
@@ -701,7 +716,7 @@ def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GE
         raise ValueError(f"out must be {M} x {N}")
     _on_device(device)
     if out is None:
-        out = _torch().empty((M, N), dtype=out_dtype, device=device)
+        out = _empty((M, N), out_dtype, device, stream)
         ldd = N
     else:
         ldd = _row_major(out, "out")
