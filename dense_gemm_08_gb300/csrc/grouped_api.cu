@@ -19,6 +19,10 @@ constexpr int64_t kMaxDim = 0x7fffffff;
 // Strides are at most 2^40 elements, more than any device holds.
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
+// The row products walk the groups 32 at a time to find a tile's (GroupWalk): 2^24
+// of them take 0.3 s, and 32-bit group numbers keep room for a step past the last.
+constexpr int64_t kMaxGroups = int64_t(1) << 24;
+
 bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxDim; }
 bool is_order(gemm_order_t o) { return o == GEMM_ROW_MAJOR || o == GEMM_COL_MAJOR; }
 int64_t at_least_1(int64_t v) { return v > 1 ? v : 1; }
@@ -63,8 +67,8 @@ gemm_status_t grouped(InType in, int64_t groups, int64_t rows, int64_t N, int64_
                       cudaStream_t stream) {
     gemm::set_last_kernel("");
     gemm_epilogue_t ep;
-    if (!dim_ok(groups) || !dim_ok(rows) || !dim_ok(N) || !dim_ok(K) || !is_order(order_b) ||
-        !epilogue_ok(epilogue, in, &ep))
+    if (!dim_ok(groups) || groups > kMaxGroups || !dim_ok(rows) || !dim_ok(N) || !dim_ok(K) ||
+        !is_order(order_b) || !epilogue_ok(epilogue, in, &ep))
         return GEMM_ERR_INVALID_VALUE;
     if (groups == 0 || rows == 0 || N == 0) return GEMM_OK;
     if (!usable(offsets, 4) || !usable(D, out_bytes(ep.d_type)) || ldd < N)

@@ -294,7 +294,8 @@ gemm_status_t gemm_bf16_f32acc_ex(int64_t M, int64_t N, int64_t K, float alpha,
  *   128 x groups counts.
  * Special values: a row's infinities and NaNs reach that row's results only
  *   (for the weight gradient: that group's); the activations pass NaNs on.
- * Sizes: each of rows, M, N, K, groups is at most 2^31 - 1; no rows or no
+ * Sizes: each of rows, M, N, K, groups is at most 2^31 - 1 (gemm_grouped_*:
+ *   2^24 groups, which each CTA walks to find its rows); no rows or no
  *   columns is a no-op (the weight gradient's groups without rows still give
  *   beta * C).  K == 0 or alpha == 0: A and B are not read.
  */
