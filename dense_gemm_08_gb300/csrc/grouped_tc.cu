@@ -1443,7 +1443,7 @@ cudaError_t launch_grouped_tc(const GroupedProblem &whole, InType in, cudaStream
     a.out.row_vec = row_alignment(p.D, p.ldd, 0, p.out == kOutF32 ? 4 : 2);
     a.b_kmajor = p.b_kmajor ? 1 : 0;
     a.ab_format = bf16 ? 1 : 0;
-    a.timeout_ns = 1000ull * 1000ull * 1000ull;
+    a.timeout_ns = wait_limit_ns(ceil_div(p.K, BK), p.groups);
     const bool one_b = p.groups == 1 || p.stride_b == 0;
     a.z_step = one_b ? 0 : 1;
     // Groups that may hold rows, and row tiles if the rows spread evenly.
@@ -1549,7 +1549,6 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     a.stride_d = p.stride_d;
     a.stride_c = p.stride_c;
     a.ab_format = bf16 ? 1 : 0;
-    a.timeout_ns = 1000ull * 1000ull * 1000ull;
     const int64_t pair_tiles = p.groups * ceil_div(p.M, 2 * BM) * ceil_div(p.N, 256);
     const bool pair = d->pairs > 0 && p.M > BM && pair_tiles >= d->pairs;
     const int cg = pair ? 2 : 1;
@@ -1607,6 +1606,7 @@ cudaError_t launch_wgrad_tc(const WgradProblem &whole, InType in, cudaStream_t s
     }
     if (a.staged) take_boxes(a, p.beta != 0.f ? kBoxesC : kBoxes);
     const int64_t max_tiles = p.groups * a.tiles_m * a.tiles_n;
+    a.timeout_ns = wait_limit_ns(ceil_div(p.rows, BK), 0, ceil_div(max_tiles * cg, d->sms));
     const bool parts = p.out == kOutF32 && p.rows > kPart;
     static const char *const kNames[2][2] = {{"wgrad_tc<f16>", "wgrad_tc<f16,pair>"},
                                              {"wgrad_tc<bf16>", "wgrad_tc<bf16,pair>"}};
@@ -1644,9 +1644,9 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
     a.out.row_vec = row_alignment(p.D, p.ldd, 0, elt);
     a.b_kmajor = p.w_kmajor ? 1 : 0;
     a.ab_format = bf16 ? 1 : 0;
-    // 1 s per wait, and what lora_redo may take meanwhile: up to four blocks a
-    // warp, 1 us per step of K in all (16 are allowed)
-    a.timeout_ns = 1000ull * 1000ull * 1000ull;
+    a.timeout_ns = wait_limit_ns(ceil_div(p.K, BK));
+    // and what lora_redo may take meanwhile: up to four blocks a warp, 1 us per
+    // step of K in all (16 are allowed)
     if (p.adapters > 0) a.timeout_ns += static_cast<uint64_t>(p.K) * 16000ull;
     const bool parts = p.out == kOutF32 && p.K > kPart;
     const int64_t pair_tiles = ceil_div(p.M, 2 * BM) * ceil_div(p.N, 256);

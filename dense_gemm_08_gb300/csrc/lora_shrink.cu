@@ -607,7 +607,7 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     a.p = p;
     a.plan = plan;
     a.ab_format = in == InType::BF16 ? 1 : 0;
-    a.timeout_ns = 1000ull * 1000ull * 1000ull;
+    a.timeout_ns = wait_limit_ns((p.K + BK - 1) / BK);
     cudaLaunchAttribute attr[2];
     set_pdl_attribute(&attr[0]);
     attr[1].id = cudaLaunchAttributeClusterDimension;

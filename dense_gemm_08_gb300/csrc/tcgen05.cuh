@@ -111,6 +111,16 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// The limit of a launch's waits: 1 s, and what a wait may span -- `steps` blocks
+// of 64 of K (the sums of one tile: 1 us each where all SMs load from DRAM at
+// once; 10 us are allowed), `groups` empty groups to walk past (20 ns; 200) and
+// `tiles` of the CTA that have no rows, written while the other warps are ahead
+// (2 us; 20).
+inline uint64_t wait_limit_ns(int64_t steps, int64_t groups = 0, int64_t tiles = 0) {
+    return 1000000000ull + static_cast<uint64_t>(steps) * 10000ull +
+           static_cast<uint64_t>(groups) * 200ull + static_cast<uint64_t>(tiles) * 20000ull;
+}
+
 __device__ __forceinline__ void raise_abort(volatile int *abort_flag) {
     *abort_flag = 1;
     atomicExch(&g_status, 1);
