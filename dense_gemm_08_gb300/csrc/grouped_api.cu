@@ -74,7 +74,7 @@ gemm_status_t grouped(InType in, int64_t groups, int64_t rows, int64_t N, int64_
     if (!usable(offsets, 4) || !usable(D, out_bytes(ep.d_type)) || ldd < N)
         return GEMM_ERR_INVALID_VALUE;
     if (K > 0 && alpha != 0.f) {
-        if (!usable(A, in_bytes(in)) || lda < K || !dim_ok(rows_a) ||
+        if ((!usable(A, in_bytes(in)) && rows_a != 0) || lda < K || !dim_ok(rows_a) ||
             (row_index == nullptr ? rows_a < rows : !usable(row_index, 4)) ||
             !stack_ok(B, in, K, N, ldb, order_b, stride_b, groups))
             return GEMM_ERR_INVALID_VALUE;
@@ -123,8 +123,8 @@ gemm_status_t wgrad(InType in, int64_t groups, int64_t rows, int64_t M, int64_t 
     if (beta != 0.f && (!usable(C, 4) || ldc < N || stride_c < 0 || stride_c > kMaxStride))
         return GEMM_ERR_INVALID_VALUE;
     if (rows > 0 && alpha != 0.f) {
-        if (!usable(A, in_bytes(in)) || !usable(B, in_bytes(in)) || lda < M || ldb < N ||
-            !dim_ok(rows_a) || (row_index == nullptr ? rows_a < rows : !usable(row_index, 4)))
+        if ((!usable(A, in_bytes(in)) && rows_a != 0) || !usable(B, in_bytes(in)) || lda < M ||
+            ldb < N || !dim_ok(rows_a) || (row_index == nullptr ? rows_a < rows : !usable(row_index, 4)))
             return GEMM_ERR_INVALID_VALUE;
     }
     const gemm_status_t dev = gemm::check_device_status();

@@ -271,7 +271,8 @@ gemm_status_t gemm_bf16_f32acc_ex(int64_t M, int64_t N, int64_t K, float alpha,
  *   computed from them is stored.
  * row_index (or NULL): product row r reads row row_index[r] of A, so rows
  *   need not be copied into group order first; an index outside [0, rows_a)
- *   reads a row of zeros.  Without it row r of A is read and rows_a >= rows.
+ *   reads a row of zeros (rows_a == 0: A may be NULL).  Without it row r of A is
+ *   read and rows_a >= rows.
  * Matrices: A and D are row-major (a group is a run of rows).  Matrix g of a
  *   stack starts stride elements after matrix g - 1 (stride_b = 0: one B for
  *   all groups).  Every matrix and group stride is in elements.
