@@ -1249,6 +1249,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
     std::once_flag once;
     cudaError_t err = cudaSuccess;
+    int dev = 0;
     int sms = 1;
     int pairs = 0;  // CTA pairs resident at once
 };
@@ -1271,18 +1272,25 @@ cudaLaunchConfig_t config(int grid, int ring, cudaStream_t stream, cudaLaunchAtt
     return cfg;
 }
 
+// Prepares a kernel on device `dev` before its first launch there.  Each kernel
+// has its own answer: one that cannot run does not take the others with it.
 template <int CG, int MODE, bool GATHER, bool PARTS>
-cudaError_t allow_smem() {
-    const auto kernel = grouped_tc_kernel<CG, MODE, GATHER, PARTS>;
-    if (PARTS) {
-        // the warpgroups divide what the launch gives: without it they would wait
-        cudaFuncAttributes at;
-        const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
-        if (e != cudaSuccess) return e;
-        if (at.numRegs != kPartsRegs) return cudaErrorInvalidKernelImage;
-    }
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_bytes(kRingBytes));
+cudaError_t prepared(int dev) {
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    std::call_once(once[dev], [dev] {
+        const auto kernel = grouped_tc_kernel<CG, MODE, GATHER, PARTS>;
+        if (PARTS) {
+            // the warpgroups divide what the launch gives: without it they would wait
+            cudaFuncAttributes at;
+            err[dev] = cudaFuncGetAttributes(&at, kernel);
+            if (err[dev] == cudaSuccess && at.numRegs != kPartsRegs) err[dev] = cudaErrorInvalidKernelImage;
+            if (err[dev] != cudaSuccess) return;
+        }
+        err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        smem_bytes(kRingBytes));
+    });
+    return err[dev];
 }
 
 DeviceInfo *device_info() {
@@ -1290,19 +1298,12 @@ DeviceInfo *device_info() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
     DeviceInfo *d = &g_dev[dev];
     std::call_once(d->once, [d, dev] {
+        d->dev = dev;
         int n = 0;
         d->err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (d->err != cudaSuccess) return;
         d->sms = n > 0 ? n : 1;
-        for (cudaError_t e :
-             {allow_smem<1, kRows, false, false>(), allow_smem<1, kRows, false, true>(),
-              allow_smem<1, kRows, true, false>(), allow_smem<1, kRows, true, true>(),
-              allow_smem<2, kRows, false, false>(), allow_smem<2, kRows, false, true>(),
-              allow_smem<1, kWgrad, false, false>(), allow_smem<1, kWgrad, false, true>(),
-              allow_smem<2, kWgrad, false, false>(), allow_smem<2, kWgrad, false, true>(),
-              allow_smem<1, kLora, false, false>(), allow_smem<1, kLora, false, true>(),
-              allow_smem<2, kLora, false, false>(), allow_smem<2, kLora, false, true>()})
-            if (d->err == cudaSuccess) d->err = e;
+        d->err = prepared<2, kRows, false, false>(dev);
         if (d->err != cudaSuccess) return;
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = config<2, kRows, false, false>(2 * (d->sms / 2), kRingBytes, 0, attr);
@@ -1318,7 +1319,10 @@ DeviceInfo *device_info() {
 }
 
 template <int CG, int MODE, bool GATHER, bool PARTS>
-cudaError_t launch_as(const CUtensorMap (&maps)[8], const Args &a, int grid, cudaStream_t stream) {
+cudaError_t launch_as(const CUtensorMap (&maps)[8], const Args &a, int grid, const DeviceInfo *d,
+                      cudaStream_t stream) {
+    const cudaError_t e = prepared<CG, MODE, GATHER, PARTS>(d->dev);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = config<CG, MODE, GATHER, PARTS>(grid, a.ring_bytes, stream, attr);
     return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, GATHER, PARTS>, maps[0], maps[1],
@@ -1343,14 +1347,14 @@ cudaError_t launch(const CUtensorMap (&maps)[8], Args &a, bool gather, int64_t m
     if (parts) {
         if (a.boxes == 0) take_boxes(a, kBoxes);
         if constexpr (MODE == kRows && CG == 1) {
-            if (gather) return launch_as<CG, MODE, true, true>(maps, a, grid, stream);
+            if (gather) return launch_as<CG, MODE, true, true>(maps, a, grid, d, stream);
         }
-        return launch_as<CG, MODE, false, true>(maps, a, grid, stream);
+        return launch_as<CG, MODE, false, true>(maps, a, grid, d, stream);
     }
     if constexpr (MODE == kRows && CG == 1) {
-        if (gather) return launch_as<CG, MODE, true, false>(maps, a, grid, stream);
+        if (gather) return launch_as<CG, MODE, true, false>(maps, a, grid, d, stream);
     }
-    return launch_as<CG, MODE, false, false>(maps, a, grid, stream);
+    return launch_as<CG, MODE, false, false>(maps, a, grid, d, stream);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
