@@ -116,7 +116,8 @@ bool lora_shrink_eligible(const LoraProblem &p);
 size_t lora_shrink_part_bytes(int64_t rows, int r_pad);
 cudaError_t lora_shrink_read_and_clear_status(cudaStream_t stream, int *status);
 
-// Reads and clears those kernels' device status word (after a sync).
+// Reads and clears those kernels' device status word (after a sync); 0 without a
+// copy while none of them has been launched on the device.
 cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status);
 
 // Rows grouped by a number (group_rows.cu).

@@ -21,6 +21,7 @@
 //     16-row slices that hold rows are multiplied.
 //   lora:   D(i, :) = act(X(i, :) op(W) + V(i, :) op(LB) + bias): the projection
 //     of all rows, its K loop continued over the slots of the tile's adapters.
+#include <atomic>
 #include <cfloat>
 #include <mutex>
 
@@ -1254,6 +1255,9 @@ struct DeviceInfo {
     int pairs = 0;  // CTA pairs resident at once
 };
 DeviceInfo g_dev[kMaxDevices];
+// A kernel of this file has been launched on the device (and stays so: it may
+// set its status word at any time until it ends).
+std::atomic<bool> g_launched[kMaxDevices];
 
 template <int CG, int MODE, bool GATHER, bool PARTS>
 cudaLaunchConfig_t config(int grid, int ring, cudaStream_t stream, cudaLaunchAttribute *attr) {
@@ -1323,6 +1327,7 @@ cudaError_t launch_as(const CUtensorMap (&maps)[8], const Args &a, int grid, con
                       cudaStream_t stream) {
     const cudaError_t e = prepared<CG, MODE, GATHER, PARTS>(d->dev);
     if (e != cudaSuccess) return e;
+    g_launched[d->dev].store(true);
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = config<CG, MODE, GATHER, PARTS>(grid, a.ring_bytes, stream, attr);
     return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<CG, MODE, GATHER, PARTS>, maps[0], maps[1],
@@ -1765,8 +1770,13 @@ cudaError_t launch_lora_tc(const LoraProblem &p, InType in, cudaStream_t stream,
 }
 
 cudaError_t grouped_tc_read_and_clear_status(cudaStream_t stream, int *status) {
+    *status = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !g_launched[dev].load()) return cudaSuccess;
     const int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_status, sizeof(int), 0,
+    e = cudaMemcpyFromSymbolAsync(status, g_status, sizeof(int), 0,
                                               cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e == cudaSuccess && *status != 0) {

@@ -17,6 +17,7 @@
 //              cluster of up to 8 CTAs splits K, as many passes run beside
 //              each other as the SMs have room for, and the parts of a sum
 //              are added in cluster order.
+#include <atomic>
 #include <mutex>
 
 #include "grouped.cuh"
@@ -575,6 +576,9 @@ constexpr int kMaxDevices = 64;
 std::once_flag g_once[kMaxDevices];
 cudaError_t g_err[kMaxDevices];
 int g_sms[kMaxDevices];
+// The tensor-core kernel has been launched on the device (the other one waits
+// for nothing).
+std::atomic<bool> g_launched[kMaxDevices];
 
 }  // namespace
 
@@ -677,12 +681,18 @@ cudaError_t launch_lora_shrink(const LoraProblem &p, const LoraPlan &plan, InTyp
     cfg.gridDim = dim3(static_cast<unsigned>(a.ks), static_cast<unsigned>(tiles),
                        static_cast<unsigned>(z));
     cfg.dynamicSmemBytes = kTcSmem;
+    g_launched[dev].store(true);
     return cudaLaunchKernelEx(&cfg, lora_shrink_tc_kernel, map_x, map_la, a);
 }
 
 cudaError_t lora_shrink_read_and_clear_status(cudaStream_t stream, int *status) {
+    *status = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !g_launched[dev].load()) return cudaSuccess;
     const int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(status, g_status, sizeof(int), 0,
+    e = cudaMemcpyFromSymbolAsync(status, g_status, sizeof(int), 0,
                                               cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e == cudaSuccess && *status != 0) {
