@@ -400,8 +400,9 @@ gemm_status_t gemm_grouped_wgrad_f16_f32acc(int64_t groups, int64_t rows, int64_
  * and the host does not read the numbers.  scale is `adapters` FP32 values or
  * NULL (all 1); epilogue as for gemm_grouped_* with one bias of N values.
  * The input gradient is the same call with W, LA and LB exchanged:
- * dX = dD op(W)^T + scale (dD LB^T) LA^T; the adapters' own gradients are
- * gemm_grouped_wgrad_* over rows grouped by adapter.
+ * dX = dD op(W)^T + scale (dD LB^T) LA^T.  The adapters' own gradients come from
+ * rows grouped by adapter (gemm_group_rows): U = X LA and T = dD LB^T are
+ * gemm_grouped_*, dLB = scale U^T dD and dLA = scale X^T T gemm_grouped_wgrad_*.
  * An adapter's values reach the rows that use it only (also infinities and
  * NaNs).  Rounding: the first product scale * X LA is summed in FP32 and
  * enters the second one rounded to the inputs' type when D has that type, and
