@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                                 if (leader)
                                     mbar_arrive_expect_tx(full0 + 8 * stage, v_tx + CG * slices * slice_bytes);
                                 if (mine > 0) tma_load_2d<CG>(sa, &map_v, c0, m0, fb);
-    #pragma unroll
+#pragma unroll
                                 for (int q = 0; q < 4; ++q)
                                     if (q < slices && (q < 2 || !args.slice_warp))
                                         slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0,
@@ -642,12 +642,12 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
             if (leader) {
                 const bool a_mn = MODE == kWgrad, b_mn = MODE == kWgrad || !args.b_kmajor;
                 // N of an MMA: the tile's columns in whole blocks of the epilogue (a
-            // pair's B lies half in either CTA: always all of it)
-            auto idesc_of = [&](const Tile &tile, uint32_t b_mn_major) {
-                const int64_t rest = (args.N - tile.n0 + 31) / 32 * 32;
-                const int n = CG == 1 && rest < args.bn ? static_cast<int>(rest) : args.bn;
-                return make_idesc(BM * CG, n, MODE == kWgrad, b_mn_major, args.ab_format);
-            };
+                // pair's B lies half in either CTA: always all of it)
+                auto idesc_of = [&](const Tile &tile, uint32_t b_mn_major) {
+                    const int64_t rest = (args.N - tile.n0 + 31) / 32 * 32;
+                    const int n = CG == 1 && rest < args.bn ? static_cast<int>(rest) : args.bn;
+                    return make_idesc(BM * CG, n, MODE == kWgrad, b_mn_major, args.ab_format);
+                };
                 const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring0, 0) : desc_kmajor(ring0, 0);
                 const uint64_t b_desc0 =
                     b_mn ? smem_desc(ring0 + a_region, static_cast<uint32_t>(ksub) * 8192u, 1024)
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                 // lora: slices of LB -- K-major: 32-byte rows (32-byte swizzle);
                 // N-major: 16 rows per 64-column block (128-byte swizzle)
                 const bool lb_mn = MODE == kLora && !args.l.b_kmajor;
-                    const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
+                const uint64_t lb_desc0 = lb_mn ? smem_desc(ring0 + a_region, 16 * 128, 1024)
                                                 : smem_desc(ring0 + a_region, 16, 256, kSwizzle32);
                 const uint64_t stage_step = stage_bytes >> 4;
                 int stage = 0;
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     if (!wait_all(empty0 + 8 * stage, phase ^ 1)) break;
                     const uint32_t sb = ring0 + stage * stage_bytes + a_region;
                     if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                         for (int q = 2; q < 4; ++q)
                             if (q < slices)
                                 slice_copies<CG>(args, &map_b_rows, sb + q * slice_bytes, b_rows, b0, j0s[q],
@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                     const int rows = cta_rows(t, rank);  // (groups of few rows: at most 64)
                     quads = (rows + 3) / 4;
                     __syncwarp();
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int r = lane + i * 32;
                         mine[r] = r < rows ? __ldg(args.row_index + m0 + r) : -1;
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(max_threads<CG, MODE, GATHER, PARTS>(), 1)
                         work = part;
                         if (work) {
                             __syncwarp();
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const int r = lane + j * 32;
                                 mine[r] = r < rem ? static_cast<int>(r0 + r) : -1;
