@@ -533,8 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[4] += y[k].x, u[5] += y[k].y, u[6] += y[k].z, u[7] += y[k].w;
         }
         const float scale = p.scale != nullptr ? p.scale[t.list[own]] : 1.f;
+        // (columns past the rank are zeros of LA, NaN beside an infinity of X)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] *= scale;
+        for (int k = 0; k < 8; ++k) u[k] = j + k < p.rank ? u[k] * scale : 0.f;
         // (in the first part's place, which this thread alone has read)
         *reinterpret_cast<float4 *>(part) = make_float4(u[0], u[1], u[2], u[3]);
         *reinterpret_cast<float4 *>(part + 4) = make_float4(u[4], u[5], u[6], u[7]);

@@ -48,10 +48,10 @@ def check(X, W, LA, LB, ids, dtype, out):
     assert bool((off <= tol[finite] * (1 + 2.0 ** -8) + unit * np.abs(want[finite]) + 2.0 ** -24).all())
 
 
-def case(seed, M, dtype, order, K=200, N=300):
+def case(seed, M, dtype, order, K=200, N=300, rank=16):
     rng = np.random.default_rng(seed)
     n = 6
-    X, W, LA, LB = operands(rng, M, K, N, 16, n, dtype, order)
+    X, W, LA, LB = operands(rng, M, K, N, rank, n, dtype, order)
     ids = torch.from_numpy((np.arange(M) % (n + 1) - 1).astype(np.int32)).cuda()
     return X, W, LA, LB, ids
 
@@ -81,6 +81,19 @@ def test_in_one_and_in_several_adapters(dtype, out, M, order):
     LA[3, 100, 7] = NAN
     X[5, 8], X[6, 9] = NAN, INF
     W[0, 5], W[0, 6] = INF, NAN
+    check(X, W, LA, LB, ids, dtype, out)
+
+
+@pytest.mark.parametrize("dtype,out", OUT)
+@pytest.mark.parametrize("M", [20, 300])
+@pytest.mark.parametrize("rank", [1, 4, 24, 40])
+@pytest.mark.parametrize("order", [(1, 1, 1), (0, 0, 0)])
+def test_ranks_between_powers_of_two(dtype, out, M, rank, order):
+    # (the kernels pad them with zeros, which infinities must not meet)
+    X, W, LA, LB, ids = case(M + rank, M, dtype, order, rank=rank)
+    X[5, 8], X[6, 9], X[7, 10], X[13, 199] = INF, -INF, INF, NAN
+    check(X, W, LA, LB, ids, dtype, out)
+    LB[2, 0, 5] = INF
     check(X, W, LA, LB, ids, dtype, out)
 
 
