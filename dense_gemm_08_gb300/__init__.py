@@ -474,8 +474,8 @@ def stack_order(t):
 def _row_major(t, what):
     """Leading dimension of a row-major matrix, or of each matrix of a stack: the columns of a
     row are adjacent (one row has no pitch, one column no distance)."""
-    r, q = t.shape[-2:]
-    s0, s1 = t.stride()[-2:]
+    *_, r, q = t.shape
+    *_, s0, s1 = t.stride()
     if (s1 == 1 or q <= 1) and (s0 >= q or r <= 1):
         return max(s0, q, 1)
     raise ValueError(f"{what} must be row-major")
@@ -523,16 +523,20 @@ def _stream_of(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
-def _empty(shape, dtype, device, stream):
-    """An output that `stream` (None: torch's current stream) writes: memory of that stream's
-    pool, as work of another stream may still use what the current one's pool hands out."""
+def _empty_for(stream):
+    """torch.empty for an output that `stream` (None: torch's current stream) writes: memory of
+    that stream's pool, as work of another stream may still use what the current one's pool
+    hands out."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+
+    def empty(*args, **kwargs):
+        with torch.cuda.stream(stream):
+            return torch.empty(*args, **kwargs)
+    return empty
 
 
 def _on_device(device):
@@ -582,9 +586,10 @@ def group_rows(ids, groups, stream=None):
     at = _int_vector(ids, n, "ids", device)
     _on_device(device)
     # (views of one allocation would cost the host more than three allocations)
-    offsets = _empty(groups + 1, torch.int32, device, stream)
-    order = _empty(n, torch.int32, device, stream)
-    position = _empty(n, torch.int32, device, stream)
+    empty = _empty_for(stream)
+    offsets = empty(groups + 1, dtype=torch.int32, device=device)
+    order = empty(n, dtype=torch.int32, device=device)
+    position = empty(n, dtype=torch.int32, device=device)
     st = library().gemm_group_rows(n, groups, at, offsets.data_ptr(), order.data_ptr(),
                                    position.data_ptr(), _stream_of(stream))
     if st != GEMM_OK:
@@ -619,7 +624,7 @@ def gemm_grouped(A, B, offsets, row_index=None, bias=None, activation=GEMM_ACT_N
         raise ValueError(f"out must be {rows} x {N}")
     _on_device(device)
     if out is None:
-        out = _empty((rows, N), out_dtype, device, stream)
+        out = _empty_for(stream)((rows, N), dtype=out_dtype, device=device)
         ldd = N
     else:
         ldd = _row_major(out, "out")
@@ -672,7 +677,7 @@ def gemm_grouped_wgrad(A, B, offsets, row_index=None, C=None, alpha=1.0, beta=0.
         c = C.data_ptr()
     _on_device(device)
     if out is None:
-        out = _empty((groups, M, N), out_dtype, device, stream)
+        out = _empty_for(stream)((groups, M, N), dtype=out_dtype, device=device)
         ldd, stride_d = max(N, 1), M * N
     fn = "gemm_grouped_wgrad_" + suffix
     st = getattr(library(), fn)(groups, rows, M, N, alpha, A.data_ptr(), lda, rows_a, index, at,
@@ -716,7 +721,7 @@ def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GE
         raise ValueError(f"out must be {M} x {N}")
     _on_device(device)
     if out is None:
-        out = _empty((M, N), out_dtype, device, stream)
+        out = _empty_for(stream)((M, N), dtype=out_dtype, device=device)
         ldd = N
     else:
         ldd = _row_major(out, "out")
