@@ -177,3 +177,13 @@ def test_a_tile_of_sums_computed_again_within_the_waits():
     assert bool(torch.isinf(D[5]).all())
     D[5] = K + 8.0 * K
     assert bool((D == K + 8.0 * K).all())
+
+
+@pytest.mark.parametrize("dtype,out", OUT)
+def test_tiles_of_two_ctas(dtype, out):
+    X, W, LA, LB, ids = case(3, 2600, dtype, (1, 1, 1), K=136, N=2600, rank=20)
+    X[5, 8], X[1300, 9], X[2599, 135] = INF, NAN, -INF
+    W[7, 2000] = INF
+    LB[2, 3, 5], LB[4, 0, 1000], LB[1, 19, 2599] = INF, NAN, -INF
+    check(X, W, LA, LB, ids, dtype, out)
+    assert lib.gemm_last_kernel().endswith("pair>")
