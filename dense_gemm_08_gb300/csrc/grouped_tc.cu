@@ -270,10 +270,10 @@ __device__ __forceinline__ uint32_t top_of_8(uint4 q) {
 // lora: a slot's LB meets zeros of V in the rows of other adapters; where it
 // holds infinities or NaNs those products are NaN, and the sum says nothing.
 // Such values of D are computed again by their definition in FP32, from the
-// row's own adapter alone -- but not the others whose sums are not finite, which
-// their own row of X or column of W made so: a request with a NaN costs its
-// batch nothing.  So are the rows whose first product passed the inputs' type
-// (65504 for FP16) and is infinite in V only.
+// row's own adapter alone, and so are the rows whose first product passed the
+// inputs' type (65504 for FP16) and is infinite in V only.  Other sums that are
+// not finite have it from their own row of X or column of W and stay: a request
+// with a NaN costs its batch nothing.
 //
 // A warp's 32 x 32 block of D from row0 and n0 on, already written; bit j of
 // `bad`: the sum of this lane's row and column n0 + j is not finite.  Left as
