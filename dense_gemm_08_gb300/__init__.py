@@ -14,6 +14,9 @@ Same names as the C ABI:
     gemm_grouped_f32, gemm_grouped_bf16_f32acc, gemm_grouped_f16_f32acc,
     gemm_grouped_wgrad_f32, gemm_grouped_wgrad_bf16_f32acc, gemm_grouped_wgrad_f16_f32acc,
     gemm_lora_bf16_f32acc, gemm_lora_f16_f32acc,
+    gemm_route, gemm_route_grad, gemm_combine, gemm_combine_grad,
+    gemm_fused_f32, gemm_fused_bf16_f32acc, gemm_fused_f16_f32acc,
+    gemm_fused_grad_f32, gemm_fused_grad_bf16_f32acc, gemm_fused_grad_f16_f32acc,
     gemm_probe_tc_bf16, gemm_probe_fma_f32, gemm_probe_wait_timeout
 Pointer arguments take an integer device address or a torch CUDA tensor;
 ``stream`` takes an integer ``cudaStream_t``, a ``torch.cuda.Stream`` or None
@@ -22,7 +25,10 @@ Pointer arguments take an integer device address or a torch CUDA tensor;
 ``gemm(...)`` is a convenience wrapper for torch tensors that reads each
 operand's storage order and leading dimension from its strides; so are
 ``group_rows(...)``, ``gemm_grouped(...)``, ``gemm_grouped_wgrad(...)`` and
-``gemm_lora(...)`` for the grouped operators.
+``gemm_lora(...)`` for the grouped operators, ``route(...)``,
+``route_grad(...)``, ``combine(...)`` and ``combine_grad(...)`` around them, and
+``gemm_fused(...)`` and ``gemm_fused_grad(...)`` for products with bias,
+activation and residual.
 """
 from __future__ import annotations
 
@@ -51,14 +57,20 @@ EXPORTED = ("gemm_f32", "gemm_bf16_f32acc", "gemm_f16_f32acc", "gemm_bf16_f32acc
             "gemm_grouped_f16_f32acc", "gemm_grouped_wgrad_f32",
             "gemm_grouped_wgrad_bf16_f32acc", "gemm_grouped_wgrad_f16_f32acc",
             "gemm_lora_bf16_f32acc", "gemm_lora_f16_f32acc",
+            "gemm_route", "gemm_route_grad", "gemm_combine", "gemm_combine_grad",
+            "gemm_fused_f32", "gemm_fused_bf16_f32acc", "gemm_fused_f16_f32acc",
+            "gemm_fused_grad_f32", "gemm_fused_grad_bf16_f32acc", "gemm_fused_grad_f16_f32acc",
             "gemm_probe_tc_bf16", "gemm_probe_fma_f32", "gemm_probe_wait_timeout")
 
 GEMM_ACT_NONE = 0
 GEMM_ACT_RELU = 1
 GEMM_ACT_GELU = 2
+GEMM_ACT_SILU = 3  # the fused products only
 GEMM_D_F32 = 0
 GEMM_D_BF16 = 1
-GEMM_D_F16 = 2  # the grouped operators with FP16 inputs only
+GEMM_D_F16 = 2  # not of the dense products
+GEMM_SCORE_SOFTMAX = 0
+GEMM_SCORE_SIGMOID = 1
 
 
 class MemoryInfo(ctypes.Structure):
@@ -70,6 +82,22 @@ class MemoryInfo(ctypes.Structure):
 class Epilogue(ctypes.Structure):
     """gemm_epilogue_t: bias (device pointer or None), activation, d_type."""
     _fields_ = [("bias", ctypes.c_void_p), ("activation", ctypes.c_int), ("d_type", ctypes.c_int)]
+
+
+
+class RouteRule(ctypes.Structure):
+    """gemm_route_rule_t: how a router scores and chooses experts."""
+    _fields_ = [("score", ctypes.c_int), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int32),
+                ("groups_kept", ctypes.c_int32), ("group_top", ctypes.c_int32)]
+
+
+class Fusion(ctypes.Structure):
+    """gemm_fusion_t: what follows a fused product."""
+    _fields_ = [("bias", ctypes.c_void_p), ("activation", ctypes.c_int),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("pre", ctypes.c_void_p), ("ld_pre", ctypes.c_int64)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -131,6 +159,25 @@ def library() -> ctypes.CDLL:
                 fn = getattr(lib, "gemm_lora_" + t)
                 fn.argtypes = [i64, i64, i64, vp, i64, vp, i64, ip, i64, i64, vp, vp, vp, i64,
                                i64, ip, vp, i64, i64, ip, vp, i64, ep, vp]
+                fn.restype = ip
+            rule = ctypes.POINTER(RouteRule)
+            lib.gemm_route.argtypes = [i64, i64, i64, vp, i64, ip, rule, vp, vp, vp]
+            lib.gemm_route.restype = ip
+            lib.gemm_route_grad.argtypes = [i64, i64, i64, vp, i64, ip, rule, vp, vp, vp, i64, vp]
+            lib.gemm_route_grad.restype = ip
+            lib.gemm_combine.argtypes = [i64, i64, i64, vp, i64, i64, ip, vp, vp, vp, i64, vp,
+                                         i64, ip, vp]
+            lib.gemm_combine.restype = ip
+            lib.gemm_combine_grad.argtypes = [i64, i64, i64, vp, i64, ip, vp, i64, i64, ip, vp, vp,
+                                              vp, i64, vp, vp]
+            lib.gemm_combine_grad.restype = ip
+            for t in ("f32", "bf16_f32acc", "f16_f32acc"):
+                head = [i64, i64, i64, f32, vp, i64, ip, vp, i64, ip]
+                fn = getattr(lib, "gemm_fused_" + t)
+                fn.argtypes = head + [vp, i64, ctypes.POINTER(Fusion), vp]
+                fn.restype = ip
+                fn = getattr(lib, "gemm_fused_grad_" + t)
+                fn.argtypes = head + [ip, vp, i64, vp, i64, vp, vp]
                 fn.restype = ip
             dp = ctypes.POINTER(ctypes.c_double)
             lib.gemm_probe_tc_bf16.argtypes = [ip, i64, dp, vp]
@@ -364,6 +411,122 @@ def gemm_lora_f16_f32acc(M, N, K, X, ldx, W, ldw, order_w, adapters, rank, adapt
     return _call_lora("gemm_lora_f16_f32acc", M, N, K, X, ldx, W, ldw, order_w, adapters, rank,
                       adapter_of_row, scale, LA, ld_a, stride_a, order_a, LB, ld_b, stride_b,
                       order_b, D, ldd, bias, activation, d_type, stream, check)
+
+def gemm_route(tokens, experts, k, logits, ld, type, chosen, weights, score=GEMM_SCORE_SOFTMAX,
+               renormalize=1, scale=1.0, bias=None, groups=1, groups_kept=1, group_top=1,
+               stream=None, check=True) -> int:
+    """Each token's experts and their weights (see include/gemm.h)."""
+    rule = RouteRule(int(score), int(renormalize), float(scale), _addr(bias), int(groups),
+                     int(groups_kept), int(group_top))
+    st = library().gemm_route(int(tokens), int(experts), int(k), _addr(logits), int(ld), int(type),
+                              rule, _addr(chosen), _addr(weights), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_route")
+    return st
+
+
+def gemm_route_grad(tokens, experts, k, logits, ld, type, chosen, dweights, dlogits, ld_d,
+                    score=GEMM_SCORE_SOFTMAX, renormalize=1, scale=1.0, stream=None,
+                    check=True) -> int:
+    """The gradient of gemm_route's weights (see include/gemm.h)."""
+    rule = RouteRule(int(score), int(renormalize), float(scale), None, 1, 1, 1)
+    st = library().gemm_route_grad(int(tokens), int(experts), int(k), _addr(logits), int(ld),
+                                   int(type), rule, _addr(chosen), _addr(dweights),
+                                   _addr(dlogits), int(ld_d), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_route_grad")
+    return st
+
+
+def gemm_combine(tokens, k, N, Y, ldy, rows_y, y_type, position, weights, residual, ld_r, D, ldd,
+                 d_type, stream=None, check=True) -> int:
+    """D(t, :) = residual(t, :) + sum_j weights(t, j) Y(position(t, j), :)."""
+    st = library().gemm_combine(int(tokens), int(k), int(N), _addr(Y), int(ldy), int(rows_y),
+                                int(y_type), _addr(position), _addr(weights), _addr(residual),
+                                int(ld_r), _addr(D), int(ldd), int(d_type), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_combine")
+    return st
+
+
+def gemm_combine_grad(tokens, k, N, dD, ld_d, d_type, Y, ldy, rows_y, y_type, position, weights,
+                      dY, ld_dy, dweights, stream=None, check=True) -> int:
+    """gemm_combine's gradients with respect to Y and the weights."""
+    st = library().gemm_combine_grad(int(tokens), int(k), int(N), _addr(dD), int(ld_d),
+                                     int(d_type), _addr(Y), int(ldy), int(rows_y), int(y_type),
+                                     _addr(position), _addr(weights), _addr(dY), int(ld_dy),
+                                     _addr(dweights), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, "gemm_combine_grad")
+    return st
+
+
+def _call_fused(fn_name, M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D, ldd, bias,
+                activation, residual, ld_residual, pre, ld_pre, stream, check):
+    f = Fusion(_addr(bias), int(activation), _addr(residual), int(ld_residual), _addr(pre),
+               int(ld_pre))
+    st = getattr(library(), fn_name)(int(M), int(N), int(K), float(alpha), _addr(A), int(lda),
+                                     int(order_a), _addr(B), int(ldb), int(order_b), _addr(D),
+                                     int(ldd), f, _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, fn_name)
+    return st
+
+
+def _call_fused_grad(fn_name, M, N, K, alpha, A, lda, order_a, B, ldb, order_b, activation, pre,
+                     ld_pre, D, ldd, dbias, stream, check):
+    st = getattr(library(), fn_name)(int(M), int(N), int(K), float(alpha), _addr(A), int(lda),
+                                     int(order_a), _addr(B), int(ldb), int(order_b),
+                                     int(activation), _addr(pre), int(ld_pre), _addr(D), int(ldd),
+                                     _addr(dbias), _stream(stream))
+    if check and st != GEMM_OK:
+        raise GemmError(st, fn_name)
+    return st
+
+
+def gemm_fused_f32(M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D, ldd, bias=None,
+                   activation=GEMM_ACT_NONE, residual=None, ld_residual=0,
+                   pre=None, ld_pre=0, stream=None, check=True) -> int:
+    """D = act(Z) + residual, Z = alpha * op(A) op(B) + bias, Z kept in pre; FP32 on the CUDA cores."""
+    return _call_fused("gemm_fused_f32", M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D,
+                       ldd, bias, activation, residual, ld_residual, pre, ld_pre, stream, check)
+
+
+def gemm_fused_grad_f32(M, N, K, alpha, A, lda, order_a, B, ldb, order_b, activation, pre,
+                        ld_pre, D, ldd, dbias=None, stream=None, check=True) -> int:
+    """D = alpha * op(A) op(B) * act'(pre), dbias = its column sums; FP32 on the CUDA cores."""
+    return _call_fused_grad("gemm_fused_grad_f32", M, N, K, alpha, A, lda, order_a, B, ldb,
+                            order_b, activation, pre, ld_pre, D, ldd, dbias, stream, check)
+
+
+def gemm_fused_bf16_f32acc(M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D, ldd, bias=None,
+                           activation=GEMM_ACT_NONE, residual=None, ld_residual=0,
+                           pre=None, ld_pre=0, stream=None, check=True) -> int:
+    """D = act(Z) + residual, Z = alpha * op(A) op(B) + bias, Z kept in pre; BF16."""
+    return _call_fused("gemm_fused_bf16_f32acc", M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D,
+                       ldd, bias, activation, residual, ld_residual, pre, ld_pre, stream, check)
+
+
+def gemm_fused_grad_bf16_f32acc(M, N, K, alpha, A, lda, order_a, B, ldb, order_b, activation, pre,
+                                ld_pre, D, ldd, dbias=None, stream=None, check=True) -> int:
+    """D = alpha * op(A) op(B) * act'(pre), dbias = its column sums; BF16."""
+    return _call_fused_grad("gemm_fused_grad_bf16_f32acc", M, N, K, alpha, A, lda, order_a, B, ldb,
+                            order_b, activation, pre, ld_pre, D, ldd, dbias, stream, check)
+
+
+def gemm_fused_f16_f32acc(M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D, ldd, bias=None,
+                          activation=GEMM_ACT_NONE, residual=None, ld_residual=0,
+                          pre=None, ld_pre=0, stream=None, check=True) -> int:
+    """D = act(Z) + residual, Z = alpha * op(A) op(B) + bias, Z kept in pre; FP16."""
+    return _call_fused("gemm_fused_f16_f32acc", M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D,
+                       ldd, bias, activation, residual, ld_residual, pre, ld_pre, stream, check)
+
+
+def gemm_fused_grad_f16_f32acc(M, N, K, alpha, A, lda, order_a, B, ldb, order_b, activation, pre,
+                               ld_pre, D, ldd, dbias=None, stream=None, check=True) -> int:
+    """D = alpha * op(A) op(B) * act'(pre), dbias = its column sums; FP16."""
+    return _call_fused_grad("gemm_fused_grad_f16_f32acc", M, N, K, alpha, A, lda, order_a, B, ldb,
+                            order_b, activation, pre, ld_pre, D, ldd, dbias, stream, check)
 
 
 def gemm_probe_tc_bf16(cta_group, n_mma, stream=None, check=True):
@@ -733,3 +896,287 @@ def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GE
     if st != GEMM_OK:
         raise GemmError(st, fn)
     return out
+
+
+# ------------------------------------ torch helpers, router and fused products
+def _types_of_values():
+    torch = _torch()
+    return {torch.float32: GEMM_D_F32, torch.bfloat16: GEMM_D_BF16, torch.float16: GEMM_D_F16}
+
+
+_value_types = None
+
+
+def _value_type(t, what):
+    """gemm_d_type_t of a tensor."""
+    global _value_types
+    if _value_types is None:
+        _value_types = _types_of_values()
+    kind = _value_types.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{what} must be float32, bfloat16 or float16")
+    return kind
+
+
+def _matrix(t, shape, what, device):
+    """Leading dimension of a row-major matrix of this shape on the device."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+    return _row_major(t, what)
+
+
+def _pairs(t, shape, dtype, what, device):
+    """Address of a contiguous tokens x k tensor."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {str(dtype)[6:]}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with shape {shape}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+    return t.data_ptr()
+
+
+def route(logits, k, score=GEMM_SCORE_SOFTMAX, bias=None, groups=1, groups_kept=1, group_top=1,
+          renormalize=True, scale=1.0, stream=None):
+    """(experts, weights) of each token, both (tokens x k), int32 and float32 (gemm_route).
+
+    logits is (tokens x experts), row-major; bias float32 per expert counts in the
+    choice only.  ``experts.view(-1)`` is what ``group_rows`` takes; a place
+    without an expert (all others masked by -inf) has -1 and weight 0.
+    """
+    torch = _torch()
+    kind = _value_type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a matrix")
+    tokens, experts = logits.shape
+    device = logits.device
+    ld = _row_major(logits, "logits")
+    rule = RouteRule(score, 1 if renormalize else 0, scale,
+                     _f32_dense(bias, (experts,), "bias", device), groups, groups_kept, group_top)
+    _on_device(device)
+    empty = _empty_for(stream)
+    # (a k that is refused below allocates nothing)
+    shape = (tokens, k if 0 < k <= experts else 0)
+    chosen = empty(shape, dtype=torch.int32, device=device)
+    weights = empty(shape, dtype=torch.float32, device=device)
+    st = library().gemm_route(tokens, experts, k, logits.data_ptr(), ld, kind, rule,
+                              chosen.data_ptr(), weights.data_ptr(), _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_route")
+    return chosen, weights
+
+
+def route_grad(logits, chosen, dweights, score=GEMM_SCORE_SOFTMAX, renormalize=True, scale=1.0,
+               out=None, stream=None):
+    """The gradient of ``route``'s weights with respect to the logits, in their dtype.
+
+    chosen is what ``route`` returned, dweights (float32) the weights' gradient;
+    score, renormalize and scale as for ``route``.  out may be logits.
+    """
+    torch = _torch()
+    kind = _value_type(logits, "logits")
+    if logits.dim() != 2 or chosen.dim() != 2:
+        raise ValueError("logits and chosen must be matrices")
+    tokens, experts = logits.shape
+    device = logits.device
+    k = chosen.shape[1]
+    ld = _row_major(logits, "logits")
+    ids = _pairs(chosen, (tokens, k), torch.int32, "chosen", device)
+    dw = _pairs(dweights, (tokens, k), torch.float32, "dweights", device)
+    if out is not None:
+        if out.dtype is not logits.dtype:
+            raise TypeError("out must have the logits' dtype")
+        ld_d = _matrix(out, (tokens, experts), "out", device)
+    rule = RouteRule(score, 1 if renormalize else 0, scale, None, 1, 1, 1)
+    _on_device(device)
+    if out is None:
+        out = _empty_for(stream)((tokens, experts), dtype=logits.dtype, device=device)
+        ld_d = experts
+    st = library().gemm_route_grad(tokens, experts, k, logits.data_ptr(), ld, kind, rule, ids, dw,
+                                   out.data_ptr(), ld_d, _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_route_grad")
+    return out
+
+
+def combine(Y, position, weights=None, residual=None, out_dtype=None, out=None, stream=None):
+    """D[t] = residual[t] + sum_j weights[t, j] * Y[position[t, j]] (gemm_combine).
+
+    Y is (rows x N), position int32 (tokens x k) (``group_rows``'s position,
+    viewed as tokens x k; a number outside Y adds nothing), weights float32 (tokens x k)
+    or None for 1.  D is float32 or Y's dtype (the default), residual of D's dtype.
+    Without weights this is the gradient of a gather of rows.
+    """
+    torch = _torch()
+    y_type = _value_type(Y, "Y")
+    if Y.dim() != 2 or position.dim() != 2:
+        raise ValueError("Y and position must be matrices")
+    rows, N = Y.shape
+    tokens, k = position.shape
+    device = Y.device
+    ldy = _row_major(Y, "Y")
+    at = _pairs(position, (tokens, k), torch.int32, "position", device)
+    w = None
+    if weights is not None:
+        w = _pairs(weights, (tokens, k), torch.float32, "weights", device)
+    if out is not None:
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError("out must have out_dtype")
+        out_dtype = out.dtype
+        ldd = _matrix(out, (tokens, N), "out", device)
+    elif out_dtype is None:
+        out_dtype = Y.dtype
+    if out_dtype is Y.dtype:
+        d_type = y_type
+    elif out_dtype is torch.float32:
+        d_type = GEMM_D_F32
+    else:
+        raise TypeError("the output must be float32 or Y's dtype")
+    r, ld_r = None, 0
+    if residual is not None:
+        if residual.dtype is not out_dtype:
+            raise TypeError("residual must have the output's dtype")
+        ld_r = _matrix(residual, (tokens, N), "residual", device)
+        r = residual.data_ptr()
+    _on_device(device)
+    if out is None:
+        out = _empty_for(stream)((tokens, N), dtype=out_dtype, device=device)
+        ldd = N
+    st = library().gemm_combine(tokens, k, N, Y.data_ptr(), ldy, rows, y_type, at, w, r, ld_r,
+                                out.data_ptr(), ldd, d_type, _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_combine")
+    return out
+
+
+def combine_grad(dD, Y, position, weights=None, weight_grad=True, out=None, stream=None):
+    """(dY, dweights) of ``combine``: dY[position[t, j]] = weights[t, j] * dD[t] in Y's dtype,
+    dweights[t, j] = dot(dD[t], Y[position[t, j]]) in float32 (None without weight_grad).
+
+    dD is float32 or has Y's dtype.  Rows of dY (``out``, or a new tensor) that no
+    position names are left as they are; the positions inside Y must differ.
+    """
+    torch = _torch()
+    y_type, d_type = _value_type(Y, "Y"), _value_type(dD, "dD")
+    if Y.dim() != 2 or position.dim() != 2:
+        raise ValueError("Y and position must be matrices")
+    rows, N = Y.shape
+    tokens, k = position.shape
+    device = Y.device
+    if d_type != y_type and d_type != GEMM_D_F32:
+        raise TypeError("dD must be float32 or have Y's dtype")
+    ld_d = _matrix(dD, (tokens, N), "dD", device)
+    ldy = _row_major(Y, "Y")
+    at = _pairs(position, (tokens, k), torch.int32, "position", device)
+    w = None
+    if weights is not None:
+        w = _pairs(weights, (tokens, k), torch.float32, "weights", device)
+    if out is not None:
+        if out.dtype is not Y.dtype:
+            raise TypeError("out must have Y's dtype")
+        ld_dy = _matrix(out, (rows, N), "out", device)
+    _on_device(device)
+    empty = _empty_for(stream)
+    if out is None:
+        out = empty((rows, N), dtype=Y.dtype, device=device)
+        ld_dy = N
+    dweights = empty((tokens, k), dtype=torch.float32, device=device) if weight_grad else None
+    if k > 0:
+        st = library().gemm_combine_grad(
+            tokens, k, N, dD.data_ptr(), ld_d, d_type, Y.data_ptr(), ldy, rows, y_type, at, w,
+            out.data_ptr(), ld_dy, dweights.data_ptr() if weight_grad else None, _stream_of(stream))
+        if st != GEMM_OK:
+            raise GemmError(st, "gemm_combine_grad")
+    return out, dweights
+
+
+_FUSED_SUFFIX = ("f32", "bf16_f32acc", "f16_f32acc")  # by gemm_d_type_t
+
+
+def _fused_operands(A, B, out):
+    """(suffix, M, N, K, lda, order_a, ldb, order_b, device) of a fused product."""
+    kind = _value_type(A, "A")
+    if B.dtype is not A.dtype:
+        raise TypeError("the operands must share a dtype")
+    order_a, lda = storage_order(A)
+    order_b, ldb = storage_order(B)
+    (M, K), (kb, N) = A.shape, B.shape
+    if kb != K:
+        raise ValueError("inner dimensions differ")
+    device = A.device
+    if B.device != device:
+        raise ValueError("the operands must share a device")
+    if out is not None and out.dtype is not A.dtype:
+        raise TypeError("out must have the operands' dtype")
+    return _FUSED_SUFFIX[kind], M, N, K, lda, order_a, ldb, order_b, device
+
+
+def gemm_fused(A, B, bias=None, activation=GEMM_ACT_NONE, residual=None, keep_pre=False, alpha=1.0,
+               out=None, stream=None):
+    """D = act(Z) + residual with Z = alpha * A @ B + bias, all in the operands' dtype
+    (gemm_fused_*); with keep_pre (D, Z), what ``gemm_fused_grad`` needs.
+
+    A (M x K) and B (K x N) are row- or column-major, float32, bfloat16 or float16;
+    bias float32 (N), residual (M x N) row-major (may be out).
+    """
+    suffix, M, N, K, lda, order_a, ldb, order_b, device = _fused_operands(A, B, out)
+    b = _f32_dense(bias, (N,), "bias", device)
+    r, ld_r = None, 0
+    if residual is not None:
+        if residual.dtype is not A.dtype:
+            raise TypeError("residual must have the operands' dtype")
+        ld_r = _matrix(residual, (M, N), "residual", device)
+        r = residual.data_ptr()
+    if out is not None:
+        ldd = _matrix(out, (M, N), "out", device)
+    _on_device(device)
+    empty = _empty_for(stream)
+    if out is None:
+        out = empty((M, N), dtype=A.dtype, device=device)
+        ldd = max(N, 1)
+    pre, z = None, None
+    if keep_pre:
+        pre = empty((M, N), dtype=A.dtype, device=device)
+        z = pre.data_ptr()
+    fn = "gemm_fused_" + suffix
+    st = getattr(library(), fn)(M, N, K, alpha, A.data_ptr(), lda, order_a, B.data_ptr(), ldb,
+                                order_b, out.data_ptr(), ldd,
+                                Fusion(b, activation, r, ld_r, z, max(N, 1)), _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, fn)
+    return (out, pre) if keep_pre else out
+
+
+def gemm_fused_grad(A, B, pre, activation=GEMM_ACT_NONE, bias_grad=False, alpha=1.0, out=None,
+                    stream=None):
+    """D = (alpha * A @ B) * act'(pre) in the operands' dtype (gemm_fused_grad_*); with
+    bias_grad (D, D's column sums in float32).
+
+    pre (M x N, row-major, may be out) is what ``gemm_fused`` kept; None without activation.
+    """
+    suffix, M, N, K, lda, order_a, ldb, order_b, device = _fused_operands(A, B, out)
+    z, ld_z = None, 0
+    if pre is not None:
+        if pre.dtype is not A.dtype:
+            raise TypeError("pre must have the operands' dtype")
+        ld_z = _matrix(pre, (M, N), "pre", device)
+        z = pre.data_ptr()
+    elif activation != GEMM_ACT_NONE:
+        raise ValueError("an activation's gradient needs pre")
+    if out is not None:
+        ldd = _matrix(out, (M, N), "out", device)
+    _on_device(device)
+    empty = _empty_for(stream)
+    if out is None:
+        out = empty((M, N), dtype=A.dtype, device=device)
+        ldd = max(N, 1)
+    dbias = empty(N, dtype=_torch().float32, device=device) if bias_grad else None
+    fn = "gemm_fused_grad_" + suffix
+    st = getattr(library(), fn)(M, N, K, alpha, A.data_ptr(), lda, order_a, B.data_ptr(), ldb,
+                                order_b, activation, z, ld_z, out.data_ptr(), ldd,
+                                dbias.data_ptr() if bias_grad else None, _stream_of(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, fn)
+    return (out, dbias) if bias_grad else out

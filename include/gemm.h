@@ -234,11 +234,16 @@ gemm_status_t gemm_f32_noalloc(int64_t M, int64_t N, int64_t K, float alpha,
  * 1e-6 |x|, plus 2^-8 |D| for BF16 rounding (half an ulp at 8 significant
  * bits).
  */
-typedef enum { GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_GELU = 2 } gemm_activation_t;
+typedef enum {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,
+    GEMM_ACT_GELU = 2,
+    GEMM_ACT_SILU = 3 /* gemm_fused_* only */
+} gemm_activation_t;
 typedef enum {
     GEMM_D_F32 = 0,
     GEMM_D_BF16 = 1,
-    GEMM_D_F16 = 2 /* the grouped operators with FP16 inputs only */
+    GEMM_D_F16 = 2 /* not of the dense products above */
 } gemm_d_type_t;
 typedef struct {
     const float *bias;
@@ -429,6 +434,208 @@ gemm_status_t gemm_lora_f16_f32acc(int64_t M, int64_t N, int64_t K, const gemm_f
                                    gemm_order_t order_a, const gemm_f16_t *LB, int64_t ld_b,
                                    int64_t stride_b, gemm_order_t order_b, void *D, int64_t ldd,
                                    const gemm_epilogue_t *epilogue, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A mixture's router and the way back from its experts, and dense products
+ * with the element-wise work around them, each with its gradient.  The GEMM
+ * pages have no counterpart to them.
+ *
+ * Common contract.  Ownership, graph capture, threads, asynchrony and errors
+ * are those of gemm_f32 above.  All results are deterministic: no sum's order
+ * depends on timing.  A `type` says what a matrix holds (gemm_d_type_t):
+ * GEMM_D_F32, GEMM_D_BF16 or GEMM_D_F16.  Matrices are row-major unless an
+ * order is given; leading dimensions are in elements; any alignment to the
+ * element size is accepted (16-byte aligned rows are faster).  Arithmetic is
+ * FP32; a result of 16 bits is rounded once, to nearest even.
+ */
+
+/*
+ * gemm_route -- the experts of each token and their weights:
+ *
+ *     s(t, e) = softmax over e or logistic function of logits(t, e)
+ *     c(t, e) = s(t, e) + bias[e]
+ *     chosen(t, 0 .. k-1) = the experts of the k largest c, by falling c
+ *     weights(t, j) = scale * s(t, chosen(t, j)) / S,
+ *     S = renormalize ? sum of s over the token's chosen experts : 1
+ *
+ * The bias (for balance) counts in the choice only.  With groups > 1 the
+ * experts form `groups` runs of experts / groups; a group's score is the sum
+ * of its group_top (1 or 2) largest c, and the choice is among the
+ * groups_kept groups of the largest scores.
+ * Order: values are compared as computed in 64 bits (without a bias c has the
+ *   order of the logits, and they are compared), equal ones by the lower
+ *   index.  A NaN counts as larger than everything.
+ * Masks: an expert whose logit or bias is -infinity is never chosen and adds
+ *   nothing to its group's score.  Where fewer than k experts can be chosen,
+ *   the places left have chosen = -1 and weights = 0 (gemm_group_rows drops
+ *   them, gemm_combine skips them).  Finite logits, however low, are no mask.
+ * NaNs and +infinities of the logits reach the token's weights as the
+ *   formulas say; chosen holds valid numbers in any case.
+ *
+ *   tokens, experts, k   experts 1 .. 1024, k 1 .. min(experts, 32); more
+ *                        than that is refused
+ *   logits, ld, type     tokens x experts
+ *   rule                 NULL: softmax, no bias, no groups, renormalised, scale 1
+ *   chosen               tokens x k int32, contiguous (device)
+ *   weights              tokens x k FP32, contiguous (device)
+ * With the numbers in row order, chosen is what gemm_group_rows takes (rows =
+ * tokens * k, row t * k + j belonging to token t).
+ * groups: 1 .. 32, a divisor of experts; groups_kept 1 .. groups.
+ */
+typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score_t;
+typedef struct {
+    gemm_score_t score;
+    int32_t renormalize; /* 0 or 1 */
+    float scale;
+    const float *bias;   /* experts FP32 values (device) or NULL */
+    int32_t groups;      /* 1: no groups (the next two are then not read) */
+    int32_t groups_kept;
+    int32_t group_top;   /* 1 or 2 */
+} gemm_route_rule_t;
+gemm_status_t gemm_route(int64_t tokens, int64_t experts, int64_t k, const void *logits,
+                         int64_t ld, gemm_d_type_t type, const gemm_route_rule_t *rule,
+                         int32_t *chosen, float *weights, cudaStream_t stream);
+
+/*
+ * gemm_route_grad -- the gradient of gemm_route's weights with respect to the
+ * logits, for a fixed choice:
+ *
+ *     dlogits(t, e) = sum_j dweights(t, j) * d weights(t, j) / d logits(t, e)
+ *
+ * rule as in the forward call; its bias and groups are not read.  chosen is
+ * the forward call's: a number outside [0, experts) has no weight, and its
+ * dweights is not read as one; a number twice counts twice.  dlogits has the
+ * logits' type (pitch ld_d) and may be logits itself.  Every element of it is
+ * written (0 where the weights do not depend on the logit).  With sigmoid
+ * scores or renormalised weights only the chosen experts' logits are read.
+ */
+gemm_status_t gemm_route_grad(int64_t tokens, int64_t experts, int64_t k, const void *logits,
+                              int64_t ld, gemm_d_type_t type, const gemm_route_rule_t *rule,
+                              const int32_t *chosen, const float *dweights, void *dlogits,
+                              int64_t ld_d, cudaStream_t stream);
+
+/*
+ * gemm_combine -- the experts' rows back to the tokens:
+ *
+ *     D(t, :) = residual(t, :) + sum_{j < k} weights(t, j) * Y(position(t, j), :)
+ *
+ *   Y, ldy, rows_y, y_type   rows_y x N
+ *   position    tokens x k int32, contiguous (gemm_group_rows's position);
+ *               a number outside [0, rows_y) adds nothing, whatever its weight
+ *   weights     tokens x k FP32, contiguous, or NULL (all 1: the gradient of a
+ *               gather of rows, such as the experts' inputs)
+ *   residual, ld_r           tokens x N of D's type, or NULL
+ *   D, ldd, d_type           tokens x N; GEMM_D_F32 or Y's type.  D may be the
+ *               residual (ldd = ld_r), and must not overlap Y.
+ * The sum is FP32, in the order of j, the residual last.  tokens, k, N, rows_y
+ * >= 0 and at most 2^31 - 1, tokens * k at most 2^40; k = 0 gives the residual
+ * or zeros.
+ */
+gemm_status_t gemm_combine(int64_t tokens, int64_t k, int64_t N, const void *Y, int64_t ldy,
+                           int64_t rows_y, gemm_d_type_t y_type, const int32_t *position,
+                           const float *weights, const void *residual, int64_t ld_r, void *D,
+                           int64_t ldd, gemm_d_type_t d_type, cudaStream_t stream);
+
+/*
+ * gemm_combine_grad -- its gradients (the residual's is dD itself):
+ *
+ *     dY(position(t, j), :) = weights(t, j) * dD(t, :)
+ *     dweights(t, j) = <dD(t, :), Y(position(t, j), :)>
+ *
+ * dD is tokens x N of d_type (GEMM_D_F32 or y_type), dY rows_y x N of y_type.
+ * The positions inside [0, rows_y) must differ from one another, as
+ * gemm_group_rows's do (of a row named twice, dY holds one of the two);
+ * entries outside have dweights = 0.  Rows of dY that no position names are
+ * left as they are.  weights NULL: all 1.  dY or dweights may be NULL (not
+ * computed); Y is read for dweights only, and NULL without it.  dY must not
+ * overlap Y or dD.  k is at least 1.
+ */
+gemm_status_t gemm_combine_grad(int64_t tokens, int64_t k, int64_t N, const void *dD, int64_t ld_d,
+                                gemm_d_type_t d_type, const void *Y, int64_t ldy, int64_t rows_y,
+                                gemm_d_type_t y_type, const int32_t *position,
+                                const float *weights, void *dY, int64_t ld_dy, float *dweights,
+                                cudaStream_t stream);
+
+/*
+ * gemm_fused_* -- a product with the element-wise work that follows it:
+ *
+ *     Z = alpha * op(A) * op(B) + bias
+ *     D = act(Z) + residual
+ *
+ * D, residual and pre are M x N row-major matrices of the inputs' type.
+ *   fusion->bias        N FP32 values, one per column (device), or NULL
+ *   fusion->activation  GEMM_ACT_NONE, _RELU, _GELU (tanh form) or _SILU
+ *                       (x / (1 + exp(-x))); NaNs pass through
+ *   fusion->residual, ld_residual   added after the activation, or NULL; may
+ *                       be D (the same pitch)
+ *   fusion->pre, ld_pre where Z is kept for the backward pass, or NULL; must
+ *                       not overlap D, A, B or the residual
+ * fusion == NULL: none of them (D = alpha op(A) op(B) in the inputs' type).
+ * D is computed from Z before Z is rounded.  M, N, K as for gemm_f32; K == 0
+ * or alpha == 0: A and B are not read, Z = bias.
+ * Kernels: tensor cores (tcgen05) for 16-bit inputs that TMA can describe
+ *   (16-byte aligned A and B, leading dimensions multiples of 8 elements),
+ *   CUDA cores otherwise and for FP32 (no TF32).  D, pre, residual: any
+ *   alignment.
+ * Accuracy: |Z - Z_ref| <= rel * sum_k |alpha A B| + 1e-6 |Z|, rel = 1e-5
+ *   (FP32) or 4e-3 (16-bit inputs); D as act's largest slope (1.13 for GELU,
+ *   1.1 for SILU) times that plus 1e-6 |Z|; each plus its rounding.
+ */
+typedef struct {
+    const float *bias;
+    gemm_activation_t activation;
+    const void *residual;
+    int64_t ld_residual;
+    void *pre;
+    int64_t ld_pre;
+} gemm_fusion_t;
+gemm_status_t gemm_fused_f32(int64_t M, int64_t N, int64_t K, float alpha, const float *A,
+                             int64_t lda, gemm_order_t order_a, const float *B, int64_t ldb,
+                             gemm_order_t order_b, float *D, int64_t ldd,
+                             const gemm_fusion_t *fusion, cudaStream_t stream);
+gemm_status_t gemm_fused_bf16_f32acc(int64_t M, int64_t N, int64_t K, float alpha,
+                                     const gemm_bf16_t *A, int64_t lda, gemm_order_t order_a,
+                                     const gemm_bf16_t *B, int64_t ldb, gemm_order_t order_b,
+                                     gemm_bf16_t *D, int64_t ldd, const gemm_fusion_t *fusion,
+                                     cudaStream_t stream);
+gemm_status_t gemm_fused_f16_f32acc(int64_t M, int64_t N, int64_t K, float alpha,
+                                    const gemm_f16_t *A, int64_t lda, gemm_order_t order_a,
+                                    const gemm_f16_t *B, int64_t ldb, gemm_order_t order_b,
+                                    gemm_f16_t *D, int64_t ldd, const gemm_fusion_t *fusion,
+                                    cudaStream_t stream);
+
+/*
+ * gemm_fused_grad_* -- the backward product through an activation:
+ *
+ *     D = (alpha * op(A) * op(B)) * act'(pre)      (element by element)
+ *     dbias[n] = sum over the rows m of D(m, n)    (FP32, before D is rounded)
+ *
+ * With Y = act(X W + b) V and the pre = X W + b that gemm_fused kept, A = dY and
+ * B = V^T (the other order of V) give D = the gradient of X W + b and dbias
+ * that of b; gemm_fused with A = D, B = W^T and a residual is then the input
+ * gradient of a residual block, and the weight gradients are plain products.
+ * pre is M x N of the inputs' type and may be D (the same pitch); it is not
+ * read when the activation is GEMM_ACT_NONE (NULL allowed).  act' of ReLU is 0
+ * at 0; a NaN in pre gives NaN.  dbias may be NULL.
+ * M == 0 with N > 0: dbias = 0.
+ */
+gemm_status_t gemm_fused_grad_f32(int64_t M, int64_t N, int64_t K, float alpha, const float *A,
+                                  int64_t lda, gemm_order_t order_a, const float *B, int64_t ldb,
+                                  gemm_order_t order_b, gemm_activation_t activation,
+                                  const float *pre, int64_t ld_pre, float *D, int64_t ldd,
+                                  float *dbias, cudaStream_t stream);
+gemm_status_t gemm_fused_grad_bf16_f32acc(int64_t M, int64_t N, int64_t K, float alpha,
+                                          const gemm_bf16_t *A, int64_t lda, gemm_order_t order_a,
+                                          const gemm_bf16_t *B, int64_t ldb, gemm_order_t order_b,
+                                          gemm_activation_t activation, const gemm_bf16_t *pre,
+                                          int64_t ld_pre, gemm_bf16_t *D, int64_t ldd,
+                                          float *dbias, cudaStream_t stream);
+gemm_status_t gemm_fused_grad_f16_f32acc(int64_t M, int64_t N, int64_t K, float alpha,
+                                         const gemm_f16_t *A, int64_t lda, gemm_order_t order_a,
+                                         const gemm_f16_t *B, int64_t ldb, gemm_order_t order_b,
+                                         gemm_activation_t activation, const gemm_f16_t *pre,
+                                         int64_t ld_pre, gemm_f16_t *D, int64_t ldd,
+                                         float *dbias, cudaStream_t stream);
 
 /* Static English description of a status code; never NULL. */
 const char *gemm_status_string(gemm_status_t status);
