@@ -38,8 +38,17 @@ struct FusedProblem {
 };
 
 // CUDA-core kernels: any type, order and alignment (fused_simt.cu).
+// Few rows of A, and operands whose K is contiguous in 16-byte pieces: launch_fused_simt
+// then streams B once, and is the faster one for 16-bit inputs too.
+bool fused_rows_eligible(const FusedProblem &p, InType in);
 cudaError_t launch_fused_simt(const FusedProblem &p, InType in, cudaStream_t stream,
                               const char **name);
+// Tensor-core kernels (fused_tc.cu): BF16 or FP16 operands that TMA can describe.
+bool fused_tc_eligible(const FusedProblem &p);
+cudaError_t launch_fused_tc(const FusedProblem &p, InType in, cudaStream_t stream,
+                            const char **name);
+// Reads and clears those kernels' device status word (after a sync).
+cudaError_t fused_tc_read_and_clear_status(cudaStream_t stream, int *status);
 // dbias[n] = the sum of `blocks` rows of `part` (pitch N), in a fixed order.
 cudaError_t launch_column_sums(const float *part, int64_t blocks, int64_t N, float *dbias,
                                cudaStream_t stream);

@@ -67,7 +67,11 @@ gemm_status_t product(InType in, int64_t M, int64_t N, int64_t K, float alpha, c
 
 gemm_status_t run(const gemm::FusedProblem &p, InType in, cudaStream_t stream) {
     const char *name = "";
-    return gemm::finish_call(gemm::launch_fused_simt(p, in, stream, &name), name);
+    // up to four rows: the CUDA cores stream B (fused_rows) where its columns are contiguous
+    const bool tc = in != InType::F32 && gemm::fused_tc_eligible(p) && !gemm::fused_rows_eligible(p, in);
+    return gemm::finish_call(tc ? gemm::launch_fused_tc(p, in, stream, &name)
+                                : gemm::launch_fused_simt(p, in, stream, &name),
+                             name);
 }
 
 gemm_status_t fused(InType in, int64_t M, int64_t N, int64_t K, float alpha, const void *A,

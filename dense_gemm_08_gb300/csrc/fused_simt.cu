@@ -375,31 +375,32 @@ cudaError_t tiles_as(const FusedProblem &p, int ks, cudaStream_t stream) {
     return e;
 }
 
+// The rows kernel's operands: K contiguous and on 16 bytes, M at most 4.
+bool rows_fit(const FusedProblem &p, int64_t bytes) {
+    if (p.M > 4 || p.K == 0 || !p.b_kmajor || !rows_on_16(p.B, p.ldb, bytes)) return false;
+    if (p.M == 1)
+        return reinterpret_cast<uintptr_t>(p.A) % 16 == 0 && (p.a_kmajor || p.lda == 1);
+    return p.a_kmajor && rows_on_16(p.A, p.lda, bytes);
+}
+
 template <int TYPE>
 cudaError_t fused_of(const FusedProblem &p, cudaStream_t stream, const char **name) {
     using V = Value<TYPE>;
     const int64_t sms = sm_count();
-    if (p.M <= 4 && p.K > 0 && p.b_kmajor && (p.a_kmajor || p.M == 1) &&
-        rows_on_16(p.B, p.ldb, V::BYTES)) {
+    if (rows_fit(p, V::BYTES)) {
         FusedProblem q = p;
-        bool ok = p.a_kmajor ? rows_on_16(p.A, p.M > 1 ? p.lda : 0, V::BYTES) : p.lda == 1;
-        if (!p.a_kmajor) {  // one row, its K lda apart: contiguous when lda is 1
-            q.a_kmajor = true;
-            q.lda = p.K;
-            ok = ok && reinterpret_cast<uintptr_t>(p.A) % 16 == 0;
-        }
-        if (ok && ceil_div(p.N, kRowsWarps) <= INT32_MAX) {
-            *name = "fused_rows";
-            // warps for about 32 per SM, each with a few steps of K
-            int split = 1;
-            while (split < kRowsWarps && p.N * split < 24 * sms &&
-                   ceil_div(p.K, 32 * V::PER_16) >= 4 * split)
-                split *= 2;
-            const int64_t ctas = ceil_div(p.N, kRowsWarps / split);
-            if (p.M == 1) return launch(fused_rows_kernel<TYPE, 1>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
-            if (p.M == 2) return launch(fused_rows_kernel<TYPE, 2>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
-            return launch(fused_rows_kernel<TYPE, 4>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
-        }
+        q.a_kmajor = true;  // (one row whose K lies one apart may be column-major)
+        *name = "fused_rows";
+        // warps for about 24 per SM, each with a few steps of K
+        int split = 1;
+        while (split < kRowsWarps && p.N * split < 24 * sms && ceil_div(p.K, 32 * V::PER_16) >= 4 * split)
+            split *= 2;
+        const int64_t ctas = ceil_div(p.N, kRowsWarps / split);
+        if (p.M == 1)
+            return launch(fused_rows_kernel<TYPE, 1>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
+        if (p.M == 2)
+            return launch(fused_rows_kernel<TYPE, 2>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
+        return launch(fused_rows_kernel<TYPE, 4>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
     }
     *name = "fused_simt";
     if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= sms) return tiles_as<TYPE, 128>(p, 1, stream);
@@ -414,6 +415,10 @@ cudaError_t fused_of(const FusedProblem &p, cudaStream_t stream, const char **na
 cudaError_t launch_column_sums(const float *part, int64_t blocks, int64_t N, float *dbias,
                                cudaStream_t stream) {
     return launch(column_sums_kernel, ceil_div(N, 32), 256, 0, 1, stream, part, blocks, N, dbias);
+}
+
+bool fused_rows_eligible(const FusedProblem &p, InType in) {
+    return rows_fit(p, in == InType::F32 ? 4 : 2);
 }
 
 cudaError_t launch_fused_simt(const FusedProblem &p, InType in, cudaStream_t stream,

@@ -1,0 +1,967 @@
+// fused_tc.cu -- the fused products on the sm_103a tensor cores (BF16 or FP16
+// inputs, FP32 accumulation).
+//
+//   forward:  Z = alpha op(A) op(B) + bias, D = act(Z) + residual, Z kept or not
+//   gradient: D = alpha op(A) op(B) * act'(pre), and D's column sums
+//
+// One warp fills a ring of 128-byte-swizzled stages by TMA, one issues
+// tcgen05.mma into one of two TMEM accumulators, eight finish the other one.
+// Large problems: CTA pairs on tiles of 256 x 256.  Others: single CTAs, tiles of
+// up to 128 rows and 64, 128 or 256 columns, persistent; or, when there are fewer
+// tiles than SMs, K split over the CTAs of a cluster, which add each other's sums
+// through distributed shared memory in the order of the pieces.
+//
+// The epilogue takes blocks of 32 rows and 64 columns, a row per lane.  What is
+// read beside the sums (residual, pre) comes by TMA into a box of shared memory
+// ahead of time -- the next block's, or the next tile's first, as soon as a box
+// has been read -- and what is written leaves through boxes by TMA, so that the
+// epilogue's memory traffic costs the warps a few 16-byte accesses per lane.  Rows
+// that do not start on 16 bytes move through the same boxes by ordinary loads and
+// stores.
+#include <atomic>
+#include <mutex>
+
+#include "fused.cuh"
+#include "internal.h"
+#include "tc_epilogue.cuh"
+#include "tcgen05.cuh"
+#include "tma_maps.h"
+
+namespace gemm {
+namespace {
+
+using namespace tc;
+
+constexpr int kGroupM = 16;     // tile rows per band of the raster
+constexpr int kMaxStages = 16;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kProducer = kEpiWarps, kIssuer = kEpiWarps + 1;
+constexpr int kBox = 4096;      // 32 rows of 64 16-bit values
+constexpr int kBody = 224 * 1024;  // ring and boxes
+constexpr int kBiasBytes = kEpiWarps * 32 * 4;
+// ring and boxes, 32 bias values per epilogue warp, barriers, alignment
+constexpr int kSmemBytes = 1024 + kBody + kBiasBytes + 512;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+constexpr int kMaxSplit = 8;
+constexpr int kSlot = 8192;     // 32 x 64 FP32 sums of another piece
+
+struct Args {
+    int64_t M, N;
+    uint32_t tiles_m, tiles_n;
+    int num_kb, ksub, ks;  // steps of K (stages), blocks of 64 per step, pieces
+    int bn, am;
+    int stages, ring_bytes, boxes;
+    uint32_t stage_bytes, a_region;
+    int a_kmajor, b_kmajor, b_blocks, ab_format;
+    float alpha;
+    const float *bias;
+    int act, out;  // out: kOutBf16 or kOutF16
+    void *D, *pre;
+    const void *in;  // forward: residual; gradient: pre
+    int64_t ldd, ld_pre, ld_in;
+    int tma_d, tma_pre, tma_in;     // rows start on 16 bytes
+    int even_d, even_pre, even_in;  // rows start on 4 bytes
+    float *part;  // gradient: sums of the 32-row blocks' columns, [blocks][N], or null
+    uint64_t timeout_ns;
+};
+
+struct Tile {
+    int64_t m0, n0;
+    int m_valid;  // its rows, 1 .. am * CG
+};
+
+template <int CG>
+__device__ __forceinline__ bool get_tile(const Args &a, uint32_t w, Tile &t) {
+    if (w >= a.tiles_m * a.tiles_n) return false;
+    const uint32_t width = kGroupM * a.tiles_n;
+    const uint32_t band = w / width, in_band = w - band * width;
+    const uint32_t rest = a.tiles_m - band * kGroupM, high = rest < kGroupM ? rest : kGroupM;
+    const uint32_t q = in_band / high;
+    const int rows = a.am * CG;
+    t.n0 = static_cast<int64_t>(q) * a.bn;
+    t.m0 = static_cast<int64_t>(band * kGroupM + (in_band - q * high)) * rows;
+    t.m_valid = a.M - t.m0 < rows ? static_cast<int>(a.M - t.m0) : rows;
+    return true;
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                              uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t at, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int32_t c0, int32_t c1,
+                                             uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Eight 16-bit values as FP32.
+__device__ __forceinline__ void widen(const uint4 &q, int type, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (type == kOutBf16) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+__device__ __forceinline__ uint4 narrow(const float (&v)[8], int type) {
+    return make_uint4(pack_16(v[0], v[1], type), pack_16(v[2], v[3], type),
+                      pack_16(v[4], v[5], type), pack_16(v[6], v[7], type));
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate_8(float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fused_activation<true>(v[i], ACT);
+}
+template <int ACT>
+__device__ __forceinline__ void slope_8(float (&v)[8], const float (&z)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= fused_slope<true>(z[i], ACT);
+}
+
+// The sum of the 32 lanes' v[j] for column j = lane, in a fixed order.
+__device__ __forceinline__ float column_sum(float (&v)[32]) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool high = (lane & s) != 0;
+#pragma unroll
+        for (int j = 0; j < s; ++j) {
+            const float give = high ? v[j] : v[j + s], keep = high ? v[j + s] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+        }
+    }
+    return v[0];
+}
+
+// 16-byte piece p of row r of a box (128-byte swizzle).
+__device__ __forceinline__ uint32_t piece_at(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
+
+// A box's rows to memory, and back, where TMA cannot: two values per lane and row.
+__device__ __forceinline__ void box_to_rows(uint32_t box, void *D, int64_t ldd, int64_t row0, int nrows,
+                                            int64_t c0, int width, bool even) {
+    const int lane = threadIdx.x % 32, c = lane * 2;
+    uint16_t *d = static_cast<uint16_t *>(D) + row0 * ldd + c0 + c;
+    if (c >= width) return;
+#pragma unroll 4
+    for (int r = 0; r < nrows; ++r, d += ldd) {
+        const uint32_t w = ld_shared_u32(box + piece_at(r, lane / 4) + lane % 4 * 4);
+        if (even && c + 1 < width) {
+            *reinterpret_cast<uint32_t *>(d) = w;
+        } else {
+            d[0] = static_cast<uint16_t>(w);
+            if (c + 1 < width) d[1] = static_cast<uint16_t>(w >> 16);
+        }
+    }
+}
+__device__ __forceinline__ void rows_to_box(uint32_t box, const void *from, int64_t ld, int64_t row0,
+                                            int nrows, int64_t c0, int width, bool even) {
+    const int lane = threadIdx.x % 32, c = lane * 2;
+    const uint16_t *s = static_cast<const uint16_t *>(from) + row0 * ld + c0 + c;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t *at = s + (r0 + i) * ld;
+            w[i] = 0;
+            if (r0 + i >= nrows || c >= width) continue;
+            if (even && c + 1 < width) {
+                w[i] = *reinterpret_cast<const uint32_t *>(at);
+            } else {
+                w[i] = at[0];
+                if (c + 1 < width) w[i] |= static_cast<uint32_t>(at[1]) << 16;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            st_shared_u32(box + piece_at(r0 + i, lane / 4) + lane % 4 * 4, w[i]);
+    }
+}
+
+template <int CG, bool SPLIT, bool GRAD>
+__global__ void __launch_bounds__(kThreads, 1)
+    fused_tc_kernel(const __grid_constant__ CUtensorMap map_a,
+                    const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_b_edge,
+                    const __grid_constant__ CUtensorMap map_in,
+                    const __grid_constant__ CUtensorMap map_d,
+                    const __grid_constant__ CUtensorMap map_pre,
+                    const __grid_constant__ Args args) {
+    static_assert(!SPLIT || CG == 1, "K is split over single CTAs");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    // barriers (8 bytes each): full[kMaxStages] TMA -> MMA (the leader's count
+    // both CTAs), empty[kMaxStages] MMA -> TMA, tfull[2] MMA -> epilogue,
+    // tempty[2] epilogue -> MMA (the leader's count both CTAs), drain,
+    // ibar[kEpiWarps] boxes of residual / pre loaded
+    const uint32_t ring0 = smem_addr(ring);
+    const uint32_t bias0 = ring0 + kBody;
+    const uint32_t full0 = bias0 + kBiasBytes, empty0 = full0 + 8 * kMaxStages;
+    const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16;
+    const uint32_t drain = tempty0 + 16, ibar0 = drain + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + (ibar0 + 8 * kEpiWarps - ring0));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 1 && !SPLIT ? 0u : cluster_rank();
+    const bool leader = CG == 1 || rank == 0;
+    const int group = SPLIT ? args.ks : CG;  // CTAs that share a tile
+    const uint32_t first_tile = blockIdx.x / group, tile_step = gridDim.x / group;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2 * kMaxStages; ++s) mbar_init(full0 + 8 * s, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, kEpiWarps * CG);
+        }
+        mbar_init(drain, 1);
+        for (int e = 0; e < kEpiWarps; ++e) mbar_init(ibar0 + 8 * e, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
+    }
+    if (warp == kIssuer) tmem_alloc<CG>(smem_addr(tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2 || SPLIT) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int stages = args.stages, ksub = args.ksub;
+    const uint32_t stage_bytes = args.stage_bytes, a_region = args.a_region;
+    const int b_rows = args.bn / CG;  // columns of B this CTA loads
+    // this CTA's steps of K
+    const int kb_first = SPLIT ? static_cast<int>(static_cast<int64_t>(args.num_kb) * rank / args.ks) : 0;
+    const int kb_end =
+        SPLIT ? static_cast<int>(static_cast<int64_t>(args.num_kb) * (rank + 1) / args.ks) : args.num_kb;
+    const int nkb = kb_end - kb_first;
+    Tile t;
+    bool aborted = false;
+    // every lane waits (the warp stays converged); false: gave up
+    auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+        const bool done = __all_sync(
+            0xffffffffu, wait_bounded(bar, parity, abort_flag, args.timeout_ns));
+        if (!done && lane == 0) raise_abort(abort_flag);
+        return done;
+    };
+
+    if (warp == kProducer) {
+        // -------------------------------------------------------- TMA producer
+        const uint32_t count0 = CG == 1 ? full0 : map_to_rank(full0, 0);
+        const uint32_t a_rows = args.a_kmajor ? static_cast<uint32_t>(args.am) : 128u;
+        const uint32_t tx = static_cast<uint32_t>(CG) *
+                            (a_rows + static_cast<uint32_t>(b_rows)) * static_cast<uint32_t>(ksub) * 128u;
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true, reverse = false;
+        for (uint32_t w = first_tile; ok && get_tile<CG>(args, w, t); w += tile_step, reverse = !reverse) {
+            const int32_t b0 = static_cast<int32_t>(t.n0 + (CG == 2 ? rank : 0u) * b_rows);
+            const int32_t m0 = static_cast<int32_t>(t.m0 + (CG == 2 ? rank : 0u) * BM);
+            // CTA pairs: every other tile walks K backwards and starts on what the
+            // tile before it read last.  Single CTAs start at different steps:
+            // columns of B are a power of two apart as a rule, and CTAs in step
+            // would read the same few DRAM channels at once.
+            int kb = CG == 2 ? (reverse ? nkb - 1 : 0)
+                             : static_cast<int>((w * 5u) % static_cast<uint32_t>(nkb));
+            for (int i = 0; i < nkb; ++i) {
+                ok = wait_all(empty0 + 8 * stage, phase ^ 1);
+                if (!ok) break;
+                const uint32_t fb = count0 + 8 * stage;
+                const uint32_t sa = ring0 + stage * stage_bytes, sb = sa + a_region;
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
+                    // several blocks of 64 at once: the maps count K in blocks
+                    const int32_t block = (kb_first + kb) * ksub;
+                    const int32_t k_in = ksub > 1 ? 0 : block * BK, k_block = ksub > 1 ? block : 0;
+                    if (args.b_kmajor) {
+                        tma_load_4d<CG>(sb, &map_b, k_in, b0, k_block, 0, fb);
+                    } else if ((static_cast<int64_t>(b0) + b_rows) / 64 <= args.b_blocks) {
+                        tma_load_4d<CG>(sb, &map_b, 0, block * BK, b0 / 64, 0, fb);
+                    } else {
+                        for (int j = 0; j < b_rows; j += 64)
+                            tma_load_3d<CG>(sb + j * 128 * ksub, &map_b_edge, b0 + j, block * BK, 0, fb);
+                    }
+                    if (args.a_kmajor) {
+                        tma_load_3d<CG>(sa, &map_a, k_in, m0, k_block, fb);
+                    } else {
+                        tma_load_2d<CG>(sa, &map_a, m0, block * BK, fb);
+                        tma_load_2d<CG>(sa + 8192, &map_a, m0 + 64, block * BK, fb);
+                    }
+                }
+                if (CG == 2 && reverse)
+                    --kb;
+                else
+                    kb = kb + 1 == nkb ? 0 : kb + 1;
+                issued += issued < static_cast<uint32_t>(stages) ? 1u : 0u;
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        __syncwarp();
+        // the copies in flight land before the CTA exits (the leader's barriers
+        // count both CTAs' bytes)
+        if (lane == 0 && leader) {
+            for (uint32_t i = 0; i < issued; ++i) {
+                if (--stage < 0) {
+                    stage = stages - 1;
+                    phase ^= 1;
+                }
+                const volatile int never = 0;
+                if (!wait_bounded(full0 + 8 * stage, phase, &never, args.timeout_ns))
+                    raise_abort(abort_flag);
+            }
+        }
+        aborted = !ok;
+        __syncwarp();
+    } else if (warp == kIssuer) {
+        // ---------------------------------------------------------- MMA issuer
+        if (leader) {
+            const bool a_mn = !args.a_kmajor, b_mn = !args.b_kmajor;
+            const uint64_t a_desc0 = a_mn ? desc_mnmajor(ring0, 0) : desc_kmajor(ring0, 0);
+            const uint64_t b_desc0 =
+                b_mn ? smem_desc(ring0 + a_region, static_cast<uint32_t>(ksub) * 8192u, 1024)
+                     : desc_kmajor(ring0 + a_region, 0);
+            const uint64_t a_step = (a_mn ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+            const uint64_t b_step = (b_mn ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+            // a step's blocks of 64: rows x 128 bytes apart (N-major: 64 rows of K)
+            const uint64_t a_sub = static_cast<uint64_t>(args.am) * 128u >> 4;
+            const uint64_t b_sub = b_mn ? 8192u >> 4 : static_cast<uint64_t>(b_rows) * 128u >> 4;
+            const uint64_t stage_step = stage_bytes >> 4;
+            const uint32_t idesc = make_idesc(BM * CG, args.bn, a_mn, b_mn, args.ab_format);
+            int stage = 0;
+            uint32_t phase = 0, acc = 0;
+            bool ok = true;
+            for (uint32_t w = first_tile; ok && get_tile<CG>(args, w, t); w += tile_step) {
+                ok = wait_all(tempty0 + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (acc & 1) * 256;
+                for (int i = 0; i < nkb; ++i) {
+                    ok = wait_all(full0 + 8 * stage, phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage) * stage_step;
+                    const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage) * stage_step;
+                    if (elect_one()) {
+                        tc_mma<CG>(d_tmem, ad, bd, idesc, i > 0 ? 1u : 0u);
+                        tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
+                        tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
+                        tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
+                        for (int u = 1; u < ksub; ++u) {
+                            const uint64_t au = ad + u * a_sub, bu = bd + u * b_sub;
+                            tc_mma<CG>(d_tmem, au, bu, idesc, 1u);
+                            tc_mma<CG>(d_tmem, au + a_step, bu + b_step, idesc, 1u);
+                            tc_mma<CG>(d_tmem, au + 2 * a_step, bu + 2 * b_step, idesc, 1u);
+                            tc_mma<CG>(d_tmem, au + 3 * a_step, bu + 3 * b_step, idesc, 1u);
+                        }
+                        tc_commit<CG>(empty0 + 8 * stage);  // frees the stage (both CTAs)
+                    }
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) tc_commit<CG>(tfull0 + 8 * (acc & 1));
+                ++acc;
+            }
+            __syncwarp();
+            // all MMAs issued here have finished once `drain` completes
+            if (elect_one()) {
+                tc_commit_local<CG>(drain);
+                const volatile int never = 0;
+                if (!wait_bounded(drain, 0, &never, args.timeout_ns)) raise_abort(abort_flag);
+            }
+            aborted = !ok;
+        }
+        __syncwarp();
+    }
+
+    // Epilogue warps: two per quarter of the TMEM lanes, each takes every other
+    // block of 64 columns.
+    const int e = warp, quarter = warp % 4, half = (e / 4) & 1;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t box_d = ring0 + args.ring_bytes + (e & 7) * args.boxes * kBox;
+    const uint32_t box_pre = box_d + kBox;  // (forward with pre kept)
+    const uint32_t box_in = box_d + (args.boxes - 1) * kBox;
+    const uint32_t bias_at = bias0 + (e & 7) * 128;
+    const uint32_t ibar = ibar0 + 8 * (e & 7);
+    const bool has_in = args.in != nullptr;
+    const bool has_pre = !GRAD && args.pre != nullptr;
+    uint32_t blocks_in = 0;  // boxes fetched by TMA and read
+    bool pending = false;    // one is on its way
+
+    int nrows = 0, n_blocks = 0;
+    int64_t row0 = 0;
+    // what this warp does of tile t
+    auto place = [&](const Tile &tile, int64_t &r0, int &rows, int &blocks) {
+        const int first = (CG == 2 ? static_cast<int>(rank) * BM : 0) + quarter * 32;
+        const int left = tile.m_valid - first;
+        rows = left < 0 ? 0 : (left > 32 ? 32 : left);
+        r0 = tile.m0 + first;
+        const int64_t cols = args.N - tile.n0;
+        const int wide = cols < args.bn ? static_cast<int>(cols) : args.bn;
+        blocks = rows > 0 ? (wide + 63) / 64 : 0;
+    };
+    auto fetch_in = [&](int64_t r0, int64_t c0) {
+        if (elect_one()) {
+            mbar_arrive_expect_tx(ibar, kBox);
+            tma_load_2d<CG>(box_in, &map_in, static_cast<int32_t>(c0), static_cast<int32_t>(r0),
+                            CG == 1 ? ibar : map_to_rank(ibar, rank));
+        }
+        __syncwarp();
+        pending = true;
+    };
+
+    // One block: 64 columns from tile column b * 64 on.  sums(h, v): the product's
+    // columns h * 32 .. of this lane's row; after(): all sums have been read; next():
+    // fetches the next box.  False: gave up.
+    auto finish_block = [&](int b, auto &&sums, auto &&after, auto &&next) -> bool {
+        const int64_t c0 = t.n0 + b * 64;
+        const int width = args.N - c0 < 64 ? static_cast<int>(args.N - c0) : 64;
+        float bias2[2] = {0.f, 0.f};
+        if (!GRAD && args.bias != nullptr) {
+            if (lane < width) bias2[0] = __ldg(args.bias + c0 + lane);
+            if (lane + 32 < width) bias2[1] = __ldg(args.bias + c0 + lane + 32);
+        }
+        if (has_in) {
+            if (args.tma_in) {
+                if (!pending) fetch_in(row0, c0);
+                if (!wait_all(ibar, blocks_in & 1)) return false;
+                ++blocks_in;
+                pending = false;
+            } else {
+                rows_to_box(box_in, args.in, args.ld_in, row0, nrows, c0, width, args.even_in != 0);
+                __syncwarp();
+            }
+        }
+        if (elect_one()) bulk_wait_read();  // the boxes of the last block have left
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!GRAD && args.bias != nullptr) {
+                st_shared_f32(bias_at + lane * 4, bias2[h]);
+                __syncwarp();
+            }
+            float v[32];
+            sums(h, v);
+            if (h == 1) after();
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                float z[8], x[8] = {};
+                if (has_in) widen(ld_shared_u4(box_in + piece_at(lane, h * 4 + p)), args.out, x);
+                if constexpr (GRAD) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[i] = args.alpha * v[p * 8 + i];
+                    if (args.act == kActGelu)
+                        slope_8<kActGelu>(z, x);
+                    else if (args.act == kActSilu)
+                        slope_8<kActSilu>(z, x);
+                    else if (args.act == kActRelu)
+                        slope_8<kActRelu>(z, x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[p * 8 + i] = z[i];
+                } else {
+                    if (args.bias != nullptr) {
+                        const float4 b0 = ld_shared_v4(bias_at + p * 32), b1 = ld_shared_v4(bias_at + p * 32 + 16);
+                        const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[i] = fmaf(args.alpha, v[p * 8 + i], bv[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[i] = args.alpha * v[p * 8 + i];
+                    }
+                    if (has_pre) {
+                        const uint4 q = narrow(z, args.out);
+                        st_shared_v4(box_pre + piece_at(lane, h * 4 + p), q.x, q.y, q.z, q.w);
+                    }
+                    if (args.act == kActGelu)
+                        activate_8<kActGelu>(z);
+                    else if (args.act == kActSilu)
+                        activate_8<kActSilu>(z);
+                    else if (args.act == kActRelu)
+                        activate_8<kActRelu>(z);
+                    if (has_in) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[i] += x[i];
+                    }
+                }
+                const uint4 q = narrow(z, args.out);
+                st_shared_v4(box_d + piece_at(lane, h * 4 + p), q.x, q.y, q.z, q.w);
+            }
+            if constexpr (GRAD) {
+                if (args.part != nullptr) {
+                    if (lane >= nrows) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    }
+                    const float s = column_sum(v);
+                    if (h * 32 + lane < width) args.part[row0 / 32 * args.N + c0 + h * 32 + lane] = s;
+                }
+            }
+            if (!GRAD && args.bias != nullptr) __syncwarp();
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (has_in && args.tma_in) next();
+        // (TMA stores whole 16-byte pieces: the block with an odd end goes by rows)
+        const bool whole = width == 64 || args.N % 8 == 0;
+        if (args.tma_d && whole) {
+            if (elect_one())
+                tma_store_2d(&map_d, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_d);
+        } else {
+            box_to_rows(box_d, args.D, args.ldd, row0, nrows, c0, width, args.even_d != 0);
+        }
+        if (has_pre) {
+            if (args.tma_pre && whole) {
+                if (elect_one())
+                    tma_store_2d(&map_pre, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_pre);
+            } else {
+                box_to_rows(box_pre, args.pre, args.ld_pre, row0, nrows, c0, width, args.even_pre != 0);
+            }
+        }
+        __syncwarp();
+        return true;
+    };
+
+    if constexpr (!SPLIT) {
+        if (warp < kEpiWarps) {
+            uint32_t acc = 0;
+            for (uint32_t w = first_tile; get_tile<CG>(args, w, t); w += tile_step) {
+                place(t, row0, nrows, n_blocks);
+                const uint32_t buf = acc & 1, t_acc = tmem_base + lane_off + buf * 256;
+                const int last = n_blocks > half ? half + (n_blocks - 1 - half) / 2 * 2 : -1;
+                if (has_in && args.tma_in && last >= 0 && !pending) fetch_in(row0, t.n0 + half * 64);
+                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                ++acc;
+                auto release_acc = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 1)
+                            mbar_arrive(tempty0 + 8 * buf);
+                        else
+                            mbar_arrive_cluster(map_to_rank(tempty0 + 8 * buf, 0));
+                    }
+                };
+                for (int b = half; b < n_blocks && !aborted; b += 2) {
+                    aborted = !finish_block(
+                        b,
+                        [&](int h, float (&v)[32]) {
+                            uint32_t raw[32];
+                            __syncwarp();
+                            tmem_load_32cols(t_acc + b * 64 + h * 32, raw);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                        },
+                        [&]() {
+                            if (b == last) release_acc();
+                        },
+                        [&]() {
+                            if (b != last) {
+                                fetch_in(row0, t.n0 + (b + 2) * 64);
+                                return;
+                            }
+                            Tile u;  // the next tile's first block
+                            int64_t r0;
+                            int rows, blocks;
+                            if (!get_tile<CG>(args, w + tile_step, u)) return;
+                            place(u, r0, rows, blocks);
+                            if (blocks > half) fetch_in(r0, u.n0 + half * 64);
+                        });
+                }
+                if (aborted) break;
+                if (last < 0) release_acc();
+            }
+        }
+    } else {
+        // The pieces' sums: each 32 x 64 block has one owner among the cluster's
+        // CTAs, which adds the others' to its own.  The blocks travel into the
+        // owners' rings, which nothing uses once every piece is multiplied.
+        const bool mine = get_tile<CG>(args, first_tile, t) && warp < kEpiWarps;
+        int quarters = 0;
+        if (mine) {
+            place(t, row0, nrows, n_blocks);
+            quarters = (t.m_valid + 31) / 32;
+            if (!wait_all(tfull0, 0)) aborted = true;
+            tc_fence_after();
+        }
+        const uint32_t t_acc = tmem_base + lane_off;
+        cluster_sync();
+        auto owner_of = [&](int b, int &slot) -> int {
+            const int u = b * quarters + quarter;
+            slot = u / args.ks * (args.ks - 1);
+            return u % args.ks;
+        };
+        if (mine) {
+            for (int b = half; b < n_blocks; b += 2) {
+                int slot;
+                const int owner = owner_of(b, slot);
+                if (owner == static_cast<int>(rank)) continue;
+                // (a slot per other piece, in their order)
+                slot += static_cast<int>(rank) - (static_cast<int>(rank) > owner ? 1 : 0);
+                const uint32_t to = map_to_rank(ring0 + slot * kSlot + lane * 256, owner);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t raw[32];
+                    __syncwarp();
+                    tmem_load_32cols(t_acc + b * 64 + h * 32, raw);
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+                        st_cluster_v4(to + (((h * 8 + p) ^ (lane & 15)) << 4), raw[p * 4], raw[p * 4 + 1],
+                                      raw[p * 4 + 2], raw[p * 4 + 3]);
+                }
+            }
+        }
+        cluster_sync();
+        if (mine && !aborted) {
+            for (int b = half; b < n_blocks && !aborted; b += 2) {
+                int slot;
+                if (owner_of(b, slot) != static_cast<int>(rank)) continue;
+                aborted = !finish_block(
+                    b,
+                    [&](int h, float (&v)[32]) {
+                        uint32_t raw[32];
+                        __syncwarp();
+                        tmem_load_32cols(t_acc + b * 64 + h * 32, raw);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                        for (int q = 0; q < args.ks; ++q) {
+                            if (q == static_cast<int>(rank)) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(raw[j]);
+                                continue;
+                            }
+                            const int s = slot + q - (q > static_cast<int>(rank) ? 1 : 0);
+                            const uint32_t from = ring0 + s * kSlot + lane * 256;
+#pragma unroll
+                            for (int p = 0; p < 8; ++p) {
+                                const float4 f = ld_shared_v4(from + (((h * 8 + p) ^ (lane & 15)) << 4));
+                                v[p * 4] += f.x, v[p * 4 + 1] += f.y;
+                                v[p * 4 + 2] += f.z, v[p * 4 + 3] += f.w;
+                            }
+                        }
+                    },
+                    [] {}, [] {});
+            }
+        }
+    }
+    if (warp < kEpiWarps) {
+        // a box that was fetched for nothing lands, and D is written
+        if (pending) wait_all(ibar, blocks_in & 1);
+        __syncwarp();
+        if (elect_one()) bulk_wait_all();
+        __syncwarp();
+    }
+
+    if (aborted) {
+        // give copies issued by a peer that gave up a short time to land
+        const uint64_t t0 = global_timer();
+        while (global_timer() - t0 < 2000000ull) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2 || SPLIT) cluster_sync();
+    tc_fence_after();
+    if (warp == kIssuer) tmem_dealloc<CG>(tmem_base);
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bit
+
+std::atomic<bool> g_launched[kMaxDevices];
+
+template <int CG, bool SPLIT, bool GRAD>
+cudaLaunchConfig_t config(int grid, int cluster, cudaStream_t stream, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    set_pdl_attribute(&attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Prepares a kernel on device `dev` before its first launch there; resident[c]:
+// clusters of c CTAs the device holds at once (0: none, or not asked).
+struct Prepared {
+    std::once_flag once;
+    cudaError_t err = cudaSuccess;
+    int resident[kMaxSplit + 1] = {};
+};
+template <int CG, bool SPLIT, bool GRAD>
+const Prepared &prepared(int dev) {
+    static Prepared all[kMaxDevices];
+    Prepared &p = all[dev];
+    std::call_once(p.once, [&p, dev] {
+        const auto kernel = fused_tc_kernel<CG, SPLIT, GRAD>;
+        p.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (p.err != cudaSuccess) return;
+        int sms = 0;
+        p.err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (p.err != cudaSuccess) return;
+        p.resident[1] = sms > 0 ? sms : 1;
+        for (int c = 2; c <= (CG == 2 ? 2 : SPLIT ? kMaxSplit : 1); c *= 2) {
+            cudaLaunchAttribute attr[2];
+            cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD>(c, c, 0, attr);
+            cfg.attrs = attr + 1;  // the occupancy query takes the cluster shape only
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&p.resident[c], kernel, &cfg) != cudaSuccess) {
+                p.resident[c] = 0;
+                (void)cudaGetLastError();  // that cluster size is then not used
+            }
+        }
+    });
+    return p;
+}
+
+struct Maps {
+    CUtensorMap a, b, b_edge, in, d, pre;
+};
+
+template <int CG, bool SPLIT, bool GRAD>
+cudaError_t launch_as(const Maps &m, const Args &a, int dev, int grid, int cluster,
+                      cudaStream_t stream) {
+    g_launched[dev].store(true);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD>(grid, cluster, stream, attr);
+    return cudaLaunchKernelEx(&cfg, fused_tc_kernel<CG, SPLIT, GRAD>, m.a, m.b, m.b_edge, m.in, m.d,
+                              m.pre, a);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A way to cut the product.
+struct Cut {
+    int cg, am, bn, ks;
+};
+
+// The cut whose slowest CTA is done first, by a model: a step of K takes the
+// longer of its MMAs (512 clocks of the SM's tensor core for 128 x 256 x 64, or a
+// pair's 256 x 256 x 64) and its bytes from L2 at 120 GB/s per SM; a tile costs
+// 2 us beside that, an exchange of pieces 2 us more.
+Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &split, int sms) {
+    const int64_t kb = ceil_div(p.K, BK);
+    Cut best = {1, BM, 256, 1};
+    double least = 1e30;
+    auto consider = [&](const Cut &c, int64_t slots) {
+        if (slots <= 0) return;
+        const int64_t tiles = ceil_div(p.M, c.am * c.cg) * ceil_div(p.N, c.bn);
+        const int64_t rounds = ceil_div(tiles, slots);
+        const double mma = 0.27 * c.bn / 256, l2 = (c.am + c.bn / c.cg) * 128 / 120e3;
+        const double steps = static_cast<double>(ceil_div(kb, c.ks));
+        const double cost = rounds * (steps * (mma > l2 ? mma : l2) + 2.0) + (c.ks > 1 ? 2.0 : 0.0);
+        if (cost < least) least = cost, best = c;
+    };
+    if (p.M > BM) consider({2, BM, 256, 1}, pair.resident[2]);
+    const int am = !p.a_kmajor || p.M > 64 ? BM : (p.M <= 16 ? 16 : (p.M <= 32 ? 32 : 64));
+    for (int bn : {256, 128, 64}) {
+        if (bn > 64 && p.N <= bn / 2) continue;
+        consider({1, am, bn, 1}, sms);
+        for (int ks = 2; ks <= kMaxSplit; ks *= 2) {
+            const int64_t tiles = ceil_div(p.M, am) * ceil_div(p.N, bn);
+            if (kb >= 2 * ks && tiles <= split.resident[ks]) consider({1, am, bn, ks}, split.resident[ks]);
+        }
+    }
+    return best;
+}
+
+// Blocks of 64 of K per step: a copy takes the producer about 100 ns to issue
+// whatever its size, while a 128 x 128 tile multiplies a block in 130 ns.  The
+// copies of K-major operands then count K in blocks of 64, which needs K to be a
+// multiple of 64.
+int sub_blocks(const FusedProblem &p, const Cut &c) {
+    if (c.cg == 2 || p.K % BK != 0 || !p.a_kmajor) return 1;
+    const int64_t piece = ceil_div(p.K, BK) / c.ks;
+    int ksub = 1;
+    while (ksub < 4 && c.bn * 2 * ksub <= 256 && (c.am + c.bn) * 128 * 2 * ksub <= 65536 &&
+           piece >= 4 * ksub)
+        ksub *= 2;
+    return ksub;
+}
+
+}  // namespace
+
+bool fused_tc_eligible(const FusedProblem &p) {
+    return p.K > 0 && tma_rows(p.A, p.lda) && tma_rows(p.B, p.ldb) &&
+           ceil_div(p.M, 16) * ceil_div(p.N, 64) < kMaxTiles;
+}
+
+template <bool GRAD>
+static cudaError_t launch_tc_as(const FusedProblem &p, InType in, int dev, cudaStream_t stream,
+                                const char **name) {
+    const bool bf16 = in == InType::BF16;
+    const Prepared &pair = prepared<2, false, GRAD>(dev), &one = prepared<1, false, GRAD>(dev),
+                   &split = prepared<1, true, GRAD>(dev);
+    for (const Prepared *q : {&pair, &one, &split})
+        if (q->err != cudaSuccess) return q->err;
+    const Cut cut = choose_cut(p, pair, split, one.resident[1]);
+    Args a = {};
+    a.M = p.M;
+    a.N = p.N;
+    a.am = cut.am;
+    a.bn = cut.bn;
+    a.ks = cut.ks;
+    a.ksub = sub_blocks(p, cut);
+    a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
+    a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, cut.am * cut.cg));
+    a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, cut.bn));
+    a.a_kmajor = p.a_kmajor;
+    a.b_kmajor = p.b_kmajor;
+    a.b_blocks = static_cast<int>(p.N / 64);
+    a.ab_format = bf16 ? 1 : 0;
+    a.alpha = p.alpha;
+    a.bias = p.bias;
+    a.act = p.act;
+    a.out = bf16 ? kOutBf16 : kOutF16;
+    a.D = p.D;
+    a.ldd = p.ldd;
+    a.in = GRAD ? p.pre : p.residual;
+    a.ld_in = GRAD ? p.ld_pre : p.ld_r;
+    a.pre = GRAD ? nullptr : p.pre;
+    a.ld_pre = p.ld_pre;
+    a.tma_d = tma_rows(a.D, a.ldd);
+    a.tma_in = a.in != nullptr && tma_rows(a.in, a.ld_in);
+    a.tma_pre = a.pre != nullptr && tma_rows(a.pre, a.ld_pre);
+    a.even_d = reinterpret_cast<uintptr_t>(a.D) % 4 == 0 && a.ldd % 2 == 0;
+    a.even_in = reinterpret_cast<uintptr_t>(a.in) % 4 == 0 && a.ld_in % 2 == 0;
+    a.even_pre = reinterpret_cast<uintptr_t>(a.pre) % 4 == 0 && a.ld_pre % 2 == 0;
+    // ring and boxes share the body; the last stage keeps 128 rows of A inside the
+    // ring (am < 128: the MMA's operand runs on into B and the next stages, stale
+    // rows that reach only accumulator rows which are not stored)
+    a.boxes = 1 + (a.pre != nullptr) + (a.in != nullptr);
+    a.ring_bytes = kBody - kEpiWarps * a.boxes * kBox;
+    a.a_region = static_cast<uint32_t>((p.a_kmajor ? a.am : BM) * a.ksub) * BK * 2;
+    a.stage_bytes = a.a_region + static_cast<uint32_t>(a.bn / cut.cg * a.ksub) * BK * 2;
+    const int over = BM * BK * 2 - static_cast<int>(a.stage_bytes);
+    const int fit = (a.ring_bytes - (over > 0 ? over : 0)) / static_cast<int>(a.stage_bytes);
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    a.timeout_ns = wait_limit_ns(ceil_div(p.K, BK));
+
+    Maps m;
+    bool ok = p.a_kmajor ? encode_kmajor(&m.a, bf16, p.A, p.K, p.M, p.lda, 1, p.lda, a.am, a.ksub, 3)
+                         : encode_stack(&m.a, bf16, p.A, p.M, p.K, p.lda, 1, 0, 64, BK, 2);
+    if (p.b_kmajor)
+        ok = ok && encode_kmajor(&m.b, bf16, p.B, p.K, p.N, p.ldb, 1, p.ldb, a.bn / cut.cg, a.ksub, 4);
+    else
+        ok = ok && encode_nmajor(&m.b, &m.b_edge, bf16, p.B, p.N, p.K, p.ldb, 1, p.ldb,
+                                 a.bn / cut.cg, a.ksub);
+    if (p.b_kmajor) m.b_edge = m.b;
+    m.in = m.d = m.pre = m.a;
+    auto rows_map = [&](CUtensorMap *map, const void *base, int64_t ld) {
+        return encode_stack(map, bf16, base, p.N, p.M, ld, 1, 0, 64, 32, 2);
+    };
+    if (a.tma_d) ok = ok && rows_map(&m.d, a.D, a.ldd);
+    if (a.tma_in) ok = ok && rows_map(&m.in, a.in, a.ld_in);
+    if (a.tma_pre) ok = ok && rows_map(&m.pre, a.pre, a.ld_pre);
+    if (!ok) return cudaErrorInvalidValue;
+
+    // the column sums of blocks of 32 rows, added by a second kernel
+    const int64_t blocks = ceil_div(p.M, 32);
+    void *ws = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (GRAD && p.dbias != nullptr) {
+        a.part = p.dbias;
+        if (blocks > 1) {
+            e = workspace_alloc(static_cast<size_t>(blocks * p.N) * sizeof(float), stream, &ws);
+            if (e != cudaSuccess) return e;
+            a.part = static_cast<float *>(ws);
+        }
+    }
+    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+    static const char *const kNames[3][2] = {{"fused_tc<f16>", "fused_tc<bf16>"},
+                                             {"fused_tc<f16,pair>", "fused_tc<bf16,pair>"},
+                                             {"fused_tc<f16,split>", "fused_tc<bf16,split>"}};
+    *name = kNames[cut.ks > 1 ? 2 : cut.cg - 1][bf16];
+    if (cut.cg == 2) {
+        const int64_t n = tiles < pair.resident[2] ? tiles : pair.resident[2];
+        e = launch_as<2, false, GRAD>(m, a, dev, static_cast<int>(2 * n), 2, stream);
+    } else if (cut.ks > 1) {
+        e = launch_as<1, true, GRAD>(m, a, dev, static_cast<int>(tiles * cut.ks), cut.ks, stream);
+    } else {
+        const int64_t n = tiles < one.resident[1] ? tiles : one.resident[1];
+        e = launch_as<1, false, GRAD>(m, a, dev, static_cast<int>(n), 1, stream);
+    }
+    if (ws != nullptr) {
+        if (e == cudaSuccess) e = launch_column_sums(a.part, blocks, p.N, p.dbias, stream);
+        const cudaError_t ef = workspace_free(ws, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e;
+}
+
+cudaError_t launch_fused_tc(const FusedProblem &p, InType in, cudaStream_t stream,
+                            const char **name) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    return p.grad ? launch_tc_as<true>(p, in, dev, stream, name)
+                  : launch_tc_as<false>(p, in, dev, stream, name);
+}
+
+cudaError_t fused_tc_read_and_clear_status(cudaStream_t stream, int *status) {
+    *status = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // (no copy while none of these kernels has been launched on the device)
+    if (dev < 0 || dev >= kMaxDevices || !g_launched[dev].load()) return cudaSuccess;
+    const int zero = 0;
+    e = cudaMemcpyFromSymbolAsync(status, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && *status != 0) {
+        e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    return e;
+}
+
+}  // namespace gemm

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "call.h"
+#include "fused.h"
 #include "gemm.h"
 #include "gemm_probe.h"
 #include "grouped.h"
@@ -281,11 +282,12 @@ GEMM_API const char *gemm_status_string(gemm_status_t status) {
 GEMM_API gemm_status_t gemm_last_device_status(cudaStream_t stream) {
     int status = 0;
     if (gemm::tc_read_and_clear_status(stream, &status) != cudaSuccess) return GEMM_ERR_INTERNAL;
-    int grouped = 0, shrink = 0;
+    int grouped = 0, shrink = 0, fused = 0;
     if (gemm::grouped_tc_read_and_clear_status(stream, &grouped) != cudaSuccess ||
-        gemm::lora_shrink_read_and_clear_status(stream, &shrink) != cudaSuccess)
+        gemm::lora_shrink_read_and_clear_status(stream, &shrink) != cudaSuccess ||
+        gemm::fused_tc_read_and_clear_status(stream, &fused) != cudaSuccess)
         return GEMM_ERR_INTERNAL;
-    if (status || grouped || shrink) {
+    if (status || grouped || shrink || fused) {
         // a kernel that gave up may have left split counters mid-count
         if (gemm::split_sync_release_device() != cudaSuccess) return GEMM_ERR_INTERNAL;
         return GEMM_ERR_TIMEOUT;

@@ -239,3 +239,102 @@ def test_offsets_past_32_bits():
     del fz, gd
     Bt = far(torch.from_numpy(rng.standard_normal((3, 64))).bfloat16().cuda())  # 3 columns, far apart
     assert torch.equal(lib.gemm_fused(A, Bt.t()), lib.gemm_fused(A, Bt.contiguous().t()))
+
+
+# ------------------------------------------------- larger products, each way they are cut
+def big(M, N, K, dtype, oa, ob, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = TORCH[dtype]
+
+    def normal(r, c, order, sigma=1.0):
+        if order:
+            return normal(c, r, 0, sigma).t()
+        ld = -(-c // 8) * 8
+        return torch.empty(r, ld, device="cuda", dtype=t).normal_(0, sigma, generator=g)[:, :c]
+
+    return (normal(M, K, oa), normal(K, N, ob, K ** -0.5), normal(M, N, 0), normal(M, N, 0),
+            torch.randn(N, device="cuda", generator=g))
+
+
+def near(got, ref, size, K, dtype, steep=1.0, extra=0.0):
+    """Within the sums' bound (rel_sum(K) of `size`), the epilogue's and half a step of the type."""
+    from grouped_harness import rel_sum
+    from mixture_harness import HALF_STEP, LEAST
+    tol = steep * rel_sum(K) * size + 2.0 ** -20 * ref.abs() + 2.0 ** -19 + extra
+    tol = tol * (1 + HALF_STEP[dtype]) + ref.abs() * HALF_STEP[dtype] + LEAST[dtype]
+    off = (got.double() - ref).abs()
+    assert (off <= tol).all(), f"{int((off > tol).sum())} off, worst {float((off / tol).max()):.3g}"
+
+
+CUTS = [("fused_tc<{},pair>", 2100, 2500, 200), ("fused_tc<{},pair>", 4097, 2305, 72),
+        ("fused_tc<{},pair>", 600, 9000, 328), ("fused_tc<{},pair>", 2561, 2048, 640),
+        ("fused_tc<{}>", 100, 9001, 264), ("fused_tc<{}>", 40, 20000, 512), ("fused_tc<{}>", 9, 12345, 64),
+        ("fused_tc<{},split>", 64, 1000, 4096), (None, 256, 515, 2048), (None, 130, 9001, 264),
+        ("fused_tc<{},split>", 16, 200, 8192), ("fused_tc<{},split>", 33, 64, 4000), (None, 33, 64, 1000),
+        (None, 500, 300, 3000)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("oa,ob", [(0, 1), (0, 0), (1, 0)])
+@pytest.mark.parametrize("kernel,M,N,K", CUTS)
+def test_cuts(dtype, oa, ob, kernel, M, N, K):
+    A, B, R, Z, b = big(M, N, K, dtype, oa, ob)
+    z = A.double() @ B.double()
+    size = A.double().abs() @ B.double().abs()
+    got, pre = lib.gemm_fused(A, B, bias=b, activation=SILU, residual=R, keep_pre=True)
+    name = lib.gemm_last_kernel()
+    if kernel is not None and not oa:  # (an M-major A has 128 rows per tile)
+        assert name == kernel.format(dtype)
+    near(pre, z + b.double(), size, K, dtype)
+    ref = torch.nn.functional.silu(z + b.double()) + R.double()
+    near(got, ref, size, K, dtype, 1.13)
+    only = lib.gemm_fused(A, B)
+    near(only, z, size, K, dtype)
+    d, sums = lib.gemm_fused_grad(A, B, Z, activation=GELU, bias_grad=True)
+    x = Z.double().requires_grad_()
+    torch.nn.functional.gelu(x, approximate="tanh").sum().backward()
+    ref = z * x.grad
+    near(d, ref, size, K, dtype, 1.13, 2.0 ** -18 * z.abs())
+    from grouped_harness import rel_sum
+    tol = ((1.13 * rel_sum(K) * size).sum(0) + (2.0 ** -18 * z.abs()).sum(0) +
+           200 * 2.0 ** -24 * ref.abs().sum(0))
+    assert ((sums.double() - ref.sum(0)).abs() <= tol).all()
+    assert lib.gemm_last_device_status() == lib.GEMM_OK
+    # the same bits every time, whatever the matrices' alignment
+    again, sums2 = lib.gemm_fused_grad(A, B, Z, activation=GELU, bias_grad=True)
+    assert torch.equal(again, d) and torch.equal(sums, sums2)
+    odd = torch.empty(M, N + 3, dtype=A.dtype, device="cuda")[:, 1:N + 1]
+    zo = torch.empty(M, N + 5, dtype=A.dtype, device="cuda")[:, 2:N + 2]
+    zo.copy_(Z)
+    again, sums2 = lib.gemm_fused_grad(A, B, zo, activation=GELU, bias_grad=True, out=odd)
+    assert torch.equal(again, d) and torch.equal(sums, sums2)
+
+
+def test_rows_behind_the_last_are_left():
+    for M, N, K in ((300, 520, 128), (2100, 2500, 64), (20, 4096, 2048)):
+        A, B, R, Z, b = big(M, N, K, "bf16", 0, 1)
+        buf = torch.full((M + 300, N + 72), 7.0, dtype=torch.bfloat16, device="cuda")
+        lib.gemm_fused(A, B, bias=b, residual=R, out=buf[:M, :N])
+        assert (buf[M:] == 7.0).all() and (buf[:, N:] == 7.0).all()
+        lib.gemm_fused_grad(A, B, Z, activation=SILU, out=buf[:M, :N])
+        assert (buf[M:] == 7.0).all() and (buf[:, N:] == 7.0).all()
+
+
+def test_large_in_place_and_on_many_streams():
+    """The residual read ahead of the tiles that overwrite it; several products at once."""
+    M, N, K = 2304, 2560, 128
+    A, B, R, Z, b = big(M, N, K, "f16", 0, 0)
+    want = lib.gemm_fused(A, B, bias=b, residual=R, activation=GELU)
+    dw, sw = lib.gemm_fused_grad(A, B, Z, activation=GELU, bias_grad=True)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        over, grad = R.clone(), Z.clone()
+        lib.gemm_fused(A, B, bias=b, residual=over, activation=GELU, out=over)
+        _, s = lib.gemm_fused_grad(A, B, grad, activation=GELU, bias_grad=True, out=grad)
+        assert torch.equal(over, want) and torch.equal(grad, dw) and torch.equal(s, sw)
+    sides = [torch.cuda.Stream() for _ in range(4)]
+    outs = [(lib.gemm_fused(A, B, bias=b, residual=R, activation=GELU, stream=s),
+             lib.gemm_fused_grad(A, B, Z, activation=GELU, bias_grad=True, stream=s)) for s in sides]
+    torch.cuda.synchronize()
+    for o, (d, s) in outs:
+        assert torch.equal(o, want) and torch.equal(d, dw) and torch.equal(s, sw)
