@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["gemm_api.cu", "sgemm_simt.cu", "sgemm_cluster.cu", "gemm_tc.cu", "workspace.cu",
            "probe.cu", "skinny.cu", "grouped_api.cu", "grouped_simt.cu",
            "grouped_tc.cu", "lora_shrink.cu", "group_rows.cu",
-           "mixture_api.cu", "route.cu", "combine.cu", "fused_api.cu", "fused_simt.cu",
+           "mixture_api.cu", "route.cu", "combine.cu",
+           "combine_bulk.cu", "fused_api.cu", "fused_simt.cu",
            "fused_tc.cu"]
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "epilogue.cuh"),
            os.path.join(CSRC, "call.h"), os.path.join(CSRC, "grouped.h"),
@@ -30,6 +31,7 @@ HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "epilogue.cuh"),
            os.path.join(CSRC, "tc_epilogue.cuh"), os.path.join(CSRC, "tma_maps.h"),
            os.path.join(CSRC, "mixture.h"), os.path.join(CSRC, "fused.h"),
            os.path.join(CSRC, "fused.cuh"), os.path.join(CSRC, "values.cuh"),
+           os.path.join(CSRC, "combine.h"),
            os.path.join(INCLUDE, "gemm.h"), os.path.join(INCLUDE, "gemm_probe.h")]
 
 NVCC_FLAGS = [

@@ -10,193 +10,210 @@
 // experts.
 #include <type_traits>
 
-#include "mixture.h"
-#include "values.cuh"
+#include "combine.h"
+#include "internal.h"
 
 namespace gemm {
 namespace {
 
-constexpr int kRowsAhead = 8;  // rows of Y in flight per thread
+// Loads of Y in flight per thread: R rows (the power of two that k fills, at most
+// 8) times the pieces of each.  (k = 2 with one piece of two rows: 369 us for 16384
+// tokens of 8192 BF16 columns.)
+__host__ __device__ constexpr int pieces_of(int rows) { return rows == 8 ? 1 : rows == 1 ? 4 : 2; }
+constexpr int kGradThreads = 256;
 
-// `n` values of a row from column c on: 16 bytes at once, or one by one where
-// the row does not start on 16 bytes or ends inside (n < PER_16).
-template <int TYPE, bool VEC>
-__device__ __forceinline__ void load_piece(const void *row, int64_t c, int n,
-                                           float (&v)[Value<TYPE>::PER_16]) {
-    using V = Value<TYPE>;
-    if (VEC && n == V::PER_16) {
-        V::unpack(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + c * V::BYTES)), v);
-    } else {
+// Row numbers and weights of R of a token's choices from j0 on (-1: none).
+template <int R>
+struct Choices {
+    int32_t at[R];
+    float w[R];
+    __device__ __forceinline__ Choices(const CombineProblem &p, int64_t t, int64_t j0) {
 #pragma unroll
-        for (int i = 0; i < V::PER_16; ++i) v[i] = i < n ? V::load(row, c + i) : 0.f;
-    }
-}
-
-// `n` of WIDE values to a row of another type; and from one (the residual, dD).
-template <int TYPE, bool VEC, int WIDE>
-__device__ __forceinline__ void store_values(void *row, int64_t c, int n, const float (&v)[WIDE]) {
-    using V = Value<TYPE>;
-    if (VEC && n == WIDE) {
-        uint8_t *to = static_cast<uint8_t *>(row) + c * V::BYTES;
-#pragma unroll
-        for (int i = 0; i < WIDE / V::PER_16; ++i)
-            reinterpret_cast<uint4 *>(to)[i] = V::pack(v + i * V::PER_16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < WIDE; ++i)
-            if (i < n) V::store(row, c + i, v[i]);
-    }
-}
-template <int TYPE, bool VEC, int WIDE>
-__device__ __forceinline__ void load_values(const void *row, int64_t c, int n, float (&v)[WIDE]) {
-    using V = Value<TYPE>;
-    if (VEC && n == WIDE) {
-        const uint8_t *from = static_cast<const uint8_t *>(row) + c * V::BYTES;
-#pragma unroll
-        for (int i = 0; i < WIDE / V::PER_16; ++i) {
-            float part[V::PER_16];
-            V::unpack(reinterpret_cast<const uint4 *>(from)[i], part);
-#pragma unroll
-            for (int j = 0; j < V::PER_16; ++j) v[i * V::PER_16 + j] = part[j];
+        for (int j = 0; j < R; ++j) {
+            const bool there = t < p.tokens && j0 + j < p.k;
+            at[j] = there ? __ldg(p.position + t * p.k + j0 + j) : -1;
+            w[j] = there && p.weights != nullptr ? __ldg(p.weights + t * p.k + j0 + j) : 1.f;
         }
-    } else {
 #pragma unroll
-        for (int i = 0; i < WIDE; ++i) v[i] = i < n ? V::load(row, c + i) : 0.f;
+        for (int j = 0; j < R; ++j)
+            if (at[j] < 0 || at[j] >= p.rows_y) at[j] = -1;
+    }
+};
+
+// A thread's C pieces of D, `apart` pieces apart from column c0 on (FULL: all inside).
+template <int YT, int DT, bool YVEC, bool FULL, int R, int C>
+__device__ __forceinline__ void combine_pieces(const CombineProblem &p, int64_t t, int64_t c0,
+                                               int64_t apart, bool dvec) {
+    using Y = Value<YT>;
+    constexpr int WIDE = Y::PER_16;
+    float sum[C][WIDE] = {}, r[C][WIDE] = {};
+    int n[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t left = p.N - (c0 + c * apart);
+        n[c] = FULL || left >= WIDE ? WIDE : (left > 0 ? static_cast<int>(left) : 0);
+        // (the residual is under way with the rows)
+        if (p.residual != nullptr)
+            load_values<DT, FULL, WIDE>(p.residual, t * p.ld_r, c0 + c * apart, n[c], dvec, r[c]);
+    }
+    for (int64_t j0 = 0; j0 < p.k; j0 += R) {
+        const Choices<R> ch(p, t, j0);
+        uint4 q[R][C];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                q[j][c] = make_uint4(0, 0, 0, 0);
+                if (ch.at[j] >= 0)
+                    q[j][c] = load_piece<YT, YVEC, FULL>(p.Y, ch.at[j] * p.ldy, c0 + c * apart, n[c]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (ch.at[j] < 0) continue;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float y[WIDE];
+                Y::unpack(q[j][c], y);
+#pragma unroll
+                for (int i = 0; i < WIDE; ++i) sum[c][i] = fmaf(ch.w[j], y[i], sum[c][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int i = 0; i < WIDE; ++i) sum[c][i] += r[c][i];
+        store_values<DT, FULL, WIDE>(p.D, t * p.ldd, c0 + c * apart, n[c], dvec, sum[c]);
     }
 }
 
-// A thread per 16 bytes of Y's columns and token; `pieces` of them in a row.
-template <int YT, int DT, bool YVEC, bool DVEC>
+// `lanes` threads (a power of two, at most 32) take lanes * C pieces of a token:
+// piece (chunk * C + c) * lanes + lane; `chunks` such runs make a row.
+template <int YT, int DT, bool YVEC, int R>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineProblem p,
-                                                      int64_t pieces) {
-    using Y = Value<YT>;
-    constexpr int WIDE = Y::PER_16;
+                                                      int lanes, uint32_t chunks, bool dvec) {
+    constexpr int WIDE = Value<YT>::PER_16, C = pieces_of(R);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t all = p.tokens * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < all; q += step) {
-        const int64_t t = all <= UINT32_MAX
-                              ? static_cast<uint32_t>(q) / static_cast<uint32_t>(pieces)
-                              : q / pieces;
-        const int64_t c = (q - t * pieces) * WIDE;
-        const int n = p.N - c < WIDE ? static_cast<int>(p.N - c) : WIDE;
-        float sum[WIDE] = {};
-        for (int64_t j0 = 0; j0 < p.k; j0 += kRowsAhead) {
-            int32_t at[kRowsAhead];
-            float w[kRowsAhead], y[kRowsAhead][WIDE];
-#pragma unroll
-            for (int j = 0; j < kRowsAhead; ++j) {
-                const int64_t r = t * p.k + j0 + j;
-                at[j] = j0 + j < p.k ? __ldg(p.position + r) : -1;
-                w[j] = j0 + j < p.k && p.weights != nullptr ? __ldg(p.weights + r) : 1.f;
-                if (at[j] < 0 || at[j] >= p.rows_y) at[j] = -1;
-            }
-#pragma unroll
-            for (int j = 0; j < kRowsAhead; ++j)
-                if (at[j] >= 0)
-                    load_piece<YT, YVEC>(static_cast<const uint8_t *>(p.Y) + at[j] * p.ldy * Y::BYTES, c, n, y[j]);
-#pragma unroll
-            for (int j = 0; j < kRowsAhead; ++j) {
-                if (at[j] < 0) continue;
-#pragma unroll
-                for (int i = 0; i < WIDE; ++i) sum[i] = fmaf(w[j], y[j][i], sum[i]);
-            }
-        }
-        if (p.residual != nullptr) {
-            float r[WIDE];
-            load_values<DT, DVEC, WIDE>(
-                static_cast<const uint8_t *>(p.residual) + t * p.ld_r * Value<DT>::BYTES, c, n, r);
-#pragma unroll
-            for (int i = 0; i < WIDE; ++i) sum[i] += r[i];
-        }
-        store_values<DT, DVEC, WIDE>(static_cast<uint8_t *>(p.D) + t * p.ldd * Value<DT>::BYTES, c,
-                                     n, sum);
+    const int lane = threadIdx.x & (lanes - 1);
+    const int64_t all = p.tokens * chunks, step = static_cast<int64_t>(gridDim.x) * (blockDim.x / lanes);
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes; u < all;
+         u += step) {
+        const int64_t t = all <= UINT32_MAX ? static_cast<uint32_t>(u) / chunks : u / chunks;
+        const int64_t c0 = ((u - t * chunks) * C * lanes + lane) * WIDE, apart = lanes * WIDE;
+        if (c0 + (C - 1) * apart + WIDE <= p.N)
+            combine_pieces<YT, DT, YVEC, true, R, C>(p, t, c0, apart, dvec);
+        else if (c0 < p.N)
+            combine_pieces<YT, DT, YVEC, false, R, C>(p, t, c0, apart, dvec);
     }
 }
 
-// `warps` warps per token (1, 2, 4 or 8 of the CTA's eight).  A thread keeps its
-// share of eight dot products; the token's warps add theirs in a fixed order.
-template <int YT, int DT, bool YVEC, bool DVEC>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const __grid_constant__ CombineProblem p,
-                                                           int64_t pieces, int warps) {
+// A thread's C pieces of the gradients: its part of the dot products, and dY.
+template <int YT, int DT, bool YVEC, bool FULL, int R, int C>
+__device__ __forceinline__ void grad_pieces(const CombineProblem &p, const Choices<R> &ch, int64_t t,
+                                            int64_t c0, int64_t apart, bool dvec,
+                                            float (&dot)[R]) {
     using Y = Value<YT>;
     constexpr int WIDE = Y::PER_16;
-    __shared__ float parts[8][kRowsAhead];
+    uint4 q[R][C];
+    int n[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t left = p.N - (c0 + c * apart);
+        n[c] = FULL || left >= WIDE ? WIDE : (left > 0 ? static_cast<int>(left) : 0);
+    }
+    if (p.dweights != nullptr) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                q[j][c] = make_uint4(0, 0, 0, 0);
+                if (ch.at[j] >= 0)
+                    q[j][c] = load_piece<YT, YVEC, FULL>(p.Y, ch.at[j] * p.ldy, c0 + c * apart, n[c]);
+            }
+        }
+    }
+    float d[C][WIDE];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        load_values<DT, FULL, WIDE>(p.D, t * p.ldd, c0 + c * apart, n[c], dvec, d[c]);
+    if (p.dY != nullptr) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (ch.at[j] < 0) continue;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float g[WIDE];
+#pragma unroll
+                for (int i = 0; i < WIDE; ++i) g[i] = ch.w[j] * d[c][i];
+                store_values<YT, FULL, WIDE>(p.dY, ch.at[j] * p.ld_dy, c0 + c * apart, n[c], YVEC, g);
+            }
+        }
+    }
+    if (p.dweights != nullptr) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (ch.at[j] < 0) continue;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float y[WIDE];
+                Y::unpack(q[j][c], y);
+#pragma unroll
+                for (int i = 0; i < WIDE; ++i) dot[j] = fmaf(d[c][i], y[i], dot[j]);
+            }
+        }
+    }
+}
+
+// `lanes` threads per token (a power of two, at most the CTA's).  A thread keeps
+// its share of R dot products; they are added in a fixed order.
+template <int YT, int DT, bool YVEC, int R>
+__global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const __grid_constant__ CombineProblem p,
+                                                           int lanes, bool dvec) {
+    constexpr int WIDE = Value<YT>::PER_16, C = pieces_of(R);
+    __shared__ float parts[kGradThreads / 32][R];
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int in_token = warp % warps, per_cta = 8 / warps;
-    const int64_t ctas = (p.tokens + per_cta - 1) / per_cta;
+    const int lane = threadIdx.x & (lanes - 1), per_cta = kGradThreads / lanes;
+    const int warp = threadIdx.x / 32, warps = lanes / 32;  // warps of a token (0: part of one)
+    const int64_t ctas = (p.tokens + per_cta - 1) / per_cta, apart = lanes * WIDE;
     for (int64_t b = blockIdx.x; b < ctas; b += gridDim.x) {
-        const int64_t t = b * per_cta + warp / warps;
-        for (int64_t j0 = 0; j0 < p.k; j0 += kRowsAhead) {
-            int32_t at[kRowsAhead];
-            float w[kRowsAhead], dot[kRowsAhead] = {};
-#pragma unroll
-            for (int j = 0; j < kRowsAhead; ++j) {
-                const bool there = t < p.tokens && j0 + j < p.k;
-                const int64_t r = t * p.k + j0 + j;
-                at[j] = there ? __ldg(p.position + r) : -1;
-                w[j] = there && p.weights != nullptr ? __ldg(p.weights + r) : 1.f;
-                if (at[j] < 0 || at[j] >= p.rows_y) at[j] = -1;
-            }
-            for (int64_t v = in_token * 32 + lane; t < p.tokens && v < pieces; v += warps * 32) {
-                const int64_t c = v * WIDE;
-                const int n = p.N - c < WIDE ? static_cast<int>(p.N - c) : WIDE;
-                float d[WIDE];
-                load_values<DT, DVEC, WIDE>(
-                    static_cast<const uint8_t *>(p.D) + t * p.ldd * Value<DT>::BYTES, c, n, d);
-                if (p.dweights != nullptr) {
-                    float y[kRowsAhead][WIDE];
-#pragma unroll
-                    for (int j = 0; j < kRowsAhead; ++j)
-                        if (at[j] >= 0)
-                            load_piece<YT, YVEC>(
-                                static_cast<const uint8_t *>(p.Y) + at[j] * p.ldy * Y::BYTES, c, n, y[j]);
-#pragma unroll
-                    for (int j = 0; j < kRowsAhead; ++j) {
-                        if (at[j] < 0) continue;
-#pragma unroll
-                        for (int i = 0; i < WIDE; ++i) dot[j] = fmaf(d[i], y[j][i], dot[j]);
-                    }
-                }
-                if (p.dY != nullptr) {
-#pragma unroll
-                    for (int j = 0; j < kRowsAhead; ++j) {
-                        if (at[j] < 0) continue;
-                        float g[WIDE];
-#pragma unroll
-                        for (int i = 0; i < WIDE; ++i) g[i] = w[j] * d[i];
-                        store_values<YT, YVEC, WIDE>(
-                            static_cast<uint8_t *>(p.dY) + at[j] * p.ld_dy * Y::BYTES, c, n, g);
-                    }
+        const int64_t t = b * per_cta + threadIdx.x / lanes;
+        for (int64_t j0 = 0; j0 < p.k; j0 += R) {
+            const Choices<R> ch(p, t, j0);
+            float dot[R] = {};
+            if (t < p.tokens) {
+                for (int64_t c0 = lane * WIDE; c0 < p.N; c0 += C * apart) {
+                    if (c0 + (C - 1) * apart + WIDE <= p.N)
+                        grad_pieces<YT, DT, YVEC, true, R, C>(p, ch, t, c0, apart, dvec, dot);
+                    else
+                        grad_pieces<YT, DT, YVEC, false, R, C>(p, ch, t, c0, apart, dvec, dot);
                 }
             }
             if (p.dweights == nullptr) continue;
+            for (int s = (lanes < 32 ? lanes : 32) / 2; s > 0; s >>= 1) {
 #pragma unroll
-            for (int j = 0; j < kRowsAhead; ++j) {
-#pragma unroll
-                for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
+                for (int j = 0; j < R; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
             }
             if (warps > 1) {
                 __syncthreads();  // (the parts of the step before have been read)
-                if (lane == 0) {
+                if (lane % 32 == 0) {
 #pragma unroll
-                    for (int j = 0; j < kRowsAhead; ++j) parts[warp][j] = dot[j];
+                    for (int j = 0; j < R; ++j) parts[warp][j] = dot[j];
                 }
                 __syncthreads();
-                if (in_token == 0) {
+                if (lane == 0) {
                     for (int s = 1; s < warps; ++s) {
 #pragma unroll
-                        for (int j = 0; j < kRowsAhead; ++j) dot[j] += parts[warp + s][j];
+                        for (int j = 0; j < R; ++j) dot[j] += parts[warp + s][j];
                     }
                 }
             }
-            if (in_token == 0 && t < p.tokens) {
+            if (lane == 0 && t < p.tokens) {
 #pragma unroll
-                for (int j = 0; j < kRowsAhead; ++j)
-                    if (lane == j && j0 + j < p.k)
-                        p.dweights[t * p.k + j0 + j] = at[j] >= 0 ? dot[j] : 0.f;
+                for (int j = 0; j < R; ++j)
+                    if (j0 + j < p.k) p.dweights[t * p.k + j0 + j] = ch.at[j] >= 0 ? dot[j] : 0.f;
             }
         }
     }
@@ -215,64 +232,89 @@ cudaError_t launch(K kernel, int64_t ctas, int threads, cudaStream_t stream, A..
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int YT, int DT>
+// The power of two at or above n, at most `most`.
+int power_of_2(int64_t n, int most) {
+    int v = 1;
+    while (v < n && v < most) v *= 2;
+    return v;
+}
+
+template <int YT, int DT, int R>
 cudaError_t combine_as(const CombineProblem &p, cudaStream_t stream) {
     using Y = Value<YT>;
     using D = Value<DT>;
-    const int64_t pieces = (p.N + Y::PER_16 - 1) / Y::PER_16;
-    const int64_t threads = p.tokens * pieces;
+    const int64_t pieces = (p.N + Y::PER_16 - 1) / Y::PER_16, per_thread = pieces_of(R);
+    const int lanes = power_of_2((pieces + per_thread - 1) / per_thread, 32);
+    const int64_t chunks = (pieces + lanes * per_thread - 1) / (lanes * per_thread);
+    const int64_t threads = p.tokens * chunks * lanes;
     // few rows: small CTAs, so that every SM has one
-    const int cta = threads < 152 * 256 ? 64 : 256;
+    const int cta = threads < int64_t(sm_count()) * 256 ? 64 : 256;
     const int64_t ctas = (threads + cta - 1) / cta;
     const bool yv = rows_on_16(p.Y, p.ldy, Y::BYTES);
     const bool dv = rows_on_16(p.D, p.ldd, D::BYTES) &&
                     (p.residual == nullptr || rows_on_16(p.residual, p.ld_r, D::BYTES));
-    if (yv)
-        return dv ? launch(combine_kernel<YT, DT, true, true>, ctas, cta, stream, p, pieces)
-                  : launch(combine_kernel<YT, DT, true, false>, ctas, cta, stream, p, pieces);
-    return dv ? launch(combine_kernel<YT, DT, false, true>, ctas, cta, stream, p, pieces)
-              : launch(combine_kernel<YT, DT, false, false>, ctas, cta, stream, p, pieces);
+    const uint32_t n = static_cast<uint32_t>(chunks);
+    return yv ? launch(combine_kernel<YT, DT, true, R>, ctas, cta, stream, p, lanes, n, dv)
+              : launch(combine_kernel<YT, DT, false, R>, ctas, cta, stream, p, lanes, n, dv);
 }
 
-template <int YT, int DT>
+template <int YT, int DT, int R>
 cudaError_t combine_grad_as(const CombineProblem &p, cudaStream_t stream) {
     using Y = Value<YT>;
     using D = Value<DT>;
-    const int64_t pieces = (p.N + Y::PER_16 - 1) / Y::PER_16;
-    // two steps per thread at most, up to eight warps
-    int warps = 1;
-    while (warps < 8 && warps * 64 < pieces) warps *= 2;
-    const int64_t ctas = (p.tokens + 8 / warps - 1) / (8 / warps);
+    const int64_t pieces = (p.N + Y::PER_16 - 1) / Y::PER_16, per_thread = pieces_of(R);
+    // two steps per thread, up to a CTA per token
+    const int lanes = power_of_2((pieces + 2 * per_thread - 1) / (2 * per_thread), kGradThreads);
+    const int64_t ctas = (p.tokens + kGradThreads / lanes - 1) / (kGradThreads / lanes);
     const bool yv = (p.dweights == nullptr || rows_on_16(p.Y, p.ldy, Y::BYTES)) &&
                     (p.dY == nullptr || rows_on_16(p.dY, p.ld_dy, Y::BYTES));
     const bool dv = rows_on_16(p.D, p.ldd, D::BYTES);
-    if (yv)
-        return dv ? launch(combine_grad_kernel<YT, DT, true, true>, ctas, 256, stream, p, pieces, warps)
-                  : launch(combine_grad_kernel<YT, DT, true, false>, ctas, 256, stream, p, pieces, warps);
-    return dv ? launch(combine_grad_kernel<YT, DT, false, true>, ctas, 256, stream, p, pieces, warps)
-              : launch(combine_grad_kernel<YT, DT, false, false>, ctas, 256, stream, p, pieces, warps);
+    const int n = kGradThreads;
+    return yv ? launch(combine_grad_kernel<YT, DT, true, R>, ctas, n, stream, p, lanes, dv)
+              : launch(combine_grad_kernel<YT, DT, false, R>, ctas, n, stream, p, lanes, dv);
+}
+
+template <int YT, int DT>
+cudaError_t combine_rows(const CombineProblem &p, cudaStream_t stream) {
+    if (p.k <= 1) return combine_as<YT, DT, 1>(p, stream);
+    if (p.k == 2) return combine_as<YT, DT, 2>(p, stream);
+    return p.k <= 4 ? combine_as<YT, DT, 4>(p, stream) : combine_as<YT, DT, 8>(p, stream);
+}
+template <int YT, int DT>
+cudaError_t combine_grad_rows(const CombineProblem &p, cudaStream_t stream) {
+    if (p.k <= 1) return combine_grad_as<YT, DT, 1>(p, stream);
+    if (p.k == 2) return combine_grad_as<YT, DT, 2>(p, stream);
+    return p.k <= 4 ? combine_grad_as<YT, DT, 4>(p, stream) : combine_grad_as<YT, DT, 8>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_combine(const CombineProblem &p, cudaStream_t stream, const char **name) {
+    if (combine_bulk_eligible(p, false)) {
+        *name = "combine<bulk>";
+        return launch_combine_bulk(p, false, stream);
+    }
     *name = "combine";
-    if (p.y_type == kOutF32) return combine_as<kOutF32, kOutF32>(p, stream);
+    if (p.y_type == kOutF32) return combine_rows<kOutF32, kOutF32>(p, stream);
     if (p.y_type == kOutBf16)
-        return p.d_type == kOutF32 ? combine_as<kOutBf16, kOutF32>(p, stream)
-                                   : combine_as<kOutBf16, kOutBf16>(p, stream);
-    return p.d_type == kOutF32 ? combine_as<kOutF16, kOutF32>(p, stream)
-                               : combine_as<kOutF16, kOutF16>(p, stream);
+        return p.d_type == kOutF32 ? combine_rows<kOutBf16, kOutF32>(p, stream)
+                                   : combine_rows<kOutBf16, kOutBf16>(p, stream);
+    return p.d_type == kOutF32 ? combine_rows<kOutF16, kOutF32>(p, stream)
+                               : combine_rows<kOutF16, kOutF16>(p, stream);
 }
 
 cudaError_t launch_combine_grad(const CombineProblem &p, cudaStream_t stream, const char **name) {
+    if (combine_bulk_eligible(p, true)) {
+        *name = "combine_grad<bulk>";
+        return launch_combine_bulk(p, true, stream);
+    }
     *name = "combine_grad";
-    if (p.y_type == kOutF32) return combine_grad_as<kOutF32, kOutF32>(p, stream);
+    if (p.y_type == kOutF32) return combine_grad_rows<kOutF32, kOutF32>(p, stream);
     if (p.y_type == kOutBf16)
-        return p.d_type == kOutF32 ? combine_grad_as<kOutBf16, kOutF32>(p, stream)
-                                   : combine_grad_as<kOutBf16, kOutBf16>(p, stream);
-    return p.d_type == kOutF32 ? combine_grad_as<kOutF16, kOutF32>(p, stream)
-                               : combine_grad_as<kOutF16, kOutF16>(p, stream);
+        return p.d_type == kOutF32 ? combine_grad_rows<kOutBf16, kOutF32>(p, stream)
+                                   : combine_grad_rows<kOutBf16, kOutBf16>(p, stream);
+    return p.d_type == kOutF32 ? combine_grad_rows<kOutF16, kOutF32>(p, stream)
+                               : combine_grad_rows<kOutF16, kOutF16>(p, stream);
 }
 
 }  // namespace gemm

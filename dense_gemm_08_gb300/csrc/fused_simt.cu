@@ -14,6 +14,7 @@
 #include <atomic>
 
 #include "fused.cuh"
+#include "mixture.h"
 #include "values.cuh"
 
 namespace gemm {
@@ -313,18 +314,6 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float *part, int
     }
 }
 
-int sm_count() {
-    static std::atomic<int> counts[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    int n = counts[dev].load();
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
-        counts[dev].store(n);
-    }
-    return n;
-}
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <typename K, typename... A>
@@ -411,6 +400,18 @@ cudaError_t fused_of(const FusedProblem &p, cudaStream_t stream, const char **na
 }
 
 }  // namespace
+
+int sm_count() {
+    static std::atomic<int> counts[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    int n = counts[dev].load();
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
+        counts[dev].store(n);
+    }
+    return n;
+}
 
 cudaError_t launch_column_sums(const float *part, int64_t blocks, int64_t N, float *dbias,
                                cudaStream_t stream) {

@@ -15,6 +15,9 @@ constexpr int kMaxExperts = 1024, kMaxChoices = 32, kMaxExpertGroups = 32;
 
 enum : int { kSoftmax = 0, kSigmoid = 1 };  // = gemm_score_t
 
+// SMs of the current device (1 if that cannot be asked).
+int sm_count();
+
 struct RouteProblem {
     int64_t tokens;
     int experts, k;
@@ -53,5 +56,7 @@ struct CombineProblem {
 };
 cudaError_t launch_combine(const CombineProblem &p, cudaStream_t stream, const char **name);
 cudaError_t launch_combine_grad(const CombineProblem &p, cudaStream_t stream, const char **name);
+// Reads and clears the combination's device status word (after a sync).
+cudaError_t combine_read_and_clear_status(cudaStream_t stream, int *status);
 
 }  // namespace gemm

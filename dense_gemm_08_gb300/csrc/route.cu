@@ -1,19 +1,25 @@
 // route.cu -- the experts of each token and their weights, and the gradient of
 // the weights with respect to the logits (the formulas stand in include/gemm.h).
 //
-// A warp per token; lane l holds the experts l * ept .. l * ept + ept - 1, so
-// that among equal values the lowest lane, and in it the lowest register, is
-// the lowest index.  The k largest come one after another: each lane keeps its
-// best value as an integer of the same order, one redux finds the warp's
-// largest and one ballot the lane; that lane drops it and looks for its next.
+// A warp per token; lane l holds the experts l * ept .. l * ept + ept - 1, and
+// values are compared as integers of the same order.  The k largest:
+//   1. a lower bound of the k-th largest: the k-th largest of the lanes' own
+//      largest values (each lane counts, from shared memory, how many lanes have at
+//      least its own);
+//   2. the values that reach it, some k + 1 to k + 3 of them, are dealt out to the
+//      lanes, one each; a lane counts those that come before its own: its place.
+// No step waits on a chain of shuffles (two sorts across the lanes, or k rounds of
+// one maximum each, took twice the time).  Where more than 32 values reach the
+// bound (a row of equal logits) they are taken one after another.
 //
 // The choice must not depend on how FP32 rounds.  Without a bias the order is
-// the logits' own and nothing is rounded.  With one (and for group scores of two
-// terms), c is computed in FP32 together with a bound of its error; wherever two
-// values that a decision compares are closer than that, the token is chosen
-// again in 64 bits.  That is 0.3 % of the tokens for 256 experts with sigmoid
-// scores of N(0, 1.5^2) logits (FP64 runs at 1/64 of the FP32 rate: all tokens in
-// FP64 would take some hundred times the kernel's time).
+// the logits' own and nothing is rounded.  With one, c is computed in FP32 together
+// with a bound of its error; the candidates are all that could be among the k
+// largest, and where two that are next to each other are closer than that, the
+// candidates (one per lane) are compared again in 64 bits: 0.3 % of the tokens for
+// 256 experts with sigmoid scores of N(0, 1.5^2) logits.  Group scores of two
+// rounded terms that are too close are rarer; then the whole token is chosen again
+// in 64 bits.  (FP64 runs at 1/64 of the FP32 rate.)
 #include <type_traits>
 
 #include "mixture.h"
@@ -25,34 +31,34 @@ namespace {
 constexpr int kWarps = 4;  // tokens per CTA
 constexpr uint32_t kAll = 0xffffffffu;
 
-// Integers in the order of the values, 0 for "not there" (no value maps to it
-// but -infinity, which is not there either); a NaN is the largest.
+// Integers in the order of the values, 0 for -infinity ("not there"); a NaN is the
+// largest.  Adding 0 makes -0 a 0 and every NaN the one with all bits but the sign.
 template <typename F>
 struct Order;
 template <>
 struct Order<float> {
     using Key = uint32_t;
     static __device__ __forceinline__ Key of(float v) {
-        if (isnan(v)) return 0xffffffffu;
-        const uint32_t b = __float_as_uint(v + 0.f);  // -0 becomes 0
-        const Key k = b >> 31 ? ~b : b | 0x80000000u;
-        return v == -INFINITY ? 0u : k;
+        const int b = __float_as_int(v + 0.f);
+        return static_cast<Key>(b ^ ((b >> 31) | INT32_MIN)) - 0x007fffffu;
     }
-    static __device__ __forceinline__ float value(Key k) {  // (NaN: some NaN)
-        return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
+    static __device__ __forceinline__ float value(Key k) {
+        const uint32_t b = k + 0x007fffffu;
+        return __uint_as_float(b >> 31 ? b & 0x7fffffffu : ~b);
     }
     static __device__ __forceinline__ Key warp_max(Key k) { return __reduce_max_sync(kAll, k); }
+    static constexpr Key NAN_KEY = 0xff800000u;
 };
 template <>
 struct Order<double> {
     using Key = unsigned long long;
     static __device__ __forceinline__ Key of(double v) {
-        if (isnan(v)) return ~0ull;
+        if (isnan(v)) return NAN_KEY;
         const Key b = static_cast<Key>(__double_as_longlong(v + 0.0));
         const Key k = b >> 63 ? ~b : b | (1ull << 63);
         return v == -INFINITY ? 0ull : k;
     }
-    static __device__ __forceinline__ double value(Key k) {
+    static __device__ __forceinline__ double value(Key k) {  // (not of a NaN's)
         return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
     }
     static __device__ __forceinline__ Key warp_max(Key k) {
@@ -63,26 +69,31 @@ struct Order<double> {
         }
         return k;
     }
+    static constexpr Key NAN_KEY = ~0ull;
 };
 
+// The lanes that n values take, as a power of two.
+__device__ __forceinline__ int lanes_of(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+// Sums and maxima over the warp (NaNs do not count), or its first `width` lanes.
 template <typename F>
-__device__ __forceinline__ F warp_sum(F v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+__device__ __forceinline__ F warp_sum(F v, int width = 32) {
+    for (int d = width / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
-template <typename F>
-__device__ __forceinline__ F warp_max(F v) {  // (NaNs do not count)
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const F o = __shfl_xor_sync(kAll, v, d);
-        v = o > v || isnan(v) ? o : v;
-    }
+__device__ __forceinline__ float warp_max(float v, int width = 32) {
+    for (int d = width / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
     return v;
 }
 
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
+// For the choice: the hardware's exponential (off by 2 + 1.2 |x| units of 2^-23) and
+// reciprocal (2 units; 0 past 2^126) in FP32.
+__device__ __forceinline__ float rough_exp(float x) { return __expf(x); }
+__device__ __forceinline__ double rough_exp(double x) { return exp(x); }
+__device__ __forceinline__ float rough_inverse(float x) { return __fdividef(1.f, x); }
+__device__ __forceinline__ double rough_inverse(double x) { return 1.0 / x; }
 
 // The two largest of both pairs (first >= second).
 template <typename Key>
@@ -128,8 +139,7 @@ __device__ __forceinline__ void softmax_stats(const float (&x)[VPT], F &m, F &z)
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) top = fmaxf(top, x[i]);
-    top = warp_max(top);
-    m = top;
+    m = warp_max(top);
     z = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -137,183 +147,321 @@ __device__ __forceinline__ void softmax_stats(const float (&x)[VPT], F &m, F &z)
     z = warp_sum(z);
 }
 
-// The token's choice: `mine` = lane j's expert (j < k), or -1.  In FP32 false
-// where a decision is too close to call.
+// A score for the choice, from the row's statistics (1 / z, or z itself if that is a NaN).
+template <typename F>
+__device__ __forceinline__ F score_of(const RouteProblem &p, float x, F m, F inv) {
+    if (p.score == kSigmoid) return rough_inverse(F(1) + rough_exp(-static_cast<F>(x)));
+    return isnan(inv) ? inv : rough_exp(static_cast<F>(x) - m) * inv;
+}
+
+// The k largest keys one after another: each time the warp's largest, and among
+// its equals the lowest number.  Lane r gets the r-th one's number (or -1).
 template <typename F, int VPT>
-__device__ __forceinline__ bool choose(const RouteProblem &p, const float (&x)[VPT], int ept, F m,
-                                       F z, int &mine) {
+__device__ __forceinline__ int in_rounds(const RouteProblem &p, int ept,
+                                         const typename Order<F>::Key (&key)[VPT], uint32_t out) {
     using Key = typename Order<F>::Key;
-    constexpr bool FAST = std::is_same<F, float>::value;
     const int lane = threadIdx.x % 32;
-    const bool biased = p.bias != nullptr;
-    const bool group_sums = p.groups > 1 && p.top == 2;
-    bool safe = true;
-    F most = 0;  // FP32: the largest s + |b|, which the error of c is in proportion to
-
-    // scores, and c as an ordered integer
-    Key key[VPT];
-    F s[VPT];
-    const F inv = z > 0 ? F(1) / z : F(0);  // (0: every expert is masked; NaN stays NaN below)
-    float b[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int e = lane * ept + i;
-        b[i] = biased && i < ept && e < p.experts ? __ldg(p.bias + e) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const bool masked = x[i] == -INFINITY;
-        s[i] = 0;
-        if ((biased || group_sums) && !masked) {
-            if (p.score == kSigmoid)
-                s[i] = F(1) / (F(1) + exp_of(-static_cast<F>(x[i])));
-            else
-                s[i] = isnan(z) ? z : exp_of(static_cast<F>(x[i]) - m) * inv;
-        }
-        if (biased) {
-            const F c = s[i] + static_cast<F>(b[i]);
-            key[i] = masked ? Key(0) : Order<F>::of(c);
-            if (FAST && !masked && key[i] != 0) {
-                const F size = s[i] + fabsf(b[i]);
-                most = size > most ? size : most;
-            }
-        } else {
-            key[i] = masked ? Key(0) : Order<F>::of(static_cast<F>(x[i]));
-        }
-    }
-    // Errors in FP32.  A score: expf and the division a few units of 2^-24, the
-    // sum z of a softmax at most 37 roundings, the rounding of x - m (it moves
-    // exp(x - m) by 2^-24 |x - m| of itself, at most 0.37 * 2^-24 of the largest
-    // score); altogether below 2^-18.7 of s + |b| for a softmax, 2^-21 for a
-    // sigmoid.  Two values differ for certain when they are twice that apart,
-    // sums of two of them four times.
-    F tol = 0;
-    if (FAST && biased) tol = warp_max(most) * (p.score == kSigmoid ? 0x1p-19f : 0x1p-17f);
-
-    uint32_t out = 0;  // bit i: expert i of this lane is out of the choice
-    if (p.groups > 1 && p.kept < p.groups) {
-        const int size = p.experts / p.groups;
-        Key g1 = 0, g2 = 0;  // lane g: group g's two largest
-        // what the groups are compared by: c, or s where a sum is wanted
-        auto by = [&](int i) -> Key {
-            if (biased || !group_sums) return key[i];
-            return x[i] == -INFINITY ? Key(0) : Order<F>::of(s[i]);
-        };
-        const int lanes = 32 / p.groups;  // of a group, when groups end with lanes
-        if (32 % p.groups == 0 && p.experts == 32 * ept) {
-            Key a1 = 0, a2 = 0;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (i < ept) merge_top(a1, a2, by(i), Key(0));
-            for (int d = lanes / 2; d > 0; d /= 2) {
-                const Key o1 = __shfl_xor_sync(kAll, a1, d), o2 = __shfl_xor_sync(kAll, a2, d);
-                merge_top(a1, a2, o1, o2);
-            }
-            g1 = __shfl_sync(kAll, a1, (lane * lanes) & 31);
-            g2 = __shfl_sync(kAll, a2, (lane * lanes) & 31);
-        } else {
-            for (int g = 0; g < p.groups; ++g) {
-                Key a1 = 0, a2 = 0;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int e = lane * ept + i;
-                    if (i < ept && e >= g * size && e < (g + 1) * size) merge_top(a1, a2, by(i), Key(0));
-                }
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) {
-                    const Key o1 = __shfl_xor_sync(kAll, a1, d), o2 = __shfl_xor_sync(kAll, a2, d);
-                    merge_top(a1, a2, o1, o2);
-                }
-                if (lane == g) g1 = a1, g2 = a2;
-            }
-        }
-        Key score = g1;
-        if (p.top == 2 && g2 != 0) {
-            score = Order<F>::of(Order<F>::value(g1) + Order<F>::value(g2));
-            if (g1 == ~Key(0) || g2 == ~Key(0)) score = ~Key(0);  // (a NaN among them)
-        }
-        if (lane >= p.groups) score = 0;
-        uint32_t kept = 0;
-        Key last = 0;
-        for (int r = 0; r < p.kept; ++r) {
-            const Key left = (kept >> lane) & 1u ? Key(0) : score;
-            const Key best = Order<F>::warp_max(left);
-            if (best == 0) break;
-            last = best;
-            kept |= 1u << (__ffs(__ballot_sync(kAll, left == best)) - 1);
-        }
-        if (FAST && (biased || group_sums)) {
-            const Key next = Order<F>::warp_max((kept >> lane) & 1u ? Key(0) : score);
-            if (next != 0) {
-                const F a = Order<F>::value(last), c = Order<F>::value(next);
-                // (without a bias scores are positive, and their errors relative:
-                // 2^-24 |x - m| <= 100 * 2^-24 more for a softmax)
-                const F near = biased ? 2 * tol
-                                      : a * (p.score == kSigmoid ? F(0x1p-18) : F(0x1p-15));
-                if (!(a - c > near) || (!biased && !(a > F(1e-30)))) safe = false;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (i < ept && !((kept >> ((lane * ept + i) / size & 31)) & 1u)) out |= 1u << i;
-    }
-    if (!safe) return false;
-
-    Key best = 0;
-    int at = 0;
+    int mine = -1, at = 0;
+    Key best;
     auto look = [&]() {
         best = 0;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
+        for (int i = 0; i < VPT; ++i)
             if (key[i] > best && !((out >> i) & 1u)) best = key[i], at = i;
-        }
     };
     look();
-    mine = -1;
-    Key before = 0;
-    int e_before = 0;
-    // (with a bias one more round: the first that is not chosen must not be too close)
-    const int rounds = FAST && biased ? p.k + 1 : p.k;
-    for (int r = 0; r < rounds; ++r) {
+    for (int r = 0; r < p.k; ++r) {
         const Key top = Order<F>::warp_max(best);
         if (top == 0) break;
         const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
         const int e = __shfl_sync(kAll, lane * ept + at, owner);
-        if (FAST && biased && r > 0) {
-            if (!(Order<F>::value(before) - Order<F>::value(top) > tol)) {
-                // the same logit and the same bias are equal for certain
-                float xa = 0.f, xb = 0.f;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    if (lane * ept + i == e_before) xa = x[i];
-                    if (lane * ept + i == e) xb = x[i];
-                }
-                xa = __shfl_sync(kAll, xa, e_before / ept);
-                xb = __shfl_sync(kAll, xb, owner);
-                if (!(xa == xb && __ldg(p.bias + e_before) == __ldg(p.bias + e))) return false;
-            }
-        }
-        before = top;
-        e_before = e;
-        if (r < p.k && lane == r) mine = e;
+        if (lane == r) mine = e;
         if (lane == owner) {
             out |= 1u << at;
             look();
         }
     }
+    return mine;
+}
+
+// Scores and keys of the lane's experts, and which of them are out of the choice
+// because their group is (bit i of `out`).  most: the largest s + |b|, to which the
+// error of c in FP32 is in proportion.  FP32: false where two groups are too close.
+template <typename F, int VPT, bool VEC>
+__device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[VPT], int ept, F m,
+                                        F z, typename Order<F>::Key (&key)[VPT], uint32_t &out,
+                                        float &tol) {
+    using Key = typename Order<F>::Key;
+    constexpr bool FAST = std::is_same<F, float>::value;
+    const int lane = threadIdx.x % 32;
+    const bool biased = p.bias != nullptr;
+    const bool group_sums = p.groups > 1 && p.top == 2;
+    Key by[VPT];  // what groups are compared by: c, or s for a sum without a bias
+    out = 0;
+    tol = 0.f;
+    if (biased || group_sums) {
+        const F inv = z > 0 ? F(1) / z : (isnan(z) ? z : F(0));  // (0: every expert is masked)
+        float most = 0.f, b[VPT] = {};
+        if (biased) {
+            const float *from = p.bias + lane * ept;
+            if (VEC && VPT % 4 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < VPT / 4; ++i) {
+                    const float4 q = __ldg(reinterpret_cast<const float4 *>(from) + i);
+                    b[i * 4] = q.x, b[i * 4 + 1] = q.y, b[i * 4 + 2] = q.z, b[i * 4 + 3] = q.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (i < ept && lane * ept + i < p.experts) b[i] = __ldg(from + i);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const bool masked = x[i] == -INFINITY;
+            const F s = masked ? F(0) : score_of<F>(p, x[i], m, inv);
+            if (biased) {
+                key[i] = masked ? Key(0) : Order<F>::of(s + static_cast<F>(b[i]));
+                by[i] = key[i];
+                // (a bias of -infinity is a mask)
+                if (FAST && key[i] != 0) most = fmaxf(most, static_cast<float>(s) + fabsf(b[i]));
+            } else {
+                key[i] = Order<F>::of(static_cast<F>(x[i]));
+                by[i] = masked ? Key(0) : Order<F>::of(s);
+            }
+        }
+        // Errors in FP32, of the largest score or of s + |b|.  exp(-|x|) and exp(x - m)
+        // are off by 2 + 1.2 |x| units of 2^-23 of themselves and by the rounding of
+        // x - m: at most 1 unit of the largest score, as |x| exp(-|x|) < 0.4, or 3 where
+        // |x| is small; the reciprocal and the products 4; the sum z of a softmax 37 roundings;
+        // c itself 1.  Together below 2^-20 for a sigmoid, 2^-18 for a softmax.  Two
+        // values differ for certain when they are twice that apart, sums of two of
+        // them four times.
+        if (FAST && biased) tol = warp_max(most) * (p.score == kSigmoid ? 0x1p-19f : 0x1p-17f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) by[i] = key[i] = Order<F>::of(static_cast<F>(x[i]));
+    }
+    if (p.groups == 1 || p.kept == p.groups) return true;
+
+    // lane g: group g's largest two
+    Key g1 = 0, g2 = 0;
+    const int size = p.experts / p.groups;
+    const int lanes = 32 / p.groups;  // of a group, when groups end with lanes
+    const bool aligned = 32 % p.groups == 0 && p.experts == 32 * ept;
+    if (aligned) {
+        Key a1 = 0, a2 = 0;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i < ept) merge_top(a1, a2, by[i], Key(0));
+        for (int d = lanes / 2; d > 0; d /= 2) {
+            const Key o1 = __shfl_xor_sync(kAll, a1, d), o2 = __shfl_xor_sync(kAll, a2, d);
+            merge_top(a1, a2, o1, o2);
+        }
+        g1 = __shfl_sync(kAll, a1, (lane * lanes) & 31);
+        g2 = __shfl_sync(kAll, a2, (lane * lanes) & 31);
+    } else {
+        for (int g = 0; g < p.groups; ++g) {
+            Key a1 = 0, a2 = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int e = lane * ept + i;
+                if (i < ept && e >= g * size && e < (g + 1) * size) merge_top(a1, a2, by[i], Key(0));
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                const Key o1 = __shfl_xor_sync(kAll, a1, d), o2 = __shfl_xor_sync(kAll, a2, d);
+                merge_top(a1, a2, o1, o2);
+            }
+            if (lane == g) g1 = a1, g2 = a2;
+        }
+    }
+    Key score = g1;
+    if (p.top == 2 && g2 != 0)
+        score = g1 == Order<F>::NAN_KEY ? g1
+                                        : Order<F>::of(Order<F>::value(g1) + Order<F>::value(g2));
+    if (lane >= p.groups) score = 0;
+    // a group stays when fewer than groups_kept come before it
+    int before = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const Key o = __shfl_sync(kAll, score, g);
+        before += o > score || (o == score && g < lane) ? 1 : 0;
+    }
+    const uint32_t kept = __ballot_sync(kAll, score != 0 && before < p.kept);
+    const bool stays = (kept >> lane) & 1u;
+    if (aligned) {
+        out = (kept >> (lane / lanes)) & 1u ? 0u : ~0u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i < ept && !((kept >> ((lane * ept + i) / size & 31)) & 1u)) out |= 1u << i;
+    }
+    if constexpr (FAST) {
+        if (biased || group_sums) {
+            const Key next = Order<F>::warp_max(stays ? Key(0) : score);
+            const Key last = ~Order<F>::warp_max(stays ? ~score : Key(0));
+            if (next != 0) {
+                const float a = Order<F>::value(last), c = Order<F>::value(next);
+                // (without a bias scores are positive and their errors relative, 1.2 |x|
+                // units of 2^-23 with |x| below 80 among them: below 2^-16)
+                const float near = biased ? 2 * tol : a * 0x1p-14f;
+                if (!(a - c > near) || (!biased && !(a > 1e-30f))) return false;
+            }
+        }
+    }
     return true;
 }
 
-// Rarely called, and much larger than the FP32 form: a function of its own.
+// The whole choice in 64 bits: rarely called, and much larger than the FP32 form.
 template <int TYPE, int VPT, bool VEC>
 __device__ __noinline__ int choose_exactly(const RouteProblem &p, const void *row, int ept) {
-    float x[VPT];
+    float x[VPT], tol;
     load_row<TYPE, VPT, VEC>(p, row, ept, x);
     double m = 0, z = 0;
     if (p.score == kSoftmax) softmax_stats<double>(x, m, z);
-    int mine;
-    choose<double>(p, x, ept, m, z, mine);
-    return mine;
+    Order<double>::Key key[VPT];
+    uint32_t out;
+    keys_of<double, VPT, VEC>(p, x, ept, m, z, key, out, tol);
+    return in_rounds<double>(p, ept, key, out);
+}
+
+// The lane's candidate again in 64 bits: how many of the `total` come before it.
+template <int TYPE, int VPT, bool VEC>
+__device__ __noinline__ int place_exactly(const RouteProblem &p, const void *row, int ept, int total,
+                                          int e, float x) {
+    double m = 0, z = 0;
+    if (p.score == kSoftmax) {
+        float all[VPT];
+        load_row<TYPE, VPT, VEC>(p, row, ept, all);
+        softmax_stats<double>(all, m, z);
+    }
+    Order<double>::Key key = 0;
+    if (e >= 0) key = Order<double>::of(score_of<double>(p, x, m, 1.0 / z) + __ldg(p.bias + e));
+    int before = 0;
+    for (int i = 0; i < total; ++i) {
+        const Order<double>::Key o = __shfl_sync(kAll, key, i);
+        const int n = __shfl_sync(kAll, e, i);
+        before += o > key || (o == key && n < e) ? 1 : 0;
+    }
+    return before;
+}
+
+// Shared memory of a warp.
+template <int VPT>
+struct Slots {
+    __align__(16) uint32_t key[32 * VPT];  // of register i of lane l at l * VPT + i
+    __align__(16) unsigned long long candidate[32];
+    __align__(16) uint32_t best[32];
+    uint16_t at[32];
+    int number[32];
+    float logit[32];
+};
+
+// What a lane knows of the choice: an expert (or -1), its logit and its place.
+struct Choice {
+    int expert, place;
+    float logit;
+};
+
+// The token's choice in FP32; lanes below `width` may have one.  False where a
+// decision is too close to call and not among 32 candidates.
+template <int TYPE, int VPT, bool VEC>
+__device__ __forceinline__ bool choose(const RouteProblem &p, const void *row, const float (&x)[VPT],
+                                       int ept, float m, float z, Slots<VPT> &s, Choice &mine,
+                                       int &width) {
+    const int lane = threadIdx.x % 32;
+    const bool biased = p.bias != nullptr;
+    uint32_t key[VPT], out;
+    float tol;
+    if (!keys_of<float, VPT, VEC>(p, x, ept, m, z, key, out, tol)) return false;
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if ((out >> i) & 1u) key[i] = 0;
+        best = max(best, key[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; i += 4) {
+        if constexpr (VPT >= 4)
+            *reinterpret_cast<uint4 *>(s.key + lane * VPT + i) =
+                make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+        else
+            *reinterpret_cast<uint2 *>(s.key + lane * VPT) = make_uint2(key[0], key[1]);
+    }
+    uint32_t bound;
+    if (p.k == 1) {
+        bound = __reduce_max_sync(kAll, best);
+    } else {
+        s.best[lane] = best;
+        __syncwarp();
+        int as_large = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint4 o = reinterpret_cast<const uint4 *>(s.best)[q];
+            as_large += (o.x >= best) + (o.y >= best) + (o.z >= best) + (o.w >= best);
+        }
+        bound = __reduce_max_sync(kAll, as_large >= p.k ? best : 0u);
+    }
+    // (a value that only seems smaller than the bound may be larger)
+    if (biased && bound != 0) {
+        const float low = Order<float>::value(bound) - tol;
+        if (isnan(low)) return false;
+        bound = Order<float>::of(low);
+    }
+    if (bound == 0) bound = 1;
+    uint32_t mask = 0;  // this lane's candidates
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) mask |= key[i] >= bound ? 1u << i : 0u;
+    int total = 0;
+    for (uint32_t who; (who = __ballot_sync(kAll, mask != 0)) != 0; mask &= mask - 1) {
+        const int slot = total + __popc(who & ((1u << lane) - 1u));
+        if (mask != 0 && slot < 32) s.at[slot] = static_cast<uint16_t>(lane * VPT + __ffs(mask) - 1);
+        total += __popc(who);
+        if (total > 32) break;
+    }
+    if (total > 32) {
+        if (biased) return false;
+        mine.expert = in_rounds<float>(p, ept, key, 0u);
+        mine.place = lane;
+        mine.logit = mine.expert >= 0 ? Value<TYPE>::load(row, mine.expert) : 0.f;
+        width = 32;
+        return true;
+    }
+    __syncwarp();
+    // lane i: candidate i, and how many of the others come before it
+    uint32_t k32 = 0, at = 0;
+    if (lane < total) at = s.at[lane], k32 = s.key[at];
+    const unsigned long long cand =
+        lane < total ? static_cast<unsigned long long>(k32) << 32 | static_cast<uint32_t>(~at) : 0ull;
+    s.candidate[lane] = cand;
+    __syncwarp();
+    int place = 0;
+    for (int q = 0; q < total; q += 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(s.candidate + q);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s.candidate + q + 2);
+        place += (a.x > cand) + (a.y > cand) + (b.x > cand) + (b.y > cand);
+    }
+    const int e = lane < total ? static_cast<int>(at / VPT * ept + at % VPT) : -1;
+    float l = Order<float>::value(k32);  // (without a bias a key is a logit)
+    if (biased) {
+        l = e >= 0 ? Value<TYPE>::load(row, e) : 0.f;
+        if (e >= 0) s.best[place] = k32, s.number[place] = e, s.logit[place] = l;
+        __syncwarp();
+        // the candidates in order: too close to the next one, unless that has the
+        // same logit and the same bias (equal for certain)?
+        bool close = false;
+        if (lane < p.k && lane + 1 < total &&
+            !(Order<float>::value(s.best[lane]) - Order<float>::value(s.best[lane + 1]) > tol))
+            close = !(s.logit[lane] == s.logit[lane + 1] &&
+                      __ldg(p.bias + s.number[lane]) == __ldg(p.bias + s.number[lane + 1]));
+        if (__any_sync(kAll, close)) place = place_exactly<TYPE, VPT, VEC>(p, row, ept, total, e, l);
+    }
+    mine.expert = e;
+    mine.place = place;
+    mine.logit = l;
+    width = lanes_of(total);
+    __syncwarp();
+    return true;
 }
 
 // log of the logistic function, for scores that FP32 cannot hold
@@ -321,56 +469,77 @@ __device__ __forceinline__ float log_sigmoid(float x) {
     return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
 }
 
-// The lane's share of the chosen experts' scores (lanes with `has`): s_j / sum s.
-// Scores too small for FP32 keep their ratios.
-__device__ __forceinline__ float share(const RouteProblem &p, bool has, float x) {
+// The lane's share of the chosen experts' scores (lanes with `has`, all below
+// `width`): s_j / sum s.  Scores too small for FP32 keep their ratios.
+__device__ __forceinline__ float share(const RouteProblem &p, bool has, float x, int width) {
     if (p.score == kSoftmax) {
-        const float m = warp_max(has ? x : -INFINITY);
+        const float m = warp_max(has ? x : -INFINITY, width);
         const float e = has ? expf(x - m) : 0.f;
-        return e / warp_sum(e);
+        return __fdividef(e, warp_sum(e, width));
     }
-    const float s = has ? 1.f / (1.f + expf(-x)) : 0.f;
-    const float sum = warp_sum(s);
+    const float s = has ? __fdividef(1.f, 1.f + expf(-x)) : 0.f;
+    const float sum = __shfl_sync(kAll, warp_sum(s, width), 0);
     if (sum < 1e-30f) {
         const float l = has ? log_sigmoid(x) : -INFINITY;
-        const float m = warp_max(l);
+        const float m = warp_max(l, width);
         const float e = has ? expf(l - m) : 0.f;
-        return e / warp_sum(e);
+        return __fdividef(e, warp_sum(e, width));
     }
-    return s / sum;
+    return __fdividef(s, sum);
 }
 
 template <int TYPE, int VPT, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constant__ RouteProblem p) {
-    pdl_wait();
-    pdl_launch_dependents();
+__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 8 : VPT <= 16 ? 5 : 3)
+    route_kernel(const __grid_constant__ RouteProblem p) {
+    __shared__ Slots<VPT> slots[kWarps];
     const int lane = threadIdx.x % 32;
     const int ept = VEC ? VPT : (p.experts + 31) / 32;
-    for (int64_t t = blockIdx.x * int64_t(kWarps) + threadIdx.x / 32; t < p.tokens;
-         t += gridDim.x * int64_t(kWarps)) {
-        const void *row = static_cast<const uint8_t *>(p.logits) + t * p.ld * Value<TYPE>::BYTES;
+    const int64_t step = gridDim.x * int64_t(kWarps);
+    int64_t t = blockIdx.x * int64_t(kWarps) + threadIdx.x / 32;
+    auto row_of = [&](int64_t i) -> const void * {
+        return static_cast<const uint8_t *>(p.logits) + i * p.ld * Value<TYPE>::BYTES;
+    };
+    pdl_wait();
+    pdl_launch_dependents();
+    float next[VPT];  // the next token's logits, under way while this one is chosen
+    if (t < p.tokens) load_row<TYPE, VPT, VEC>(p, row_of(t), ept, next);
+    for (; t < p.tokens; t += step) {
         float x[VPT];
-        load_row<TYPE, VPT, VEC>(p, row, ept, x);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) x[i] = next[i];
+        const void *row = row_of(t);
+        if (t + step < p.tokens) load_row<TYPE, VPT, VEC>(p, row_of(t + step), ept, next);
         const bool sums = p.bias != nullptr || (p.groups > 1 && p.top == 2);
         float m = 0.f, z = 0.f;
         if (p.score == kSoftmax && (sums || !p.renorm)) softmax_stats<float>(x, m, z);
-        int mine;
-        if (!choose<float>(p, x, ept, m, z, mine))
-            mine = choose_exactly<TYPE, VPT, VEC>(p, row, ept);
-        const bool has = lane < p.k && mine >= 0;
-        const float mx = has ? Value<TYPE>::load(row, mine) : 0.f;
+        Choice mine;
+        int width;
+        if (!choose<TYPE, VPT, VEC>(p, row, x, ept, m, z, slots[threadIdx.x / 32], mine, width)) {
+            mine.expert = choose_exactly<TYPE, VPT, VEC>(p, row, ept);
+            mine.place = lane;
+            mine.logit = mine.expert >= 0 ? Value<TYPE>::load(row, mine.expert) : 0.f;
+            width = 32;
+        }
+        const bool has = mine.expert >= 0 && mine.place < p.k;
         float w;
         if (p.renorm) {
-            w = share(p, has, mx);
+            w = share(p, has, mine.logit, width);
             if (isnan(z)) w = z;  // (with a bias, other experts than the NaN may be chosen)
         } else if (p.score == kSigmoid) {
-            w = 1.f / (1.f + expf(-mx));
+            w = __fdividef(1.f, 1.f + expf(-mine.logit));
         } else {
-            w = expf(mx - m) / z;
+            w = __fdividef(expf(mine.logit - m), z);
         }
-        if (lane < p.k) {
-            p.chosen[t * p.k + lane] = mine;
-            p.weights[t * p.k + lane] = has ? w * p.scale : 0.f;
+        int32_t *chosen = p.chosen + t * p.k;
+        float *weights = p.weights + t * p.k;
+        if (has) {
+            chosen[mine.place] = mine.expert;
+            weights[mine.place] = w * p.scale;
+        }
+        const int count = __popc(__ballot_sync(kAll, has));
+        if (lane >= count && lane < p.k) {  // fewer than k can be chosen
+            chosen[lane] = -1;
+            weights[lane] = 0.f;
         }
     }
 }
@@ -399,7 +568,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
         const float dw = has ? p.dweights[t * p.k + lane] * p.scale : 0.f;
         float dx;
         if (p.renorm) {
-            const float q = share(p, has, x);
+            const float q = share(p, has, x, lanes_of(p.k));
             dx = q * (dw - warp_sum(has ? q * dw : 0.f));
             if (p.score == kSigmoid) dx *= 1.f / (1.f + expf(x));
             for (int i = lane; i < p.experts; i += 32) mine[i] = 0.f;
@@ -441,13 +610,16 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
     }
 }
 
+// At most `most` CTAs (those of a pass of the whole GPU), whose warps then take
+// several tokens each.
 template <typename K>
-cudaError_t launch(K kernel, const RouteProblem &p, size_t smem, cudaStream_t stream) {
+cudaError_t launch(K kernel, const RouteProblem &p, size_t smem, int64_t most,
+                   cudaStream_t stream) {
     cudaLaunchAttribute attr;
     set_pdl_attribute(&attr);
     cudaLaunchConfig_t cfg = {};
     const int64_t ctas = (p.tokens + kWarps - 1) / kWarps;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas < (1 << 20) ? ctas : (1 << 20)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -460,8 +632,9 @@ template <int TYPE, int VPT>
 cudaError_t route_as(const RouteProblem &p, cudaStream_t stream) {
     // whole lanes of 16-byte (or smaller, whole) pieces
     const bool vec = p.experts == 32 * VPT && rows_on_16(p.logits, p.ld, Value<TYPE>::BYTES);
-    return vec ? launch(route_kernel<TYPE, VPT, true>, p, 0, stream)
-               : launch(route_kernel<TYPE, VPT, false>, p, 0, stream);
+    const int64_t most = int64_t(sm_count()) * (VPT <= 8 ? 8 : VPT <= 16 ? 5 : 3);
+    return vec ? launch(route_kernel<TYPE, VPT, true>, p, 0, most, stream)
+               : launch(route_kernel<TYPE, VPT, false>, p, 0, most, stream);
 }
 
 template <int TYPE>
@@ -479,8 +652,8 @@ cudaError_t route_grad_of(const RouteProblem &p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>((p.experts + 7) / 8 * 8) * kWarps * sizeof(float);
     const bool vec = p.experts % Value<TYPE>::PER_16 == 0 &&
                      rows_on_16(p.dlogits, p.ld_d, Value<TYPE>::BYTES);
-    return vec ? launch(route_grad_kernel<TYPE, true>, p, smem, stream)
-               : launch(route_grad_kernel<TYPE, false>, p, smem, stream);
+    return vec ? launch(route_grad_kernel<TYPE, true>, p, smem, 1 << 20, stream)
+               : launch(route_grad_kernel<TYPE, false>, p, smem, 1 << 20, stream);
 }
 
 }  // namespace

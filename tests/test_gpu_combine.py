@@ -226,3 +226,86 @@ def test_many_tokens(T, k, N):
     ref = (dD.double()[:, None] * Y.double()[at.long()]).sum(-1)
     size = (dD.double().abs()[:, None] * Y.double().abs()[at.long()]).sum(-1)
     assert ((dw.double() - ref).abs() <= size * (N / 32 + 24) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("y,d", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"),
+                                 ("f16", "f32")])
+@pytest.mark.parametrize("T,k,N", [(3400, 1, 8192), (1701, 2, 9001), (3300, 3, 2575), (900, 5, 8200), (1777, 8, 2100),
+                                   (1640, 11, 2055), (700, 20, 2080), (7001, 2, 2049), (701, 8, 1056), (1500, 4, 515)])
+def test_large_batches(y, d, T, k, N):
+    """Rows by bulk copy: several runs of columns, sets of rows, odd ends, rows without a place."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    t, u = TORCH[y], TORCH[d]
+    ld = -(-N // 8) * 8
+
+    def normal(r, kind):
+        return torch.empty(r, ld, device="cuda", dtype=kind).normal_(generator=g)[:, :N]
+
+    Y, R = normal(T * k, t), normal(T, u)
+    at = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+    at[::7] = -1
+    at[3::50] = T * k + 5
+    at = at.view(T, k)
+    inside = (at >= 0) & (at < T * k)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    w[~inside] = float("nan")
+    rows = Y.double()[at.long().clamp(0, T * k - 1)] * inside[..., None]
+    wd = torch.where(inside, w, torch.zeros_like(w)).double()
+    for weights, residual in ((w, R), (None, None)):
+        s = wd if weights is not None else inside.double()
+        ref, size = (rows * s[..., None]).sum(1), (rows.abs() * s[..., None]).sum(1)
+        if residual is not None:
+            ref, size = ref + R.double(), size + R.double().abs()
+        tol = size * (2 * k + 2) * 2.0 ** -24 + ref.abs() * HALF_STEP[d] * 1.001 + 2.0 ** -24
+        out = torch.full((T, ld + 8), 7.0, device="cuda", dtype=u)
+        got = lib.combine(Y, at, weights=weights, residual=residual, out=out[:, :N])
+        row = N * Y.element_size()
+        bulk = row >= (8192 if k < 4 else 4096) and row * k * T >= 48 << 20
+        assert lib.gemm_last_kernel() == ("combine<bulk>" if bulk else "combine")
+        assert ((got.double() - ref).abs() <= tol).all() and (out[:, N:] == 7.0).all()
+        odd = torch.empty(T, N + 1, device="cuda", dtype=u)[:, 1:]  # rows off 16 bytes
+        assert torch.equal(lib.combine(Y, at, weights=weights, residual=residual, out=odd), got)
+        if residual is not None:
+            over = R.clone()
+            assert torch.equal(lib.combine(Y, at, weights=w, residual=over, out=over), got)
+    dD = normal(T, u)
+    for weights in (w, None):
+        s = wd if weights is not None else inside.double()
+        buf = torch.full((T * k, ld), 7.0, device="cuda", dtype=t)
+        dY, dw = lib.combine_grad(dD, Y, at, weights=weights, out=buf[:, :N])
+        row = N * Y.element_size()
+        bulk = k >= 2 and row >= 2048 and row * k >= 8192 and row * k * T >= 16 << 20
+        assert lib.gemm_last_kernel() == ("combine_grad<bulk>" if bulk else "combine_grad")
+        want = torch.full((T * k, N), 7.0, device="cuda", dtype=torch.float64)
+        want[at[inside].long()] = (dD.double()[:, None] * s[..., None])[inside]
+        assert ((dY.double() - want).abs() <= want.abs() * HALF_STEP[y] * 1.001 + 2.0 ** -24).all()
+        assert (buf[:, N:] == 7.0).all()
+        ref = (dD.double()[:, None] * rows).sum(-1)
+        size = (dD.double().abs()[:, None] * rows.abs()).sum(-1)
+        # (a thread's share: at most N / 32 products and 8, then 5 shuffles and 8 warps)
+        assert ((dw.double() - ref).abs() <= size * (N / 32 + 8 + 16) * 2.0 ** -24).all()
+        only, none = lib.combine_grad(dD, Y, at, weights=weights, weight_grad=False)
+        assert none is None and torch.equal(only[at[inside].long()], dY[at[inside].long()])
+    assert lib.gemm_last_device_status() == lib.GEMM_OK
+
+
+def test_large_batches_on_streams_and_in_graphs():
+    T, k, N = 3200, 4, 2048
+    Y, at, w, R = make(T, k, N, "bf16", "bf16")
+    want = lib.combine(Y, at, weights=w, residual=R)
+    assert lib.gemm_last_kernel() == "combine<bulk>"
+    dY, dw = lib.combine_grad(R, Y, at, weights=w)
+    assert lib.gemm_last_kernel() == "combine_grad<bulk>"
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(3)]
+    got = [(lib.combine(Y, at, weights=w, residual=R, stream=s),
+            *lib.combine_grad(R, Y, at, weights=w, stream=s)) for s in sides]
+    torch.cuda.synchronize()
+    for a, b, c in got:
+        assert torch.equal(a, want) and torch.equal(b, dY) and torch.equal(c, dw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lib.combine(Y, at, weights=w, residual=R)
+        oY, ow = lib.combine_grad(R, Y, at, weights=w)
+    graph.replay()
+    assert torch.equal(out, want) and torch.equal(oY, dY) and torch.equal(ow, dw)

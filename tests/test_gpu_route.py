@@ -162,6 +162,16 @@ def test_nans_and_infinities_stay_in_their_row(score, groups):
         assert torch.isnan(w[3]).all()
 
 
+def test_every_nan_is_the_same():
+    """NaNs of either sign and any payload are chosen first, by their numbers."""
+    bits = np.array([0x7f800001, 0xff800001, 0x7fc00000, 0xffffffff, 0xffc12345], dtype=np.uint32)
+    x = np.zeros((5, 40), dtype=np.float32)
+    x[:, 7:40:8] = bits.view(np.float32)[:5][None].repeat(5, 0)[:, :5]
+    chosen, w = lib.route(torch.from_numpy(x).cuda(), 6, score=SIG, renormalize=False)
+    assert chosen.cpu().tolist() == [[7, 15, 23, 31, 39, 0]] * 5
+    assert torch.isnan(w[:, :5]).all() and (w[:, 5] == 0.5).all()
+
+
 def test_many_tokens_and_every_row_once():
     """More tokens than one pass of the grid at once, the last ones too."""
     T, E, k = 70001, 16, 3
