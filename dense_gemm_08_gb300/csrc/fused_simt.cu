@@ -1,17 +1,20 @@
-// fused_simt.cu -- the fused products on the CUDA cores: FP32 inputs (no TF32),
-// and 16-bit inputs that TMA cannot describe.
+// fused_simt.cu -- the fused products on the CUDA cores.
 //
-// Tiles of 128 x 128 (8 x 8 sums per thread) or, where those would not fill the
-// SMs, 64 x 64 (4 x 4); slices of 16 of K come through registers into two
-// shared-memory buffers, sums are paired FMAs.  Few 64 x 64 tiles: K is split
-// over a cluster, whose CTAs add each other's sums through distributed shared
-// memory, each for its share of the tile's rows and in the order of the pieces.
-// The tile then lies in shared memory, and a thread finishes one of its columns:
-// bias, activation, residual, the value before the activation, column sums.
+// Large FP32 products (no TF32): the library's FP32 product (launch_f32) into D --
+// into the value before the activation where that is kept -- and one pass over it
+// (fused_finish_kernel: bias, activation, residual, slopes, column sums).
 //
-// Up to four rows of A and a K-contiguous B: warps stream B's columns once
-// (fused_rows_kernel).
+// Small FP32 products, and 16-bit inputs that TMA cannot describe: tiles of 64 x 64 (4 x 4 sums per thread);
+// slices of 16 of K come through registers into two shared-memory buffers, sums are
+// paired FMAs.  Few tiles: K is split over a cluster, whose CTAs add each other's
+// sums through distributed shared memory, each for its share of the tile's rows and
+// in the order of the pieces.  The tile then lies in shared memory, and a thread
+// finishes one of its columns.
+//
+// A row or two of A (FP32: four) and a K-contiguous B: warps stream B's columns
+// once (fused_rows_kernel).
 #include <atomic>
+#include <type_traits>
 
 #include "fused.cuh"
 #include "mixture.h"
@@ -23,19 +26,19 @@ namespace {
 constexpr int BK = 16;
 constexpr int THREADS = 256;
 
+// What follows the sum of one value; D's value before rounding.
 template <int TYPE>
 __device__ __forceinline__ float finish(const FusedProblem &p, float sum, int64_t r, int64_t c,
                                         float bias) {
-    constexpr bool FAST = TYPE != kOutF32;
     using V = Value<TYPE>;
     float d;
     if (p.grad) {
         d = p.alpha * sum;
-        if (p.act != kActNone) d *= fused_slope<FAST>(V::load(p.pre, r * p.ld_pre + c), p.act);
+        if (p.act != kActNone) d *= fused_slope(V::load(p.pre, r * p.ld_pre + c), p.act);
     } else {
         const float z = fmaf(p.alpha, sum, bias);
         if (p.pre != nullptr) V::store(p.pre, r * p.ld_pre + c, z);
-        d = fused_activation<FAST>(z, p.act);
+        d = fused_activation(z, p.act);
         if (p.residual != nullptr) d += V::load(p.residual, r * p.ld_r + c);
     }
     V::store(p.D, r * p.ldd + c, d);
@@ -61,25 +64,22 @@ __device__ __forceinline__ void fma_pair(float2 &acc, float2 a, float2 b) {
         : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
 }
 
-template <int T>
-struct Tile {
-    static constexpr int T_ = T;            // rows and columns of a tile
-    static constexpr int S = T / 16;        // and of a thread's block, 4 at a time
-    static constexpr int PITCH = T + 4;     // of a slice's rows
-    static constexpr int OUT = T + 1;       // of the finished tile's
-    static constexpr int LOADS = T * BK / THREADS;
-    static constexpr int SLICES = 4 * BK * PITCH;  // two buffers of A's and B's
-    static constexpr int FLOATS = SLICES > T * OUT ? SLICES : T * OUT;
-};
+constexpr int kTile = 64;             // rows and columns of a tile
+constexpr int kPitch = kTile + 4;     // of a slice's rows
+constexpr int kOutPitch = kTile + 1;  // of the finished tile's
+constexpr int kLoads = kTile * BK / THREADS;
+constexpr int kSliceFloats = 4 * BK * kPitch;  // two buffers of A's and B's
+constexpr int kTileFloats =
+    kSliceFloats > kTile * kOutPitch ? kSliceFloats : kTile * kOutPitch;
 
 // ks pieces of K per tile (cluster), blockIdx.x = tile * ks + piece.
-template <int TYPE, int T>
+template <int TYPE>
 __global__ void __launch_bounds__(THREADS)
     fused_tile_kernel(const __grid_constant__ FusedProblem p, int64_t tiles_n, int ks, float *part) {
     using V = Value<TYPE>;
-    using C = Tile<T>;
+    constexpr int T = kTile;
     extern __shared__ __align__(16) float smem[];
-    float *const sa = smem, *const sb = smem + 2 * BK * C::PITCH;
+    float *const sa = smem, *const sb = smem + 2 * BK * kPitch;
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     const int64_t tile = blockIdx.x / ks;
     const int piece = static_cast<int>(blockIdx.x % ks);
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(THREADS)
     pdl_launch_dependents();
 
     // the values of a slice that this thread brings: K fastest where K is contiguous
-    float ra[C::LOADS], rb[C::LOADS];
+    float ra[kLoads], rb[kLoads];
     auto where = [&](bool kmajor, int i, int &k, int &x) {
         const int v = tid + i * THREADS;
         k = kmajor ? v % BK : v / T;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(THREADS)
     auto fetch = [&](int64_t slice) {
         const int64_t k0 = slice * BK;
 #pragma unroll
-        for (int i = 0; i < C::LOADS; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             int k, x;
             where(p.a_kmajor, i, k, x);
             ra[i] = m0 + x < p.M && k0 + k < p.K
@@ -113,15 +113,15 @@ __global__ void __launch_bounds__(THREADS)
     };
     auto put = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < C::LOADS; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             int k, x;
             where(p.a_kmajor, i, k, x);
-            sa[(buf * BK + k) * C::PITCH + x] = ra[i];
+            sa[(buf * BK + k) * kPitch + x] = ra[i];
             where(p.b_kmajor, i, k, x);
-            sb[(buf * BK + k) * C::PITCH + x] = rb[i];
+            sb[(buf * BK + k) * kPitch + x] = rb[i];
         }
     };
-    float2 acc[C::S][C::S / 2] = {};
+    float2 acc[4][2] = {};
     if (first < end) {
         fetch(first);
         put(0);
@@ -132,20 +132,15 @@ __global__ void __launch_bounds__(THREADS)
         if (s + 1 < end) fetch(s + 1);
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
-            const float *a = sa + (buf * BK + k) * C::PITCH, *b = sb + (buf * BK + k) * C::PITCH;
-            float av[C::S];
-            float2 bv[C::S / 2];
+            const float *a = sa + (buf * BK + k) * kPitch, *b = sb + (buf * BK + k) * kPitch;
+            const float4 av = *reinterpret_cast<const float4 *>(a + ty * 4);
+            const float4 bv = *reinterpret_cast<const float4 *>(b + tx * 4);
+            const float ai[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
-            for (int h = 0; h < C::S / 4; ++h) {
-                const float4 q = *reinterpret_cast<const float4 *>(a + h * (T / 2) + ty * 4);
-                av[h * 4] = q.x, av[h * 4 + 1] = q.y, av[h * 4 + 2] = q.z, av[h * 4 + 3] = q.w;
-                const float4 u = *reinterpret_cast<const float4 *>(b + h * (T / 2) + tx * 4);
-                bv[h * 2] = make_float2(u.x, u.y), bv[h * 2 + 1] = make_float2(u.z, u.w);
+            for (int i = 0; i < 4; ++i) {
+                fma_pair(acc[i][0], make_float2(ai[i], ai[i]), make_float2(bv.x, bv.y));
+                fma_pair(acc[i][1], make_float2(ai[i], ai[i]), make_float2(bv.z, bv.w));
             }
-#pragma unroll
-            for (int i = 0; i < C::S; ++i)
-#pragma unroll
-                for (int j = 0; j < C::S / 2; ++j) fma_pair(acc[i][j], make_float2(av[i], av[i]), bv[j]);
         }
         if (s + 1 < end) put(buf ^ 1);
         __syncthreads();
@@ -153,14 +148,10 @@ __global__ void __launch_bounds__(THREADS)
 
     // the sums into shared memory, in place of the slices
 #pragma unroll
-    for (int i = 0; i < C::S; ++i)
-#pragma unroll
-        for (int j = 0; j < C::S / 2; ++j) {
-            float *to = smem + (i / 4 * (T / 2) + ty * 4 + i % 4) * C::OUT + j / 2 * (T / 2) + tx * 4 +
-                        j % 2 * 2;
-            to[0] = acc[i][j].x;
-            to[1] = acc[i][j].y;
-        }
+    for (int i = 0; i < 4; ++i) {
+        float *to = smem + (ty * 4 + i) * kOutPitch + tx * 4;
+        to[0] = acc[i][0].x, to[1] = acc[i][0].y, to[2] = acc[i][1].x, to[3] = acc[i][1].y;
+    }
     if (ks > 1)
         cluster_sync_all();
     else
@@ -176,9 +167,9 @@ __global__ void __launch_bounds__(THREADS)
         float sum = 0.f;
         if (ks > 1) {
             for (int q = 0; q < ks; ++q)
-                sum += ld_of_rank(base + static_cast<uint32_t>(r * C::OUT + col) * 4u, q);
+                sum += ld_of_rank(base + static_cast<uint32_t>(r * kOutPitch + col) * 4u, q);
         } else {
-            sum = smem[r * C::OUT + col];
+            sum = smem[r * kOutPitch + col];
         }
         if (inside && m0 + r < p.M) column += finish<TYPE>(p, sum, m0 + r, n0 + col, bias);
     }
@@ -198,14 +189,14 @@ __global__ void __launch_bounds__(THREADS)
 
 // ------------------------------------------------------------- few rows of A
 // D for up to ROWS rows of A and a K-contiguous B: `split` warps of a CTA share a
-// column's K, 16 bytes a lane and four loads of B in flight; their sums are added
+// column's K, 16 bytes a lane and eight loads of B in flight; their sums are added
 // in order.  B is read once, A comes from L1.
 constexpr int kRowsWarps = 8;
 template <int TYPE, int ROWS>
 __global__ void __launch_bounds__(32 * kRowsWarps)
     fused_rows_kernel(const __grid_constant__ FusedProblem p, int split) {
     using V = Value<TYPE>;
-    constexpr int W = V::PER_16, AHEAD = 4;
+    constexpr int W = V::PER_16, AHEAD = 8;
     __shared__ float sums[kRowsWarps][ROWS];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int per_cta = kRowsWarps / split;
@@ -219,39 +210,44 @@ __global__ void __launch_bounds__(32 * kRowsWarps)
     pdl_wait();
     pdl_launch_dependents();
     float sum[ROWS] = {};
-    for (int64_t s = first; inside && s < end; s += AHEAD) {
-        uint4 q[AHEAD];
+    // N whole steps from s on: all loads of B first, then A from L1
+    auto whole_steps = [&](int64_t s, auto count) {
+        constexpr int n = decltype(count)::value;
+        uint4 q[n];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            const int64_t k = ((s + u) * 32 + lane) * W;
-            q[u] = make_uint4(0, 0, 0, 0);
-            if (s + u < end && k + W <= p.K) q[u] = __ldcs(reinterpret_cast<const uint4 *>(b + k * V::BYTES));
-        }
+        for (int u = 0; u < n; ++u)
+            q[u] = __ldcs(reinterpret_cast<const uint4 *>(b + ((s + u) * 32 + lane) * W * V::BYTES));
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            const int64_t k = ((s + u) * 32 + lane) * W;
-            if (s + u >= end || k >= p.K) continue;
+        for (int u = 0; u < n; ++u) {
             float bv[W];
-            if (k + W <= p.K) {
-                V::unpack(q[u], bv);
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i) bv[i] = k + i < p.K ? V::load(b, k + i) : 0.f;
-            }
+            V::unpack(q[u], bv);
 #pragma unroll
             for (int m = 0; m < ROWS; ++m) {
-                if (m >= p.M) continue;
-                const uint8_t *a = static_cast<const uint8_t *>(p.A) + (m * p.lda + k) * V::BYTES;
+                if (ROWS > 2 && m >= p.M) continue;  // (ROWS up to 2 is M)
                 float av[W];
-                if (k + W <= p.K) {
-                    V::unpack(__ldg(reinterpret_cast<const uint4 *>(a)), av);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) av[i] = k + i < p.K ? V::load(a, i) : 0.f;
-                }
+                V::unpack(__ldg(reinterpret_cast<const uint4 *>(
+                              static_cast<const uint8_t *>(p.A) +
+                              (m * p.lda + ((s + u) * 32 + lane) * W) * V::BYTES)),
+                          av);
 #pragma unroll
                 for (int i = 0; i < W; ++i) sum[m] = fmaf(av[i], bv[i], sum[m]);
             }
+        }
+    };
+    const int64_t whole = p.K / (32 * W), last = end < whole ? end : whole;
+    int64_t s = first;
+    if (inside) {
+        for (; s + AHEAD <= last; s += AHEAD) whole_steps(s, std::integral_constant<int, AHEAD>());
+        for (; s < last; ++s) whole_steps(s, std::integral_constant<int, 1>());
+    }
+    if (inside && end > whole) {  // K's end
+        for (int i = 0; i < W; ++i) {
+            const int64_t k = (whole * 32 + lane) * W + i;
+            if (k >= p.K) break;
+            const float bv = V::load(b, k);
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m)
+                if (m < p.M) sum[m] = fmaf(V::load(p.A, m * p.lda + k), bv, sum[m]);
         }
     }
 #pragma unroll
@@ -283,6 +279,94 @@ __global__ void __launch_bounds__(32 * kRowsWarps)
 #pragma unroll
         for (int s = ROWS / 2; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
         if (lane == 0) p.dbias[n] = d;
+    }
+}
+
+// ------------------------------------------------------------- FP32: second pass
+// D from the product in T (null: a product of nothing).  A CTA takes 64 times four
+// columns of 32 rows, a thread four columns of eight of them; T may be D or the value
+// kept.  With part the block's column sums go there.
+constexpr int kPassRows = 32, kPassCols = 256;
+template <bool VEC>
+__global__ void __launch_bounds__(256) fused_finish_kernel(const __grid_constant__ FusedProblem p,
+                                                           const float *T, int64_t ldt, float *part) {
+    __shared__ float sums[4][kPassCols];
+    const int64_t wide = (p.N + kPassCols - 1) / kPassCols;
+    const int64_t blocks = (p.M + kPassRows - 1) / kPassRows * wide;
+    const int quad = threadIdx.x % 64, group = threadIdx.x / 64;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const int64_t block = b / wide, c0 = (b - block * wide) * kPassCols + quad * 4;
+        const int64_t r0 = block * kPassRows + group;  // and every fourth row on
+        const int n = p.N - c0 < 4 ? static_cast<int>(p.N - c0 < 0 ? 0 : p.N - c0) : 4;
+        auto load = [&](const void *m, int64_t ld, int64_t r, float (&v)[4]) {
+            const float *from = static_cast<const float *>(m) + r * ld + c0;
+            if (VEC && n == 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(from);
+                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = i < n ? from[i] : 0.f;
+            }
+        };
+        auto store = [&](void *m, int64_t ld, int64_t r, const float (&v)[4]) {
+            float *to = static_cast<float *>(m) + r * ld + c0;
+            if (VEC && n == 4) {
+                *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n) to[i] = v[i];
+            }
+        };
+        float bias[4] = {}, column[4] = {};
+        if (!p.grad && p.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) bias[i] = p.bias[c0 + i];
+        }
+        const void *const other = p.grad ? (p.act != kActNone ? p.pre : nullptr) : p.residual;
+        const int64_t ld_other = p.grad ? p.ld_pre : p.ld_r;
+#pragma unroll
+        for (int h = 0; h < kPassRows / 4; h += 4) {  // four rows' loads at once
+            float z[4][4] = {}, x[4][4] = {};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t r = r0 + (h + u) * 4;
+                if (r >= p.M || n == 0) continue;
+                if (T != nullptr) load(T, ldt, r, z[u]);
+                if (other != nullptr) load(other, ld_other, r, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t r = r0 + (h + u) * 4;
+                if (r >= p.M || n == 0) continue;
+                float d[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (p.grad) {
+                        d[i] = p.act != kActNone ? z[u][i] * fused_slope(x[u][i], p.act) : z[u][i];
+                        column[i] += d[i];
+                    } else {
+                        z[u][i] += bias[i];
+                        d[i] = fused_activation(z[u][i], p.act) + x[u][i];
+                    }
+                }
+                if (!p.grad && p.pre != nullptr) store(p.pre, p.ld_pre, r, z[u]);
+                store(p.D, p.ldd, r, d);
+            }
+        }
+        if (part != nullptr) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[group][quad * 4 + i] = column[i];
+            __syncthreads();
+            const int64_t c = (b - block * wide) * kPassCols + threadIdx.x;
+            if (c < p.N)
+                part[block * p.N + c] = (sums[0][threadIdx.x] + sums[1][threadIdx.x]) +
+                                        (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
+        }
     }
 }
 
@@ -336,67 +420,118 @@ cudaError_t launch(K kernel, int64_t ctas, int threads, size_t smem, int cluster
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int TYPE, int T>
-cudaError_t tiles_as(const FusedProblem &p, int ks, cudaStream_t stream) {
-    const int64_t tiles_m = ceil_div(p.M, T), tiles_n = ceil_div(p.N, T);
-    constexpr size_t smem = Tile<T>::FLOATS * sizeof(float);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            fused_tile_kernel<TYPE, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    const int64_t blocks = tiles_m * ks;
-    float *part = p.dbias;
-    void *ws = nullptr;
-    cudaError_t e = cudaSuccess;
-    if (p.grad && p.dbias != nullptr && blocks > 1) {
-        e = workspace_alloc(static_cast<size_t>(blocks * p.N) * sizeof(float), stream, &ws);
-        if (e != cudaSuccess) return e;
-        part = static_cast<float *>(ws);
-    }
-    e = launch(fused_tile_kernel<TYPE, T>, tiles_m * tiles_n * ks, THREADS, smem, ks, stream, p,
-               tiles_n, ks, part);
-    if (ws != nullptr) {
-        if (e == cudaSuccess) e = launch_column_sums(part, blocks, p.N, p.dbias, stream);
-        const cudaError_t ef = workspace_free(ws, stream);
-        if (e == cudaSuccess) e = ef;
-    }
-    return e;
-}
-
-// The rows kernel's operands: K contiguous and on 16 bytes, M at most 4.
+// The rows kernel's operands: K contiguous and on 16 bytes, few rows.  Past two rows
+// of 16 bits its arithmetic is the time, and the tensor cores are faster where B is
+// large (4096 x 4096: 1 row 7.8 us, 2 rows 8.1, 4 rows 14.9 and 14.4; 4096 x 14336,
+// 4 rows 43 and 26; 4096 x 1024, 4 rows 7.3 and 11).
 bool rows_fit(const FusedProblem &p, int64_t bytes) {
-    if (p.M > 4 || p.K == 0 || !p.b_kmajor || !rows_on_16(p.B, p.ldb, bytes)) return false;
+    if (p.M > (bytes == 4 || p.N * p.K <= (int64_t(8) << 20) ? 4 : 2) || p.K == 0 || !p.b_kmajor || !rows_on_16(p.B, p.ldb, bytes)) return false;
     if (p.M == 1)
         return reinterpret_cast<uintptr_t>(p.A) % 16 == 0 && (p.a_kmajor || p.lda == 1);
     return p.a_kmajor && rows_on_16(p.A, p.lda, bytes);
 }
 
+// Column sums of `blocks` blocks of rows: where the kernel puts them (*part), dbias
+// itself if there is one block, and the sum of several.
+cudaError_t sums_begin(const FusedProblem &p, int64_t blocks, cudaStream_t stream, float **part,
+                       void **ws) {
+    *part = p.dbias;
+    *ws = nullptr;
+    if (!p.grad || p.dbias == nullptr || blocks <= 1) return cudaSuccess;
+    const cudaError_t e = workspace_alloc(static_cast<size_t>(blocks * p.N) * sizeof(float), stream, ws);
+    if (e == cudaSuccess) *part = static_cast<float *>(*ws);
+    return e;
+}
+cudaError_t sums_end(const FusedProblem &p, int64_t blocks, cudaStream_t stream, float *part, void *ws,
+                     cudaError_t e) {
+    if (ws == nullptr) return e;
+    if (e == cudaSuccess) e = launch_column_sums(part, blocks, p.N, p.dbias, stream);
+    const cudaError_t ef = workspace_free(ws, stream);
+    return e == cudaSuccess ? ef : e;
+}
+
 template <int TYPE>
-cudaError_t fused_of(const FusedProblem &p, cudaStream_t stream, const char **name) {
-    using V = Value<TYPE>;
-    const int64_t sms = sm_count();
-    if (rows_fit(p, V::BYTES)) {
-        FusedProblem q = p;
-        q.a_kmajor = true;  // (one row whose K lies one apart may be column-major)
-        *name = "fused_rows";
-        // warps for about 24 per SM, each with a few steps of K
-        int split = 1;
-        while (split < kRowsWarps && p.N * split < 24 * sms && ceil_div(p.K, 32 * V::PER_16) >= 4 * split)
-            split *= 2;
-        const int64_t ctas = ceil_div(p.N, kRowsWarps / split);
-        if (p.M == 1)
-            return launch(fused_rows_kernel<TYPE, 1>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
-        if (p.M == 2)
-            return launch(fused_rows_kernel<TYPE, 2>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
-        return launch(fused_rows_kernel<TYPE, 4>, ctas, 32 * kRowsWarps, 0, 1, stream, q, split);
-    }
-    *name = "fused_simt";
-    if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= sms) return tiles_as<TYPE, 128>(p, 1, stream);
-    const int64_t tiles = ceil_div(p.M, 64) * ceil_div(p.N, 64);
+cudaError_t tiles_of(const FusedProblem &p, cudaStream_t stream) {
+    const int64_t tiles_m = ceil_div(p.M, kTile), tiles_n = ceil_div(p.N, kTile);
     int ks = 1;
-    while (ks < 8 && tiles * ks * 2 <= 2 * sms && p.K >= 128 * ks) ks *= 2;
-    return tiles_as<TYPE, 64>(p, ks, stream);
+    while (ks < 8 && tiles_m * tiles_n * ks * 2 <= 2 * sm_count() && p.K >= 128 * ks) ks *= 2;
+    float *part;
+    void *ws;
+    cudaError_t e = sums_begin(p, tiles_m * ks, stream, &part, &ws);
+    if (e == cudaSuccess)
+        e = launch(fused_tile_kernel<TYPE>, tiles_m * tiles_n * ks, THREADS, kTileFloats * sizeof(float), ks,
+                   stream, p, tiles_n, ks, part);
+    return sums_end(p, tiles_m * ks, stream, part, ws, e);
+}
+
+template <int TYPE>
+cudaError_t rows_of(const FusedProblem &p, cudaStream_t stream) {
+    FusedProblem q = p;
+    q.a_kmajor = true;  // (one row whose K lies one apart may be column-major)
+    // warps for about 24 per SM, each with a few steps of K
+    int split = 1;
+    while (split < kRowsWarps && p.N * split < 24 * sm_count() &&
+           ceil_div(p.K, 32 * Value<TYPE>::PER_16) >= 4 * split)
+        split *= 2;
+    const int64_t ctas = ceil_div(p.N, kRowsWarps / split);
+    const int n = 32 * kRowsWarps;
+    if (p.M == 1) return launch(fused_rows_kernel<TYPE, 1>, ctas, n, 0, 1, stream, q, split);
+    if (p.M == 2) return launch(fused_rows_kernel<TYPE, 2>, ctas, n, 0, 1, stream, q, split);
+    return launch(fused_rows_kernel<TYPE, 4>, ctas, n, 0, 1, stream, q, split);
+}
+
+// FP32: the product, then what follows it.
+cudaError_t f32_of(const FusedProblem &p, cudaStream_t stream, const char **name) {
+    Problem g = {};
+    g.M = p.M, g.N = p.N, g.K = p.K;
+    g.alpha = p.alpha;
+    g.A = p.A, g.lda = p.lda, g.a_kmajor = p.a_kmajor;
+    g.B = p.B, g.ldb = p.ldb, g.b_kmajor = p.b_kmajor;
+    g.D = static_cast<float *>(p.D), g.ldd = p.ldd;
+    const bool alone = p.act == kActNone && p.bias == nullptr && (p.grad || p.pre == nullptr) &&
+                       p.dbias == nullptr;
+    if (alone && p.K > 0) {  // nothing follows that the product's own epilogue cannot do
+        if (!p.grad && p.residual != nullptr) {
+            g.beta = 1.f;
+            g.C = static_cast<const float *>(p.residual), g.ldc = p.ld_r;
+        }
+        return launch_f32(g, stream, name);
+    }
+    // the product goes where nothing that is still needed lies
+    void *product = nullptr;
+    if (!p.grad && p.pre != nullptr) {
+        g.D = static_cast<float *>(p.pre), g.ldd = p.ld_pre;
+    } else if (p.D == p.residual || p.D == p.pre) {
+        if (p.K > 0) {
+            const cudaError_t e =
+                workspace_alloc(static_cast<size_t>(p.M) * p.N * sizeof(float), stream, &product);
+            if (e != cudaSuccess) return e;
+        }
+        g.D = static_cast<float *>(product), g.ldd = p.N;
+    }
+    cudaError_t e = p.K > 0 ? launch_f32(g, stream, name) : cudaSuccess;
+    FusedProblem q = p;
+    q.alpha = 1.f;  // (in the product)
+    const int64_t blocks = ceil_div(p.M, kPassRows);
+    float *part = nullptr;
+    void *ws = nullptr;
+    if (e == cudaSuccess) e = sums_begin(q, blocks, stream, &part, &ws);
+    if (e == cudaSuccess) {
+        const int64_t ctas = blocks * ceil_div(p.N, kPassCols), most = 32 * int64_t(sm_count());
+        const bool vec = rows_on_16(p.D, p.ldd, 4) && rows_on_16(g.D, g.ldd, 4) &&
+                         (p.pre == nullptr || rows_on_16(p.pre, p.ld_pre, 4)) &&
+                         (p.residual == nullptr || rows_on_16(p.residual, p.ld_r, 4));
+        e = launch(vec ? fused_finish_kernel<true> : fused_finish_kernel<false>, ctas < most ? ctas : most,
+                   256, 0, 1, stream, q, static_cast<const float *>(p.K > 0 ? g.D : nullptr), g.ldd,
+                   p.grad && p.dbias != nullptr ? part : nullptr);
+    }
+    e = sums_end(q, blocks, stream, part, ws, e);
+    if (product != nullptr) {
+        const cudaError_t ef = workspace_free(product, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    *name = "fused_f32";
+    return e;
 }
 
 }  // namespace
@@ -424,9 +559,19 @@ bool fused_rows_eligible(const FusedProblem &p, InType in) {
 
 cudaError_t launch_fused_simt(const FusedProblem &p, InType in, cudaStream_t stream,
                               const char **name) {
-    if (in == InType::F32) return fused_of<kOutF32>(p, stream, name);
-    return in == InType::BF16 ? fused_of<kOutBf16>(p, stream, name)
-                              : fused_of<kOutF16>(p, stream, name);
+    if (fused_rows_eligible(p, in)) {
+        *name = "fused_rows";
+        if (in == InType::F32) return rows_of<kOutF32>(p, stream);
+        return in == InType::BF16 ? rows_of<kOutBf16>(p, stream) : rows_of<kOutF16>(p, stream);
+    }
+    *name = "fused_simt";
+    if (in == InType::F32) {
+        // few tiles: one kernel with K split over clusters (64 x 1024, K = 1000: 16 us,
+        // product and pass 21; 512 x 512 x 512: 22 and 24; 2000 x 200, K = 1000: 69 and 48)
+        const bool few = ceil_div(p.M, kTile) * ceil_div(p.N, kTile) * 2 <= sm_count();
+        return few ? tiles_of<kOutF32>(p, stream) : f32_of(p, stream, name);
+    }
+    return in == InType::BF16 ? tiles_of<kOutBf16>(p, stream) : tiles_of<kOutF16>(p, stream);
 }
 
 }  // namespace gemm

@@ -56,7 +56,7 @@ struct Args {
     int a_kmajor, b_kmajor, b_blocks, ab_format;
     float alpha;
     const float *bias;
-    int act, out;  // out: kOutBf16 or kOutF16
+    int act;
     void *D, *pre;
     const void *in;  // forward: residual; gradient: pre
     int64_t ldd, ld_pre, ld_in;
@@ -117,11 +117,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int32_t c0,
 }
 
 // Eight 16-bit values as FP32.
-__device__ __forceinline__ void widen(const uint4 &q, int type, float (&v)[8]) {
+template <int TYPE>
+__device__ __forceinline__ void widen(const uint4 &q, float *v) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (type == kOutBf16) {
+        if constexpr (TYPE == kOutBf16) {
             v[2 * i] = __uint_as_float(w[i] << 16);
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         } else {
@@ -131,39 +132,67 @@ __device__ __forceinline__ void widen(const uint4 &q, int type, float (&v)[8]) {
         }
     }
 }
-__device__ __forceinline__ uint4 narrow(const float (&v)[8], int type) {
-    return make_uint4(pack_16(v[0], v[1], type), pack_16(v[2], v[3], type),
-                      pack_16(v[4], v[5], type), pack_16(v[6], v[7], type));
-}
-
 template <int ACT>
-__device__ __forceinline__ void activate_8(float (&v)[8]) {
+__device__ __forceinline__ void activate_16(float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fused_activation<true>(v[i], ACT);
+    for (int j = 0; j < 16; ++j) v[j] = quick_activation<ACT>(v[j]);
 }
 template <int ACT>
-__device__ __forceinline__ void slope_8(float (&v)[8], const float (&z)[8]) {
+__device__ __forceinline__ void slope_16(float (&v)[16], const float (&z)[16]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= fused_slope<true>(z[i], ACT);
+    for (int j = 0; j < 16; ++j) v[j] *= quick_slope<ACT>(z[j]);
 }
 
-// The sum of the 32 lanes' v[j] for column j = lane, in a fixed order.
-__device__ __forceinline__ float column_sum(float (&v)[32]) {
+// The sum of the 32 lanes' v[j] for column j = lane / 2, in a fixed order.
+__device__ __forceinline__ float column_sum(float (&v)[16]) {
     const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        const bool high = (lane & s) != 0;
+    for (int s = 8; s > 0; s >>= 1) {
+        const bool high = (lane & (2 * s)) != 0;
 #pragma unroll
         for (int j = 0; j < s; ++j) {
             const float give = high ? v[j] : v[j + s], keep = high ? v[j + s] : v[j];
-            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * s);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// 32 lanes x 16 columns of 32-bit TMEM words.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
 }
 
 // 16-byte piece p of row r of a box (128-byte swizzle).
 __device__ __forceinline__ uint32_t piece_at(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
+
+// Sixteen values of this lane's row, from column h * 16 of the box on, rounded.
+template <int TYPE>
+__device__ __forceinline__ void narrow_16(const float (&v)[16], uint32_t box, int lane, int h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (TYPE == kOutBf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        } else {
+            const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+    st_shared_v4(box + piece_at(lane, h * 2), w[0], w[1], w[2], w[3]);
+    st_shared_v4(box + piece_at(lane, h * 2 + 1), w[4], w[5], w[6], w[7]);
+}
 
 // A box's rows to memory, and back, where TMA cannot: two values per lane and row.
 __device__ __forceinline__ void box_to_rows(uint32_t box, void *D, int64_t ldd, int64_t row0, int nrows,
@@ -207,7 +236,7 @@ __device__ __forceinline__ void rows_to_box(uint32_t box, const void *from, int6
     }
 }
 
-template <int CG, bool SPLIT, bool GRAD>
+template <int CG, bool SPLIT, bool GRAD, int TYPE>
 __global__ void __launch_bounds__(kThreads, 1)
     fused_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                     const __grid_constant__ CUtensorMap map_b,
@@ -238,8 +267,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = SPLIT ? args.ks : CG;  // CTAs that share a tile
     const uint32_t first_tile = blockIdx.x / group, tile_step = gridDim.x / group;
 
+    if (threadIdx.x == 32) {
+        // (the maps are fetched while another warp sets up the barriers)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_in)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_d)) : "memory");
+    }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2 * kMaxStages; ++s) mbar_init(full0 + 8 * s, 1);
+        for (int s = 0; s < args.stages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, kEpiWarps * CG);
@@ -249,8 +288,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
     }
     if (warp == kIssuer) tmem_alloc<CG>(smem_addr(tmem_slot));
     tc_fence_before();
@@ -450,11 +487,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // One block: 64 columns from tile column b * 64 on.  sums(h, v): the product's
-    // columns h * 32 .. of this lane's row; after(): all sums have been read; next():
-    // fetches the next box.  False: gave up.
+    // columns h * 16 .. of this lane's row; after(): all sums have been read; next():
+    // fetches the next box.  False: gave up.  (Sixteen columns at a time, in a loop
+    // that is not unrolled: a tile that is alone on its SM runs its epilogue once,
+    // and fetching straight-line code for 64 columns took most of 3 us.)
     auto finish_block = [&](int b, auto &&sums, auto &&after, auto &&next) -> bool {
         const int64_t c0 = t.n0 + b * 64;
-        const int width = args.N - c0 < 64 ? static_cast<int>(args.N - c0) : 64;
+        const int in_tile = args.bn - b * 64 < 64 ? args.bn - b * 64 : 64;
+        const int width = args.N - c0 < in_tile ? static_cast<int>(args.N - c0) : in_tile;
         float bias2[2] = {0.f, 0.f};
         if (!GRAD && args.bias != nullptr) {
             if (lane < width) bias2[0] = __ldg(args.bias + c0 + lane);
@@ -473,75 +513,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) bulk_wait_read();  // the boxes of the last block have left
         __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!GRAD && args.bias != nullptr) {
-                st_shared_f32(bias_at + lane * 4, bias2[h]);
+#pragma unroll 1
+        for (int h = 0; h * 16 < in_tile; ++h) {
+            if (!GRAD && args.bias != nullptr && (h & 1) == 0) {
+                __syncwarp();
+                st_shared_f32(bias_at + lane * 4, h == 0 ? bias2[0] : bias2[1]);
                 __syncwarp();
             }
-            float v[32];
+            float v[16];
             sums(h, v);
-            if (h == 1) after();
+            if ((h + 1) * 16 >= in_tile) after();
+            if (!GRAD && args.bias != nullptr) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                float z[8], x[8] = {};
-                if (has_in) widen(ld_shared_u4(box_in + piece_at(lane, h * 4 + p)), args.out, x);
-                if constexpr (GRAD) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[i] = args.alpha * v[p * 8 + i];
-                    if (args.act == kActGelu)
-                        slope_8<kActGelu>(z, x);
-                    else if (args.act == kActSilu)
-                        slope_8<kActSilu>(z, x);
-                    else if (args.act == kActRelu)
-                        slope_8<kActRelu>(z, x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[p * 8 + i] = z[i];
-                } else {
-                    if (args.bias != nullptr) {
-                        const float4 b0 = ld_shared_v4(bias_at + p * 32), b1 = ld_shared_v4(bias_at + p * 32 + 16);
-                        const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] = fmaf(args.alpha, v[p * 8 + i], bv[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] = args.alpha * v[p * 8 + i];
-                    }
-                    if (has_pre) {
-                        const uint4 q = narrow(z, args.out);
-                        st_shared_v4(box_pre + piece_at(lane, h * 4 + p), q.x, q.y, q.z, q.w);
-                    }
-                    if (args.act == kActGelu)
-                        activate_8<kActGelu>(z);
-                    else if (args.act == kActSilu)
-                        activate_8<kActSilu>(z);
-                    else if (args.act == kActRelu)
-                        activate_8<kActRelu>(z);
-                    if (has_in) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] += x[i];
-                    }
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 q = ld_shared_v4(bias_at + (h & 1) * 64 + j * 4);
+                    v[j] = fmaf(args.alpha, v[j], q.x), v[j + 1] = fmaf(args.alpha, v[j + 1], q.y);
+                    v[j + 2] = fmaf(args.alpha, v[j + 2], q.z), v[j + 3] = fmaf(args.alpha, v[j + 3], q.w);
                 }
-                const uint4 q = narrow(z, args.out);
-                st_shared_v4(box_d + piece_at(lane, h * 4 + p), q.x, q.y, q.z, q.w);
+            } else if (args.alpha != 1.f) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] *= args.alpha;
             }
+            if constexpr (!GRAD) {
+                if (has_pre) {
+                    narrow_16<TYPE>(v, box_pre, lane, h);
+                }
+                if (args.act == kActGelu)
+                    activate_16<kActGelu>(v);
+                else if (args.act == kActSilu)
+                    activate_16<kActSilu>(v);
+                else if (args.act == kActRelu)
+                    activate_16<kActRelu>(v);
+            }
+            if (has_in) {
+                float x[16];
+                widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2)), x);
+                widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2 + 1)), x + 8);
+                if constexpr (GRAD) {
+                    if (args.act == kActGelu)
+                        slope_16<kActGelu>(v, x);
+                    else if (args.act == kActSilu)
+                        slope_16<kActSilu>(v, x);
+                    else if (args.act == kActRelu)
+                        slope_16<kActRelu>(v, x);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += x[j];
+                }
+            }
+            narrow_16<TYPE>(v, box_d, lane, h);
             if constexpr (GRAD) {
                 if (args.part != nullptr) {
                     if (lane >= nrows) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
                     }
-                    const float s = column_sum(v);
-                    if (h * 32 + lane < width) args.part[row0 / 32 * args.N + c0 + h * 32 + lane] = s;
+                    const float sum = column_sum(v);
+                    const int c = h * 16 + lane / 2;
+                    if (lane % 2 == 0 && c < width) args.part[row0 / 32 * args.N + c0 + c] = sum;
                 }
             }
-            if (!GRAD && args.bias != nullptr) __syncwarp();
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (has_in && args.tma_in) next();
-        // (TMA stores whole 16-byte pieces: the block with an odd end goes by rows)
-        const bool whole = width == 64 || args.N % 8 == 0;
+        // (TMA stores whole 16-byte pieces, and its box is 64 columns wide: a block with
+        // an odd end, or cut by the tile's, goes by rows)
+        const bool whole = width == 64 || (args.N % 8 == 0 && c0 + width == args.N);
         if (args.tma_d && whole) {
             if (elect_one())
                 tma_store_2d(&map_d, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_d);
@@ -587,12 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = half; b < n_blocks && !aborted; b += 2) {
                     aborted = !finish_block(
                         b,
-                        [&](int h, float (&v)[32]) {
-                            uint32_t raw[32];
+                        [&](int h, float (&v)[16]) {
                             __syncwarp();
-                            tmem_load_32cols(t_acc + b * 64 + h * 32, raw);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                            tmem_load_16cols(t_acc + b * 64 + h * 16, v);
                         },
                         [&]() {
                             if (b == last) release_acc();
@@ -641,15 +676,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (a slot per other piece, in their order)
                 slot += static_cast<int>(rank) - (static_cast<int>(rank) > owner ? 1 : 0);
                 const uint32_t to = map_to_rank(ring0 + slot * kSlot + lane * 256, owner);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t raw[32];
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    float v[16];
                     __syncwarp();
-                    tmem_load_32cols(t_acc + b * 64 + h * 32, raw);
+                    tmem_load_16cols(t_acc + b * 64 + h * 16, v);
 #pragma unroll
-                    for (int p = 0; p < 8; ++p)
-                        st_cluster_v4(to + (((h * 8 + p) ^ (lane & 15)) << 4), raw[p * 4], raw[p * 4 + 1],
-                                      raw[p * 4 + 2], raw[p * 4 + 3]);
+                    for (int p = 0; p < 4; ++p)
+                        st_cluster_v4(to + (((h * 4 + p) ^ (lane & 15)) << 4), __float_as_uint(v[p * 4]),
+                                      __float_as_uint(v[p * 4 + 1]), __float_as_uint(v[p * 4 + 2]),
+                                      __float_as_uint(v[p * 4 + 3]));
                 }
             }
         }
@@ -660,23 +696,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (owner_of(b, slot) != static_cast<int>(rank)) continue;
                 aborted = !finish_block(
                     b,
-                    [&](int h, float (&v)[32]) {
-                        uint32_t raw[32];
+                    [&](int h, float (&v)[16]) {
+                        float own[16];
                         __syncwarp();
-                        tmem_load_32cols(t_acc + b * 64 + h * 32, raw);
+                        tmem_load_16cols(t_acc + b * 64 + h * 16, own);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+#pragma unroll 1
                         for (int q = 0; q < args.ks; ++q) {
                             if (q == static_cast<int>(rank)) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(raw[j]);
+                                for (int j = 0; j < 16; ++j) v[j] += own[j];
                                 continue;
                             }
-                            const int s = slot + q - (q > static_cast<int>(rank) ? 1 : 0);
-                            const uint32_t from = ring0 + s * kSlot + lane * 256;
+                            const int at = slot + q - (q > static_cast<int>(rank) ? 1 : 0);
+                            const uint32_t from = ring0 + at * kSlot + lane * 256;
 #pragma unroll
-                            for (int p = 0; p < 8; ++p) {
-                                const float4 f = ld_shared_v4(from + (((h * 8 + p) ^ (lane & 15)) << 4));
+                            for (int p = 0; p < 4; ++p) {
+                                const float4 f = ld_shared_v4(from + (((h * 4 + p) ^ (lane & 15)) << 4));
                                 v[p * 4] += f.x, v[p * 4 + 1] += f.y;
                                 v[p * 4 + 2] += f.z, v[p * 4 + 3] += f.w;
                             }
@@ -712,7 +749,7 @@ constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bi
 
 std::atomic<bool> g_launched[kMaxDevices];
 
-template <int CG, bool SPLIT, bool GRAD>
+template <int CG, bool SPLIT, bool GRAD, int TYPE>
 cudaLaunchConfig_t config(int grid, int cluster, cudaStream_t stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -736,12 +773,12 @@ struct Prepared {
     cudaError_t err = cudaSuccess;
     int resident[kMaxSplit + 1] = {};
 };
-template <int CG, bool SPLIT, bool GRAD>
+template <int CG, bool SPLIT, bool GRAD, int TYPE>
 const Prepared &prepared(int dev) {
     static Prepared all[kMaxDevices];
     Prepared &p = all[dev];
     std::call_once(p.once, [&p, dev] {
-        const auto kernel = fused_tc_kernel<CG, SPLIT, GRAD>;
+        const auto kernel = fused_tc_kernel<CG, SPLIT, GRAD, TYPE>;
         p.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (p.err != cudaSuccess) return;
         int sms = 0;
@@ -750,7 +787,7 @@ const Prepared &prepared(int dev) {
         p.resident[1] = sms > 0 ? sms : 1;
         for (int c = 2; c <= (CG == 2 ? 2 : SPLIT ? kMaxSplit : 1); c *= 2) {
             cudaLaunchAttribute attr[2];
-            cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD>(c, c, 0, attr);
+            cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD, TYPE>(c, c, 0, attr);
             cfg.attrs = attr + 1;  // the occupancy query takes the cluster shape only
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&p.resident[c], kernel, &cfg) != cudaSuccess) {
@@ -766,52 +803,23 @@ struct Maps {
     CUtensorMap a, b, b_edge, in, d, pre;
 };
 
-template <int CG, bool SPLIT, bool GRAD>
+template <int CG, bool SPLIT, bool GRAD, int TYPE>
 cudaError_t launch_as(const Maps &m, const Args &a, int dev, int grid, int cluster,
                       cudaStream_t stream) {
     g_launched[dev].store(true);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD>(grid, cluster, stream, attr);
-    return cudaLaunchKernelEx(&cfg, fused_tc_kernel<CG, SPLIT, GRAD>, m.a, m.b, m.b_edge, m.in, m.d,
+    cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD, TYPE>(grid, cluster, stream, attr);
+    return cudaLaunchKernelEx(&cfg, fused_tc_kernel<CG, SPLIT, GRAD, TYPE>, m.a, m.b, m.b_edge, m.in, m.d,
                               m.pre, a);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A way to cut the product.
+// A way to cut the product: CTAs per tile's accumulator, rows and columns of a tile
+// (per CTA and in all), pieces of K.
 struct Cut {
     int cg, am, bn, ks;
 };
-
-// The cut whose slowest CTA is done first, by a model: a step of K takes the
-// longer of its MMAs (512 clocks of the SM's tensor core for 128 x 256 x 64, or a
-// pair's 256 x 256 x 64) and its bytes from L2 at 120 GB/s per SM; a tile costs
-// 2 us beside that, an exchange of pieces 2 us more.
-Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &split, int sms) {
-    const int64_t kb = ceil_div(p.K, BK);
-    Cut best = {1, BM, 256, 1};
-    double least = 1e30;
-    auto consider = [&](const Cut &c, int64_t slots) {
-        if (slots <= 0) return;
-        const int64_t tiles = ceil_div(p.M, c.am * c.cg) * ceil_div(p.N, c.bn);
-        const int64_t rounds = ceil_div(tiles, slots);
-        const double mma = 0.27 * c.bn / 256, l2 = (c.am + c.bn / c.cg) * 128 / 120e3;
-        const double steps = static_cast<double>(ceil_div(kb, c.ks));
-        const double cost = rounds * (steps * (mma > l2 ? mma : l2) + 2.0) + (c.ks > 1 ? 2.0 : 0.0);
-        if (cost < least) least = cost, best = c;
-    };
-    if (p.M > BM) consider({2, BM, 256, 1}, pair.resident[2]);
-    const int am = !p.a_kmajor || p.M > 64 ? BM : (p.M <= 16 ? 16 : (p.M <= 32 ? 32 : 64));
-    for (int bn : {256, 128, 64}) {
-        if (bn > 64 && p.N <= bn / 2) continue;
-        consider({1, am, bn, 1}, sms);
-        for (int ks = 2; ks <= kMaxSplit; ks *= 2) {
-            const int64_t tiles = ceil_div(p.M, am) * ceil_div(p.N, bn);
-            if (kb >= 2 * ks && tiles <= split.resident[ks]) consider({1, am, bn, ks}, split.resident[ks]);
-        }
-    }
-    return best;
-}
 
 // Blocks of 64 of K per step: a copy takes the producer about 100 ns to issue
 // whatever its size, while a 128 x 128 tile multiplies a block in 130 ns.  The
@@ -827,19 +835,66 @@ int sub_blocks(const FusedProblem &p, const Cut &c) {
     return ksub;
 }
 
+// The cut whose slowest CTA is done first, by a model in microseconds fitted to 1022
+// measured times (90 shapes from 8 x 512 x 512 to 4096 x 4096 x 14336, every cut;
+// the cuts that it picks are 1.4 % slower than the best ones on the mean, 21 % at
+// most; the times themselves are met within 10 %):
+//   a block of 64 of K    the longest of its MMAs (0.27 for 128 x 256 or a pair's 256 x
+//                         256), its bytes at 109 GB/s per SM, and its step's copies (0.16)
+//   a tile's epilogue     3.0 + 1.7 per block of 64 columns of a warp, beside the next
+//                         tile's sum where there is one
+//   a launch              2.0, a pair 1.7 more; an exchange of pieces 2.0 and 1.5 per
+//                         64 columns of 128 rows
+//   all operands          once at 6.4 TB/s; tiles of 32 columns read at 0.6 of that
+Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &split, int sms) {
+    const int64_t kb = ceil_div(p.K, BK);
+    const double bytes = 2.0 * (static_cast<double>(p.M) * p.K + static_cast<double>(p.K) * p.N);
+    Cut best = {1, BM, 256, 1};
+    double least = 1e300;
+    auto consider = [&](const Cut &c, int64_t slots) {
+        if (slots <= 0) return;
+        const int64_t tiles = ceil_div(p.M, c.am * c.cg) * ceil_div(p.N, c.bn);
+        const double rounds = static_cast<double>(ceil_div(tiles, slots));
+        double block = 0.27 * c.bn / 256;
+        const double l2 = (c.am + c.bn / c.cg) * 128 / 109e3, issue = 0.16 / sub_blocks(p, c);
+        block = l2 > block ? l2 : block;
+        block = issue > block ? issue : block;
+        const double sum = static_cast<double>(ceil_div(kb, c.ks)) * block;
+        const double epilogue = 3.0 + 1.7 * (c.bn == 32 ? 0.5 : (c.bn + 127) / 128);
+        const double reads = bytes / (c.bn == 32 ? 3.8e6 : 6.4e6);
+        double sums = (rounds - 1) * (sum > epilogue ? sum : epilogue) + sum;
+        if (reads > sums) sums = reads;
+        const double cost = 2.0 + (c.cg == 2 ? 1.7 : 0.0) + sums + epilogue +
+                            (c.ks > 1 ? 2.0 + 1.5 * ((c.bn + 63) / 64) * c.am / BM : 0.0);
+        if (cost < least) least = cost, best = c;
+    };
+    if (p.M > BM) consider({2, BM, 256, 1}, pair.resident[2]);
+    const int am = !p.a_kmajor || p.M > 64 ? BM : (p.M <= 16 ? 16 : (p.M <= 32 ? 32 : 64));
+    for (int bn : {256, 128, 64, 32}) {
+        if (bn > 64 && p.N <= bn / 2) continue;
+        if (bn == 32 && !p.b_kmajor) continue;  // (N-major copies are 64 columns wide)
+        consider({1, am, bn, 1}, sms);
+        for (int ks = 2; ks <= kMaxSplit; ks *= 2) {
+            const int64_t tiles = ceil_div(p.M, am) * ceil_div(p.N, bn);
+            if (kb >= 2 * ks && tiles <= split.resident[ks]) consider({1, am, bn, ks}, split.resident[ks]);
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 bool fused_tc_eligible(const FusedProblem &p) {
     return p.K > 0 && tma_rows(p.A, p.lda) && tma_rows(p.B, p.ldb) &&
-           ceil_div(p.M, 16) * ceil_div(p.N, 64) < kMaxTiles;
+           ceil_div(p.M, 16) * ceil_div(p.N, 32) < kMaxTiles;
 }
 
-template <bool GRAD>
-static cudaError_t launch_tc_as(const FusedProblem &p, InType in, int dev, cudaStream_t stream,
+template <bool GRAD, int TYPE>
+static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t stream,
                                 const char **name) {
-    const bool bf16 = in == InType::BF16;
-    const Prepared &pair = prepared<2, false, GRAD>(dev), &one = prepared<1, false, GRAD>(dev),
-                   &split = prepared<1, true, GRAD>(dev);
+    constexpr bool bf16 = TYPE == kOutBf16;
+    const Prepared &pair = prepared<2, false, GRAD, TYPE>(dev), &one = prepared<1, false, GRAD, TYPE>(dev),
+                   &split = prepared<1, true, GRAD, TYPE>(dev);
     for (const Prepared *q : {&pair, &one, &split})
         if (q->err != cudaSuccess) return q->err;
     const Cut cut = choose_cut(p, pair, split, one.resident[1]);
@@ -860,7 +915,6 @@ static cudaError_t launch_tc_as(const FusedProblem &p, InType in, int dev, cudaS
     a.alpha = p.alpha;
     a.bias = p.bias;
     a.act = p.act;
-    a.out = bf16 ? kOutBf16 : kOutF16;
     a.D = p.D;
     a.ldd = p.ldd;
     a.in = GRAD ? p.pre : p.residual;
@@ -922,12 +976,12 @@ static cudaError_t launch_tc_as(const FusedProblem &p, InType in, int dev, cudaS
     *name = kNames[cut.ks > 1 ? 2 : cut.cg - 1][bf16];
     if (cut.cg == 2) {
         const int64_t n = tiles < pair.resident[2] ? tiles : pair.resident[2];
-        e = launch_as<2, false, GRAD>(m, a, dev, static_cast<int>(2 * n), 2, stream);
+        e = launch_as<2, false, GRAD, TYPE>(m, a, dev, static_cast<int>(2 * n), 2, stream);
     } else if (cut.ks > 1) {
-        e = launch_as<1, true, GRAD>(m, a, dev, static_cast<int>(tiles * cut.ks), cut.ks, stream);
+        e = launch_as<1, true, GRAD, TYPE>(m, a, dev, static_cast<int>(tiles * cut.ks), cut.ks, stream);
     } else {
         const int64_t n = tiles < one.resident[1] ? tiles : one.resident[1];
-        e = launch_as<1, false, GRAD>(m, a, dev, static_cast<int>(n), 1, stream);
+        e = launch_as<1, false, GRAD, TYPE>(m, a, dev, static_cast<int>(n), 1, stream);
     }
     if (ws != nullptr) {
         if (e == cudaSuccess) e = launch_column_sums(a.part, blocks, p.N, p.dbias, stream);
@@ -943,8 +997,11 @@ cudaError_t launch_fused_tc(const FusedProblem &p, InType in, cudaStream_t strea
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    return p.grad ? launch_tc_as<true>(p, in, dev, stream, name)
-                  : launch_tc_as<false>(p, in, dev, stream, name);
+    if (in == InType::BF16)
+        return p.grad ? launch_tc_as<true, kOutBf16>(p, dev, stream, name)
+                      : launch_tc_as<false, kOutBf16>(p, dev, stream, name);
+    return p.grad ? launch_tc_as<true, kOutF16>(p, dev, stream, name)
+                  : launch_tc_as<false, kOutF16>(p, dev, stream, name);
 }
 
 cudaError_t fused_tc_read_and_clear_status(cudaStream_t stream, int *status) {

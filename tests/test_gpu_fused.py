@@ -266,12 +266,14 @@ def near(got, ref, size, K, dtype, steep=1.0, extra=0.0):
     assert (off <= tol).all(), f"{int((off > tol).sum())} off, worst {float((off / tol).max()):.3g}"
 
 
-CUTS = [("fused_tc<{},pair>", 2100, 2500, 200), ("fused_tc<{},pair>", 4097, 2305, 72),
-        ("fused_tc<{},pair>", 600, 9000, 328), ("fused_tc<{},pair>", 2561, 2048, 640),
+# (None: whichever the library's model of their times picks)
+CUTS = [("fused_tc<{},pair>", 2300, 4100, 4096), ("fused_tc<{},pair>", 4097, 8200, 1000), (None, 4097, 2305, 72),
+        (None, 600, 9000, 328), (None, 2100, 2500, 200),
         ("fused_tc<{}>", 100, 9001, 264), ("fused_tc<{}>", 40, 20000, 512), ("fused_tc<{}>", 9, 12345, 64),
-        ("fused_tc<{},split>", 64, 1000, 4096), (None, 256, 515, 2048), (None, 130, 9001, 264),
-        ("fused_tc<{},split>", 16, 200, 8192), ("fused_tc<{},split>", 33, 64, 4000), (None, 33, 64, 1000),
-        (None, 500, 300, 3000)]
+        ("fused_tc<{}>", 7, 1000, 640), (None, 64, 4096, 4096), (None, 120, 14336, 1024),
+        ("fused_tc<{},split>", 64, 1000, 8192), ("fused_tc<{},split>", 16, 200, 8192),
+        ("fused_tc<{},split>", 33, 64, 8000), (None, 33, 64, 1000), (None, 256, 515, 2048), (None, 130, 9001, 264),
+        (None, 500, 300, 3000), (None, 300, 130, 9000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
