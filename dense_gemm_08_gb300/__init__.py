@@ -899,43 +899,85 @@ def gemm_lora(X, W, LA, LB, adapter_of_row, scale=None, bias=None, activation=GE
 
 
 # ------------------------------------ torch helpers, router and fused products
-def _types_of_values():
+# Written for few Python operations (the host's time is what bounds a decode step's
+# small calls): each tensor attribute is read once, checks are made in place.
+_kinds = None  # gemm_d_type_t by torch dtype, filled with the functions below
+_f32 = _i32 = None
+_fused_fns = _fused_grad_fns = None  # C entry points by gemm_d_type_t
+_current_device = _current_stream = None
+_new = None  # torch.empty
+
+
+def _ready():
+    """Look up once what every call needs."""
+    global _kinds, _f32, _i32, _fused_fns, _fused_grad_fns, _current_device, _current_stream, _new
     torch = _torch()
-    return {torch.float32: GEMM_D_F32, torch.bfloat16: GEMM_D_BF16, torch.float16: GEMM_D_F16}
+    lib = library()
+    _f32, _i32, _new = torch.float32, torch.int32, torch.empty
+    names = ("f32", "bf16_f32acc", "f16_f32acc")
+    _fused_fns = tuple(getattr(lib, "gemm_fused_" + n) for n in names)
+    _fused_grad_fns = tuple(getattr(lib, "gemm_fused_grad_" + n) for n in names)
+    _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _kinds = {torch.float32: GEMM_D_F32, torch.bfloat16: GEMM_D_BF16, torch.float16: GEMM_D_F16}
+    return _kinds
 
 
-_value_types = None
-
-
-def _value_type(t, what):
+def _kind_of(t, what):
     """gemm_d_type_t of a tensor."""
-    global _value_types
-    if _value_types is None:
-        _value_types = _types_of_values()
-    kind = _value_types.get(t.dtype)
+    kind = (_kinds or _ready()).get(t.dtype)
     if kind is None:
         raise TypeError(f"{what} must be float32, bfloat16 or float16")
     return kind
 
 
-def _matrix(t, shape, what, device):
-    """Leading dimension of a row-major matrix of this shape on the device."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must be {shape[0]} x {shape[1]}")
+def _pitch(t, rows, cols, what, device):
+    """Leading dimension of a row-major rows x cols matrix on the device."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must be {rows} x {cols}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}")
-    return _row_major(t, what)
+    s0, s1 = t.stride()
+    if (s1 == 1 or cols <= 1) and (s0 >= cols or rows <= 1):
+        return s0 if s0 > cols else cols or 1
+    raise ValueError(f"{what} must be row-major")
 
 
-def _pairs(t, shape, dtype, what, device):
-    """Address of a contiguous tokens x k tensor."""
+def _order(t, rows, cols):
+    """(order, leading dimension) of a rows x cols matrix (as storage_order)."""
+    s0, s1 = t.stride()
+    if s1 == 1 and (s0 >= cols or rows <= 1):
+        return ROW_MAJOR, s0 if s0 > cols else cols or 1
+    if s0 == 1 and (s1 >= rows or cols <= 1):
+        return COL_MAJOR, s1 if s1 > rows else rows or 1
+    raise ValueError(f"tensor with strides {t.stride()} is neither row- nor column-major")
+
+
+def _dense(t, shape, dtype, what, device):
+    """Address of a contiguous tensor of this shape and dtype on the device."""
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {str(dtype)[6:]}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous with shape {shape}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}")
     return t.data_ptr()
+
+
+def _here(device):
+    """The current device's number, which the operands are on."""
+    if device.type != "cuda":
+        raise ValueError("the operands must be CUDA tensors")
+    now = _current_device()
+    if device.index != now:
+        raise ValueError(f"the operands are on {device}, which is not the current device")
+    return now
+
+
+def _two(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a matrix")
+    return t.shape
 
 
 def route(logits, k, score=GEMM_SCORE_SOFTMAX, bias=None, groups=1, groups_kept=1, group_top=1,
@@ -946,24 +988,22 @@ def route(logits, k, score=GEMM_SCORE_SOFTMAX, bias=None, groups=1, groups_kept=
     choice only.  ``experts.view(-1)`` is what ``group_rows`` takes; a place
     without an expert (all others masked by -inf) has -1 and weight 0.
     """
-    torch = _torch()
-    kind = _value_type(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be a matrix")
-    tokens, experts = logits.shape
+    kind = _kind_of(logits, "logits")
+    tokens, experts = _two(logits, "logits")
     device = logits.device
-    ld = _row_major(logits, "logits")
-    rule = RouteRule(score, 1 if renormalize else 0, scale,
-                     _f32_dense(bias, (experts,), "bias", device), groups, groups_kept, group_top)
-    _on_device(device)
-    empty = _empty_for(stream)
-    # (a k that is refused below allocates nothing)
-    shape = (tokens, k if 0 < k <= experts else 0)
-    chosen = empty(shape, dtype=torch.int32, device=device)
-    weights = empty(shape, dtype=torch.float32, device=device)
-    st = library().gemm_route(tokens, experts, k, logits.data_ptr(), ld, kind, rule,
-                              chosen.data_ptr(), weights.data_ptr(), _stream_of(stream))
-    if st != GEMM_OK:
+    ld = _pitch(logits, tokens, experts, "logits", device)
+    b = None if bias is None else _dense(bias, (experts,), _f32, "bias", device)
+    now = _here(device)
+    new = _new if stream is None else _empty_for(stream)
+    shape = (tokens, k if 0 < k <= experts else 0)  # (a k that is refused below: nothing)
+    chosen = new(shape, dtype=_i32, device=device)
+    weights = new(shape, dtype=_f32, device=device)
+    st = _lib.gemm_route(tokens, experts, k, logits.data_ptr(), ld, kind,
+                         RouteRule(score, 1 if renormalize else 0, scale, b, groups, groups_kept,
+                                   group_top),
+                         chosen.data_ptr(), weights.data_ptr(),
+                         _current_stream(now) if stream is None else _stream(stream))
+    if st:
         raise GemmError(st, "gemm_route")
     return chosen, weights
 
@@ -975,28 +1015,27 @@ def route_grad(logits, chosen, dweights, score=GEMM_SCORE_SOFTMAX, renormalize=T
     chosen is what ``route`` returned, dweights (float32) the weights' gradient;
     score, renormalize and scale as for ``route``.  out may be logits.
     """
-    torch = _torch()
-    kind = _value_type(logits, "logits")
-    if logits.dim() != 2 or chosen.dim() != 2:
-        raise ValueError("logits and chosen must be matrices")
-    tokens, experts = logits.shape
+    kind = _kind_of(logits, "logits")
+    tokens, experts = _two(logits, "logits")
+    k = _two(chosen, "chosen")[1]
     device = logits.device
-    k = chosen.shape[1]
-    ld = _row_major(logits, "logits")
-    ids = _pairs(chosen, (tokens, k), torch.int32, "chosen", device)
-    dw = _pairs(dweights, (tokens, k), torch.float32, "dweights", device)
+    ld = _pitch(logits, tokens, experts, "logits", device)
+    ids = _dense(chosen, (tokens, k), _i32, "chosen", device)
+    dw = _dense(dweights, (tokens, k), _f32, "dweights", device)
     if out is not None:
         if out.dtype is not logits.dtype:
             raise TypeError("out must have the logits' dtype")
-        ld_d = _matrix(out, (tokens, experts), "out", device)
-    rule = RouteRule(score, 1 if renormalize else 0, scale, None, 1, 1, 1)
-    _on_device(device)
+        ld_d = _pitch(out, tokens, experts, "out", device)
+    now = _here(device)
     if out is None:
-        out = _empty_for(stream)((tokens, experts), dtype=logits.dtype, device=device)
+        new = _new if stream is None else _empty_for(stream)
+        out = new((tokens, experts), dtype=logits.dtype, device=device)
         ld_d = experts
-    st = library().gemm_route_grad(tokens, experts, k, logits.data_ptr(), ld, kind, rule, ids, dw,
-                                   out.data_ptr(), ld_d, _stream_of(stream))
-    if st != GEMM_OK:
+    st = _lib.gemm_route_grad(tokens, experts, k, logits.data_ptr(), ld, kind,
+                              RouteRule(score, 1 if renormalize else 0, scale, None, 1, 1, 1), ids,
+                              dw, out.data_ptr(), ld_d,
+                              _current_stream(now) if stream is None else _stream(stream))
+    if st:
         raise GemmError(st, "gemm_route_grad")
     return out
 
@@ -1009,28 +1048,24 @@ def combine(Y, position, weights=None, residual=None, out_dtype=None, out=None, 
     or None for 1.  D is float32 or Y's dtype (the default), residual of D's dtype.
     Without weights this is the gradient of a gather of rows.
     """
-    torch = _torch()
-    y_type = _value_type(Y, "Y")
-    if Y.dim() != 2 or position.dim() != 2:
-        raise ValueError("Y and position must be matrices")
-    rows, N = Y.shape
-    tokens, k = position.shape
+    y_type = _kind_of(Y, "Y")
+    rows, N = _two(Y, "Y")
+    pairs = _two(position, "position")
+    tokens, k = pairs
     device = Y.device
-    ldy = _row_major(Y, "Y")
-    at = _pairs(position, (tokens, k), torch.int32, "position", device)
-    w = None
-    if weights is not None:
-        w = _pairs(weights, (tokens, k), torch.float32, "weights", device)
+    ldy = _pitch(Y, rows, N, "Y", device)
+    at = _dense(position, pairs, _i32, "position", device)
+    w = None if weights is None else _dense(weights, pairs, _f32, "weights", device)
     if out is not None:
         if out_dtype is not None and out.dtype is not out_dtype:
             raise TypeError("out must have out_dtype")
         out_dtype = out.dtype
-        ldd = _matrix(out, (tokens, N), "out", device)
+        ldd = _pitch(out, tokens, N, "out", device)
     elif out_dtype is None:
         out_dtype = Y.dtype
     if out_dtype is Y.dtype:
         d_type = y_type
-    elif out_dtype is torch.float32:
+    elif out_dtype is _f32:
         d_type = GEMM_D_F32
     else:
         raise TypeError("the output must be float32 or Y's dtype")
@@ -1038,15 +1073,17 @@ def combine(Y, position, weights=None, residual=None, out_dtype=None, out=None, 
     if residual is not None:
         if residual.dtype is not out_dtype:
             raise TypeError("residual must have the output's dtype")
-        ld_r = _matrix(residual, (tokens, N), "residual", device)
+        ld_r = _pitch(residual, tokens, N, "residual", device)
         r = residual.data_ptr()
-    _on_device(device)
+    now = _here(device)
     if out is None:
-        out = _empty_for(stream)((tokens, N), dtype=out_dtype, device=device)
+        new = _new if stream is None else _empty_for(stream)
+        out = new((tokens, N), dtype=out_dtype, device=device)
         ldd = N
-    st = library().gemm_combine(tokens, k, N, Y.data_ptr(), ldy, rows, y_type, at, w, r, ld_r,
-                                out.data_ptr(), ldd, d_type, _stream_of(stream))
-    if st != GEMM_OK:
+    st = _lib.gemm_combine(tokens, k, N, Y.data_ptr(), ldy, rows, y_type, at, w, r, ld_r,
+                           out.data_ptr(), ldd, d_type,
+                           _current_stream(now) if stream is None else _stream(stream))
+    if st:
         raise GemmError(st, "gemm_combine")
     return out
 
@@ -1058,59 +1095,35 @@ def combine_grad(dD, Y, position, weights=None, weight_grad=True, out=None, stre
     dD is float32 or has Y's dtype.  Rows of dY (``out``, or a new tensor) that no
     position names are left as they are; the positions inside Y must differ.
     """
-    torch = _torch()
-    y_type, d_type = _value_type(Y, "Y"), _value_type(dD, "dD")
-    if Y.dim() != 2 or position.dim() != 2:
-        raise ValueError("Y and position must be matrices")
-    rows, N = Y.shape
-    tokens, k = position.shape
+    y_type, d_type = _kind_of(Y, "Y"), _kind_of(dD, "dD")
+    rows, N = _two(Y, "Y")
+    pairs = _two(position, "position")
+    tokens, k = pairs
     device = Y.device
     if d_type != y_type and d_type != GEMM_D_F32:
         raise TypeError("dD must be float32 or have Y's dtype")
-    ld_d = _matrix(dD, (tokens, N), "dD", device)
-    ldy = _row_major(Y, "Y")
-    at = _pairs(position, (tokens, k), torch.int32, "position", device)
-    w = None
-    if weights is not None:
-        w = _pairs(weights, (tokens, k), torch.float32, "weights", device)
+    ld_d = _pitch(dD, tokens, N, "dD", device)
+    ldy = _pitch(Y, rows, N, "Y", device)
+    at = _dense(position, pairs, _i32, "position", device)
+    w = None if weights is None else _dense(weights, pairs, _f32, "weights", device)
     if out is not None:
         if out.dtype is not Y.dtype:
             raise TypeError("out must have Y's dtype")
-        ld_dy = _matrix(out, (rows, N), "out", device)
-    _on_device(device)
-    empty = _empty_for(stream)
+        ld_dy = _pitch(out, rows, N, "out", device)
+    now = _here(device)
+    new = _new if stream is None else _empty_for(stream)
     if out is None:
-        out = empty((rows, N), dtype=Y.dtype, device=device)
+        out = new((rows, N), dtype=Y.dtype, device=device)
         ld_dy = N
-    dweights = empty((tokens, k), dtype=torch.float32, device=device) if weight_grad else None
+    dweights = new(pairs, dtype=_f32, device=device) if weight_grad else None
     if k > 0:
-        st = library().gemm_combine_grad(
+        st = _lib.gemm_combine_grad(
             tokens, k, N, dD.data_ptr(), ld_d, d_type, Y.data_ptr(), ldy, rows, y_type, at, w,
-            out.data_ptr(), ld_dy, dweights.data_ptr() if weight_grad else None, _stream_of(stream))
-        if st != GEMM_OK:
+            out.data_ptr(), ld_dy, dweights.data_ptr() if weight_grad else None,
+            _current_stream(now) if stream is None else _stream(stream))
+        if st:
             raise GemmError(st, "gemm_combine_grad")
     return out, dweights
-
-
-_FUSED_SUFFIX = ("f32", "bf16_f32acc", "f16_f32acc")  # by gemm_d_type_t
-
-
-def _fused_operands(A, B, out):
-    """(suffix, M, N, K, lda, order_a, ldb, order_b, device) of a fused product."""
-    kind = _value_type(A, "A")
-    if B.dtype is not A.dtype:
-        raise TypeError("the operands must share a dtype")
-    order_a, lda = storage_order(A)
-    order_b, ldb = storage_order(B)
-    (M, K), (kb, N) = A.shape, B.shape
-    if kb != K:
-        raise ValueError("inner dimensions differ")
-    device = A.device
-    if B.device != device:
-        raise ValueError("the operands must share a device")
-    if out is not None and out.dtype is not A.dtype:
-        raise TypeError("out must have the operands' dtype")
-    return _FUSED_SUFFIX[kind], M, N, K, lda, order_a, ldb, order_b, device
 
 
 def gemm_fused(A, B, bias=None, activation=GEMM_ACT_NONE, residual=None, keep_pre=False, alpha=1.0,
@@ -1121,31 +1134,44 @@ def gemm_fused(A, B, bias=None, activation=GEMM_ACT_NONE, residual=None, keep_pr
     A (M x K) and B (K x N) are row- or column-major, float32, bfloat16 or float16;
     bias float32 (N), residual (M x N) row-major (may be out).
     """
-    suffix, M, N, K, lda, order_a, ldb, order_b, device = _fused_operands(A, B, out)
-    b = _f32_dense(bias, (N,), "bias", device)
+    dtype = A.dtype
+    kind = _kind_of(A, "A")
+    if B.dtype is not dtype:
+        raise TypeError("the operands must share a dtype")
+    M, K = _two(A, "A")
+    kb, N = _two(B, "B")
+    if kb != K:
+        raise ValueError("inner dimensions differ")
+    order_a, lda = _order(A, M, K)
+    order_b, ldb = _order(B, K, N)
+    device = A.device
+    if B.device != device:
+        raise ValueError("the operands must share a device")
+    b = None if bias is None else _dense(bias, (N,), _f32, "bias", device)
     r, ld_r = None, 0
     if residual is not None:
-        if residual.dtype is not A.dtype:
+        if residual.dtype is not dtype:
             raise TypeError("residual must have the operands' dtype")
-        ld_r = _matrix(residual, (M, N), "residual", device)
+        ld_r = _pitch(residual, M, N, "residual", device)
         r = residual.data_ptr()
     if out is not None:
-        ldd = _matrix(out, (M, N), "out", device)
-    _on_device(device)
-    empty = _empty_for(stream)
+        if out.dtype is not dtype:
+            raise TypeError("out must have the operands' dtype")
+        ldd = _pitch(out, M, N, "out", device)
+    now = _here(device)
+    new = _new if stream is None else _empty_for(stream)
     if out is None:
-        out = empty((M, N), dtype=A.dtype, device=device)
-        ldd = max(N, 1)
+        out = new((M, N), dtype=dtype, device=device)
+        ldd = N or 1
     pre, z = None, None
     if keep_pre:
-        pre = empty((M, N), dtype=A.dtype, device=device)
+        pre = new((M, N), dtype=dtype, device=device)
         z = pre.data_ptr()
-    fn = "gemm_fused_" + suffix
-    st = getattr(library(), fn)(M, N, K, alpha, A.data_ptr(), lda, order_a, B.data_ptr(), ldb,
-                                order_b, out.data_ptr(), ldd,
-                                Fusion(b, activation, r, ld_r, z, max(N, 1)), _stream_of(stream))
-    if st != GEMM_OK:
-        raise GemmError(st, fn)
+    st = _fused_fns[kind](M, N, K, alpha, A.data_ptr(), lda, order_a, B.data_ptr(), ldb, order_b,
+                          out.data_ptr(), ldd, Fusion(b, activation, r, ld_r, z, N or 1),
+                          _current_stream(now) if stream is None else _stream(stream))
+    if st:
+        raise GemmError(st, _fused_fns[kind].__name__)
     return (out, pre) if keep_pre else out
 
 
@@ -1156,27 +1182,41 @@ def gemm_fused_grad(A, B, pre, activation=GEMM_ACT_NONE, bias_grad=False, alpha=
 
     pre (M x N, row-major, may be out) is what ``gemm_fused`` kept; None without activation.
     """
-    suffix, M, N, K, lda, order_a, ldb, order_b, device = _fused_operands(A, B, out)
+    dtype = A.dtype
+    kind = _kind_of(A, "A")
+    if B.dtype is not dtype:
+        raise TypeError("the operands must share a dtype")
+    M, K = _two(A, "A")
+    kb, N = _two(B, "B")
+    if kb != K:
+        raise ValueError("inner dimensions differ")
+    order_a, lda = _order(A, M, K)
+    order_b, ldb = _order(B, K, N)
+    device = A.device
+    if B.device != device:
+        raise ValueError("the operands must share a device")
     z, ld_z = None, 0
     if pre is not None:
-        if pre.dtype is not A.dtype:
+        if pre.dtype is not dtype:
             raise TypeError("pre must have the operands' dtype")
-        ld_z = _matrix(pre, (M, N), "pre", device)
+        ld_z = _pitch(pre, M, N, "pre", device)
         z = pre.data_ptr()
     elif activation != GEMM_ACT_NONE:
         raise ValueError("an activation's gradient needs pre")
     if out is not None:
-        ldd = _matrix(out, (M, N), "out", device)
-    _on_device(device)
-    empty = _empty_for(stream)
+        if out.dtype is not dtype:
+            raise TypeError("out must have the operands' dtype")
+        ldd = _pitch(out, M, N, "out", device)
+    now = _here(device)
+    new = _new if stream is None else _empty_for(stream)
     if out is None:
-        out = empty((M, N), dtype=A.dtype, device=device)
-        ldd = max(N, 1)
-    dbias = empty(N, dtype=_torch().float32, device=device) if bias_grad else None
-    fn = "gemm_fused_grad_" + suffix
-    st = getattr(library(), fn)(M, N, K, alpha, A.data_ptr(), lda, order_a, B.data_ptr(), ldb,
-                                order_b, activation, z, ld_z, out.data_ptr(), ldd,
-                                dbias.data_ptr() if bias_grad else None, _stream_of(stream))
-    if st != GEMM_OK:
-        raise GemmError(st, fn)
+        out = new((M, N), dtype=dtype, device=device)
+        ldd = N or 1
+    dbias = new(N, dtype=_f32, device=device) if bias_grad else None
+    st = _fused_grad_fns[kind](M, N, K, alpha, A.data_ptr(), lda, order_a, B.data_ptr(), ldb,
+                               order_b, activation, z, ld_z, out.data_ptr(), ldd,
+                               dbias.data_ptr() if bias_grad else None,
+                               _current_stream(now) if stream is None else _stream(stream))
+    if st:
+        raise GemmError(st, _fused_grad_fns[kind].__name__)
     return (out, dbias) if bias_grad else out
