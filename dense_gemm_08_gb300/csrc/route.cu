@@ -158,10 +158,11 @@ __device__ __forceinline__ F score_of(const RouteProblem &p, float x, F m, F inv
 // its equals the lowest number.  Lane r gets the r-th one's number (or -1).
 template <typename F, int VPT>
 __device__ __forceinline__ int in_rounds(const RouteProblem &p, int ept,
-                                         const typename Order<F>::Key (&key)[VPT], uint32_t out) {
+                                         const typename Order<F>::Key (&key)[VPT]) {
     using Key = typename Order<F>::Key;
     const int lane = threadIdx.x % 32;
     int mine = -1, at = 0;
+    uint32_t out = 0;  // bit i: taken
     Key best;
     auto look = [&]() {
         best = 0;
@@ -184,20 +185,18 @@ __device__ __forceinline__ int in_rounds(const RouteProblem &p, int ept,
     return mine;
 }
 
-// Scores and keys of the lane's experts, and which of them are out of the choice
-// because their group is (bit i of `out`).  most: the largest s + |b|, to which the
-// error of c in FP32 is in proportion.  FP32: false where two groups are too close.
+// Keys of the lane's experts, 0 where they or their groups are out of the choice.
+// tol: how far apart two c must be to differ for certain.  FP32: false where two
+// groups are too close.
 template <typename F, int VPT, bool VEC>
 __device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[VPT], int ept, F m,
-                                        F z, typename Order<F>::Key (&key)[VPT], uint32_t &out,
-                                        float &tol) {
+                                        F z, typename Order<F>::Key (&key)[VPT], float &tol) {
     using Key = typename Order<F>::Key;
     constexpr bool FAST = std::is_same<F, float>::value;
     const int lane = threadIdx.x % 32;
     const bool biased = p.bias != nullptr;
     const bool group_sums = p.groups > 1 && p.top == 2;
     Key by[VPT];  // what groups are compared by: c, or s for a sum without a bias
-    out = 0;
     tol = 0.f;
     if (biased || group_sums) {
         const F inv = z > 0 ? F(1) / z : (isnan(z) ? z : F(0));  // (0: every expert is masked)
@@ -283,6 +282,7 @@ __device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[
     if (lane >= p.groups) score = 0;
     // a group stays when fewer than groups_kept come before it
     int before = 0;
+#pragma unroll 4
     for (int g = 0; g < p.groups; ++g) {
         const Key o = __shfl_sync(kAll, score, g);
         before += o > score || (o == score && g < lane) ? 1 : 0;
@@ -290,11 +290,13 @@ __device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[
     const uint32_t kept = __ballot_sync(kAll, score != 0 && before < p.kept);
     const bool stays = (kept >> lane) & 1u;
     if (aligned) {
-        out = (kept >> (lane / lanes)) & 1u ? 0u : ~0u;
+        const bool mine = (kept >> (lane / lanes)) & 1u;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) key[i] = mine ? key[i] : Key(0);
     } else {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i < ept && !((kept >> ((lane * ept + i) / size & 31)) & 1u)) out |= 1u << i;
+            if (i < ept && !((kept >> ((lane * ept + i) / size & 31)) & 1u)) key[i] = 0;
     }
     if constexpr (FAST) {
         if (biased || group_sums) {
@@ -320,9 +322,8 @@ __device__ __noinline__ int choose_exactly(const RouteProblem &p, const void *ro
     double m = 0, z = 0;
     if (p.score == kSoftmax) softmax_stats<double>(x, m, z);
     Order<double>::Key key[VPT];
-    uint32_t out;
-    keys_of<double, VPT, VEC>(p, x, ept, m, z, key, out, tol);
-    return in_rounds<double>(p, ept, key, out);
+    keys_of<double, VPT, VEC>(p, x, ept, m, z, key, tol);
+    return in_rounds<double>(p, ept, key);
 }
 
 // The lane's candidate again in 64 bits: how many of the `total` come before it.
@@ -371,15 +372,12 @@ __device__ __forceinline__ bool choose(const RouteProblem &p, const void *row, c
                                        int &width) {
     const int lane = threadIdx.x % 32;
     const bool biased = p.bias != nullptr;
-    uint32_t key[VPT], out;
+    uint32_t key[VPT];
     float tol;
-    if (!keys_of<float, VPT, VEC>(p, x, ept, m, z, key, out, tol)) return false;
+    if (!keys_of<float, VPT, VEC>(p, x, ept, m, z, key, tol)) return false;
     uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if ((out >> i) & 1u) key[i] = 0;
-        best = max(best, key[i]);
-    }
+    for (int i = 0; i < VPT; ++i) best = max(best, key[i]);
 #pragma unroll
     for (int i = 0; i < VPT; i += 4) {
         if constexpr (VPT >= 4)
@@ -421,7 +419,7 @@ __device__ __forceinline__ bool choose(const RouteProblem &p, const void *row, c
     }
     if (total > 32) {
         if (biased) return false;
-        mine.expert = in_rounds<float>(p, ept, key, 0u);
+        mine.expert = in_rounds<float>(p, ept, key);
         mine.place = lane;
         mine.logit = mine.expert >= 0 ? Value<TYPE>::load(row, mine.expert) : 0.f;
         width = 32;
@@ -488,27 +486,22 @@ __device__ __forceinline__ float share(const RouteProblem &p, bool has, float x,
     return __fdividef(s, sum);
 }
 
+// (Register limits: many warps per SM hide the latency of each; the spills are in the
+// parts that run rarely.  Up to 256 experts 12 CTAs per SM: 16384 x 256 without a bias
+// 10.8 us, with 8 CTAs 11.6; CTAs that stay and load the next token ahead 14.4.)
 template <int TYPE, int VPT, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 8 : VPT <= 16 ? 5 : 3)
+__global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 12 : VPT <= 16 ? 5 : 3)
     route_kernel(const __grid_constant__ RouteProblem p) {
     __shared__ Slots<VPT> slots[kWarps];
     const int lane = threadIdx.x % 32;
     const int ept = VEC ? VPT : (p.experts + 31) / 32;
-    const int64_t step = gridDim.x * int64_t(kWarps);
-    int64_t t = blockIdx.x * int64_t(kWarps) + threadIdx.x / 32;
-    auto row_of = [&](int64_t i) -> const void * {
-        return static_cast<const uint8_t *>(p.logits) + i * p.ld * Value<TYPE>::BYTES;
-    };
     pdl_wait();
     pdl_launch_dependents();
-    float next[VPT];  // the next token's logits, under way while this one is chosen
-    if (t < p.tokens) load_row<TYPE, VPT, VEC>(p, row_of(t), ept, next);
-    for (; t < p.tokens; t += step) {
+    for (int64_t t = blockIdx.x * int64_t(kWarps) + threadIdx.x / 32; t < p.tokens;
+         t += gridDim.x * int64_t(kWarps)) {
+        const void *row = static_cast<const uint8_t *>(p.logits) + t * p.ld * Value<TYPE>::BYTES;
         float x[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) x[i] = next[i];
-        const void *row = row_of(t);
-        if (t + step < p.tokens) load_row<TYPE, VPT, VEC>(p, row_of(t + step), ept, next);
+        load_row<TYPE, VPT, VEC>(p, row, ept, x);
         const bool sums = p.bias != nullptr || (p.groups > 1 && p.top == 2);
         float m = 0.f, z = 0.f;
         if (p.score == kSoftmax && (sums || !p.renorm)) softmax_stats<float>(x, m, z);
@@ -610,16 +603,13 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
     }
 }
 
-// At most `most` CTAs (those of a pass of the whole GPU), whose warps then take
-// several tokens each.
 template <typename K>
-cudaError_t launch(K kernel, const RouteProblem &p, size_t smem, int64_t most,
-                   cudaStream_t stream) {
+cudaError_t launch(K kernel, const RouteProblem &p, size_t smem, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     set_pdl_attribute(&attr);
     cudaLaunchConfig_t cfg = {};
     const int64_t ctas = (p.tokens + kWarps - 1) / kWarps;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < (1 << 20) ? ctas : (1 << 20)), 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -632,9 +622,8 @@ template <int TYPE, int VPT>
 cudaError_t route_as(const RouteProblem &p, cudaStream_t stream) {
     // whole lanes of 16-byte (or smaller, whole) pieces
     const bool vec = p.experts == 32 * VPT && rows_on_16(p.logits, p.ld, Value<TYPE>::BYTES);
-    const int64_t most = int64_t(sm_count()) * (VPT <= 8 ? 8 : VPT <= 16 ? 5 : 3);
-    return vec ? launch(route_kernel<TYPE, VPT, true>, p, 0, most, stream)
-               : launch(route_kernel<TYPE, VPT, false>, p, 0, most, stream);
+    return vec ? launch(route_kernel<TYPE, VPT, true>, p, 0, stream)
+               : launch(route_kernel<TYPE, VPT, false>, p, 0, stream);
 }
 
 template <int TYPE>
@@ -652,8 +641,8 @@ cudaError_t route_grad_of(const RouteProblem &p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>((p.experts + 7) / 8 * 8) * kWarps * sizeof(float);
     const bool vec = p.experts % Value<TYPE>::PER_16 == 0 &&
                      rows_on_16(p.dlogits, p.ld_d, Value<TYPE>::BYTES);
-    return vec ? launch(route_grad_kernel<TYPE, true>, p, smem, 1 << 20, stream)
-               : launch(route_grad_kernel<TYPE, false>, p, smem, 1 << 20, stream);
+    return vec ? launch(route_grad_kernel<TYPE, true>, p, smem, stream)
+               : launch(route_grad_kernel<TYPE, false>, p, smem, stream);
 }
 
 }  // namespace

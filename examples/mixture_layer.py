@@ -2,11 +2,11 @@
 on the library's grouped operators.
 
     h   = x W + s (x LA_a) LB_a          a = the request's adapter     gemm_lora
-    e   = the top experts of each token, by the router's scores
+    e, weight = the top experts of each token, by the router's scores  route
     off, order, pos = rows grouped by expert                           group_rows
     u   = gelu(h[token] W1_e + b1_e)     rows gathered by token        gemm_grouped
     y   = u W2_e                                                       gemm_grouped
-    out = sum over a token's experts of weight * y
+    out = sum over a token's experts of weight * y                     combine
 
 `forward` serves (any number of tokens, one included); `gradients` is the
 backward pass of the expert layers without the activation: the grouped products
@@ -42,10 +42,9 @@ def make(width=1024, hidden=2048, experts=16, adapters=8, rank=16, dtype=torch.b
 def route(p, h, top):
     """Experts of each token's rows, grouped: (offsets, token of each row, place, weights)."""
     scores = lib.gemm(h, p["router"])  # FP32
-    weights, chosen = torch.topk(torch.softmax(scores, -1), top)
-    experts = p["W1"].shape[0]
-    offsets, order, place = lib.group_rows(chosen.to(torch.int32).flatten(), experts)
-    return offsets, order // top, place.long(), weights
+    chosen, weights = lib.route(scores, top, renormalize=False)
+    offsets, order, place = lib.group_rows(chosen.view(-1), p["W1"].shape[0])
+    return offsets, order // top, place, weights
 
 
 def forward(p, x, adapter, top=2):
@@ -55,7 +54,7 @@ def forward(p, x, adapter, top=2):
     u = lib.gemm_grouped(h, p["W1"].transpose(1, 2), offsets, row_index=token, bias=p["b1"],
                          activation=lib.GEMM_ACT_GELU)
     y = lib.gemm_grouped(u, p["W2"].transpose(1, 2), offsets, out_dtype=torch.float32)
-    return (y[place].view(*weights.shape, -1) * weights[..., None]).sum(1)
+    return lib.combine(y, place.view_as(weights), weights=weights)
 
 
 def gradients(p, h, offsets, token, dv):
