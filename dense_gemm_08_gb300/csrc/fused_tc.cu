@@ -20,6 +20,7 @@
 // stores.
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "fused.cuh"
 #include "internal.h"
@@ -35,7 +36,6 @@ using namespace tc;
 constexpr int kGroupM = 16;     // tile rows per band of the raster
 constexpr int kMaxStages = 16;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kProducer = kEpiWarps, kIssuer = kEpiWarps + 1;
 constexpr int kBox = 4096;      // 32 rows of 64 16-bit values
 constexpr int kBody = 224 * 1024;  // ring and boxes
@@ -46,10 +46,32 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr int kMaxSplit = 8;
 constexpr int kSlot = 8192;     // 32 x 64 FP32 sums of another piece
 
+// Column sums of a long K: sums in parts.  The tensor cores cut what an addition to
+// the accumulator cannot hold (they do not round it), so that a sum comes out smaller
+// by 1e-9 of itself per step of K.  A D of 16 bits does not show it, the FP32 sums of
+// its columns do (4.5e-6 at K = 4096, 0.6e-6 for FP32 products).  Where they are
+// wanted and a tile's K is longer than kUncut (an error of 2e-6), each part of kPart
+// is summed in the other accumulator and the epilogue warps add the parts in
+// registers: 1.2e-6 at any K.  The 128 registers per thread that this takes come from
+// the other warps.  (Measured at 4096 x 14336 x 4096: parts of 768 and 1024, whose
+// multiplication is over before the last tile's epilogue, take 670 and 633 us, of
+// 1280 578, of 1536 and 2048 563 us with errors of 1.4e-6 and 2.1e-6; one part 573.
+// At K = 1408 two parts take 20.8 us, one 18.5: an error of 1.7e-6.)
+constexpr int kPart = 1280, kUncut = 2048;
+static_assert(kPart % (4 * BK) == 0, "a part is a number of steps");
+constexpr int kEpiRegs = 216, kOtherRegs = 72, kPartsRegs = 168;
+static_assert(2 * kEpiRegs + kOtherRegs <= 3 * kPartsRegs,
+              "three warpgroups share the launch's registers");
+template <bool PARTS>
+constexpr int threads() {
+    return PARTS ? 384 : 64 + 32 * kEpiWarps;
+}
+
 struct Args {
     int64_t M, N;
     uint32_t tiles_m, tiles_n;
     int num_kb, ksub, ks;  // steps of K (stages), blocks of 64 per step, pieces
+    int part_steps;        // of K
     int bn, am;
     int stages, ring_bytes, boxes;
     uint32_t stage_bytes, a_region;
@@ -138,9 +160,9 @@ __device__ __forceinline__ void activate_16(float (&v)[16]) {
     for (int j = 0; j < 16; ++j) v[j] = quick_activation<ACT>(v[j]);
 }
 template <int ACT>
-__device__ __forceinline__ void slope_16(float (&v)[16], const float (&z)[16]) {
+__device__ __forceinline__ void slope_8(float *v, const float (&z)[8]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= quick_slope<ACT>(z[j]);
+    for (int j = 0; j < 8; ++j) v[j] *= quick_slope<ACT>(z[j]);
 }
 
 // The sum of the 32 lanes' v[j] for column j = lane / 2, in a fixed order.
@@ -236,8 +258,8 @@ __device__ __forceinline__ void rows_to_box(uint32_t box, const void *from, int6
     }
 }
 
-template <int CG, bool SPLIT, bool GRAD, int TYPE>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int CG, bool SPLIT, bool GRAD, int TYPE, bool PARTS>
+__global__ void __launch_bounds__(threads<PARTS>(), 1)
     fused_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                     const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_b_edge,
@@ -246,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap map_pre,
                     const __grid_constant__ Args args) {
     static_assert(!SPLIT || CG == 1, "K is split over single CTAs");
+    static_assert(!PARTS || (GRAD && !SPLIT), "parts are for column sums");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -316,6 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return done;
     };
 
+    if constexpr (PARTS) {
+        if (warp >= kEpiWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    }
     if (warp == kProducer) {
         // -------------------------------------------------------- TMA producer
         const uint32_t count0 = CG == 1 ? full0 : map_to_rank(full0, 0);
@@ -405,18 +431,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, acc = 0;
             bool ok = true;
             for (uint32_t w = first_tile; ok && get_tile<CG>(args, w, t); w += tile_step) {
-                ok = wait_all(tempty0 + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1);
+                uint32_t d_tmem = 0;
+                auto take = [&]() {  // the accumulator not filled last, once it has been read
+                    ok = wait_all(tempty0 + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1);
+                    tc_fence_after();
+                    d_tmem = tmem_base + (acc & 1) * 256;
+                };
+                take();
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (acc & 1) * 256;
-                for (int i = 0; i < nkb; ++i) {
+                int in_part = 0;
+                for (int i = 0; i < nkb; ++i, ++in_part) {
+                    if (PARTS && in_part == args.part_steps) {
+                        if (elect_one()) tc_commit<CG>(tfull0 + 8 * (acc & 1));
+                        ++acc;
+                        take();
+                        if (!ok) break;
+                        in_part = 0;
+                    }
                     ok = wait_all(full0 + 8 * stage, phase);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage) * stage_step;
                     const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage) * stage_step;
                     if (elect_one()) {
-                        tc_mma<CG>(d_tmem, ad, bd, idesc, i > 0 ? 1u : 0u);
+                        tc_mma<CG>(d_tmem, ad, bd, idesc, in_part > 0 ? 1u : 0u);
                         tc_mma<CG>(d_tmem, ad + a_step, bd + b_step, idesc, 1u);
                         tc_mma<CG>(d_tmem, ad + 2 * a_step, bd + 2 * b_step, idesc, 1u);
                         tc_mma<CG>(d_tmem, ad + 3 * a_step, bd + 3 * b_step, idesc, 1u);
@@ -450,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }
 
+    if (SPLIT || warp < kEpiWarps) {
+    if constexpr (PARTS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // Epilogue warps: two per quarter of the TMEM lanes, each takes every other
     // block of 64 columns.
     const int e = warp, quarter = warp % 4, half = (e / 4) & 1;
@@ -486,6 +526,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         pending = true;
     };
 
+    // Before a block is written: its box of residual / pre is there, and the boxes of
+    // the block before have left.  False: gave up.
+    auto open_block = [&](int64_t c0, int width) -> bool {
+        if (has_in) {
+            if (args.tma_in) {
+                if (!pending) fetch_in(row0, c0);
+                if (!wait_all(ibar, blocks_in & 1)) return false;
+                ++blocks_in;
+                pending = false;
+            } else {
+                rows_to_box(box_in, args.in, args.ld_in, row0, nrows, c0, width, args.even_in != 0);
+                __syncwarp();
+            }
+        }
+        if (elect_one()) bulk_wait_read();
+        __syncwarp();
+        return true;
+    };
+    // After: next() fetches the next box, the written ones go to memory.
+    auto close_block = [&](int64_t c0, int width, auto &&next) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (has_in && args.tma_in) next();
+        // (TMA stores whole 16-byte pieces, and its box is 64 columns wide: a block with
+        // an odd end, or cut by the tile's, goes by rows)
+        const bool whole = width == 64 || (args.N % 8 == 0 && c0 + width == args.N);
+        if (args.tma_d && whole) {
+            if (elect_one())
+                tma_store_2d(&map_d, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_d);
+        } else {
+            box_to_rows(box_d, args.D, args.ldd, row0, nrows, c0, width, args.even_d != 0);
+        }
+        if (has_pre) {
+            if (args.tma_pre && whole) {
+                if (elect_one())
+                    tma_store_2d(&map_pre, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_pre);
+            } else {
+                box_to_rows(box_pre, args.pre, args.ld_pre, row0, nrows, c0, width, args.even_pre != 0);
+            }
+        }
+        __syncwarp();
+    };
+
+    // Gradient: sixteen values times the slopes at pre's, from column h * 16 of the block.
+    auto times_slopes = [&](float (&v)[16], int h) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float x[8];
+            widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2 + p)), x);
+            if (args.act == kActGelu)
+                slope_8<kActGelu>(v + p * 8, x);
+            else if (args.act == kActSilu)
+                slope_8<kActSilu>(v + p * 8, x);
+            else if (args.act == kActRelu)
+                slope_8<kActRelu>(v + p * 8, x);
+        }
+    };
+    // The sums of those sixteen columns over the block's rows.
+    auto add_columns = [&](float (&v)[16], int64_t c0, int h, int width) {
+        if (lane >= nrows) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        }
+        const float sum = column_sum(v);
+        const int c = h * 16 + lane / 2;
+        if (lane % 2 == 0 && c < width) args.part[row0 / 32 * args.N + c0 + c] = sum;
+    };
+
     // One block: 64 columns from tile column b * 64 on.  sums(h, v): the product's
     // columns h * 16 .. of this lane's row; after(): all sums have been read; next():
     // fetches the next box.  False: gave up.  (Sixteen columns at a time, in a loop
@@ -500,19 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < width) bias2[0] = __ldg(args.bias + c0 + lane);
             if (lane + 32 < width) bias2[1] = __ldg(args.bias + c0 + lane + 32);
         }
-        if (has_in) {
-            if (args.tma_in) {
-                if (!pending) fetch_in(row0, c0);
-                if (!wait_all(ibar, blocks_in & 1)) return false;
-                ++blocks_in;
-                pending = false;
-            } else {
-                rows_to_box(box_in, args.in, args.ld_in, row0, nrows, c0, width, args.even_in != 0);
-                __syncwarp();
-            }
-        }
-        if (elect_one()) bulk_wait_read();  // the boxes of the last block have left
-        __syncwarp();
+        if (!open_block(c0, width)) return false;
 #pragma unroll 1
         for (int h = 0; h * 16 < in_tile; ++h) {
             if (!GRAD && args.bias != nullptr && (h & 1) == 0) {
@@ -546,55 +642,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     activate_16<kActRelu>(v);
             }
             if (has_in) {
-                float x[16];
-                widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2)), x);
-                widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2 + 1)), x + 8);
                 if constexpr (GRAD) {
-                    if (args.act == kActGelu)
-                        slope_16<kActGelu>(v, x);
-                    else if (args.act == kActSilu)
-                        slope_16<kActSilu>(v, x);
-                    else if (args.act == kActRelu)
-                        slope_16<kActRelu>(v, x);
+                    times_slopes(v, h);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] += x[j];
+                    for (int p = 0; p < 2; ++p) {
+                        float x[8];
+                        widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2 + p)), x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[p * 8 + j] += x[j];
+                    }
                 }
             }
             narrow_16<TYPE>(v, box_d, lane, h);
-            if constexpr (GRAD) {
-                if (args.part != nullptr) {
-                    if (lane >= nrows) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
-                    }
-                    const float sum = column_sum(v);
-                    const int c = h * 16 + lane / 2;
-                    if (lane % 2 == 0 && c < width) args.part[row0 / 32 * args.N + c0 + c] = sum;
-                }
-            }
+            if (GRAD && args.part != nullptr) add_columns(v, c0, h, width);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (has_in && args.tma_in) next();
-        // (TMA stores whole 16-byte pieces, and its box is 64 columns wide: a block with
-        // an odd end, or cut by the tile's, goes by rows)
-        const bool whole = width == 64 || (args.N % 8 == 0 && c0 + width == args.N);
-        if (args.tma_d && whole) {
-            if (elect_one())
-                tma_store_2d(&map_d, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_d);
-        } else {
-            box_to_rows(box_d, args.D, args.ldd, row0, nrows, c0, width, args.even_d != 0);
-        }
-        if (has_pre) {
-            if (args.tma_pre && whole) {
-                if (elect_one())
-                    tma_store_2d(&map_pre, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_pre);
-            } else {
-                box_to_rows(box_pre, args.pre, args.ld_pre, row0, nrows, c0, width, args.even_pre != 0);
-            }
-        }
-        __syncwarp();
+        close_block(c0, width, next);
         return true;
     };
 
@@ -603,15 +666,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t acc = 0;
             for (uint32_t w = first_tile; get_tile<CG>(args, w, t); w += tile_step) {
                 place(t, row0, nrows, n_blocks);
-                const uint32_t buf = acc & 1, t_acc = tmem_base + lane_off + buf * 256;
                 const int last = n_blocks > half ? half + (n_blocks - 1 - half) / 2 * 2 : -1;
                 if (has_in && args.tma_in && last >= 0 && !pending) fetch_in(row0, t.n0 + half * 64);
-                if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) {
-                    aborted = true;
-                    break;
-                }
-                tc_fence_after();
-                ++acc;
+                uint32_t buf = 0, t_acc = 0;  // the accumulator being read
+                auto next_acc = [&]() -> bool {
+                    buf = acc & 1;
+                    t_acc = tmem_base + lane_off + buf * 256;
+                    if (!wait_all(tfull0 + 8 * buf, (acc >> 1) & 1)) return false;
+                    tc_fence_after();
+                    ++acc;
+                    return true;
+                };
                 auto release_acc = [&]() {
                     tc_fence_before();
                     __syncwarp();
@@ -622,6 +687,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_arrive_cluster(map_to_rank(tempty0 + 8 * buf, 0));
                     }
                 };
+                auto fetch_next = [&](int b) {  // the box after block b's
+                    if (b != last) {
+                        fetch_in(row0, t.n0 + (b + 2) * 64);
+                        return;
+                    }
+                    Tile u;  // the next tile's first block
+                    int64_t r0;
+                    int rows, blocks;
+                    if (!get_tile<CG>(args, w + tile_step, u)) return;
+                    place(u, r0, rows, blocks);
+                    if (blocks > half) fetch_in(r0, u.n0 + half * 64);
+                };
+                if constexpr (PARTS) {
+                    // the parts' sums of this warp's four times 32 columns (indices fixed
+                    // at compile time)
+                    float run[4][32] = {};
+                    for (int from = 0; from < nkb; from += args.part_steps) {
+                        if (!next_acc()) {
+                            aborted = true;
+                            break;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (half + 2 * (q / 2) > last) continue;
+                            uint32_t raw[32];
+                            __syncwarp();
+                            tmem_load_32cols(t_acc + (half + 2 * (q / 2)) * 64 + q % 2 * 32, raw);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) run[q][j] += __uint_as_float(raw[j]);
+                        }
+                        release_acc();
+                    }
+                    // (By way of shared memory, which the multiplication keeps busy, this took
+                    // 18 us a tile, and eight columns at a time 14; this takes 10.)
+#pragma unroll 1
+                    for (int g = 0; g < 8 && !aborted; ++g) {
+                        const int b = half + 2 * (g / 4), h = g % 4;
+                        if (b > last) break;
+                        const int64_t c0 = t.n0 + b * 64;
+                        const int in_tile = args.bn - b * 64 < 64 ? args.bn - b * 64 : 64;
+                        const int width = args.N - c0 < in_tile ? static_cast<int>(args.N - c0) : in_tile;
+                        if (h == 0 && !open_block(c0, width)) {
+                            aborted = true;
+                            break;
+                        }
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (i != g) continue;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = args.alpha * run[i / 2][i % 2 * 16 + j];
+                        }
+                        if (has_in) times_slopes(v, h);
+                        narrow_16<TYPE>(v, box_d, lane, h);
+                        add_columns(v, c0, h, width);
+                        if (h == 3) close_block(c0, width, [&]() { fetch_next(b); });
+                    }
+                    if (aborted) break;
+                    continue;
+                }
+                if (!next_acc()) {
+                    aborted = true;
+                    break;
+                }
                 for (int b = half; b < n_blocks && !aborted; b += 2) {
                     aborted = !finish_block(
                         b,
@@ -632,18 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         [&]() {
                             if (b == last) release_acc();
                         },
-                        [&]() {
-                            if (b != last) {
-                                fetch_in(row0, t.n0 + (b + 2) * 64);
-                                return;
-                            }
-                            Tile u;  // the next tile's first block
-                            int64_t r0;
-                            int rows, blocks;
-                            if (!get_tile<CG>(args, w + tile_step, u)) return;
-                            place(u, r0, rows, blocks);
-                            if (blocks > half) fetch_in(r0, u.n0 + half * 64);
-                        });
+                        [&]() { fetch_next(b); });
                 }
                 if (aborted) break;
                 if (last < 0) release_acc();
@@ -730,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) bulk_wait_all();
         __syncwarp();
     }
+    }
 
     if (aborted) {
         // give copies issued by a peer that gave up a short time to land
@@ -749,11 +868,11 @@ constexpr int64_t kMaxTiles = int64_t(1) << 30;  // the tile arithmetic is 32-bi
 
 std::atomic<bool> g_launched[kMaxDevices];
 
-template <int CG, bool SPLIT, bool GRAD, int TYPE>
+template <int CG, bool SPLIT, bool GRAD, int TYPE, bool PARTS>
 cudaLaunchConfig_t config(int grid, int cluster, cudaStream_t stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(threads<PARTS>(), 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -773,12 +892,19 @@ struct Prepared {
     cudaError_t err = cudaSuccess;
     int resident[kMaxSplit + 1] = {};
 };
-template <int CG, bool SPLIT, bool GRAD, int TYPE>
+template <int CG, bool SPLIT, bool GRAD, int TYPE, bool PARTS>
 const Prepared &prepared(int dev) {
     static Prepared all[kMaxDevices];
     Prepared &p = all[dev];
     std::call_once(p.once, [&p, dev] {
-        const auto kernel = fused_tc_kernel<CG, SPLIT, GRAD, TYPE>;
+        const auto kernel = fused_tc_kernel<CG, SPLIT, GRAD, TYPE, PARTS>;
+        if (PARTS) {
+            // the warpgroups divide what the launch gives: without it they would wait
+            cudaFuncAttributes at;
+            p.err = cudaFuncGetAttributes(&at, kernel);
+            if (p.err == cudaSuccess && at.numRegs != kPartsRegs) p.err = cudaErrorInvalidKernelImage;
+            if (p.err != cudaSuccess) return;
+        }
         p.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (p.err != cudaSuccess) return;
         int sms = 0;
@@ -787,7 +913,7 @@ const Prepared &prepared(int dev) {
         p.resident[1] = sms > 0 ? sms : 1;
         for (int c = 2; c <= (CG == 2 ? 2 : SPLIT ? kMaxSplit : 1); c *= 2) {
             cudaLaunchAttribute attr[2];
-            cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD, TYPE>(c, c, 0, attr);
+            cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD, TYPE, PARTS>(c, c, 0, attr);
             cfg.attrs = attr + 1;  // the occupancy query takes the cluster shape only
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&p.resident[c], kernel, &cfg) != cudaSuccess) {
@@ -803,13 +929,13 @@ struct Maps {
     CUtensorMap a, b, b_edge, in, d, pre;
 };
 
-template <int CG, bool SPLIT, bool GRAD, int TYPE>
+template <int CG, bool SPLIT, bool GRAD, int TYPE, bool PARTS>
 cudaError_t launch_as(const Maps &m, const Args &a, int dev, int grid, int cluster,
                       cudaStream_t stream) {
     g_launched[dev].store(true);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD, TYPE>(grid, cluster, stream, attr);
-    return cudaLaunchKernelEx(&cfg, fused_tc_kernel<CG, SPLIT, GRAD, TYPE>, m.a, m.b, m.b_edge, m.in, m.d,
+    cudaLaunchConfig_t cfg = config<CG, SPLIT, GRAD, TYPE, PARTS>(grid, cluster, stream, attr);
+    return cudaLaunchKernelEx(&cfg, fused_tc_kernel<CG, SPLIT, GRAD, TYPE, PARTS>, m.a, m.b, m.b_edge, m.in, m.d,
                               m.pre, a);
 }
 
@@ -847,6 +973,7 @@ int sub_blocks(const FusedProblem &p, const Cut &c) {
 //                         64 columns of 128 rows
 //   all operands          once at 6.4 TB/s; tiles of 32 columns read at 0.6 of that
 Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &split, int sms) {
+    const bool sums = p.grad && p.dbias != nullptr;
     const int64_t kb = ceil_div(p.K, BK);
     const double bytes = 2.0 * (static_cast<double>(p.M) * p.K + static_cast<double>(p.K) * p.N);
     Cut best = {1, BM, 256, 1};
@@ -859,12 +986,12 @@ Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &spli
         const double l2 = (c.am + c.bn / c.cg) * 128 / 109e3, issue = 0.16 / sub_blocks(p, c);
         block = l2 > block ? l2 : block;
         block = issue > block ? issue : block;
-        const double sum = static_cast<double>(ceil_div(kb, c.ks)) * block;
+        const double multiply = static_cast<double>(ceil_div(kb, c.ks)) * block;
         const double epilogue = 3.0 + 1.7 * (c.bn == 32 ? 0.5 : (c.bn + 127) / 128);
         const double reads = bytes / (c.bn == 32 ? 3.8e6 : 6.4e6);
-        double sums = (rounds - 1) * (sum > epilogue ? sum : epilogue) + sum;
-        if (reads > sums) sums = reads;
-        const double cost = 2.0 + (c.cg == 2 ? 1.7 : 0.0) + sums + epilogue +
+        double whole = (rounds - 1) * (multiply > epilogue ? multiply : epilogue) + multiply;
+        if (reads > whole) whole = reads;
+        const double cost = 2.0 + (c.cg == 2 ? 1.7 : 0.0) + whole + epilogue +
                             (c.ks > 1 ? 2.0 + 1.5 * ((c.bn + 63) / 64) * c.am / BM : 0.0);
         if (cost < least) least = cost, best = c;
     };
@@ -876,6 +1003,7 @@ Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &spli
         consider({1, am, bn, 1}, sms);
         for (int ks = 2; ks <= kMaxSplit; ks *= 2) {
             const int64_t tiles = ceil_div(p.M, am) * ceil_div(p.N, bn);
+            if (sums && p.K > static_cast<int64_t>(kUncut) * ks) continue;
             if (kb >= 2 * ks && tiles <= split.resident[ks]) consider({1, am, bn, ks}, split.resident[ks]);
         }
     }
@@ -893,8 +1021,9 @@ template <bool GRAD, int TYPE>
 static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t stream,
                                 const char **name) {
     constexpr bool bf16 = TYPE == kOutBf16;
-    const Prepared &pair = prepared<2, false, GRAD, TYPE>(dev), &one = prepared<1, false, GRAD, TYPE>(dev),
-                   &split = prepared<1, true, GRAD, TYPE>(dev);
+    const Prepared &pair = prepared<2, false, GRAD, TYPE, false>(dev);
+    const Prepared &one = prepared<1, false, GRAD, TYPE, false>(dev);
+    const Prepared &split = prepared<1, true, GRAD, TYPE, false>(dev);
     for (const Prepared *q : {&pair, &one, &split})
         if (q->err != cudaSuccess) return q->err;
     const Cut cut = choose_cut(p, pair, split, one.resident[1]);
@@ -906,6 +1035,7 @@ static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t str
     a.ks = cut.ks;
     a.ksub = sub_blocks(p, cut);
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
+    a.part_steps = kPart / (BK * a.ksub);
     a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, cut.am * cut.cg));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, cut.bn));
     a.a_kmajor = p.a_kmajor;
@@ -974,14 +1104,24 @@ static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t str
                                              {"fused_tc<f16,pair>", "fused_tc<bf16,pair>"},
                                              {"fused_tc<f16,split>", "fused_tc<bf16,split>"}};
     *name = kNames[cut.ks > 1 ? 2 : cut.cg - 1][bf16];
-    if (cut.cg == 2) {
-        const int64_t n = tiles < pair.resident[2] ? tiles : pair.resident[2];
-        e = launch_as<2, false, GRAD, TYPE>(m, a, dev, static_cast<int>(2 * n), 2, stream);
-    } else if (cut.ks > 1) {
-        e = launch_as<1, true, GRAD, TYPE>(m, a, dev, static_cast<int>(tiles * cut.ks), cut.ks, stream);
-    } else {
-        const int64_t n = tiles < one.resident[1] ? tiles : one.resident[1];
-        e = launch_as<1, false, GRAD, TYPE>(m, a, dev, static_cast<int>(n), 1, stream);
+    // a pair, or one CTA, takes tile after tile (all variants fill an SM: as many run)
+    const auto launch_tiles = [&](auto parts) -> cudaError_t {
+        constexpr bool PARTS = decltype(parts)::value;
+        const Prepared &q = cut.cg == 2 ? prepared<2, false, GRAD, TYPE, PARTS>(dev)
+                                        : prepared<1, false, GRAD, TYPE, PARTS>(dev);
+        if (q.err != cudaSuccess) return q.err;
+        const int n = static_cast<int>(tiles < q.resident[cut.cg] ? tiles : q.resident[cut.cg]);
+        if (n == 0) return cudaErrorInvalidConfiguration;
+        return cut.cg == 2 ? launch_as<2, false, GRAD, TYPE, PARTS>(m, a, dev, 2 * n, 2, stream)
+                           : launch_as<1, false, GRAD, TYPE, PARTS>(m, a, dev, n, 1, stream);
+    };
+    if (e == cudaSuccess) {
+        if (cut.ks > 1)
+            e = launch_as<1, true, GRAD, TYPE, false>(m, a, dev, static_cast<int>(tiles * cut.ks), cut.ks, stream);
+        else if constexpr (GRAD)
+            e = p.dbias != nullptr && p.K > kUncut ? launch_tiles(std::true_type{}) : launch_tiles(std::false_type{});
+        else
+            e = launch_tiles(std::false_type{});
     }
     if (ws != nullptr) {
         if (e == cudaSuccess) e = launch_column_sums(a.part, blocks, p.N, p.dbias, stream);
@@ -997,11 +1137,12 @@ cudaError_t launch_fused_tc(const FusedProblem &p, InType in, cudaStream_t strea
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (in == InType::BF16)
-        return p.grad ? launch_tc_as<true, kOutBf16>(p, dev, stream, name)
-                      : launch_tc_as<false, kOutBf16>(p, dev, stream, name);
-    return p.grad ? launch_tc_as<true, kOutF16>(p, dev, stream, name)
-                  : launch_tc_as<false, kOutF16>(p, dev, stream, name);
+    const bool bf16 = in == InType::BF16;
+    if (!p.grad)
+        return bf16 ? launch_tc_as<false, kOutBf16>(p, dev, stream, name)
+                    : launch_tc_as<false, kOutF16>(p, dev, stream, name);
+    return bf16 ? launch_tc_as<true, kOutBf16>(p, dev, stream, name)
+                : launch_tc_as<true, kOutF16>(p, dev, stream, name);
 }
 
 cudaError_t fused_tc_read_and_clear_status(cudaStream_t stream, int *status) {

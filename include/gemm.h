@@ -544,7 +544,7 @@ gemm_status_t gemm_combine(int64_t tokens, int64_t k, int64_t N, const void *Y, 
  *
  * dD is tokens x N of d_type (GEMM_D_F32 or y_type), dY rows_y x N of y_type.
  * The positions inside [0, rows_y) must differ from one another, as
- * gemm_group_rows's do (of a row named twice, dY holds one of the two);
+ * gemm_group_rows's do (of a row named twice, each element of dY is one of the two's);
  * entries outside have dweights = 0.  Rows of dY that no position names are
  * left as they are.  weights NULL: all 1.  dY or dweights may be NULL (not
  * computed); Y is read for dweights only, and NULL without it.  dY must not
@@ -616,8 +616,13 @@ gemm_status_t gemm_fused_f16_f32acc(int64_t M, int64_t N, int64_t K, float alpha
  * gradient of a residual block, and the weight gradients are plain products.
  * pre is M x N of the inputs' type and may be D (the same pitch); it is not
  * read when the activation is GEMM_ACT_NONE (NULL allowed).  act' of ReLU is 0
- * at 0; a NaN in pre gives NaN.  dbias may be NULL.
- * M == 0 with N > 0: dbias = 0.
+ * at 0; a NaN in pre gives NaN.  dbias may be NULL; it must not overlap
+ * another matrix of the call.  M == 0 with N > 0: dbias = 0.
+ * Kernels and D's accuracy are gemm_fused_*'s (the largest slope's factor is
+ * the slope's own).  The tensor cores cut an accumulator's last place where
+ * others round it: a tile's sum is smaller by 1e-9 of itself per step of K,
+ * which only dbias shows (2e-6).  Where dbias is wanted K is summed in parts
+ * for that reason, so that D's last bit may differ from a call without it.
  */
 gemm_status_t gemm_fused_grad_f32(int64_t M, int64_t N, int64_t K, float alpha, const float *A,
                                   int64_t lda, gemm_order_t order_a, const float *B, int64_t ldb,
@@ -643,8 +648,9 @@ const char *gemm_status_string(gemm_status_t status);
 /*
  * gemm_last_device_status -- synchronises `stream`, then reads and clears
  * the current device's status word.  Returns GEMM_OK, or GEMM_ERR_TIMEOUT if
- * a tensor-core launch on this device gave up a bounded wait since the last
- * read (its D is then incomplete), or GEMM_ERR_INTERNAL if the read itself
+ * a tensor-core launch (or one of gemm_combine's and gemm_combine_grad's that
+ * copy rows in bulk) on this device gave up a bounded wait since the last
+ * read (its results are then incomplete), or GEMM_ERR_INTERNAL if the read itself
  * failed.  After a timeout it also synchronises the device and frees every
  * stream's split counters (the counts of finished K pieces that each stream
  * keeps between calls, and that a kernel which gave up may have left
