@@ -467,13 +467,16 @@ __device__ __forceinline__ float log_sigmoid(float x) {
     return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
 }
 
+// (of equal numbers 1, exactly: a single expert's share; the gradient through it is 0)
+__device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f : __fdividef(a, b); }
+
 // The lane's share of the chosen experts' scores (lanes with `has`, all below
 // `width`): s_j / sum s.  Scores too small for FP32 keep their ratios.
 __device__ __forceinline__ float share(const RouteProblem &p, bool has, float x, int width) {
     if (p.score == kSoftmax) {
         const float m = warp_max(has ? x : -INFINITY, width);
         const float e = has ? expf(x - m) : 0.f;
-        return __fdividef(e, warp_sum(e, width));
+        return ratio(e, warp_sum(e, width));
     }
     const float s = has ? __fdividef(1.f, 1.f + expf(-x)) : 0.f;
     const float sum = __shfl_sync(kAll, warp_sum(s, width), 0);
@@ -481,9 +484,9 @@ __device__ __forceinline__ float share(const RouteProblem &p, bool has, float x,
         const float l = has ? log_sigmoid(x) : -INFINITY;
         const float m = warp_max(l, width);
         const float e = has ? expf(l - m) : 0.f;
-        return __fdividef(e, warp_sum(e, width));
+        return ratio(e, warp_sum(e, width));
     }
-    return __fdividef(s, sum);
+    return ratio(s, sum);
 }
 
 // (Register limits: many warps per SM hide the latency of each; the spills are in the
@@ -558,6 +561,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
         if (lane < p.k) e = p.chosen[t * p.k + lane];
         const bool has = e >= 0 && e < p.experts;
         const float x = has ? V::load(row, e) : 0.f;
+        // an expert named twice: its terms are added in the order of the names
+        if (has) mine[e] = __int_as_float(lane);
+        __syncwarp();
+        const bool twice = __any_sync(kAll, has && __float_as_int(mine[e]) != lane);
+        __syncwarp();
         const float dw = has ? p.dweights[t * p.k + lane] * p.scale : 0.f;
         float dx;
         if (p.renorm) {
@@ -590,7 +598,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
             for (int i = lane; i < p.experts; i += 32) mine[i] *= -dot;
         }
         __syncwarp();
-        if (has) atomicAdd(mine + e, dx);
+        if (!twice) {
+            if (has) mine[e] += dx;
+        } else {
+            for (int j = 0; j < p.k; ++j) {
+                if (has && lane == j) mine[e] += dx;
+                __syncwarp();
+            }
+        }
         __syncwarp();
         uint8_t *out = static_cast<uint8_t *>(p.dlogits) + t * p.ld_d * V::BYTES;
         if constexpr (VEC) {

@@ -245,6 +245,40 @@ def test_gradient_against_differences(score, renorm):
     check(got, ref, size * (10 * h * h + 1e-10 + 200 * 2.0 ** -23))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("experts", [1, 28, 64])
+def test_a_single_expert_takes_all(dtype, score, experts):
+    """Renormalised, one expert's weight is 1 whatever its logit, and the gradient 0: exactly."""
+    rng = np.random.default_rng(experts)
+    logits = stored(rng.standard_normal((1000, experts)) * 3, dtype)
+    dw = torch.from_numpy(rng.standard_normal((1000, 1)).astype(np.float32)).cuda()
+    chosen, w = lib.route(logits, 1, score=score, scale=2.5)
+    assert (w == 2.5).all()
+    assert (lib.route_grad(logits, chosen, dw, score=score, scale=2.5) == 0).all()
+    if experts < 4:
+        return
+    more = torch.full((1000, 4), -1, dtype=torch.int32, device="cuda")
+    more[:, 2] = chosen[:, 0]
+    assert (lib.route_grad(logits, more, dw.expand(1000, 4).contiguous(), score=score) == 0).all()
+
+
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_one_expert_named_many_times(score, renorm):
+    """All 32 places name two experts: the sums are the formula's, and the same bits every time."""
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((40, 33))
+    ids = np.where(rng.random((40, 32)) < 0.5, 3, 7)
+    dw = rng.standard_normal((40, 32)).astype(np.float32)
+    args = (stored(x, "f32"), torch.from_numpy(ids.astype(np.int32)).cuda(), torch.from_numpy(dw).cuda())
+    got = lib.route_grad(*args, score=score, renormalize=renorm)
+    ref = route_grad_ref(f64(args[0]), ids, dw.astype(np.float64), score, renorm, 1.0)
+    check(got, ref, 200 * 2.0 ** -23 * np.abs(dw).sum(1, keepdims=True))
+    for _ in range(5):
+        assert torch.equal(lib.route_grad(*args, score=score, renormalize=renorm), got)
+
+
 def test_gradient_of_dropped_repeated_and_masked_experts():
     rng = np.random.default_rng(4)
     x = rng.standard_normal((5, 16))
