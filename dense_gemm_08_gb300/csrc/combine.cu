@@ -40,8 +40,12 @@ struct Choices {
     }
 };
 
-// A thread's C pieces of D, `apart` pieces apart from column c0 on (FULL: all inside).
-template <int YT, int DT, bool YVEC, bool FULL, int R, int C>
+// A thread's C pieces of D, `apart` columns apart from column c0 on.  HELD: what of
+// them is inside the row.  (With loads of single values for all pieces of a run that
+// is not all inside, the gradient of 16384 tokens, 4 rows of 640 BF16, took 126 us, now
+// 78; with whole pieces that are there or not as the only other way, 8 rows of 512
+// took 89, now 58.)
+template <int YT, int DT, bool YVEC, int HELD, int R, int C>
 __device__ __forceinline__ void combine_pieces(const CombineProblem &p, int64_t t, int64_t c0,
                                                int64_t apart, bool dvec) {
     using Y = Value<YT>;
@@ -51,10 +55,10 @@ __device__ __forceinline__ void combine_pieces(const CombineProblem &p, int64_t 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t left = p.N - (c0 + c * apart);
-        n[c] = FULL || left >= WIDE ? WIDE : (left > 0 ? static_cast<int>(left) : 0);
+        n[c] = HELD == kAll || left >= WIDE ? WIDE : (left > 0 ? static_cast<int>(left) : 0);
         // (the residual is under way with the rows)
         if (p.residual != nullptr)
-            load_values<DT, FULL, WIDE>(p.residual, t * p.ld_r, c0 + c * apart, n[c], dvec, r[c]);
+            load_values<DT, HELD, WIDE>(p.residual, t * p.ld_r, c0 + c * apart, n[c], dvec, r[c]);
     }
     for (int64_t j0 = 0; j0 < p.k; j0 += R) {
         const Choices<R> ch(p, t, j0);
@@ -65,7 +69,7 @@ __device__ __forceinline__ void combine_pieces(const CombineProblem &p, int64_t 
             for (int c = 0; c < C; ++c) {
                 q[j][c] = make_uint4(0, 0, 0, 0);
                 if (ch.at[j] >= 0)
-                    q[j][c] = load_piece<YT, YVEC, FULL>(p.Y, ch.at[j] * p.ldy, c0 + c * apart, n[c]);
+                    q[j][c] = load_piece<YT, YVEC, HELD>(p.Y, ch.at[j] * p.ldy, c0 + c * apart, n[c]);
             }
         }
 #pragma unroll
@@ -84,7 +88,7 @@ __device__ __forceinline__ void combine_pieces(const CombineProblem &p, int64_t 
     for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int i = 0; i < WIDE; ++i) sum[c][i] += r[c][i];
-        store_values<DT, FULL, WIDE>(p.D, t * p.ldd, c0 + c * apart, n[c], dvec, sum[c]);
+        store_values<DT, HELD, WIDE>(p.D, t * p.ldd, c0 + c * apart, n[c], dvec, sum[c]);
     }
 }
 
@@ -101,16 +105,21 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Co
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes; u < all;
          u += step) {
         const int64_t t = all <= UINT32_MAX ? static_cast<uint32_t>(u) / chunks : u / chunks;
-        const int64_t c0 = ((u - t * chunks) * C * lanes + lane) * WIDE, apart = lanes * WIDE;
-        if (c0 + (C - 1) * apart + WIDE <= p.N)
-            combine_pieces<YT, DT, YVEC, true, R, C>(p, t, c0, apart, dvec);
-        else if (c0 < p.N)
-            combine_pieces<YT, DT, YVEC, false, R, C>(p, t, c0, apart, dvec);
+        const int64_t apart = lanes * WIDE, run = (u - t * chunks) * C * apart, c0 = run + lane * WIDE;
+        // (several pieces: the same way for all threads of a run)
+        if ((C == 1 ? c0 + WIDE : run + C * apart) <= p.N)
+            combine_pieces<YT, DT, YVEC, kAll, R, C>(p, t, c0, apart, dvec);
+        else if (c0 >= p.N)
+            continue;
+        else if (C > 1 && !has_end<WIDE, C>(p.N, c0, apart))
+            combine_pieces<YT, DT, YVEC, (C > 1 ? kAllOrNone : kSome), R, C>(p, t, c0, apart, dvec);
+        else
+            combine_pieces<YT, DT, YVEC, kSome, R, C>(p, t, c0, apart, dvec);
     }
 }
 
 // A thread's C pieces of the gradients: its part of the dot products, and dY.
-template <int YT, int DT, bool YVEC, bool FULL, int R, int C>
+template <int YT, int DT, bool YVEC, int HELD, int R, int C>
 __device__ __forceinline__ void grad_pieces(const CombineProblem &p, const Choices<R> &ch, int64_t t,
                                             int64_t c0, int64_t apart, bool dvec,
                                             float (&dot)[R]) {
@@ -121,7 +130,7 @@ __device__ __forceinline__ void grad_pieces(const CombineProblem &p, const Choic
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t left = p.N - (c0 + c * apart);
-        n[c] = FULL || left >= WIDE ? WIDE : (left > 0 ? static_cast<int>(left) : 0);
+        n[c] = HELD == kAll || left >= WIDE ? WIDE : (left > 0 ? static_cast<int>(left) : 0);
     }
     if (p.dweights != nullptr) {
 #pragma unroll
@@ -130,14 +139,14 @@ __device__ __forceinline__ void grad_pieces(const CombineProblem &p, const Choic
             for (int c = 0; c < C; ++c) {
                 q[j][c] = make_uint4(0, 0, 0, 0);
                 if (ch.at[j] >= 0)
-                    q[j][c] = load_piece<YT, YVEC, FULL>(p.Y, ch.at[j] * p.ldy, c0 + c * apart, n[c]);
+                    q[j][c] = load_piece<YT, YVEC, HELD>(p.Y, ch.at[j] * p.ldy, c0 + c * apart, n[c]);
             }
         }
     }
     float d[C][WIDE];
 #pragma unroll
     for (int c = 0; c < C; ++c)
-        load_values<DT, FULL, WIDE>(p.D, t * p.ldd, c0 + c * apart, n[c], dvec, d[c]);
+        load_values<DT, HELD, WIDE>(p.D, t * p.ldd, c0 + c * apart, n[c], dvec, d[c]);
     if (p.dY != nullptr) {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
@@ -147,7 +156,7 @@ __device__ __forceinline__ void grad_pieces(const CombineProblem &p, const Choic
                 float g[WIDE];
 #pragma unroll
                 for (int i = 0; i < WIDE; ++i) g[i] = ch.w[j] * d[c][i];
-                store_values<YT, FULL, WIDE>(p.dY, ch.at[j] * p.ld_dy, c0 + c * apart, n[c], YVEC, g);
+                store_values<YT, HELD, WIDE>(p.dY, ch.at[j] * p.ld_dy, c0 + c * apart, n[c], YVEC, g);
             }
         }
     }
@@ -185,10 +194,12 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const __grid
             float dot[R] = {};
             if (t < p.tokens) {
                 for (int64_t c0 = lane * WIDE; c0 < p.N; c0 += C * apart) {
-                    if (c0 + (C - 1) * apart + WIDE <= p.N)
-                        grad_pieces<YT, DT, YVEC, true, R, C>(p, ch, t, c0, apart, dvec, dot);
+                    if ((C == 1 ? c0 + WIDE : c0 - lane * WIDE + C * apart) <= p.N)
+                        grad_pieces<YT, DT, YVEC, kAll, R, C>(p, ch, t, c0, apart, dvec, dot);
+                    else if (C > 1 && !has_end<WIDE, C>(p.N, c0, apart))
+                        grad_pieces<YT, DT, YVEC, (C > 1 ? kAllOrNone : kSome), R, C>(p, ch, t, c0, apart, dvec, dot);
                     else
-                        grad_pieces<YT, DT, YVEC, false, R, C>(p, ch, t, c0, apart, dvec, dot);
+                        grad_pieces<YT, DT, YVEC, kSome, R, C>(p, ch, t, c0, apart, dvec, dot);
                 }
             }
             if (p.dweights == nullptr) continue;

@@ -4,10 +4,10 @@
 // A CTA takes tokens one after another, a token in steps of up to eight rows and a
 // run of columns.  One warp has each row's run (and the residual's, or dD's) copied
 // into a stage of shared memory, as many stages ahead as fit; the number and weight
-// of each row go with it.  Two groups of four warps take every other token each.  So
-// some 70 to 100 KB per CTA, two per SM, are under way at any time, whatever the rows'
-// number and without registers: 6.8 TB/s, where loads into registers (combine.cu)
-// reached 5.1 with 8 rows and less with fewer.
+// of each row go with it.  Two groups of four warps (or four of two) take a token
+// each.  So some 70 to 100 KB per CTA, two per SM, are under way at any time, whatever
+// the rows' number and without registers: 6.8 TB/s, where loads into registers
+// (combine.cu) reached 5.1 with 8 rows and less with fewer.
 #include <atomic>
 #include <type_traits>
 
@@ -21,9 +21,9 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 8;         // of a stage at most
-constexpr int kWarps = 4;        // that take a token
-constexpr int kGroups = 2;       // of them
-constexpr int kThreads = 32 * kWarps * kGroups + 32;
+constexpr int kWarps = 8;        // that sum, in groups of 2 or 4 that take a token
+constexpr int kMaxGroups = 4;
+constexpr int kThreads = 32 * kWarps + 32;
 constexpr int kMaxStages = 16;
 constexpr int kRing = 104 * 1024;
 // what goes with a stage: the rows' numbers (-1: none) and weights
@@ -33,8 +33,7 @@ struct __align__(16) Meta {
 };
 // ring, meta, dot products of the warps (two sets of them), barriers, alignment
 constexpr int kSmemBytes = 128 + kRing + kMaxStages * static_cast<int>(sizeof(Meta)) +
-                           2 * kGroups * kWarps * kRows * 4 + (kGroups + 1) * kMaxStages * 8 + 16;
-static_assert(kGroups == 2, "the groups skip one token");
+                           2 * kWarps * kRows * 4 + (kMaxGroups + 1) * kMaxStages * 8 + 16;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 
 struct BulkArgs {
@@ -64,33 +63,33 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t at) {
     return v;
 }
 
-template <int YT, int DT, bool GRAD>
+template <int YT, int DT, bool GRAD, int WARPS>
 __global__ void __launch_bounds__(kThreads, 2)
     combine_bulk_kernel(const __grid_constant__ BulkArgs a) {
     using Y = Value<YT>;
     using D = Value<DT>;
-    constexpr int WIDE = Y::PER_16;
+    constexpr int WIDE = Y::PER_16, GROUPS = kWarps / WARPS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                                       ~static_cast<uintptr_t>(127));
     Meta *const meta = reinterpret_cast<Meta *>(ring + kRing);
-    float *const parts = reinterpret_cast<float *>(meta + kMaxStages);  // [kGroups][2][kWarps][kRows]
-    constexpr int kParts = kGroups * 2 * kWarps * kRows;
+    float *const parts = reinterpret_cast<float *>(meta + kMaxStages);  // [GROUPS][2][WARPS][kRows]
+    constexpr int kParts = 2 * kWarps * kRows;
     const uint32_t ring0 = smem_addr(ring);
-    // barriers: full[kGroups][kMaxStages] copies -> the group the stage is for,
+    // barriers: full[GROUPS][kMaxStages] copies -> the group the stage is for,
     // empty[kMaxStages] sums -> copies.  (A full barrier per group: a group waits for
     // each of its own stages in turn, so one parity bit per stage tells them apart;
     // with one for both it could take a stage that the other has not seen yet for
     // its own.)
-    const uint32_t full0 = smem_addr(parts + kParts), empty0 = full0 + 8 * kGroups * kMaxStages;
+    const uint32_t full0 = smem_addr(parts + kParts), empty0 = full0 + 8 * GROUPS * kMaxStages;
     volatile int *const abort_flag =
-        reinterpret_cast<volatile int *>(parts + kParts + 2 * (kGroups + 1) * kMaxStages);
+        reinterpret_cast<volatile int *>(parts + kParts + 2 * (GROUPS + 1) * kMaxStages);
     const CombineProblem &p = a.p;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            for (int g = 0; g < kGroups; ++g) mbar_init(full0 + 8 * (g * kMaxStages + s), 1);
-            mbar_init(empty0 + 8 * s, kWarps);
+            for (int g = 0; g < GROUPS; ++g) mbar_init(full0 + 8 * (g * kMaxStages + s), 1);
+            mbar_init(empty0 + 8 * s, WARPS);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     // A token's steps: forward all rows of a run of columns (their sum stays in
     // registers), gradient all columns of a set of rows (so do its dot products).
-    const int steps = a.j_steps * a.chunks;
+    const uint32_t steps = a.j_steps * a.chunks;
     auto set_of = [&](int s) { return GRAD ? s / a.chunks : s % a.j_steps; };
     auto run_of = [&](int s) { return GRAD ? s % a.chunks : s / a.j_steps; };
     auto cols_of = [&](int c) {
@@ -117,36 +116,48 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool with_y = !GRAD || p.dweights != nullptr;
     int stage = 0;
 
-    if (warp == kWarps * kGroups) {
+    if (warp == kWarps) {
         // ------------------------------------------------------- copies
-        auto choices = [&](int64_t t, int set, int32_t &at, float &w) {
-            const int64_t j = static_cast<int64_t>(set) * a.rows + lane;
+        // The rows' numbers and weights are loaded for 32 rows at a time, some steps
+        // ahead: with those of the next step alone under way, every step waited for
+        // their latency (8190 tokens, 2 rows of 2048 FP16, gradient: 40 us, now 33).
+        const uint32_t per = 32 / a.rows;  // steps
+        auto advance = [&](int64_t &t, uint32_t &s, uint32_t by) {
+            s += by;
+            t += static_cast<int64_t>(s / steps) * gridDim.x;
+            s %= steps;
+        };
+        auto choices = [&](int64_t t, uint32_t s, int32_t &at, float &w) {
+            advance(t, s, lane / a.rows);
+            const int64_t j = static_cast<int64_t>(set_of(s)) * a.rows + lane % a.rows;
             at = -1;
             w = 1.f;
-            if (lane < a.rows && j < p.k && t < p.tokens) {
+            if (t < p.tokens && j < p.k) {
                 at = __ldg(p.position + t * p.k + j);
                 if (p.weights != nullptr) w = __ldg(p.weights + t * p.k + j);
             }
             if (at >= p.rows_y) at = -1;
         };
-        int32_t at, next_at;
-        float w, next_w;
+        int32_t ats, next_ats;
+        float ws, next_ws;
         int64_t t = blockIdx.x;
-        choices(t, 0, at, w);
+        uint32_t s = 0;
+        choices(t, s, ats, ws);
         uint32_t phase = 0;           // of the empty barriers
-        uint32_t told[kGroups] = {};  // bit s: parity of the next copies on the group's full[s]
-        uint32_t group = 0, used = 0, of = 0;  // bit s: stage s was filled; for group 1
+        uint32_t told[GROUPS] = {};  // bit s: parity of the next copies on the group's full[s]
+        uint32_t group = 0, used[GROUPS] = {};  // bit s: stage s was filled last for the group
         bool ok = true;
-        for (; ok && t < p.tokens; t += gridDim.x, group ^= 1) {
-            for (int s = 0; s < steps; ++s) {
-                // the next step's rows, under way while this one waits for its stage
-                const bool last = s + 1 == steps;
-                if (last || set_of(s + 1) != set_of(s)) {
-                    choices(last ? t + gridDim.x : t, last ? 0 : set_of(s + 1), next_at, next_w);
-                } else {
-                    next_at = at;
-                    next_w = w;
-                }
+        for (; ok && t < p.tokens; ats = next_ats, ws = next_ws) {
+            {
+                int64_t t_next = t;
+                uint32_t s_next = s;
+                advance(t_next, s_next, per);
+                choices(t_next, s_next, next_ats, next_ws);
+            }
+            for (uint32_t b = 0; b < per && t < p.tokens; ++b) {
+                int32_t at = __shfl_sync(0xffffffffu, ats, (b * a.rows + lane) % 32);
+                const float w = __shfl_sync(0xffffffffu, ws, (b * a.rows + lane) % 32);
+                if (lane >= a.rows) at = -1;
                 ok = wait_all(empty0 + 8 * stage, phase ^ 1);
                 if (!ok) break;
                 const int c = run_of(s), cols = cols_of(c);
@@ -179,42 +190,48 @@ __global__ void __launch_bounds__(kThreads, 2)
                     bulk_load(to + a.rows * a.row_bytes, from, d_bytes, bar);
                 }
                 const uint32_t bit = 1u << stage;
-                told[0] ^= group == 0 ? bit : 0u;
-                told[1] ^= group == 1 ? bit : 0u;
-                used |= bit;
-                of = group == 1 ? of | bit : of & ~bit;
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    told[g] ^= group == g ? bit : 0u;
+                    used[g] = group == g ? used[g] | bit : used[g] & ~bit;
+                }
                 if (++stage == a.stages) {
                     stage = 0;
                     phase ^= 1;
                 }
-                at = next_at;
-                w = next_w;
+                if (++s == steps) {
+                    s = 0;
+                    t += gridDim.x;
+                    group = (group + 1) % GROUPS;
+                }
             }
         }
         __syncwarp();
         // the copies in flight land before the CTA exits
-        for (int i = 0; i < a.stages; ++i) {
-            if (!((used >> i) & 1u)) continue;
-            const uint32_t g = (of >> i) & 1u, parity = (((g ? told[1] : told[0]) >> i) & 1u) ^ 1u;
-            const volatile int never = 0;
-            if (!wait_bounded(full0 + 8 * (g * kMaxStages + i), parity, &never, a.timeout_ns))
-                raise_abort(abort_flag);
-        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+            for (int i = 0; i < a.stages; ++i) {
+                if (!((used[g] >> i) & 1u)) continue;
+                const volatile int never = 0;
+                if (!wait_bounded(full0 + 8 * (g * kMaxStages + i), ((told[g] >> i) & 1u) ^ 1u, &never,
+                                  a.timeout_ns))
+                    raise_abort(abort_flag);
+            }
         return;
     }
 
     // ------------------------------------------------------------- sums
-    const int group = warp / kWarps, tid = threadIdx.x - group * 32 * kWarps;
+    const int group = warp / WARPS, tid = threadIdx.x - group * 32 * WARPS;
     uint32_t flip = 0;  // which of the two sets of parts
     bool ok = true;     // (after a wait that ran out the warps still meet at their barrier)
     uint32_t seen = 0;  // bit s: parity of the next copies on this group's full[s]
-    auto skip_token = [&]() { stage = (stage + steps) % a.stages; };  // the other group's stages
-    if (group == 1) skip_token();
+    auto skip_tokens = [&](uint32_t n) { stage = (stage + n * steps) % a.stages; };  // other groups' stages
+    skip_tokens(group);
     for (int64_t t = blockIdx.x + static_cast<int64_t>(group) * gridDim.x; t < p.tokens;
-         t += static_cast<int64_t>(kGroups) * gridDim.x, skip_token()) {
+         t += static_cast<int64_t>(GROUPS) * gridDim.x, skip_tokens(GROUPS - 1)) {
         float sum[WIDE] = {};    // forward, several sets of rows: one piece per thread
         float dot[kRows] = {};   // gradient
-        for (int s = 0; s < steps; ++s) {
+        for (uint32_t s = 0; s < steps; ++s) {
             ok = ok && wait_all(full0 + 8 * (group * kMaxStages + stage), (seen >> stage) & 1u);
             seen ^= 1u << stage;
             const int c = run_of(s), set = set_of(s), cols = cols_of(c);
@@ -247,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int u = 0; u < D::PER_16; ++u) d[i * D::PER_16 + u] = v[u];
                     }
                 } else if (GRAD) {
-                    load_values<DT, false, WIDE>(p.D, t * p.ldd, c0, n, false, d);
+                    load_values<DT, kSome, WIDE>(p.D, t * p.ldd, c0, n, false, d);
                 } else if (p.residual != nullptr && set == a.j_steps - 1) {
-                    load_values<DT, false, WIDE>(p.residual, t * p.ld_r, c0, n, false, d);
+                    load_values<DT, kSome, WIDE>(p.residual, t * p.ld_r, c0, n, false, d);
                 }
 #pragma unroll
                 for (int j = 0; j < kRows; ++j) {
@@ -259,16 +276,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int i = 0; i < WIDE; ++i) g[i] = w[j] * d[i];
                         if (ALL || n == WIDE)
-                            store_values<YT, true, WIDE>(p.dY, at[j] * p.ld_dy, c0, n, true, g);
+                            store_values<YT, kAll, WIDE>(p.dY, at[j] * p.ld_dy, c0, n, true, g);
                         else
-                            store_values<YT, false, WIDE>(p.dY, at[j] * p.ld_dy, c0, n, true, g);
+                            store_values<YT, kSome, WIDE>(p.dY, at[j] * p.ld_dy, c0, n, true, g);
                     }
                     if (!with_y) continue;
                     float y[WIDE];
                     // (of the last row the end that is no whole 16 bytes was not copied)
                     Y::unpack(ALL || n == WIDE || at[j] + 1 < p.rows_y
                                   ? ld_shared_u4(from + j * a.row_bytes + piece * 16)
-                                  : load_piece<YT, false, false>(p.Y, at[j] * p.ldy, c0, n),
+                                  : load_piece<YT, false, kSome>(p.Y, at[j] * p.ldy, c0, n),
                               y);
 #pragma unroll
                     for (int i = 0; i < WIDE; ++i) {
@@ -283,14 +300,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int i = 0; i < WIDE; ++i) sum[i] += d[i];
                     if (ALL || n == WIDE)
-                        store_values<DT, true, WIDE>(p.D, t * p.ldd, c0, n, a.dvec, sum);
+                        store_values<DT, kAll, WIDE>(p.D, t * p.ldd, c0, n, a.dvec, sum);
                     else
-                        store_values<DT, false, WIDE>(p.D, t * p.ldd, c0, n, a.dvec, sum);
+                        store_values<DT, kSome, WIDE>(p.D, t * p.ldd, c0, n, a.dvec, sum);
 #pragma unroll
                     for (int i = 0; i < WIDE; ++i) sum[i] = 0.f;
                 }
             };
-            for (int piece = tid; ok && piece * WIDE < cols; piece += 32 * kWarps) {
+            for (int piece = tid; ok && piece * WIDE < cols; piece += 32 * WARPS) {
                 const int n = cols - piece * WIDE < WIDE ? cols - piece * WIDE : WIDE;
                 if (lowest == 0 && n == WIDE)
                     take(piece, WIDE, std::true_type());
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (lane == 0) mbar_arrive(empty0 + 8 * stage);
             if (++stage == a.stages) stage = 0;
             if (GRAD && with_y && c == a.chunks - 1) {
-                float *const mine = parts + ((group * 2 + flip) * kWarps + warp % kWarps) * kRows;
+                float *const mine = parts + ((group * 2 + flip) * WARPS + warp % WARPS) * kRows;
                 float all = 0.f;
 #pragma unroll
                 for (int j = 0; j < kRows; ++j) {
@@ -311,10 +328,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     dot[j] = 0.f;
                 }
                 if (lane < kRows) mine[lane] = all;
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kWarps) : "memory");
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * WARPS) : "memory");
                 const int64_t j = static_cast<int64_t>(set) * a.rows + lane;
-                if (ok && warp % kWarps == 0 && lane < a.rows && j < p.k) {
-                    for (int i = 1; i < kWarps; ++i) all += mine[i * kRows + lane];
+                if (ok && warp % WARPS == 0 && lane < a.rows && j < p.k) {
+                    for (int i = 1; i < WARPS; ++i) all += mine[i * kRows + lane];
                     int32_t mine_at = -1;
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) mine_at = lane == i ? at[i] : mine_at;
@@ -329,17 +346,33 @@ __global__ void __launch_bounds__(kThreads, 2)
 constexpr int kMaxDevices = 64;
 std::atomic<bool> g_launched[kMaxDevices];
 
+template <int YT, int DT, bool GRAD, int WARPS>
+cudaError_t launch_groups(const BulkArgs &a, cudaStream_t stream) {
+    const auto kernel = combine_bulk_kernel<YT, DT, GRAD, WARPS>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    set_pdl_attribute(&attr);
+    cudaLaunchConfig_t cfg = {};
+    const int64_t most = 2 * int64_t(sm_count());
+    cfg.gridDim = dim3(static_cast<unsigned>(a.p.tokens < most ? a.p.tokens : most), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <int YT, int DT, bool GRAD>
 cudaError_t launch_as(const CombineProblem &p, cudaStream_t stream) {
     using Y = Value<YT>;
     using D = Value<DT>;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    const auto kernel = combine_bulk_kernel<YT, DT, GRAD>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
     BulkArgs a = {};
     a.p = p;
     a.rows = 1;
@@ -365,17 +398,12 @@ cudaError_t launch_as(const CombineProblem &p, cudaStream_t stream) {
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     a.timeout_ns = 1000000000ull;  // (a stage's copies, or the sums of one)
     g_launched[dev].store(true);
-    cudaLaunchAttribute attr;
-    set_pdl_attribute(&attr);
-    cudaLaunchConfig_t cfg = {};
-    const int64_t most = 2 * int64_t(sm_count());
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tokens < most ? p.tokens : most), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    // A token whose step is short is mostly latency: four groups of two warps (us, two
+    // groups of four / four of two, BF16, gradient: 16384 tokens, 2 rows of 1024 52 / 44,
+    // 1 of 4096 78 / 64, 8 of 1024 102 / 100, 8 of 2048 186 / 196; forward: 2 rows of
+    // 2048 46 / 44, 4 of 2048 63.6 / 62.9, 8 of 2048 103 / 116).
+    if (a.j_steps == 1 && a.rows * bytes <= 16384) return launch_groups<YT, DT, GRAD, 2>(a, stream);
+    return launch_groups<YT, DT, GRAD, 4>(a, stream);
 }
 
 template <bool GRAD>
@@ -395,19 +423,24 @@ bool combine_bulk_eligible(const CombineProblem &p, bool grad) {
     if (p.k == 0 || p.rows_y == 0) return false;
     // A step costs some time whatever its bytes, so rows must be long; and the
     // pipeline must run for a while.  Both ways measured in BF16, loads / bulk, us:
-    //   forward   16384 tokens, 8 rows: 2048 columns 132 / 106, 1024 columns 69 / 83;
-    //             2 rows: 4096 columns 110 / 88, 2048 columns 57 / 70;
-    //             8 rows of 4096: 1024 tokens 19 / 18, 256 tokens 7.4 / 7.4
-    //   gradient  16384 tokens, 8 rows: 1024 columns 110 / 100, 512 columns 58 / 89;
-    //             2 rows: 2048 columns 114 / 78, 1024 columns 58 / 69;
-    //             32768 tokens, 1 row of 4096: 141 / 150; 1024 tokens, 8 of 1024: 10 / 11
+    //   forward   16384 tokens, 8 rows: 2048 columns 132 / 103, 1024 columns 68 / 62,
+    //             768 columns 53 / 56, 512 columns 36 / 55; 4 rows of 1024 46 / 45;
+    //             2 rows: 4096 columns 110 / 83, 2048 columns 56 / 44, 1024 30 / 40;
+    //             4096 tokens, 2 rows of 2048: 15.2 / 13.8; 512, 8 of 4096: 10.9 / 11.1
+    //   gradient  16384 tokens, 8 rows: 1024 columns 110 / 100, 512 columns 58 / 61;
+    //             4 rows of 640 75 / 49, 512 42 / 47; 2 rows: 2048 columns 114 / 64,
+    //             1024 58 / 44;
+    //             1 row: 4096 columns 73 / 64, 2048 38 / 44; 2048 tokens, 2 rows of
+    //             2048 17.8 / 12.0, 1 row of 4096 12.4 / 13.8
     const int64_t row = p.N * bytes, all = row * p.k * p.tokens, mb = int64_t(1) << 20;
     if (grad) {
-        if (p.k < 2 || row < 2048 || row * p.k < 8192 || all < 16 * mb) return false;
+        if (row < 1280 || row * p.k < 4096 || all < 16 * mb) return false;
+        if (p.k == 1 && (row < 8192 || all < 64 * mb)) return false;
     } else {
-        if (row < 4096 || (row < 8192 && p.k < 4) || all < 48 * mb) return false;
+        if (row < 2048 || row * p.k < 8192 || all < 32 * mb) return false;
     }
-    if (p.k > (int64_t(1) << 20) || p.N > (int64_t(1) << 28)) return false;
+    // (a token's steps are counted in 31 bits; no step has less than 4 KB)
+    if (p.k > (int64_t(1) << 20) || p.N > (int64_t(1) << 28) || p.k > (int64_t(1) << 40) / p.N) return false;
     if (grad)
         return (p.dweights == nullptr || rows_on_16(p.Y, p.ldy, bytes)) &&
                (p.dY == nullptr || rows_on_16(p.dY, p.ld_dy, bytes));

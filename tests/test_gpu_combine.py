@@ -231,7 +231,8 @@ def test_many_tokens(T, k, N):
 @pytest.mark.parametrize("y,d", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"),
                                  ("f16", "f32")])
 @pytest.mark.parametrize("T,k,N", [(3400, 1, 8192), (1701, 2, 9001), (3300, 3, 2575), (900, 5, 8200), (1777, 8, 2100),
-                                   (1640, 11, 2055), (700, 20, 2080), (7001, 2, 2049), (701, 8, 1056), (1500, 4, 515)])
+                                   (1640, 11, 2055), (700, 20, 2080), (7001, 2, 2049), (701, 8, 1056), (1500, 4, 515),
+                                   (4500, 2, 1032), (6000, 2, 900), (5000, 1, 8200), (3001, 4, 777)])
 def test_large_batches(y, d, T, k, N):
     """Rows by bulk copy: several runs of columns, sets of rows, odd ends, rows without a place."""
     g = torch.Generator(device="cuda").manual_seed(T)
@@ -260,7 +261,7 @@ def test_large_batches(y, d, T, k, N):
         out = torch.full((T, ld + 8), 7.0, device="cuda", dtype=u)
         got = lib.combine(Y, at, weights=weights, residual=residual, out=out[:, :N])
         row = N * Y.element_size()
-        bulk = row >= (8192 if k < 4 else 4096) and row * k * T >= 48 << 20
+        bulk = row >= 2048 and row * k >= 8192 and row * k * T >= 32 << 20
         assert lib.gemm_last_kernel() == ("combine<bulk>" if bulk else "combine")
         assert ((got.double() - ref).abs() <= tol).all() and (out[:, N:] == 7.0).all()
         odd = torch.empty(T, N + 1, device="cuda", dtype=u)[:, 1:]  # rows off 16 bytes
@@ -274,7 +275,8 @@ def test_large_batches(y, d, T, k, N):
         buf = torch.full((T * k, ld), 7.0, device="cuda", dtype=t)
         dY, dw = lib.combine_grad(dD, Y, at, weights=weights, out=buf[:, :N])
         row = N * Y.element_size()
-        bulk = k >= 2 and row >= 2048 and row * k >= 8192 and row * k * T >= 16 << 20
+        bulk = row >= 1280 and row * k >= 4096 and row * k * T >= 16 << 20
+        bulk = bulk and (k > 1 or (row >= 8192 and row * T >= 64 << 20))
         assert lib.gemm_last_kernel() == ("combine_grad<bulk>" if bulk else "combine_grad")
         want = torch.full((T * k, N), 7.0, device="cuda", dtype=torch.float64)
         want[at[inside].long()] = (dD.double()[:, None] * s[..., None])[inside]
