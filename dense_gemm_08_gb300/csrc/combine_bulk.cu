@@ -420,7 +420,7 @@ cudaError_t launch_types(const CombineProblem &p, cudaStream_t stream) {
 
 bool combine_bulk_eligible(const CombineProblem &p, bool grad) {
     const int64_t bytes = value_bytes(p.y_type);
-    if (p.k == 0 || p.rows_y == 0) return false;
+    if (p.k == 0 || p.N == 0 || p.rows_y == 0) return false;
     // A step costs some time whatever its bytes, so rows must be long; and the
     // pipeline must run for a while.  Both ways measured in BF16, loads / bulk, us:
     //   forward   16384 tokens, 8 rows: 2048 columns 132 / 103, 1024 columns 68 / 62,
@@ -432,15 +432,17 @@ bool combine_bulk_eligible(const CombineProblem &p, bool grad) {
     //             1024 58 / 44;
     //             1 row: 4096 columns 73 / 64, 2048 38 / 44; 2048 tokens, 2 rows of
     //             2048 17.8 / 12.0, 1 row of 4096 12.4 / 13.8
-    const int64_t row = p.N * bytes, all = row * p.k * p.tokens, mb = int64_t(1) << 20;
-    if (grad) {
-        if (row < 1280 || row * p.k < 4096 || all < 16 * mb) return false;
-        if (p.k == 1 && (row < 8192 || all < 64 * mb)) return false;
-    } else {
-        if (row < 2048 || row * p.k < 8192 || all < 32 * mb) return false;
-    }
     // (a token's steps are counted in 31 bits; no step has less than 4 KB)
-    if (p.k > (int64_t(1) << 20) || p.N > (int64_t(1) << 28) || p.k > (int64_t(1) << 40) / p.N) return false;
+    if (p.k > (int64_t(1) << 20) || p.N > (int64_t(1) << 28) || p.k * p.N > (int64_t(1) << 40))
+        return false;
+    const int64_t row = p.N * bytes;
+    auto all_mb = [&](int64_t mb) { return p.tokens * p.k >= ((mb << 20) + row - 1) / row; };
+    if (grad) {
+        if (row < 1280 || row * p.k < 4096 || !all_mb(16)) return false;
+        if (p.k == 1 && (row < 8192 || !all_mb(64))) return false;
+    } else {
+        if (row < 2048 || row * p.k < 8192 || !all_mb(32)) return false;
+    }
     if (grad)
         return (p.dweights == nullptr || rows_on_16(p.Y, p.ldy, bytes)) &&
                (p.dY == nullptr || rows_on_16(p.dY, p.ld_dy, bytes));

@@ -48,7 +48,8 @@ gemm_status_t product(InType in, int64_t M, int64_t N, int64_t K, float alpha, c
     if (M == 0 || N == 0) return GEMM_OK;
     if (!rows_ok(D, in, N, ldd)) return GEMM_ERR_INVALID_VALUE;
     const bool sums = K > 0 && alpha != 0.f;
-    if (sums && (!operand_ok(A, in, M, K, lda, order_a) || !operand_ok(B, in, K, N, ldb, order_b)))
+    if (sums && (!operand_ok(A, in, M, K, lda, order_a) || !operand_ok(B, in, K, N, ldb, order_b) ||
+                 D == A || D == B))
         return GEMM_ERR_INVALID_VALUE;
     p->M = M;
     p->N = N;
@@ -86,8 +87,10 @@ gemm_status_t fused(InType in, int64_t M, int64_t N, int64_t K, float alpha, con
         product(in, M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D, ldd, &p);
     if (st != GEMM_OK || p.N == 0) return st;
     if ((f.bias != nullptr && !usable(f.bias, 4)) ||
-        (f.residual != nullptr && !rows_ok(f.residual, in, N, f.ld_residual)) ||
-        (f.pre != nullptr && (!rows_ok(f.pre, in, N, f.ld_pre) || f.pre == D || f.pre == f.residual)))
+        (f.residual != nullptr && (!rows_ok(f.residual, in, N, f.ld_residual) ||
+                                   (f.residual == D && f.ld_residual != ldd))) ||
+        (f.pre != nullptr && (!rows_ok(f.pre, in, N, f.ld_pre) || f.pre == D || f.pre == f.residual ||
+                              (p.K > 0 && (f.pre == A || f.pre == B)))))
         return GEMM_ERR_INVALID_VALUE;
     const gemm_status_t dev = gemm::check_device_status();
     if (dev != GEMM_OK) return dev;
@@ -112,7 +115,9 @@ gemm_status_t fused_grad(InType in, int64_t M, int64_t N, int64_t K, float alpha
         product(in, M, N, K, alpha, A, lda, order_a, B, ldb, order_b, D, ldd, &p);
     if (st != GEMM_OK || N == 0) return st;
     if (M == 0 && dbias == nullptr) return GEMM_OK;
-    if (M > 0 && activation != GEMM_ACT_NONE && !rows_ok(pre, in, N, ld_pre))
+    if (M > 0 && activation != GEMM_ACT_NONE && (!rows_ok(pre, in, N, ld_pre) || (pre == D && ld_pre != ldd)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (dbias != nullptr && (dbias == D || dbias == pre || dbias == A || dbias == B))
         return GEMM_ERR_INVALID_VALUE;
     const gemm_status_t dev = gemm::check_device_status();
     if (dev != GEMM_OK) return dev;

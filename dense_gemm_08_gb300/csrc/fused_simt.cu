@@ -4,12 +4,12 @@
 // into the value before the activation where that is kept -- and one pass over it
 // (fused_finish_kernel: bias, activation, residual, slopes, column sums).
 //
-// Small FP32 products, and 16-bit inputs that TMA cannot describe: tiles of 64 x 64 (4 x 4 sums per thread);
-// slices of 16 of K come through registers into two shared-memory buffers, sums are
-// paired FMAs.  Few tiles: K is split over a cluster, whose CTAs add each other's
-// sums through distributed shared memory, each for its share of the tile's rows and
-// in the order of the pieces.  The tile then lies in shared memory, and a thread
-// finishes one of its columns.
+// Small FP32 products, and 16-bit inputs that TMA cannot describe: tiles of 64 x 64
+// (4 x 4 sums per thread); slices of 16 of K come through registers into two
+// shared-memory buffers, sums are paired FMAs.  Few tiles: K is split over a cluster,
+// whose CTAs add each other's sums through distributed shared memory, each for its
+// share of the tile's rows and in the order of the pieces.  The tile then lies in
+// shared memory, and a thread finishes one of its columns.
 //
 // A row or two of A (FP32: four) and a K-contiguous B: warps stream B's columns
 // once (fused_rows_kernel).

@@ -102,7 +102,7 @@ GEMM_API gemm_status_t gemm_route_grad(int64_t tokens, int64_t experts, int64_t 
         return GEMM_ERR_INVALID_VALUE;
     if (tokens == 0) return GEMM_OK;
     if (!matrix_ok(logits, experts, ld, type) || !matrix_ok(dlogits, experts, ld_d, type) ||
-        !usable(chosen, 4) || !usable(dweights, 4))
+        !usable(chosen, 4) || !usable(dweights, 4) || (logits == dlogits && ld != ld_d))
         return GEMM_ERR_INVALID_VALUE;
     const gemm_status_t dev = gemm::check_device_status();
     if (dev != GEMM_OK) return dev;
@@ -143,7 +143,8 @@ GEMM_API gemm_status_t gemm_combine(int64_t tokens, int64_t k, int64_t N, const 
         (residual != nullptr && !matrix_ok(residual, N, ld_r, d_type)) ||
         (k > 0 && !usable(position, 4)) ||
         (weights != nullptr && !usable(weights, 4)) ||
-        (k > 0 && rows_y > 0 && !matrix_ok(Y, N, ldy, y_type)))
+        (k > 0 && rows_y > 0 && (!matrix_ok(Y, N, ldy, y_type) || Y == D)) ||
+        (residual == D && ld_r != ldd))
         return GEMM_ERR_INVALID_VALUE;
     const gemm_status_t dev = gemm::check_device_status();
     if (dev != GEMM_OK) return dev;
@@ -180,7 +181,8 @@ GEMM_API gemm_status_t gemm_combine_grad(int64_t tokens, int64_t k, int64_t N, c
         (weights != nullptr && !usable(weights, 4)) ||
         (dweights != nullptr && !usable(dweights, 4)) ||
         (N > 0 && rows_y > 0 && dweights != nullptr && !matrix_ok(Y, N, ldy, y_type)) ||
-        (N > 0 && rows_y > 0 && dY != nullptr && !matrix_ok(dY, N, ld_dy, y_type)))
+        (N > 0 && rows_y > 0 && dY != nullptr && (!matrix_ok(dY, N, ld_dy, y_type) || dY == dD)) ||
+        (dY != nullptr && dY == Y) || (dweights != nullptr && dweights == weights))
         return GEMM_ERR_INVALID_VALUE;
     const gemm_status_t dev = gemm::check_device_status();
     if (dev != GEMM_OK) return dev;

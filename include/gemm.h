@@ -548,7 +548,7 @@ gemm_status_t gemm_combine(int64_t tokens, int64_t k, int64_t N, const void *Y, 
  * entries outside have dweights = 0.  Rows of dY that no position names are
  * left as they are.  weights NULL: all 1.  dY or dweights may be NULL (not
  * computed); Y is read for dweights only, and NULL without it.  dY must not
- * overlap Y or dD.  k is at least 1.
+ * overlap Y or dD, nor dweights the weights.  k is at least 1.
  */
 gemm_status_t gemm_combine_grad(int64_t tokens, int64_t k, int64_t N, const void *dD, int64_t ld_d,
                                 gemm_d_type_t d_type, const void *Y, int64_t ldy, int64_t rows_y,
@@ -572,11 +572,14 @@ gemm_status_t gemm_combine_grad(int64_t tokens, int64_t k, int64_t N, const void
  *                       not overlap D, A, B or the residual
  * fusion == NULL: none of them (D = alpha op(A) op(B) in the inputs' type).
  * D is computed from Z before Z is rounded.  M, N, K as for gemm_f32; K == 0
- * or alpha == 0: A and B are not read, Z = bias.
+ * or alpha == 0: A and B are not read, Z = bias.  D must not overlap A or B.
+ * (Where two matrices of a call must not overlap, or only with the same pitch,
+ * the same address is refused; parts of one another are not looked for.)
  * Kernels: tensor cores (tcgen05) for 16-bit inputs that TMA can describe
  *   (16-byte aligned A and B, leading dimensions multiples of 8 elements),
- *   CUDA cores otherwise and for FP32 (no TF32).  D, pre, residual: any
- *   alignment.
+ *   CUDA cores otherwise and for FP32 (no TF32; a larger FP32 product by
+ *   gemm_f32's kernels and a pass for what follows it, which where D is the
+ *   residual or pre takes workspace of D's size).  D, pre, residual: any alignment.
  * Accuracy: |Z - Z_ref| <= rel * sum_k |alpha A B| + 1e-6 |Z|, rel = 1e-5
  *   (FP32) or 4e-3 (16-bit inputs); D as act's largest slope (1.13 for GELU,
  *   1.1 for SILU) times that plus 1e-6 |Z|; each plus its rounding.

@@ -96,6 +96,34 @@ def test_fused_refusals(t):
         assert fn(**dict(good, A=None, B=None, D=None, pre=None, **change), stream=0) == lib.GEMM_OK
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16_f32acc", "f16_f32acc"])
+def test_matrices_at_the_same_address(t):
+    """Refused where they must not overlap, or only with the same pitch."""
+    route = dict(tokens=5, experts=16, k=4, logits=FAKE, ld=16, type=1, chosen=FAKE, dweights=FAKE,
+                 dlogits=FAKE, ld_d=24)
+    assert lib.gemm_route_grad(**route, stream=0, check=False) == BAD
+    combine = dict(tokens=5, k=2, N=16, Y=FAKE, ldy=16, rows_y=10, y_type=1, position=FAKE,
+                   weights=FAKE, residual=FAKE, ld_r=16, D=FAKE2, ldd=16, d_type=1)
+    for change in [dict(D=FAKE), dict(residual=FAKE2, ld_r=24)]:
+        assert lib.gemm_combine(**dict(combine, **change), stream=0, check=False) == BAD, change
+    grad = dict(tokens=5, k=2, N=16, dD=FAKE, ld_d=16, d_type=0, Y=2 * FAKE2, ldy=16, rows_y=10,
+                y_type=2, position=FAKE, weights=FAKE, dY=FAKE2, ld_dy=16, dweights=FAKE2)
+    for change in [dict(dY=FAKE), dict(dY=2 * FAKE2), dict(dweights=FAKE)]:
+        assert lib.gemm_combine_grad(**dict(grad, **change), stream=0, check=False) == BAD, change
+    fused = dict(M=5, N=16, K=16, alpha=1.0, A=FAKE, lda=16, order_a=0, B=2 * FAKE, ldb=16, order_b=0,
+                 D=3 * FAKE, ldd=16, residual=4 * FAKE, ld_residual=16, pre=5 * FAKE, ld_pre=16)
+    for change in [dict(D=FAKE), dict(D=2 * FAKE), dict(D=4 * FAKE, ldd=24), dict(pre=FAKE),
+                   dict(pre=2 * FAKE), dict(pre=3 * FAKE), dict(pre=4 * FAKE)]:
+        fn = getattr(lib, "gemm_fused_" + t)
+        assert fn(**dict(fused, **change), stream=0, check=False) == BAD, change
+    grad = dict(M=5, N=16, K=16, alpha=1.0, A=FAKE, lda=16, order_a=0, B=2 * FAKE, ldb=16, order_b=0,
+                activation=2, pre=4 * FAKE, ld_pre=16, D=3 * FAKE, ldd=16, dbias=5 * FAKE)
+    for change in [dict(D=FAKE), dict(D=2 * FAKE), dict(D=4 * FAKE, ldd=24), dict(dbias=FAKE),
+                   dict(dbias=2 * FAKE), dict(dbias=3 * FAKE), dict(dbias=4 * FAKE)]:
+        fn = getattr(lib, "gemm_fused_grad_" + t)
+        assert fn(**dict(grad, **change), stream=0, check=False) == BAD, change
+
+
 def test_silu_is_of_the_fused_products_only():
     assert lib.gemm_bf16_f32acc_ex(8, 8, 8, 1.0, FAKE, 8, 0, FAKE, 8, 0, 0.0, None, 8, FAKE2, 8, 0,
                                    activation=lib.GEMM_ACT_SILU, stream=0, check=False) == BAD
