@@ -50,14 +50,14 @@ constexpr int kSlot = 8192;     // 32 x 64 FP32 sums of another piece
 // the accumulator cannot hold (they do not round it), so that a sum comes out smaller
 // by 1e-9 of itself per step of K.  A D of 16 bits does not show it, the FP32 sums of
 // its columns do (4.5e-6 at K = 4096, 0.6e-6 for FP32 products).  Where they are
-// wanted and a tile's K is longer than kUncut (an error of 2e-6), each part of kPart
-// is summed in the other accumulator and the epilogue warps add the parts in
-// registers: 1.2e-6 at any K.  The 128 registers per thread that this takes come from
-// the other warps.  (Measured at 4096 x 14336 x 4096: parts of 768 and 1024, whose
-// multiplication is over before the last tile's epilogue, take 670 and 633 us, of
-// 1280 578, of 1536 and 2048 563 us with errors of 1.4e-6 and 2.1e-6; one part 573.
-// At K = 1408 two parts take 20.8 us, one 18.5: an error of 1.7e-6.)
-constexpr int kPart = 1280, kUncut = 2048;
+// wanted and a tile's K is longer than a part, each part is summed in the other
+// accumulator and the epilogue warps add the parts in registers: 0.7e-6 (BF16) to
+// 0.95e-6 (FP16) at any K.  The 128 registers per thread that this takes come from the
+// other warps.  (Measured at 4096 x 14336 x 4096: parts of 768 602 us, of 896 588, of
+// 1280 -- whose two next parts cover a tile's epilogue -- 560 with an error of
+// 1.2e-6, one part 573.  At K = 1408 two parts 19.9 us, one 18.5: an error of 1.7e-6.)
+// A piece of K that a cluster's CTA adds alone may be kPiece long: 2.1e-6.
+constexpr int kPart = 768, kPiece = 2048;
 static_assert(kPart % (4 * BK) == 0, "a part is a number of steps");
 constexpr int kEpiRegs = 216, kOtherRegs = 72, kPartsRegs = 168;
 static_assert(2 * kEpiRegs + kOtherRegs <= 3 * kPartsRegs,
@@ -193,6 +193,23 @@ __device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, float (&v)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+// 32 lanes x 64 columns, one wait for two loads.
+__device__ __forceinline__ void tmem_load_64cols(uint32_t taddr, float (&v)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr + 0));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+        : "r"(taddr + 32));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 64; ++j) asm volatile("" : "+f"(v[j]));
 }
 
 // 16-byte piece p of row r of a box (128-byte swizzle).
@@ -709,19 +726,20 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
                             break;
                         }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (half + 2 * (q / 2) > last) continue;
-                            uint32_t raw[32];
+                        for (int q = 0; q < 4; q += 2) {
+                            if (half + q > last) continue;
+                            float raw[64];
                             __syncwarp();
-                            tmem_load_32cols(t_acc + (half + 2 * (q / 2)) * 64 + q % 2 * 32, raw);
+                            tmem_load_64cols(t_acc + (half + q) * 64, raw);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) run[q][j] += __uint_as_float(raw[j]);
+                            for (int j = 0; j < 64; ++j) run[q + j / 32][j % 32] += raw[j];
                         }
                         release_acc();
                     }
-                    // (By way of shared memory, which the multiplication keeps busy, this took
-                    // 18 us a tile, and eight columns at a time 14; this takes 10.)
-#pragma unroll 1
+                    // (Four sixteens of columns in a row: 10.6 us a tile one by one, 602 us
+                    // against 640 in all.  By way of shared memory, which the multiplication
+                    // keeps busy, it took 18.)
+#pragma unroll 4
                     for (int g = 0; g < 8 && !aborted; ++g) {
                         const int b = half + 2 * (g / 4), h = g % 4;
                         if (b > last) break;
@@ -1003,7 +1021,7 @@ Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &spli
         consider({1, am, bn, 1}, sms);
         for (int ks = 2; ks <= kMaxSplit; ks *= 2) {
             const int64_t tiles = ceil_div(p.M, am) * ceil_div(p.N, bn);
-            if (sums && p.K > static_cast<int64_t>(kUncut) * ks) continue;
+            if (sums && p.K > static_cast<int64_t>(kPiece) * ks) continue;
             if (kb >= 2 * ks && tiles <= split.resident[ks]) consider({1, am, bn, ks}, split.resident[ks]);
         }
     }
@@ -1119,7 +1137,7 @@ static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t str
         if (cut.ks > 1)
             e = launch_as<1, true, GRAD, TYPE, false>(m, a, dev, static_cast<int>(tiles * cut.ks), cut.ks, stream);
         else if constexpr (GRAD)
-            e = p.dbias != nullptr && p.K > kUncut ? launch_tiles(std::true_type{}) : launch_tiles(std::false_type{});
+            e = p.dbias != nullptr && p.K > kPart ? launch_tiles(std::true_type{}) : launch_tiles(std::false_type{});
         else
             e = launch_tiles(std::false_type{});
     }

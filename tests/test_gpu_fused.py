@@ -318,26 +318,29 @@ def test_cuts(dtype, oa, ob, kernel, M, N, K):
 @pytest.mark.parametrize("oa,ob", [(0, 0), (0, 1), (1, 0)])
 @pytest.mark.parametrize("kernel,M,N,K", [("fused_tc<{},pair>", 2300, 2600, 6000), ("fused_tc<{}>", 500, 1100, 14336),
                                           ("fused_tc<{}>", 130, 1030, 20001), (None, 64, 300, 4100),
-                                          (None, 1, 64, 30000), (None, 2000, 30, 2049)])
+                                          (None, 1, 64, 30000), (None, 2000, 30, 2049),
+                                          (None, 700, 1500, 776)])
 def test_column_sums_of_a_long_k(dtype, oa, ob, kernel, M, N, K):
     """Sums in parts.  An addition to the accumulator cuts half a unit of its last place on the mean, 0.36 *
     2^-23 of it; sixteen products enter at once, and a random sum's size on the way is 2/3 of its last: 1.8e-9 per
-    step of K, that is 2.3e-6 for a part of 1280 and 3.7e-6 for the 2048 that go without parts (3.6e-5 for the
-    longest K here, if it were not cut).  Twice that, and 1e-6 for the rest."""
+    step of K, that is 1.4e-6 for a part of 768 and 3.7e-6 for a cluster's piece of 2048 (3.6e-5 for the longest
+    K here, if it were not cut).  Twice that, and 1e-6 for the rest."""
     A, B, _, Z, _ = big(M, N, K, dtype, oa, ob, seed=3)
     z = A.double() @ B.double()
     size = A.double().abs() @ B.double().abs()
     for act in (NONE, GELU):
         d, sums = lib.gemm_fused_grad(A, B, Z, activation=act, bias_grad=True)
+        name = lib.gemm_last_kernel()
         if kernel is not None and not oa and K % 8 == 0:
-            assert lib.gemm_last_kernel() == kernel.format(dtype)
+            assert name == kernel.format(dtype)
         x = Z.double().requires_grad_()
         (x if act == NONE else torch.nn.functional.gelu(x, approximate="tanh")).sum().backward()
         ref = z * x.grad
         near(d, ref, size, K, dtype, 1.13, 2.0 ** -18 * z.abs())
         want = ref.sum(0)
         slope = 0 if act == NONE else float((2.0 ** -18 * z.abs()).norm())  # (its error: rows' are independent)
-        assert float((sums.double() - want).norm()) <= 8.4e-6 * float(want.norm()) + slope
+        most = 8.4e-6 if "split" in name else 3.8e-6
+        assert float((sums.double() - want).norm()) <= most * float(want.norm()) + slope
         assert lib.gemm_last_device_status() == lib.GEMM_OK
     odd = torch.empty(M, N + 3, dtype=A.dtype, device="cuda")[:, 1:N + 1]
     again, sums2 = lib.gemm_fused_grad(A, B, Z, activation=GELU, bias_grad=True, out=odd)
