@@ -54,7 +54,7 @@ constexpr int kSlot = 8192;     // 32 x 64 FP32 sums of another piece
 // accumulator and the epilogue warps add the parts in registers: 0.7e-6 (BF16) to
 // 0.95e-6 (FP16) at any K.  The 128 registers per thread that this takes come from the
 // other warps.  (Measured at 4096 x 14336 x 4096: parts of 768 602 us, of 896 588, of
-// 1280 -- whose two next parts cover a tile's epilogue -- 560 with an error of
+// 1280 -- two of which cover a tile's epilogue -- 560 with an error of
 // 1.2e-6, one part 573.  At K = 1408 two parts 19.9 us, one 18.5: an error of 1.7e-6.)
 // A piece of K that a cluster's CTA adds alone may be kPiece long: 2.1e-6.
 constexpr int kPart = 768, kPiece = 2048;
@@ -511,9 +511,14 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
     // block of 64 columns.
     const int e = warp, quarter = warp % 4, half = (e / 4) & 1;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t box_d = ring0 + args.ring_bytes + (e & 7) * args.boxes * kBox;
-    const uint32_t box_pre = box_d + kBox;  // (forward with pre kept)
-    const uint32_t box_in = box_d + (args.boxes - 1) * kBox;
+    // A block's box: residual / pre comes into it and D leaves from it.  With a residual
+    // or pre there are two in turn, so that the next block's is fetched while this
+    // block is computed (8192 x 8192 x 512 with a residual: 84 us with one box for it and
+    // one for D, now 75).
+    const uint32_t box_0 = ring0 + args.ring_bytes + (e & 7) * args.boxes * kBox;
+    const uint32_t box_pre = box_0 + kBox;  // (forward with pre kept)
+    const uint32_t other = args.in != nullptr ? (args.boxes - 1) * kBox : 0;
+    uint32_t box = box_0, flip = 0;  // this block's; which one is the next block's
     const uint32_t bias_at = bias0 + (e & 7) * 128;
     const uint32_t ibar = ibar0 + 8 * (e & 7);
     const bool has_in = args.in != nullptr;
@@ -534,46 +539,52 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
         blocks = rows > 0 ? (wide + 63) / 64 : 0;
     };
     auto fetch_in = [&](int64_t r0, int64_t c0) {
+        // (this warp's own reads of the box are over)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
         if (elect_one()) {
+            bulk_wait_read();  // (its last D has left)
             mbar_arrive_expect_tx(ibar, kBox);
-            tma_load_2d<CG>(box_in, &map_in, static_cast<int32_t>(c0), static_cast<int32_t>(r0),
+            tma_load_2d<CG>(box_0 + flip * other, &map_in, static_cast<int32_t>(c0), static_cast<int32_t>(r0),
                             CG == 1 ? ibar : map_to_rank(ibar, rank));
         }
         __syncwarp();
         pending = true;
     };
 
-    // Before a block is written: its box of residual / pre is there, and the boxes of
-    // the block before have left.  False: gave up.
+    // Before a block is written: its residual / pre is in its box, and what the boxes
+    // held before has left.  False: gave up.
     auto open_block = [&](int64_t c0, int width) -> bool {
-        if (has_in) {
-            if (args.tma_in) {
-                if (!pending) fetch_in(row0, c0);
-                if (!wait_all(ibar, blocks_in & 1)) return false;
-                ++blocks_in;
-                pending = false;
-            } else {
-                rows_to_box(box_in, args.in, args.ld_in, row0, nrows, c0, width, args.even_in != 0);
-                __syncwarp();
-            }
+        const bool fetched = has_in && args.tma_in;
+        if (fetched && !pending) fetch_in(row0, c0);
+        box = box_0 + flip * other;
+        flip ^= 1;
+        if (!fetched || has_pre) {
+            if (elect_one()) bulk_wait_read();
+            __syncwarp();
         }
-        if (elect_one()) bulk_wait_read();
-        __syncwarp();
+        if (fetched) {
+            if (!wait_all(ibar, blocks_in & 1)) return false;
+            ++blocks_in;
+            pending = false;
+        } else if (has_in) {
+            rows_to_box(box, args.in, args.ld_in, row0, nrows, c0, width, args.even_in != 0);
+            __syncwarp();
+        }
         return true;
     };
-    // After: next() fetches the next box, the written ones go to memory.
-    auto close_block = [&](int64_t c0, int width, auto &&next) {
+    // After: the boxes go to memory.
+    auto close_block = [&](int64_t c0, int width) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (has_in && args.tma_in) next();
         // (TMA stores whole 16-byte pieces, and its box is 64 columns wide: a block with
         // an odd end, or cut by the tile's, goes by rows)
         const bool whole = width == 64 || (args.N % 8 == 0 && c0 + width == args.N);
         if (args.tma_d && whole) {
             if (elect_one())
-                tma_store_2d(&map_d, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box_d);
+                tma_store_2d(&map_d, static_cast<int32_t>(c0), static_cast<int32_t>(row0), box);
         } else {
-            box_to_rows(box_d, args.D, args.ldd, row0, nrows, c0, width, args.even_d != 0);
+            box_to_rows(box, args.D, args.ldd, row0, nrows, c0, width, args.even_d != 0);
         }
         if (has_pre) {
             if (args.tma_pre && whole) {
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             float x[8];
-            widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2 + p)), x);
+            widen<TYPE>(ld_shared_u4(box + piece_at(lane, h * 2 + p)), x);
             if (args.act == kActGelu)
                 slope_8<kActGelu>(v + p * 8, x);
             else if (args.act == kActSilu)
@@ -665,16 +676,17 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         float x[8];
-                        widen<TYPE>(ld_shared_u4(box_in + piece_at(lane, h * 2 + p)), x);
+                        widen<TYPE>(ld_shared_u4(box + piece_at(lane, h * 2 + p)), x);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[p * 8 + j] += x[j];
                     }
                 }
             }
-            narrow_16<TYPE>(v, box_d, lane, h);
+            narrow_16<TYPE>(v, box, lane, h);
             if (GRAD && args.part != nullptr) add_columns(v, c0, h, width);
+            if (h == 0 && has_in && args.tma_in) next();
         }
-        close_block(c0, width, next);
+        close_block(c0, width);
         return true;
     };
 
@@ -758,9 +770,10 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
                             for (int j = 0; j < 16; ++j) v[j] = args.alpha * run[i / 2][i % 2 * 16 + j];
                         }
                         if (has_in) times_slopes(v, h);
-                        narrow_16<TYPE>(v, box_d, lane, h);
+                        narrow_16<TYPE>(v, box, lane, h);
                         add_columns(v, c0, h, width);
-                        if (h == 3) close_block(c0, width, [&]() { fetch_next(b); });
+                        if (h == 0 && has_in && args.tma_in) fetch_next(b);
+                        if (h == 3) close_block(c0, width);
                     }
                     if (aborted) break;
                     continue;
