@@ -53,7 +53,7 @@ constexpr int kSlot = 8192;     // 32 x 64 FP32 sums of another piece
 // wanted and a tile's K is longer than a part, each part is summed in the other
 // accumulator and the epilogue warps add the parts in registers: 0.7e-6 (BF16) to
 // 0.95e-6 (FP16) at any K.  The 128 registers per thread that this takes come from the
-// other warps.  (Measured at 4096 x 14336 x 4096: parts of 768 602 us, of 896 588, of
+// other warps.  (Measured at 8192 x 14336 x 4096: parts of 768 602 us, of 896 588, of
 // 1280 -- two of which cover a tile's epilogue -- 560 with an error of
 // 1.2e-6, one part 573.  At K = 1408 two parts 19.9 us, one 18.5: an error of 1.7e-6.)
 // A piece of K that a cluster's CTA adds alone may be kPiece long: 2.1e-6.

@@ -347,6 +347,37 @@ def test_column_sums_of_a_long_k(dtype, oa, ob, kernel, M, N, K):
     assert torch.equal(again, d) and torch.equal(sums, sums2)
 
 
+@pytest.mark.parametrize("M,N,K", [(2304, 2560, 1600), (300, 520, 1000)])
+def test_column_sums_on_streams_in_graphs_and_in_place(M, N, K):
+    """Sums in parts, and the workspace of the blocks' sums, several calls at once."""
+    A, B, _, Z, _ = big(M, N, K, "bf16", 0, 0)
+    want, sums = lib.gemm_fused_grad(A, B, Z, activation=SILU, bias_grad=True)
+    over = Z.clone()
+    d, s = lib.gemm_fused_grad(A, B, over, activation=SILU, bias_grad=True, out=over)
+    assert torch.equal(over, want) and torch.equal(s, sums)
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(4)]
+    got = [lib.gemm_fused_grad(A, B, Z, activation=SILU, bias_grad=True, stream=side) for side in sides * 3]
+    torch.cuda.synchronize()
+    assert all(torch.equal(d, want) and torch.equal(s, sums) for d, s in got)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            graphs.append((graph, *lib.gemm_fused_grad(A, B, Z, activation=SILU, bias_grad=True)))
+    for graph, d, s in graphs:
+        d.zero_(), s.zero_()
+    torch.cuda.synchronize()
+    for (graph, _, _), side in zip(graphs, sides):  # side by side
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, d, s in graphs:
+        assert torch.equal(d, want) and torch.equal(s, sums)
+    assert lib.gemm_last_device_status() == lib.GEMM_OK
+
+
 def test_rows_behind_the_last_are_left():
     for M, N, K in ((300, 520, 128), (2100, 2500, 64), (20, 4096, 2048)):
         A, B, R, Z, b = big(M, N, K, "bf16", 0, 1)
