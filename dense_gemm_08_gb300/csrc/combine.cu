@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const __grid
                     if ((C == 1 ? c0 + WIDE : c0 - lane * WIDE + C * apart) <= p.N)
                         grad_pieces<YT, DT, YVEC, kAll, R, C>(p, ch, t, c0, apart, dvec, dot);
                     else if (C > 1 && !has_end<WIDE, C>(p.N, c0, apart))
-                        grad_pieces<YT, DT, YVEC, (C > 1 ? kAllOrNone : kSome), R, C>(p, ch, t, c0, apart, dvec, dot);
+                        grad_pieces<YT, DT, YVEC, (C > 1 ? kAllOrNone : kSome), R, C>(p, ch, t, c0, apart, dvec,
+                                                                                      dot);
                     else
                         grad_pieces<YT, DT, YVEC, kSome, R, C>(p, ch, t, c0, apart, dvec, dot);
                 }

@@ -425,7 +425,8 @@ cudaError_t launch(K kernel, int64_t ctas, int threads, size_t smem, int cluster
 // large (4096 x 4096: 1 row 7.8 us, 2 rows 8.1, 4 rows 14.9 and 14.4; 4096 x 14336,
 // 4 rows 43 and 26; 4096 x 1024, 4 rows 7.3 and 11).
 bool rows_fit(const FusedProblem &p, int64_t bytes) {
-    if (p.M > (bytes == 4 || p.N * p.K <= (int64_t(8) << 20) ? 4 : 2) || p.K == 0 || !p.b_kmajor || !rows_on_16(p.B, p.ldb, bytes)) return false;
+    const int most = bytes == 4 || p.N * p.K <= (int64_t(8) << 20) ? 4 : 2;
+    if (p.M > most || p.K == 0 || !p.b_kmajor || !rows_on_16(p.B, p.ldb, bytes)) return false;
     if (p.M == 1)
         return reinterpret_cast<uintptr_t>(p.A) % 16 == 0 && (p.a_kmajor || p.lda == 1);
     return p.a_kmajor && rows_on_16(p.A, p.lda, bytes);
