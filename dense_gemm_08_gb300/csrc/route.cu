@@ -17,9 +17,10 @@
 // with a bound of its error; the candidates are all that could be among the k
 // largest, and where two that are next to each other are closer than that, the
 // candidates (one per lane) are compared again in 64 bits: 0.3 % of the tokens for
-// 256 experts with sigmoid scores of N(0, 1.5^2) logits.  Group scores of two
-// rounded terms that are too close are rarer; then the whole token is chosen again
-// in 64 bits.  (FP64 runs at 1/64 of the FP32 rate.)
+// 256 experts with sigmoid scores of N(0, 1.5^2) logits.  Group scores of two rounded
+// terms that are too close are rarer; those groups' largest experts are then computed
+// in 64 bits, or, where they are too many, the whole token is chosen again.  (FP64 runs
+// at 1/64 of the FP32 rate.)
 #include <type_traits>
 
 #include "mixture.h"
@@ -185,12 +186,106 @@ __device__ __forceinline__ int in_rounds(const RouteProblem &p, int ept,
     return mine;
 }
 
+// Shared memory of a warp.
+template <int VPT>
+struct Slots {
+    __align__(16) uint32_t key[32 * VPT];  // of register i of lane l at l * VPT + i
+    __align__(16) unsigned long long candidate[32];
+    __align__(16) uint32_t best[32];
+    uint16_t at[32];
+    int number[32];
+    float logit[32];
+};
+
+// The groups that stay, where FP32 cannot tell: `score`, the lane's group's, lies near
+// the border between `last` (stays) and `next` (does not).  Groups further off than
+// `near` are certain; of the others the experts that may be among a group's two
+// largest (at least its second, g2, less `tol`, or a relative bound without a bias) are
+// dealt out to the lanes and computed in 64 bits.  False: more than 32 of them, or NaNs.
+// (Choosing the whole token again in 64 bits takes 8 us, at the end of a launch more
+// often than not: 16384 tokens of 256 experts in 8 groups 30 us, now 25.)
+template <int TYPE, int VPT, bool VEC>
+__device__ __noinline__ bool kept_exactly(const RouteProblem &p, const void *row, int ept,
+                                          Slots<VPT> &s, float m, float z, uint32_t g2, uint32_t score,
+                                          uint32_t last, uint32_t next, float near, float tol,
+                                          uint32_t &kept) {
+    using V = Value<TYPE>;
+    const int lane = threadIdx.x % 32, size = p.experts / p.groups;
+    const bool biased = p.bias != nullptr;
+    const float high = Order<float>::value(last) + near, low = Order<float>::value(next) - near;
+    if (!(high >= low) || (!biased && !(low > 1e-30f))) return false;
+    const float mine = Order<float>::value(score);
+    const bool open = score != 0 && mine <= high && mine >= low;
+    const uint32_t in = __ballot_sync(kAll, score != 0 && !open && score > last);
+    // what an expert of the lane's group must reach
+    float least = -INFINITY;
+    if (g2 != 0 && p.top == 2)
+        least = biased ? Order<float>::value(g2) - tol : Order<float>::value(g2) * (1.f - 0x1p-14f);
+    else if (p.top == 1)
+        least = mine - tol;
+    if (__any_sync(kAll, open && isnan(least))) return false;
+    const uint32_t opened = __ballot_sync(kAll, open);
+    float x[VPT];
+    load_row<TYPE, VPT, VEC>(p, row, ept, x);
+    const float inv = z > 0 ? 1.f / z : 0.f;
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int e = lane * ept + i;
+        const bool there = i < ept && e < p.experts;
+        const int g = there ? e / size : 0;
+        const float from = __shfl_sync(kAll, least, g);
+        if (!there || x[i] == -INFINITY || !((opened >> g) & 1u)) continue;
+        const float c = score_of<float>(p, x[i], m, inv) + (biased ? __ldg(p.bias + e) : 0.f);
+        if (!(c < from) && c != -INFINITY) mask |= 1u << i;
+    }
+    int total = 0;
+    for (uint32_t who; (who = __ballot_sync(kAll, mask != 0)) != 0; mask &= mask - 1) {
+        const int slot = total + __popc(who & ((1u << lane) - 1u));
+        if (mask != 0 && slot < 32) s.at[slot] = static_cast<uint16_t>(lane * ept + __ffs(mask) - 1);
+        total += __popc(who);
+        if (total > 32) break;
+    }
+    __syncwarp();
+    if (total > 32) return false;
+    double md = 0, zd = 0;
+    if (p.score == kSoftmax) softmax_stats<double>(x, md, zd);
+    using Key = Order<double>::Key;
+    Key key = 0;
+    int of = -1;
+    if (lane < total) {
+        const int e = s.at[lane];
+        double c = score_of<double>(p, V::load(row, e), md, 1.0 / zd);
+        if (biased) c += __ldg(p.bias + e);
+        key = Order<double>::of(c);
+        of = e / size;
+    }
+    Key a1 = 0, a2 = 0;
+    for (int i = 0; i < total; ++i) {
+        const Key o = __shfl_sync(kAll, key, i);
+        if (__shfl_sync(kAll, of, i) == lane) merge_top(a1, a2, o, Key(0));
+    }
+    Key sum = a1;
+    if (p.top == 2 && a2 != 0)
+        sum = a1 == Order<double>::NAN_KEY ? a1
+                                           : Order<double>::of(Order<double>::value(a1) + Order<double>::value(a2));
+    int before = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const Key o = __shfl_sync(kAll, sum, g);
+        if ((opened >> g) & 1u) before += o > sum || (o == sum && g < lane) ? 1 : 0;
+    }
+    kept = in | __ballot_sync(kAll, open && before < p.kept - __popc(in));
+    __syncwarp();
+    return true;
+}
+
 // Keys of the lane's experts, 0 where they or their groups are out of the choice.
 // tol: how far apart two c must be to differ for certain.  FP32: false where two
 // groups are too close.
-template <typename F, int VPT, bool VEC>
-__device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[VPT], int ept, F m,
-                                        F z, typename Order<F>::Key (&key)[VPT], float &tol) {
+template <typename F, int TYPE, int VPT, bool VEC>
+__device__ __forceinline__ bool keys_of(const RouteProblem &p, const void *row, Slots<VPT> *slots,
+                                        const float (&x)[VPT], int ept, F m, F z,
+                                        typename Order<F>::Key (&key)[VPT], float &tol) {
     using Key = typename Order<F>::Key;
     constexpr bool FAST = std::is_same<F, float>::value;
     const int lane = threadIdx.x % 32;
@@ -287,8 +382,24 @@ __device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[
         const Key o = __shfl_sync(kAll, score, g);
         before += o > score || (o == score && g < lane) ? 1 : 0;
     }
-    const uint32_t kept = __ballot_sync(kAll, score != 0 && before < p.kept);
-    const bool stays = (kept >> lane) & 1u;
+    uint32_t kept = __ballot_sync(kAll, score != 0 && before < p.kept);
+    if constexpr (FAST) {
+        if (biased || group_sums) {
+            const bool stays = (kept >> lane) & 1u;
+            const Key next = Order<F>::warp_max(stays ? Key(0) : score);
+            const Key last = ~Order<F>::warp_max(stays ? ~score : Key(0));
+            if (next != 0) {
+                const float a = Order<F>::value(last), c = Order<F>::value(next);
+                // (without a bias scores are positive and their errors relative, 1.2 |x|
+                // units of 2^-23 with |x| below 80 among them: below 2^-16)
+                const float near = biased ? 2 * tol : a * 0x1p-14f;
+                if ((!(a - c > near) || (!biased && !(a > 1e-30f))) &&
+                    !kept_exactly<TYPE, VPT, VEC>(p, row, ept, *slots, m, z, g2, score, last, next, near,
+                                                  tol, kept))
+                    return false;
+            }
+        }
+    }
     if (aligned) {
         const bool mine = (kept >> (lane / lanes)) & 1u;
 #pragma unroll
@@ -297,19 +408,6 @@ __device__ __forceinline__ bool keys_of(const RouteProblem &p, const float (&x)[
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (i < ept && !((kept >> ((lane * ept + i) / size & 31)) & 1u)) key[i] = 0;
-    }
-    if constexpr (FAST) {
-        if (biased || group_sums) {
-            const Key next = Order<F>::warp_max(stays ? Key(0) : score);
-            const Key last = ~Order<F>::warp_max(stays ? ~score : Key(0));
-            if (next != 0) {
-                const float a = Order<F>::value(last), c = Order<F>::value(next);
-                // (without a bias scores are positive and their errors relative, 1.2 |x|
-                // units of 2^-23 with |x| below 80 among them: below 2^-16)
-                const float near = biased ? 2 * tol : a * 0x1p-14f;
-                if (!(a - c > near) || (!biased && !(a > 1e-30f))) return false;
-            }
-        }
     }
     return true;
 }
@@ -322,7 +420,7 @@ __device__ __noinline__ int choose_exactly(const RouteProblem &p, const void *ro
     double m = 0, z = 0;
     if (p.score == kSoftmax) softmax_stats<double>(x, m, z);
     Order<double>::Key key[VPT];
-    keys_of<double, VPT, VEC>(p, x, ept, m, z, key, tol);
+    keys_of<double, TYPE, VPT, VEC>(p, row, static_cast<Slots<VPT> *>(nullptr), x, ept, m, z, key, tol);
     return in_rounds<double>(p, ept, key);
 }
 
@@ -347,17 +445,6 @@ __device__ __noinline__ int place_exactly(const RouteProblem &p, const void *row
     return before;
 }
 
-// Shared memory of a warp.
-template <int VPT>
-struct Slots {
-    __align__(16) uint32_t key[32 * VPT];  // of register i of lane l at l * VPT + i
-    __align__(16) unsigned long long candidate[32];
-    __align__(16) uint32_t best[32];
-    uint16_t at[32];
-    int number[32];
-    float logit[32];
-};
-
 // What a lane knows of the choice: an expert (or -1), its logit and its place.
 struct Choice {
     int expert, place;
@@ -374,7 +461,7 @@ __device__ __forceinline__ bool choose(const RouteProblem &p, const void *row, c
     const bool biased = p.bias != nullptr;
     uint32_t key[VPT];
     float tol;
-    if (!keys_of<float, VPT, VEC>(p, x, ept, m, z, key, tol)) return false;
+    if (!keys_of<float, TYPE, VPT, VEC>(p, row, &s, x, ept, m, z, key, tol)) return false;
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) best = max(best, key[i]);
@@ -446,9 +533,10 @@ __device__ __forceinline__ bool choose(const RouteProblem &p, const void *row, c
         if (e >= 0) s.best[place] = k32, s.number[place] = e, s.logit[place] = l;
         __syncwarp();
         // the candidates in order: too close to the next one, unless that has the
-        // same logit and the same bias (equal for certain)?
+        // same logit and the same bias (equal for certain)?  (Also past the k-th: equal
+        // ones may stand between it and one that is close.)
         bool close = false;
-        if (lane < p.k && lane + 1 < total &&
+        if (lane + 1 < total &&
             !(Order<float>::value(s.best[lane]) - Order<float>::value(s.best[lane + 1]) > tol))
             close = !(s.logit[lane] == s.logit[lane + 1] &&
                       __ldg(p.bias + s.number[lane]) == __ldg(p.bias + s.number[lane + 1]));
@@ -491,7 +579,7 @@ __device__ __forceinline__ float share(const RouteProblem &p, bool has, float x,
 
 // (Register limits: many warps per SM hide the latency of each; the spills are in the
 // parts that run rarely.  Up to 256 experts 12 CTAs per SM: 16384 x 256 without a bias
-// 10.8 us, with 8 CTAs 11.6; CTAs that stay and load the next token ahead 14.4.)
+// 11.4 us, with 8 CTAs 0.8 more; CTAs that stay and load the next token ahead 14.4.)
 template <int TYPE, int VPT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 12 : VPT <= 16 ? 5 : 3)
     route_kernel(const __grid_constant__ RouteProblem p) {

@@ -245,6 +245,35 @@ def test_gradient_against_differences(score, renorm):
     check(got, ref, size * (10 * h * h + 1e-10 + 200 * 2.0 ** -23))
 
 
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("experts,groups,kept", [(256, 8, 4), (256, 16, 5), (256, 32, 7), (160, 8, 3), (64, 2, 1)])
+def test_groups_that_fp32_cannot_tell_apart(score, biased, top, experts, groups, kept):
+    """Groups of the same logits, each in an order of its own, some a few units apart or equal."""
+    rng = np.random.default_rng([experts, groups, top])
+    T, size = 300, experts // groups
+    base = rng.standard_normal((T, 1, size)).astype(np.float32) * 1.5
+    x = np.repeat(base, groups, 1)
+    units = rng.integers(-3, 4, x.shape) * (rng.random(x.shape) < 0.3)
+    x = (x.view(np.int32) + units.astype(np.int32)).view(np.float32)
+    bias = np.tile(0.1 * rng.standard_normal(size), groups).astype(np.float32) if biased else None
+    if not biased:
+        x = rng.permuted(x, axis=2)
+    x[::9] = base[::9, :, :]  # equal groups
+    x[::11, 1::2] = rng.standard_normal((len(x[::11]), groups // 2, size)).astype(np.float32)
+    x = x.reshape(T, experts)
+    for g, n in ((groups, kept), (1, 1)):  # (and by themselves)
+        chosen, _ = lib.route(torch.from_numpy(x).cuda(), min(6, size), score=score,
+                              bias=torch.from_numpy(bias).cuda() if biased else None, groups=g,
+                              groups_kept=n, group_top=top)
+        ids, _ = route_ref(x.astype(np.float64), min(6, size), score,
+                           None if bias is None else bias.astype(np.float64), g, n, top, True, 1.0)
+        off = (chosen.cpu().numpy() != ids).any(1)
+        # (64 bits round too: sums of two scores below 2 that are within 2^-50 may go either way)
+        assert off.sum() <= T // 100, off.sum()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 @pytest.mark.parametrize("score", [SOFT, SIG])
 @pytest.mark.parametrize("experts", [1, 28, 64])
