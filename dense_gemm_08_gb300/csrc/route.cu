@@ -236,8 +236,9 @@ __device__ __noinline__ bool kept_exactly(const RouteProblem &p, const void *row
         const int g = there ? e / size : 0;
         const float from = __shfl_sync(kAll, least, g);
         if (!there || x[i] == -INFINITY || !((opened >> g) & 1u)) continue;
-        const float c = score_of<float>(p, x[i], m, inv) + (biased ? __ldg(p.bias + e) : 0.f);
-        if (!(c < from) && c != -INFINITY) mask |= 1u << i;
+        const float b = biased ? __ldg(p.bias + e) : 0.f;
+        const float c = score_of<float>(p, x[i], m, inv) + b;
+        if (!(c < from) && b != -INFINITY) mask |= 1u << i;
     }
     int total = 0;
     for (uint32_t who; (who = __ballot_sync(kAll, mask != 0)) != 0; mask &= mask - 1) {
@@ -312,12 +313,12 @@ __device__ __forceinline__ bool keys_of(const RouteProblem &p, const void *row, 
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const bool masked = x[i] == -INFINITY;
+            // (a bias of -infinity is a mask too, also of a NaN)
+            const bool masked = x[i] == -INFINITY || (biased && b[i] == -INFINITY);
             const F s = masked ? F(0) : score_of<F>(p, x[i], m, inv);
             if (biased) {
                 key[i] = masked ? Key(0) : Order<F>::of(s + static_cast<F>(b[i]));
                 by[i] = key[i];
-                // (a bias of -infinity is a mask)
                 if (FAST && key[i] != 0) most = fmaxf(most, static_cast<float>(s) + fabsf(b[i]));
             } else {
                 key[i] = Order<F>::of(static_cast<F>(x[i]));
