@@ -325,14 +325,25 @@ __device__ __forceinline__ bool keys_of(const RouteProblem &p, const void *row, 
                 by[i] = masked ? Key(0) : Order<F>::of(s);
             }
         }
-        // Errors in FP32, of the largest score or of s + |b|.  exp(-|x|) and exp(x - m)
-        // are off by 2 + 1.2 |x| units of 2^-23 of themselves and by the rounding of
-        // x - m: at most 1 unit of the largest score, as |x| exp(-|x|) < 0.4, or 3 where
-        // |x| is small; the reciprocal and the products 4; the sum z of a softmax 37 roundings;
-        // c itself 1.  Together below 2^-20 for a sigmoid, 2^-18 for a softmax.  Two
-        // values differ for certain when they are twice that apart, sums of two of
-        // them four times.
-        if (FAST && biased) tol = warp_max(most) * (p.score == kSigmoid ? 0x1p-19f : 0x1p-17f);
+        // Errors in FP32, in units of 2^-23; top is the largest s + |b|.  A score's
+        // exponential is off by 2 + 1.2 d units of itself, with d = |x| for a sigmoid (past
+        // x = 0 it is the smaller term, and d exp(-d) < 0.4) and d = m - x for a softmax, whose
+        // x - m is rounded: 0.5 d more.  The sum and the reciprocal add 3 units, of a softmax
+        // 25 (z is a sum of 37 roundings), c itself half a unit of s + |b|: 5 or 28 units of
+        // top, and 1.2 or 1.7 d s.  As d <= log(1 / s), and s log(1 / s) grows up to s = 1 / e,
+        // the latter is 1.2 or 1.7 log(1 / top) units of top at most: 3 or 4 from top = 1 / 8
+        // on, and the largest part where all scores are small (a sigmoid's logits far below 0,
+        // a softmax whose largest logits the bias masks; with 8 units for all, groups at -60
+        // were chosen wrong).  Results below 2^-126 may be 0 instead.  So 8 or 32 units, times the
+        // logarithm's share, and 2^-125; two values differ for certain when they are twice
+        // that apart, sums of two of them four times.
+        if (FAST && biased) {
+            const float top = warp_max(most);
+            tol = top * (p.score == kSigmoid ? 0x1p-19f : 0x1p-17f);
+            if (top < 0.125f)
+                tol *= 1.f - (p.score == kSigmoid ? 0.15f : 0.06f) * __logf(fmaxf(top, 0x1p-126f));
+            tol += 0x1p-124f;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) by[i] = key[i] = Order<F>::of(static_cast<F>(x[i]));
