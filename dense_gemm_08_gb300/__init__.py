@@ -686,19 +686,20 @@ def _stream_of(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
-def _empty_for(stream):
-    """torch.empty for an output that `stream` (None: torch's current stream) writes: memory of
-    that stream's pool, as work of another stream may still use what the current one's pool
-    hands out."""
+def _empty_for(stream, make=None):
+    """torch.empty (or `make`) for an output that `stream` (None: torch's current stream) writes:
+    memory of that stream's pool, as work of another stream may still use what the current
+    one's pool hands out."""
     torch = _torch()
+    make = torch.empty if make is None else make
     if stream is None:
-        return torch.empty
+        return make
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
 
     def empty(*args, **kwargs):
         with torch.cuda.stream(stream):
-            return torch.empty(*args, **kwargs)
+            return make(*args, **kwargs)
     return empty
 
 
@@ -1092,8 +1093,10 @@ def combine_grad(dD, Y, position, weights=None, weight_grad=True, out=None, stre
     """(dY, dweights) of ``combine``: dY[position[t, j]] = weights[t, j] * dD[t] in Y's dtype,
     dweights[t, j] = dot(dD[t], Y[position[t, j]]) in float32 (None without weight_grad).
 
-    dD is float32 or has Y's dtype.  Rows of dY (``out``, or a new tensor) that no
-    position names are left as they are; the positions inside Y must differ.
+    dD is float32 or has Y's dtype; the positions inside Y must differ.  Rows of dY
+    that no position names are 0 in a new tensor, which is filled first, and left as they
+    are in ``out`` (where every row has a token, or the others are not read,
+    ``out=torch.empty_like(Y)`` saves the filling).
     """
     y_type, d_type = _kind_of(Y, "Y"), _kind_of(dD, "dD")
     rows, N = _two(Y, "Y")
@@ -1113,7 +1116,8 @@ def combine_grad(dD, Y, position, weights=None, weight_grad=True, out=None, stre
     now = _here(device)
     new = _new if stream is None else _empty_for(stream)
     if out is None:
-        out = new((rows, N), dtype=Y.dtype, device=device)
+        zeros = _torch().zeros if stream is None else _empty_for(stream, _torch().zeros)
+        out = zeros((rows, N), dtype=Y.dtype, device=device)
         ld_dy = N
     dweights = new(pairs, dtype=_f32, device=device) if weight_grad else None
     if k > 0:

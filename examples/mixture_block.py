@@ -61,7 +61,8 @@ def backward(p, saved, dout):
     dz, db1 = lib.gemm_fused_grad(dout, p["W2"], z, activation=lib.GEMM_ACT_GELU, bias_grad=True)
     dm = lib.gemm_fused(dz, p["W1"], residual=dout)
     d = dict(W1=lib.gemm(dz.t(), m), b1=db1, W2=lib.gemm(dout.t(), h), b2=lib.gemm(ones, dout)[0])
-    dy, dweights = lib.combine_grad(dm, y, place, weights=weights)
+    # (rows of dropped tokens, behind the last group, are not read below)
+    dy, dweights = lib.combine_grad(dm, y, place, weights=weights, out=torch.empty_like(y))
     d["We"] = lib.gemm_grouped_wgrad(x, dy, offsets, row_index=token).transpose(1, 2)
     rows = lib.gemm_grouped(dy, p["We"], offsets)
     dx = lib.combine(rows, place, residual=dm)  # (of the gather: no weights)
