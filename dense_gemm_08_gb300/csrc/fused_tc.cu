@@ -52,17 +52,22 @@ constexpr int kMaxSplit = 8;
 constexpr int kSlot = 8192;     // 32 x 64 FP32 sums of another piece
 
 // Column sums of a long K: sums in parts.  The tensor cores cut what an addition to
-// the accumulator cannot hold (they do not round it), so that a sum comes out smaller
-// by 1e-9 of itself per step of K.  A D of 16 bits does not show it, the FP32 sums of
-// its columns do (4.5e-6 at K = 4096, 0.6e-6 for FP32 products).  Where they are
-// wanted and a tile's K is longer than a part, each part is summed in the other
-// accumulator and the epilogue warps add the parts in registers: 0.7e-6 (BF16) to
-// 0.95e-6 (FP16) at any K.  The 128 registers per thread that this takes come from the
+// the accumulator cannot hold (they do not round it): half a unit of its last place on the
+// mean for 16 steps of K, so that a sum of random signs comes out smaller by 1e-9 of itself per
+// step (of one sign 1.3e-9; FP16, whose products are cut too, 5e-9).  A D of 16 bits
+// does not show it, the FP32 sums of its columns do (4.5e-6 at K = 4096, 0.6e-6 for
+// FP32 products).  Where they are wanted and a tile's K is longer than a part, each part
+// is summed in the other accumulator and the epilogue warps add the parts in registers:
+// 0.7e-6 (BF16) to 0.95e-6 (FP16) at any K, 1.0e-6 and 3.9e-6 for products of one sign.
+// The 128 registers per thread that this takes come from the
 // other warps.  (Measured at 8192 x 14336 x 4096: parts of 768 602 us, of 896 588, of
 // 1280 -- two of which cover a tile's epilogue -- 560 with an error of
 // 1.2e-6, one part 573.  At K = 1408 two parts 19.9 us, one 18.5: an error of 1.7e-6.)
-// A piece of K that a cluster's CTA adds alone may be kPiece long: 2.1e-6.
-constexpr int kPart = 768, kPiece = 2048;
+// The piece of K of a cluster's CTA is summed in parts too, side by side in TMEM: its one
+// tile leaves room for them, and they are added as they are read (64 x 1000, K = 8192:
+// 16.5 us, 16.2 with a piece of 1024 in one; 300 x 1024 25.9 and 24.9; 128 x 2048, K = 10000,
+// whose pieces would be too long in one and were not split, 24.2 and 34).
+constexpr int kPart = 768;
 static_assert(kPart % (4 * BK) == 0, "a part is a number of steps");
 constexpr int kEpiRegs = 216, kOtherRegs = 72, kPartsRegs = 168;
 static_assert(2 * kEpiRegs + kOtherRegs <= 3 * kPartsRegs,
@@ -76,7 +81,7 @@ struct Args {
     int64_t M, N;
     uint32_t tiles_m, tiles_n;
     int num_kb, ksub, ks;  // steps of K (stages), blocks of 64 per step, pieces
-    int part_steps;        // of K
+    int part_steps;        // of K in a part (a piece's: as many as it has, if it is not cut)
     int bn, am;
     int stages, ring_bytes, boxes;
     uint32_t stage_bytes, a_region;
@@ -481,6 +486,10 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
                         if (!ok) break;
                         in_part = 0;
                     }
+                    if (SPLIT && in_part == args.part_steps) {  // the next columns of TMEM
+                        d_tmem += static_cast<uint32_t>(args.bn);
+                        in_part = 0;
+                    }
                     ok = wait_all(full0 + 8 * stage, phase);
                     if (!ok) break;
                     tc_fence_after();
@@ -827,6 +836,19 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
             tc_fence_after();
         }
         const uint32_t t_acc = tmem_base + lane_off;
+        // this CTA's sums of sixteen columns: its parts of K, in their order
+        auto own_sums = [&](int b, int h, float (&v)[16]) {
+            const uint32_t at = t_acc + b * 64 + h * 16;
+            __syncwarp();
+            tmem_load_16cols(at, v);
+#pragma unroll 1
+            for (int from = args.part_steps, q = 1; from < nkb; from += args.part_steps, ++q) {
+                float more[16];
+                tmem_load_16cols(at + q * args.bn, more);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += more[j];
+            }
+        };
         cluster_sync();
         auto owner_of = [&](int b, int &slot) -> int {
             const int u = b * quarters + quarter;
@@ -844,8 +866,7 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     float v[16];
-                    __syncwarp();
-                    tmem_load_16cols(t_acc + b * 64 + h * 16, v);
+                    own_sums(b, h, v);
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
                         st_cluster_v4(to + (((h * 4 + p) ^ (lane & 15)) << 4), __float_as_uint(v[p * 4]),
@@ -863,8 +884,7 @@ __global__ void __launch_bounds__(threads<PARTS>(), 1)
                     b,
                     [&](int h, float (&v)[16]) {
                         float own[16];
-                        __syncwarp();
-                        tmem_load_16cols(t_acc + b * 64 + h * 16, own);
+                        own_sums(b, h, own);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = 0.f;
 #pragma unroll 1
@@ -1008,6 +1028,20 @@ int sub_blocks(const FusedProblem &p, const Cut &c) {
     return ksub;
 }
 
+// Steps of K that one accumulator of a cluster's CTA adds.
+int piece_part_steps(const FusedProblem &p, const Cut &c) {
+    const int ksub = sub_blocks(p, c);
+    const int64_t piece = ceil_div(ceil_div(p.K, BK * ksub), c.ks);
+    return static_cast<int>(p.grad && p.dbias != nullptr && piece > kPart / (BK * ksub) ? kPart / (BK * ksub)
+                                                                                        : piece);
+}
+// Its parts lie side by side in TMEM (and are read 64 columns at a time).
+bool parts_fit(const FusedProblem &p, const Cut &c) {
+    const int64_t piece = ceil_div(ceil_div(p.K, BK * sub_blocks(p, c)), c.ks);
+    const int64_t parts = ceil_div(piece, piece_part_steps(p, c));
+    return parts * (c.bn > 64 ? c.bn : 64) <= kTmemCols;
+}
+
 // The cut whose slowest CTA is done first, by a model in microseconds fitted to 1022
 // measured times (90 shapes from 8 x 512 x 512 to 4096 x 4096 x 14336, every cut;
 // the cuts that it picks are 1.4 % slower than the best ones on the mean, 21 % at
@@ -1020,7 +1054,6 @@ int sub_blocks(const FusedProblem &p, const Cut &c) {
 //                         64 columns of 128 rows
 //   all operands          once at 6.4 TB/s; tiles of 32 columns read at 0.6 of that
 Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &split, int sms) {
-    const bool sums = p.grad && p.dbias != nullptr;
     const int64_t kb = ceil_div(p.K, BK);
     const double bytes = 2.0 * (static_cast<double>(p.M) * p.K + static_cast<double>(p.K) * p.N);
     Cut best = {1, BM, 256, 1};
@@ -1050,8 +1083,8 @@ Cut choose_cut(const FusedProblem &p, const Prepared &pair, const Prepared &spli
         consider({1, am, bn, 1}, sms);
         for (int ks = 2; ks <= kMaxSplit; ks *= 2) {
             const int64_t tiles = ceil_div(p.M, am) * ceil_div(p.N, bn);
-            if (sums && p.K > static_cast<int64_t>(kPiece) * ks) continue;
-            if (kb >= 2 * ks && tiles <= split.resident[ks]) consider({1, am, bn, ks}, split.resident[ks]);
+            if (kb >= 2 * ks && tiles <= split.resident[ks] && parts_fit(p, {1, am, bn, ks}))
+                consider({1, am, bn, ks}, split.resident[ks]);
         }
     }
     return best;
@@ -1082,7 +1115,7 @@ static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t str
     a.ks = cut.ks;
     a.ksub = sub_blocks(p, cut);
     a.num_kb = static_cast<int>(ceil_div(p.K, BK * a.ksub));
-    a.part_steps = kPart / (BK * a.ksub);
+    a.part_steps = cut.ks > 1 ? piece_part_steps(p, cut) : kPart / (BK * a.ksub);
     a.tiles_m = static_cast<uint32_t>(ceil_div(p.M, cut.am * cut.cg));
     a.tiles_n = static_cast<uint32_t>(ceil_div(p.N, cut.bn));
     a.a_kmajor = p.a_kmajor;
