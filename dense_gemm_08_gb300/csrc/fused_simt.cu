@@ -11,8 +11,8 @@
 // share of the tile's rows and in the order of the pieces.  The tile then lies in
 // shared memory, and a thread finishes one of its columns.
 //
-// A row or two of A (FP32: four) and a K-contiguous B: warps stream B's columns
-// once (fused_rows_kernel).
+// A row or two of A (up to four in FP32, or where B is small) and a K-contiguous B:
+// warps stream B's columns once (fused_rows_kernel).
 #include <atomic>
 #include <type_traits>
 

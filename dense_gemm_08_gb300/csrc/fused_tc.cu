@@ -1137,9 +1137,10 @@ static cudaError_t launch_tc_as(const FusedProblem &p, int dev, cudaStream_t str
     a.even_d = reinterpret_cast<uintptr_t>(a.D) % 4 == 0 && a.ldd % 2 == 0;
     a.even_in = reinterpret_cast<uintptr_t>(a.in) % 4 == 0 && a.ld_in % 2 == 0;
     a.even_pre = reinterpret_cast<uintptr_t>(a.pre) % 4 == 0 && a.ld_pre % 2 == 0;
-    // ring and boxes share the body; the last stage keeps 128 rows of A inside the
-    // ring (am < 128: the MMA's operand runs on into B and the next stages, stale
-    // rows that reach only accumulator rows which are not stored)
+    // ring and boxes share the body.  With am < 128 the MMA's operand runs on past A into
+    // B and the next stages, in the last stage past it: its first block of 64 stays inside
+    // the ring, its second (tiles of 32 columns) may reach 4 KB into the boxes.  Whatever lies
+    // there reaches only accumulator rows that are not stored.
     a.boxes = 1 + (a.pre != nullptr) + (a.in != nullptr);
     a.ring_bytes = kBody - kEpiWarps * a.boxes * kBox;
     a.a_region = static_cast<uint32_t>((p.a_kmajor ? a.am : BM) * a.ksub) * BK * 2;

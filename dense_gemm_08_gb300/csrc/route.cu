@@ -591,7 +591,7 @@ __device__ __forceinline__ float share(const RouteProblem &p, bool has, float x,
 
 // (Register limits: many warps per SM hide the latency of each; the spills are in the
 // parts that run rarely.  Up to 256 experts 12 CTAs per SM: 16384 x 256 without a bias
-// 11.4 us, with 8 CTAs 0.8 more; CTAs that stay and load the next token ahead 14.4.)
+// 11.7 us, with 8 CTAs 0.8 more; CTAs that stay and load the next token ahead 14.4.)
 template <int TYPE, int VPT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps, VPT <= 8 ? 12 : VPT <= 16 ? 5 : 3)
     route_kernel(const __grid_constant__ RouteProblem p) {

@@ -16,7 +16,7 @@ DOUBT = 2.0 ** -47
 def _falling(v):
     """Order of the last axis by falling value, a NaN first, equal ones by index."""
     nan = np.isnan(v)
-    return np.argsort(np.where(nan, -np.inf, -np.where(nan, 0.0, v)), axis=-1, kind="stable")
+    return np.lexsort((-np.where(nan, 0.0, v), ~nan), axis=-1)  # (stable; a NaN before +infinity)
 
 
 def _in_doubt(a, b, size, same):
